@@ -1,7 +1,7 @@
 """Build the C-ABI library libfsdp_pack.so in-tree for sm_103a.
 
-Two translation units compiled in parallel (the host planner with g++, the
-kernels with nvcc), linked by nvcc into ``_build/libfsdp_pack.so``.  Nothing
+The translation units in ``csrc`` compiled in parallel (the host planner with
+g++, the kernels with nvcc), linked by nvcc into ``_build/libfsdp_pack.so``.  Nothing
 is installed; the library is rebuilt whenever a source or header is newer.
 """
 from __future__ import annotations

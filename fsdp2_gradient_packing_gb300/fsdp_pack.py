@@ -555,3 +555,12 @@ def fsdp_debug_stream_widen(src, n: int, dst, stream=None) -> None:
 
 def fsdp_layout_destroy(layout: Layout) -> None:
     layout.close()
+
+
+def __getattr__(name):
+    """The training operators (include/fsdp_ops.h) are names of this module too."""
+    from . import fsdp_ops
+    if name in fsdp_ops.__all__:
+        globals()[name] = value = getattr(fsdp_ops, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

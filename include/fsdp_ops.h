@@ -1,0 +1,152 @@
+/*
+ * fsdp_ops.h - C ABI of the training operators that stand next to the
+ * packing library (fsdp_pack.h): the feed-forward half of a transformer
+ * block, whose gradients are what a fully_shard group packs.
+ *
+ *   fsdp_layer_norm_forward / _backward   layer norm with its parameter
+ *                                         gradients
+ *   fsdp_act8_store / _load               activation checkpoints in 8 bits
+ *   fsdp_gated_ffn_forward / _backward    both projections, the activation
+ *                                         and the product of a gated
+ *                                         feed-forward block
+ *
+ * The backward calls read the 8-bit checkpoints in place of the tensors they
+ * were taken from, and write gradients in the dtypes that
+ * fsdp_pack_reduce_scatter reads (BF16 or FP32).
+ *
+ * Conventions, on top of those of fsdp_pack.h (device pointers, asynchronous
+ * on the stream, arguments checked on the host before anything is launched,
+ * one-line errors through fsdp_last_error()):
+ *   - Matrices are row-major with unit column stride; `ld` is the distance
+ *     between rows in elements and at least the number of columns.
+ *   - Every pointer need only be aligned to its element size, except
+ *     checkpoints and workspaces (16 bytes).  Rows whose start is 16-byte
+ *     aligned take faster paths.
+ *   - Indexing is 64-bit throughout.
+ *   - No call allocates device memory: calls that need scratch take a
+ *     workspace, whose size the matching _workspace call gives.  A workspace
+ *     holds nothing between calls, and one workspace serves one call at a
+ *     time.
+ *   - Results are the same, bit for bit, on every run: sums run in a fixed
+ *     order and no result goes through an atomic.
+ *   - rows may be 0: outputs of that many rows are empty, and gradients of
+ *     parameters (sums over no rows) are written as 0.
+ *   - NaN and infinities propagate as the formulas say.
+ *   - Every wait inside the kernels is bounded; fsdp_ops_sync_status tells
+ *     whether one gave up.
+ */
+#ifndef FSDP_OPS_H
+#define FSDP_OPS_H
+
+#include "fsdp_pack.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* In the activation dtype fields below, beside FSDP_DTYPE_F32 and
+ * FSDP_DTYPE_BF16: the activation is given by its 8-bit checkpoint. */
+#define FSDP_ACT8 2
+
+/* Elements of a row that share one scale of an 8-bit checkpoint. */
+#define FSDP_ACT8_GROUP 32
+
+/*
+ * Activation checkpoints in 8 bits.
+ *
+ * A checkpoint of a [rows, cols] matrix x is one buffer, 16-byte aligned:
+ * int8 codes [rows, 32 G], then one scale byte per group [rows, G], with
+ * G = ceil(cols / 32).  A group is 32 consecutive elements of a row (the last
+ * one of a row may be shorter; its missing elements count and are stored as
+ * 0).  With a = max |x| over the group and e the least integer >= -126 with
+ * a <= 127 * 2^e:
+ *   scale byte = e + 127,   code = x * 2^-e rounded to the nearest integer,
+ *                                  ties to even (for e = 122 held to
+ *                                  [-63, 63]: 64 * 2^122 is infinite)
+ *   value read back = code * 2^(scale byte - 127)
+ * A group that holds a NaN or an infinity has scale byte 255 and codes 0, and
+ * reads back as NaN throughout, so that a check for overflowed gradients
+ * still sees it.  Codes have 7 bits and the scale is a power of two, so every
+ * value that reads back is exact in BF16 (and so on the tensor cores), and
+ * storing what was read back gives the same checkpoint again.  The error of an
+ * element is at most 2^(e-1), below a / 127 (2^e for e = 122).
+ */
+
+/* Bytes of the checkpoint of a [rows, cols] matrix: rows * 33 * G.
+ * FSDP_EINVAL for NULL bytes, rows < 0 or cols < 1. */
+fsdp_status_t fsdp_act8_bytes(int64_t rows, int64_t cols, int64_t *bytes);
+
+/* x [rows, cols] (dtype FSDP_DTYPE_F32 or _BF16) -> ckpt. */
+fsdp_status_t fsdp_act8_store(const void *x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, void *ckpt,
+                              fsdp_stream_t stream);
+
+/* ckpt -> y [rows, cols] (dtype FSDP_DTYPE_F32 or _BF16: exact in both). */
+fsdp_status_t fsdp_act8_load(const void *ckpt, int64_t rows, int64_t cols, void *y, int32_t dtype, int64_t ld,
+                             fsdp_stream_t stream);
+
+/*
+ * Layer norm over the rows of a [rows, cols] matrix.  For each row:
+ *   mean = sum x / cols,  rstd = (sum (x - mean)^2 / cols + eps)^(-1/2),
+ *   xh = (x - mean) * rstd,  y = xh * weight + bias
+ * and for the backward pass, with g = dy * weight:
+ *   dx = rstd * (g - mean(g) - xh * mean(g * xh)),
+ *   dweight = sum over rows of dy * xh,  dbias = sum over rows of dy.
+ * All arithmetic and sums are in binary32.
+ */
+typedef struct {
+  int64_t rows;         /* >= 0 */
+  int64_t cols;         /* 1 .. FSDP_NORM_MAX_COLS */
+  int64_t ld_x;         /* row distance of x (ignored for a checkpoint) */
+  int64_t ld_y;         /* row distance of y (forward) or dy (backward) */
+  int64_t ld_dx;        /* row distance of dx (backward) */
+  int32_t x_dtype;      /* FSDP_DTYPE_F32, FSDP_DTYPE_BF16 or FSDP_ACT8 */
+  int32_t y_dtype;      /* dtype of y and dy: F32 or BF16 */
+  int32_t dx_dtype;     /* dtype of dx: F32 or BF16 */
+  int32_t param_dtype;  /* dtype of weight and bias: F32 or BF16 */
+  int32_t grad_dtype;   /* dtype of dweight and dbias: F32 or BF16 */
+  float eps;            /* >= 0 */
+} fsdp_norm_desc_t;
+
+#define FSDP_NORM_MAX_COLS 65536
+
+/*
+ *   x:          [rows, cols], or its checkpoint (x_dtype FSDP_ACT8).
+ *   weight:     cols elements of param_dtype, or NULL for all ones.
+ *   bias:       cols elements of param_dtype, or NULL for none.
+ *   mean, rstd: rows binary32 values each, written for the backward pass; both
+ *               may be NULL.
+ *   keep:       NULL, or receives the 8-bit checkpoint of x in the same pass
+ *               (x_dtype F32 or BF16 only).
+ */
+fsdp_status_t fsdp_layer_norm_forward(const fsdp_norm_desc_t *desc, const void *x, const void *weight,
+                                      const void *bias, void *y, float *mean, float *rstd, void *keep,
+                                      fsdp_stream_t stream);
+
+/*
+ *   x, weight:      as in the forward pass (x may be the checkpoint that the
+ *                   forward pass kept); mean and rstd: what it wrote.
+ *   dx:             [rows, cols] of dx_dtype, or NULL if not wanted.
+ *   dweight, dbias: cols elements of grad_dtype each, written (not added to);
+ *                   either may be NULL if not wanted.
+ *   workspace:      fsdp_layer_norm_workspace bytes, 16-byte aligned.
+ */
+fsdp_status_t fsdp_layer_norm_backward(const fsdp_norm_desc_t *desc, const void *dy, const void *x,
+                                       const void *weight, const float *mean, const float *rstd, void *dx,
+                                       void *dweight, void *dbias, void *workspace, int64_t workspace_bytes,
+                                       fsdp_stream_t stream);
+
+/* Bytes of workspace that fsdp_layer_norm_backward needs on the current
+ * device (a limit for any device when there is none). */
+fsdp_status_t fsdp_layer_norm_workspace(const fsdp_norm_desc_t *desc, int64_t *bytes);
+
+/* Synchronise `stream`, then read and clear the device word in which the
+ * kernels of this header record a wait that gave up.  The word is one per
+ * device, shared by all calls of the process.  FSDP_ETIMEOUT if any was
+ * recorded since the last call. */
+fsdp_status_t fsdp_ops_sync_status(fsdp_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FSDP_OPS_H */
