@@ -969,6 +969,9 @@ fsdp_status_t batch_launch(const fsdp_layout *const *Ls, int n, Op op, const voi
 // Host-side argument checks (nothing is launched unless all pass), shared
 // with reduce.cu.
 // ---------------------------------------------------------------------------
+int32_t wait_fault() { return g_fault.load(std::memory_order_relaxed); }
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
+
 fsdp_status_t check_layout(const fsdp_layout *L) {
   if (!L) return fail(FSDP_EINVAL, "layout is NULL");
   if (L->device < 0) return fail(FSDP_EINVAL, "layout was planned without a device table");

@@ -116,4 +116,8 @@ void device_release(fsdp_layout *L);
 // error message (index < 0: no index).
 fsdp_status_t check_layout(const fsdp_layout *L);
 fsdp_status_t check_ptr(const void *p, int64_t bytes, int64_t align, const char *what, int64_t index);
+
+// The test hook's fault and the limit of device-side waits (fsdp_debug_set_wait_fault).
+int32_t wait_fault();
+uint64_t wait_limit_ns();
 }  // namespace fsdp

@@ -27,7 +27,9 @@ FSDP_KEEP_NONE, FSDP_KEEP_ACT8, FSDP_KEEP_BF16 = 0, 1, 2
 
 __all__ = ["FSDP_ACT8", "FSDP_ACT8_GROUP", "FSDP_NORM_MAX_COLS", "fsdp_norm_desc_t", "Act8", "fsdp_act8_bytes",
            "fsdp_act8_store", "fsdp_act8_load", "fsdp_layer_norm_forward", "fsdp_layer_norm_backward",
-           "fsdp_layer_norm_workspace", "fsdp_ops_sync_status"]
+           "fsdp_layer_norm_workspace", "FSDP_ACT_SILU", "FSDP_ACT_GELU", "FSDP_KEEP_NONE", "FSDP_KEEP_ACT8",
+           "FSDP_KEEP_BF16", "fsdp_ffn_desc_t", "fsdp_gated_ffn_forward", "fsdp_gated_ffn_backward",
+           "fsdp_gated_ffn_workspace", "fsdp_ops_sync_status"]
 
 _CODE = {torch.float32: FSDP_DTYPE_F32, torch.bfloat16: FSDP_DTYPE_BF16}
 
@@ -39,6 +41,12 @@ class fsdp_norm_desc_t(ctypes.Structure):
                 ("grad_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
+class fsdp_ffn_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "d", "f", "ld_x", "ld_w_gate", "ld_w_up", "ld_h", "ld_kept",
+                                              "ld_dx", "ld_dw_gate", "ld_dw_up")] + \
+               [(n, ctypes.c_int32) for n in ("activation", "keep", "x_dtype", "dx_dtype", "dw_dtype", "unaligned")]
+
+
 _P, _ST, _I64, _I32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int32
 _SIGNATURES = {
     "fsdp_act8_bytes": [_I64, _I64, ctypes.POINTER(_I64)],
@@ -47,6 +55,9 @@ _SIGNATURES = {
     "fsdp_layer_norm_forward": [ctypes.POINTER(fsdp_norm_desc_t), _P, _P, _P, _P, _P, _P, _P, _P],
     "fsdp_layer_norm_backward": [ctypes.POINTER(fsdp_norm_desc_t), _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P],
     "fsdp_layer_norm_workspace": [ctypes.POINTER(fsdp_norm_desc_t), ctypes.POINTER(_I64)],
+    "fsdp_gated_ffn_workspace": [ctypes.POINTER(fsdp_ffn_desc_t), _I32, ctypes.POINTER(_I64)],
+    "fsdp_gated_ffn_forward": [ctypes.POINTER(fsdp_ffn_desc_t), _P, _P, _P, _P, _P, _P, _P, _I64, _P],
+    "fsdp_gated_ffn_backward": [ctypes.POINTER(fsdp_ffn_desc_t)] + [_P] * 10 + [_I64, _P],
     "fsdp_ops_sync_status": [_P],
 }
 for _name, _args in _SIGNATURES.items():
@@ -244,6 +255,97 @@ def _norm_workspace(d) -> int:
 def fsdp_layer_norm_workspace(rows: int, cols: int) -> int:
     """Bytes of workspace that fsdp_layer_norm_backward needs for a [rows, cols] matrix."""
     return _norm_workspace(fsdp_norm_desc_t(rows, cols, cols, cols, cols, 0, 0, 0, 0, 0, 0.0))
+
+
+_BF16_ONLY = (torch.bfloat16,)
+
+
+def _kept(a: _Args, gate, up, rows, f):
+    """(gate pointer, up pointer, row distance, FSDP_KEEP_*)."""
+    if (gate is None) != (up is None):
+        a.fail("gate and up are given together or not at all")
+    if gate is None:
+        return None, None, f, FSDP_KEEP_NONE
+    if isinstance(gate, Act8) or isinstance(up, Act8):
+        return a.ckpt("gate", gate, rows, f), a.ckpt("up", up, rows, f), f, FSDP_KEEP_ACT8
+    pg, lg, _ = a.matrix("gate", gate, rows, f, _BF16_ONLY)
+    pu, lu, _ = a.matrix("up", up, rows, f, _BF16_ONLY)
+    if lg != lu:
+        a.fail("gate and up have different row distances")
+    return pg, pu, lg, FSDP_KEEP_BF16
+
+
+def _ffn_workspace(d, backward) -> int:
+    out = _I64()
+    _check(_lib.fsdp_gated_ffn_workspace(ctypes.byref(d), backward, ctypes.byref(out)), "fsdp_gated_ffn_workspace")
+    return out.value
+
+
+def fsdp_gated_ffn_workspace(rows: int, d: int, f: int, backward: bool, keep: int = FSDP_KEEP_NONE,
+                             x_act8: bool = False) -> int:
+    """Bytes of workspace of a call on contiguous matrices, d and f multiples of 8, that start on 16-byte boundaries;
+    for others, an upper bound with everything that may have to be copied."""
+    odd = 0 if d % 8 == 0 else 7
+    desc = fsdp_ffn_desc_t(rows, d, f, d, d, d, f, f, d, d, d, FSDP_ACT_SILU, keep,
+                           FSDP_ACT8 if x_act8 else FSDP_DTYPE_BF16, FSDP_DTYPE_BF16, FSDP_DTYPE_BF16, odd)
+    return _ffn_workspace(desc, int(backward))
+
+
+def _off16(*ptrs) -> int:
+    return sum(1 << i for i, p in enumerate(ptrs) if p is not None and p % 16)
+
+
+def fsdp_gated_ffn_forward(x, w_gate, w_up, h, gate=None, up=None, activation=FSDP_ACT_SILU, workspace=None,
+                           stream=None) -> None:
+    """gate, up: what is kept for the backward pass: ``Act8`` checkpoints, BF16 tensors, or nothing."""
+    a = _Args("fsdp_gated_ffn_forward")
+    px, ld_x, _ = a.matrix("x", x, dtypes=_BF16_ONLY)
+    rows, d = x.shape
+    pg, ld_g, _ = a.matrix("w_gate", w_gate, None, d, _BF16_ONLY)
+    f = w_gate.shape[0]
+    pu, ld_u, _ = a.matrix("w_up", w_up, f, d, _BF16_ONLY)
+    ph, ld_h, _ = a.matrix("h", h, rows, f, _BF16_ONLY)
+    pkg, pku, ld_k, keep = _kept(a, gate, up, rows, f)
+    desc = fsdp_ffn_desc_t(rows, d, f, ld_x, ld_g, ld_u, ld_h, ld_k, d, d, d, activation, keep, FSDP_DTYPE_BF16,
+                           FSDP_DTYPE_BF16, FSDP_DTYPE_BF16, _off16(px, pg, pu))
+    handle = a.stream(stream)
+    pws, nws, _owner = a.workspace(workspace, _ffn_workspace(desc, 0), handle)
+    _check(_lib.fsdp_gated_ffn_forward(ctypes.byref(desc), px, pg, pu, ph, pkg, pku, pws, nws, handle),
+           "fsdp_gated_ffn_forward")
+
+
+def fsdp_gated_ffn_backward(dh, x, w_gate, w_up, dx=None, dw_gate=None, dw_up=None, gate=None, up=None,
+                            activation=FSDP_ACT_SILU, workspace=None, stream=None) -> None:
+    """x: the forward pass's input or its ``Act8`` checkpoint; gate, up: as kept (None: computed again);
+    dx, dw_gate and dw_up: what is wanted, written."""
+    a = _Args("fsdp_gated_ffn_backward")
+    pdh, ld_h, _ = a.matrix("dh", dh, dtypes=_BF16_ONLY)
+    rows, f = dh.shape
+    pg, ld_g, _ = a.matrix("w_gate", w_gate, f, None, _BF16_ONLY)
+    d = w_gate.shape[1]
+    pu, ld_u, _ = a.matrix("w_up", w_up, f, d, _BF16_ONLY)
+    if isinstance(x, Act8):
+        px, ld_x, dt_x = a.ckpt("x", x, rows, d), d, FSDP_ACT8
+    else:
+        px, ld_x, dt_x = a.matrix("x", x, rows, d, _BF16_ONLY)
+    pkg, pku, ld_k, keep = _kept(a, gate, up, rows, f)
+    pdx, ld_dx, dt_dx = (None, d, FSDP_DTYPE_BF16) if dx is None else a.matrix("dx", dx, rows, d)
+    if (dw_gate is None) != (dw_up is None):
+        a.fail("dw_gate and dw_up are given together or not at all")
+    pdg = pdu = None
+    ld_dg = ld_du = d
+    dt_dw = FSDP_DTYPE_BF16
+    if dw_gate is not None:
+        pdg, ld_dg, dt_dw = a.matrix("dw_gate", dw_gate, f, d)
+        pdu, ld_du, dt_u = a.matrix("dw_up", dw_up, f, d)
+        if dt_u != dt_dw:
+            a.fail("dw_gate and dw_up have different dtypes")
+    desc = fsdp_ffn_desc_t(rows, d, f, ld_x, ld_g, ld_u, ld_h, ld_k, ld_dx, ld_dg, ld_du, activation, keep, dt_x, dt_dx,
+                           dt_dw, _off16(None if dt_x == FSDP_ACT8 else px, pg, pu))
+    handle = a.stream(stream)
+    pws, nws, _owner = a.workspace(workspace, _ffn_workspace(desc, 1), handle)
+    _check(_lib.fsdp_gated_ffn_backward(ctypes.byref(desc), pdh, px, pg, pu, pkg, pku, pdx, pdg, pdu, pws, nws, handle),
+           "fsdp_gated_ffn_backward")
 
 
 def fsdp_ops_sync_status(stream=None) -> None:

@@ -139,6 +139,68 @@ fsdp_status_t fsdp_layer_norm_backward(const fsdp_norm_desc_t *desc, const void 
  * device (a limit for any device when there is none). */
 fsdp_status_t fsdp_layer_norm_workspace(const fsdp_norm_desc_t *desc, int64_t *bytes);
 
+/*
+ * Gated feed-forward block over rows of d features with f hidden features: both
+ * projections, the activation and the product in one kernel.
+ *   g = x w_gate^T,  u = x w_up^T,  h = act(g) * u        (forward)
+ *   dg = dh * u * act'(g),  du = dh * act(g)
+ *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x   (backward)
+ * with act(g) = g / (1 + e^-g) (FSDP_ACT_SILU) or g * Phi(g), Phi the normal
+ * distribution (FSDP_ACT_GELU, the exact form).  Matrices are BF16 unless a
+ * dtype field says otherwise; products run on the tensor cores with binary32
+ * sums, and activations, their derivatives and products in binary32.  dg and du
+ * are rounded to BF16 once, as operands of the backward products; g and u are
+ * not rounded unless they are kept.
+ *
+ * Kept for the backward pass (`keep`): nothing (the backward call computes g
+ * and u again), the 8-bit checkpoints of g and u (33/32 byte an element), or
+ * both in BF16.
+ */
+typedef enum { FSDP_ACT_SILU = 0, FSDP_ACT_GELU = 1 } fsdp_activation_t;
+typedef enum { FSDP_KEEP_NONE = 0, FSDP_KEEP_ACT8 = 1, FSDP_KEEP_BF16 = 2 } fsdp_keep_t;
+
+typedef struct {
+  int64_t rows;        /* tokens, >= 0 */
+  int64_t d, f;        /* features in and hidden, >= 1 */
+  int64_t ld_x;        /* row distances; of matrices that a call is not given, ignored */
+  int64_t ld_w_gate, ld_w_up;
+  int64_t ld_h;        /* of h (forward) or dh (backward) */
+  int64_t ld_kept;     /* of gate and up kept in BF16 */
+  int64_t ld_dx, ld_dw_gate, ld_dw_up;
+  int32_t activation;  /* fsdp_activation_t */
+  int32_t keep;        /* fsdp_keep_t */
+  int32_t x_dtype;     /* FSDP_DTYPE_BF16, or in the backward pass FSDP_ACT8 */
+  int32_t dx_dtype;    /* F32 or BF16 */
+  int32_t dw_dtype;    /* F32 or BF16 */
+  int32_t unaligned;   /* which operands start off a 16-byte boundary: 1 x, 2 w_gate, 4 w_up */
+} fsdp_ffn_desc_t;
+
+/* Bytes of workspace of the forward (backward = 0) or backward call.  Operands
+ * whose rows do not all start on 16-byte boundaries (by their row distance or
+ * by `unaligned`) are copied there once per call, which costs their bytes. */
+fsdp_status_t fsdp_gated_ffn_workspace(const fsdp_ffn_desc_t *desc, int32_t backward, int64_t *bytes);
+
+/*
+ *   x [rows, d], w_gate and w_up [f, d], h [rows, f].
+ *   gate, up: by `keep`, NULL; [rows, f] checkpoints of fsdp_act8_bytes(rows, f)
+ *             bytes; or [rows, f] BF16 matrices.
+ *   workspace: may be NULL if fsdp_gated_ffn_workspace gives 0.
+ */
+fsdp_status_t fsdp_gated_ffn_forward(const fsdp_ffn_desc_t *desc, const void *x, const void *w_gate,
+                                     const void *w_up, void *h, void *gate, void *up, void *workspace,
+                                     int64_t workspace_bytes, fsdp_stream_t stream);
+
+/*
+ *   dh [rows, f]; x as in the forward pass or its checkpoint; gate and up as kept
+ *   (NULL for FSDP_KEEP_NONE).
+ *   dx [rows, d], dw_gate and dw_up [f, d]: written (not added to); dx may be
+ *   NULL, and dw_gate and dw_up together, where they are not wanted.
+ */
+fsdp_status_t fsdp_gated_ffn_backward(const fsdp_ffn_desc_t *desc, const void *dh, const void *x,
+                                      const void *w_gate, const void *w_up, const void *gate, const void *up,
+                                      void *dx, void *dw_gate, void *dw_up, void *workspace,
+                                      int64_t workspace_bytes, fsdp_stream_t stream);
+
 /* Synchronise `stream`, then read and clear the device word in which the
  * kernels of this header record a wait that gave up.  The word is one per
  * device, shared by all calls of the process.  FSDP_ETIMEOUT if any was
