@@ -5,8 +5,8 @@
 // A thread holds one 16-byte vector of the matrix (8 BF16 or 4 FP32 elements),
 // so a group of 32 is 4 or 8 neighbouring lanes and its maximum 2 or 3
 // shuffles; each thread has kUnroll vectors in flight.  Rows that no vector
-// divides or that start off a 16-byte boundary go element by element, one group
-// to a warp, which keeps every load and store of a warp contiguous.
+// divides or that start off a 16-byte boundary go element by element, kUnroll
+// groups of a row to a warp, which keeps every load and store of a warp contiguous.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -40,11 +40,12 @@ template <class T>
 constexpr int kVec = 16 / (int)sizeof(T);  // elements of one vector
 
 template <class T>
-__device__ __forceinline__ void unpack_vec(uint4 r, float (&v)[kVec<T>]) {
+__device__ __forceinline__ void unpack_vec(uint4 r, float2 (&v)[kVec<T> / 2]) {
   if constexpr (sizeof(T) == 2) {
     unpack8(r, v);
   } else {
-    v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y), v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
+    v[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+    v[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
   }
 }
 
@@ -81,22 +82,15 @@ __global__ void __launch_bounds__(kThreads) store_vec_kernel(const __grid_consta
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int64_t i = first + u * kThreads;
-    float v[E];
+    float2 v[E / 2];
     unpack_vec<T>(raw[u], v);
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    uint32_t top = act8_top(v);
 #pragma unroll
     for (int m = 1; m < kLanes; m *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
     const uint32_t s = act8_scale_byte(top);
     if (i < a.units) {
       // Units run over whole groups, so unit i's codes are at i * E whatever the row.
-      if constexpr (E == 8) {
-        const uint2 c = make_uint2(act8_code4(v[0], v[1], v[2], v[3], s), act8_code4(v[4], v[5], v[6], v[7], s));
-        *reinterpret_cast<uint2 *>(a.codes + i * E) = c;
-      } else {
-        *reinterpret_cast<uint32_t *>(a.codes + i * E) = act8_code4(v[0], v[1], v[2], v[3], s);
-      }
+      act8_store<E>(a.codes + i * E, v, s);
       if (threadIdx.x % kLanes == 0) a.scales[i / kLanes] = (uint8_t)s;
     }
   }
@@ -130,70 +124,62 @@ __global__ void __launch_bounds__(kThreads) load_vec_kernel(const __grid_constan
     int64_t row, at;
     place(i, per_row, a.rows, &row, &at);
     if (at * E >= a.cols) continue;
-    const float scale = act8_scale(s[u]);
-    float v[E];
+    const float2 scale = both(act8_scale(s[u]));
+    float2 v[E / 2];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = act8_value(code[u][e / 4], e % 4, scale);
+    for (int e = 0; e < E / 2; ++e) v[e] = __fmul2_rn(act8_codes_of(act8_biased(code[u][e / 2]), e % 2), scale);
     uint4 r;
     if constexpr (E == 8)
-      r = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+      r = make_uint4(bf16_pair(v[0].x, v[0].y), bf16_pair(v[1].x, v[1].y), bf16_pair(v[2].x, v[2].y), bf16_pair(v[3].x, v[3].y));
     else
-      r = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+      r = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
     *reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + row * a.ld + at * E) = r;
   }
 }
 
-// One group to a warp, one element to a lane.
+// kUnroll groups of one row to a warp, one element of each to a lane.
 template <class T>
 __global__ void __launch_bounds__(kThreads) store_rows_kernel(const __grid_constant__ Act8Args a) {
   const int lane = threadIdx.x & 31;
-  const int64_t first = (int64_t)blockIdx.x * (kThreads / 32 * kUnroll) + threadIdx.x / 32;
+  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32, per_row = (a.groups + kUnroll - 1) / kUnroll;
   wait_for_previous();
   let_next_start();
+  if (i >= a.units) return;
+  int64_t row, at;
+  place(i, per_row, a.rows, &row, &at);
+  const int64_t j = at * (kUnroll * kActGroup) + lane, g = row * a.groups + at * kUnroll;
+  const T *x = static_cast<const T *>(a.x) + row * a.ld + j;
   float v[kUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = first + u * (kThreads / 32);
-    v[u] = 0.0f;
-    if (i < a.units) {
-      int64_t row, at;
-      place(i, a.groups, a.rows, &row, &at);
-      const int64_t j = at * kActGroup + lane;
-      if (j < a.cols) v[u] = load_any(a.x, row * a.ld + j, sizeof(T) == 2);
-    }
-  }
+  for (int u = 0; u < kUnroll; ++u) v[u] = j + u * kActGroup < a.cols ? (float)x[u * kActGroup] : 0.0f;
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = first + u * (kThreads / 32);
+    if (at * kUnroll + u >= a.groups) break;
     const uint32_t s = act8_scale_byte(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[u]) & 0x7FFFFFFFu));
-    if (i < a.units) {
-      a.codes[i * kActGroup + lane] = (uint8_t)act8_code(v[u], s);
-      if (lane == 0) a.scales[i] = (uint8_t)s;
-    }
+    a.codes[(g + u) * kActGroup + lane] = (uint8_t)act8_code(v[u], s);
+    if (lane == 0) a.scales[g + u] = (uint8_t)s;
   }
 }
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) load_rows_kernel(const __grid_constant__ Act8Args a) {
   const int lane = threadIdx.x & 31;
-  const int64_t first = (int64_t)blockIdx.x * (kThreads / 32 * kUnroll) + threadIdx.x / 32;
+  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32, per_row = (a.groups + kUnroll - 1) / kUnroll;
   wait_for_previous();
   let_next_start();
+  if (i >= a.units) return;
+  int64_t row, at;
+  place(i, per_row, a.rows, &row, &at);
+  const int64_t j = at * (kUnroll * kActGroup) + lane, g = row * a.groups + at * kUnroll;
+  const uint8_t *codes = a.codes + g * kActGroup + lane, *scales = a.scales + g;
+  T *y = static_cast<T *>(a.y) + row * a.ld + j;
   uint32_t code[kUnroll], s[kUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = first + u * (kThreads / 32);
-    if (i < a.units) code[u] = a.codes[i * kActGroup + lane], s[u] = a.scales[i];
-  }
+  for (int u = 0; u < kUnroll; ++u)
+    if (at * kUnroll + u < a.groups) code[u] = codes[u * kActGroup], s[u] = scales[u];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = first + u * (kThreads / 32);
-    if (i >= a.units) continue;
-    int64_t row, at;
-    place(i, a.groups, a.rows, &row, &at);
-    const int64_t j = at * kActGroup + lane;
-    if (j < a.cols) store_any(a.y, row * a.ld + j, sizeof(T) == 2, act8_value(code[u], 0, act8_scale(s[u])));
-  }
+  for (int u = 0; u < kUnroll; ++u)
+    if (j + u * kActGroup < a.cols) y[u * kActGroup] = (T)act8_value(act8_biased(code[u]), act8_scale(s[u]));
 }
 
 template <class T>
@@ -206,9 +192,8 @@ fsdp_status_t run(Act8Args a, bool store, cudaStream_t stream) {
     a.ld = a.cols;
     a.rows = 1;
   }
-  const int per_group = vec ? (int)kActGroup / kVec<T> : 1;
-  a.units = a.rows * a.groups * per_group;
-  const int64_t per_block = (vec ? kThreads : kThreads / 32) * (int64_t)kUnroll;
+  a.units = a.rows * (vec ? a.groups * ((int)kActGroup / kVec<T>) : (a.groups + kUnroll - 1) / kUnroll);
+  const int64_t per_block = vec ? kThreads * kUnroll : kThreads / 32;
   const int64_t grid = (a.units + per_block - 1) / per_block;
   if (grid > INT32_MAX) return fail(FSDP_EUNSUPPORTED, "the matrix is too large for one launch");
   const void *fn = store ? (vec ? reinterpret_cast<const void *>(&store_vec_kernel<T>)

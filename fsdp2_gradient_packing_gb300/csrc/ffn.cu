@@ -95,43 +95,39 @@ __global__ void __launch_bounds__(kThreads) slope_kernel(const __grid_constant__
       row = i / per_row, at = i % per_row;
     const int64_t j = at * 8;
     const bool whole = j + 8 <= a.f;
-    float d[8], g[8], u[8];
-    if (whole && a.dh_vec) {
-      load8(a.dh, row * a.ld_dh + j, true, d);
-    } else {
+    float2 d[4], g[4], u[4];
+    auto load = [&](float2(&v)[4], const void *p, int64_t at, bool vec) {
+      if (whole && vec) {
+        load8(p, at, true, v);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] = j + e < a.f ? load_any(a.dh, row * a.ld_dh + j + e, true) : 0.0f;
-    }
+        for (int e = 0; e < 8; ++e) element(v, e) = j + e < a.f ? load_any(p, at + e, true) : 0.0f;
+      }
+    };
+    load(d, a.dh, row * a.ld_dh + j, a.dh_vec != 0);
     if (a.act8) {
       const int64_t c = row * a.groups * kActGroup + j, s = row * a.groups + j / (int)kActGroup;
       const uint2 p = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.gate) + c);
       const uint2 q = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.up) + c);
-      const float sg = act8_scale(a.scales[0][s]), su = act8_scale(a.scales[1][s]);
+      const float2 sg = both(act8_scale(a.scales[0][s])), su = both(act8_scale(a.scales[1][s]));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        g[e] = act8_value(e < 4 ? p.x : p.y, e % 4, sg);
-        u[e] = act8_value(e < 4 ? q.x : q.y, e % 4, su);
+      for (int e = 0; e < 4; ++e) {
+        g[e] = __fmul2_rn(act8_codes_of(act8_biased(e < 2 ? p.x : p.y), e % 2), sg);
+        u[e] = __fmul2_rn(act8_codes_of(act8_biased(e < 2 ? q.x : q.y), e % 2), su);
       }
-    } else if (whole && a.kept_vec) {
-      load8(a.gate, row * a.ld_kept + j, true, g);
-      load8(a.up, row * a.ld_kept + j, true, u);
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        g[e] = j + e < a.f ? load_any(a.gate, row * a.ld_kept + j + e, true) : 0.0f;
-        u[e] = j + e < a.f ? load_any(a.up, row * a.ld_kept + j + e, true) : 0.0f;
-      }
+      load(g, a.gate, row * a.ld_kept + j, a.kept_vec != 0);
+      load(u, a.up, row * a.ld_kept + j, a.kept_vec != 0);
     }
-    float x[8], y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float2 t = act_of<true>(g[e], a.act);
-      x[e] = d[e] * u[e] * t.y;
-      y[e] = d[e] * t.x;
+    for (int e = 0; e < 4; ++e) {
+      const float2 p = act_of<true>(g[e].x, a.act), q = act_of<true>(g[e].y, a.act);
+      g[e] = __fmul2_rn(__fmul2_rn(d[e], u[e]), make_float2(p.y, q.y));
+      u[e] = __fmul2_rn(d[e], make_float2(p.x, q.x));
     }
     // The pitch holds whole vectors; what lies past the row's end is never read.
-    store8(a.dg, row * a.pitch + j, true, x);
-    store8(a.du, row * a.pitch + j, true, y);
+    store8(a.dg, row * a.pitch + j, true, g);
+    store8(a.du, row * a.pitch + j, true, u);
   }
 }
 
@@ -143,21 +139,47 @@ struct JoinArgs {
   void *out[2];
   int64_t ld[2];
   int64_t rows, half, cols;  // rows from `half` on belong to out[1]
-  int32_t splits, bf16;
+  int32_t splits, bf16, vec;
 };
 
+// Bound: L2, where the parts still are.  VEC columns to a thread, one row to a block
+// at a time.
+template <int VEC>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ JoinArgs a) {
   const int64_t total = a.rows * a.cols;
   wait_for_previous();
   let_next_start();
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-    float s = a.partial[i];
-    for (int k = 1; k < a.splits; ++k) s += a.partial[k * total + i];
-    int64_t row = i / a.cols;
-    const int64_t col = i - row * a.cols;
-    const int second = row >= a.half;
-    if (second) row -= a.half;
-    store_any(a.out[second], row * a.ld[second] + col, a.bf16 != 0, s);
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const bool second = r >= a.half;
+    const int64_t row = second ? r - a.half : r;
+    for (int64_t col = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * VEC; col < a.cols; col += (int64_t)gridDim.y * kThreads * VEC) {
+      const float *p = a.partial + r * a.cols + col;
+      float s[VEC];
+      if constexpr (VEC == 4) {
+        float4 v = *reinterpret_cast<const float4 *>(p);
+#pragma unroll 4
+        for (int k = 1; k < a.splits; ++k) {
+          const float4 q = *reinterpret_cast<const float4 *>(p + k * total);
+          v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+        }
+        s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+        if (a.vec) {
+          const int64_t at = row * a.ld[second] + col;
+          if (a.bf16)
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out[second]) + at) =
+                make_uint2(bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3]));
+          else
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.out[second]) + at) = v;
+          continue;
+        }
+      } else {
+        s[0] = p[0];
+#pragma unroll 4
+        for (int k = 1; k < a.splits; ++k) s[0] += p[k * total];
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) store_any(a.out[second], row * a.ld[second] + col + e, a.bf16 != 0, s[e]);
+    }
   }
 }
 
@@ -173,7 +195,7 @@ struct Tiling {
 // work for every SM.
 Tiling tiling(Mode mode, int64_t m, int64_t n, int64_t k, int sms) {
   Tiling t = {};
-  t.pair = false;
+  t.pair = true;
   const int64_t tile_m = t.pair ? 2 * kTileM : kTileM, tile_n = mode == FORWARD || mode == RECOMPUTE ? 128 : 256;
   t.m_half = blocks_of(m, tile_m);
   t.m_tiles = mode == DW ? 2 * t.m_half : t.m_half;
@@ -202,7 +224,7 @@ bool rows_off(int64_t rows, int64_t ld, bool base) { return base || (rows > 1 &&
 Plan plan_of(const fsdp_ffn_desc_t *d, bool backward) {
   Plan p = {};
   p.sms = device_sms() > 0 ? device_sms() : 160;
-  p.d_pitch = up_to(d->d, 8), p.f_pitch = up_to(d->f, 8);
+  p.d_pitch = up_to(d->d, 8), p.f_pitch = up_to(d->f, 16);
   p.stage_x = d->x_dtype == FSDP_ACT8 || rows_off(d->rows, d->ld_x, d->unaligned & 1);
   p.stage_wg = rows_off(d->f, d->ld_w_gate, d->unaligned & 2);
   p.stage_wu = rows_off(d->f, d->ld_w_up, d->unaligned & 4);
@@ -339,11 +361,15 @@ struct Call {
     j.ld[0] = a.ld_out[0], j.ld[1] = a.ld_out[1];
     j.rows = mode == DW ? 2 * m : m, j.half = m, j.cols = n;
     j.splits = (int32_t)t.splits, j.bf16 = a.out_bf16;
+    j.vec = a.out_width >= 16;
     void *args[] = {&j};
-    int64_t grid = blocks_of(j.rows * j.cols, kThreads);
-    if (grid > plan.sms * 32) grid = plan.sms * 32;
-    return launched(launch_kernel(reinterpret_cast<const void *>(&join_kernel), dim3((unsigned)grid), dim3(kThreads), args,
-                                  0, stream, true));
+    const int vec = n % 4 == 0 ? 4 : 1;
+    int64_t across = blocks_of(n, (int64_t)kThreads * vec), down = j.rows;
+    if (across > 64) across = 64;
+    if (down > plan.sms * 64) down = plan.sms * 64;
+    return launched(launch_kernel(vec == 4 ? reinterpret_cast<const void *>(&join_kernel<4>)
+                                           : reinterpret_cast<const void *>(&join_kernel<1>),
+                                  dim3((unsigned)down, (unsigned)across), dim3(kThreads), args, 0, stream, true));
   }
 };
 
@@ -357,7 +383,9 @@ void kept_into(const fsdp_ffn_desc_t *d, void *gate, void *up, Args &a) {
     a.kept[i] = p[i];
   }
   a.ld_kept = d->ld_kept;
-  a.keep_vec = vec_rows(gate, d->rows, d->ld_kept, 2) && vec_rows(up, d->rows, d->ld_kept, 2);
+  const int64_t ld = d->keep == FSDP_KEEP_ACT8 ? 16 : d->ld_kept;  // a checkpoint's groups are 32 bytes each
+  const int wg = row_width(gate, d->rows, ld, 2), wu = row_width(up, d->rows, ld, 2);
+  a.keep_width = wg < wu ? wg : wu;
 }
 
 }  // namespace
@@ -395,7 +423,7 @@ fsdp_status_t fsdp_gated_ffn_forward(const fsdp_ffn_desc_t *d, const void *x, co
     if ((st = c.stage(x, w_gate, w_up)) != FSDP_OK) return st;
     Args a = {};
     a.out[0] = h, a.ld_out[0] = d->ld_h;
-    a.out_bf16 = 1, a.out_vec = vec_rows(h, d->rows, d->ld_h, 2);
+    a.out_bf16 = 1, a.out_width = row_width(h, d->rows, d->ld_h, 2);
     kept_into(d, gate, up, a);
     if ((st = c.product(FORWARD, d->rows, d->f, d->d, c.x, c.x, c.wg, c.wu, a)) != FSDP_OK) return st;
   }
@@ -446,7 +474,7 @@ fsdp_status_t fsdp_gated_ffn_backward(const fsdp_ffn_desc_t *d, const void *dh, 
     Args a = {};
     a.out[0] = dg, a.out[1] = du;
     a.ld_out[0] = a.ld_out[1] = c.plan.f_pitch;
-    a.out_bf16 = a.out_vec = 1;
+    a.out_bf16 = 1, a.out_width = row_width(c.ws, d->rows, c.plan.f_pitch, 2);
     a.dh = dh, a.ld_dh = d->ld_h, a.dh_vec = vec_rows(dh, d->rows, d->ld_h, 2);
     if ((st = c.product(RECOMPUTE, d->rows, d->f, d->d, c.x, c.x, c.wg, c.wu, a)) != FSDP_OK) return st;
   } else {
@@ -474,7 +502,7 @@ fsdp_status_t fsdp_gated_ffn_backward(const fsdp_ffn_desc_t *d, const void *dh, 
     a.out[0] = a.out[1] = dx;
     a.ld_out[0] = a.ld_out[1] = d->ld_dx;
     a.out_bf16 = d->dx_dtype == FSDP_DTYPE_BF16;
-    a.out_vec = vec_rows(dx, d->rows, d->ld_dx, xsize);
+    a.out_width = row_width(dx, d->rows, d->ld_dx, xsize);
     if ((st = c.product(DX, d->rows, d->d, d->f, og, ou, c.wg, c.wu, a)) != FSDP_OK) return st;
   }
   if (dw_gate) {
@@ -482,7 +510,8 @@ fsdp_status_t fsdp_gated_ffn_backward(const fsdp_ffn_desc_t *d, const void *dh, 
     a.out[0] = dw_gate, a.out[1] = dw_up;
     a.ld_out[0] = d->ld_dw_gate, a.ld_out[1] = d->ld_dw_up;
     a.out_bf16 = d->dw_dtype == FSDP_DTYPE_BF16;
-    a.out_vec = vec_rows(dw_gate, d->f, d->ld_dw_gate, wsize) && vec_rows(dw_up, d->f, d->ld_dw_up, wsize);
+    const int rg = row_width(dw_gate, d->f, d->ld_dw_gate, wsize), ru = row_width(dw_up, d->f, d->ld_dw_up, wsize);
+    a.out_width = rg < ru ? rg : ru;
     if ((st = c.product(DW, d->f, d->d, d->rows, og, ou, c.x, c.x, a)) != FSDP_OK) return st;
   }
   clear_error();

@@ -13,7 +13,7 @@
 //
 // Work is split by role: one lane loads 64-deep K slices with TMA into a ring of
 // shared-memory stages, one lane issues tcgen05.mma into one of two accumulators
-// in TMEM, and four or more warps drain the other, so loads, products and
+// in TMEM, and eight warps drain the other, so loads, products and
 // epilogues overlap across the tiles of a persistent block.
 #pragma once
 
@@ -44,14 +44,14 @@ struct Args {
   // Outputs, [m, n] with row distance ld.
   void *out[2];       // FORWARD: h; RECOMPUTE: dg, du; DX: dx; DW: dWg, dWu
   int64_t ld_out[2];
-  int32_t out_bf16, out_vec;   // dtype; rows start on 16-byte boundaries
+  int32_t out_bf16, out_width;  // dtype; row_width() of the outputs
   float *partial;     // splits > 1: [splits][m (DW: 2 m)][n] in binary32 instead of out
   const void *dh;     // RECOMPUTE
   int64_t ld_dh;
   int32_t dh_vec;
   // FORWARD: what is kept for the backward pass.
   int32_t keep;       // 0 nothing, 1 8-bit checkpoints, 2 BF16
-  int32_t keep_vec;
+  int32_t keep_width;  // row_width() of what is kept, both
   uint8_t *codes[2], *scales[2];
   int64_t groups;
   void *kept[2];

@@ -5,7 +5,8 @@ namespace fsdp {
 namespace ffn {
 namespace {
 
-constexpr int kThreads = 192;     // TMA warp, MMA warp, 4 epilogue warps
+constexpr int kEpilogueWarps = 8; // two to each quarter of TMEM's lanes
+constexpr int kThreads = 64 + 32 * kEpilogueWarps;  // and a TMA and an MMA warp
 constexpr int kTileN = 256;       // accumulator columns
 constexpr int kAccumulators = 2;  // 2 x 256 columns: all of TMEM
 constexpr int kTmemColumns = kTileN * kAccumulators;
@@ -76,42 +77,60 @@ __device__ __forceinline__ void load_stage(const Args &a, const Unit &u, int kb,
   }
 }
 
-// 32 consecutive elements of a row to memory: `n` of them exist.
-__device__ __forceinline__ void store_run(void *p, int64_t at, bool bf16, bool vec, const float (&v)[32], int n) {
-  if (vec && n >= 32) {
+// 32 consecutive elements of a row to memory: `n` of them exist; `width`: row_width().
+// A thread has a row of its own, so a store instruction of a warp goes to 32 rows;
+// whole 32-byte sectors keep that from costing two writes a sector.
+__device__ __forceinline__ void store_run(void *p, int64_t at, bool bf16, int width, const float2 (&v)[16], int n) {
+  if (width >= 16 && n >= 32) {
     if (bf16) {
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = bf16_pair(v[i].x, v[i].y);
       uint4 *q = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + at);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        q[i] = make_uint4(bf16_pair(v[8 * i], v[8 * i + 1]), bf16_pair(v[8 * i + 2], v[8 * i + 3]),
-                          bf16_pair(v[8 * i + 4], v[8 * i + 5]), bf16_pair(v[8 * i + 6], v[8 * i + 7]));
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t(&h)[8] = reinterpret_cast<const uint32_t(&)[8]>(w[8 * i]);
+        if (width == 32)
+          store32(q + 2 * i, h);
+        else
+          q[2 * i] = make_uint4(h[0], h[1], h[2], h[3]), q[2 * i + 1] = make_uint4(h[4], h[5], h[6], h[7]);
+      }
     } else {
       float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      for (int i = 0; i < 4; ++i) {
+        if (width == 32) {
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[e] = __float_as_uint(element(v, 8 * i + e));
+          store32(q + 2 * i, h);
+        } else {
+          q[2 * i] = make_float4(v[4 * i].x, v[4 * i].y, v[4 * i + 1].x, v[4 * i + 1].y);
+          q[2 * i + 1] = make_float4(v[4 * i + 2].x, v[4 * i + 2].y, v[4 * i + 3].x, v[4 * i + 3].y);
+        }
+      }
     }
     return;
   }
 #pragma unroll
   for (int i = 0; i < 32; ++i)
-    if (i < n) store_any(p, at + i, bf16, v[i]);
+    if (i < n) store_any(p, at + i, bf16, element(v, i));
 }
 
 // The 8-bit checkpoint of 32 consecutive elements, one whole group; elements from n on are 0.
-__device__ __forceinline__ void keep_group(uint8_t *codes, uint8_t *scale, const float (&v)[32], int n) {
-  uint32_t top = 0;
+__device__ __forceinline__ void keep_group(uint8_t *codes, uint8_t *scale, float2 (&v)[16], int n, bool sector) {
+  if (n < 32) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) top = max(top, i < n ? __float_as_uint(v[i]) & 0x7FFFFFFFu : 0u);
-  const uint32_t s = act8_scale_byte(top);
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w[i] = act8_code4(4 * i < n ? v[4 * i] : 0.0f, 4 * i + 1 < n ? v[4 * i + 1] : 0.0f,
-                      4 * i + 2 < n ? v[4 * i + 2] : 0.0f, 4 * i + 3 < n ? v[4 * i + 3] : 0.0f, s);
-  uint4 *q = reinterpret_cast<uint4 *>(codes);
-  q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    for (int i = 0; i < 32; ++i)
+      if (i >= n) element(v, i) = 0.0f;
+  }
+  const uint32_t s = act8_scale_byte(act8_top(v));
+  act8_store<32>(codes, v, s, sector);
   *scale = (uint8_t)s;
+}
+
+__device__ __forceinline__ float2 pair_at(const uint32_t (&r)[32], int i) {
+  return make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 
 // One thread's part of a gate / up tile: 32 columns of one row.
@@ -119,46 +138,44 @@ template <int MODE>
 __device__ __forceinline__ void gated_run(const Args &a, const uint32_t (&gr)[32], const uint32_t (&ur)[32], int64_t row,
                                           int64_t col) {
   const int n = (int)min((int64_t)32, a.n - col);
-  float x[32], y[32];
+  float2 x[16], y[16];
   if constexpr (MODE == FORWARD) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = act_of<false>(__uint_as_float(gr[i]), a.act).x * __uint_as_float(ur[i]);
-    store_run(a.out[0], row * a.ld_out[0] + col, true, a.out_vec != 0, x, n);
+    for (int i = 0; i < 16; ++i) {
+      const float2 g = pair_at(gr, i);
+      x[i] = __fmul2_rn(make_float2(act_of<false>(g.x, a.act).x, act_of<false>(g.y, a.act).x), pair_at(ur, i));
+    }
+    store_run(a.out[0], row * a.ld_out[0] + col, true, a.out_width, x, n);
     if (a.keep) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(gr[i]), y[i] = __uint_as_float(ur[i]);
+      for (int i = 0; i < 16; ++i) x[i] = pair_at(gr, i), y[i] = pair_at(ur, i);
       if (a.keep == 1) {
         const int64_t group = row * a.groups + col / (int)kActGroup;
-        keep_group(a.codes[0] + group * kActGroup, a.scales[0] + group, x, n);
-        keep_group(a.codes[1] + group * kActGroup, a.scales[1] + group, y, n);
+        keep_group(a.codes[0] + group * kActGroup, a.scales[0] + group, x, n, a.keep_width == 32);
+        keep_group(a.codes[1] + group * kActGroup, a.scales[1] + group, y, n, a.keep_width == 32);
       } else {
-        store_run(a.kept[0], row * a.ld_kept + col, true, a.keep_vec != 0, x, n);
-        store_run(a.kept[1], row * a.ld_kept + col, true, a.keep_vec != 0, y, n);
+        store_run(a.kept[0], row * a.ld_kept + col, true, a.keep_width, x, n);
+        store_run(a.kept[1], row * a.ld_kept + col, true, a.keep_width, y, n);
       }
     }
   } else {
     const __nv_bfloat16 *dh = static_cast<const __nv_bfloat16 *>(a.dh) + row * a.ld_dh + col;
-    float d[32];
+    float2 d[16];
     if (a.dh_vec && n >= 32) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float q[8];
-        load8(dh, 8 * i, true, q);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d[8 * i + e] = q[e];
-      }
+      for (int i = 0; i < 4; ++i) load8(dh, 8 * i, true, reinterpret_cast<float2(&)[4]>(d[4 * i]));
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) d[i] = i < n ? __bfloat162float(dh[i]) : 0.0f;
+      for (int i = 0; i < 32; ++i) element(d, i) = i < n ? __bfloat162float(dh[i]) : 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float2 f = act_of<true>(__uint_as_float(gr[i]), a.act);
-      x[i] = d[i] * __uint_as_float(ur[i]) * f.y;
-      y[i] = d[i] * f.x;
+    for (int i = 0; i < 16; ++i) {
+      const float2 g = pair_at(gr, i), p = act_of<true>(g.x, a.act), q = act_of<true>(g.y, a.act);
+      x[i] = __fmul2_rn(__fmul2_rn(d[i], pair_at(ur, i)), make_float2(p.y, q.y));
+      y[i] = __fmul2_rn(d[i], make_float2(p.x, q.x));
     }
-    store_run(a.out[0], row * a.ld_out[0] + col, true, true, x, n);
-    store_run(a.out[1], row * a.ld_out[1] + col, true, true, y, n);
+    store_run(a.out[0], row * a.ld_out[0] + col, true, a.out_width, x, n);
+    store_run(a.out[1], row * a.ld_out[1] + col, true, a.out_width, y, n);
   }
 }
 
@@ -205,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     for (int s = 0; s < kAccumulators; ++s) {
       tc::bar_init(tc::smem(&sh.tmem_full[s]), 1);
-      tc::bar_init(tc::smem(&sh.tmem_empty[s]), 4 * CG);
+      tc::bar_init(tc::smem(&sh.tmem_empty[s]), kEpilogueWarps * CG);
     }
     tc::bar_init(tc::smem(&sh.drain), 1);
     sh.stop = sh.filled = 0;
@@ -283,7 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
   } else {
     // ---- epilogue ------------------------------------------------------------
-    const int quarter = warp & 3;  // the lanes of TMEM that this warp may read
+    const int quarter = warp & 3;          // the lanes of TMEM that this warp may read
+    const int side = (warp - 2) / 4;       // and its half of the columns
     uint32_t acc = 0, acc_phase = 0;
     for (int i = worker; i < units; i += workers) {
       const Unit u = unit_at(a, i);
@@ -294,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if constexpr (MODE == FORWARD || MODE == RECOMPUTE) {
         const int64_t row = ((int64_t)u.m * CG + rank) * kTileM + quarter * 32 + lane;
 #pragma unroll 1
-        for (int c = 0; c < kTileN / 2; c += 32) {
+        for (int c = side * (kTileN / 4); c < (side + 1) * (kTileN / 4); c += 32) {
           const int64_t col = (int64_t)u.n * (kTileN / 2) + c;
           if (col >= a.n) break;
           uint32_t g[32], up[32];
@@ -308,23 +326,23 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const int half = MODE == DW && u.m >= a.m_half ? 1 : 0;
         const int64_t row = ((int64_t)(half ? u.m - a.m_half : u.m) * CG + rank) * kTileM + quarter * 32 + lane;
 #pragma unroll 1
-        for (int c = 0; c < kTileN; c += 32) {
+        for (int c = side * (kTileN / 2); c < (side + 1) * (kTileN / 2); c += 32) {
           const int64_t col = (int64_t)u.n * kTileN + c;
           if (col >= a.n) break;
           uint32_t r[32];
           __syncwarp();
           tc::tmem_load32(from + c, r);
           tc::tmem_load_wait();
-          float v[32];
+          float2 v[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = some ? __uint_as_float(r[e]) : 0.0f;
+          for (int e = 0; e < 16; ++e) v[e] = some ? pair_at(r, e) : both(0.0f);
           if (row < a.m) {
             const int n = (int)min((int64_t)32, a.n - col);
             if (a.splits > 1) {
               const int64_t rows = MODE == DW ? 2 * a.m : a.m;
-              store_run(a.partial, ((int64_t)u.split * rows + half * a.m + row) * a.n + col, false, a.n % 4 == 0, v, n);
+              store_run(a.partial, ((int64_t)u.split * rows + half * a.m + row) * a.n + col, false, a.n % 8 == 0 ? 32 : a.n % 4 == 0 ? 16 : 0, v, n);
             } else {
-              store_run(a.out[half], row * a.ld_out[half] + col, a.out_bf16 != 0, a.out_vec != 0, v, n);
+              store_run(a.out[half], row * a.ld_out[half] + col, a.out_bf16 != 0, a.out_width, v, n);
             }
           }
         }

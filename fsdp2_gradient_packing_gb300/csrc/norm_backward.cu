@@ -12,114 +12,131 @@ namespace fsdp {
 namespace {
 using namespace norm;
 
+constexpr int kMostThreads = 512;  // of a block beside its loading warp, at 120 registers
+
 template <int XK, bool YB, bool VEC, int G, int K, bool CLUSTER>
-__global__ void __launch_bounds__(G == 32 ? 128 : G) backward_kernel(const __grid_constant__ Args a) {
-  constexpr int NT = G == 32 ? 128 : G, RG = NT / G;
+__global__ void __launch_bounds__(kMostThreads + 32, 1) backward_kernel(const __grid_constant__ Args a) {
   constexpr int DK = YB ? X_BF16 : X_F32;
-  __shared__ Slots slots;
-  int turn = 0;
-  const int t = threadIdx.x % G, cols = (int)a.cols;
-  int base = 0;
+  __shared__ Shared sh;
+  extern __shared__ __align__(16) uint8_t memory[];
+  float *const weight = reinterpret_cast<float *>(memory);
+  uint8_t *const stages = memory + G * K * 8 * sizeof(float);
+  const int group = threadIdx.x / G, groups = (blockDim.x - 32) / G, t = threadIdx.x % G, cols = (int)a.cols;
+  int turn = 0, base = 0;
   int64_t unit = blockIdx.x, units = gridDim.x;
   if constexpr (CLUSTER) {
-    namespace cg = cooperative_groups;
-    base = (int)cg::this_cluster().block_rank() * (G * K * 8);
-    unit /= cg::this_cluster().num_blocks();
-    units /= cg::this_cluster().num_blocks();
+    base = (int)tc::cluster_rank() * (G * K * 8);
+    unit /= cluster_blocks();
+    units /= cluster_blocks();
   }
+  Ring<G, K> ring(a, sh, stages, group, base);
+  begin_block<CLUSTER>(sh, groups, a.stages);
   wait_for_previous();
-
-  int64_t row = unit * RG + threadIdx.x / G;
-  const int64_t step = units * RG;
-  Raw<XK, VEC, K> raw_x;
-  Raw<DK, VEC, K> raw_dy;
+  int64_t row = unit * groups + group;
+  const int64_t step = units * groups;
   const int dy_kind = a.y_bf16 ? X_BF16 : X_F32;
   float mean = 0.0f, rstd = 0.0f;
-  if (row < a.rows) {
-    load_row<XK, VEC, G, K>(raw_x, a.x, a.x_scales, a.x_kind, row, a.ld_x, a.groups, cols, base, t);
-    load_row<DK, VEC, G, K>(raw_dy, a.dy, nullptr, dy_kind, row, a.ld_y, 0, cols, base, t);
-    mean = a.mean[row], rstd = a.rstd[row];
-  }
-  float w[K][8], dw[K][8], db[K][8];
-  load_param<VEC, G, K>(w, a.weight, a.param_bf16 != 0, 1.0f, cols, base, t);
+  const bool loads = (int)threadIdx.x >= groups * G;
+  if (!loads && row < a.rows) mean = a.mean[row], rstd = a.rstd[row];
+  stage_param<VEC, G, K>(weight, a.weight, a.param_bf16 != 0, 1.0f, cols, base);
+  float2 dw[K][4], db[K][4];
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[k][e] = db[k][e] = 0.0f;
+    for (int e = 0; e < 4; ++e) dw[k][e] = db[k][e] = both(0.0f);
+  __syncthreads();
+  if (loads) load_rows<G, K>(a, sh, stages, groups, base, unit * groups, step);
 
-  for (; row < a.rows; row += step) {
-    float xh[K][8], g[K][8];
-    unpack_row<XK, VEC, K>(raw_x, xh);
-    unpack_row<DK, VEC, K>(raw_dy, g);
-    const float r = rstd, m = mean;
-    if (row + step < a.rows) {
-      load_row<XK, VEC, G, K>(raw_x, a.x, a.x_scales, a.x_kind, row + step, a.ld_x, a.groups, cols, base, t);
-      load_row<DK, VEC, G, K>(raw_dy, a.dy, nullptr, dy_kind, row + step, a.ld_y, 0, cols, base, t);
-      mean = a.mean[row + step], rstd = a.rstd[row + step];
-    }
-    float2 s = make_float2(0.0f, 0.0f);
+  const int mine = columns_of<VEC, G, K>(ring.width, t);
+  const int dx_size = a.dx_bf16 ? 2 : 4;
+  uint8_t *dx = static_cast<uint8_t *>(a.dx) + (row * a.ld_dx + base) * dx_size;
+  const int64_t dx_step = step * a.ld_dx * dx_size;
+
+  for (; !loads && row < a.rows; row += step, dx += dx_step) {
+    float2 xh[K][4], g[K][4];
+    float unit[K], one[K];
+    ring.wait();
+    read_row<XK, VEC, G, K>(xh, unit, ring.data(0, row, VEC), ring.data(1, row, false), a.x_kind, mine, t, sh.zeros);
+    read_row<DK, VEC, G, K>(g, one, ring.data(2, row, VEC), nullptr, dy_kind, mine, t, sh.zeros);
+    const float r = rstd, m = -mean * rstd;
+    if (row + step < a.rows) mean = a.mean[row + step], rstd = a.rstd[row + step];
+    float2 s0 = both(0.0f), s1 = both(0.0f);
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+      float2 w[4];
+      read_param<VEC, G, K>(w, weight, t, k);
+      const float2 by = both(r * unit[k]), from = both(m);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        xh[k][e] = (xh[k][e] - m) * r;
-        db[k][e] += g[k][e];
-        dw[k][e] = fmaf(g[k][e], xh[k][e], dw[k][e]);
-        g[k][e] *= w[k][e];
-        s.x += g[k][e];
-        s.y = fmaf(g[k][e], xh[k][e], s.y);
+      for (int e = 0; e < 4; ++e) {
+        xh[k][e] = __ffma2_rn(xh[k][e], by, from);
+        db[k][e] = __fadd2_rn(db[k][e], g[k][e]);
+        dw[k][e] = __ffma2_rn(g[k][e], xh[k][e], dw[k][e]);
+        g[k][e] = __fmul2_rn(g[k][e], w[e]);
+        s0 = __fadd2_rn(s0, g[k][e]);
+        s1 = __ffma2_rn(g[k][e], xh[k][e], s1);
       }
+    }
+    float s[2] = {s0.x + s0.y, s1.x + s1.y};
+    row_sum<2, G, CLUSTER>(s, sh, turn, group, a.wait_limit_ns);
+    if (t == 0) ring.release();
+    ring.next();
     if (a.dx) {
-      s = row_sum<G, CLUSTER>(s, slots, turn);
-      const float c2 = s.x * a.inv_cols, c1 = s.y * a.inv_cols;
+      const float2 c2 = both(-s[0] * a.inv_cols * r), c1 = both(-s[1] * a.inv_cols * r);
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[k][e] = (g[k][e] - c2 - xh[k][e] * c1) * r;
-      store_row<VEC, G, K>(g, a.dx, a.dx_bf16 != 0, row * a.ld_dx, cols, base, t);
+        for (int e = 0; e < 4; ++e) g[k][e] = __ffma2_rn(xh[k][e], c1, __ffma2_rn(g[k][e], both(r), c2));
+      store_row<VEC, G, K>(g, dx, a.dx_bf16 != 0, mine, t);
     }
   }
   let_next_start();
 
-  // Column sums of the block's row groups, added in order.
-  if constexpr (RG > 1) {
-    __shared__ float column_sum[2][G * K * 8];
-    for (int q = 0; q < RG; ++q) {
-      if ((int)threadIdx.x / G == q) {
+  // Column sums of the block's row groups, added in order, in the ring's memory.
+  if (groups > 1) {
+    float *const sums = reinterpret_cast<float *>(stages);
+    __syncthreads();
+    for (int q = 0; q < groups; ++q) {
+      if (group == q) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int j = column<VEC, G>(0, t, k, e);
-            if (q > 0) dw[k][e] += column_sum[0][j], db[k][e] += column_sum[1][j];
-            if (q < RG - 1) column_sum[0][j] = dw[k][e], column_sum[1][j] = db[k][e];
+            const int at = param_at<VEC, G, K>(t, k, e);
+            float &w = element(dw[k], e), &b = element(db[k], e);
+            if (q > 0) w += sums[at], b += sums[G * K * 8 + at];
+            if (q < groups - 1) sums[at] = w, sums[G * K * 8 + at] = b;
           }
       }
       __syncthreads();
     }
   }
-  if ((int)threadIdx.x / G == RG - 1) {
+  if (group == groups - 1) {
     if (a.partial) {
-      store_row<VEC, G, K>(dw, a.partial, false, unit * 2 * a.cols, cols, base, t);
-      store_row<VEC, G, K>(db, a.partial, false, (unit * 2 + 1) * a.cols, cols, base, t);
+      float *to = a.partial + unit * 2 * a.cols + base;
+      store_row<VEC, G, K>(dw, reinterpret_cast<uint8_t *>(to), false, mine, t);
+      store_row<VEC, G, K>(db, reinterpret_cast<uint8_t *>(to + a.cols), false, mine, t);
     } else {  // one unit: its sums are the gradients
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int j = column<VEC, G>(base, t, k, e);
-          if (j < cols && a.dweight) store_any(a.dweight, j, a.grad_bf16 != 0, dw[k][e]);
-          if (j < cols && a.dbias) store_any(a.dbias, j, a.grad_bf16 != 0, db[k][e]);
+          if (j < cols && a.dweight) store_any(a.dweight, j, a.grad_bf16 != 0, element(dw[k], e));
+          if (j < cols && a.dbias) store_any(a.dbias, j, a.grad_bf16 != 0, element(db[k], e));
         }
     }
   }
-  if constexpr (CLUSTER) cooperative_groups::this_cluster().sync();
+  if constexpr (CLUSTER) {
+    __syncwarp();
+    tc::cluster_sync();
+  }
+  end_block(sh, a);
 }
 
 // dweight | dbias [cols] from partial [units][2][cols]: 32 columns of one of the
-// two to a block, its 8 warps each adding every eighth unit, then the warps' sums
+// two to a block, its 32 warps each adding every 32nd unit, then the warps' sums
 // in order.
-constexpr int kSumThreads = 256;
+constexpr int kSumThreads = 1024;
 
 __global__ void __launch_bounds__(kSumThreads) column_sum_kernel(const float *partial, int64_t units, int64_t cols,
                                                                  void *dweight, void *dbias, int32_t bf16) {
@@ -145,52 +162,45 @@ __global__ void __launch_bounds__(kSumThreads) column_sum_kernel(const float *pa
   }
 }
 
-template <int XK, bool YB>
-const void *vector_kernel(int index) {
+// The narrowest shape that holds a row; two chunks a thread at most, whose sums and
+// values take 64 registers.
+//   columns <=  512   one warp, 2 chunks
+//           <= 2048   128 threads, 2 chunks (1 up to 1024)
+//           <= 4096   256 threads, 2 chunks
+//           <= 8192   512 threads, 2 chunks; above: clusters of 2, 4 or 8 such blocks
+Shape shape_of(int64_t cols) {
+  if (cols <= 512) return {32, 2, 1, 0};
+  if (cols <= 1024) return {128, 1, 1, 1};
+  if (cols <= 2048) return {128, 2, 1, 2};
+  if (cols <= 4096) return {256, 2, 1, 3};
+  const int cluster = cluster_of(cols, 8192);
+  return {512, 2, cluster, cluster > 1 ? 5 : 4};
+}
+
+template <int XK, bool YB, bool VEC>
+const void *kernel_of(int index) {
   switch (index) {
-    case 0: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, true, 32, 2, false>);
-    case 1: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, true, 128, 1, false>);
-    case 2: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, true, 256, 1, false>);
-    case 3: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, true, 256, 2, false>);
-    case 4: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, true, 512, 2, false>);
-    default: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, true, 512, 2, true>);
+    case 0: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 32, 2, false>);
+    case 1: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 128, 1, false>);
+    case 2: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 128, 2, false>);
+    case 3: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 256, 2, false>);
+    case 4: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 512, 2, false>);
+    default: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 512, 2, true>);
   }
 }
 
-const void *kernel_for(const Shape &s, bool vec, int kind, bool y_bf16) {
-  if (!vec) {
-    switch (s.index) {
-      case 0: return reinterpret_cast<const void *>(&backward_kernel<X_F32, false, false, 32, 2, false>);
-      case 1: return reinterpret_cast<const void *>(&backward_kernel<X_F32, false, false, 128, 2, false>);
-      case 4: return reinterpret_cast<const void *>(&backward_kernel<X_F32, false, false, 512, 2, false>);
-      default: return reinterpret_cast<const void *>(&backward_kernel<X_F32, false, false, 512, 2, true>);
-    }
-  }
+const void *kernel_for(int index, bool vec, int kind, bool y_bf16) {
+  if (!vec) return kernel_of<X_F32, false, false>(index);
   switch (kind) {
-    case X_F32: return y_bf16 ? vector_kernel<X_F32, true>(s.index) : vector_kernel<X_F32, false>(s.index);
-    case X_BF16: return y_bf16 ? vector_kernel<X_BF16, true>(s.index) : vector_kernel<X_BF16, false>(s.index);
-    default: return y_bf16 ? vector_kernel<X_ACT8, true>(s.index) : vector_kernel<X_ACT8, false>(s.index);
+    case X_F32: return y_bf16 ? kernel_of<X_F32, true, true>(index) : kernel_of<X_F32, false, true>(index);
+    case X_BF16: return y_bf16 ? kernel_of<X_BF16, true, true>(index) : kernel_of<X_BF16, false, true>(index);
+    default: return y_bf16 ? kernel_of<X_ACT8, true, true>(index) : kernel_of<X_ACT8, false, true>(index);
   }
-}
-
-// Units (blocks or clusters) of a call: as many as are resident, about 512
-// threads an SM.  An upper bound over both kinds of kernel serves the workspace.
-int64_t units_for(int64_t rows, const Shape &s, int sms) {
-  const int64_t per_block = s.threads / s.group;
-  const int64_t need = (rows + per_block - 1) / per_block;
-  int64_t most = (int64_t)sms * (512 / s.threads) / s.cluster;
-  if (most < 1) most = 1;
-  return need < most ? need : most;
 }
 
 int64_t workspace_bytes_for(const fsdp_norm_desc_t *d) {
   const int sms = device_sms() > 0 ? device_sms() : 256;
-  int64_t units = 0;
-  for (int vec = 0; vec < 2; ++vec) {
-    const int64_t n = units_for(d->rows, shape_of(d->cols, vec != 0), sms);
-    if (n > units) units = n;
-  }
-  return units * 2 * d->cols * 4;
+  return units_of(d->rows, shape_of(d->cols), sms, kMostThreads) * 2 * d->cols * 4;
 }
 
 }  // namespace
@@ -247,34 +257,27 @@ fsdp_status_t fsdp_layer_norm_backward(const fsdp_norm_desc_t *d, const void *dy
     return FSDP_OK;
   }
   Args a = {};
-  a.rows = d->rows, a.cols = d->cols, a.ld_x = d->ld_x, a.ld_y = d->ld_y, a.ld_dx = d->ld_dx;
-  a.groups = act8_groups(d->cols);
-  a.x = x;
-  a.x_kind = act8 ? X_ACT8 : d->x_dtype == FSDP_DTYPE_BF16 ? X_BF16 : X_F32;
-  if (act8) a.x_scales = static_cast<const uint8_t *>(x) + d->rows * a.groups * kActGroup;
-  a.weight = weight, a.dy = dy, a.dx = dx, a.dweight = dweight, a.dbias = dbias;
+  a.rows = d->rows, a.cols = d->cols, a.ld_dx = d->ld_dx;
+  set_x(a, d, x);
+  a.in[2] = {static_cast<const uint8_t *>(dy), d->ld_y * ysize, (int32_t)ysize, 0};
+  a.weight = weight, a.dx = dx, a.dweight = dweight, a.dbias = dbias;
   a.mean = const_cast<float *>(mean), a.rstd = const_cast<float *>(rstd);
   a.y_bf16 = d->y_dtype == FSDP_DTYPE_BF16;
   a.dx_bf16 = dx && d->dx_dtype == FSDP_DTYPE_BF16;
   a.param_bf16 = d->param_dtype == FSDP_DTYPE_BF16;
   a.grad_bf16 = gsize == 2;
   a.inv_cols = 1.0f / (float)d->cols;
-  auto rows_aligned = [&](const void *p, int64_t ld, int64_t size) {
-    return aligned16(p) && (d->rows == 1 || ld * size % 16 == 0);
-  };
-  const bool vec = d->cols % 8 == 0 && (act8 || rows_aligned(x, d->ld_x, dtype_bytes(d->x_dtype))) &&
-                   rows_aligned(dy, d->ld_y, ysize) && (!dx || rows_aligned(dx, d->ld_dx, dxsize)) && aligned16(weight);
-  const Shape sh = shape_of(d->cols, vec);
+  const bool vec = d->cols % 8 == 0 && (act8 || rows_aligned(x, d->rows, d->ld_x, dtype_bytes(d->x_dtype))) &&
+                   rows_aligned(dy, d->rows, d->ld_y, ysize) && (!dx || rows_aligned(dx, d->rows, d->ld_dx, dxsize)) &&
+                   aligned16(weight);
+  const Shape sh = shape_of(d->cols);
   const int sms = device_sms();
-  const int64_t units = units_for(d->rows, sh, sms > 0 ? sms : 1);
-  a.partial = units > 1 ? static_cast<float *>(workspace) : nullptr;
-  void *args[] = {&a};
-  st = launched(launch_kernel(kernel_for(sh, vec, a.x_kind, a.y_bf16 != 0), dim3((unsigned)(units * sh.cluster)),
-                              dim3((unsigned)sh.threads), args, 0, s, true, sh.cluster));
-  if (st != FSDP_OK) return st;
+  const Launch l = plan_launch(a, sh, sms > 0 ? sms : 1, kMostThreads, 1, 2);
+  a.partial = l.units > 1 ? static_cast<float *>(workspace) : nullptr;
+  if ((st = run(kernel_for(sh.index, vec, a.x_kind, a.y_bf16 != 0), a, l, sh, s)) != FSDP_OK) return st;
   if (a.partial && (dweight || dbias)) {
     const float *partial = a.partial;
-    int64_t n = units, cols = d->cols;
+    int64_t n = l.units, cols = d->cols;
     int32_t bf16 = a.grad_bf16;
     void *sum_args[] = {&partial, &n, &cols, &dweight, &dbias, &bf16};
     st = launched(launch_kernel(reinterpret_cast<const void *>(&column_sum_kernel), dim3((unsigned)((cols + 31) / 32), 2),

@@ -31,6 +31,13 @@ inline fsdp_status_t launched(cudaError_t e) {
 
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
+// Widest store that every row's start allows: 32, 16 or 0 bytes (elements one by one).
+inline int row_width(const void *p, int64_t rows, int64_t ld, int64_t size) {
+  for (int w = 32; w >= 16; w /= 2)
+    if ((uintptr_t)p % w == 0 && (rows <= 1 || ld * size % w == 0)) return w;
+  return 0;
+}
+
 // Launch, optionally letting it start while the previous kernel on the stream
 // drains (such kernels call wait_for_previous() before they touch memory), and
 // optionally in clusters along x.
@@ -62,29 +69,47 @@ __device__ __forceinline__ void store_any(void *p, int64_t j, bool bf16, float v
     static_cast<float *>(p)[j] = v;
 }
 
-// Eight consecutive elements, 16-byte aligned, of either dtype.
-__device__ __forceinline__ void store8(void *p, int64_t j, bool bf16, const float (&v)[8]) {
+// One whole 32-byte sector.
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Eight consecutive elements as four pairs, 16-byte aligned, of either dtype.
+__device__ __forceinline__ void store8(void *p, int64_t j, bool bf16, const float2 (&v)[4]) {
   if (bf16) {
     *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + j) =
-        make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+        make_uint4(bf16_pair(v[0].x, v[0].y), bf16_pair(v[1].x, v[1].y), bf16_pair(v[2].x, v[2].y), bf16_pair(v[3].x, v[3].y));
   } else {
     float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + j);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    q[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    q[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
   }
 }
-__device__ __forceinline__ void unpack8(uint4 r, float (&v)[8]) {
-  v[0] = bf16_low(r.x), v[1] = bf16_high(r.x), v[2] = bf16_low(r.y), v[3] = bf16_high(r.y);
-  v[4] = bf16_low(r.z), v[5] = bf16_high(r.z), v[6] = bf16_low(r.w), v[7] = bf16_high(r.w);
+__device__ __forceinline__ void unpack8(uint4 r, float2 (&v)[4]) {
+  v[0] = make_float2(bf16_low(r.x), bf16_high(r.x)), v[1] = make_float2(bf16_low(r.y), bf16_high(r.y));
+  v[2] = make_float2(bf16_low(r.z), bf16_high(r.z)), v[3] = make_float2(bf16_low(r.w), bf16_high(r.w));
 }
-__device__ __forceinline__ void load8(const void *p, int64_t j, bool bf16, float (&v)[8]) {
+__device__ __forceinline__ void load8(const void *p, int64_t j, bool bf16, float2 (&v)[4]) {
   if (bf16) {
     unpack8(*reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + j), v);
   } else {
     const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + j);
     const float4 a = q[0], b = q[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w), v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
   }
+}
+// Element e of pairs, for code that goes element by element.
+template <int N>
+__device__ __forceinline__ float &element(float2 (&v)[N], int e) {
+  return e % 2 ? v[e / 2].y : v[e / 2].x;
+}
+template <int N>
+__device__ __forceinline__ float element(const float2 (&v)[N], int e) {
+  return e % 2 ? v[e / 2].y : v[e / 2].x;
 }
 #endif
 
