@@ -308,18 +308,26 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if (!(ok = tc::bar_wait(tc::smem(&sh.tmem_full[acc]), acc_phase, a.wait_limit_ns, stop))) break;
       tc::fence_after();
       const uint32_t from = tmem + acc * kTileN + ((uint32_t)quarter * 32u << 16);
+      // This warp has read its part of the accumulator: the next tile may overwrite it
+      // while this one's results are still being worked out and stored.
+      auto drained = [&] {
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive_relaxed(tc::at_rank(tc::smem(&sh.tmem_empty[acc]), 0));
+      };
       const bool some = u.k1 > u.k0;  // an empty part of a K loop: the sum is 0
       if constexpr (MODE == FORWARD || MODE == RECOMPUTE) {
         const int64_t row = ((int64_t)u.m * CG + rank) * kTileM + quarter * 32 + lane;
 #pragma unroll 1
         for (int c = side * (kTileN / 4); c < (side + 1) * (kTileN / 4); c += 32) {
           const int64_t col = (int64_t)u.n * (kTileN / 2) + c;
-          if (col >= a.n) break;
           uint32_t g[32], up[32];
           __syncwarp();
           tc::tmem_load32(from + c, g);
           tc::tmem_load32(from + kTileN / 2 + c, up);
           tc::tmem_load_wait();
+          if (c + 32 == (side + 1) * (kTileN / 4)) drained();
+          if (col >= a.n) continue;
           if (row < a.m) gated_run<MODE>(a, g, up, row, col);
         }
       } else {
@@ -328,11 +336,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll 1
         for (int c = side * (kTileN / 2); c < (side + 1) * (kTileN / 2); c += 32) {
           const int64_t col = (int64_t)u.n * kTileN + c;
-          if (col >= a.n) break;
           uint32_t r[32];
           __syncwarp();
           tc::tmem_load32(from + c, r);
           tc::tmem_load_wait();
+          if (c + 32 == (side + 1) * (kTileN / 2)) drained();
+          if (col >= a.n) continue;
           float2 v[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = some ? pair_at(r, e) : both(0.0f);
@@ -346,14 +355,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             }
           }
         }
-      }
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (CG == 1)
-          tc::bar_arrive(tc::smem(&sh.tmem_empty[acc]));
-        else
-          tc::bar_arrive_cluster(tc::at_rank(tc::smem(&sh.tmem_empty[acc]), 0));
       }
       if (++acc == kAccumulators) acc = 0, acc_phase ^= 1u;
     }
