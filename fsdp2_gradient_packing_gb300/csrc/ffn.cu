@@ -2,8 +2,8 @@
 // plan of the launches, and the kernels around the products.
 //
 // Forward: one launch.  Backward: dg and du (from what was kept, one pass over
-// dh, gate and up; or as the epilogue of the forward product), then dx, then both
-// weight gradients.  dg and du pass through the workspace in BF16.
+// dh, gate and up; or as the epilogue of the forward product), then dx and both
+// weight gradients in one launch.  dg and du pass through the workspace in BF16.
 #include <cuda.h>
 
 #include <mutex>
@@ -60,13 +60,34 @@ bool encode(CUtensorMap *map, const Operand &o, int box_rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Copy of a matrix whose rows start anywhere, to rows of `pitch` elements.
-__global__ void __launch_bounds__(kThreads) copy_rows_kernel(const uint16_t *src, int64_t ld, uint16_t *dst, int64_t pitch,
-                                                             int64_t rows, int64_t cols) {
+// Copies of up to three matrices whose rows start anywhere, to rows of `pitch`
+// elements: one warp to a row at a time, four elements a lane in flight.
+struct CopyArgs {
+  const uint16_t *src[3];
+  uint16_t *dst[3];
+  int64_t ld[3], rows[3];
+  int64_t pitch, cols;
+};
+__global__ void __launch_bounds__(kThreads) copy_rows_kernel(const __grid_constant__ CopyArgs a) {
+  const int lane = threadIdx.x & 31;
   wait_for_previous();
   let_next_start();
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int64_t j = threadIdx.x; j < cols; j += kThreads) dst[r * pitch + j] = src[r * ld + j];
+  const int64_t all = a.rows[0] + a.rows[1] + a.rows[2];
+  for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; i < all; i += (int64_t)gridDim.x * (kThreads / 32)) {
+    const int which = i < a.rows[0] ? 0 : i < a.rows[0] + a.rows[1] ? 1 : 2;
+    const int64_t r = which == 0 ? i : which == 1 ? i - a.rows[0] : i - a.rows[0] - a.rows[1];
+    const uint16_t *src = a.src[which] + r * a.ld[which];
+    uint16_t *dst = a.dst[which] + r * a.pitch;
+    for (int64_t j = lane; j < a.cols; j += 128) {
+      uint16_t v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (j + u * 32 < a.cols) v[u] = src[j + u * 32];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (j + u * 32 < a.cols) dst[j + u * 32] = v[u];
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -82,52 +103,65 @@ struct SlopeArgs {
 };
 
 // Bound: HBM, 2 + 33/16 + 4 bytes an element from 8-bit checkpoints.  Eight columns
-// to a thread.
+// make a unit; a thread has kUnits of them in flight.
+constexpr int kUnits = 2;
+
 __global__ void __launch_bounds__(kThreads) slope_kernel(const __grid_constant__ SlopeArgs a) {
   const int64_t per_row = (a.f + 7) / 8, total = a.rows * per_row;
   wait_for_previous();
   let_next_start();
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-    int64_t row, at;
-    if ((uint64_t)total >> 32 == 0)
-      row = (uint32_t)i / (uint32_t)per_row, at = (uint32_t)i % (uint32_t)per_row;
-    else
-      row = i / per_row, at = i % per_row;
-    const int64_t j = at * 8;
-    const bool whole = j + 8 <= a.f;
-    float2 d[4], g[4], u[4];
-    auto load = [&](float2(&v)[4], const void *p, int64_t at, bool vec) {
-      if (whole && vec) {
-        load8(p, at, true, v);
-      } else {
+  const int64_t stride = (int64_t)gridDim.x * (kThreads * kUnits);
+  for (int64_t i0 = (int64_t)blockIdx.x * (kThreads * kUnits) + threadIdx.x; i0 < total; i0 += stride) {
+    int64_t row[kUnits], col[kUnits];
+    uint4 d[kUnits], g[kUnits], u[kUnits];  // eight BF16 values, or of g and u eight codes and the scale byte
 #pragma unroll
-        for (int e = 0; e < 8; ++e) element(v, e) = j + e < a.f ? load_any(p, at + e, true) : 0.0f;
-      }
-    };
-    load(d, a.dh, row * a.ld_dh + j, a.dh_vec != 0);
-    if (a.act8) {
-      const int64_t c = row * a.groups * kActGroup + j, s = row * a.groups + j / (int)kActGroup;
-      const uint2 p = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.gate) + c);
-      const uint2 q = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.up) + c);
-      const float2 sg = both(act8_scale(a.scales[0][s])), su = both(act8_scale(a.scales[1][s]));
+    for (int q = 0; q < kUnits; ++q) {
+      const int64_t i = i0 + q * kThreads;
+      if (i >= total) continue;
+      if ((uint64_t)total >> 32 == 0)
+        row[q] = (uint32_t)i / (uint32_t)per_row, col[q] = (uint32_t)i % (uint32_t)per_row * 8;
+      else
+        row[q] = i / per_row, col[q] = (i - row[q] * per_row) * 8;
+      const int n = (int)(a.f - col[q] < 8 ? a.f - col[q] : 8);
+      auto load = [&](const void *p, int64_t ld, bool vec) {
+        const uint16_t *from = static_cast<const uint16_t *>(p) + row[q] * ld + col[q];
+        if (vec && n == 8) return __ldcs(reinterpret_cast<const uint4 *>(from));
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = e < n ? from[e] : 0u;
+        return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+      };
+      auto load_codes = [&](const void *p, const uint8_t *scales) {
+        const uint2 c = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(p) + row[q] * a.groups * kActGroup + col[q]));
+        return make_uint4(c.x, c.y, scales[row[q] * a.groups + col[q] / (int)kActGroup], 0);
+      };
+      d[q] = load(a.dh, a.ld_dh, a.dh_vec != 0);
+      g[q] = a.act8 ? load_codes(a.gate, a.scales[0]) : load(a.gate, a.ld_kept, a.kept_vec != 0);
+      u[q] = a.act8 ? load_codes(a.up, a.scales[1]) : load(a.up, a.ld_kept, a.kept_vec != 0);
+    }
+#pragma unroll
+    for (int q = 0; q < kUnits; ++q) {
+      if (i0 + q * kThreads >= total) continue;
+      float2 dv[4], gv[4], uv[4];
+      unpack8(d[q], dv);
+      auto values = [&](float2(&v)[4], const uint4 &r) {
+        if (!a.act8) return unpack8(r, v);
+        const float2 scale = both(act8_scale(r.z));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __fmul2_rn(act8_codes_of(act8_biased(e < 2 ? r.x : r.y), e % 2), scale);
+      };
+      values(gv, g[q]);
+      values(uv, u[q]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        g[e] = __fmul2_rn(act8_codes_of(act8_biased(e < 2 ? p.x : p.y), e % 2), sg);
-        u[e] = __fmul2_rn(act8_codes_of(act8_biased(e < 2 ? q.x : q.y), e % 2), su);
+        const float2 p = act_of<true>(gv[e].x, a.act), r = act_of<true>(gv[e].y, a.act);
+        gv[e] = __fmul2_rn(__fmul2_rn(dv[e], uv[e]), make_float2(p.y, r.y));
+        uv[e] = __fmul2_rn(dv[e], make_float2(p.x, r.x));
       }
-    } else {
-      load(g, a.gate, row * a.ld_kept + j, a.kept_vec != 0);
-      load(u, a.up, row * a.ld_kept + j, a.kept_vec != 0);
+      // The pitch holds whole vectors; what lies past the row's end is never read.
+      store8(a.dg, row[q] * a.pitch + col[q], true, gv);
+      store8(a.du, row[q] * a.pitch + col[q], true, uv);
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 p = act_of<true>(g[e].x, a.act), q = act_of<true>(g[e].y, a.act);
-      g[e] = __fmul2_rn(__fmul2_rn(d[e], u[e]), make_float2(p.y, q.y));
-      u[e] = __fmul2_rn(d[e], make_float2(p.x, q.x));
-    }
-    // The pitch holds whole vectors; what lies past the row's end is never read.
-    store8(a.dg, row * a.pitch + j, true, g);
-    store8(a.du, row * a.pitch + j, true, u);
   }
 }
 
@@ -186,29 +220,86 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 // ---------------------------------------------------------------------------
 // Plan
 // ---------------------------------------------------------------------------
-struct Tiling {
-  bool pair;
-  int64_t m_tiles, n_tiles, m_half, k_blocks, splits;
-};
+// Rows of a tile: one block's 128, or a pair's 256.
+bool pairs(int64_t rows) { return rows > kTileM; }
+int64_t tile_rows(bool pair) { return pair ? 2 * kTileM : kTileM; }
 
-// The tiles of one product, and how often its K loop is split so that there is
-// work for every SM.
-Tiling tiling(Mode mode, int64_t m, int64_t n, int64_t k, int sms) {
-  Tiling t = {};
-  t.pair = true;
-  const int64_t tile_m = t.pair ? 2 * kTileM : kTileM, tile_n = mode == FORWARD || mode == RECOMPUTE ? 128 : 256;
-  t.m_half = blocks_of(m, tile_m);
-  t.m_tiles = mode == DW ? 2 * t.m_half : t.m_half;
-  t.n_tiles = blocks_of(n, tile_n);
-  t.k_blocks = mode == DX ? 2 * blocks_of(k, kTileK) : blocks_of(k, kTileK);
-  t.splits = 1;
-  if (mode == DX || mode == DW) {
-    const int64_t workers = t.pair ? sms / 2 : sms, tiles = t.m_tiles * t.n_tiles;
-    int64_t s = workers / tiles;
-    if (s > t.k_blocks / 8) s = t.k_blocks / 8;
-    if (s > 16) s = 16;
-    if (s > 1) t.splits = blocks_of(t.k_blocks, blocks_of(t.k_blocks, s));  // no part is empty
+// Row tiles of a band (see unit_at): 4,096 rows.
+int32_t band(int64_t tile_m) { return (int32_t)(4096 / tile_m); }
+
+// The gate / up tile: as many features as fill the workers in the fewest, fullest
+// rounds.  A tile costs its features and, for its x slices and its start, about 24
+// more; whole groups of 32, so that a checkpoint's groups stay within a tile.
+struct GatedTiles {
+  bool pair;
+  Grid grid;
+  int32_t tile_n;
+};
+GatedTiles gated_tiles(int64_t rows, int64_t f, int64_t d, int sms) {
+  GatedTiles t = {};
+  t.pair = pairs(rows);
+  const int64_t m = blocks_of(rows, tile_rows(t.pair)), workers = t.pair ? sms / 2 : sms;
+  int64_t best = INT64_MAX;
+  for (int64_t features = 128; features >= 32; features -= 32) {
+    const int64_t n = blocks_of(f, features), cost = blocks_of(m * n, workers) * (features + 24);
+    if (cost >= best) continue;
+    best = cost;
+    t.tile_n = (int32_t)(2 * features);
+    t.grid = {(int32_t)m, (int32_t)n, 1, band(tile_rows(t.pair)), (int32_t)blocks_of(d, kTileK)};
   }
+  return t;
+}
+
+// The backward products: tiles of 256 columns.  K loops are split where that
+// shortens the longest worker's share, counted in K blocks (a K block of a pair takes
+// about 0.27 us): a unit costs its K blocks (an epilogue's 10 at least), and joining
+// parts a launch (15) and the parts' bytes, written and read, at about 1.2 MB a block.
+// A call that wants only some of the gradients splits as if it wanted all.
+struct BackwardTiles {
+  bool pair;
+  Grid grid[2];       // weight gradients, dx
+  int64_t half[2];    // tiles of one weight's rows; K blocks of one half of dx
+};
+BackwardTiles backward_tiles(int64_t rows, int64_t d, int64_t f, int sms) {
+  BackwardTiles t = {};
+  t.pair = pairs(rows);
+  const int64_t tile_m = tile_rows(t.pair), n = blocks_of(d, 256), workers = t.pair ? sms / 2 : sms;
+  t.half[0] = blocks_of(f, tile_m), t.half[1] = blocks_of(f, kTileK);
+  const int64_t tiles[2] = {2 * t.half[0] * n, blocks_of(rows, tile_m) * n};
+  const int64_t k[2] = {blocks_of(rows, kTileK), 2 * t.half[1]};
+  const int64_t bytes[2] = {2 * f * d * 4, rows * d * 4};  // of one part
+  constexpr int kChoices = 8;
+  const int64_t by[kChoices] = {1, 2, 3, 4, 6, 8, 12, 16};
+  // Cost of a unit, units, and cost of the join for each choice.
+  int64_t cost[2][kChoices], units[2][kChoices], join[2][kChoices];
+  for (int w = 0; w < 2; ++w)
+    for (int c = 0; c < kChoices; ++c) {
+      const int64_t per = blocks_of(k[w], by[c]);
+      cost[w][c] = (per > 10 ? per : 10) + 1;
+      units[w][c] = tiles[w] * by[c];
+      join[w][c] = c == 0 ? 0 : 15 + 2 * by[c] * bytes[w] / 1200000;
+      if (c > 0 && (per < 4 || blocks_of(k[w], per) != by[c])) units[w][c] = 0;  // parts too short, or empty ones
+    }
+  const int choices = tiles[0] + tiles[1] > 8 * workers ? 1 : kChoices;
+  int64_t best = INT64_MAX;
+  int parts[2] = {0, 0};
+  for (int p = 0; p < choices; ++p)
+    for (int q = 0; q < choices; ++q) {
+      const int64_t u0 = units[0][p], u = u0 + units[1][q];
+      if (u0 == 0 || u == u0) continue;
+      // Worker i takes units i, i + workers, ...: shares change at three workers only.
+      const int64_t at[3] = {0, u0 % workers, u % workers};
+      int64_t longest = 0;
+      for (int64_t i : at) {
+        const int64_t first = (u0 - i + workers - 1) / workers, all = (u - i + workers - 1) / workers;
+        const int64_t share = first * cost[0][p] + (all - first) * cost[1][q];
+        longest = share > longest ? share : longest;
+      }
+      const int64_t total = longest + join[0][p] + join[1][q];
+      if (total < best) best = total, parts[0] = p, parts[1] = q;
+    }
+  t.grid[0] = {(int32_t)(2 * t.half[0]), (int32_t)n, (int32_t)by[parts[0]], band(tile_m), (int32_t)k[0]};
+  t.grid[1] = {(int32_t)blocks_of(rows, tile_m), (int32_t)n, (int32_t)by[parts[1]], band(tile_m), (int32_t)k[1]};
   return t;
 }
 
@@ -216,7 +307,8 @@ struct Plan {
   int sms;
   bool stage_x, stage_wg, stage_wu;
   int64_t d_pitch, f_pitch;
-  int64_t at_x, at_wg, at_wu, at_dg, at_du, at_partial, bytes;
+  BackwardTiles tiles;
+  int64_t at_x, at_wg, at_wu, at_dg, at_du, at_partial[2], bytes;
 };
 
 bool rows_off(int64_t rows, int64_t ld, bool base) { return base || (rows > 1 && ld % 8 != 0); }
@@ -225,6 +317,7 @@ Plan plan_of(const fsdp_ffn_desc_t *d, bool backward) {
   Plan p = {};
   p.sms = device_sms() > 0 ? device_sms() : 160;
   p.d_pitch = up_to(d->d, 8), p.f_pitch = up_to(d->f, 16);
+  if (!backward && d->rows <= kFewRows) return p;  // reads its operands where they are
   p.stage_x = d->x_dtype == FSDP_ACT8 || rows_off(d->rows, d->ld_x, d->unaligned & 1);
   p.stage_wg = rows_off(d->f, d->ld_w_gate, d->unaligned & 2);
   p.stage_wu = rows_off(d->f, d->ld_w_up, d->unaligned & 4);
@@ -240,10 +333,12 @@ Plan plan_of(const fsdp_ffn_desc_t *d, bool backward) {
   if (backward && d->rows > 0) {
     p.at_dg = take(true, d->rows * p.f_pitch * 2);
     p.at_du = take(true, d->rows * p.f_pitch * 2);
-    const Tiling x = tiling(DX, d->rows, d->d, d->f, p.sms), w = tiling(DW, d->f, d->d, d->rows, p.sms);
-    const int64_t px = x.splits > 1 ? x.splits * d->rows * d->d * 4 : 0;
-    const int64_t pw = w.splits > 1 ? w.splits * 2 * d->f * d->d * 4 : 0;
-    p.at_partial = take(true, px > pw ? px : pw);
+    p.tiles = backward_tiles(d->rows, d->d, d->f, p.sms);
+    const int64_t rows[2] = {2 * d->f, d->rows};
+    for (int w = 0; w < 2; ++w) {
+      const int64_t parts = p.tiles.grid[w].splits;
+      p.at_partial[w] = take(parts > 1, parts * rows[w] * d->d * 4);
+    }
   }
   p.bytes = at;
   return p;
@@ -307,64 +402,78 @@ struct Call {
   cudaStream_t stream;
   Operand x, wg, wu;
 
-  fsdp_status_t copy(Operand &o, bool want, int64_t at) {
-    if (!want || o.rows == 0) return FSDP_OK;
-    const uint16_t *src = static_cast<const uint16_t *>(o.p);
-    uint16_t *dst = reinterpret_cast<uint16_t *>(ws + at);
-    int64_t ld = o.ld, pitch = plan.d_pitch, rows = o.rows, cols = o.cols;
-    void *args[] = {&src, &ld, &dst, &pitch, &rows, &cols};
-    const int64_t grid = rows < plan.sms * 8 ? rows : plan.sms * 8;
-    o.p = dst, o.ld = pitch;
-    return launched(launch_kernel(reinterpret_cast<const void *>(&copy_rows_kernel), dim3((unsigned)grid), dim3(kThreads),
-                                  args, 0, stream, true));
-  }
-
   fsdp_status_t stage(const void *px, const void *pwg, const void *pwu) {
     wg = {pwg, d->f, d->d, d->ld_w_gate};
     wu = {pwu, d->f, d->d, d->ld_w_up};
     x = {px, d->rows, d->d, d->ld_x};
-    fsdp_status_t st = copy(wg, plan.stage_wg, plan.at_wg);
-    if (st == FSDP_OK) st = copy(wu, plan.stage_wu, plan.at_wu);
-    if (st != FSDP_OK) return st;
+    CopyArgs a = {};
+    a.pitch = plan.d_pitch, a.cols = d->d;
+    auto copy = [&](Operand &o, bool want, int64_t at, int i) {
+      if (!want || o.rows == 0) return;
+      a.src[i] = static_cast<const uint16_t *>(o.p), a.dst[i] = reinterpret_cast<uint16_t *>(ws + at);
+      a.ld[i] = o.ld, a.rows[i] = o.rows;
+      o.p = a.dst[i], o.ld = plan.d_pitch;
+    };
+    copy(wg, plan.stage_wg, plan.at_wg, 0);
+    copy(wu, plan.stage_wu, plan.at_wu, 1);
     if (d->x_dtype == FSDP_ACT8) {
       x.p = ws + plan.at_x, x.ld = plan.d_pitch;
-      return fsdp_act8_load(px, d->rows, d->d, ws + plan.at_x, FSDP_DTYPE_BF16, plan.d_pitch,
-                            reinterpret_cast<fsdp_stream_t>(stream));
+      fsdp_status_t st = fsdp_act8_load(px, d->rows, d->d, ws + plan.at_x, FSDP_DTYPE_BF16, plan.d_pitch,
+                                        reinterpret_cast<fsdp_stream_t>(stream));
+      if (st != FSDP_OK) return st;
+    } else {
+      copy(x, plan.stage_x, plan.at_x, 2);
     }
-    return copy(x, plan.stage_x, plan.at_x);
+    const int64_t rows = a.rows[0] + a.rows[1] + a.rows[2];
+    if (rows == 0) return FSDP_OK;
+    int64_t grid = blocks_of(rows, kThreads / 32);
+    if (grid > plan.sms * 8) grid = plan.sms * 8;
+    void *args[] = {&a};
+    return launched(launch_kernel(reinterpret_cast<const void *>(&copy_rows_kernel), dim3((unsigned)grid), dim3(kThreads),
+                                  args, 0, stream, true));
   }
 
-  // One product; args' outputs and flags are set by the caller.
-  fsdp_status_t product(Mode mode, int64_t m, int64_t n, int64_t k, const Operand &a0, const Operand &a1,
-                        const Operand &b0, const Operand &b1, Args &a) {
-    const Tiling t = tiling(mode, m, n, k, plan.sms);
-    const int a_rows = mode == DW ? 64 : 128, b_rows = mode == FORWARD || mode == RECOMPUTE ? 128 : 64;
-    if (!encode(&a.a[0], a0, a_rows) || !encode(&a.a[1], a1, a_rows) || !encode(&a.b[0], b0, b_rows) ||
-        !encode(&a.b[1], b1, b_rows))
-      return fail(FSDP_ECUDA, "cuTensorMapEncodeTiled failed or is missing");
+  bool operands(Args &a, const Operand (&left)[2], int left_rows, const Operand (&right)[3], int right_rows) {
+    for (int i = 0; i < 2; ++i)
+      if (!encode(&a.a[i], left[i], left_rows)) return false;
+    for (int i = 0; i < 3; ++i)
+      if (!encode(&a.b[i], right[i], right_rows)) return false;
+    return true;
+  }
+
+  // Launches one product; args' operands, tiles and outputs are set.
+  fsdp_status_t launch(Mode mode, bool pair, Args &a) {
     cudaError_t e = status_word(&a.status);
     if (e != cudaSuccess) return fail(FSDP_ECUDA, std::string("status word: ") + cudaGetErrorString(e));
     a.wait_limit_ns = wait_limit_ns();
     a.fault = wait_fault();
     a.act = d->activation == FSDP_ACT_SILU ? SILU : GELU;
-    a.m_tiles = (int32_t)t.m_tiles, a.n_tiles = (int32_t)t.n_tiles, a.splits = (int32_t)t.splits;
-    a.raster = 16;
-    a.m_half = (int32_t)t.m_half;
-    a.k_blocks = (int32_t)t.k_blocks, a.k_half = (int32_t)(t.k_blocks / 2);
-    a.m = m, a.n = n;
-    if (t.splits > 1) a.partial = reinterpret_cast<float *>(ws + plan.at_partial);
-    fsdp_status_t st = launched(launch_product(mode, t.pair, a, plan.sms, stream));
-    if (st != FSDP_OK || t.splits == 1) return st;
+    return launched(launch_product(mode, pair, a, plan.sms, stream));
+  }
+
+  // FORWARD or RECOMPUTE.
+  fsdp_status_t gated(Mode mode, Args &a) {
+    const GatedTiles t = gated_tiles(d->rows, d->f, d->d, plan.sms);
+    if (!operands(a, {x, x}, kTileM, {wg, wu, wu}, t.tile_n / 2))
+      return fail(FSDP_ECUDA, "cuTensorMapEncodeTiled failed or is missing");
+    a.grid[0] = t.grid;
+    a.tile_n = t.tile_n;
+    a.m[0] = d->rows, a.n = d->f;
+    return launch(mode, t.pair, a);
+  }
+
+  // Adds up the parts of product w, if its K loops are split.
+  fsdp_status_t join(const Args &a, int w) {
+    if (a.grid[w].splits == 1) return FSDP_OK;
     JoinArgs j = {};
-    j.partial = a.partial;
-    j.out[0] = a.out[0], j.out[1] = a.out[1];
-    j.ld[0] = a.ld_out[0], j.ld[1] = a.ld_out[1];
-    j.rows = mode == DW ? 2 * m : m, j.half = m, j.cols = n;
-    j.splits = (int32_t)t.splits, j.bf16 = a.out_bf16;
-    j.vec = a.out_width >= 16;
+    j.partial = a.partial[w];
+    for (int i = 0; i < 2; ++i) j.out[i] = a.out[w == 1 ? 2 : i], j.ld[i] = a.ld_out[w == 1 ? 2 : i];
+    j.rows = w == 0 ? 2 * a.m[0] : a.m[1], j.half = a.m[w], j.cols = a.n;
+    j.splits = a.grid[w].splits, j.bf16 = a.out_bf16[w];
+    j.vec = a.out_width[w] >= 16;
     void *args[] = {&j};
-    const int vec = n % 4 == 0 ? 4 : 1;
-    int64_t across = blocks_of(n, (int64_t)kThreads * vec), down = j.rows;
+    const int vec = a.n % 4 == 0 ? 4 : 1;
+    int64_t across = blocks_of(a.n, (int64_t)kThreads * vec), down = j.rows;
     if (across > 64) across = 64;
     if (down > plan.sms * 64) down = plan.sms * 64;
     return launched(launch_kernel(vec == 4 ? reinterpret_cast<const void *>(&join_kernel<4>)
@@ -373,7 +482,8 @@ struct Call {
   }
 };
 
-void kept_into(const fsdp_ffn_desc_t *d, void *gate, void *up, Args &a) {
+template <class A>
+void kept_into(const fsdp_ffn_desc_t *d, void *gate, void *up, A &a) {
   a.keep = d->keep;
   a.groups = act8_groups(d->f);
   void *p[2] = {gate, up};
@@ -383,9 +493,6 @@ void kept_into(const fsdp_ffn_desc_t *d, void *gate, void *up, Args &a) {
     a.kept[i] = p[i];
   }
   a.ld_kept = d->ld_kept;
-  const int64_t ld = d->keep == FSDP_KEEP_ACT8 ? 16 : d->ld_kept;  // a checkpoint's groups are 32 bytes each
-  const int wg = row_width(gate, d->rows, ld, 2), wu = row_width(up, d->rows, ld, 2);
-  a.keep_width = wg < wu ? wg : wu;
 }
 
 }  // namespace
@@ -419,13 +526,26 @@ fsdp_status_t fsdp_gated_ffn_forward(const fsdp_ffn_desc_t *d, const void *x, co
   Call c = {d, plan_of(d, false), static_cast<uint8_t *>(workspace), reinterpret_cast<cudaStream_t>(stream), {}, {}, {}};
   if (workspace_bytes < c.plan.bytes) return fail(FSDP_EINVAL, "workspace_bytes is below fsdp_gated_ffn_workspace");
   if ((st = check_ptr(workspace, c.plan.bytes, 16, "workspace", -1)) != FSDP_OK) return st;
-  if (d->rows > 0) {
+  if (d->rows > 0 && d->rows <= kFewRows) {
+    RowsArgs a = {};
+    a.x = x, a.w_gate = w_gate, a.w_up = w_up, a.h = h;
+    a.rows = d->rows, a.d = d->d, a.f = d->f;
+    a.ld_x = d->ld_x, a.ld_gate = d->ld_w_gate, a.ld_up = d->ld_w_up, a.ld_h = d->ld_h;
+    a.act = d->activation == FSDP_ACT_SILU ? SILU : GELU;
+    kept_into(d, gate, up, a);
+    const bool vec = d->d % 8 == 0 && vec_rows(x, d->rows, d->ld_x, 2) && vec_rows(w_gate, d->f, d->ld_w_gate, 2) &&
+                     vec_rows(w_up, d->f, d->ld_w_up, 2);
+    if ((st = launched(launch_rows(a, vec, c.stream))) != FSDP_OK) return st;
+  } else if (d->rows > 0) {
     if ((st = c.stage(x, w_gate, w_up)) != FSDP_OK) return st;
     Args a = {};
     a.out[0] = h, a.ld_out[0] = d->ld_h;
-    a.out_bf16 = 1, a.out_width = row_width(h, d->rows, d->ld_h, 2);
+    a.out_width[0] = row_width(h, d->rows, d->ld_h, 2);
     kept_into(d, gate, up, a);
-    if ((st = c.product(FORWARD, d->rows, d->f, d->d, c.x, c.x, c.wg, c.wu, a)) != FSDP_OK) return st;
+    const int64_t ld = d->keep == FSDP_KEEP_ACT8 ? 16 : d->ld_kept;  // a checkpoint's groups are 32 bytes each
+    const int wg = row_width(gate, d->rows, ld, 2), wu = row_width(up, d->rows, ld, 2);
+    a.keep_width = wg < wu ? wg : wu;
+    if ((st = c.gated(FORWARD, a)) != FSDP_OK) return st;
   }
   clear_error();
   return FSDP_OK;
@@ -474,9 +594,9 @@ fsdp_status_t fsdp_gated_ffn_backward(const fsdp_ffn_desc_t *d, const void *dh, 
     Args a = {};
     a.out[0] = dg, a.out[1] = du;
     a.ld_out[0] = a.ld_out[1] = c.plan.f_pitch;
-    a.out_bf16 = 1, a.out_width = row_width(c.ws, d->rows, c.plan.f_pitch, 2);
+    a.out_width[0] = row_width(c.ws, d->rows, c.plan.f_pitch, 2);
     a.dh = dh, a.ld_dh = d->ld_h, a.dh_vec = vec_rows(dh, d->rows, d->ld_h, 2);
-    if ((st = c.product(RECOMPUTE, d->rows, d->f, d->d, c.x, c.x, c.wg, c.wu, a)) != FSDP_OK) return st;
+    if ((st = c.gated(RECOMPUTE, a)) != FSDP_OK) return st;
   } else {
     SlopeArgs s = {};
     s.dh = dh, s.gate = gate, s.up = up;
@@ -489,7 +609,7 @@ fsdp_status_t fsdp_gated_ffn_backward(const fsdp_ffn_desc_t *d, const void *dh, 
     s.act = d->activation == FSDP_ACT_SILU ? SILU : GELU;
     s.dh_vec = vec_rows(dh, d->rows, d->ld_h, 2);
     s.kept_vec = vec_rows(gate, d->rows, d->ld_kept, 2) && vec_rows(up, d->rows, d->ld_kept, 2);
-    int64_t grid = blocks_of(d->rows * blocks_of(d->f, 8), kThreads);
+    int64_t grid = blocks_of(d->rows * blocks_of(d->f, 8), kThreads * kUnits);
     if (grid > (int64_t)c.plan.sms * 64) grid = (int64_t)c.plan.sms * 64;
     void *args[] = {&s};
     st = launched(launch_kernel(reinterpret_cast<const void *>(&slope_kernel), dim3((unsigned)grid), dim3(kThreads), args, 0,
@@ -497,23 +617,27 @@ fsdp_status_t fsdp_gated_ffn_backward(const fsdp_ffn_desc_t *d, const void *dh, 
     if (st != FSDP_OK) return st;
   }
   const Operand og = {dg, d->rows, d->f, c.plan.f_pitch}, ou = {du, d->rows, d->f, c.plan.f_pitch};
-  if (dx) {
-    Args a = {};
-    a.out[0] = a.out[1] = dx;
-    a.ld_out[0] = a.ld_out[1] = d->ld_dx;
-    a.out_bf16 = d->dx_dtype == FSDP_DTYPE_BF16;
-    a.out_width = row_width(dx, d->rows, d->ld_dx, xsize);
-    if ((st = c.product(DX, d->rows, d->d, d->f, og, ou, c.wg, c.wu, a)) != FSDP_OK) return st;
+  Args a = {};
+  if (!c.operands(a, {og, ou}, 64, {c.wg, c.wu, c.x}, 64))
+    return fail(FSDP_ECUDA, "cuTensorMapEncodeTiled failed or is missing");
+  const BackwardTiles &t = c.plan.tiles;
+  a.out[0] = dw_gate, a.out[1] = dw_up, a.out[2] = dx;
+  a.ld_out[0] = d->ld_dw_gate, a.ld_out[1] = d->ld_dw_up, a.ld_out[2] = d->ld_dx;
+  a.m[0] = d->f, a.m[1] = d->rows, a.n = d->d;
+  a.out_bf16[0] = d->dw_dtype == FSDP_DTYPE_BF16, a.out_bf16[1] = d->dx_dtype == FSDP_DTYPE_BF16;
+  const int rg = row_width(dw_gate, d->f, d->ld_dw_gate, wsize), ru = row_width(dw_up, d->f, d->ld_dw_up, wsize);
+  a.out_width[0] = rg < ru ? rg : ru, a.out_width[1] = row_width(dx, d->rows, d->ld_dx, xsize);
+  for (int w = 0; w < 2; ++w) {
+    a.grid[w] = t.grid[w], a.half[w] = (int32_t)t.half[w];
+    if (t.grid[w].splits == 1) continue;
+    a.partial[w] = reinterpret_cast<float *>(c.ws + c.plan.at_partial[w]);
+    a.partial_width[w] = row_width(a.partial[w], 2, d->d, 4);
   }
-  if (dw_gate) {
-    Args a = {};
-    a.out[0] = dw_gate, a.out[1] = dw_up;
-    a.ld_out[0] = d->ld_dw_gate, a.ld_out[1] = d->ld_dw_up;
-    a.out_bf16 = d->dw_dtype == FSDP_DTYPE_BF16;
-    const int rg = row_width(dw_gate, d->f, d->ld_dw_gate, wsize), ru = row_width(dw_up, d->f, d->ld_dw_up, wsize);
-    a.out_width = rg < ru ? rg : ru;
-    if ((st = c.product(DW, d->f, d->d, d->rows, og, ou, c.x, c.x, a)) != FSDP_OK) return st;
-  }
+  if (!dw_gate) a.grid[0].m = 0;  // no tiles
+  if (!dx) a.grid[1].m = 0;
+  if ((st = c.launch(BACKWARD, t.pair, a)) != FSDP_OK) return st;
+  for (int w = 0; w < 2; ++w)
+    if (a.grid[w].m > 0 && (st = c.join(a, w)) != FSDP_OK) return st;
   clear_error();
   return FSDP_OK;
 }

@@ -1,20 +1,22 @@
 // The gated feed-forward block's products on the tensor cores: one persistent
-// kernel, four uses.  Included by the ffn*.cu files only.
+// kernel, three uses.  Included by the ffn*.cu files only.
 //
 //   FORWARD   [g | u] = x [Wg | Wu]^T          epilogue: h = act(g) u, kept copies
 //   RECOMPUTE the same product                 epilogue: dg, du from dh
-//   DX        dx = dg Wg + du Wu               one sum over both, K = 2 f
-//   DW        dWg = dg^T x, dWu = du^T x       K = rows
+//   BACKWARD  dWg = dg^T x, dWu = du^T x       K = rows
+//             dx = dg Wg + du Wu               one sum over both, K = 2 f
 //
 // The gate and up weights enter one tile side by side (half its columns each), so
-// both values of an element meet in one thread of the epilogue.  DX and DW read
-// the matrices as they are stored, with the K index along rows (MN-major operands),
-// so nothing is ever transposed in memory.
+// both values of an element meet in one thread of the epilogue.  The backward
+// products read the matrices as they are stored, with the K index along rows
+// (MN-major operands), so nothing is ever transposed in memory; both are in one
+// launch, whose tiles then fill the SMs together.
 //
 // Work is split by role: one lane loads 64-deep K slices with TMA into a ring of
 // shared-memory stages, one lane issues tcgen05.mma into one of two accumulators
-// in TMEM, and eight warps drain the other, so loads, products and
-// epilogues overlap across the tiles of a persistent block.
+// in TMEM, and eight warps drain the other, so loads, products and epilogues
+// overlap across the tiles of a persistent block (or of a pair of blocks, whose
+// tile has 256 rows and whose tensor cores each read half of the B operand).
 #pragma once
 
 #include "ops.h"
@@ -23,29 +25,37 @@
 namespace fsdp {
 namespace ffn {
 
-enum Mode { FORWARD = 0, RECOMPUTE = 1, DX = 2, DW = 3 };
+enum Mode { FORWARD = 0, RECOMPUTE = 1, BACKWARD = 2 };
 enum Act { SILU = 0, GELU = 1 };
 
 constexpr int kTileM = 128;  // rows of a block's tile (TMEM lanes)
 constexpr int kTileK = 64;   // K values of a stage: one 128-byte swizzled row
 constexpr uint32_t kStatusGemm = 16u;  // a wait of this kernel gave up
 
+// The tiles of one product: m x n of them, each K loop in `splits` parts.
+struct Grid {
+  int32_t m, n, splits;
+  int32_t raster;    // row tiles of a band (see unit_at)
+  int32_t k_blocks;  // of the whole K loop
+};
+
 struct Args {
-  CUtensorMap a[2], b[2];
+  CUtensorMap a[2];   // FORWARD, RECOMPUTE: x; BACKWARD: dg, du
+  CUtensorMap b[3];   // Wg, Wu; BACKWARD: also x
   uint32_t *status;
   uint64_t wait_limit_ns;
   int32_t fault;
   int32_t act;        // Act
-  // Tiles: m_tiles x n_tiles, each K loop split into `splits` parts.
-  int32_t m_tiles, n_tiles, splits, raster;
-  int32_t m_half;     // DW: tiles from here on are the up half
-  int32_t k_blocks, k_half;  // K blocks in all; DX: from here on the up half
-  int64_t m, n;       // rows and columns of the output (FORWARD, RECOMPUTE: n = f)
+  Grid grid[2];       // BACKWARD: weight gradients, dx; else the first only
+  int32_t tile_n;     // accumulator columns of a tile (FORWARD, RECOMPUTE: half of them gate)
+  int32_t half[2];    // BACKWARD: the row tile / the K block from which on the up half is meant
+  int64_t m[2], n;    // rows and columns of the outputs (FORWARD, RECOMPUTE: n = f)
   // Outputs, [m, n] with row distance ld.
-  void *out[2];       // FORWARD: h; RECOMPUTE: dg, du; DX: dx; DW: dWg, dWu
-  int64_t ld_out[2];
-  int32_t out_bf16, out_width;  // dtype; row_width() of the outputs
-  float *partial;     // splits > 1: [splits][m (DW: 2 m)][n] in binary32 instead of out
+  void *out[3];       // FORWARD: h; RECOMPUTE: dg, du; BACKWARD: dWg, dWu, dx
+  int64_t ld_out[3];
+  int32_t out_bf16[2], out_width[2];  // dtype and row_width(), by product
+  float *partial[2];  // by product, splits > 1: [splits][m (weight gradients: 2 m)][n] in binary32 instead of out
+  int32_t partial_width[2];
   const void *dh;     // RECOMPUTE
   int64_t ld_dh;
   int32_t dh_vec;
@@ -71,6 +81,22 @@ __device__ __forceinline__ float2 act_of(float g, int act) {
   const float p = normcdff(g);
   return make_float2(g * p, SLOPE ? fmaf(g * 0.3989422804014327f, __expf(-0.5f * g * g), p) : 0.0f);
 }
+
+// The forward pass of few rows (ffn_rows.cu).
+struct RowsArgs {
+  const void *x, *w_gate, *w_up;
+  void *h;
+  int64_t rows, d, f, ld_x, ld_gate, ld_up, ld_h;
+  int32_t act, keep;  // as in Args
+  uint8_t *codes[2], *scales[2];
+  int64_t groups;
+  void *kept[2];
+  int64_t ld_kept;
+};
+constexpr int kFewRows = 4;
+// a.rows in 1 .. kFewRows; `vec`: d is a multiple of 8 and every row of x and the weights
+// starts on a 16-byte boundary.
+cudaError_t launch_rows(const RowsArgs &a, bool vec, cudaStream_t stream);
 
 // Launches the product kernel of `mode`; `pair`: tiles of two blocks (256 rows).
 cudaError_t launch_product(Mode mode, bool pair, Args &a, int sms, cudaStream_t stream);

@@ -7,9 +7,14 @@ namespace {
 
 constexpr int kEpilogueWarps = 8; // two to each quarter of TMEM's lanes
 constexpr int kThreads = 64 + 32 * kEpilogueWarps;  // and a TMA and an MMA warp
-constexpr int kTileN = 256;       // accumulator columns
+constexpr int kTileN = 256;       // most accumulator columns of a tile
 constexpr int kAccumulators = 2;  // 2 x 256 columns: all of TMEM
 constexpr int kTmemColumns = kTileN * kAccumulators;
+
+// Each epilogue warp's buffer for 32 rows x 16 columns that change from a row to a
+// thread to a row to half a warp, for rows that no vector store fits.
+constexpr int kTurnPitch = 17;
+constexpr int kTurnBytes = 32 * kTurnPitch * 4;
 
 template <int CG>
 struct Shape {
@@ -17,7 +22,7 @@ struct Shape {
   static constexpr int kB = kTileN / CG * kTileK * 2;   // bytes of a block's B stage
   static constexpr int kStage = kA + kB;
   static constexpr int kStages = CG == 1 ? 4 : 6;
-  static constexpr int kSmem = kStages * kStage + 1024;  // stages start on 1,024-byte boundaries
+  static constexpr int kSmem = kStages * kStage + 1024 + kEpilogueWarps * kTurnBytes;  // stages start on 1,024-byte boundaries
 };
 
 struct Shared {
@@ -27,23 +32,33 @@ struct Shared {
 
 // A unit of work: one tile and one part of its K loop.
 struct Unit {
+  int which;           // of Args::grid
   int m, n, split;     // tile indices
   int k0, k1;          // K blocks
 };
 
+__device__ __forceinline__ int units_of(const Grid &g) { return g.m * g.n * g.splits; }
+
+template <int MODE>
 __device__ __forceinline__ Unit unit_at(const Args &a, int i) {
   Unit u;
-  u.split = i % a.splits;
-  const int t = i / a.splits;
+  u.which = 0;
+  if constexpr (MODE == BACKWARD) {
+    const int first = units_of(a.grid[0]);
+    if (i >= first) u.which = 1, i -= first;
+  }
+  const Grid &g = a.grid[u.which];
+  u.split = i % g.splits;
+  const int t = i / g.splits;
   // Down a band of `raster` row tiles, then to the next column tile, so that the
   // tiles at work at one time share few operand slices, which stay in L2.
-  const int band = a.raster * a.n_tiles, b = t / band, first = b * a.raster;
-  const int height = min(a.m_tiles - first, a.raster), r = t - b * band;
+  const int band = g.raster * g.n, b = t / band, first = b * g.raster;
+  const int height = min(g.m - first, g.raster), r = t - b * band;
   u.m = first + r % height;
   u.n = r / height;
-  const int per = (a.k_blocks + a.splits - 1) / a.splits;
-  u.k0 = min(u.split * per, a.k_blocks);
-  u.k1 = min(u.k0 + per, a.k_blocks);
+  const int per = (g.k_blocks + g.splits - 1) / g.splits;
+  u.k0 = min(u.split * per, g.k_blocks);
+  u.k1 = min(u.k0 + per, g.k_blocks);
   return u;
 }
 
@@ -53,68 +68,123 @@ __device__ __forceinline__ void load_stage(const Args &a, const Unit &u, int kb,
   using S = Shape<CG>;
   const uint32_t sa = at, sb = at + S::kA;
   if constexpr (MODE == FORWARD || MODE == RECOMPUTE) {
+    const int half = a.tile_n / 2, n0 = u.n * half;
     tc::tma_load<CG>(sa, &a.a[0], kb * kTileK, (u.m * CG + rank) * kTileM, bar);
-    const int n0 = u.n * (kTileN / 2);
     if constexpr (CG == 1) {
       tc::tma_load<CG>(sb, &a.b[0], kb * kTileK, n0, bar);
-      tc::tma_load<CG>(sb + S::kB / 2, &a.b[1], kb * kTileK, n0, bar);
+      tc::tma_load<CG>(sb + half * (kTileK * 2), &a.b[1], kb * kTileK, n0, bar);
     } else {
       tc::tma_load<CG>(sb, &a.b[rank], kb * kTileK, n0, bar);
     }
-  } else if constexpr (MODE == DX) {
-    const int half = kb >= a.k_half ? 1 : 0, k0 = (half ? kb - a.k_half : kb) * kTileK;
-    tc::tma_load<CG>(sa, &a.a[half], k0, (u.m * CG + rank) * kTileM, bar);
-#pragma unroll
-    for (int c = 0; c < kTileN / CG / 64; ++c)
-      tc::tma_load<CG>(sb + c * 8192, &a.b[half], u.n * kTileN + rank * (kTileN / CG) + c * 64, k0, bar);
   } else {
-    const int half = u.m >= a.m_half ? 1 : 0, m0 = ((half ? u.m - a.m_half : u.m) * CG + rank) * kTileM;
+    // Boxes of 64 x 64 throughout.  Along K in a row (A of dx): two boxes of 64 rows lie
+    // one after the other; along M or N in a row: one box to 64 of them.
+    const CUtensorMap *ma, *mb;
+    int k0 = kb * kTileK, m0;
+    if (u.which == 1) {
+      const int up = kb >= a.half[1];
+      ma = &a.a[up], mb = &a.b[up];
+      k0 -= up * a.half[1] * kTileK;
+      m0 = (u.m * CG + rank) * kTileM;
+    } else {
+      const int up = u.m >= a.half[0];
+      ma = &a.a[up], mb = &a.b[2];
+      m0 = ((u.m - up * a.half[0]) * CG + rank) * kTileM;
+    }
 #pragma unroll
-    for (int c = 0; c < kTileM / 64; ++c) tc::tma_load<CG>(sa + c * 8192, &a.a[half], m0 + c * 64, kb * kTileK, bar);
+    for (int c = 0; c < kTileM / 64; ++c)
+      tc::tma_load<CG>(sa + c * 8192, ma, u.which == 1 ? k0 : m0 + c * 64, u.which == 1 ? m0 + c * 64 : k0, bar);
 #pragma unroll
     for (int c = 0; c < kTileN / CG / 64; ++c)
-      tc::tma_load<CG>(sb + c * 8192, &a.b[0], u.n * kTileN + rank * (kTileN / CG) + c * 64, kb * kTileK, bar);
+      tc::tma_load<CG>(sb + c * 8192, mb, u.n * kTileN + rank * (kTileN / CG) + c * 64, k0, bar);
   }
 }
 
-// 32 consecutive elements of a row to memory: `n` of them exist; `width`: row_width().
-// A thread has a row of its own, so a store instruction of a warp goes to 32 rows;
-// whole 32-byte sectors keep that from costing two writes a sector.
-__device__ __forceinline__ void store_run(void *p, int64_t at, bool bf16, int width, const float2 (&v)[16], int n) {
-  if (width >= 16 && n >= 32) {
+// A warp's 32 x 32 part of a tile: one row to a thread.
+struct Part {
+  int64_t col;   // first column
+  int n;         // columns that exist, at most 32
+  int rows;      // rows that exist (lanes below it), at most 32
+  int64_t row;   // this thread's row
+  float *turn;   // the warp's buffer
+};
+
+// The part to memory; `width`: row_width().  Stores of a row to a thread go to 32 rows at
+// a time; whole 32-byte sectors keep that from costing two writes a sector.  Rows that no
+// vector fits go through the warp's buffer, half a warp to a row (element by element from
+// a row to a thread, a store instruction would touch 32 sectors for 64 bytes).
+__device__ __forceinline__ void store_part(void *p, int64_t ld, bool bf16, int width, const float2 (&v)[16], const Part &q) {
+  if (width >= 16 && q.n >= 32) {
+    if ((int)(threadIdx.x & 31) >= q.rows) return;
+    const int64_t at = q.row * ld + q.col;
     if (bf16) {
       uint32_t w[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) w[i] = bf16_pair(v[i].x, v[i].y);
-      uint4 *q = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + at);
+      uint4 *to = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + at);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t(&h)[8] = reinterpret_cast<const uint32_t(&)[8]>(w[8 * i]);
         if (width == 32)
-          store32(q + 2 * i, h);
+          store32(to + 2 * i, h);
         else
-          q[2 * i] = make_uint4(h[0], h[1], h[2], h[3]), q[2 * i + 1] = make_uint4(h[4], h[5], h[6], h[7]);
+          to[2 * i] = make_uint4(h[0], h[1], h[2], h[3]), to[2 * i + 1] = make_uint4(h[4], h[5], h[6], h[7]);
       }
     } else {
-      float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
+      float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (width == 32) {
           uint32_t h[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) h[e] = __float_as_uint(element(v, 8 * i + e));
-          store32(q + 2 * i, h);
+          store32(to + 2 * i, h);
         } else {
-          q[2 * i] = make_float4(v[4 * i].x, v[4 * i].y, v[4 * i + 1].x, v[4 * i + 1].y);
-          q[2 * i + 1] = make_float4(v[4 * i + 2].x, v[4 * i + 2].y, v[4 * i + 3].x, v[4 * i + 3].y);
+          to[2 * i] = make_float4(v[4 * i].x, v[4 * i].y, v[4 * i + 1].x, v[4 * i + 1].y);
+          to[2 * i + 1] = make_float4(v[4 * i + 2].x, v[4 * i + 2].y, v[4 * i + 3].x, v[4 * i + 3].y);
         }
       }
     }
     return;
   }
+  const int lane = threadIdx.x & 31;
+  const int64_t first = q.row - lane;
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (i < n) store_any(p, at + i, bf16, element(v, i));
+  for (int side = 0; side < 2; ++side) {
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) q.turn[lane * kTurnPitch + e] = element(v, side * 16 + e);
+    __syncwarp();
+    const int c = side * 16 + lane % 16;
+    if (c < q.n)
+      for (int r = lane / 16; r < q.rows; r += 2)
+        store_any(p, (first + r) * ld + q.col + c, bf16, q.turn[r * kTurnPitch + lane % 16]);
+  }
+}
+
+// The part of a BF16 matrix, 0 where there is none; `vec`: its rows start on 16-byte boundaries.
+__device__ __forceinline__ void load_part(const __nv_bfloat16 *p, int64_t ld, bool vec, float2 (&v)[16], const Part &q) {
+  const int lane = threadIdx.x & 31;
+  if (vec && q.n >= 32) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = both(0.0f);
+    if (lane >= q.rows) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load8(p + q.row * ld + q.col, 8 * i, true, reinterpret_cast<float2(&)[4]>(v[4 * i]));
+    return;
+  }
+  const int64_t first = q.row - lane;
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    const int c = side * 16 + lane % 16;
+    __syncwarp();
+    for (int r = lane / 16; r < 32; r += 2)
+      q.turn[r * kTurnPitch + lane % 16] =
+          c < q.n && r < q.rows ? __bfloat162float(p[(first + r) * ld + q.col + c]) : 0.0f;
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) element(v, side * 16 + e) = q.turn[lane * kTurnPitch + e];
+  }
 }
 
 // The 8-bit checkpoint of 32 consecutive elements, one whole group; elements from n on are 0.
@@ -133,11 +203,9 @@ __device__ __forceinline__ float2 pair_at(const uint32_t (&r)[32], int i) {
   return make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 
-// One thread's part of a gate / up tile: 32 columns of one row.
+// A warp's part of a gate / up tile.
 template <int MODE>
-__device__ __forceinline__ void gated_run(const Args &a, const uint32_t (&gr)[32], const uint32_t (&ur)[32], int64_t row,
-                                          int64_t col) {
-  const int n = (int)min((int64_t)32, a.n - col);
+__device__ __forceinline__ void gated_part(const Args &a, const uint32_t (&gr)[32], const uint32_t (&ur)[32], const Part &q) {
   float2 x[16], y[16];
   if constexpr (MODE == FORWARD) {
 #pragma unroll
@@ -145,38 +213,44 @@ __device__ __forceinline__ void gated_run(const Args &a, const uint32_t (&gr)[32
       const float2 g = pair_at(gr, i);
       x[i] = __fmul2_rn(make_float2(act_of<false>(g.x, a.act).x, act_of<false>(g.y, a.act).x), pair_at(ur, i));
     }
-    store_run(a.out[0], row * a.ld_out[0] + col, true, a.out_width, x, n);
+    store_part(a.out[0], a.ld_out[0], true, a.out_width[0], x, q);
     if (a.keep) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = pair_at(gr, i), y[i] = pair_at(ur, i);
-      if (a.keep == 1) {
-        const int64_t group = row * a.groups + col / (int)kActGroup;
-        keep_group(a.codes[0] + group * kActGroup, a.scales[0] + group, x, n, a.keep_width == 32);
-        keep_group(a.codes[1] + group * kActGroup, a.scales[1] + group, y, n, a.keep_width == 32);
-      } else {
-        store_run(a.kept[0], row * a.ld_kept + col, true, a.keep_width, x, n);
-        store_run(a.kept[1], row * a.ld_kept + col, true, a.keep_width, y, n);
+      if (a.keep == 2) {
+        store_part(a.kept[0], a.ld_kept, true, a.keep_width, x, q);
+        store_part(a.kept[1], a.ld_kept, true, a.keep_width, y, q);
+      } else if ((int)(threadIdx.x & 31) < q.rows) {
+        const int64_t group = q.row * a.groups + q.col / (int)kActGroup;
+        keep_group(a.codes[0] + group * kActGroup, a.scales[0] + group, x, q.n, a.keep_width == 32);
+        keep_group(a.codes[1] + group * kActGroup, a.scales[1] + group, y, q.n, a.keep_width == 32);
       }
     }
   } else {
-    const __nv_bfloat16 *dh = static_cast<const __nv_bfloat16 *>(a.dh) + row * a.ld_dh + col;
     float2 d[16];
-    if (a.dh_vec && n >= 32) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) load8(dh, 8 * i, true, reinterpret_cast<float2(&)[4]>(d[4 * i]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) element(d, i) = i < n ? __bfloat162float(dh[i]) : 0.0f;
-    }
+    load_part(static_cast<const __nv_bfloat16 *>(a.dh), a.ld_dh, a.dh_vec != 0, d, q);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float2 g = pair_at(gr, i), p = act_of<true>(g.x, a.act), q = act_of<true>(g.y, a.act);
-      x[i] = __fmul2_rn(__fmul2_rn(d[i], pair_at(ur, i)), make_float2(p.y, q.y));
-      y[i] = __fmul2_rn(d[i], make_float2(p.x, q.x));
+      const float2 g = pair_at(gr, i), p = act_of<true>(g.x, a.act), r = act_of<true>(g.y, a.act);
+      x[i] = __fmul2_rn(__fmul2_rn(d[i], pair_at(ur, i)), make_float2(p.y, r.y));
+      y[i] = __fmul2_rn(d[i], make_float2(p.x, r.x));
     }
-    store_run(a.out[0], row * a.ld_out[0] + col, true, a.out_width, x, n);
-    store_run(a.out[1], row * a.ld_out[1] + col, true, a.out_width, y, n);
+    store_part(a.out[0], a.ld_out[0], true, a.out_width[0], x, q);
+    store_part(a.out[1], a.ld_out[1], true, a.out_width[0], y, q);
   }
+}
+
+// The four MMAs of one stage.  Descriptors advance by 16 K values: 32 bytes within a
+// row, or 16 rows of 128 bytes.  With the majors known at run time only, one thread
+// could no longer issue them at the tensor cores' rate (11 % of the products' time).
+template <int CG, bool A_MN, bool B_MN>
+__device__ __forceinline__ void multiply_stage(uint32_t d, uint32_t sa, uint32_t sb, int columns, bool add) {
+  constexpr uint32_t kStepA = A_MN ? 2048 : 32, kStepB = B_MN ? 2048 : 32;
+  const uint32_t idesc = tc::instruction(kTileM * CG, columns, A_MN, B_MN);
+#pragma unroll
+  for (int k = 0; k < kTileK / 16; ++k)
+    tc::mma<CG>(d, tc::operand(sa + k * kStepA, A_MN ? 8192 : 16, 1024), tc::operand(sb + k * kStepB, B_MN ? 8192 : 16, 1024),
+                idesc, add || k > 0);
 }
 
 // Test hook: the first worker leaves its first stage empty, so the wait for it gives up.
@@ -212,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   const uint32_t stages = (tc::smem(dynamic) + 1023u) & ~1023u;
   const int rank = CG == 1 ? 0 : (int)tc::cluster_rank();
   const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
-  const int units = a.m_tiles * a.n_tiles * a.splits;
+  const int units = units_of(a.grid[0]) + (MODE == BACKWARD ? units_of(a.grid[1]) : 0);
   volatile uint32_t *stop = &sh.stop;
 
   if (warp == 0 && lane == 0) {
@@ -246,32 +320,35 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     // ---- loads ---------------------------------------------------------------
     if (lane == 0) {
       uint32_t stage = 0, phase = 0, filled = 0;
+      const uint32_t bytes = CG * S::kA + (MODE == BACKWARD ? kTileN : a.tile_n) * (kTileK * 2);
       for (int i = worker; i < units && ok; i += workers) {
-        const Unit u = unit_at(a, i);
+        const Unit u = unit_at<MODE>(a, i);
         for (int kb = u.k0; kb < u.k1; ++kb) {
           const uint32_t full = tc::smem(&sh.full[stage]), full_leader = CG == 1 ? full : tc::at_rank(full, 0);
           if (!(ok = tc::bar_wait(tc::smem(&sh.empty[stage]), phase ^ 1u, a.wait_limit_ns, stop))) break;
           if (!skips_first(a, worker) || filled > 0) {
-            if (rank == 0) tc::bar_expect(full, CG * S::kStage);
+            if (rank == 0) tc::bar_expect(full, bytes);
             load_stage<MODE, CG>(a, u, kb, rank, stages + stage * S::kStage, full_leader);
           }
           ++filled;
           if (++stage == S::kStages) stage = 0, phase ^= 1u;
         }
       }
+      // The last products hand their stages back before this block leaves: the other
+      // block of a pair must not signal into shared memory that is no longer its own.
+      for (int s = 0; ok && s < S::kStages; ++s) {
+        ok = tc::bar_wait(tc::smem(&sh.empty[stage]), phase ^ 1u, a.wait_limit_ns, stop);
+        if (++stage == S::kStages) stage = 0, phase ^= 1u;
+      }
       sh.filled = filled;
     }
   } else if (warp == 1) {
     // ---- products ------------------------------------------------------------
     if (lane == 0 && rank == 0) {
-      constexpr bool kAMn = MODE == DW, kBMn = MODE == DX || MODE == DW;
-      constexpr uint32_t idesc = tc::instruction(kTileM * CG, kTileN, kAMn, kBMn);
-      // Descriptors advance by 16 K values: 32 bytes within a row, or 16 rows of 128 bytes.
-      constexpr uint32_t kStepA = kAMn ? 2048 : 32, kStepB = kBMn ? 2048 : 32;
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool issued = false;
       for (int i = worker; i < units && ok; i += workers) {
-        const Unit u = unit_at(a, i);
+        const Unit u = unit_at<MODE>(a, i);
         if (!(ok = tc::bar_wait(tc::smem(&sh.tmem_empty[acc]), acc_phase ^ 1u, a.wait_limit_ns, stop))) break;
         tc::fence_after();
         const uint32_t d = tmem + acc * kTileN;
@@ -279,10 +356,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           if (!(ok = tc::bar_wait(tc::smem(&sh.full[stage]), phase, a.wait_limit_ns, stop))) break;
           tc::fence_after();
           const uint32_t sa = stages + stage * S::kStage, sb = sa + S::kA;
-#pragma unroll
-          for (int k = 0; k < kTileK / 16; ++k)
-            tc::mma<CG>(d, tc::operand(sa + k * kStepA, kAMn ? 8192 : 16, 1024),
-                        tc::operand(sb + k * kStepB, kBMn ? 8192 : 16, 1024), idesc, kb > u.k0 || k > 0);
+          if (MODE != BACKWARD)
+            multiply_stage<CG, false, false>(d, sa, sb, a.tile_n, kb > u.k0);
+          else if (u.which == 0)
+            multiply_stage<CG, true, true>(d, sa, sb, kTileN, kb > u.k0);
+          else
+            multiply_stage<CG, false, true>(d, sa, sb, kTileN, kb > u.k0);
           issued = true;
           tc::mma_commit<CG>(tc::smem(&sh.empty[stage]));
           if (++stage == S::kStages) stage = 0, phase ^= 1u;
@@ -302,9 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     // ---- epilogue ------------------------------------------------------------
     const int quarter = warp & 3;          // the lanes of TMEM that this warp may read
     const int side = (warp - 2) / 4;       // and its half of the columns
+    float *const turn = reinterpret_cast<float *>(dynamic + (stages - tc::smem(dynamic)) + S::kStages * S::kStage) +
+                        (warp - 2) * (kTurnBytes / 4);
     uint32_t acc = 0, acc_phase = 0;
     for (int i = worker; i < units; i += workers) {
-      const Unit u = unit_at(a, i);
+      const Unit u = unit_at<MODE>(a, i);
       if (!(ok = tc::bar_wait(tc::smem(&sh.tmem_full[acc]), acc_phase, a.wait_limit_ns, stop))) break;
       tc::fence_after();
       const uint32_t from = tmem + acc * kTileN + ((uint32_t)quarter * 32u << 16);
@@ -318,21 +399,25 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const bool some = u.k1 > u.k0;  // an empty part of a K loop: the sum is 0
       if constexpr (MODE == FORWARD || MODE == RECOMPUTE) {
         const int64_t row = ((int64_t)u.m * CG + rank) * kTileM + quarter * 32 + lane;
+        const int half = a.tile_n / 2, runs = half / 32, mid = (runs + 1) / 2;
+        const int begin = side ? mid : 0, end = side ? runs : mid;
+        if (begin == end) drained();
 #pragma unroll 1
-        for (int c = side * (kTileN / 4); c < (side + 1) * (kTileN / 4); c += 32) {
-          const int64_t col = (int64_t)u.n * (kTileN / 2) + c;
+        for (int c = begin; c < end; ++c) {
+          const int64_t col = (int64_t)u.n * half + c * 32;
           uint32_t g[32], up[32];
           __syncwarp();
-          tc::tmem_load32(from + c, g);
-          tc::tmem_load32(from + kTileN / 2 + c, up);
+          tc::tmem_load32(from + c * 32, g);
+          tc::tmem_load32(from + half + c * 32, up);
           tc::tmem_load_wait();
-          if (c + 32 == (side + 1) * (kTileN / 4)) drained();
-          if (col >= a.n) continue;
-          if (row < a.m) gated_run<MODE>(a, g, up, row, col);
+          if (c + 1 == end) drained();
+          const int64_t rows = a.m[0] - (row - lane);
+          if (rows > 0 && col < a.n)
+            gated_part<MODE>(a, g, up, {col, (int)min((int64_t)32, a.n - col), (int)min((int64_t)32, rows), row, turn});
         }
       } else {
-        const int half = MODE == DW && u.m >= a.m_half ? 1 : 0;
-        const int64_t row = ((int64_t)(half ? u.m - a.m_half : u.m) * CG + rank) * kTileM + quarter * 32 + lane;
+        const int which = u.which, up = which == 0 && u.m >= a.half[0] ? 1 : 0, to = which == 1 ? 2 : up;
+        const int64_t row = ((int64_t)(u.m - up * a.half[0]) * CG + rank) * kTileM + quarter * 32 + lane, m = a.m[which];
 #pragma unroll 1
         for (int c = side * (kTileN / 2); c < (side + 1) * (kTileN / 2); c += 32) {
           const int64_t col = (int64_t)u.n * kTileN + c;
@@ -341,17 +426,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           tc::tmem_load32(from + c, r);
           tc::tmem_load_wait();
           if (c + 32 == (side + 1) * (kTileN / 2)) drained();
-          if (col >= a.n) continue;
-          float2 v[16];
+          const int64_t rows = m - (row - lane);
+          if (rows > 0 && col < a.n) {
+            const Part q = {col, (int)min((int64_t)32, a.n - col), (int)min((int64_t)32, rows), row, turn};
+            float2 v[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = some ? pair_at(r, e) : both(0.0f);
-          if (row < a.m) {
-            const int n = (int)min((int64_t)32, a.n - col);
-            if (a.splits > 1) {
-              const int64_t rows = MODE == DW ? 2 * a.m : a.m;
-              store_run(a.partial, ((int64_t)u.split * rows + half * a.m + row) * a.n + col, false, a.n % 8 == 0 ? 32 : a.n % 4 == 0 ? 16 : 0, v, n);
+            for (int e = 0; e < 16; ++e) v[e] = some ? pair_at(r, e) : both(0.0f);
+            if (a.grid[which].splits > 1) {
+              const int64_t all = which == 0 ? 2 * m : m;
+              store_part(a.partial[which] + ((int64_t)u.split * all + up * m) * a.n, a.n, false, a.partial_width[which], v, q);
             } else {
-              store_run(a.out[half], row * a.ld_out[half] + col, a.out_bf16 != 0, a.out_width, v, n);
+              store_part(a.out[to], a.ld_out[to], a.out_bf16[which] != 0, a.out_width[which], v, q);
             }
           }
         }
@@ -378,7 +463,8 @@ cudaError_t launch(Args &a, int sms, cudaStream_t stream) {
   const void *fn = reinterpret_cast<const void *>(&product_kernel<MODE, CG>);
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t units = (int64_t)a.m_tiles * a.n_tiles * a.splits;
+  int64_t units = 0;
+  for (int w = 0; w < (MODE == BACKWARD ? 2 : 1); ++w) units += (int64_t)a.grid[w].m * a.grid[w].n * a.grid[w].splits;
   int64_t workers = sms / CG;
   if (workers > units) workers = units;
   void *args[] = {&a};
@@ -391,8 +477,7 @@ cudaError_t launch_product(Mode mode, bool pair, Args &a, int sms, cudaStream_t 
   switch (mode) {
     case FORWARD: return pair ? launch<FORWARD, 2>(a, sms, stream) : launch<FORWARD, 1>(a, sms, stream);
     case RECOMPUTE: return pair ? launch<RECOMPUTE, 2>(a, sms, stream) : launch<RECOMPUTE, 1>(a, sms, stream);
-    case DX: return pair ? launch<DX, 2>(a, sms, stream) : launch<DX, 1>(a, sms, stream);
-    default: return pair ? launch<DW, 2>(a, sms, stream) : launch<DW, 1>(a, sms, stream);
+    default: return pair ? launch<BACKWARD, 2>(a, sms, stream) : launch<BACKWARD, 1>(a, sms, stream);
   }
 }
 
