@@ -61,7 +61,7 @@ bool encode(CUtensorMap *map, const Operand &o, int box_rows) {
 }
 
 // Copies of up to three matrices whose rows start anywhere, to rows of `pitch`
-// elements: one warp to a row at a time, four elements a lane in flight.
+// elements: a warp to 256 elements of a row, all of them in flight at once.
 struct CopyArgs {
   const uint16_t *src[3];
   uint16_t *dst[3];
@@ -69,24 +69,24 @@ struct CopyArgs {
   int64_t pitch, cols;
 };
 __global__ void __launch_bounds__(kThreads) copy_rows_kernel(const __grid_constant__ CopyArgs a) {
+  constexpr int kEach = 8;
   const int lane = threadIdx.x & 31;
+  const int64_t pieces = (a.cols + 32 * kEach - 1) / (32 * kEach), all = (a.rows[0] + a.rows[1] + a.rows[2]) * pieces;
   wait_for_previous();
   let_next_start();
-  const int64_t all = a.rows[0] + a.rows[1] + a.rows[2];
   for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; i < all; i += (int64_t)gridDim.x * (kThreads / 32)) {
-    const int which = i < a.rows[0] ? 0 : i < a.rows[0] + a.rows[1] ? 1 : 2;
-    const int64_t r = which == 0 ? i : which == 1 ? i - a.rows[0] : i - a.rows[0] - a.rows[1];
-    const uint16_t *src = a.src[which] + r * a.ld[which];
-    uint16_t *dst = a.dst[which] + r * a.pitch;
-    for (int64_t j = lane; j < a.cols; j += 128) {
-      uint16_t v[4];
+    int64_t r = i / pieces;
+    const int64_t j = (i - r * pieces) * (32 * kEach) + lane;
+    int which = 0;
+    while (r >= a.rows[which]) r -= a.rows[which++];
+    const uint16_t *src = a.src[which] + r * a.ld[which] + j;
+    uint16_t *dst = a.dst[which] + r * a.pitch + j, v[kEach];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (j + u * 32 < a.cols) v[u] = src[j + u * 32];
+    for (int u = 0; u < kEach; ++u)
+      if (j + u * 32 < a.cols) v[u] = src[u * 32];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (j + u * 32 < a.cols) dst[j + u * 32] = v[u];
-    }
+    for (int u = 0; u < kEach; ++u)
+      if (j + u * 32 < a.cols) dst[u * 32] = v[u];
   }
 }
 
@@ -303,9 +303,15 @@ BackwardTiles backward_tiles(int64_t rows, int64_t d, int64_t f, int sms) {
   return t;
 }
 
+// A TMA map of fewer rows loads slowly: the 4096 x 12288 block takes 39 us with 16
+// rows and 48 to 68 with 5 to 15.  The forward pass then copies x into a map of 16 rows,
+// whose other rows may hold anything (they meet no result).
+constexpr int64_t kMapRows = 16;
+
 struct Plan {
   int sms;
   bool stage_x, stage_wg, stage_wu;
+  bool pad_x;   // x staged as kMapRows rows
   int64_t d_pitch, f_pitch;
   BackwardTiles tiles;
   int64_t at_x, at_wg, at_wu, at_dg, at_du, at_partial[2], bytes;
@@ -319,6 +325,8 @@ Plan plan_of(const fsdp_ffn_desc_t *d, bool backward) {
   p.d_pitch = up_to(d->d, 8), p.f_pitch = up_to(d->f, 16);
   if (!backward && d->rows <= kFewRows) return p;  // reads its operands where they are
   p.stage_x = d->x_dtype == FSDP_ACT8 || rows_off(d->rows, d->ld_x, d->unaligned & 1);
+  p.pad_x = !backward && d->rows < kMapRows;
+  p.stage_x = p.stage_x || p.pad_x;
   p.stage_wg = rows_off(d->f, d->ld_w_gate, d->unaligned & 2);
   p.stage_wu = rows_off(d->f, d->ld_w_up, d->unaligned & 4);
   int64_t at = 0;
@@ -327,7 +335,7 @@ Plan plan_of(const fsdp_ffn_desc_t *d, bool backward) {
     if (want) at += up_to(bytes, 256);
     return here;
   };
-  p.at_x = take(p.stage_x, d->rows * p.d_pitch * 2);
+  p.at_x = take(p.stage_x, (p.pad_x ? kMapRows : d->rows) * p.d_pitch * 2);
   p.at_wg = take(p.stage_wg, d->f * p.d_pitch * 2);
   p.at_wu = take(p.stage_wu, d->f * p.d_pitch * 2);
   if (backward && d->rows > 0) {
@@ -413,6 +421,7 @@ struct Call {
       a.src[i] = static_cast<const uint16_t *>(o.p), a.dst[i] = reinterpret_cast<uint16_t *>(ws + at);
       a.ld[i] = o.ld, a.rows[i] = o.rows;
       o.p = a.dst[i], o.ld = plan.d_pitch;
+      if (i == 2 && plan.pad_x) o.rows = kMapRows;
     };
     copy(wg, plan.stage_wg, plan.at_wg, 0);
     copy(wu, plan.stage_wu, plan.at_wu, 1);
@@ -426,8 +435,8 @@ struct Call {
     }
     const int64_t rows = a.rows[0] + a.rows[1] + a.rows[2];
     if (rows == 0) return FSDP_OK;
-    int64_t grid = blocks_of(rows, kThreads / 32);
-    if (grid > plan.sms * 8) grid = plan.sms * 8;
+    int64_t grid = blocks_of(rows * blocks_of(a.cols, 256), kThreads / 32);
+    if (grid > plan.sms * 16) grid = plan.sms * 16;
     void *args[] = {&a};
     return launched(launch_kernel(reinterpret_cast<const void *>(&copy_rows_kernel), dim3((unsigned)grid), dim3(kThreads),
                                   args, 0, stream, true));

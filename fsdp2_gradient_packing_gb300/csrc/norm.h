@@ -241,7 +241,8 @@ __device__ __forceinline__ void read_row(float2 (&v)[K][4], float (&unit)[K], co
       const int j = column<VEC, G>(0, t, k, 0);
       if constexpr (XK == X_ACT8) {
         const uint2 c = *reinterpret_cast<const uint2 *>(k < mine ? p + j : reinterpret_cast<const uint8_t *>(zeros));
-        unit[k] = act8_scale(scales[k < mine ? j / (int)kActGroup : 0]);
+        // An absent chunk's scale is 0 too: in a block without columns the stage holds anything.
+        unit[k] = k < mine ? act8_scale(scales[j / (int)kActGroup]) : 0.0f;
         const uint32_t lo = act8_biased(c.x), hi = act8_biased(c.y);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[k][e] = act8_codes_of(e < 2 ? lo : hi, e % 2);

@@ -67,93 +67,96 @@ for _name, _args in _SIGNATURES.items():
 
 
 # ---------------------------------------------------------------------------
-# Arguments
+# Arguments.  Each check takes and returns the device that the call's tensors are
+# on (None before the first).  A small call costs little more on the GPU than
+# these checks do on the host, so they are plain functions with few steps.
 # ---------------------------------------------------------------------------
-class _Args:
-    """Checks the tensors of one call: where they are, and their shapes and dtypes."""
+_BOTH, _BF16, _F32 = dict(_CODE), {torch.bfloat16: FSDP_DTYPE_BF16}, {torch.float32: FSDP_DTYPE_F32}
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
-    def __init__(self, where):
-        self.where, self.device = where, None
 
-    def fail(self, why):
-        raise ValueError(f"{self.where}: {why}")
-
-    def _placed(self, what, t):
-        if not isinstance(t, torch.Tensor):
-            self.fail(f"{what} is not a tensor")
-        index = t.get_device()
+def _placed(where, what, t, device):
+    index = t.get_device()
+    if index != device:
         if index < 0:
-            self.fail(f"{what} is not a CUDA tensor")
-        if self.device is None:
-            self.device = index
-        elif index != self.device:
-            self.fail(f"{what} is on cuda:{index}, another argument on cuda:{self.device}")
+            raise ValueError(f"{where}: {what} is not a CUDA tensor")
+        if device is not None:
+            raise ValueError(f"{where}: {what} is on cuda:{index}, another argument on cuda:{device}")
+    return index
 
-    def matrix(self, what, t, rows=None, cols=None, dtypes=(torch.float32, torch.bfloat16)):
-        """(pointer, row distance, dtype code) of a [rows, cols] tensor."""
-        if not isinstance(t, torch.Tensor):
-            self.fail(f"{what} is not a tensor")
-        if t.dim() != 2:
-            self.fail(f"{what} has {t.dim()} dimensions, not 2")
+
+def _matrix(where, what, t, rows, cols, codes, device):
+    """(pointer, row distance, dtype code, device) of a [rows, cols] tensor; None: any size."""
+    try:
         r, c = t.shape
-        if (rows is not None and r != rows) or (cols is not None and c != cols):
-            self.fail(f"{what} is {r} x {c}, not {r if rows is None else rows} x {c if cols is None else cols}")
-        if t.dtype not in dtypes:
-            self.fail(f"{what} is {t.dtype}, not one of {', '.join(map(str, dtypes))}")
-        if c < 1:
-            self.fail(f"{what} has no columns")
+        code = codes[t.dtype]
         s0, s1 = t.stride()
-        if c > 1 and s1 != 1:
-            self.fail(f"{what} has column stride {s1}, not 1")
-        if r <= 1:
-            s0 = c
-        elif s0 < c:
-            self.fail(f"{what} has rows {s0} elements apart, fewer than its {c} columns")
-        self._placed(what, t)
-        return t.data_ptr(), s0, _CODE[t.dtype]
-
-    def vector(self, what, t, n, dtypes=(torch.float32, torch.bfloat16)):
-        """(pointer, dtype code) of a contiguous vector of n elements; (None, None) for None."""
-        if t is None:
-            return None, None
+    except (AttributeError, TypeError, ValueError, KeyError):
         if not isinstance(t, torch.Tensor):
-            self.fail(f"{what} is not a tensor")
-        if t.numel() != n or t.dim() > 1 and t.shape[-1] != n or not t.is_contiguous():
-            self.fail(f"{what} is not a contiguous vector of {n} elements")
-        if t.dtype not in dtypes:
-            self.fail(f"{what} is {t.dtype}, not one of {', '.join(map(str, dtypes))}")
-        self._placed(what, t)
-        return t.data_ptr(), _CODE[t.dtype]
+            raise ValueError(f"{where}: {what} is not a tensor") from None
+        if t.dim() != 2:
+            raise ValueError(f"{where}: {what} has {t.dim()} dimensions, not 2") from None
+        raise ValueError(f"{where}: {what} is {t.dtype}, not one of {', '.join(map(str, codes))}") from None
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{where}: {what} is {r} x {c}, not {r if rows is None else rows} x {c if cols is None else cols}")
+    if c < 1:
+        raise ValueError(f"{where}: {what} has no columns")
+    if s1 != 1 and c > 1:
+        raise ValueError(f"{where}: {what} has column stride {s1}, not 1")
+    if r <= 1:
+        s0 = c
+    elif s0 < c:
+        raise ValueError(f"{where}: {what} has rows {s0} elements apart, fewer than its {c} columns")
+    return t.data_ptr(), s0, code, _placed(where, what, t, device)
 
-    def ckpt(self, what, a, rows=None, cols=None):
-        if not isinstance(a, Act8):
-            self.fail(f"{what} is not an Act8 checkpoint")
-        if (rows is not None and a.rows != rows) or (cols is not None and a.cols != cols):
-            self.fail(f"{what} is a checkpoint of {a.rows} x {a.cols}, not of {rows} x {cols}")
-        self._placed(what, a.data)
-        return a.data.data_ptr()
 
-    def stream(self, stream):
-        """The handle of the stream to run on; the tensors have to be on the current device."""
-        if self.device is not None and self.device != torch.cuda.current_device():
-            self.fail(f"the tensors are on cuda:{self.device}, the current device is {torch.cuda.current_device()}")
-        if stream is None:
-            return _current_stream()
-        return stream if isinstance(stream, int) else stream.cuda_stream
+def _vector(where, what, t, n, codes, device):
+    """(pointer, dtype code, device) of a contiguous vector of n elements; no pointer or code for None."""
+    if t is None:
+        return None, None, device
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{where}: {what} is not a tensor")
+    if t.numel() != n or not t.is_contiguous() or t.dim() > 1 and t.shape[-1] != n:
+        raise ValueError(f"{where}: {what} is not a contiguous vector of {n} elements")
+    code = codes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{where}: {what} is {t.dtype}, not one of {', '.join(map(str, codes))}")
+    return t.data_ptr(), code, _placed(where, what, t, device)
 
-    def workspace(self, given, nbytes, handle):
-        """(pointer, bytes, owner) of the caller's workspace or of one taken for this call."""
-        if given is not None:
-            if given.dtype != torch.uint8 or not given.is_contiguous():
-                self.fail("workspace is not a contiguous uint8 tensor")
-            self._placed("workspace", given)
-            if given.numel() < nbytes:
-                self.fail(f"workspace holds {given.numel()} bytes, the call needs {nbytes}")
-            return given.data_ptr(), given.numel(), given
-        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=f"cuda:{self.device}")
-        if handle != _current_stream():  # the allocator may not reuse it before the call's stream is done with it
-            ws.record_stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream())
-        return ws.data_ptr(), nbytes, ws
+
+def _ckpt(where, what, a, rows, cols, device):
+    """(pointer, device) of the checkpoint of a [rows, cols] matrix."""
+    if not isinstance(a, Act8):
+        raise ValueError(f"{where}: {what} is not an Act8 checkpoint")
+    if a.rows != rows or a.cols != cols:
+        raise ValueError(f"{where}: {what} is a checkpoint of {a.rows} x {a.cols}, not of {rows} x {cols}")
+    return a.data.data_ptr(), _placed(where, what, a.data, device)
+
+
+def _handle(where, stream, device):
+    """The handle of the stream to run on; the tensors have to be on the current device."""
+    if device != _get_device():
+        raise ValueError(f"{where}: the tensors are on cuda:{device}, the current device is {_get_device()}")
+    if stream is None:
+        return _current_stream()
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _workspace(where, given, nbytes, handle, device):
+    """(pointer, bytes, owner) of the caller's workspace, or of one taken for this call."""
+    if given is not None:
+        if given.dtype != torch.uint8 or not given.is_contiguous():
+            raise ValueError(f"{where}: workspace is not a contiguous uint8 tensor")
+        _placed(where, "workspace", given, device)
+        if given.numel() < nbytes:
+            raise ValueError(f"{where}: workspace holds {given.numel()} bytes, the call needs {nbytes}")
+        return given.data_ptr(), given.numel(), given
+    if nbytes == 0:
+        return None, 0, None
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+    if handle != _current_stream():  # the allocator may not reuse it before the call's stream is done with it
+        ws.record_stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream())
+    return ws.data_ptr(), nbytes, ws
 
 
 class Act8:
@@ -178,72 +181,77 @@ def fsdp_act8_bytes(rows: int, cols: int) -> int:
 
 
 def fsdp_act8_store(x, ckpt: Act8, stream=None) -> None:
-    a = _Args("fsdp_act8_store")
-    p, ld, dt = a.matrix("x", x)
-    c = a.ckpt("ckpt", ckpt, x.shape[0], x.shape[1])
-    _check(_lib.fsdp_act8_store(p, dt, ckpt.rows, ckpt.cols, ld, c, a.stream(stream)), "fsdp_act8_store")
+    where = "fsdp_act8_store"
+    p, ld, dt, dev = _matrix(where, "x", x, None, None, _BOTH, None)
+    c, dev = _ckpt(where, "ckpt", ckpt, *x.shape, dev)
+    _check(_lib.fsdp_act8_store(p, dt, ckpt.rows, ckpt.cols, ld, c, _handle(where, stream, dev)), where)
 
 
 def fsdp_act8_load(ckpt: Act8, y, stream=None) -> None:
-    a = _Args("fsdp_act8_load")
-    p, ld, dt = a.matrix("y", y)
-    c = a.ckpt("ckpt", ckpt, y.shape[0], y.shape[1])
-    _check(_lib.fsdp_act8_load(c, ckpt.rows, ckpt.cols, p, dt, ld, a.stream(stream)), "fsdp_act8_load")
+    where = "fsdp_act8_load"
+    p, ld, dt, dev = _matrix(where, "y", y, None, None, _BOTH, None)
+    c, dev = _ckpt(where, "ckpt", ckpt, *y.shape, dev)
+    _check(_lib.fsdp_act8_load(c, ckpt.rows, ckpt.cols, p, dt, ld, _handle(where, stream, dev)), where)
 
 
-def _norm_input(a: _Args, x, rows, cols):
-    """(pointer, row distance, dtype code) of a norm's input, a tensor or a checkpoint."""
+def _norm_input(where, x, rows, cols, dev):
+    """(pointer, row distance, dtype code, device) of a norm's input, a tensor or a checkpoint."""
     if isinstance(x, Act8):
-        return a.ckpt("x", x, rows, cols), cols, FSDP_ACT8
-    return a.matrix("x", x, rows, cols)
+        p, dev = _ckpt(where, "x", x, rows, cols, dev)
+        return p, cols, FSDP_ACT8, dev
+    return _matrix(where, "x", x, rows, cols, _BOTH, dev)
 
 
 def fsdp_layer_norm_forward(x, weight, bias, y, mean=None, rstd=None, eps=1e-5, keep=None, stream=None) -> None:
     """x: a tensor or its ``Act8`` checkpoint; keep: an ``Act8`` that receives x's checkpoint in the same pass."""
-    a = _Args("fsdp_layer_norm_forward")
-    py, ld_y, dt_y = a.matrix("y", y)
+    where = "fsdp_layer_norm_forward"
+    py, ld_y, dt_y, dev = _matrix(where, "y", y, None, None, _BOTH, None)
     rows, cols = y.shape
-    px, ld_x, dt_x = _norm_input(a, x, rows, cols)
-    pw, dt_w = a.vector("weight", weight, cols)
-    pb, dt_b = a.vector("bias", bias, cols)
-    if dt_w is not None and dt_b is not None and dt_w != dt_b:
-        a.fail("weight and bias have different dtypes")
-    f32 = (torch.float32,)
-    pm, pr = a.vector("mean", mean, rows, f32)[0], a.vector("rstd", rstd, rows, f32)[0]
-    pk = None if keep is None else a.ckpt("keep", keep, rows, cols)
-    d = fsdp_norm_desc_t(rows, cols, ld_x, ld_y, cols, dt_x, dt_y, FSDP_DTYPE_F32,
-                         dt_w if dt_w is not None else dt_b if dt_b is not None else FSDP_DTYPE_F32, FSDP_DTYPE_F32, eps)
-    if rows and (pm is None) != (pr is None):
-        a.fail("mean and rstd are given together or not at all")
+    px, ld_x, dt_x, dev = _norm_input(where, x, rows, cols, dev)
+    pw, dt_w, dev = _vector(where, "weight", weight, cols, _BOTH, dev)
+    pb, dt_b, dev = _vector(where, "bias", bias, cols, _BOTH, dev)
+    if dt_w is None:
+        dt_w = FSDP_DTYPE_F32 if dt_b is None else dt_b
+    elif dt_b is not None and dt_w != dt_b:
+        raise ValueError(f"{where}: weight and bias have different dtypes")
+    pm, _, dev = _vector(where, "mean", mean, rows, _F32, dev)
+    pr, _, dev = _vector(where, "rstd", rstd, rows, _F32, dev)
+    if (mean is None) != (rstd is None):
+        raise ValueError(f"{where}: mean and rstd are given together or not at all")
     if rows == 0:
         pm = pr = None
-    _check(_lib.fsdp_layer_norm_forward(ctypes.byref(d), px, pw, pb, py, pm, pr, pk, a.stream(stream)),
-           "fsdp_layer_norm_forward")
+    pk = None
+    if keep is not None:
+        pk, dev = _ckpt(where, "keep", keep, rows, cols, dev)
+    d = fsdp_norm_desc_t(rows, cols, ld_x, ld_y, cols, dt_x, dt_y, FSDP_DTYPE_F32, dt_w, FSDP_DTYPE_F32, eps)
+    _check(_lib.fsdp_layer_norm_forward(ctypes.byref(d), px, pw, pb, py, pm, pr, pk, _handle(where, stream, dev)), where)
 
 
 def fsdp_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None, workspace=None,
                              stream=None) -> None:
     """x: a tensor or its ``Act8`` checkpoint; dx, dweight and dbias: what is wanted, written."""
-    a = _Args("fsdp_layer_norm_backward")
-    py, ld_y, dt_y = a.matrix("dy", dy)
+    where = "fsdp_layer_norm_backward"
+    py, ld_y, dt_y, dev = _matrix(where, "dy", dy, None, None, _BOTH, None)
     rows, cols = dy.shape
-    px, ld_x, dt_x = _norm_input(a, x, rows, cols)
-    pw, dt_w = a.vector("weight", weight, cols)
-    f32 = (torch.float32,)
+    px, ld_x, dt_x, dev = _norm_input(where, x, rows, cols, dev)
+    pw, dt_w, dev = _vector(where, "weight", weight, cols, _BOTH, dev)
     if mean is None or rstd is None:
-        a.fail("mean and rstd are needed")
-    pm, pr = a.vector("mean", mean, rows, f32)[0], a.vector("rstd", rstd, rows, f32)[0]
-    pd, ld_d, dt_d = (None, cols, FSDP_DTYPE_F32) if dx is None else a.matrix("dx", dx, rows, cols)
-    pdw, dt_dw = a.vector("dweight", dweight, cols)
-    pdb, dt_db = a.vector("dbias", dbias, cols)
-    if dt_dw is not None and dt_db is not None and dt_dw != dt_db:
-        a.fail("dweight and dbias have different dtypes")
-    d = fsdp_norm_desc_t(rows, cols, ld_x, ld_y, ld_d, dt_x, dt_y, dt_d, dt_w if dt_w is not None else FSDP_DTYPE_F32,
-                         dt_dw if dt_dw is not None else dt_db if dt_db is not None else FSDP_DTYPE_F32, 0.0)
-    handle = a.stream(stream)
-    pws, nws, _owner = a.workspace(workspace, _norm_workspace(d), handle)
-    _check(_lib.fsdp_layer_norm_backward(ctypes.byref(d), py, px, pw, pm, pr, pd, pdw, pdb, pws, nws, handle),
-           "fsdp_layer_norm_backward")
+        raise ValueError(f"{where}: mean and rstd are needed")
+    pm, _, dev = _vector(where, "mean", mean, rows, _F32, dev)
+    pr, _, dev = _vector(where, "rstd", rstd, rows, _F32, dev)
+    pd, ld_d, dt_d = None, cols, FSDP_DTYPE_F32
+    if dx is not None:
+        pd, ld_d, dt_d, dev = _matrix(where, "dx", dx, rows, cols, _BOTH, dev)
+    pdw, dt_dw, dev = _vector(where, "dweight", dweight, cols, _BOTH, dev)
+    pdb, dt_db, dev = _vector(where, "dbias", dbias, cols, _BOTH, dev)
+    if dt_dw is None:
+        dt_dw = FSDP_DTYPE_F32 if dt_db is None else dt_db
+    elif dt_db is not None and dt_dw != dt_db:
+        raise ValueError(f"{where}: dweight and dbias have different dtypes")
+    d = fsdp_norm_desc_t(rows, cols, ld_x, ld_y, ld_d, dt_x, dt_y, dt_d, FSDP_DTYPE_F32 if dt_w is None else dt_w, dt_dw, 0.0)
+    handle = _handle(where, stream, dev)
+    pws, nws, _owner = _workspace(where, workspace, _norm_workspace(d), handle, dev)
+    _check(_lib.fsdp_layer_norm_backward(ctypes.byref(d), py, px, pw, pm, pr, pd, pdw, pdb, pws, nws, handle), where)
 
 
 def _norm_workspace(d) -> int:
@@ -257,22 +265,21 @@ def fsdp_layer_norm_workspace(rows: int, cols: int) -> int:
     return _norm_workspace(fsdp_norm_desc_t(rows, cols, cols, cols, cols, 0, 0, 0, 0, 0, 0.0))
 
 
-_BF16_ONLY = (torch.bfloat16,)
-
-
-def _kept(a: _Args, gate, up, rows, f):
-    """(gate pointer, up pointer, row distance, FSDP_KEEP_*)."""
+def _kept(where, gate, up, rows, f, dev):
+    """(gate pointer, up pointer, row distance, FSDP_KEEP_*, device)."""
     if (gate is None) != (up is None):
-        a.fail("gate and up are given together or not at all")
+        raise ValueError(f"{where}: gate and up are given together or not at all")
     if gate is None:
-        return None, None, f, FSDP_KEEP_NONE
+        return None, None, f, FSDP_KEEP_NONE, dev
     if isinstance(gate, Act8) or isinstance(up, Act8):
-        return a.ckpt("gate", gate, rows, f), a.ckpt("up", up, rows, f), f, FSDP_KEEP_ACT8
-    pg, lg, _ = a.matrix("gate", gate, rows, f, _BF16_ONLY)
-    pu, lu, _ = a.matrix("up", up, rows, f, _BF16_ONLY)
+        pg, dev = _ckpt(where, "gate", gate, rows, f, dev)
+        pu, dev = _ckpt(where, "up", up, rows, f, dev)
+        return pg, pu, f, FSDP_KEEP_ACT8, dev
+    pg, lg, _, dev = _matrix(where, "gate", gate, rows, f, _BF16, dev)
+    pu, lu, _, dev = _matrix(where, "up", up, rows, f, _BF16, dev)
     if lg != lu:
-        a.fail("gate and up have different row distances")
-    return pg, pu, lg, FSDP_KEEP_BF16
+        raise ValueError(f"{where}: gate and up have different row distances")
+    return pg, pu, lg, FSDP_KEEP_BF16, dev
 
 
 def _ffn_workspace(d, backward) -> int:
@@ -291,63 +298,62 @@ def fsdp_gated_ffn_workspace(rows: int, d: int, f: int, backward: bool, keep: in
     return _ffn_workspace(desc, int(backward))
 
 
-def _off16(*ptrs) -> int:
-    return sum(1 << i for i, p in enumerate(ptrs) if p is not None and p % 16)
-
-
 def fsdp_gated_ffn_forward(x, w_gate, w_up, h, gate=None, up=None, activation=FSDP_ACT_SILU, workspace=None,
                            stream=None) -> None:
     """gate, up: what is kept for the backward pass: ``Act8`` checkpoints, BF16 tensors, or nothing."""
-    a = _Args("fsdp_gated_ffn_forward")
-    px, ld_x, _ = a.matrix("x", x, dtypes=_BF16_ONLY)
+    where = "fsdp_gated_ffn_forward"
+    px, ld_x, dt, dev = _matrix(where, "x", x, None, None, _BF16, None)
     rows, d = x.shape
-    pg, ld_g, _ = a.matrix("w_gate", w_gate, None, d, _BF16_ONLY)
+    pg, ld_g, _, dev = _matrix(where, "w_gate", w_gate, None, d, _BF16, dev)
     f = w_gate.shape[0]
-    pu, ld_u, _ = a.matrix("w_up", w_up, f, d, _BF16_ONLY)
-    ph, ld_h, _ = a.matrix("h", h, rows, f, _BF16_ONLY)
-    pkg, pku, ld_k, keep = _kept(a, gate, up, rows, f)
-    desc = fsdp_ffn_desc_t(rows, d, f, ld_x, ld_g, ld_u, ld_h, ld_k, d, d, d, activation, keep, FSDP_DTYPE_BF16,
-                           FSDP_DTYPE_BF16, FSDP_DTYPE_BF16, _off16(px, pg, pu))
-    handle = a.stream(stream)
-    pws, nws, _owner = a.workspace(workspace, _ffn_workspace(desc, 0), handle)
-    _check(_lib.fsdp_gated_ffn_forward(ctypes.byref(desc), px, pg, pu, ph, pkg, pku, pws, nws, handle),
-           "fsdp_gated_ffn_forward")
+    pu, ld_u, _, dev = _matrix(where, "w_up", w_up, f, d, _BF16, dev)
+    ph, ld_h, _, dev = _matrix(where, "h", h, rows, f, _BF16, dev)
+    pkg, pku, ld_k, keep, dev = _kept(where, gate, up, rows, f, dev)
+    off = (px % 16 > 0) + 2 * (pg % 16 > 0) + 4 * (pu % 16 > 0)
+    desc = fsdp_ffn_desc_t(rows, d, f, ld_x, ld_g, ld_u, ld_h, ld_k, d, d, d, activation, keep, dt, dt, dt, off)
+    handle = _handle(where, stream, dev)
+    pws, nws, _owner = _workspace(where, workspace, _ffn_workspace(desc, 0), handle, dev)
+    _check(_lib.fsdp_gated_ffn_forward(ctypes.byref(desc), px, pg, pu, ph, pkg, pku, pws, nws, handle), where)
 
 
 def fsdp_gated_ffn_backward(dh, x, w_gate, w_up, dx=None, dw_gate=None, dw_up=None, gate=None, up=None,
                             activation=FSDP_ACT_SILU, workspace=None, stream=None) -> None:
     """x: the forward pass's input or its ``Act8`` checkpoint; gate, up: as kept (None: computed again);
     dx, dw_gate and dw_up: what is wanted, written."""
-    a = _Args("fsdp_gated_ffn_backward")
-    pdh, ld_h, _ = a.matrix("dh", dh, dtypes=_BF16_ONLY)
+    where = "fsdp_gated_ffn_backward"
+    pdh, ld_h, dt, dev = _matrix(where, "dh", dh, None, None, _BF16, None)
     rows, f = dh.shape
-    pg, ld_g, _ = a.matrix("w_gate", w_gate, f, None, _BF16_ONLY)
+    pg, ld_g, _, dev = _matrix(where, "w_gate", w_gate, f, None, _BF16, dev)
     d = w_gate.shape[1]
-    pu, ld_u, _ = a.matrix("w_up", w_up, f, d, _BF16_ONLY)
+    pu, ld_u, _, dev = _matrix(where, "w_up", w_up, f, d, _BF16, dev)
+    off = 2 * (pg % 16 > 0) + 4 * (pu % 16 > 0)
     if isinstance(x, Act8):
-        px, ld_x, dt_x = a.ckpt("x", x, rows, d), d, FSDP_ACT8
+        px, dev = _ckpt(where, "x", x, rows, d, dev)
+        ld_x, dt_x = d, FSDP_ACT8
     else:
-        px, ld_x, dt_x = a.matrix("x", x, rows, d, _BF16_ONLY)
-    pkg, pku, ld_k, keep = _kept(a, gate, up, rows, f)
-    pdx, ld_dx, dt_dx = (None, d, FSDP_DTYPE_BF16) if dx is None else a.matrix("dx", dx, rows, d)
+        px, ld_x, dt_x, dev = _matrix(where, "x", x, rows, d, _BF16, dev)
+        off += px % 16 > 0
+    pkg, pku, ld_k, keep, dev = _kept(where, gate, up, rows, f, dev)
+    pdx, ld_dx, dt_dx = None, d, dt
+    if dx is not None:
+        pdx, ld_dx, dt_dx, dev = _matrix(where, "dx", dx, rows, d, _BOTH, dev)
     if (dw_gate is None) != (dw_up is None):
-        a.fail("dw_gate and dw_up are given together or not at all")
+        raise ValueError(f"{where}: dw_gate and dw_up are given together or not at all")
     pdg = pdu = None
     ld_dg = ld_du = d
-    dt_dw = FSDP_DTYPE_BF16
+    dt_dw = dt
     if dw_gate is not None:
-        pdg, ld_dg, dt_dw = a.matrix("dw_gate", dw_gate, f, d)
-        pdu, ld_du, dt_u = a.matrix("dw_up", dw_up, f, d)
+        pdg, ld_dg, dt_dw, dev = _matrix(where, "dw_gate", dw_gate, f, d, _BOTH, dev)
+        pdu, ld_du, dt_u, dev = _matrix(where, "dw_up", dw_up, f, d, _BOTH, dev)
         if dt_u != dt_dw:
-            a.fail("dw_gate and dw_up have different dtypes")
+            raise ValueError(f"{where}: dw_gate and dw_up have different dtypes")
     desc = fsdp_ffn_desc_t(rows, d, f, ld_x, ld_g, ld_u, ld_h, ld_k, ld_dx, ld_dg, ld_du, activation, keep, dt_x, dt_dx,
-                           dt_dw, _off16(None if dt_x == FSDP_ACT8 else px, pg, pu))
-    handle = a.stream(stream)
-    pws, nws, _owner = a.workspace(workspace, _ffn_workspace(desc, 1), handle)
+                           dt_dw, off)
+    handle = _handle(where, stream, dev)
+    pws, nws, _owner = _workspace(where, workspace, _ffn_workspace(desc, 1), handle, dev)
     _check(_lib.fsdp_gated_ffn_backward(ctypes.byref(desc), pdh, px, pg, pu, pkg, pku, pdx, pdg, pdu, pws, nws, handle),
-           "fsdp_gated_ffn_backward")
+           where)
 
 
 def fsdp_ops_sync_status(stream=None) -> None:
-    a = _Args("fsdp_ops_sync_status")
-    _check(_lib.fsdp_ops_sync_status(a.stream(stream)), "fsdp_ops_sync_status")
+    _check(_lib.fsdp_ops_sync_status(_fp._stream(stream)), "fsdp_ops_sync_status")
