@@ -62,43 +62,66 @@ __device__ __forceinline__ Unit unit_at(const Args &a, int i) {
   return u;
 }
 
-// Loads one K block of a tile into a stage.  `rank`: this block's place in its pair.
+// How a tile's K blocks are loaded: boxes at (x, y) of two maps, advanced by (kx, ky) from
+// K block to K block.  One thread loads and one issues MMAs, about 500 cycles to a K
+// block, so what they do for each is worked out once a tile.
 template <int MODE, int CG>
-__device__ __forceinline__ void load_stage(const Args &a, const Unit &u, int kb, int rank, uint32_t at, uint32_t bar) {
-  using S = Shape<CG>;
-  const uint32_t sa = at, sb = at + S::kA;
-  if constexpr (MODE == FORWARD || MODE == RECOMPUTE) {
-    const int half = a.tile_n / 2, n0 = u.n * half;
-    tc::tma_load<CG>(sa, &a.a[0], kb * kTileK, (u.m * CG + rank) * kTileM, bar);
-    if constexpr (CG == 1) {
-      tc::tma_load<CG>(sb, &a.b[0], kb * kTileK, n0, bar);
-      tc::tma_load<CG>(sb + half * (kTileK * 2), &a.b[1], kb * kTileK, n0, bar);
+struct Loader {
+  const CUtensorMap *ma, *mb, *mb2;
+  int ax, ay, bx, by;        // next box of A and of B
+  int acx, acy;              // from one box of A to the next in the stage
+  int kax, kay, kby;         // K block to K block: A along x or y, B (not FORWARD) along y
+
+  __device__ Loader(const Args &a, const Unit &u, int rank) {
+    if constexpr (MODE != BACKWARD) {
+      const int half = a.tile_n / 2;
+      ma = &a.a[0], mb = &a.b[CG == 1 ? 0 : rank], mb2 = &a.b[1];
+      ax = u.k0 * kTileK, ay = (u.m * CG + rank) * kTileM;
+      bx = ax, by = u.n * half;
     } else {
-      tc::tma_load<CG>(sb, &a.b[rank], kb * kTileK, n0, bar);
+      // Boxes of 64 x 64 throughout.  Along K in a row (A of dx): two boxes of 64 rows lie
+      // one after the other; along M or N in a row: one box to 64 of them.
+      bx = u.n * kTileN + rank * (kTileN / CG);
+      if (u.which == 1) {
+        go_to(a, u.k0);
+        ay = (u.m * CG + rank) * kTileM;
+        acx = 0, acy = 64, kax = kTileK, kay = 0;
+      } else {
+        const int up = u.m >= a.half[0];
+        ma = &a.a[up], mb = &a.b[2];
+        ax = ((u.m - up * a.half[0]) * CG + rank) * kTileM, ay = by = u.k0 * kTileK;
+        acx = 64, acy = 0, kax = 0, kay = kTileK;
+      }
+      kby = kTileK;
     }
-  } else {
-    // Boxes of 64 x 64 throughout.  Along K in a row (A of dx): two boxes of 64 rows lie
-    // one after the other; along M or N in a row: one box to 64 of them.
-    const CUtensorMap *ma, *mb;
-    int k0 = kb * kTileK, m0;
-    if (u.which == 1) {
-      const int up = kb >= a.half[1];
-      ma = &a.a[up], mb = &a.b[up];
-      k0 -= up * a.half[1] * kTileK;
-      m0 = (u.m * CG + rank) * kTileM;
-    } else {
-      const int up = u.m >= a.half[0];
-      ma = &a.a[up], mb = &a.b[2];
-      m0 = ((u.m - up * a.half[0]) * CG + rank) * kTileM;
-    }
-#pragma unroll
-    for (int c = 0; c < kTileM / 64; ++c)
-      tc::tma_load<CG>(sa + c * 8192, ma, u.which == 1 ? k0 : m0 + c * 64, u.which == 1 ? m0 + c * 64 : k0, bar);
-#pragma unroll
-    for (int c = 0; c < kTileN / CG / 64; ++c)
-      tc::tma_load<CG>(sb + c * 8192, mb, u.n * kTileN + rank * (kTileN / CG) + c * 64, k0, bar);
   }
-}
+  // dx: the K block `kb` of the sum over gate and up.
+  __device__ __forceinline__ void go_to(const Args &a, int kb) {
+    const int up = kb >= a.half[1];
+    ma = &a.a[up], mb = &a.b[up];
+    ax = by = (kb - up * a.half[1]) * kTileK;
+  }
+  __device__ __forceinline__ void load(const Args &a, uint32_t at, uint32_t bar) const {
+    using S = Shape<CG>;
+    const uint32_t sb = at + S::kA;
+    if constexpr (MODE != BACKWARD) {
+      tc::tma_load<CG>(at, ma, ax, ay, bar);
+      tc::tma_load<CG>(sb, mb, bx, by, bar);
+      if constexpr (CG == 1) tc::tma_load<CG>(sb + a.tile_n / 2 * (kTileK * 2), mb2, bx, by, bar);
+    } else {
+#pragma unroll
+      for (int c = 0; c < kTileM / 64; ++c) tc::tma_load<CG>(at + c * 8192, ma, ax + c * acx, ay + c * acy, bar);
+#pragma unroll
+      for (int c = 0; c < kTileN / CG / 64; ++c) tc::tma_load<CG>(sb + c * 8192, mb, bx + c * 64, by, bar);
+    }
+  }
+  __device__ __forceinline__ void advance() {
+    if constexpr (MODE != BACKWARD)
+      ax += kTileK, bx += kTileK;
+    else
+      ax += kax, ay += kay, by += kby;
+  }
+};
 
 // A warp's 32 x 32 part of a tile: one row to a thread.
 struct Part {
@@ -240,19 +263,6 @@ __device__ __forceinline__ void gated_part(const Args &a, const uint32_t (&gr)[3
   }
 }
 
-// The four MMAs of one stage.  Descriptors advance by 16 K values: 32 bytes within a
-// row, or 16 rows of 128 bytes.  With the majors known at run time only, one thread
-// could no longer issue them at the tensor cores' rate (11 % of the products' time).
-template <int CG, bool A_MN, bool B_MN>
-__device__ __forceinline__ void multiply_stage(uint32_t d, uint32_t sa, uint32_t sb, int columns, bool add) {
-  constexpr uint32_t kStepA = A_MN ? 2048 : 32, kStepB = B_MN ? 2048 : 32;
-  const uint32_t idesc = tc::instruction(kTileM * CG, columns, A_MN, B_MN);
-#pragma unroll
-  for (int k = 0; k < kTileK / 16; ++k)
-    tc::mma<CG>(d, tc::operand(sa + k * kStepA, A_MN ? 8192 : 16, 1024), tc::operand(sb + k * kStepB, B_MN ? 8192 : 16, 1024),
-                idesc, add || k > 0);
-}
-
 // Test hook: the first worker leaves its first stage empty, so the wait for it gives up.
 __device__ __forceinline__ bool skips_first(const Args &a, int worker) { return a.fault != 0 && worker == 0; }
 
@@ -321,15 +331,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     if (lane == 0) {
       uint32_t stage = 0, phase = 0, filled = 0;
       const uint32_t bytes = CG * S::kA + (MODE == BACKWARD ? kTileN : a.tile_n) * (kTileK * 2);
+      const uint32_t full = tc::smem(&sh.full[0]), empty = tc::smem(&sh.empty[0]);
+      const uint32_t leader = CG == 1 ? full : tc::at_rank(full, 0);
+      const bool skip = skips_first(a, worker);
       for (int i = worker; i < units && ok; i += workers) {
         const Unit u = unit_at<MODE>(a, i);
+        Loader<MODE, CG> from(a, u, rank);
         for (int kb = u.k0; kb < u.k1; ++kb) {
-          const uint32_t full = tc::smem(&sh.full[stage]), full_leader = CG == 1 ? full : tc::at_rank(full, 0);
-          if (!(ok = tc::bar_wait(tc::smem(&sh.empty[stage]), phase ^ 1u, a.wait_limit_ns, stop))) break;
-          if (!skips_first(a, worker) || filled > 0) {
-            if (rank == 0) tc::bar_expect(full, bytes);
-            load_stage<MODE, CG>(a, u, kb, rank, stages + stage * S::kStage, full_leader);
+          if (!(ok = tc::bar_wait(empty + stage * 8, phase ^ 1u, a.wait_limit_ns, stop))) break;
+          if (MODE == BACKWARD && u.which == 1 && kb == a.half[1]) from.go_to(a, kb);
+          if (!skip || filled > 0) {
+            if (rank == 0) tc::bar_expect(full + stage * 8, bytes);
+            from.load(a, stages + stage * S::kStage, leader + stage * 8);
           }
+          from.advance();
           ++filled;
           if (++stage == S::kStages) stage = 0, phase ^= 1u;
         }
@@ -347,23 +362,31 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     if (lane == 0 && rank == 0) {
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool issued = false;
+      const uint32_t full = tc::smem(&sh.full[0]), empty = tc::smem(&sh.empty[0]);
       for (int i = worker; i < units && ok; i += workers) {
         const Unit u = unit_at<MODE>(a, i);
         if (!(ok = tc::bar_wait(tc::smem(&sh.tmem_empty[acc]), acc_phase ^ 1u, a.wait_limit_ns, stop))) break;
         tc::fence_after();
         const uint32_t d = tmem + acc * kTileN;
+        // Majors by use.  Descriptors advance by 16 K values: 32 bytes within a row, or 16
+        // rows of 128 bytes (in units of 16 bytes).
+        const bool a_mn = MODE == BACKWARD && u.which == 0, b_mn = MODE == BACKWARD;
+        const uint32_t idesc = tc::instruction(kTileM * CG, MODE == BACKWARD ? kTileN : a.tile_n, a_mn, b_mn);
+        const uint32_t a0 = tc::operand_low(stages, a_mn ? 8192 : 16), b0 = tc::operand_low(stages + S::kA, b_mn ? 8192 : 16);
+        const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;
+        constexpr uint32_t kHigh = tc::operand_high(1024);
+        uint32_t add = 0;
         for (int kb = u.k0; kb < u.k1; ++kb) {
-          if (!(ok = tc::bar_wait(tc::smem(&sh.full[stage]), phase, a.wait_limit_ns, stop))) break;
+          if (!(ok = tc::bar_wait(full + stage * 8, phase, a.wait_limit_ns, stop))) break;
           tc::fence_after();
-          const uint32_t sa = stages + stage * S::kStage, sb = sa + S::kA;
-          if (MODE != BACKWARD)
-            multiply_stage<CG, false, false>(d, sa, sb, a.tile_n, kb > u.k0);
-          else if (u.which == 0)
-            multiply_stage<CG, true, true>(d, sa, sb, kTileN, kb > u.k0);
-          else
-            multiply_stage<CG, false, true>(d, sa, sb, kTileN, kb > u.k0);
+          uint32_t al = a0 + stage * (S::kStage / 16), bl = b0 + stage * (S::kStage / 16);
+#pragma unroll
+          for (int k = 0; k < kTileK / 16; ++k) {
+            tc::mma<CG>(d, al, kHigh, bl, kHigh, idesc, add);
+            al += a_step, bl += b_step, add = 1;
+          }
           issued = true;
-          tc::mma_commit<CG>(tc::smem(&sh.empty[stage]));
+          tc::mma_commit<CG>(empty + stage * 8);
           if (++stage == S::kStages) stage = 0, phase ^= 1u;
         }
         if (!ok) break;

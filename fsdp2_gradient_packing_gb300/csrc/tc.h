@@ -125,20 +125,22 @@ __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// D (TMEM) = A * B (+ D), BF16 operands in shared memory, one K step of 16.
+// D (TMEM) = A * B (+ D), BF16 operands in shared memory, one K step of 16.  Operand
+// descriptors come as two words: only the low one, with the address, moves along K.
 template <int CG>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_low, uint32_t a_high, uint32_t b_low, uint32_t b_high,
+                                    uint32_t idesc, uint32_t add) {
   if constexpr (CG == 1) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_low), "r"(a_high), "r"(b_low), "r"(b_high), "r"(idesc), "r"(add)
         : "memory");
   } else {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_low), "r"(a_high), "r"(b_low), "r"(b_high), "r"(idesc), "r"(add)
         : "memory");
   }
 }
@@ -171,10 +173,10 @@ __device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::l
 // (128 bytes), 8 of them an atom, atoms `stride` bytes apart.  MN-major: rows of 64
 // M or N values, one row per K; 8 K rows an atom, atoms `stride` bytes apart along
 // K and `lead` bytes apart along M or N.
-__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lead, uint32_t stride) {
-  return (uint64_t)((at & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+__device__ __forceinline__ uint32_t operand_low(uint32_t at, uint32_t lead) {
+  return (at & 0x3FFFFu) >> 4 | (lead >> 4) << 16;
 }
+__host__ __device__ constexpr uint32_t operand_high(uint32_t stride) { return stride >> 4 | 1u << 14 | 2u << 29; }
 // Instruction descriptor: BF16 x BF16 -> FP32, M x N, operand majors.
 __host__ __device__ constexpr uint32_t instruction(int m, int n, bool a_mn_major, bool b_mn_major) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)a_mn_major << 15 | (uint32_t)b_mn_major << 16 |
