@@ -99,13 +99,14 @@ struct SlopeArgs {
   const uint8_t *scales[2];
   uint16_t *dg, *du;
   int64_t rows, f, ld_dh, ld_kept, groups, pitch;
-  int32_t act, act8, dh_vec, kept_vec;
+  int32_t dh_vec, kept_vec;
 };
 
 // Bound: HBM, 2 + 33/16 + 4 bytes an element from 8-bit checkpoints.  Eight columns
 // make a unit; a thread has kUnits of them in flight.
 constexpr int kUnits = 2;
 
+template <int ACT, bool ACT8>
 __global__ void __launch_bounds__(kThreads) slope_kernel(const __grid_constant__ SlopeArgs a) {
   const int64_t per_row = (a.f + 7) / 8, total = a.rows * per_row;
   wait_for_previous();
@@ -136,8 +137,8 @@ __global__ void __launch_bounds__(kThreads) slope_kernel(const __grid_constant__
         return make_uint4(c.x, c.y, scales[row[q] * a.groups + col[q] / (int)kActGroup], 0);
       };
       d[q] = load(a.dh, a.ld_dh, a.dh_vec != 0);
-      g[q] = a.act8 ? load_codes(a.gate, a.scales[0]) : load(a.gate, a.ld_kept, a.kept_vec != 0);
-      u[q] = a.act8 ? load_codes(a.up, a.scales[1]) : load(a.up, a.ld_kept, a.kept_vec != 0);
+      g[q] = ACT8 ? load_codes(a.gate, a.scales[0]) : load(a.gate, a.ld_kept, a.kept_vec != 0);
+      u[q] = ACT8 ? load_codes(a.up, a.scales[1]) : load(a.up, a.ld_kept, a.kept_vec != 0);
     }
 #pragma unroll
     for (int q = 0; q < kUnits; ++q) {
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) slope_kernel(const __grid_constant__
       float2 dv[4], gv[4], uv[4];
       unpack8(d[q], dv);
       auto values = [&](float2(&v)[4], const uint4 &r) {
-        if (!a.act8) return unpack8(r, v);
+        if (!ACT8) return unpack8(r, v);
         const float2 scale = both(act8_scale(r.z));
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = __fmul2_rn(act8_codes_of(act8_biased(e < 2 ? r.x : r.y), e % 2), scale);
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) slope_kernel(const __grid_constant__
       values(uv, u[q]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 p = act_of<true>(gv[e].x, a.act), r = act_of<true>(gv[e].y, a.act);
+        const float2 p = act_of<true>(gv[e].x, ACT), r = act_of<true>(gv[e].y, ACT);
         gv[e] = __fmul2_rn(__fmul2_rn(dv[e], uv[e]), make_float2(p.y, r.y));
         uv[e] = __fmul2_rn(dv[e], make_float2(p.x, r.x));
       }
@@ -457,7 +458,9 @@ struct Call {
     a.wait_limit_ns = wait_limit_ns();
     a.fault = wait_fault();
     a.act = d->activation == FSDP_ACT_SILU ? SILU : GELU;
-    return launched(launch_product(mode, pair, a, plan.sms, stream));
+    return launched((mode == FORWARD     ? launch_forward
+                     : mode == RECOMPUTE ? launch_recompute
+                                         : launch_backward)(pair, a, plan.sms, stream));
   }
 
   // FORWARD or RECOMPUTE.
@@ -610,18 +613,21 @@ fsdp_status_t fsdp_gated_ffn_backward(const fsdp_ffn_desc_t *d, const void *dh, 
     SlopeArgs s = {};
     s.dh = dh, s.gate = gate, s.up = up;
     s.groups = act8_groups(d->f);
-    s.act8 = d->keep == FSDP_KEEP_ACT8;
     const void *p[2] = {gate, up};
     for (int i = 0; i < 2; ++i) s.scales[i] = static_cast<const uint8_t *>(p[i]) + d->rows * s.groups * kActGroup;
     s.dg = dg, s.du = du;
     s.rows = d->rows, s.f = d->f, s.ld_dh = d->ld_h, s.ld_kept = d->ld_kept, s.pitch = c.plan.f_pitch;
-    s.act = d->activation == FSDP_ACT_SILU ? SILU : GELU;
     s.dh_vec = vec_rows(dh, d->rows, d->ld_h, 2);
     s.kept_vec = vec_rows(gate, d->rows, d->ld_kept, 2) && vec_rows(up, d->rows, d->ld_kept, 2);
     int64_t grid = blocks_of(d->rows * blocks_of(d->f, 8), kThreads * kUnits);
     if (grid > (int64_t)c.plan.sms * 64) grid = (int64_t)c.plan.sms * 64;
+    const bool silu = d->activation == FSDP_ACT_SILU, act8 = d->keep == FSDP_KEEP_ACT8;
+    const void *fn = silu ? (act8 ? reinterpret_cast<const void *>(&slope_kernel<SILU, true>)
+                                  : reinterpret_cast<const void *>(&slope_kernel<SILU, false>))
+                          : (act8 ? reinterpret_cast<const void *>(&slope_kernel<GELU, true>)
+                                  : reinterpret_cast<const void *>(&slope_kernel<GELU, false>));
     void *args[] = {&s};
-    st = launched(launch_kernel(reinterpret_cast<const void *>(&slope_kernel), dim3((unsigned)grid), dim3(kThreads), args, 0,
+    st = launched(launch_kernel(fn, dim3((unsigned)grid), dim3(kThreads), args, 0,
                                 c.stream, true));
     if (st != FSDP_OK) return st;
   }

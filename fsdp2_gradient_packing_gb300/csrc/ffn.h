@@ -98,8 +98,10 @@ constexpr int kFewRows = 4;
 // starts on a 16-byte boundary.
 cudaError_t launch_rows(const RowsArgs &a, bool vec, cudaStream_t stream);
 
-// Launches the product kernel of `mode`; `pair`: tiles of two blocks (256 rows).
-cudaError_t launch_product(Mode mode, bool pair, Args &a, int sms, cudaStream_t stream);
+// Launch the product kernel for one use; `pair`: tiles of two blocks (256 rows).
+cudaError_t launch_forward(bool pair, Args &a, int sms, cudaStream_t stream);
+cudaError_t launch_recompute(bool pair, Args &a, int sms, cudaStream_t stream);
+cudaError_t launch_backward(bool pair, Args &a, int sms, cudaStream_t stream);
 
 }  // namespace ffn
 }  // namespace fsdp

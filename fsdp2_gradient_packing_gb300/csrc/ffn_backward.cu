@@ -1,0 +1,11 @@
+#include "ffn_product.h"
+
+namespace fsdp {
+namespace ffn {
+
+cudaError_t launch_backward(bool pair, Args &a, int sms, cudaStream_t stream) {
+  return launch_mode<BACKWARD>(pair, a, sms, stream);
+}
+
+}  // namespace ffn
+}  // namespace fsdp

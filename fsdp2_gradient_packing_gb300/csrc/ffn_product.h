@@ -1,4 +1,7 @@
-// The tensor-core kernel of the gated feed-forward block (see ffn.h).
+// The tensor-core kernel of the gated feed-forward block (see ffn.h).  Included by the
+// files that instantiate it, one to a use, which compile side by side.
+#pragma once
+
 #include "ffn.h"
 
 namespace fsdp {
@@ -227,20 +230,20 @@ __device__ __forceinline__ float2 pair_at(const uint32_t (&r)[32], int i) {
 }
 
 // A warp's part of a gate / up tile.
-template <int MODE>
+template <int MODE, int ACT, int KEEP>
 __device__ __forceinline__ void gated_part(const Args &a, const uint32_t (&gr)[32], const uint32_t (&ur)[32], const Part &q) {
   float2 x[16], y[16];
   if constexpr (MODE == FORWARD) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float2 g = pair_at(gr, i);
-      x[i] = __fmul2_rn(make_float2(act_of<false>(g.x, a.act).x, act_of<false>(g.y, a.act).x), pair_at(ur, i));
+      x[i] = __fmul2_rn(make_float2(act_of<false>(g.x, ACT).x, act_of<false>(g.y, ACT).x), pair_at(ur, i));
     }
     store_part(a.out[0], a.ld_out[0], true, a.out_width[0], x, q);
-    if (a.keep) {
+    if constexpr (KEEP != 0) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = pair_at(gr, i), y[i] = pair_at(ur, i);
-      if (a.keep == 2) {
+      if constexpr (KEEP == 2) {
         store_part(a.kept[0], a.ld_kept, true, a.keep_width, x, q);
         store_part(a.kept[1], a.ld_kept, true, a.keep_width, y, q);
       } else if ((int)(threadIdx.x & 31) < q.rows) {
@@ -254,7 +257,7 @@ __device__ __forceinline__ void gated_part(const Args &a, const uint32_t (&gr)[3
     load_part(static_cast<const __nv_bfloat16 *>(a.dh), a.ld_dh, a.dh_vec != 0, d, q);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float2 g = pair_at(gr, i), p = act_of<true>(g.x, a.act), r = act_of<true>(g.y, a.act);
+      const float2 g = pair_at(gr, i), p = act_of<true>(g.x, ACT), r = act_of<true>(g.y, ACT);
       x[i] = __fmul2_rn(__fmul2_rn(d[i], pair_at(ur, i)), make_float2(p.y, r.y));
       y[i] = __fmul2_rn(d[i], make_float2(p.x, r.x));
     }
@@ -287,7 +290,7 @@ __device__ __noinline__ void land_copies(Shared &sh, const Args &a, int rank, bo
   }
 }
 
-template <int MODE, int CG>
+template <int MODE, int CG, int ACT, int KEEP>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Args a) {
   using S = Shape<CG>;
   extern __shared__ uint8_t dynamic[];
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           if (c + 1 == end) drained();
           const int64_t rows = a.m[0] - (row - lane);
           if (rows > 0 && col < a.n)
-            gated_part<MODE>(a, g, up, {col, (int)min((int64_t)32, a.n - col), (int)min((int64_t)32, rows), row, turn});
+            gated_part<MODE, ACT, KEEP>(a, g, up, {col, (int)min((int64_t)32, a.n - col), (int)min((int64_t)32, rows), row, turn});
         }
       } else {
         const int which = u.which, up = which == 0 && u.m >= a.half[0] ? 1 : 0, to = which == 1 ? 2 : up;
@@ -480,10 +483,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   if (warp == 1) tc::tmem_free<CG>(tmem, kTmemColumns);
 }
 
-template <int MODE, int CG>
+template <int MODE, int CG, int ACT, int KEEP>
 cudaError_t launch(Args &a, int sms, cudaStream_t stream) {
   using S = Shape<CG>;
-  const void *fn = reinterpret_cast<const void *>(&product_kernel<MODE, CG>);
+  const void *fn = reinterpret_cast<const void *>(&product_kernel<MODE, CG, ACT, KEEP>);
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   int64_t units = 0;
@@ -494,15 +497,25 @@ cudaError_t launch(Args &a, int sms, cudaStream_t stream) {
   return launch_kernel(fn, dim3((unsigned)(workers * CG)), dim3(kThreads), args, S::kSmem, stream, true, CG);
 }
 
-}  // namespace
-
-cudaError_t launch_product(Mode mode, bool pair, Args &a, int sms, cudaStream_t stream) {
-  switch (mode) {
-    case FORWARD: return pair ? launch<FORWARD, 2>(a, sms, stream) : launch<FORWARD, 1>(a, sms, stream);
-    case RECOMPUTE: return pair ? launch<RECOMPUTE, 2>(a, sms, stream) : launch<RECOMPUTE, 1>(a, sms, stream);
-    default: return pair ? launch<BACKWARD, 2>(a, sms, stream) : launch<BACKWARD, 1>(a, sms, stream);
+template <int MODE, int CG, int ACT>
+cudaError_t launch_keep(Args &a, int sms, cudaStream_t stream) {
+  if constexpr (MODE == FORWARD) {
+    if (a.keep == 1) return launch<MODE, CG, ACT, 1>(a, sms, stream);
+    if (a.keep == 2) return launch<MODE, CG, ACT, 2>(a, sms, stream);
   }
+  return launch<MODE, CG, ACT, 0>(a, sms, stream);
 }
+
+template <int MODE>
+cudaError_t launch_mode(bool pair, Args &a, int sms, cudaStream_t stream) {
+  if (MODE == BACKWARD || a.act == SILU)
+    return pair ? launch_keep<MODE, 2, SILU>(a, sms, stream) : launch_keep<MODE, 1, SILU>(a, sms, stream);
+  if constexpr (MODE != BACKWARD)
+    return pair ? launch_keep<MODE, 2, GELU>(a, sms, stream) : launch_keep<MODE, 1, GELU>(a, sms, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
 
 }  // namespace ffn
 }  // namespace fsdp
