@@ -385,7 +385,7 @@ inline int64_t units_of(int64_t rows, const Shape &s, int sms, int most_threads)
 }
 
 // Lays out the ring and the rest of shared memory: `params` vectors, then the stages,
-// or after them `sums` vectors (the column sums of the groups) in the same place.
+// or after them `sums` vectors of each group but one (column sums) in the same place.
 inline Launch plan_launch(Args &a, const Shape &s, int sms, int most_threads, int params, int sums) {
   Launch l;
   l.groups = groups_of(a.rows, s, sms, most_threads);
@@ -409,7 +409,7 @@ inline Launch plan_launch(Args &a, const Shape &s, int sms, int most_threads, in
   if (stages > kMaxStages) stages = kMaxStages;
   if (stages > turns) stages = turns;
   a.stages = (int32_t)(stages > 1 ? stages : 1);
-  const int ring = l.groups * a.stages * at, tail = l.groups > 1 ? sums * width * 4 : 0;
+  const int ring = l.groups * a.stages * at, tail = (l.groups - 1) * sums * width * 4;
   l.smem = fixed + (ring > tail ? ring : tail);
   return l;
 }

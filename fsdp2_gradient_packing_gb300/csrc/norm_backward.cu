@@ -12,7 +12,10 @@ namespace fsdp {
 namespace {
 using namespace norm;
 
-constexpr int kMostThreads = 512;  // of a block beside its loading warp, at 120 registers
+// Threads of a block beside its loading warp, at 96 registers: a thread's column sums
+// take 32, its values of a row 32 more.  (A third group at 72 registers spills: 111 us
+// instead of 63 at 16384 x 4096 in BF16 from the checkpoint.)
+constexpr int kMostThreads = 512;
 
 template <int XK, bool YB, bool VEC, int G, int K, bool CLUSTER>
 __global__ void __launch_bounds__(kMostThreads + 32, 1) backward_kernel(const __grid_constant__ Args a) {
@@ -91,26 +94,33 @@ __global__ void __launch_bounds__(kMostThreads + 32, 1) backward_kernel(const __
   }
   let_next_start();
 
-  // Column sums of the block's row groups, added in order, in the ring's memory.
+  // Column sums of the block's row groups, in the ring's memory: each group's to a place
+  // of its own, then each thread of the first group adds its columns in order.
   if (groups > 1) {
     float *const sums = reinterpret_cast<float *>(stages);
     __syncthreads();
-    for (int q = 0; q < groups; ++q) {
-      if (group == q) {
+    if (group > 0 && !loads) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int at = (group - 1) * (2 * G * K * 8) + param_at<VEC, G, K>(t, k, e);
+          sums[at] = element(dw[k], e), sums[at + G * K * 8] = element(db[k], e);
+        }
+    }
+    __syncthreads();
+    if (group == 0)
+#pragma unroll 1
+      for (int q = 0; q < groups - 1; ++q)
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int at = param_at<VEC, G, K>(t, k, e);
-            float &w = element(dw[k], e), &b = element(db[k], e);
-            if (q > 0) w += sums[at], b += sums[G * K * 8 + at];
-            if (q < groups - 1) sums[at] = w, sums[G * K * 8 + at] = b;
+            const int at = q * (2 * G * K * 8) + param_at<VEC, G, K>(t, k, e);
+            element(dw[k], e) += sums[at], element(db[k], e) += sums[at + G * K * 8];
           }
-      }
-      __syncthreads();
-    }
   }
-  if (group == groups - 1) {
+  if (group == 0) {
     if (a.partial) {
       float *to = a.partial + unit * 2 * a.cols + base;
       store_row<VEC, G, K>(dw, reinterpret_cast<uint8_t *>(to), false, mine, t);

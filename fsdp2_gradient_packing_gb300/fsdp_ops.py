@@ -13,6 +13,7 @@ All names here are also names of ``fsdp_pack``.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -73,6 +74,11 @@ for _name, _args in _SIGNATURES.items():
 # ---------------------------------------------------------------------------
 _BOTH, _BF16, _F32 = dict(_CODE), {torch.bfloat16: FSDP_DTYPE_BF16}, {torch.float32: FSDP_DTYPE_F32}
 _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+@functools.lru_cache(maxsize=None)
+def _device(index):
+    return torch.device("cuda", index)
 
 
 def _placed(where, what, t, device):
@@ -153,7 +159,7 @@ def _workspace(where, given, nbytes, handle, device):
         return given.data_ptr(), given.numel(), given
     if nbytes == 0:
         return None, 0, None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=_device(device))
     if handle != _current_stream():  # the allocator may not reuse it before the call's stream is done with it
         ws.record_stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream())
     return ws.data_ptr(), nbytes, ws
@@ -166,7 +172,9 @@ class Act8:
     __slots__ = ("rows", "cols", "data")
 
     def __init__(self, rows, cols, data=None, device="cuda"):
-        nbytes = fsdp_act8_bytes(rows, cols)
+        if rows < 0 or cols < 1:
+            raise ValueError(f"Act8: no checkpoint of {rows} x {cols}")
+        nbytes = rows * (FSDP_ACT8_GROUP + 1) * ((cols + FSDP_ACT8_GROUP - 1) // FSDP_ACT8_GROUP)
         if data is None:
             data = torch.empty(nbytes, dtype=torch.uint8, device=device)
         elif data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() < nbytes:
