@@ -324,7 +324,7 @@ Plan plan_of(const fsdp_ffn_desc_t *d, bool backward) {
   Plan p = {};
   p.sms = device_sms() > 0 ? device_sms() : 160;
   p.d_pitch = up_to(d->d, 8), p.f_pitch = up_to(d->f, 16);
-  if (!backward && d->rows <= kFewRows) return p;  // reads its operands where they are
+  if (!backward && few_rows(d->rows, d->d, d->f)) return p;  // reads its operands where they are
   p.stage_x = d->x_dtype == FSDP_ACT8 || rows_off(d->rows, d->ld_x, d->unaligned & 1);
   p.pad_x = !backward && d->rows < kMapRows;
   p.stage_x = p.stage_x || p.pad_x;
@@ -538,7 +538,7 @@ fsdp_status_t fsdp_gated_ffn_forward(const fsdp_ffn_desc_t *d, const void *x, co
   Call c = {d, plan_of(d, false), static_cast<uint8_t *>(workspace), reinterpret_cast<cudaStream_t>(stream), {}, {}, {}};
   if (workspace_bytes < c.plan.bytes) return fail(FSDP_EINVAL, "workspace_bytes is below fsdp_gated_ffn_workspace");
   if ((st = check_ptr(workspace, c.plan.bytes, 16, "workspace", -1)) != FSDP_OK) return st;
-  if (d->rows > 0 && d->rows <= kFewRows) {
+  if (d->rows > 0 && few_rows(d->rows, d->d, d->f)) {
     RowsArgs a = {};
     a.x = x, a.w_gate = w_gate, a.w_up = w_up, a.h = h;
     a.rows = d->rows, a.d = d->d, a.f = d->f;

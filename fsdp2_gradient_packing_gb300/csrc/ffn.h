@@ -94,6 +94,13 @@ struct RowsArgs {
   int64_t ld_kept;
 };
 constexpr int kFewRows = 4;
+// When dot products beat the tiles, in us for 1 / 2 / 4 rows (the tiles take the same for
+// all): 512 x 1408 2.9 / 3.2 / 4.2 to 6.3; 1024 x 4096 5.5 / 5.9 / 7.4 to 12.6; 2048 x 6144
+// 11 / 12 / 17 to 22; 4096 x 12288 33 / 42 / 48 to 38.  One row always; more up to 128 MB
+// of weights, where the lines through these meet.
+inline bool few_rows(int64_t rows, int64_t d, int64_t f) {
+  return rows == 1 || (rows <= kFewRows && d * f <= int64_t(1) << 25);
+}
 // a.rows in 1 .. kFewRows; `vec`: d is a multiple of 8 and every row of x and the weights
 // starts on a 16-byte boundary.
 cudaError_t launch_rows(const RowsArgs &a, bool vec, cudaStream_t stream);

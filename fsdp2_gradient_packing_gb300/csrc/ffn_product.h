@@ -19,17 +19,18 @@ constexpr int kTmemColumns = kTileN * kAccumulators;
 constexpr int kTurnPitch = 17;
 constexpr int kTurnBytes = 32 * kTurnPitch * 4;
 
-template <int CG>
-struct Shape {
-  static constexpr int kA = kTileM * kTileK * 2;        // bytes of a block's A stage
-  static constexpr int kB = kTileN / CG * kTileK * 2;   // bytes of a block's B stage
-  static constexpr int kStage = kA + kB;
-  static constexpr int kStages = CG == 1 ? 4 : 6;
-  static constexpr int kSmem = kStages * kStage + 1024 + kEpilogueWarps * kTurnBytes;  // stages start on 1,024-byte boundaries
-};
+constexpr int kA = kTileM * kTileK * 2;  // bytes of a block's A in a stage; B follows
+constexpr int kMostStages = 8;
+// Shared memory of the stages: what the rest leaves, with the stages on 1,024-byte boundaries.
+constexpr int kRing = 227 * 1024 - 1024 - kEpilogueWarps * kTurnBytes - 1024;
+
+// Bytes of a block's stage, and how many fit: narrow tiles get more, so that as many bytes
+// are in flight (with four stages for all, 16 rows through 2048 x 6144 took 22 us).
+__host__ __device__ __forceinline__ int stage_bytes(int columns, int cg) { return kA + columns / cg * (kTileK * 2); }
+__host__ __device__ __forceinline__ int stages_of(int bytes) { return min(kRing / bytes, kMostStages); }
 
 struct Shared {
-  uint64_t full[6], empty[6], tmem_full[kAccumulators], tmem_empty[kAccumulators], drain;
+  uint64_t full[kMostStages], empty[kMostStages], tmem_full[kAccumulators], tmem_empty[kAccumulators], drain;
   uint32_t tmem, stop, filled;
 };
 
@@ -105,8 +106,7 @@ struct Loader {
     ax = by = (kb - up * a.half[1]) * kTileK;
   }
   __device__ __forceinline__ void load(const Args &a, uint32_t at, uint32_t bar) const {
-    using S = Shape<CG>;
-    const uint32_t sb = at + S::kA;
+    const uint32_t sb = at + kA;
     if constexpr (MODE != BACKWARD) {
       tc::tma_load<CG>(at, ma, ax, ay, bar);
       tc::tma_load<CG>(sb, mb, bx, by, bar);
@@ -273,15 +273,13 @@ __device__ __forceinline__ bool skips_first(const Args &a, int worker) { return 
 // (again for a limited time) until the copies in flight have landed.  The leader's
 // barriers count both blocks' bytes; what the other block of a pair sent to a stage
 // that the leader never armed is not counted anywhere and gets a fixed time.
-template <int CG>
-__device__ __noinline__ void land_copies(Shared &sh, const Args &a, int rank, bool skipped) {
-  using S = Shape<CG>;
+__device__ __noinline__ void land_copies(Shared &sh, const Args &a, uint32_t stages, int rank, bool skipped) {
   if (rank == 0) {
-    uint32_t f = sh.filled > (uint32_t)S::kStages ? sh.filled - S::kStages : 0;
+    uint32_t f = sh.filled > stages ? sh.filled - stages : 0;
     if (f == 0 && skipped) f = 1;
     for (; f < sh.filled; ++f) {
       uint32_t never = 0;
-      tc::bar_wait(tc::smem(&sh.full[f % S::kStages]), (f / S::kStages) & 1u, a.wait_limit_ns, &never);
+      tc::bar_wait(tc::smem(&sh.full[f % stages]), (f / stages) & 1u, a.wait_limit_ns, &never);
     }
   } else {
     const uint64_t began = tc::now_ns();
@@ -292,9 +290,10 @@ __device__ __noinline__ void land_copies(Shared &sh, const Args &a, int rank, bo
 
 template <int MODE, int CG, int ACT, int KEEP>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Args a) {
-  using S = Shape<CG>;
   extern __shared__ uint8_t dynamic[];
   __shared__ Shared sh;
+  const int columns = MODE == BACKWARD ? kTileN : a.tile_n;
+  const uint32_t stage_size = stage_bytes(columns, CG), stage_count = stages_of((int)stage_size);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const uint32_t stages = (tc::smem(dynamic) + 1023u) & ~1023u;
   const int rank = CG == 1 ? 0 : (int)tc::cluster_rank();
@@ -303,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   volatile uint32_t *stop = &sh.stop;
 
   if (warp == 0 && lane == 0) {
-    for (int s = 0; s < S::kStages; ++s) {
+    for (uint32_t s = 0; s < stage_count; ++s) {
       tc::bar_init(tc::smem(&sh.full[s]), 1);
       tc::bar_init(tc::smem(&sh.empty[s]), 1);
     }
@@ -333,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     // ---- loads ---------------------------------------------------------------
     if (lane == 0) {
       uint32_t stage = 0, phase = 0, filled = 0;
-      const uint32_t bytes = CG * S::kA + (MODE == BACKWARD ? kTileN : a.tile_n) * (kTileK * 2);
+      const uint32_t bytes = CG * stage_size;
       const uint32_t full = tc::smem(&sh.full[0]), empty = tc::smem(&sh.empty[0]);
       const uint32_t leader = CG == 1 ? full : tc::at_rank(full, 0);
       const bool skip = skips_first(a, worker);
@@ -345,18 +344,18 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           if (MODE == BACKWARD && u.which == 1 && kb == a.half[1]) from.go_to(a, kb);
           if (!skip || filled > 0) {
             if (rank == 0) tc::bar_expect(full + stage * 8, bytes);
-            from.load(a, stages + stage * S::kStage, leader + stage * 8);
+            from.load(a, stages + stage * stage_size, leader + stage * 8);
           }
           from.advance();
           ++filled;
-          if (++stage == S::kStages) stage = 0, phase ^= 1u;
+          if (++stage == stage_count) stage = 0, phase ^= 1u;
         }
       }
       // The last products hand their stages back before this block leaves: the other
       // block of a pair must not signal into shared memory that is no longer its own.
-      for (int s = 0; ok && s < S::kStages; ++s) {
+      for (uint32_t s = 0; ok && s < stage_count; ++s) {
         ok = tc::bar_wait(tc::smem(&sh.empty[stage]), phase ^ 1u, a.wait_limit_ns, stop);
-        if (++stage == S::kStages) stage = 0, phase ^= 1u;
+        if (++stage == stage_count) stage = 0, phase ^= 1u;
       }
       sh.filled = filled;
     }
@@ -374,15 +373,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         // Majors by use.  Descriptors advance by 16 K values: 32 bytes within a row, or 16
         // rows of 128 bytes (in units of 16 bytes).
         const bool a_mn = MODE == BACKWARD && u.which == 0, b_mn = MODE == BACKWARD;
-        const uint32_t idesc = tc::instruction(kTileM * CG, MODE == BACKWARD ? kTileN : a.tile_n, a_mn, b_mn);
-        const uint32_t a0 = tc::operand_low(stages, a_mn ? 8192 : 16), b0 = tc::operand_low(stages + S::kA, b_mn ? 8192 : 16);
+        const uint32_t idesc = tc::instruction(kTileM * CG, columns, a_mn, b_mn);
+        const uint32_t a0 = tc::operand_low(stages, a_mn ? 8192 : 16), b0 = tc::operand_low(stages + kA, b_mn ? 8192 : 16);
         const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;
         constexpr uint32_t kHigh = tc::operand_high(1024);
         uint32_t add = 0;
         for (int kb = u.k0; kb < u.k1; ++kb) {
           if (!(ok = tc::bar_wait(full + stage * 8, phase, a.wait_limit_ns, stop))) break;
           tc::fence_after();
-          uint32_t al = a0 + stage * (S::kStage / 16), bl = b0 + stage * (S::kStage / 16);
+          uint32_t al = a0 + stage * (stage_size / 16), bl = b0 + stage * (stage_size / 16);
 #pragma unroll
           for (int k = 0; k < kTileK / 16; ++k) {
             tc::mma<CG>(d, al, kHigh, bl, kHigh, idesc, add);
@@ -390,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           }
           issued = true;
           tc::mma_commit<CG>(empty + stage * 8);
-          if (++stage == S::kStages) stage = 0, phase ^= 1u;
+          if (++stage == stage_count) stage = 0, phase ^= 1u;
         }
         if (!ok) break;
         tc::mma_commit<CG>(tc::smem(&sh.tmem_full[acc]));
@@ -407,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     // ---- epilogue ------------------------------------------------------------
     const int quarter = warp & 3;          // the lanes of TMEM that this warp may read
     const int side = (warp - 2) / 4;       // and its half of the columns
-    float *const turn = reinterpret_cast<float *>(dynamic + (stages - tc::smem(dynamic)) + S::kStages * S::kStage) +
+    float *const turn = reinterpret_cast<float *>(dynamic + (stages - tc::smem(dynamic)) + kRing / 1024 * 1024) +
                         (warp - 2) * (kTurnBytes / 4);
     uint32_t acc = 0, acc_phase = 0;
     for (int i = worker; i < units; i += workers) {
@@ -475,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   __syncthreads();
   if (threadIdx.x == 0 && sh.stop) {
     atomicOr(a.status, kStatusGemm);
-    land_copies<CG>(sh, a, rank, skips_first(a, worker));
+    land_copies(sh, a, stage_count, rank, skips_first(a, worker));
   }
   __syncthreads();
   if constexpr (CG == 2) tc::cluster_sync();
@@ -485,16 +484,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
 template <int MODE, int CG, int ACT, int KEEP>
 cudaError_t launch(Args &a, int sms, cudaStream_t stream) {
-  using S = Shape<CG>;
+  constexpr int kSmem = 1024 + kRing + kEpilogueWarps * kTurnBytes;
   const void *fn = reinterpret_cast<const void *>(&product_kernel<MODE, CG, ACT, KEEP>);
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   int64_t units = 0;
   for (int w = 0; w < (MODE == BACKWARD ? 2 : 1); ++w) units += (int64_t)a.grid[w].m * a.grid[w].n * a.grid[w].splits;
   int64_t workers = sms / CG;
   if (workers > units) workers = units;
   void *args[] = {&a};
-  return launch_kernel(fn, dim3((unsigned)(workers * CG)), dim3(kThreads), args, S::kSmem, stream, true, CG);
+  return launch_kernel(fn, dim3((unsigned)(workers * CG)), dim3(kThreads), args, kSmem, stream, true, CG);
 }
 
 template <int MODE, int CG, int ACT>

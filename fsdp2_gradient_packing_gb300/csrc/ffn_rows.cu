@@ -4,7 +4,7 @@
 // With so few rows every weight is used once or a few times, so the bound is HBM:
 // 4 d f bytes of weights.  A warp reads whole rows of both weights, 512 bytes of
 // each of 8 rows (4 features, gate and up) in flight at a time, which streams better
-// than the tile path's 128-byte pieces of many rows (see kFewRows for both sides).
+// than the tile path's 128-byte pieces of many rows (few_rows() has both sides).
 #include "ffn.h"
 
 namespace fsdp {
