@@ -304,15 +304,9 @@ BackwardTiles backward_tiles(int64_t rows, int64_t d, int64_t f, int sms) {
   return t;
 }
 
-// A TMA map of fewer rows loads slowly: the 4096 x 12288 block takes 39 us with 16
-// rows and 48 to 68 with 5 to 15.  The forward pass then copies x into a map of 16 rows,
-// whose other rows may hold anything (they meet no result).
-constexpr int64_t kMapRows = 16;
-
 struct Plan {
   int sms;
   bool stage_x, stage_wg, stage_wu;
-  bool pad_x;   // x staged as kMapRows rows
   int64_t d_pitch, f_pitch;
   BackwardTiles tiles;
   int64_t at_x, at_wg, at_wu, at_dg, at_du, at_partial[2], bytes;
@@ -326,8 +320,6 @@ Plan plan_of(const fsdp_ffn_desc_t *d, bool backward) {
   p.d_pitch = up_to(d->d, 8), p.f_pitch = up_to(d->f, 16);
   if (!backward && few_rows(d->rows, d->d, d->f)) return p;  // reads its operands where they are
   p.stage_x = d->x_dtype == FSDP_ACT8 || rows_off(d->rows, d->ld_x, d->unaligned & 1);
-  p.pad_x = !backward && d->rows < kMapRows;
-  p.stage_x = p.stage_x || p.pad_x;
   p.stage_wg = rows_off(d->f, d->ld_w_gate, d->unaligned & 2);
   p.stage_wu = rows_off(d->f, d->ld_w_up, d->unaligned & 4);
   int64_t at = 0;
@@ -336,7 +328,7 @@ Plan plan_of(const fsdp_ffn_desc_t *d, bool backward) {
     if (want) at += up_to(bytes, 256);
     return here;
   };
-  p.at_x = take(p.stage_x, (p.pad_x ? kMapRows : d->rows) * p.d_pitch * 2);
+  p.at_x = take(p.stage_x, d->rows * p.d_pitch * 2);
   p.at_wg = take(p.stage_wg, d->f * p.d_pitch * 2);
   p.at_wu = take(p.stage_wu, d->f * p.d_pitch * 2);
   if (backward && d->rows > 0) {
@@ -422,7 +414,6 @@ struct Call {
       a.src[i] = static_cast<const uint16_t *>(o.p), a.dst[i] = reinterpret_cast<uint16_t *>(ws + at);
       a.ld[i] = o.ld, a.rows[i] = o.rows;
       o.p = a.dst[i], o.ld = plan.d_pitch;
-      if (i == 2 && plan.pad_x) o.rows = kMapRows;
     };
     copy(wg, plan.stage_wg, plan.at_wg, 0);
     copy(wu, plan.stage_wu, plan.at_wu, 1);
@@ -466,7 +457,11 @@ struct Call {
   // FORWARD or RECOMPUTE.
   fsdp_status_t gated(Mode mode, Args &a) {
     const GatedTiles t = gated_tiles(d->rows, d->f, d->d, plan.sms);
-    if (!operands(a, {x, x}, kTileM, {wg, wu, wu}, t.tile_n / 2))
+    // Boxes of x no higher than x: rows that a box has to fill with zeros are slow (5 to 15
+    // rows through 4096 x 12288 took 48 to 68 us with boxes of 128, 35 with these).  What the
+    // rest of a stage holds meets only rows that are not stored.
+    a.a_rows = (int32_t)(d->rows < kTileM ? up_to(d->rows, 8) : kTileM);
+    if (!operands(a, {x, x}, a.a_rows, {wg, wu, wu}, t.tile_n / 2))
       return fail(FSDP_ECUDA, "cuTensorMapEncodeTiled failed or is missing");
     a.grid[0] = t.grid;
     a.tile_n = t.tile_n;

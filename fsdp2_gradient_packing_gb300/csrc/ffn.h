@@ -47,6 +47,7 @@ struct Args {
   int32_t fault;
   int32_t act;        // Act
   Grid grid[2];       // BACKWARD: weight gradients, dx; else the first only
+  int32_t a_rows;     // FORWARD, RECOMPUTE: rows of an x box (see gated())
   int32_t tile_n;     // accumulator columns of a tile (FORWARD, RECOMPUTE: half of them gate)
   int32_t half[2];    // BACKWARD: the row tile / the K block from which on the up half is meant
   int64_t m[2], n;    // rows and columns of the outputs (FORWARD, RECOMPUTE: n = f)
@@ -95,11 +96,11 @@ struct RowsArgs {
 };
 constexpr int kFewRows = 4;
 // When dot products beat the tiles, in us for 1 / 2 / 4 rows (the tiles take the same for
-// all): 512 x 1408 2.9 / 3.2 / 4.2 to 6.3; 1024 x 4096 5.5 / 5.9 / 7.4 to 12.6; 2048 x 6144
-// 11 / 12 / 17 to 22; 4096 x 12288 33 / 42 / 48 to 38.  One row always; more up to 128 MB
-// of weights, where the lines through these meet.
+// all): 512 x 1408 2.9 / 3.2 / 4.2 to 5.0; 1024 x 4096 5.5 / 5.9 / 7.4 to 7.4; 2048 x 6144
+// 11 / 12 / 17 to 13; 4096 x 12288 33 / 42 / 48 to 35.  One row always; more as long as
+// rows x weights stay small, with the border where those meet.
 inline bool few_rows(int64_t rows, int64_t d, int64_t f) {
-  return rows == 1 || (rows <= kFewRows && d * f <= int64_t(1) << 25);
+  return rows == 1 || (rows <= kFewRows && rows * d * f <= int64_t(3) << 23);
 }
 // a.rows in 1 .. kFewRows; `vec`: d is a multiple of 8 and every row of x and the weights
 // starts on a 16-byte boundary.

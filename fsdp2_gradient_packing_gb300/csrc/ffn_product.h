@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     // ---- loads ---------------------------------------------------------------
     if (lane == 0) {
       uint32_t stage = 0, phase = 0, filled = 0;
-      const uint32_t bytes = CG * stage_size;
+      const uint32_t bytes = CG * stage_size - (MODE == BACKWARD ? 0 : (kTileM - a.a_rows) * (kTileK * 2));
       const uint32_t full = tc::smem(&sh.full[0]), empty = tc::smem(&sh.empty[0]);
       const uint32_t leader = CG == 1 ? full : tc::at_rank(full, 0);
       const bool skip = skips_first(a, worker);
