@@ -45,6 +45,7 @@ struct Args {
   int32_t stages, stage_bytes;
   uint32_t *status;
   uint64_t wait_limit_ns;
+  int32_t fault;             // test hook: block 0 leaves its first stage empty
   const void *weight, *bias;
   float *mean, *rstd;        // written forward, read backward
   // forward
@@ -195,6 +196,7 @@ __device__ __forceinline__ void load_rows(const Args &a, Shared &sh, uint8_t *me
     bytes[i] = s.elem ? width * s.elem : (width + (int)kActGroup - 1) / (int)kActGroup;
   }
   const uint32_t ring = tc::smem(memory) + (uint32_t)lane * a.stages * a.stage_bytes;
+  bool skip = a.fault != 0 && blockIdx.x == 0 && lane == 0;
   int stage = 0;
   uint32_t parity = 1;
   for (; row < a.rows; row += step) {
@@ -206,16 +208,17 @@ __device__ __forceinline__ void load_rows(const Args &a, Shared &sh, uint8_t *me
       n[i] = a.in[i].at < 0 ? 0u : (((uint32_t)from[i] & 15u) + bytes[i] + 15u) & ~15u;
       total += n[i];
     }
-    tc::bar_expect(full, total);
+    if (!skip) tc::bar_expect(full, total);
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-      if (n[i])
+      if (n[i] && !skip)
         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                          to + a.in[i].at),
                      "l"(from[i] & ~(uintptr_t)15), "r"(n[i]), "r"(full)
                      : "memory");
       from[i] += step * a.in[i].pitch;
     }
+    skip = false;
     if (++stage == a.stages) stage = 0, parity ^= 1u;
   }
 }
@@ -445,6 +448,7 @@ inline fsdp_status_t run(const void *fn, Args &a, const Launch &l, const Shape &
   cudaError_t e = status_word(&a.status);
   if (e != cudaSuccess) return fail(FSDP_ECUDA, std::string("status word: ") + cudaGetErrorString(e));
   a.wait_limit_ns = wait_limit_ns();
+  a.fault = wait_fault();
   if (l.smem > 32 * 1024) {
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, l.smem);
     if (e != cudaSuccess) return fail(FSDP_ECUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));

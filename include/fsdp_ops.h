@@ -33,7 +33,8 @@
  *     parameters (sums over no rows) are written as 0.
  *   - NaN and infinities propagate as the formulas say.
  *   - Every wait inside the kernels is bounded; fsdp_ops_sync_status tells
- *     whether one gave up.
+ *     whether one gave up.  fsdp_debug_set_wait_fault (the limit and the test
+ *     hook) holds for these kernels' pipelines too.
  */
 #ifndef FSDP_OPS_H
 #define FSDP_OPS_H
