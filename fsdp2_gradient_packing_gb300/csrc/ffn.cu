@@ -155,9 +155,10 @@ __global__ void __launch_bounds__(kThreads) slope_kernel(const __grid_constant__
       values(uv, u[q]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 p = act_of<true>(gv[e].x, ACT), r = act_of<true>(gv[e].y, ACT);
-        gv[e] = __fmul2_rn(__fmul2_rn(dv[e], uv[e]), make_float2(p.y, r.y));
-        uv[e] = __fmul2_rn(dv[e], make_float2(p.x, r.x));
+        float2 act, slope;
+        act_of<true, ACT>(gv[e], act, slope);
+        gv[e] = __fmul2_rn(__fmul2_rn(dv[e], uv[e]), slope);
+        uv[e] = __fmul2_rn(dv[e], act);
       }
       // The pitch holds whole vectors; what lies past the row's end is never read.
       store8(a.dg, row[q] * a.pitch + col[q], true, gv);

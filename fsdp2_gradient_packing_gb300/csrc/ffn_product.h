@@ -236,8 +236,9 @@ __device__ __forceinline__ void gated_part(const Args &a, const uint32_t (&gr)[3
   if constexpr (MODE == FORWARD) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float2 g = pair_at(gr, i);
-      x[i] = __fmul2_rn(make_float2(act_of<false>(g.x, ACT).x, act_of<false>(g.y, ACT).x), pair_at(ur, i));
+      float2 y_i, none;
+      act_of<false, ACT>(pair_at(gr, i), y_i, none);
+      x[i] = __fmul2_rn(y_i, pair_at(ur, i));
     }
     store_part(a.out[0], a.ld_out[0], true, a.out_width[0], x, q);
     if constexpr (KEEP != 0) {
@@ -257,9 +258,10 @@ __device__ __forceinline__ void gated_part(const Args &a, const uint32_t (&gr)[3
     load_part(static_cast<const __nv_bfloat16 *>(a.dh), a.ld_dh, a.dh_vec != 0, d, q);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float2 g = pair_at(gr, i), p = act_of<true>(g.x, ACT), r = act_of<true>(g.y, ACT);
-      x[i] = __fmul2_rn(__fmul2_rn(d[i], pair_at(ur, i)), make_float2(p.y, r.y));
-      y[i] = __fmul2_rn(d[i], make_float2(p.x, r.x));
+      float2 act, slope;
+      act_of<true, ACT>(pair_at(gr, i), act, slope);
+      x[i] = __fmul2_rn(__fmul2_rn(d[i], pair_at(ur, i)), slope);
+      y[i] = __fmul2_rn(d[i], act);
     }
     store_part(a.out[0], a.ld_out[0], true, a.out_width[0], x, q);
     store_part(a.out[1], a.ld_out[1], true, a.out_width[0], y, q);

@@ -86,7 +86,12 @@ __global__ void __launch_bounds__(kThreads, ROWS == 1 ? 3 : 2) rows_kernel(const
   const bool in = col < a.f;
   for (int t = warp; t < a.rows; t += kWarps) {
     const float g = in ? gate[t][lane] : 0.0f, u = in ? up[t][lane] : 0.0f;
-    if (in) store_any(a.h, t * a.ld_h + col, true, act_of<false>(g, a.act).x * u);
+    float2 y, none;
+    if (a.act == SILU)
+      act_of<false, SILU>(both(g), y, none);
+    else
+      act_of<false, GELU>(both(g), y, none);
+    if (in) store_any(a.h, t * a.ld_h + col, true, y.x * u);
     if (a.keep == 1) {
       const int64_t group = t * a.groups + blockIdx.x;
 #pragma unroll

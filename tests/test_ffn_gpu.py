@@ -328,3 +328,27 @@ def test_refusals():
     st = fp._lib.fsdp_gated_ffn_forward(ctypes.byref(d), x.data_ptr() + 2, w.data_ptr(), w.data_ptr(), h.data_ptr(), None, None,
                                         None, 0, None)
     assert st == fp.FSDP_EINVAL and "unaligned" in fp.fsdp_last_error()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("rows", [1, 300])
+def test_activation_over_its_range(act, rows):
+    """g from -20 to 20 through unit weights (x and the identity), u = 1: h is act(g) to its own arithmetic and half an ulp,
+    deep in the tail too; gradients of g likewise."""
+    fp = fp_module()
+    d = 64
+    g = torch.linspace(-20, 20, rows * d).view(rows, d).to(BF16)
+    x = torch.zeros(rows, d + 8, dtype=BF16)
+    x[:, :d], x[:, d] = g, 1
+    wg, wu = torch.zeros(d, d + 8, dtype=BF16), torch.zeros(d, d + 8, dtype=BF16)
+    wg[:, :d], wu[:, d] = torch.eye(d), 1
+    x, wg, wu = x.cuda(), wg.cuda(), wu.cuda()
+    h, dh = torch.empty(rows, d, dtype=BF16, device="cuda"), torch.ones(rows, d, dtype=BF16, device="cuda")
+    fp.fsdp_gated_ffn_forward(x, wg, wu, h, activation=ACTS[act])
+    a, s = act_and_slope(g.double(), act)
+    # The exponent's rounding grows with its argument, g or g^2 / 2: 2^-23 of it.
+    fast = FAST + (g.double().abs() if act == "silu" else g.double().square() / 2) * 2.0 ** -23
+    close(h, a, a.abs() * (fast + HALF[BF16]) + 1e-37, "h")
+    dx = torch.empty(rows, d + 8, device="cuda")
+    fp.fsdp_gated_ffn_backward(dh, x, wg, wu, dx, activation=ACTS[act])
+    close(dx[:, :d], s, (1 + g.double().abs()) * fast + s.abs() * HALF[BF16] + 1e-37, "dx")
