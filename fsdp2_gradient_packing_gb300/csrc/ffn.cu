@@ -178,43 +178,41 @@ struct JoinArgs {
   int32_t splits, bf16, vec;
 };
 
-// Bound: L2, where the parts still are.  VEC columns to a thread, one row to a block
-// at a time.
+// Bound: L2, where the parts still are.  VEC columns of a row to a thread.
 template <int VEC>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ JoinArgs a) {
-  const int64_t total = a.rows * a.cols;
+  const int64_t part = a.rows * a.cols, per_row = a.cols / VEC, total = a.rows * per_row;
   wait_for_previous();
   let_next_start();
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    const bool second = r >= a.half;
-    const int64_t row = second ? r - a.half : r;
-    for (int64_t col = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * VEC; col < a.cols; col += (int64_t)gridDim.y * kThreads * VEC) {
-      const float *p = a.partial + r * a.cols + col;
-      float s[VEC];
-      if constexpr (VEC == 4) {
-        float4 v = *reinterpret_cast<const float4 *>(p);
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+    int64_t row = (uint64_t)total >> 32 == 0 ? (uint32_t)i / (uint32_t)per_row : i / per_row;
+    const int64_t col = (i - row * per_row) * VEC;
+    const float *p = a.partial + i * VEC;
+    const bool second = row >= a.half;
+    if (second) row -= a.half;
+    const int64_t at = row * a.ld[second] + col;
+    if constexpr (VEC == 4) {
+      float4 v = *reinterpret_cast<const float4 *>(p);
 #pragma unroll 4
-        for (int k = 1; k < a.splits; ++k) {
-          const float4 q = *reinterpret_cast<const float4 *>(p + k * total);
-          v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
-        }
-        s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
-        if (a.vec) {
-          const int64_t at = row * a.ld[second] + col;
-          if (a.bf16)
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out[second]) + at) =
-                make_uint2(bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3]));
-          else
-            *reinterpret_cast<float4 *>(static_cast<float *>(a.out[second]) + at) = v;
-          continue;
-        }
-      } else {
-        s[0] = p[0];
-#pragma unroll 4
-        for (int k = 1; k < a.splits; ++k) s[0] += p[k * total];
+      for (int k = 1; k < a.splits; ++k) {
+        const float4 q = *reinterpret_cast<const float4 *>(p + k * part);
+        v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
       }
+      if (!a.vec) {
+        const float s[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) store_any(a.out[second], row * a.ld[second] + col + e, a.bf16 != 0, s[e]);
+        for (int e = 0; e < 4; ++e) store_any(a.out[second], at + e, a.bf16 != 0, s[e]);
+      } else if (a.bf16) {
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out[second]) + at) =
+            make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
+      } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out[second]) + at) = v;
+      }
+    } else {
+      float s = p[0];
+#pragma unroll 4
+      for (int k = 1; k < a.splits; ++k) s += p[k * part];
+      store_any(a.out[second], at, a.bf16 != 0, s);
     }
   }
 }
@@ -481,12 +479,11 @@ struct Call {
     j.vec = a.out_width[w] >= 16;
     void *args[] = {&j};
     const int vec = a.n % 4 == 0 ? 4 : 1;
-    int64_t across = blocks_of(a.n, (int64_t)kThreads * vec), down = j.rows;
-    if (across > 64) across = 64;
-    if (down > plan.sms * 64) down = plan.sms * 64;
+    int64_t grid = blocks_of(j.rows * (a.n / vec), kThreads);
+    if (grid > plan.sms * 64) grid = plan.sms * 64;
     return launched(launch_kernel(vec == 4 ? reinterpret_cast<const void *>(&join_kernel<4>)
                                            : reinterpret_cast<const void *>(&join_kernel<1>),
-                                  dim3((unsigned)down, (unsigned)across), dim3(kThreads), args, 0, stream, true));
+                                  dim3((unsigned)grid), dim3(kThreads), args, 0, stream, true));
   }
 };
 
