@@ -250,56 +250,63 @@ GatedTiles gated_tiles(int64_t rows, int64_t f, int64_t d, int sms) {
   return t;
 }
 
-// The backward products: tiles of 256 columns.  K loops are split where that
-// shortens the longest worker's share, counted in K blocks (a K block of a pair takes
-// about 0.27 us): a unit costs its K blocks (an epilogue's 10 at least), and joining
-// parts a launch (15) and the parts' bytes, written and read, at about 1.2 MB a block.
-// A call that wants only some of the gradients splits as if it wanted all.
+// The backward products: tiles of 256 columns, or fewer where those would be mostly
+// empty.  K loops are split where that shortens the longest worker's share.  Costs are
+// in hundredths of a K block of a full tile (which takes a pair about 0.33 us): a
+// narrower tile's K block costs less, though not in proportion, for A is the same; a
+// unit its K blocks, but an epilogue at least; joining parts a launch and the parts'
+// bytes, written and read, at about 1.3 MB a K block.  A call that wants only some of
+// the gradients splits as if it wanted all.
 struct BackwardTiles {
   bool pair;
+  int32_t tile_n;
   Grid grid[2];       // weight gradients, dx
   int64_t half[2];    // tiles of one weight's rows; K blocks of one half of dx
 };
 BackwardTiles backward_tiles(int64_t rows, int64_t d, int64_t f, int sms) {
   BackwardTiles t = {};
   t.pair = pairs(rows);
-  const int64_t tile_m = tile_rows(t.pair), n = blocks_of(d, 256), workers = t.pair ? sms / 2 : sms;
+  const int64_t tile_m = tile_rows(t.pair), workers = t.pair ? sms / 2 : sms;
   t.half[0] = blocks_of(f, tile_m), t.half[1] = blocks_of(f, kTileK);
-  const int64_t tiles[2] = {2 * t.half[0] * n, blocks_of(rows, tile_m) * n};
+  const int64_t m[2] = {2 * t.half[0], blocks_of(rows, tile_m)};
   const int64_t k[2] = {blocks_of(rows, kTileK), 2 * t.half[1]};
   const int64_t bytes[2] = {2 * f * d * 4, rows * d * 4};  // of one part
   constexpr int kChoices = 8;
   const int64_t by[kChoices] = {1, 2, 3, 4, 6, 8, 12, 16};
-  // Cost of a unit, units, and cost of the join for each choice.
-  int64_t cost[2][kChoices], units[2][kChoices], join[2][kChoices];
-  for (int w = 0; w < 2; ++w)
-    for (int c = 0; c < kChoices; ++c) {
-      const int64_t per = blocks_of(k[w], by[c]);
-      cost[w][c] = (per > 10 ? per : 10) + 1;
-      units[w][c] = tiles[w] * by[c];
-      join[w][c] = c == 0 ? 0 : 15 + 2 * by[c] * bytes[w] / 1200000;
-      if (c > 0 && (per < 4 || blocks_of(k[w], per) != by[c])) units[w][c] = 0;  // parts too short, or empty ones
-    }
-  const int choices = tiles[0] + tiles[1] > 8 * workers ? 1 : kChoices;
   int64_t best = INT64_MAX;
-  int parts[2] = {0, 0};
-  for (int p = 0; p < choices; ++p)
-    for (int q = 0; q < choices; ++q) {
-      const int64_t u0 = units[0][p], u = u0 + units[1][q];
-      if (u0 == 0 || u == u0) continue;
-      // Worker i takes units i, i + workers, ...: shares change at three workers only.
-      const int64_t at[3] = {0, u0 % workers, u % workers};
-      int64_t longest = 0;
-      for (int64_t i : at) {
-        const int64_t first = (u0 - i + workers - 1) / workers, all = (u - i + workers - 1) / workers;
-        const int64_t share = first * cost[0][p] + (all - first) * cost[1][q];
-        longest = share > longest ? share : longest;
+  for (int64_t width = 256; width >= (t.pair ? 128 : 64); width /= 2) {
+    const int64_t n = blocks_of(d, width), block = width == 256 ? 100 : width == 128 ? 65 : 50;
+    const int choices = (m[0] + m[1]) * n > 8 * workers ? 1 : kChoices;
+    // Cost of a unit, units, and cost of the join for each choice.
+    int64_t cost[2][kChoices], units[2][kChoices], join[2][kChoices];
+    for (int w = 0; w < 2; ++w)
+      for (int c = 0; c < choices; ++c) {
+        const int64_t per = blocks_of(k[w], by[c]);
+        cost[w][c] = (per > 10 ? per : 10) * block + 100;
+        units[w][c] = m[w] * n * by[c];
+        join[w][c] = c == 0 ? 0 : 1500 + by[c] * bytes[w] / 6500;
+        if (c > 0 && (per < 4 || blocks_of(k[w], per) != by[c])) units[w][c] = 0;  // parts too short, or empty ones
       }
-      const int64_t total = longest + join[0][p] + join[1][q];
-      if (total < best) best = total, parts[0] = p, parts[1] = q;
-    }
-  t.grid[0] = {(int32_t)(2 * t.half[0]), (int32_t)n, (int32_t)by[parts[0]], band(tile_m), (int32_t)k[0]};
-  t.grid[1] = {(int32_t)blocks_of(rows, tile_m), (int32_t)n, (int32_t)by[parts[1]], band(tile_m), (int32_t)k[1]};
+    for (int p = 0; p < choices; ++p)
+      for (int q = 0; q < choices; ++q) {
+        const int64_t u0 = units[0][p], u = u0 + units[1][q];
+        if (u0 == 0 || u == u0) continue;
+        // Worker i takes units i, i + workers, ...: shares change at three workers only.
+        const int64_t at[3] = {0, u0 % workers, u % workers};
+        int64_t longest = 0;
+        for (int64_t i : at) {
+          const int64_t first = (u0 - i + workers - 1) / workers, all = (u - i + workers - 1) / workers;
+          const int64_t share = first * cost[0][p] + (all - first) * cost[1][q];
+          longest = share > longest ? share : longest;
+        }
+        const int64_t total = longest + join[0][p] + join[1][q];
+        if (total >= best) continue;
+        best = total;
+        t.tile_n = (int32_t)width;
+        t.grid[0] = {(int32_t)m[0], (int32_t)n, (int32_t)by[p], band(tile_m), (int32_t)k[0]};
+        t.grid[1] = {(int32_t)m[1], (int32_t)n, (int32_t)by[q], band(tile_m), (int32_t)k[1]};
+      }
+  }
   return t;
 }
 
@@ -629,6 +636,7 @@ fsdp_status_t fsdp_gated_ffn_backward(const fsdp_ffn_desc_t *d, const void *dh, 
   if (!c.operands(a, {og, ou}, 64, {c.wg, c.wu, c.x}, 64))
     return fail(FSDP_ECUDA, "cuTensorMapEncodeTiled failed or is missing");
   const BackwardTiles &t = c.plan.tiles;
+  a.tile_n = t.tile_n;
   a.out[0] = dw_gate, a.out[1] = dw_up, a.out[2] = dx;
   a.ld_out[0] = d->ld_dw_gate, a.ld_out[1] = d->ld_dw_up, a.ld_out[2] = d->ld_dx;
   a.m[0] = d->f, a.m[1] = d->rows, a.n = d->d;

@@ -48,7 +48,8 @@ struct Args {
   int32_t act;        // Act
   Grid grid[2];       // BACKWARD: weight gradients, dx; else the first only
   int32_t a_rows;     // FORWARD, RECOMPUTE: rows of an x box (see gated())
-  int32_t tile_n;     // accumulator columns of a tile (FORWARD, RECOMPUTE: half of them gate)
+  int32_t tile_n;     // accumulator columns of a tile (FORWARD, RECOMPUTE: half of them gate;
+                      // BACKWARD: a multiple of 64 a block)
   int32_t half[2];    // BACKWARD: the row tile / the K block from which on the up half is meant
   int64_t m[2], n;    // rows and columns of the outputs (FORWARD, RECOMPUTE: n = f)
   // Outputs, [m, n] with row distance ld.

@@ -85,7 +85,7 @@ struct Loader {
     } else {
       // Boxes of 64 x 64 throughout.  Along K in a row (A of dx): two boxes of 64 rows lie
       // one after the other; along M or N in a row: one box to 64 of them.
-      bx = u.n * kTileN + rank * (kTileN / CG);
+      bx = u.n * a.tile_n + rank * (a.tile_n / CG);
       if (u.which == 1) {
         go_to(a, u.k0);
         ay = (u.m * CG + rank) * kTileM;
@@ -114,8 +114,7 @@ struct Loader {
     } else {
 #pragma unroll
       for (int c = 0; c < kTileM / 64; ++c) tc::tma_load<CG>(at + c * 8192, ma, ax + c * acx, ay + c * acy, bar);
-#pragma unroll
-      for (int c = 0; c < kTileN / CG / 64; ++c) tc::tma_load<CG>(sb + c * 8192, mb, bx + c * 64, by, bar);
+      for (int c = 0; c < a.tile_n / CG / 64; ++c) tc::tma_load<CG>(sb + c * 8192, mb, bx + c * 64, by, bar);
     }
   }
   __device__ __forceinline__ void advance() {
@@ -294,7 +293,7 @@ template <int MODE, int CG, int ACT, int KEEP>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Args a) {
   extern __shared__ uint8_t dynamic[];
   __shared__ Shared sh;
-  const int columns = MODE == BACKWARD ? kTileN : a.tile_n;
+  const int columns = a.tile_n;
   const uint32_t stage_size = stage_bytes(columns, CG), stage_count = stages_of((int)stage_size);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const uint32_t stages = (tc::smem(dynamic) + 1023u) & ~1023u;
@@ -446,13 +445,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const int which = u.which, up = which == 0 && u.m >= a.half[0] ? 1 : 0, to = which == 1 ? 2 : up;
         const int64_t row = ((int64_t)(u.m - up * a.half[0]) * CG + rank) * kTileM + quarter * 32 + lane, m = a.m[which];
 #pragma unroll 1
-        for (int c = side * (kTileN / 2); c < (side + 1) * (kTileN / 2); c += 32) {
-          const int64_t col = (int64_t)u.n * kTileN + c;
+        for (int c = side * (a.tile_n / 2); c < (side + 1) * (a.tile_n / 2); c += 32) {
+          const int64_t col = (int64_t)u.n * a.tile_n + c;
           uint32_t r[32];
           __syncwarp();
           tc::tmem_load32(from + c, r);
           tc::tmem_load_wait();
-          if (c + 32 == (side + 1) * (kTileN / 2)) drained();
+          if (c + 32 == (side + 1) * (a.tile_n / 2)) drained();
           const int64_t rows = m - (row - lane);
           if (rows > 0 && col < a.n) {
             const Part q = {col, (int)min((int64_t)32, a.n - col), (int)min((int64_t)32, rows), row, turn};

@@ -376,23 +376,26 @@ struct Launch {
 
 constexpr int kSmemBudget = 208 * 1024;
 
-inline int groups_of(int64_t rows, const Shape &s, int sms, int most_threads) {
+// `rows_each`: so many rows a group may stay with one unit (0: spread over the SMs at once).
+inline int groups_of(int64_t rows, const Shape &s, int sms, int most_threads, int rows_each) {
   if (s.cluster > 1) return 1;
-  const int64_t want = (rows + sms - 1) / sms, most = most_threads / s.group;
+  const int64_t most = most_threads / s.group;
+  const int64_t want = rows <= most * rows_each ? rows : (rows + sms - 1) / sms;
   return (int)(want < 1 ? 1 : want < most ? want : most);
 }
-inline int64_t units_of(int64_t rows, const Shape &s, int sms, int most_threads) {
-  const int g = groups_of(rows, s, sms, most_threads);
+inline int64_t units_of(int64_t rows, const Shape &s, int sms, int most_threads, int rows_each) {
+  const int g = groups_of(rows, s, sms, most_threads, rows_each);
+  if (rows <= (int64_t)g * rows_each) return 1;
   const int64_t need = (rows + g - 1) / g, most = sms / s.cluster > 0 ? sms / s.cluster : 1;
   return need < most ? need : most;
 }
 
 // Lays out the ring and the rest of shared memory: `params` vectors, then the stages,
 // or after them `sums` vectors of each group but one (column sums) in the same place.
-inline Launch plan_launch(Args &a, const Shape &s, int sms, int most_threads, int params, int sums) {
+inline Launch plan_launch(Args &a, const Shape &s, int sms, int most_threads, int rows_each, int params, int sums) {
   Launch l;
-  l.groups = groups_of(a.rows, s, sms, most_threads);
-  l.units = units_of(a.rows, s, sms, most_threads);
+  l.groups = groups_of(a.rows, s, sms, most_threads, rows_each);
+  l.units = units_of(a.rows, s, sms, most_threads, rows_each);
   const int width = s.group * s.chunks * 8;
   const int cols = a.cols < width ? (int)a.cols : width;
   int at = 0;

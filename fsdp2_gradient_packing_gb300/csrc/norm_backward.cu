@@ -16,6 +16,9 @@ using namespace norm;
 // take 32, its values of a row 32 more.  (A third group at 72 registers spills: 111 us
 // instead of 63 at 16384 x 4096 in BF16 from the checkpoint.)
 constexpr int kMostThreads = 512;
+// Up to so many rows a group, one block does them all: its sums are the gradients, and
+// neither the second kernel (3 us and as much on the host) nor a workspace is needed.
+constexpr int kRowsEach = 4;
 
 template <int XK, bool YB, bool VEC, int G, int K, bool CLUSTER>
 __global__ void __launch_bounds__(kMostThreads + 32, 1) backward_kernel(const __grid_constant__ Args a) {
@@ -210,7 +213,8 @@ const void *kernel_for(int index, bool vec, int kind, bool y_bf16) {
 
 int64_t workspace_bytes_for(const fsdp_norm_desc_t *d) {
   const int sms = device_sms() > 0 ? device_sms() : 256;
-  return units_of(d->rows, shape_of(d->cols), sms, kMostThreads) * 2 * d->cols * 4;
+  const int64_t units = units_of(d->rows, shape_of(d->cols), sms, kMostThreads, kRowsEach);
+  return units > 1 ? units * 2 * d->cols * 4 : 0;
 }
 
 }  // namespace
@@ -282,7 +286,7 @@ fsdp_status_t fsdp_layer_norm_backward(const fsdp_norm_desc_t *d, const void *dy
                    aligned16(weight);
   const Shape sh = shape_of(d->cols);
   const int sms = device_sms();
-  const Launch l = plan_launch(a, sh, sms > 0 ? sms : 1, kMostThreads, 1, 2);
+  const Launch l = plan_launch(a, sh, sms > 0 ? sms : 1, kMostThreads, kRowsEach, 1, 2);
   a.partial = l.units > 1 ? static_cast<float *>(workspace) : nullptr;
   if ((st = run(kernel_for(sh.index, vec, a.x_kind, a.y_bf16 != 0), a, l, sh, s)) != FSDP_OK) return st;
   if (a.partial && (dweight || dbias)) {

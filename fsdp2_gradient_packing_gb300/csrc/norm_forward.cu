@@ -210,7 +210,7 @@ extern "C" fsdp_status_t fsdp_layer_norm_forward(const fsdp_norm_desc_t *d, cons
                    rows_aligned(y, d->rows, d->ld_y, ysize) && aligned16(weight) && aligned16(bias);
   const Shape s = shape_of(d->cols);
   const int sms = device_sms();
-  const Launch l = plan_launch(a, s, sms > 0 ? sms : 1, kMostThreads, 2, 0);
+  const Launch l = plan_launch(a, s, sms > 0 ? sms : 1, kMostThreads, 0, 2, 0);
   if ((st = run(kernel_for(s.index, vec, a.x_kind, a.y_bf16 != 0), a, l, s, reinterpret_cast<cudaStream_t>(stream))) != FSDP_OK)
     return st;
   clear_error();

@@ -81,14 +81,11 @@ def _device(index):
     return torch.device("cuda", index)
 
 
-def _placed(where, what, t, device):
-    index = t.get_device()
-    if index != device:
-        if index < 0:
-            raise ValueError(f"{where}: {what} is not a CUDA tensor")
-        if device is not None:
-            raise ValueError(f"{where}: {what} is on cuda:{index}, another argument on cuda:{device}")
-    return index
+def _misplaced(where, what, index, device):
+    if index < 0:
+        raise ValueError(f"{where}: {what} is not a CUDA tensor")
+    if device is not None:
+        raise ValueError(f"{where}: {what} is on cuda:{index}, another argument on cuda:{device}")
 
 
 def _matrix(where, what, t, rows, cols, codes, device):
@@ -105,15 +102,18 @@ def _matrix(where, what, t, rows, cols, codes, device):
         raise ValueError(f"{where}: {what} is {t.dtype}, not one of {', '.join(map(str, codes))}") from None
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{where}: {what} is {r} x {c}, not {r if rows is None else rows} x {c if cols is None else cols}")
-    if c < 1:
-        raise ValueError(f"{where}: {what} has no columns")
     if s1 != 1 and c > 1:
         raise ValueError(f"{where}: {what} has column stride {s1}, not 1")
-    if r <= 1:
+    if r <= 1 or s0 < c or c < 1:
+        if c < 1:
+            raise ValueError(f"{where}: {what} has no columns")
+        if r > 1:
+            raise ValueError(f"{where}: {what} has rows {s0} elements apart, fewer than its {c} columns")
         s0 = c
-    elif s0 < c:
-        raise ValueError(f"{where}: {what} has rows {s0} elements apart, fewer than its {c} columns")
-    return t.data_ptr(), s0, code, _placed(where, what, t, device)
+    index = t.get_device()
+    if index != device:
+        _misplaced(where, what, index, device)
+    return t.data_ptr(), s0, code, index
 
 
 def _vector(where, what, t, n, codes, device):
@@ -127,7 +127,10 @@ def _vector(where, what, t, n, codes, device):
     code = codes.get(t.dtype)
     if code is None:
         raise ValueError(f"{where}: {what} is {t.dtype}, not one of {', '.join(map(str, codes))}")
-    return t.data_ptr(), code, _placed(where, what, t, device)
+    index = t.get_device()
+    if index != device:
+        _misplaced(where, what, index, device)
+    return t.data_ptr(), code, index
 
 
 def _ckpt(where, what, a, rows, cols, device):
@@ -136,7 +139,10 @@ def _ckpt(where, what, a, rows, cols, device):
         raise ValueError(f"{where}: {what} is not an Act8 checkpoint")
     if a.rows != rows or a.cols != cols:
         raise ValueError(f"{where}: {what} is a checkpoint of {a.rows} x {a.cols}, not of {rows} x {cols}")
-    return a.data.data_ptr(), _placed(where, what, a.data, device)
+    index = a.data.get_device()
+    if index != device:
+        _misplaced(where, what, index, device)
+    return a.data.data_ptr(), index
 
 
 def _handle(where, stream, device):
@@ -153,7 +159,8 @@ def _workspace(where, given, nbytes, handle, device):
     if given is not None:
         if given.dtype != torch.uint8 or not given.is_contiguous():
             raise ValueError(f"{where}: workspace is not a contiguous uint8 tensor")
-        _placed(where, "workspace", given, device)
+        if given.get_device() != device:
+            _misplaced(where, "workspace", given.get_device(), device)
         if given.numel() < nbytes:
             raise ValueError(f"{where}: workspace holds {given.numel()} bytes, the call needs {nbytes}")
         return given.data_ptr(), given.numel(), given
@@ -258,11 +265,14 @@ def fsdp_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, d
         raise ValueError(f"{where}: dweight and dbias have different dtypes")
     d = fsdp_norm_desc_t(rows, cols, ld_x, ld_y, ld_d, dt_x, dt_y, dt_d, FSDP_DTYPE_F32 if dt_w is None else dt_w, dt_dw, 0.0)
     handle = _handle(where, stream, dev)
-    pws, nws, _owner = _workspace(where, workspace, _norm_workspace(d), handle, dev)
+    pws, nws, _owner = _workspace(where, workspace, _norm_workspace(rows, cols, dev), handle, dev)
     _check(_lib.fsdp_layer_norm_backward(ctypes.byref(d), py, px, pw, pm, pr, pd, pdw, pdb, pws, nws, handle), where)
 
 
-def _norm_workspace(d) -> int:
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace(rows, cols, device) -> int:
+    """The size depends on these alone (``device``: its SMs); a program asks for few of them, again and again."""
+    d = fsdp_norm_desc_t(rows, cols, cols, cols, cols, 0, 0, 0, 0, 0, 0.0)
     out = _I64()
     _check(_lib.fsdp_layer_norm_workspace(ctypes.byref(d), ctypes.byref(out)), "fsdp_layer_norm_workspace")
     return out.value
@@ -270,7 +280,7 @@ def _norm_workspace(d) -> int:
 
 def fsdp_layer_norm_workspace(rows: int, cols: int) -> int:
     """Bytes of workspace that fsdp_layer_norm_backward needs for a [rows, cols] matrix."""
-    return _norm_workspace(fsdp_norm_desc_t(rows, cols, cols, cols, cols, 0, 0, 0, 0, 0, 0.0))
+    return _norm_workspace(rows, cols, torch.cuda.current_device() if torch.cuda.is_available() else None)
 
 
 def _kept(where, gate, up, rows, f, dev):
@@ -290,7 +300,10 @@ def _kept(where, gate, up, rows, f, dev):
     return pg, pu, lg, FSDP_KEEP_BF16, dev
 
 
-def _ffn_workspace(d, backward) -> int:
+@functools.lru_cache(maxsize=1024)
+def _ffn_workspace(backward, device, *fields) -> int:
+    """By the fields of the descriptor, as for the norm's."""
+    d = fsdp_ffn_desc_t(*fields)
     out = _I64()
     _check(_lib.fsdp_gated_ffn_workspace(ctypes.byref(d), backward, ctypes.byref(out)), "fsdp_gated_ffn_workspace")
     return out.value
@@ -301,9 +314,9 @@ def fsdp_gated_ffn_workspace(rows: int, d: int, f: int, backward: bool, keep: in
     """Bytes of workspace of a call on contiguous matrices, d and f multiples of 8, that start on 16-byte boundaries;
     for others, an upper bound with everything that may have to be copied."""
     odd = 0 if d % 8 == 0 else 7
-    desc = fsdp_ffn_desc_t(rows, d, f, d, d, d, f, f, d, d, d, FSDP_ACT_SILU, keep,
-                           FSDP_ACT8 if x_act8 else FSDP_DTYPE_BF16, FSDP_DTYPE_BF16, FSDP_DTYPE_BF16, odd)
-    return _ffn_workspace(desc, int(backward))
+    return _ffn_workspace(int(backward), torch.cuda.current_device() if torch.cuda.is_available() else None, rows, d, f, d, d, d, f,
+                          f, d, d, d, FSDP_ACT_SILU, keep, FSDP_ACT8 if x_act8 else FSDP_DTYPE_BF16, FSDP_DTYPE_BF16,
+                          FSDP_DTYPE_BF16, odd)
 
 
 def fsdp_gated_ffn_forward(x, w_gate, w_up, h, gate=None, up=None, activation=FSDP_ACT_SILU, workspace=None,
@@ -318,10 +331,10 @@ def fsdp_gated_ffn_forward(x, w_gate, w_up, h, gate=None, up=None, activation=FS
     ph, ld_h, _, dev = _matrix(where, "h", h, rows, f, _BF16, dev)
     pkg, pku, ld_k, keep, dev = _kept(where, gate, up, rows, f, dev)
     off = (px % 16 > 0) + 2 * (pg % 16 > 0) + 4 * (pu % 16 > 0)
-    desc = fsdp_ffn_desc_t(rows, d, f, ld_x, ld_g, ld_u, ld_h, ld_k, d, d, d, activation, keep, dt, dt, dt, off)
+    fields = (rows, d, f, ld_x, ld_g, ld_u, ld_h, ld_k, d, d, d, activation, keep, dt, dt, dt, off)
     handle = _handle(where, stream, dev)
-    pws, nws, _owner = _workspace(where, workspace, _ffn_workspace(desc, 0), handle, dev)
-    _check(_lib.fsdp_gated_ffn_forward(ctypes.byref(desc), px, pg, pu, ph, pkg, pku, pws, nws, handle), where)
+    pws, nws, _owner = _workspace(where, workspace, _ffn_workspace(0, dev, *fields), handle, dev)
+    _check(_lib.fsdp_gated_ffn_forward(ctypes.byref(fsdp_ffn_desc_t(*fields)), px, pg, pu, ph, pkg, pku, pws, nws, handle), where)
 
 
 def fsdp_gated_ffn_backward(dh, x, w_gate, w_up, dx=None, dw_gate=None, dw_up=None, gate=None, up=None,
@@ -355,12 +368,11 @@ def fsdp_gated_ffn_backward(dh, x, w_gate, w_up, dx=None, dw_gate=None, dw_up=No
         pdu, ld_du, dt_u, dev = _matrix(where, "dw_up", dw_up, f, d, _BOTH, dev)
         if dt_u != dt_dw:
             raise ValueError(f"{where}: dw_gate and dw_up have different dtypes")
-    desc = fsdp_ffn_desc_t(rows, d, f, ld_x, ld_g, ld_u, ld_h, ld_k, ld_dx, ld_dg, ld_du, activation, keep, dt_x, dt_dx,
-                           dt_dw, off)
+    fields = (rows, d, f, ld_x, ld_g, ld_u, ld_h, ld_k, ld_dx, ld_dg, ld_du, activation, keep, dt_x, dt_dx, dt_dw, off)
     handle = _handle(where, stream, dev)
-    pws, nws, _owner = _workspace(where, workspace, _ffn_workspace(desc, 1), handle, dev)
-    _check(_lib.fsdp_gated_ffn_backward(ctypes.byref(desc), pdh, px, pg, pu, pkg, pku, pdx, pdg, pdu, pws, nws, handle),
-           where)
+    pws, nws, _owner = _workspace(where, workspace, _ffn_workspace(1, dev, *fields), handle, dev)
+    _check(_lib.fsdp_gated_ffn_backward(ctypes.byref(fsdp_ffn_desc_t(*fields)), pdh, px, pg, pu, pkg, pku, pdx, pdg, pdu, pws, nws,
+                                        handle), where)
 
 
 def fsdp_ops_sync_status(stream=None) -> None:

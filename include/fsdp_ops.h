@@ -129,7 +129,8 @@ fsdp_status_t fsdp_layer_norm_forward(const fsdp_norm_desc_t *desc, const void *
  *   dx:             [rows, cols] of dx_dtype, or NULL if not wanted.
  *   dweight, dbias: cols elements of grad_dtype each, written (not added to);
  *                   either may be NULL if not wanted.
- *   workspace:      fsdp_layer_norm_workspace bytes, 16-byte aligned.
+ *   workspace:      fsdp_layer_norm_workspace bytes, 16-byte aligned; may be NULL
+ *                   if that is 0.
  */
 fsdp_status_t fsdp_layer_norm_backward(const fsdp_norm_desc_t *desc, const void *dy, const void *x,
                                        const void *weight, const float *mean, const float *rstd, void *dx,

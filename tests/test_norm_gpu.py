@@ -267,8 +267,10 @@ def test_refusals():
         fp.fsdp_layer_norm_forward(fp.Act8(4, 64), w, w, torch.empty_like(x), keep=fp.Act8(4, 64))
     with pytest.raises(ValueError, match="needed"):
         fp.fsdp_layer_norm_backward(x, x, w, m, None, torch.empty_like(x))
+    many, rows = torch.zeros(4000, 64, device="cuda"), torch.zeros(4000, device="cuda")  # 4 rows need no workspace
     with pytest.raises(ValueError, match="the call needs"):
-        fp.fsdp_layer_norm_backward(x, x, w, m, m, torch.empty_like(x), workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+        fp.fsdp_layer_norm_backward(many, many, w, rows, rows, torch.empty_like(many),
+                                    workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     wide = torch.zeros(1, 65537, device="cuda")
     with pytest.raises(fp.FsdpError, match="FSDP_NORM_MAX_COLS"):
         fp.fsdp_layer_norm_forward(wide, None, None, torch.empty_like(wide))

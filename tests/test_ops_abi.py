@@ -15,6 +15,9 @@ ODD = ctypes.c_void_p(4098)
 
 @pytest.fixture(scope="module")
 def fp():
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("made-up pointers: only where no kernel could run on them")
     _build.build()
     from fsdp2_gradient_packing_gb300 import fsdp_pack
     return fsdp_pack
@@ -87,9 +90,11 @@ def test_norm_refusals(fp):
     refused(fp, backward(norm(fp, dx_dtype=5)), E, "dx_dtype")
     refused(fp, backward(norm(fp, grad_dtype=5)), E, "grad_dtype")
     refused(fp, backward(norm(fp, ld_dx=1)), E, "dx")
-    refused(fp, backward(norm(fp), n=0), E, "workspace_bytes")
-    refused(fp, backward(norm(fp), ws=ctypes.c_void_p(4104)), E, "workspace")
+    refused(fp, backward(norm(fp, rows=4000), n=0), E, "workspace_bytes")
+    refused(fp, backward(norm(fp, rows=4000), ws=ctypes.c_void_p(4104)), E, "workspace")
+    refused(fp, backward(norm(fp, rows=4000), ws=None), E, "workspace is NULL")
     assert fp.fsdp_layer_norm_workspace(1000, 512) >= 2 * 512 * 4
+    assert fp.fsdp_layer_norm_workspace(0, 512) == 0 and fp.fsdp_layer_norm_workspace(1, 512) == 0
 
 
 def ffn(fp, **k):
