@@ -46,10 +46,11 @@ struct Args {
   uint64_t wait_limit_ns;
   int32_t fault;
   int32_t act;        // Act
+  int32_t turns;      // some rows go through the epilogue warps' buffers
   Grid grid[2];       // BACKWARD: weight gradients, dx; else the first only
   int32_t a_rows;     // FORWARD, RECOMPUTE: rows of an x box (see gated())
   int32_t tile_n;     // accumulator columns of a tile (FORWARD, RECOMPUTE: half of them gate;
-                      // BACKWARD: a multiple of 64 a block)
+                      // BACKWARD: 64, 128 or 256)
   int32_t half[2];    // BACKWARD: the row tile / the K block from which on the up half is meant
   int64_t m[2], n;    // rows and columns of the outputs (FORWARD, RECOMPUTE: n = f)
   // Outputs, [m, n] with row distance ld.

@@ -4,7 +4,7 @@ namespace fsdp {
 namespace ffn {
 
 cudaError_t launch_backward(bool pair, Args &a, int sms, cudaStream_t stream) {
-  return launch_mode<BACKWARD>(pair, a, sms, stream);
+  return launch_columns(pair, a, sms, stream);
 }
 
 }  // namespace ffn

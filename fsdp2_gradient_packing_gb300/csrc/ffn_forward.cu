@@ -4,7 +4,7 @@ namespace fsdp {
 namespace ffn {
 
 cudaError_t launch_forward(bool pair, Args &a, int sms, cudaStream_t stream) {
-  return launch_mode<FORWARD>(pair, a, sms, stream);
+  return launch_gated<FORWARD>(pair, a, sms, stream);
 }
 
 }  // namespace ffn

@@ -8,8 +8,11 @@ namespace fsdp {
 namespace ffn {
 namespace {
 
-constexpr int kEpilogueWarps = 8; // two to each quarter of TMEM's lanes
-constexpr int kThreads = 64 + 32 * kEpilogueWarps;  // and a TMA and an MMA warp
+// Two epilogue warps to each quarter of TMEM's lanes, one warp that loads and one that
+// issues MMAs.  (Sixteen epilogue warps, which the registers would allow, take 5 % longer
+// at 8192 x 1024 x 4096: the MMAs bound it, and more warps slow the thread that issues them.)
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kTileN = 256;       // most accumulator columns of a tile
 constexpr int kAccumulators = 2;  // 2 x 256 columns: all of TMEM
 constexpr int kTmemColumns = kTileN * kAccumulators;
@@ -21,13 +24,17 @@ constexpr int kTurnBytes = 32 * kTurnPitch * 4;
 
 constexpr int kA = kTileM * kTileK * 2;  // bytes of a block's A in a stage; B follows
 constexpr int kMostStages = 8;
-// Shared memory of the stages: what the rest leaves, with the stages on 1,024-byte boundaries.
-constexpr int kRing = 227 * 1024 - 1024 - kEpilogueWarps * kTurnBytes - 1024;
+// Shared memory of the stages and, only where some rows take no vectors, of the warps'
+// buffers after them; the stages begin on a 1,024-byte boundary.
+constexpr int kDynamic = 226 * 1024;
+__host__ __device__ __forceinline__ int ring_bytes(bool turns) {
+  return kDynamic - 1024 - (turns ? kEpilogueWarps * kTurnBytes : 0);
+}
 
 // Bytes of a block's stage, and how many fit: narrow tiles get more, so that as many bytes
-// are in flight (with four stages for all, 16 rows through 2048 x 6144 took 22 us).
+// are in flight (with four stages for all, 16 rows through 2048 x 6144 took 22 us, not 13).
 __host__ __device__ __forceinline__ int stage_bytes(int columns, int cg) { return kA + columns / cg * (kTileK * 2); }
-__host__ __device__ __forceinline__ int stages_of(int bytes) { return min(kRing / bytes, kMostStages); }
+__host__ __device__ __forceinline__ int stages_of(int ring, int bytes) { return min(ring / bytes, kMostStages); }
 
 struct Shared {
   uint64_t full[kMostStages], empty[kMostStages], tmem_full[kAccumulators], tmem_empty[kAccumulators], drain;
@@ -42,6 +49,28 @@ struct Unit {
 };
 
 __device__ __forceinline__ int units_of(const Grid &g) { return g.m * g.n * g.splits; }
+
+// The K blocks of unit i, all that issuing its MMAs takes: worked out by one thread while
+// the tensor cores run dry, so without the divisions that find the tile.
+struct Span {
+  int which, k0, k1;
+};
+template <int MODE>
+__device__ __forceinline__ Span span_at(const Args &a, int i) {
+  Span s = {0, 0, a.grid[0].k_blocks};
+  if constexpr (MODE == BACKWARD) {
+    const int first = units_of(a.grid[0]);
+    if (i >= first) s.which = 1, i -= first;
+    const Grid &g = a.grid[s.which];
+    s.k1 = g.k_blocks;
+    if (g.splits > 1) {
+      const int per = (g.k_blocks + g.splits - 1) / g.splits;
+      s.k0 = min(i % g.splits * per, g.k_blocks);
+      s.k1 = min(s.k0 + per, g.k_blocks);
+    }
+  }
+  return s;
+}
 
 template <int MODE>
 __device__ __forceinline__ Unit unit_at(const Args &a, int i) {
@@ -69,7 +98,7 @@ __device__ __forceinline__ Unit unit_at(const Args &a, int i) {
 // How a tile's K blocks are loaded: boxes at (x, y) of two maps, advanced by (kx, ky) from
 // K block to K block.  One thread loads and one issues MMAs, about 500 cycles to a K
 // block, so what they do for each is worked out once a tile.
-template <int MODE, int CG>
+template <int MODE, int CG, int COLS>
 struct Loader {
   const CUtensorMap *ma, *mb, *mb2;
   int ax, ay, bx, by;        // next box of A and of B
@@ -85,7 +114,7 @@ struct Loader {
     } else {
       // Boxes of 64 x 64 throughout.  Along K in a row (A of dx): two boxes of 64 rows lie
       // one after the other; along M or N in a row: one box to 64 of them.
-      bx = u.n * a.tile_n + rank * (a.tile_n / CG);
+      bx = u.n * COLS + rank * (COLS / CG);
       if (u.which == 1) {
         go_to(a, u.k0);
         ay = (u.m * CG + rank) * kTileM;
@@ -114,7 +143,8 @@ struct Loader {
     } else {
 #pragma unroll
       for (int c = 0; c < kTileM / 64; ++c) tc::tma_load<CG>(at + c * 8192, ma, ax + c * acx, ay + c * acy, bar);
-      for (int c = 0; c < a.tile_n / CG / 64; ++c) tc::tma_load<CG>(sb + c * 8192, mb, bx + c * 64, by, bar);
+#pragma unroll
+      for (int c = 0; c < COLS / CG / 64; ++c) tc::tma_load<CG>(sb + c * 8192, mb, bx + c * 64, by, bar);
     }
   }
   __device__ __forceinline__ void advance() {
@@ -138,47 +168,32 @@ struct Part {
 // a time; whole 32-byte sectors keep that from costing two writes a sector.  Rows that no
 // vector fits go through the warp's buffer, half a warp to a row (element by element from
 // a row to a thread, a store instruction would touch 32 sectors for 64 bytes).
-__device__ __forceinline__ void store_part(void *p, int64_t ld, bool bf16, int width, const float2 (&v)[16], const Part &q) {
-  if (width >= 16 && q.n >= 32) {
-    if ((int)(threadIdx.x & 31) >= q.rows) return;
-    const int64_t at = q.row * ld + q.col;
-    if (bf16) {
-      uint32_t w[16];
+__device__ __forceinline__ bool whole(int width, const Part &q) { return width >= 16 && q.n >= 32; }
+
+// 32 columns as 16 or 32 words of a row of whole vectors.
+template <int WORDS>
+__device__ __forceinline__ void store_words(void *row, int width, const uint32_t (&w)[WORDS]) {
+  uint4 *to = static_cast<uint4 *>(row);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = bf16_pair(v[i].x, v[i].y);
-      uint4 *to = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + at);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t(&h)[8] = reinterpret_cast<const uint32_t(&)[8]>(w[8 * i]);
-        if (width == 32)
-          store32(to + 2 * i, h);
-        else
-          to[2 * i] = make_uint4(h[0], h[1], h[2], h[3]), to[2 * i + 1] = make_uint4(h[4], h[5], h[6], h[7]);
-      }
-    } else {
-      float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (width == 32) {
-          uint32_t h[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) h[e] = __float_as_uint(element(v, 8 * i + e));
-          store32(to + 2 * i, h);
-        } else {
-          to[2 * i] = make_float4(v[4 * i].x, v[4 * i].y, v[4 * i + 1].x, v[4 * i + 1].y);
-          to[2 * i + 1] = make_float4(v[4 * i + 2].x, v[4 * i + 2].y, v[4 * i + 3].x, v[4 * i + 3].y);
-        }
-      }
-    }
-    return;
+  for (int i = 0; i < WORDS / 8; ++i) {
+    const uint32_t(&h)[8] = reinterpret_cast<const uint32_t(&)[8]>(w[8 * i]);
+    if (width == 32)
+      store32(to + 2 * i, h);
+    else
+      to[2 * i] = make_uint4(h[0], h[1], h[2], h[3]), to[2 * i + 1] = make_uint4(h[4], h[5], h[6], h[7]);
   }
+}
+
+// Sixteen columns from `side` on, through the buffer.
+template <class F>
+__device__ __forceinline__ void store_turned(void *p, int64_t ld, bool bf16, const Part &q, F &&value) {
   const int lane = threadIdx.x & 31;
   const int64_t first = q.row - lane;
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
     __syncwarp();
 #pragma unroll
-    for (int e = 0; e < 16; ++e) q.turn[lane * kTurnPitch + e] = element(v, side * 16 + e);
+    for (int e = 0; e < 16; ++e) q.turn[lane * kTurnPitch + e] = value(side * 16 + e);
     __syncwarp();
     const int c = side * 16 + lane % 16;
     if (c < q.n)
@@ -187,83 +202,114 @@ __device__ __forceinline__ void store_part(void *p, int64_t ld, bool bf16, int w
   }
 }
 
-// The part of a BF16 matrix, 0 where there is none; `vec`: its rows start on 16-byte boundaries.
-__device__ __forceinline__ void load_part(const __nv_bfloat16 *p, int64_t ld, bool vec, float2 (&v)[16], const Part &q) {
+// Binary32 values (as bits), or BF16 pairs, in memory.
+__device__ __forceinline__ void store_part(void *p, int64_t ld, bool bf16, int width, const uint32_t (&v)[32], const Part &q) {
+  if (!whole(width, q))
+    return store_turned(p, ld, bf16, q, [&](int e) { return __uint_as_float(v[e]); });
+  if ((int)(threadIdx.x & 31) >= q.rows) return;
+  const int64_t at = q.row * ld + q.col;
+  if (bf16) {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = bf16_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+    store_words(static_cast<uint16_t *>(p) + at, width, w);
+  } else {
+    store_words(static_cast<float *>(p) + at, width, v);
+  }
+}
+__device__ __forceinline__ void store_part(void *p, int64_t ld, int width, const uint32_t (&w)[16], const Part &q) {
+  if (!whole(width, q))
+    return store_turned(p, ld, true, q, [&](int e) { return e % 2 ? bf16_high(w[e / 2]) : bf16_low(w[e / 2]); });
+  if ((int)(threadIdx.x & 31) < q.rows) store_words(static_cast<uint16_t *>(p) + q.row * ld + q.col, width, w);
+}
+
+// The part of a BF16 matrix as pairs, 0 where there is none; `vec`: its rows start on
+// 16-byte boundaries.
+__device__ __forceinline__ void load_part(const uint16_t *p, int64_t ld, bool vec, uint32_t (&w)[16], const Part &q) {
   const int lane = threadIdx.x & 31;
   if (vec && q.n >= 32) {
+    const uint4 *from = reinterpret_cast<const uint4 *>(p + q.row * ld + q.col);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = both(0.0f);
-    if (lane >= q.rows) return;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) load8(p + q.row * ld + q.col, 8 * i, true, reinterpret_cast<float2(&)[4]>(v[4 * i]));
+    for (int i = 0; i < 4; ++i) {
+      const uint4 r = lane < q.rows ? from[i] : make_uint4(0, 0, 0, 0);
+      w[4 * i] = r.x, w[4 * i + 1] = r.y, w[4 * i + 2] = r.z, w[4 * i + 3] = r.w;
+    }
     return;
   }
   const int64_t first = q.row - lane;
+  uint32_t *const turn = reinterpret_cast<uint32_t *>(q.turn);
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
     const int c = side * 16 + lane % 16;
     __syncwarp();
     for (int r = lane / 16; r < 32; r += 2)
-      q.turn[r * kTurnPitch + lane % 16] =
-          c < q.n && r < q.rows ? __bfloat162float(p[(first + r) * ld + q.col + c]) : 0.0f;
+      turn[r * kTurnPitch + lane % 16] = c < q.n && r < q.rows ? p[(first + r) * ld + q.col + c] : 0u;
     __syncwarp();
 #pragma unroll
-    for (int e = 0; e < 16; ++e) element(v, side * 16 + e) = q.turn[lane * kTurnPitch + e];
+    for (int e = 0; e < 8; ++e)
+      w[side * 8 + e] = turn[lane * kTurnPitch + 2 * e] | turn[lane * kTurnPitch + 2 * e + 1] << 16;
   }
-}
-
-// The 8-bit checkpoint of 32 consecutive elements, one whole group; elements from n on are 0.
-__device__ __forceinline__ void keep_group(uint8_t *codes, uint8_t *scale, float2 (&v)[16], int n, bool sector) {
-  if (n < 32) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i >= n) element(v, i) = 0.0f;
-  }
-  const uint32_t s = act8_scale_byte(act8_top(v));
-  act8_store<32>(codes, v, s, sector);
-  *scale = (uint8_t)s;
 }
 
 __device__ __forceinline__ float2 pair_at(const uint32_t (&r)[32], int i) {
   return make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 
-// A warp's part of a gate / up tile.
+// The 8-bit checkpoint of 32 consecutive elements, one whole group.
+__device__ __forceinline__ void keep_group(uint8_t *codes, uint8_t *scale, const uint32_t (&r)[32], bool sector) {
+  float2 v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = pair_at(r, i);
+  const uint32_t s = act8_scale_byte(act8_top(v));
+  act8_store<32>(codes, v, s, sector);
+  *scale = (uint8_t)s;
+}
+
+// A warp's part of a gate / up tile.  What is kept goes first, and results are packed as
+// they are made, so that few values live beside g and u: that leaves registers for
+// sixteen warps.
 template <int MODE, int ACT, int KEEP>
-__device__ __forceinline__ void gated_part(const Args &a, const uint32_t (&gr)[32], const uint32_t (&ur)[32], const Part &q) {
-  float2 x[16], y[16];
+__device__ __forceinline__ void gated_part(const Args &a, uint32_t (&gr)[32], uint32_t (&ur)[32], const Part &q) {
   if constexpr (MODE == FORWARD) {
+    if constexpr (KEEP == 1) {
+      if (q.n < 32) {  // a row's last group: its missing elements are 0
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float2 y_i, none;
-      act_of<false, ACT>(pair_at(gr, i), y_i, none);
-      x[i] = __fmul2_rn(y_i, pair_at(ur, i));
-    }
-    store_part(a.out[0], a.ld_out[0], true, a.out_width[0], x, q);
-    if constexpr (KEEP != 0) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = pair_at(gr, i), y[i] = pair_at(ur, i);
-      if constexpr (KEEP == 2) {
-        store_part(a.kept[0], a.ld_kept, true, a.keep_width, x, q);
-        store_part(a.kept[1], a.ld_kept, true, a.keep_width, y, q);
-      } else if ((int)(threadIdx.x & 31) < q.rows) {
-        const int64_t group = q.row * a.groups + q.col / (int)kActGroup;
-        keep_group(a.codes[0] + group * kActGroup, a.scales[0] + group, x, q.n, a.keep_width == 32);
-        keep_group(a.codes[1] + group * kActGroup, a.scales[1] + group, y, q.n, a.keep_width == 32);
+        for (int i = 0; i < 32; ++i)
+          if (i >= q.n) gr[i] = ur[i] = 0u;
       }
+      if ((int)(threadIdx.x & 31) < q.rows) {
+        const int64_t group = q.row * a.groups + q.col / (int)kActGroup;
+        keep_group(a.codes[0] + group * kActGroup, a.scales[0] + group, gr, a.keep_width == 32);
+        keep_group(a.codes[1] + group * kActGroup, a.scales[1] + group, ur, a.keep_width == 32);
+      }
+    } else if constexpr (KEEP == 2) {
+      store_part(a.kept[0], a.ld_kept, true, a.keep_width, gr, q);
+      store_part(a.kept[1], a.ld_kept, true, a.keep_width, ur, q);
     }
-  } else {
-    float2 d[16];
-    load_part(static_cast<const __nv_bfloat16 *>(a.dh), a.ld_dh, a.dh_vec != 0, d, q);
+    uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
+      float2 y, none;
+      act_of<false, ACT>(pair_at(gr, i), y, none);
+      y = __fmul2_rn(y, pair_at(ur, i));
+      w[i] = bf16_pair(y.x, y.y);
+    }
+    store_part(a.out[0], a.ld_out[0], a.out_width[0], w, q);
+  } else {
+    uint32_t d[16];
+    load_part(static_cast<const uint16_t *>(a.dh), a.ld_dh, a.dh_vec != 0, d, q);
+    uint32_t dg[16], du[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 dh = make_float2(bf16_low(d[i]), bf16_high(d[i]));
       float2 act, slope;
       act_of<true, ACT>(pair_at(gr, i), act, slope);
-      x[i] = __fmul2_rn(__fmul2_rn(d[i], pair_at(ur, i)), slope);
-      y[i] = __fmul2_rn(d[i], act);
+      slope = __fmul2_rn(__fmul2_rn(dh, pair_at(ur, i)), slope);
+      act = __fmul2_rn(dh, act);
+      dg[i] = bf16_pair(slope.x, slope.y), du[i] = bf16_pair(act.x, act.y);
     }
-    store_part(a.out[0], a.ld_out[0], true, a.out_width[0], x, q);
-    store_part(a.out[1], a.ld_out[1], true, a.out_width[0], y, q);
+    store_part(a.out[0], a.ld_out[0], a.out_width[0], dg, q);
+    store_part(a.out[1], a.ld_out[1], a.out_width[0], du, q);
   }
 }
 
@@ -289,12 +335,13 @@ __device__ __noinline__ void land_copies(Shared &sh, const Args &a, uint32_t sta
   }
 }
 
-template <int MODE, int CG, int ACT, int KEEP>
+// COLS: columns of a BACKWARD tile (other uses go by Args).
+template <int MODE, int CG, int ACT, int KEEP, int COLS>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Args a) {
   extern __shared__ uint8_t dynamic[];
   __shared__ Shared sh;
-  const int columns = a.tile_n;
-  const uint32_t stage_size = stage_bytes(columns, CG), stage_count = stages_of((int)stage_size);
+  const int columns = MODE == BACKWARD ? COLS : a.tile_n;
+  const uint32_t stage_size = stage_bytes(columns, CG), stage_count = stages_of(ring_bytes(a.turns != 0), (int)stage_size);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const uint32_t stages = (tc::smem(dynamic) + 1023u) & ~1023u;
   const int rank = CG == 1 ? 0 : (int)tc::cluster_rank();
@@ -337,12 +384,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const uint32_t full = tc::smem(&sh.full[0]), empty = tc::smem(&sh.empty[0]);
       const uint32_t leader = CG == 1 ? full : tc::at_rank(full, 0);
       const bool skip = skips_first(a, worker);
+      const int half = MODE == BACKWARD ? a.half[1] : 0;
       for (int i = worker; i < units && ok; i += workers) {
         const Unit u = unit_at<MODE>(a, i);
-        Loader<MODE, CG> from(a, u, rank);
-        for (int kb = u.k0; kb < u.k1; ++kb) {
+        Loader<MODE, CG, COLS> from(a, u, rank);
+        const int k0 = u.k0, k1 = u.k1, which = u.which;
+        for (int kb = k0; kb < k1; ++kb) {
           if (!(ok = tc::bar_wait(empty + stage * 8, phase ^ 1u, a.wait_limit_ns, stop))) break;
-          if (MODE == BACKWARD && u.which == 1 && kb == a.half[1]) from.go_to(a, kb);
+          if (MODE == BACKWARD && which == 1 && kb == half) from.go_to(a, kb);
           if (!skip || filled > 0) {
             if (rank == 0) tc::bar_expect(full + stage * 8, bytes);
             from.load(a, stages + stage * stage_size, leader + stage * 8);
@@ -367,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       bool issued = false;
       const uint32_t full = tc::smem(&sh.full[0]), empty = tc::smem(&sh.empty[0]);
       for (int i = worker; i < units && ok; i += workers) {
-        const Unit u = unit_at<MODE>(a, i);
+        const Span u = span_at<MODE>(a, i);
         if (!(ok = tc::bar_wait(tc::smem(&sh.tmem_empty[acc]), acc_phase ^ 1u, a.wait_limit_ns, stop))) break;
         tc::fence_after();
         const uint32_t d = tmem + acc * kTileN;
@@ -406,8 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   } else {
     // ---- epilogue ------------------------------------------------------------
     const int quarter = warp & 3;          // the lanes of TMEM that this warp may read
-    const int side = (warp - 2) / 4;       // and its half of the columns
-    float *const turn = reinterpret_cast<float *>(dynamic + (stages - tc::smem(dynamic)) + kRing / 1024 * 1024) +
+    const int side = (warp - 2) / 4;       // and its part of the columns, of `sides`
+    constexpr int sides = kEpilogueWarps / 4;
+    float *const turn = reinterpret_cast<float *>(dynamic + kDynamic - kEpilogueWarps * kTurnBytes) +
                         (warp - 2) * (kTurnBytes / 4);
     uint32_t acc = 0, acc_phase = 0;
     for (int i = worker; i < units; i += workers) {
@@ -425,8 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const bool some = u.k1 > u.k0;  // an empty part of a K loop: the sum is 0
       if constexpr (MODE == FORWARD || MODE == RECOMPUTE) {
         const int64_t row = ((int64_t)u.m * CG + rank) * kTileM + quarter * 32 + lane;
-        const int half = a.tile_n / 2, runs = half / 32, mid = (runs + 1) / 2;
-        const int begin = side ? mid : 0, end = side ? runs : mid;
+        const int half = a.tile_n / 2, runs = half / 32;
+        const int begin = side * runs / sides, end = (side + 1) * runs / sides;
         if (begin == end) drained();
 #pragma unroll 1
         for (int c = begin; c < end; ++c) {
@@ -444,25 +494,29 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       } else {
         const int which = u.which, up = which == 0 && u.m >= a.half[0] ? 1 : 0, to = which == 1 ? 2 : up;
         const int64_t row = ((int64_t)(u.m - up * a.half[0]) * CG + rank) * kTileM + quarter * 32 + lane, m = a.m[which];
+        constexpr int runs = COLS / 32;
+        const int begin = side * runs / sides, end = (side + 1) * runs / sides;
+        if (begin == end) drained();
 #pragma unroll 1
-        for (int c = side * (a.tile_n / 2); c < (side + 1) * (a.tile_n / 2); c += 32) {
-          const int64_t col = (int64_t)u.n * a.tile_n + c;
+        for (int c = begin; c < end; ++c) {
+          const int64_t col = (int64_t)u.n * COLS + c * 32;
           uint32_t r[32];
           __syncwarp();
-          tc::tmem_load32(from + c, r);
+          tc::tmem_load32(from + c * 32, r);
           tc::tmem_load_wait();
-          if (c + 32 == (side + 1) * (a.tile_n / 2)) drained();
+          if (c + 1 == end) drained();
           const int64_t rows = m - (row - lane);
           if (rows > 0 && col < a.n) {
             const Part q = {col, (int)min((int64_t)32, a.n - col), (int)min((int64_t)32, rows), row, turn};
-            float2 v[16];
+            if (!some) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = some ? pair_at(r, e) : both(0.0f);
+              for (int e = 0; e < 32; ++e) r[e] = 0u;
+            }
             if (a.grid[which].splits > 1) {
               const int64_t all = which == 0 ? 2 * m : m;
-              store_part(a.partial[which] + ((int64_t)u.split * all + up * m) * a.n, a.n, false, a.partial_width[which], v, q);
+              store_part(a.partial[which] + ((int64_t)u.split * all + up * m) * a.n, a.n, false, a.partial_width[which], r, q);
             } else {
-              store_part(a.out[to], a.ld_out[to], a.out_bf16[which] != 0, a.out_width[which], v, q);
+              store_part(a.out[to], a.ld_out[to], a.out_bf16[which] != 0, a.out_width[which], r, q);
             }
           }
         }
@@ -483,36 +537,48 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   if (warp == 1) tc::tmem_free<CG>(tmem, kTmemColumns);
 }
 
-template <int MODE, int CG, int ACT, int KEEP>
+template <int MODE, int CG, int ACT, int KEEP, int COLS>
 cudaError_t launch(Args &a, int sms, cudaStream_t stream) {
-  constexpr int kSmem = 1024 + kRing + kEpilogueWarps * kTurnBytes;
-  const void *fn = reinterpret_cast<const void *>(&product_kernel<MODE, CG, ACT, KEEP>);
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const void *fn = reinterpret_cast<const void *>(&product_kernel<MODE, CG, ACT, KEEP, COLS>);
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynamic);
   if (e != cudaSuccess) return e;
   int64_t units = 0;
   for (int w = 0; w < (MODE == BACKWARD ? 2 : 1); ++w) units += (int64_t)a.grid[w].m * a.grid[w].n * a.grid[w].splits;
   int64_t workers = sms / CG;
   if (workers > units) workers = units;
-  void *args[] = {&a};
-  return launch_kernel(fn, dim3((unsigned)(workers * CG)), dim3(kThreads), args, kSmem, stream, true, CG);
-}
-
-template <int MODE, int CG, int ACT>
-cudaError_t launch_keep(Args &a, int sms, cudaStream_t stream) {
-  if constexpr (MODE == FORWARD) {
-    if (a.keep == 1) return launch<MODE, CG, ACT, 1>(a, sms, stream);
-    if (a.keep == 2) return launch<MODE, CG, ACT, 2>(a, sms, stream);
+  // Rows through the warps' buffers: those that no vector fits, and a row's last columns.
+  auto odd = [](int width) { return width < 16; };
+  a.turns = a.n % 32 != 0;
+  if (MODE == BACKWARD) {
+    for (int w = 0; w < 2; ++w) a.turns |= a.grid[w].m > 0 && odd(a.grid[w].splits > 1 ? a.partial_width[w] : a.out_width[w]);
+  } else {
+    a.turns |= odd(a.out_width[0]) || (MODE == FORWARD && KEEP == 2 && odd(a.keep_width)) || (MODE == RECOMPUTE && !a.dh_vec);
   }
-  return launch<MODE, CG, ACT, 0>(a, sms, stream);
+  void *args[] = {&a};
+  return launch_kernel(fn, dim3((unsigned)(workers * CG)), dim3(kThreads), args, kDynamic, stream, true, CG);
 }
 
+// FORWARD and RECOMPUTE, by activation and by what is kept.
+template <int MODE, int CG, int ACT>
+cudaError_t launch_gated(Args &a, int sms, cudaStream_t stream) {
+  if constexpr (MODE == FORWARD) {
+    if (a.keep == 1) return launch<MODE, CG, ACT, 1, 0>(a, sms, stream);
+    if (a.keep == 2) return launch<MODE, CG, ACT, 2, 0>(a, sms, stream);
+  }
+  return launch<MODE, CG, ACT, 0, 0>(a, sms, stream);
+}
 template <int MODE>
-cudaError_t launch_mode(bool pair, Args &a, int sms, cudaStream_t stream) {
-  if (MODE == BACKWARD || a.act == SILU)
-    return pair ? launch_keep<MODE, 2, SILU>(a, sms, stream) : launch_keep<MODE, 1, SILU>(a, sms, stream);
-  if constexpr (MODE != BACKWARD)
-    return pair ? launch_keep<MODE, 2, GELU>(a, sms, stream) : launch_keep<MODE, 1, GELU>(a, sms, stream);
-  return cudaErrorInvalidValue;
+cudaError_t launch_gated(bool pair, Args &a, int sms, cudaStream_t stream) {
+  if (a.act == SILU) return pair ? launch_gated<MODE, 2, SILU>(a, sms, stream) : launch_gated<MODE, 1, SILU>(a, sms, stream);
+  return pair ? launch_gated<MODE, 2, GELU>(a, sms, stream) : launch_gated<MODE, 1, GELU>(a, sms, stream);
+}
+
+// BACKWARD, by the tile's columns.
+inline cudaError_t launch_columns(bool pair, Args &a, int sms, cudaStream_t stream) {
+  if (pair)
+    return a.tile_n == 256 ? launch<BACKWARD, 2, SILU, 0, 256>(a, sms, stream) : launch<BACKWARD, 2, SILU, 0, 128>(a, sms, stream);
+  if (a.tile_n == 256) return launch<BACKWARD, 1, SILU, 0, 256>(a, sms, stream);
+  return a.tile_n == 128 ? launch<BACKWARD, 1, SILU, 0, 128>(a, sms, stream) : launch<BACKWARD, 1, SILU, 0, 64>(a, sms, stream);
 }
 
 }  // namespace

@@ -4,7 +4,7 @@ namespace fsdp {
 namespace ffn {
 
 cudaError_t launch_recompute(bool pair, Args &a, int sms, cudaStream_t stream) {
-  return launch_mode<RECOMPUTE>(pair, a, sms, stream);
+  return launch_gated<RECOMPUTE>(pair, a, sms, stream);
 }
 
 }  // namespace ffn
