@@ -4,14 +4,17 @@
 // A row belongs to one group of G threads, of which each holds K chunks of 8
 // columns in registers, so a row is read once whatever the passes over it.
 // A persistent block per SM has several groups, each with rows of its own; a row
-// wider than 512 threads x 16 columns is split over a cluster of up to 8 blocks,
-// whose sums meet in distributed shared memory.
+// wider than a block's 8192 columns is split over a cluster of up to 8 blocks, whose
+// sums meet in distributed shared memory (three rows at a time forward, one backward;
+// 4096 x 16384 in BF16 takes 89 us forward, 168 with one row at a time).
 //
-// Rows come through a ring of shared-memory stages per group, which one lane of a
-// warp of its own fills with TMA bulk copies several rows ahead: what is in flight
-// then depends neither on registers nor on the order in which loads return, and no
-// group waits for a thread that issues copies.  A stage is free once every thread of
-// the group has summed its part, which the barrier of the row's first sum shows.
+// Rows come through a ring of shared-memory stages per group, filled with TMA bulk
+// copies several rows ahead: what is in flight then depends neither on registers nor
+// on the order in which loads return.  A stage is free once every thread of the group
+// has summed its part, which the barrier of the row's first sum shows.  Forward, one
+// lane of a warp of its own fills a group's ring; backward the groups need the whole
+// register file, 8 warps of up to 255, and a ninth warp would cost each thread 87 of
+// them, so a few lanes of each group fill its ring themselves.
 //
 // Vector kernels give a thread 8 consecutive columns.  Where rows start off a
 // 16-byte boundary or no vector divides them, a thread's 8 columns are G apart
@@ -31,6 +34,7 @@ constexpr uint32_t kStatusNorm = 32u;  // a wait of these kernels gave up
 constexpr int kMaxCluster = 8;
 constexpr int kMaxWarps = 32;
 constexpr int kMaxStages = 8;
+constexpr int kClusterGroups = 3;  // row groups of a block whose rows are split over a cluster
 
 // One matrix as it passes through the ring: rows of `row_bytes`, `pitch` bytes apart.
 struct Stream {
@@ -64,8 +68,8 @@ struct Args {
 struct alignas(16) Shared {
   uint4 zeros[2];
   float warp[2][2][kMaxWarps];
-  float block[2][2][kMaxCluster];
-  uint64_t arrived[2];
+  float block[kClusterGroups][2][2][kMaxCluster];
+  uint64_t arrived[kClusterGroups][2];
   uint64_t full[kMaxWarps][kMaxStages], empty[kMaxWarps][kMaxStages];  // one ring to a group
   uint32_t stop;
 };
@@ -112,6 +116,10 @@ __device__ __forceinline__ void row_sum(float (&v)[N], Shared &s, int &turn, int
     for (int i = 0; i < N; ++i) {
       const float4 *p = reinterpret_cast<const float4 *>(&s.warp[q][i][group * (G / 32)]);
       v[i] = 0.0f;
+      if constexpr (G == 64) {
+        const float2 a = *reinterpret_cast<const float2 *>(&s.warp[q][i][group * 2]);
+        v[i] = a.x + a.y;
+      }
 #pragma unroll
       for (int w = 0; w < G / 128; ++w) {
         const float4 a = p[w];
@@ -121,20 +129,20 @@ __device__ __forceinline__ void row_sum(float (&v)[N], Shared &s, int &turn, int
     if constexpr (CLUSTER) {
       // Thread r sends the block's sums to block r; each block's barrier counts them in.
       // No block can be two sums ahead of another, so two slots do here too.
-      const uint32_t n = cluster_blocks(), bar = tc::smem(&s.arrived[q]);
-      if (threadIdx.x < n) {
+      const uint32_t n = cluster_blocks(), bar = tc::smem(&s.arrived[group][q]), to = threadIdx.x % G;
+      if (to < n) {
         const uint32_t rank = tc::cluster_rank();
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::at_rank(tc::smem(&s.block[q][i][rank]), threadIdx.x)), "f"(v[i])
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::at_rank(tc::smem(&s.block[group][q][i][rank]), to)), "f"(v[i])
                        : "memory");
-        tc::bar_arrive_cluster(tc::at_rank(bar, threadIdx.x));
+        tc::bar_arrive_cluster(tc::at_rank(bar, to));
       }
       tc::bar_wait(bar, (uint32_t)(turn >> 1) & 1u, limit_ns, &s.stop);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        v[i] = s.block[q][i][0];
-        for (uint32_t r = 1; r < n; ++r) v[i] += s.block[q][i][r];
+        v[i] = s.block[group][q][i][0];
+        for (uint32_t r = 1; r < n; ++r) v[i] += s.block[group][q][i][r];
       }
     }
     ++turn;
@@ -222,6 +230,38 @@ __device__ __forceinline__ void load_rows(const Args &a, Shared &sh, uint8_t *me
     if (++stage == a.stages) stage = 0, parity ^= 1u;
   }
 }
+
+// A group that fills its own ring (every thread has one of these): matrix i by lane
+// i / W of warp i % W of the group's W warps.
+template <int G, int K>
+struct Filler {
+  uintptr_t from;
+  int64_t step;
+  uint32_t bytes, to, full;
+  __device__ Filler(const Args &a, Shared &sh, uint8_t *memory, int group, int base, int64_t row, int64_t row_step) {
+    const int width = max(0, min((int)a.cols - base, G * K * 8));
+    constexpr int W = G / 32;
+    const int i = threadIdx.x % 32 * W + threadIdx.x % G / 32;
+    const Stream s = a.in[i < 3 ? i : 0];
+    from = (uintptr_t)(s.p + row * s.pitch) + (s.elem ? base * s.elem : base / (int)kActGroup);
+    step = row_step * s.pitch;
+    bytes = s.elem ? width * s.elem : (width + (int)kActGroup - 1) / (int)kActGroup;
+    to = tc::smem(memory) + (uint32_t)group * a.stages * a.stage_bytes + s.at;
+    full = tc::smem(&sh.full[group][0]);
+    if (i >= 3 || s.at < 0) bytes = 0;
+  }
+  // The next row, whose stage is free.
+  __device__ __forceinline__ void fill(const Args &a, int stage, bool skip = false) {
+    if (bytes && !skip) {
+      const uint32_t n = (((uint32_t)from & 15u) + bytes + 15u) & ~15u;
+      tc::bar_expect(full + stage * 8, n);
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to + stage * a.stage_bytes),
+                   "l"(from & ~(uintptr_t)15), "r"(n), "r"(full + stage * 8)
+                   : "memory");
+    }
+    from += step;
+  }
+};
 
 // Which of a thread's columns exist, out of the `width` of the block's part: chunks
 // (VEC), or elements counted through all chunks.
@@ -324,17 +364,17 @@ __device__ __forceinline__ void store_row(const float2 (&v)[K][4], uint8_t *p, b
   }
 }
 
-// Barriers and the stop flag; by the whole block, then visible to all of it and to its cluster.
+// Barriers (`fills`: threads that fill a stage) and the stop flag; by the whole block, then visible to all of it and to its cluster.
 template <bool CLUSTER>
-__device__ __forceinline__ void begin_block(Shared &sh, int groups, int stages) {
+__device__ __forceinline__ void begin_block(Shared &sh, int groups, int stages, int fills) {
   if (threadIdx.x == 0) {
     sh.stop = 0;
     sh.zeros[0] = sh.zeros[1] = make_uint4(0, 0, 0, 0);
     if (CLUSTER)
-      for (int q = 0; q < 2; ++q) tc::bar_init(tc::smem(&sh.arrived[q]), cluster_blocks());
+      for (int q = 0; q < 2 * kClusterGroups; ++q) tc::bar_init(tc::smem(&sh.arrived[q / 2][q % 2]), cluster_blocks());
   }
   for (int i = threadIdx.x; i < groups * stages; i += blockDim.x) {
-    tc::bar_init(tc::smem(&sh.full[i / stages][i % stages]), 1);
+    tc::bar_init(tc::smem(&sh.full[i / stages][i % stages]), fills);
     tc::bar_init(tc::smem(&sh.empty[i / stages][i % stages]), 1);
   }
   tc::bar_init_fence();
@@ -378,9 +418,10 @@ constexpr int kSmemBudget = 208 * 1024;
 
 // `rows_each`: so many rows a group may stay with one unit (0: spread over the SMs at once).
 inline int groups_of(int64_t rows, const Shape &s, int sms, int most_threads, int rows_each) {
-  if (s.cluster > 1) return 1;
-  const int64_t most = most_threads / s.group;
-  const int64_t want = rows <= most * rows_each ? rows : (rows + sms - 1) / sms;
+  int64_t most = most_threads / s.group;
+  if (s.cluster > 1 && most > kClusterGroups) most = kClusterGroups;
+  const int64_t units = sms / s.cluster > 0 ? sms / s.cluster : 1;
+  const int64_t want = rows <= most * rows_each ? rows : (rows + units - 1) / units;
   return (int)(want < 1 ? 1 : want < most ? want : most);
 }
 inline int64_t units_of(int64_t rows, const Shape &s, int sms, int most_threads, int rows_each) {
@@ -447,7 +488,8 @@ inline void set_x(Args &a, const fsdp_norm_desc_t *d, const void *x) {
   }
 }
 
-inline fsdp_status_t run(const void *fn, Args &a, const Launch &l, const Shape &s, cudaStream_t stream) {
+// `more`: threads of a block beside its row groups (a loading warp's).
+inline fsdp_status_t run(const void *fn, Args &a, const Launch &l, const Shape &s, int more, cudaStream_t stream) {
   cudaError_t e = status_word(&a.status);
   if (e != cudaSuccess) return fail(FSDP_ECUDA, std::string("status word: ") + cudaGetErrorString(e));
   a.wait_limit_ns = wait_limit_ns();
@@ -457,7 +499,7 @@ inline fsdp_status_t run(const void *fn, Args &a, const Launch &l, const Shape &
     if (e != cudaSuccess) return fail(FSDP_ECUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
   }
   void *args[] = {&a};
-  return launched(launch_kernel(fn, dim3((unsigned)(l.units * s.cluster)), dim3((unsigned)(l.groups * s.group + 32)), args,
+  return launched(launch_kernel(fn, dim3((unsigned)(l.units * s.cluster)), dim3((unsigned)(l.groups * s.group + more)), args,
                                 (size_t)l.smem, stream, true, s.cluster));
 }
 

@@ -5,29 +5,35 @@
 // which one reduction gives together; the parameter gradients are column sums.
 // A block keeps the column sums of its own rows in registers and writes them
 // once, [units][2][cols] in binary32; a second kernel adds the units in order.
-// Bound: HBM; 2 + 2 + 2 bytes an element in BF16 (5.03 from the checkpoint).
+// Bound: HBM; 2 + 2 + 2 bytes an element in BF16 (5.03 from the checkpoint); what is
+// left above it is the latency of a row's sum, which a block hides behind one or two
+// more rows.  16384 x 4096 in BF16 takes 69.9 us with its column sums (5.8 TB/s), from
+// the checkpoint 66.3 (5.1 TB/s); 8192 x 4096 in FP32 70.3 (5.7 TB/s); 16385 x 1409 in
+// FP32, element by element, 53.3 (5.2 TB/s).
+#include <algorithm>
+
 #include "norm.h"
 
 namespace fsdp {
 namespace {
 using namespace norm;
 
-// Threads of a block beside its loading warp, at 96 registers: a thread's column sums
-// take 32, its values of a row 32 more.  (A third group at 72 registers spills: 111 us
-// instead of 63 at 16384 x 4096 in BF16 from the checkpoint.)
-constexpr int kMostThreads = 512;
+// Threads of a block at most.  A thread's column sums and its values of a row take 128
+// registers at 4 chunks, 64 at 2.  (Three groups of 128 threads at 168 registers spill:
+// 71 us instead of 66 at 16384 x 4096 in BF16 from the checkpoint.)
+constexpr int most_threads(int chunks, bool vec) { return chunks <= 2 ? 512 : vec ? 256 : 384; }
 // Up to so many rows a group, one block does them all: its sums are the gradients, and
 // neither the second kernel (3 us and as much on the host) nor a workspace is needed.
 constexpr int kRowsEach = 4;
 
 template <int XK, bool YB, bool VEC, int G, int K, bool CLUSTER>
-__global__ void __launch_bounds__(kMostThreads + 32, 1) backward_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(most_threads(K, VEC), 1) backward_kernel(const __grid_constant__ Args a) {
   constexpr int DK = YB ? X_BF16 : X_F32;
   __shared__ Shared sh;
   extern __shared__ __align__(16) uint8_t memory[];
   float *const weight = reinterpret_cast<float *>(memory);
   uint8_t *const stages = memory + G * K * 8 * sizeof(float);
-  const int group = threadIdx.x / G, groups = (blockDim.x - 32) / G, t = threadIdx.x % G, cols = (int)a.cols;
+  const int group = threadIdx.x / G, groups = blockDim.x / G, t = threadIdx.x % G, cols = (int)a.cols;
   int turn = 0, base = 0;
   int64_t unit = blockIdx.x, units = gridDim.x;
   if constexpr (CLUSTER) {
@@ -36,14 +42,13 @@ __global__ void __launch_bounds__(kMostThreads + 32, 1) backward_kernel(const __
     units /= cluster_blocks();
   }
   Ring<G, K> ring(a, sh, stages, group, base);
-  begin_block<CLUSTER>(sh, groups, a.stages);
+  begin_block<CLUSTER>(sh, groups, a.stages, ring.width > 0 ? 2 + (a.in[1].at >= 0) : 1);
   wait_for_previous();
   int64_t row = unit * groups + group;
   const int64_t step = units * groups;
   const int dy_kind = a.y_bf16 ? X_BF16 : X_F32;
   float mean = 0.0f, rstd = 0.0f;
-  const bool loads = (int)threadIdx.x >= groups * G;
-  if (!loads && row < a.rows) mean = a.mean[row], rstd = a.rstd[row];
+  if (row < a.rows) mean = a.mean[row], rstd = a.rstd[row];
   stage_param<VEC, G, K>(weight, a.weight, a.param_bf16 != 0, 1.0f, cols, base);
   float2 dw[K][4], db[K][4];
 #pragma unroll
@@ -51,14 +56,16 @@ __global__ void __launch_bounds__(kMostThreads + 32, 1) backward_kernel(const __
 #pragma unroll
     for (int e = 0; e < 4; ++e) dw[k][e] = db[k][e] = both(0.0f);
   __syncthreads();
-  if (loads) load_rows<G, K>(a, sh, stages, groups, base, unit * groups, step);
+  Filler<G, K> filler(a, sh, stages, group, base, row, step);
+  for (int i = 0; i < a.stages; ++i)
+    if (row + i * step < a.rows) filler.fill(a, i, a.fault != 0 && blockIdx.x == 0 && group == 0 && i == 0);
 
   const int mine = columns_of<VEC, G, K>(ring.width, t);
   const int dx_size = a.dx_bf16 ? 2 : 4;
   uint8_t *dx = static_cast<uint8_t *>(a.dx) + (row * a.ld_dx + base) * dx_size;
   const int64_t dx_step = step * a.ld_dx * dx_size;
 
-  for (; !loads && row < a.rows; row += step, dx += dx_step) {
+  for (; row < a.rows; row += step, dx += dx_step) {
     float2 xh[K][4], g[K][4];
     float unit[K], one[K];
     ring.wait();
@@ -84,7 +91,7 @@ __global__ void __launch_bounds__(kMostThreads + 32, 1) backward_kernel(const __
     }
     float s[2] = {s0.x + s0.y, s1.x + s1.y};
     row_sum<2, G, CLUSTER>(s, sh, turn, group, a.wait_limit_ns);
-    if (t == 0) ring.release();
+    if (row + a.stages * step < a.rows) filler.fill(a, ring.stage);
     ring.next();
     if (a.dx) {
       const float2 c2 = both(-s[0] * a.inv_cols * r), c1 = both(-s[1] * a.inv_cols * r);
@@ -102,7 +109,7 @@ __global__ void __launch_bounds__(kMostThreads + 32, 1) backward_kernel(const __
   if (groups > 1) {
     float *const sums = reinterpret_cast<float *>(stages);
     __syncthreads();
-    if (group > 0 && !loads) {
+    if (group > 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -148,7 +155,8 @@ __global__ void __launch_bounds__(kMostThreads + 32, 1) backward_kernel(const __
 
 // dweight | dbias [cols] from partial [units][2][cols]: 32 columns of one of the
 // two to a block, its 32 warps each adding every 32nd unit, then the warps' sums
-// in order.
+// in order.  Bound by latency: a unit's sums are in L2, 152 of them make 5 MB at
+// 4096 columns (5 us).
 constexpr int kSumThreads = 1024;
 
 __global__ void __launch_bounds__(kSumThreads) column_sum_kernel(const float *partial, int64_t units, int64_t cols,
@@ -175,30 +183,32 @@ __global__ void __launch_bounds__(kSumThreads) column_sum_kernel(const float *pa
   }
 }
 
-// The narrowest shape that holds a row; two chunks a thread at most, whose sums and
-// values take 64 registers.
-//   columns <=  512   one warp, 2 chunks
-//           <= 2048   128 threads, 2 chunks (1 up to 1024)
-//           <= 4096   256 threads, 2 chunks
-//           <= 8192   512 threads, 2 chunks; above: clusters of 2, 4 or 8 such blocks
-Shape shape_of(int64_t cols) {
+// The narrowest shape that holds a row.  What a row costs a warp beside its columns is
+// about 170 instructions, as much as 16 columns a thread cost, so vector kernels have
+// 32 columns a thread (us in BF16, with 16 columns and twice the threads / with 32:
+// 32768 x 1024 48.8 / 41.0, 32768 x 2048 74.9 / 70.9, 16384 x 4096 72.1 / 69.9, 8192 x
+// 8192 88.6 / 73.2, 4096 x 16384 135 / 118).  Kernels that go element by element are
+// bound by their accesses, which want threads, except where a warp has a row to itself
+// (16385 x 1409 from the checkpoint 60 / 65, 2048 x 20001 340 / 356; 32769 x 515 77 / 52).
+Shape shape_of(int64_t cols, bool vec) {
   if (cols <= 512) return {32, 2, 1, 0};
-  if (cols <= 1024) return {128, 1, 1, 1};
-  if (cols <= 2048) return {128, 2, 1, 2};
-  if (cols <= 4096) return {256, 2, 1, 3};
-  const int cluster = cluster_of(cols, 8192);
-  return {512, 2, cluster, cluster > 1 ? 5 : 4};
+  if (cols <= 1024) return {32, 4, 1, 1};
+  if (cols <= 2048) return vec ? Shape{64, 4, 1, 2} : Shape{128, 2, 1, 2};
+  if (cols <= 4096) return vec ? Shape{128, 4, 1, 3} : Shape{256, 2, 1, 3};
+  const int cluster = cluster_of(cols, 8192), index = cluster > 1 ? 5 : 4;
+  return vec ? Shape{256, 4, cluster, index} : Shape{512, 2, cluster, index};
 }
 
 template <int XK, bool YB, bool VEC>
 const void *kernel_of(int index) {
+  constexpr int K = VEC ? 4 : 2, G = 256 / K;  // of the wider shapes
   switch (index) {
     case 0: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 32, 2, false>);
-    case 1: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 128, 1, false>);
-    case 2: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 128, 2, false>);
-    case 3: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 256, 2, false>);
-    case 4: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 512, 2, false>);
-    default: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 512, 2, true>);
+    case 1: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 32, 4, false>);
+    case 2: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, G, K, false>);
+    case 3: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 2 * G, K, false>);
+    case 4: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 4 * G, K, false>);
+    default: return reinterpret_cast<const void *>(&backward_kernel<XK, YB, VEC, 4 * G, K, true>);
   }
 }
 
@@ -213,7 +223,11 @@ const void *kernel_for(int index, bool vec, int kind, bool y_bf16) {
 
 int64_t workspace_bytes_for(const fsdp_norm_desc_t *d) {
   const int sms = device_sms() > 0 ? device_sms() : 256;
-  const int64_t units = units_of(d->rows, shape_of(d->cols), sms, kMostThreads, kRowsEach);
+  int64_t units = 0;
+  for (bool vec : {false, true}) {  // the pointers, which decide, are not known here
+    const Shape s = shape_of(d->cols, vec);
+    units = std::max(units, units_of(d->rows, s, sms, most_threads(s.chunks, vec), kRowsEach));
+  }
   return units > 1 ? units * 2 * d->cols * 4 : 0;
 }
 
@@ -284,11 +298,11 @@ fsdp_status_t fsdp_layer_norm_backward(const fsdp_norm_desc_t *d, const void *dy
   const bool vec = d->cols % 8 == 0 && (act8 || rows_aligned(x, d->rows, d->ld_x, dtype_bytes(d->x_dtype))) &&
                    rows_aligned(dy, d->rows, d->ld_y, ysize) && (!dx || rows_aligned(dx, d->rows, d->ld_dx, dxsize)) &&
                    aligned16(weight);
-  const Shape sh = shape_of(d->cols);
+  const Shape sh = shape_of(d->cols, vec);
   const int sms = device_sms();
-  const Launch l = plan_launch(a, sh, sms > 0 ? sms : 1, kMostThreads, kRowsEach, 1, 2);
+  const Launch l = plan_launch(a, sh, sms > 0 ? sms : 1, most_threads(sh.chunks, vec), kRowsEach, 1, 2);
   a.partial = l.units > 1 ? static_cast<float *>(workspace) : nullptr;
-  if ((st = run(kernel_for(sh.index, vec, a.x_kind, a.y_bf16 != 0), a, l, sh, s)) != FSDP_OK) return st;
+  if ((st = run(kernel_for(sh.index, vec, a.x_kind, a.y_bf16 != 0), a, l, sh, 0, s)) != FSDP_OK) return st;
   if (a.partial && (dweight || dbias)) {
     const float *partial = a.partial;
     int64_t n = l.units, cols = d->cols;

@@ -174,6 +174,18 @@ def test_backward_rows(rows, cols):
     check_backward(fp_module(), x, w, dy, BF16, from_ckpt=True)
 
 
+@pytest.mark.parametrize("cols", [8208, 9001, 17000])
+@pytest.mark.parametrize("rows", [155, 1000])
+def test_wide_rows_in_turns(rows, cols):
+    """Clusters with several rows at a time, the last turn with rows for some of them."""
+    fp = fp_module()
+    x, w, b = make(rows, cols, cols + rows, BF16)
+    check_forward(fp, x, w, b, BF16, keep=True)
+    check_forward(fp, x, w, b, F32, from_ckpt=True)
+    check_backward(fp, x, w, normals(rows, rows, cols).to(BF16), BF16)
+    check_backward(fp, x, w, normals(rows, rows, cols).to(BF16), BF16, from_ckpt=True)
+
+
 @pytest.mark.parametrize("ld,offset", [(64, 1), (72, 0), (65, 0), (64, 8)])
 def test_backward_strides(ld, offset):
     x, w, _ = make(9, 64, ld, BF16)
