@@ -71,6 +71,22 @@ struct Args {
   int64_t ld_kept;
 };
 
+// 2^x and 1 / x of two values, to about 2 ulp, with 0 for a result below 2^-126: one
+// instruction each, where functions that keep such results take four or five.
+constexpr float kLog2E = 1.4426950408889634f;
+__device__ __forceinline__ float2 exp2(float2 x) {
+  float2 y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(x.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(x.y));
+  return y;
+}
+__device__ __forceinline__ float2 inverse(float2 x) {
+  float2 y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(x.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(x.y));
+  return y;
+}
+
 // act(g) and, if SLOPE, act'(g), of two values.
 //   SiLU: g s with s = 1 / (1 + e^-g);  s + g s (1 - s).  For g far below 0 the divisor
 //   overflows to infinity and s is 0, as it should be.
@@ -85,14 +101,13 @@ template <bool SLOPE, int ACT>
 __device__ __forceinline__ void act_of(float2 g, float2 &y, float2 &slope) {
   const float2 one = both(1.0f);
   if constexpr (ACT == SILU) {
-    const float2 s = make_float2(__fdividef(1.0f, 1.0f + __expf(-g.x)), __fdividef(1.0f, 1.0f + __expf(-g.y)));
+    const float2 s = inverse(__fadd2_rn(exp2(__fmul2_rn(g, both(-kLog2E))), one));
     y = __fmul2_rn(g, s);
     if constexpr (SLOPE) slope = __ffma2_rn(y, __fadd2_rn(one, make_float2(-s.x, -s.y)), s);
   } else {
-    const float2 h = __fmul2_rn(__fmul2_rn(g, both(-0.5f)), g);
-    const float2 e = make_float2(__expf(h.x), __expf(h.y));
+    const float2 e = exp2(__fmul2_rn(__fmul2_rn(g, both(-0.5f * kLog2E)), g));
     const float2 x = __ffma2_rn(make_float2(fabsf(g.x), fabsf(g.y)), both(0.36f), one);
-    const float2 t = make_float2(__fdividef(1.0f, x.x), __fdividef(1.0f, x.y));
+    const float2 t = inverse(x);
     float2 p = both(-0.0302381796f);
     p = __ffma2_rn(p, t, both(0.139508076f));
     p = __ffma2_rn(p, t, both(-0.22359911f));
