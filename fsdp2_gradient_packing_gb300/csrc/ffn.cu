@@ -6,6 +6,7 @@
 // weight gradients in one launch.  dg and du pass through the workspace in BF16.
 #include <cuda.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "ffn.h"
@@ -171,49 +172,44 @@ __global__ void __launch_bounds__(kThreads) slope_kernel(const __grid_constant__
 // The parts of split K loops, added in order
 // ---------------------------------------------------------------------------
 struct JoinArgs {
-  const float *partial;   // [splits][rows][cols]
+  const float *partial;   // Args::partial
+  Grid grid;
+  int32_t tile_m, tile_n;
   void *out[2];
   int64_t ld[2];
-  int64_t rows, half, cols;  // rows from `half` on belong to out[1]
-  int32_t splits, bf16, vec;
+  int64_t rows, cols;     // of one output
+  int32_t half;           // row tiles of the first output
+  int32_t bf16, vec;
 };
 
-// Bound: L2, where the parts still are.  VEC columns of a row to a thread.
-template <int VEC>
+// Bound: L2, where the parts still are.  Four columns of a row to a thread; a tile to
+// the blocks of one y.
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ JoinArgs a) {
-  const int64_t part = a.rows * a.cols, per_row = a.cols / VEC, total = a.rows * per_row;
+  const int part = a.tile_m * a.tile_n, i = ((int)blockIdx.x * kThreads + (int)threadIdx.x) * 4;
+  const int2 tile = tile_at(a.grid, a.grid.whole + (int)blockIdx.y);
+  const int second = tile.x >= a.half, r = i / a.tile_n;
+  const int64_t row = (int64_t)(tile.x - second * a.half) * a.tile_m + r;
+  const int64_t col = (int64_t)tile.y * a.tile_n + (i - r * a.tile_n);
   wait_for_previous();
   let_next_start();
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-    int64_t row = (uint64_t)total >> 32 == 0 ? (uint32_t)i / (uint32_t)per_row : i / per_row;
-    const int64_t col = (i - row * per_row) * VEC;
-    const float *p = a.partial + i * VEC;
-    const bool second = row >= a.half;
-    if (second) row -= a.half;
-    const int64_t at = row * a.ld[second] + col;
-    if constexpr (VEC == 4) {
-      float4 v = *reinterpret_cast<const float4 *>(p);
+  if (row >= a.rows || col >= a.cols) return;
+  const float *p = a.partial + (int64_t)blockIdx.y * a.grid.splits * part + i;
+  float4 v = *reinterpret_cast<const float4 *>(p);
 #pragma unroll 4
-      for (int k = 1; k < a.splits; ++k) {
-        const float4 q = *reinterpret_cast<const float4 *>(p + k * part);
-        v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
-      }
-      if (!a.vec) {
-        const float s[4] = {v.x, v.y, v.z, v.w};
+  for (int k = 1; k < a.grid.splits; ++k) {
+    const float4 q = *reinterpret_cast<const float4 *>(p + (int64_t)k * part);
+    v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+  }
+  const int64_t at = row * a.ld[second] + col;
+  if (!a.vec || a.cols - col < 4) {
+    const float s[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) store_any(a.out[second], at + e, a.bf16 != 0, s[e]);
-      } else if (a.bf16) {
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out[second]) + at) =
-            make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
-      } else {
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.out[second]) + at) = v;
-      }
-    } else {
-      float s = p[0];
-#pragma unroll 4
-      for (int k = 1; k < a.splits; ++k) s += p[k * part];
-      store_any(a.out[second], at, a.bf16 != 0, s);
-    }
+    for (int e = 0; e < 4; ++e)
+      if (e < a.cols - col) store_any(a.out[second], at + e, a.bf16 != 0, s[e]);
+  } else if (a.bf16) {
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out[second]) + at) = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
+  } else {
+    *reinterpret_cast<float4 *>(static_cast<float *>(a.out[second]) + at) = v;
   }
 }
 
@@ -224,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 bool pairs(int64_t rows) { return rows > kTileM; }
 int64_t tile_rows(bool pair) { return pair ? 2 * kTileM : kTileM; }
 
-// Row tiles of a band (see unit_at): 4,096 rows.
+// Row tiles of a band (see tile_at): 4,096 rows.
 int32_t band(int64_t tile_m) { return (int32_t)(4096 / tile_m); }
 
 // The gate / up tile: as many features as fill the workers in the fewest, fullest
@@ -245,69 +241,132 @@ GatedTiles gated_tiles(int64_t rows, int64_t f, int64_t d, int sms) {
     if (cost >= best) continue;
     best = cost;
     t.tile_n = (int32_t)(2 * features);
-    t.grid = {(int32_t)m, (int32_t)n, 1, band(tile_rows(t.pair)), (int32_t)blocks_of(d, kTileK)};
+    t.grid = {(int32_t)m, (int32_t)n, 0, 1, band(tile_rows(t.pair)), (int32_t)blocks_of(d, kTileK)};
   }
   return t;
 }
 
 // The backward products: tiles of 256 columns, or fewer where those would be mostly
-// empty.  K loops are split where that shortens the longest worker's share.  Costs are
-// in hundredths of a K block of a full tile (which takes a pair about 0.33 us): a
-// narrower tile's K block costs less, though not in proportion, for A is the same; a
-// unit its K blocks, but an epilogue at least; joining parts a launch and the parts'
-// bytes, written and read, at about 1.3 MB a K block.  A call that wants only some of
-// the gradients splits as if it wanted all.
+// empty.  K loops are split where that shortens the longest worker's share: those of all
+// tiles of a product, or of the tiles that are left after whole rounds (8192 x 1024 x
+// 4096: 256 tiles of 128 K blocks on 76 workers; three rounds and 28 tiles in two parts
+// each).  Costs are in hundredths of a K block of a full tile (which takes a pair about
+// 0.33 us): a narrower tile's K block costs less, though not in proportion, for A is the
+// same; a unit its K blocks, but an epilogue at least; joining parts a launch and the
+// parts' bytes, at about 1.5 MB a K block.  The weight gradients come first unless the
+// other order saves a twentieth: their operands wait in L2, dx reads the weights from HBM
+// (2048 x 2048 x 6144 took 144 us with dx first, 140 with it last, for all that the
+// shares were 337 and 358 K blocks).  A call that wants only some of the gradients splits
+// as if it wanted all.
 struct BackwardTiles {
   bool pair;
-  int32_t tile_n;
+  int32_t tile_n, first, head;  // as in Args
   Grid grid[2];       // weight gradients, dx
   int64_t half[2];    // tiles of one weight's rows; K blocks of one half of dx
 };
-BackwardTiles backward_tiles(int64_t rows, int64_t d, int64_t f, int sms) {
+
+// A product's units in a plan: `whole` of cost `cost`, then `parts` of cost `part`.
+struct Units {
+  int64_t whole, parts, cost, part;
+  int64_t all() const { return whole + parts; }
+  int64_t longest() const { return whole > 0 ? cost : part; }
+};
+// The longest share of a worker (see Walk, whose steps this follows).
+int64_t longest_share(const Units &a, const Units &b, int64_t head, int64_t workers) {
+  const int64_t rem = a.all() % workers, others = workers - rem;
+  auto count = [](int64_t from, int64_t step, int64_t below) { return from < below ? (below - from + step - 1) / step : 0; };
+  // Shares change at few workers: where the long units end, and where the rounds of the
+  // others' whole units and parts end.
+  const int64_t rest = head * others;
+  const int64_t ends[] = {0, rem, a.whole % workers, (b.whole > rest ? b.whole - rest : 0) % workers,
+                          (b.all() > rest ? b.all() - rest : 0) % workers};
+  int64_t longest = 0;
+  for (int64_t w : ends) {
+    const int64_t wholes = count(w, workers, a.whole), mine = count(w, workers, a.all());
+    int64_t share = wholes * a.cost + (mine - wholes) * a.part, got[2];
+    const int64_t below[2] = {b.whole, b.all()};
+    for (int i = 0; i < 2; ++i) {
+      got[i] = count(rest + w, workers, below[i]);
+      if (w >= rem) got[i] += std::min(head, count(w - rem, others, below[i]));
+    }
+    share += got[0] * b.cost + (got[1] - got[0]) * b.part;
+    longest = std::max(longest, share);
+  }
+  return longest;
+}
+
+BackwardTiles find_backward_tiles(int64_t rows, int64_t d, int64_t f, int sms) {
   BackwardTiles t = {};
   t.pair = pairs(rows);
   const int64_t tile_m = tile_rows(t.pair), workers = t.pair ? sms / 2 : sms;
   t.half[0] = blocks_of(f, tile_m), t.half[1] = blocks_of(f, kTileK);
   const int64_t m[2] = {2 * t.half[0], blocks_of(rows, tile_m)};
   const int64_t k[2] = {blocks_of(rows, kTileK), 2 * t.half[1]};
-  const int64_t bytes[2] = {2 * f * d * 4, rows * d * 4};  // of one part
   constexpr int kChoices = 8;
   const int64_t by[kChoices] = {1, 2, 3, 4, 6, 8, 12, 16};
   int64_t best = INT64_MAX;
   for (int64_t width = 256; width >= (t.pair ? 128 : 64); width /= 2) {
-    const int64_t n = blocks_of(d, width), block = width == 256 ? 100 : width == 128 ? 65 : 50;
-    const int choices = (m[0] + m[1]) * n > 8 * workers ? 1 : kChoices;
-    // Cost of a unit, units, and cost of the join for each choice.
-    int64_t cost[2][kChoices], units[2][kChoices], join[2][kChoices];
-    for (int w = 0; w < 2; ++w)
-      for (int c = 0; c < choices; ++c) {
-        const int64_t per = blocks_of(k[w], by[c]);
-        cost[w][c] = (per > 10 ? per : 10) * block + 100;
-        units[w][c] = m[w] * n * by[c];
-        join[w][c] = c == 0 ? 0 : 1500 + by[c] * bytes[w] / 6500;
-        if (c > 0 && (per < 4 || blocks_of(k[w], per) != by[c])) units[w][c] = 0;  // parts too short, or empty ones
-      }
-    for (int p = 0; p < choices; ++p)
-      for (int q = 0; q < choices; ++q) {
-        const int64_t u0 = units[0][p], u = u0 + units[1][q];
-        if (u0 == 0 || u == u0) continue;
-        // Worker i takes units i, i + workers, ...: shares change at three workers only.
-        const int64_t at[3] = {0, u0 % workers, u % workers};
-        int64_t longest = 0;
-        for (int64_t i : at) {
-          const int64_t first = (u0 - i + workers - 1) / workers, all = (u - i + workers - 1) / workers;
-          const int64_t share = first * cost[0][p] + (all - first) * cost[1][q];
-          longest = share > longest ? share : longest;
-        }
-        const int64_t total = longest + join[0][p] + join[1][q];
-        if (total >= best) continue;
-        best = total;
-        t.tile_n = (int32_t)width;
-        t.grid[0] = {(int32_t)m[0], (int32_t)n, (int32_t)by[p], band(tile_m), (int32_t)k[0]};
-        t.grid[1] = {(int32_t)m[1], (int32_t)n, (int32_t)by[q], band(tile_m), (int32_t)k[1]};
+    const int64_t n = blocks_of(d, width), block = width == 256 ? 100 : width == 128 ? 80 : 65;
+    auto cost = [&](int64_t blocks) { return std::max<int64_t>(blocks, 10) * block + 100; };
+    auto join = [&](int64_t parts) { return parts == 0 ? 0 : 900 + parts * (tile_m * width * 4) / 15000; };
+    // Product w with its tiles from `whole` on in by[c] parts; none where parts would be too short, or empty.
+    auto units = [&](int w, int64_t whole, int c) {
+      const int64_t per = blocks_of(k[w], by[c]), tiles = m[w] * n;
+      if (c == 0) return Units{tiles, 0, cost(k[w]), 0};
+      if (per < 4 || blocks_of(k[w], per) != by[c]) return Units{};
+      return Units{whole, (tiles - whole) * by[c], cost(k[w]), cost(per)};
+    };
+    const bool many = (m[0] + m[1]) * n > 8 * workers;
+    for (int p = 0; p < kChoices; ++p)
+      for (int q = 0; q < kChoices; ++q) {
+        // All of a product's tiles in parts, then (leaving the first product's whole) those left after whole rounds.
+        for (int left = 0; left < (p == 0 && q > 0 ? 2 : 1); ++left)
+          for (int first = 0; first < 2; ++first) {
+            if (many && (p > 0 || (q > 0 && !left))) continue;
+            const int second = first ^ 1;
+            const Units a = units(first, 0, p), one = units(second, 0, 0);
+            const int64_t other = left || q == 0 ? one.cost : units(second, 0, q).part;
+            if (a.all() == 0 || other == 0 || (first == 1 && a.longest() < other)) continue;
+            const int64_t others = workers - a.all() % workers, ratio = std::max<int64_t>(1, a.longest() / other);
+            for (int64_t head = ratio; head <= ratio + 1; ++head) {
+              int64_t whole = 0;
+              if (left) {
+                if (one.whole < head * others) continue;
+                whole = head * others + (one.whole - head * others) / workers * workers;
+              }
+              const Units b = units(second, whole, q);
+              if (b.all() == 0 || (left && b.parts == 0)) continue;
+              int64_t total = longest_share(a, b, head, workers) + join(a.parts) + join(b.parts);
+              if (first == 1) total += total / 20;
+              if (total >= best) continue;
+              best = total;
+              t.tile_n = (int32_t)width, t.first = first, t.head = (int32_t)head;
+              for (int w = 0; w < 2; ++w) {
+                const Units &u = w == first ? a : b;
+                t.grid[w] = {(int32_t)m[w], (int32_t)n, (int32_t)u.whole, (int32_t)by[w == first ? p : q], band(tile_m), (int32_t)k[w]};
+              }
+            }
+          }
       }
   }
   return t;
+}
+
+// A thread's last plans: a program has few sizes, and finding one takes longer than a launch.
+BackwardTiles backward_tiles(int64_t rows, int64_t d, int64_t f, int sms) {
+  struct Found {
+    int64_t rows, d, f;
+    int sms;
+    BackwardTiles tiles;
+  };
+  constexpr int kFound = 8;
+  static thread_local Found found[kFound] = {};
+  static thread_local int next = 0;
+  for (const Found &e : found)
+    if (e.rows == rows && e.d == d && e.f == f && e.sms == sms) return e.tiles;
+  Found &e = found[next++ % kFound];
+  e = {rows, d, f, sms, find_backward_tiles(rows, d, f, sms)};
+  return e.tiles;
 }
 
 struct Plan {
@@ -341,10 +400,9 @@ Plan plan_of(const fsdp_ffn_desc_t *d, bool backward) {
     p.at_dg = take(true, d->rows * p.f_pitch * 2);
     p.at_du = take(true, d->rows * p.f_pitch * 2);
     p.tiles = backward_tiles(d->rows, d->d, d->f, p.sms);
-    const int64_t rows[2] = {2 * d->f, d->rows};
     for (int w = 0; w < 2; ++w) {
-      const int64_t parts = p.tiles.grid[w].splits;
-      p.at_partial[w] = take(parts > 1, parts * rows[w] * d->d * 4);
+      const int64_t parts = units_of(p.tiles.grid[w]) - p.tiles.grid[w].whole;
+      p.at_partial[w] = take(parts > 0, parts * tile_rows(p.tiles.pair) * p.tiles.tile_n * 4);
     }
   }
   p.bytes = at;
@@ -475,22 +533,21 @@ struct Call {
     return launch(mode, t.pair, a);
   }
 
-  // Adds up the parts of product w, if its K loops are split.
+  // Adds up the parts of product w, if there are any.
   fsdp_status_t join(const Args &a, int w) {
-    if (a.grid[w].splits == 1) return FSDP_OK;
+    const Grid &g = a.grid[w];
+    if (units_of(g) == g.whole) return FSDP_OK;
     JoinArgs j = {};
-    j.partial = a.partial[w];
+    j.partial = a.partial[w], j.grid = g;
+    j.tile_m = (int32_t)tile_rows(plan.tiles.pair), j.tile_n = a.tile_n;
     for (int i = 0; i < 2; ++i) j.out[i] = a.out[w == 1 ? 2 : i], j.ld[i] = a.ld_out[w == 1 ? 2 : i];
-    j.rows = w == 0 ? 2 * a.m[0] : a.m[1], j.half = a.m[w], j.cols = a.n;
-    j.splits = a.grid[w].splits, j.bf16 = a.out_bf16[w];
-    j.vec = a.out_width[w] >= 16;
+    j.rows = a.m[w], j.cols = a.n;
+    j.half = w == 0 ? a.half[0] : g.m;
+    j.bf16 = a.out_bf16[w], j.vec = a.out_width[w] >= 16;
     void *args[] = {&j};
-    const int vec = a.n % 4 == 0 ? 4 : 1;
-    int64_t grid = blocks_of(j.rows * (a.n / vec), kThreads);
-    if (grid > plan.sms * 64) grid = plan.sms * 64;
-    return launched(launch_kernel(vec == 4 ? reinterpret_cast<const void *>(&join_kernel<4>)
-                                           : reinterpret_cast<const void *>(&join_kernel<1>),
-                                  dim3((unsigned)grid), dim3(kThreads), args, 0, stream, true));
+    return launched(launch_kernel(reinterpret_cast<const void *>(&join_kernel),
+                                  dim3((unsigned)(j.tile_m * j.tile_n / (4 * kThreads)), (unsigned)(g.m * g.n - g.whole)),
+                                  dim3(kThreads), args, 0, stream, true));
   }
 };
 
@@ -645,12 +702,12 @@ fsdp_status_t fsdp_gated_ffn_backward(const fsdp_ffn_desc_t *d, const void *dh, 
   a.out_width[0] = rg < ru ? rg : ru, a.out_width[1] = row_width(dx, d->rows, d->ld_dx, xsize);
   for (int w = 0; w < 2; ++w) {
     a.grid[w] = t.grid[w], a.half[w] = (int32_t)t.half[w];
-    if (t.grid[w].splits == 1) continue;
     a.partial[w] = reinterpret_cast<float *>(c.ws + c.plan.at_partial[w]);
-    a.partial_width[w] = row_width(a.partial[w], 2, d->d, 4);
   }
-  if (!dw_gate) a.grid[0].m = 0;  // no tiles
-  if (!dx) a.grid[1].m = 0;
+  a.partial_width = row_width(c.ws, 2, t.tile_n, 4);
+  a.first = t.first, a.head = t.head;
+  if (!dw_gate) a.grid[0].m = a.grid[0].whole = 0;  // no tiles
+  if (!dx) a.grid[1].m = a.grid[1].whole = 0;
   if ((st = c.launch(BACKWARD, t.pair, a)) != FSDP_OK) return st;
   for (int w = 0; w < 2; ++w)
     if (a.grid[w].m > 0 && (st = c.join(a, w)) != FSDP_OK) return st;

@@ -32,12 +32,23 @@ constexpr int kTileM = 128;  // rows of a block's tile (TMEM lanes)
 constexpr int kTileK = 64;   // K values of a stage: one 128-byte swizzled row
 constexpr uint32_t kStatusGemm = 16u;  // a wait of this kernel gave up
 
-// The tiles of one product: m x n of them, each K loop in `splits` parts.
+// The tiles of one product, m x n of them.  In the order of tile_at, the first `whole`
+// are units of work; the K loops of the others are in `splits` parts, each of them a unit.
 struct Grid {
-  int32_t m, n, splits;
-  int32_t raster;    // row tiles of a band (see unit_at)
+  int32_t m, n, whole, splits;
+  int32_t raster;    // row tiles of a band (see tile_at)
   int32_t k_blocks;  // of the whole K loop
 };
+
+__host__ __device__ __forceinline__ int units_of(const Grid &g) { return g.whole + (g.m * g.n - g.whole) * g.splits; }
+
+// Down a band of `raster` row tiles, then to the next column tile, so that the tiles at
+// work at one time share few operand slices, which stay in L2.
+__device__ __forceinline__ int2 tile_at(const Grid &g, int t) {
+  const int band = g.raster * g.n, b = t / band, first = b * g.raster;
+  const int height = min(g.m - first, g.raster), r = t - b * band;
+  return make_int2(first + r % height, r / height);
+}
 
 struct Args {
   CUtensorMap a[2];   // FORWARD, RECOMPUTE: x; BACKWARD: dg, du
@@ -48,6 +59,7 @@ struct Args {
   int32_t act;        // Act
   int32_t turns;      // some rows go through the epilogue warps' buffers
   Grid grid[2];       // BACKWARD: weight gradients, dx; else the first only
+  int32_t first, head;  // BACKWARD: whose units come first; see Walk
   int32_t a_rows;     // FORWARD, RECOMPUTE: rows of an x box (see gated())
   int32_t tile_n;     // accumulator columns of a tile (FORWARD, RECOMPUTE: half of them gate;
                       // BACKWARD: 64, 128 or 256)
@@ -57,8 +69,8 @@ struct Args {
   void *out[3];       // FORWARD: h; RECOMPUTE: dg, du; BACKWARD: dWg, dWu, dx
   int64_t ld_out[3];
   int32_t out_bf16[2], out_width[2];  // dtype and row_width(), by product
-  float *partial[2];  // by product, splits > 1: [splits][m (weight gradients: 2 m)][n] in binary32 instead of out
-  int32_t partial_width[2];
+  float *partial[2];  // by product: [tiles with parts][splits][tile rows][tile columns] in binary32
+  int32_t partial_width;  // row_width()
   const void *dh;     // RECOMPUTE
   int64_t ld_dh;
   int32_t dh_vec;

@@ -41,57 +41,93 @@ struct Shared {
   uint32_t tmem, stop, filled;
 };
 
-// A unit of work: one tile and one part of its K loop.
+// A unit of work: one tile, or one part of its K loop.
 struct Unit {
   int which;           // of Args::grid
-  int m, n, split;     // tile indices
+  int m, n;            // tile indices
+  int part;            // place among the product's parts; -1: a whole tile
   int k0, k1;          // K blocks
 };
 
-__device__ __forceinline__ int units_of(const Grid &g) { return g.m * g.n * g.splits; }
+// The units of one worker.  The units of the product with the longer ones come first,
+// every W-th of them to a worker.  What is left over, `rem` units, makes the first `rem`
+// workers one long unit later than the others, which therefore go `head` rounds of the
+// short ones ahead (as many as a long one takes); then all go on together.  Workers at
+// work at one time have units side by side throughout, which share operands in L2.
+// (4096 x 1024 x 4096: 64 units of 128 K blocks and 128 of 64 for 76 workers, of which 12
+// go two short units ahead.)
+template <int MODE>
+struct Walk {
+  int i, end, step;
+  int first, others, ahead, late;
+
+  __device__ Walk(const Args &a, int worker, int workers) : i(worker), step(workers) {
+    end = first = units_of(a.grid[MODE == BACKWARD ? a.first : 0]);
+    if constexpr (MODE == BACKWARD) {
+      end += units_of(a.grid[a.first ^ 1]);
+      const int rem = first % workers;
+      others = workers - rem;
+      ahead = worker >= rem ? a.head - 1 : 0;
+      late = worker < rem ? (a.head - 1) * others : 0;
+    }
+  }
+  __device__ __forceinline__ bool more() const { return i < end; }
+  __device__ __forceinline__ void next() {
+    if (MODE == BACKWARD && i >= first && ahead > 0) {
+      i += others, --ahead;
+    } else {
+      const bool was = i < first;
+      i += step;
+      if (MODE == BACKWARD && was && i >= first) i += late;
+    }
+  }
+};
+
+// Unit i as the product it belongs to and its place there.
+template <int MODE>
+__device__ __forceinline__ int product_of(const Args &a, int &i) {
+  if constexpr (MODE != BACKWARD) return 0;
+  const int units = units_of(a.grid[a.first]);
+  if (i < units) return a.first;
+  i -= units;
+  return a.first ^ 1;
+}
 
 // The K blocks of unit i, all that issuing its MMAs takes: worked out by one thread while
 // the tensor cores run dry, so without the divisions that find the tile.
 struct Span {
   int which, k0, k1;
 };
+__device__ __forceinline__ void part_of(const Grid &g, int split, int &k0, int &k1) {
+  const int per = (g.k_blocks + g.splits - 1) / g.splits;
+  k0 = min(split * per, g.k_blocks);
+  k1 = min(k0 + per, g.k_blocks);
+}
 template <int MODE>
 __device__ __forceinline__ Span span_at(const Args &a, int i) {
-  Span s = {0, 0, a.grid[0].k_blocks};
-  if constexpr (MODE == BACKWARD) {
-    const int first = units_of(a.grid[0]);
-    if (i >= first) s.which = 1, i -= first;
-    const Grid &g = a.grid[s.which];
-    s.k1 = g.k_blocks;
-    if (g.splits > 1) {
-      const int per = (g.k_blocks + g.splits - 1) / g.splits;
-      s.k0 = min(i % g.splits * per, g.k_blocks);
-      s.k1 = min(s.k0 + per, g.k_blocks);
-    }
-  }
+  Span s;
+  s.which = product_of<MODE>(a, i);
+  const Grid &g = a.grid[s.which];
+  s.k0 = 0, s.k1 = g.k_blocks;
+  if (MODE == BACKWARD && i >= g.whole) part_of(g, (i - g.whole) % g.splits, s.k0, s.k1);
   return s;
 }
 
 template <int MODE>
 __device__ __forceinline__ Unit unit_at(const Args &a, int i) {
   Unit u;
-  u.which = 0;
-  if constexpr (MODE == BACKWARD) {
-    const int first = units_of(a.grid[0]);
-    if (i >= first) u.which = 1, i -= first;
-  }
+  u.which = product_of<MODE>(a, i);
   const Grid &g = a.grid[u.which];
-  u.split = i % g.splits;
-  const int t = i / g.splits;
-  // Down a band of `raster` row tiles, then to the next column tile, so that the
-  // tiles at work at one time share few operand slices, which stay in L2.
-  const int band = g.raster * g.n, b = t / band, first = b * g.raster;
-  const int height = min(g.m - first, g.raster), r = t - b * band;
-  u.m = first + r % height;
-  u.n = r / height;
-  const int per = (g.k_blocks + g.splits - 1) / g.splits;
-  u.k0 = min(u.split * per, g.k_blocks);
-  u.k1 = min(u.k0 + per, g.k_blocks);
+  u.part = -1;
+  u.k0 = 0, u.k1 = g.k_blocks;
+  int t = i;
+  if (MODE == BACKWARD && i >= g.whole) {
+    u.part = i - g.whole;
+    t = g.whole + u.part / g.splits;
+    part_of(g, u.part % g.splits, u.k0, u.k1);
+  }
+  const int2 at = tile_at(g, t);
+  u.m = at.x, u.n = at.y;
   return u;
 }
 
@@ -346,7 +382,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   const uint32_t stages = (tc::smem(dynamic) + 1023u) & ~1023u;
   const int rank = CG == 1 ? 0 : (int)tc::cluster_rank();
   const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
-  const int units = units_of(a.grid[0]) + (MODE == BACKWARD ? units_of(a.grid[1]) : 0);
   volatile uint32_t *stop = &sh.stop;
 
   if (warp == 0 && lane == 0) {
@@ -385,8 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const uint32_t leader = CG == 1 ? full : tc::at_rank(full, 0);
       const bool skip = skips_first(a, worker);
       const int half = MODE == BACKWARD ? a.half[1] : 0;
-      for (int i = worker; i < units && ok; i += workers) {
-        const Unit u = unit_at<MODE>(a, i);
+      for (Walk<MODE> walk(a, worker, workers); walk.more() && ok; walk.next()) {
+        const Unit u = unit_at<MODE>(a, walk.i);
         Loader<MODE, CG, COLS> from(a, u, rank);
         const int k0 = u.k0, k1 = u.k1, which = u.which;
         for (int kb = k0; kb < k1; ++kb) {
@@ -415,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool issued = false;
       const uint32_t full = tc::smem(&sh.full[0]), empty = tc::smem(&sh.empty[0]);
-      for (int i = worker; i < units && ok; i += workers) {
-        const Span u = span_at<MODE>(a, i);
+      for (Walk<MODE> walk(a, worker, workers); walk.more() && ok; walk.next()) {
+        const Span u = span_at<MODE>(a, walk.i);
         if (!(ok = tc::bar_wait(tc::smem(&sh.tmem_empty[acc]), acc_phase ^ 1u, a.wait_limit_ns, stop))) break;
         tc::fence_after();
         const uint32_t d = tmem + acc * kTileN;
@@ -460,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     float *const turn = reinterpret_cast<float *>(dynamic + kDynamic - kEpilogueWarps * kTurnBytes) +
                         (warp - 2) * (kTurnBytes / 4);
     uint32_t acc = 0, acc_phase = 0;
-    for (int i = worker; i < units; i += workers) {
-      const Unit u = unit_at<MODE>(a, i);
+    for (Walk<MODE> walk(a, worker, workers); walk.more(); walk.next()) {
+      const Unit u = unit_at<MODE>(a, walk.i);
       if (!(ok = tc::bar_wait(tc::smem(&sh.tmem_full[acc]), acc_phase, a.wait_limit_ns, stop))) break;
       tc::fence_after();
       const uint32_t from = tmem + acc * kTileN + ((uint32_t)quarter * 32u << 16);
@@ -512,9 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
               for (int e = 0; e < 32; ++e) r[e] = 0u;
             }
-            if (a.grid[which].splits > 1) {
-              const int64_t all = which == 0 ? 2 * m : m;
-              store_part(a.partial[which] + ((int64_t)u.split * all + up * m) * a.n, a.n, false, a.partial_width[which], r, q);
+            if (u.part >= 0) {
+              const Part in = {c * 32, 32, q.rows, rank * kTileM + quarter * 32 + lane, turn};
+              store_part(a.partial[which] + (int64_t)u.part * (kTileM * CG * COLS), COLS, false, a.partial_width, r, in);
             } else {
               store_part(a.out[to], a.ld_out[to], a.out_bf16[which] != 0, a.out_width[which], r, q);
             }
@@ -543,16 +578,16 @@ cudaError_t launch(Args &a, int sms, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynamic);
   if (e != cudaSuccess) return e;
   int64_t units = 0;
-  for (int w = 0; w < (MODE == BACKWARD ? 2 : 1); ++w) units += (int64_t)a.grid[w].m * a.grid[w].n * a.grid[w].splits;
+  for (int w = 0; w < (MODE == BACKWARD ? 2 : 1); ++w) units += units_of(a.grid[w]);
   int64_t workers = sms / CG;
   if (workers > units) workers = units;
   // Rows through the warps' buffers: those that no vector fits, and a row's last columns.
   auto odd = [](int width) { return width < 16; };
-  a.turns = a.n % 32 != 0;
   if (MODE == BACKWARD) {
-    for (int w = 0; w < 2; ++w) a.turns |= a.grid[w].m > 0 && odd(a.grid[w].splits > 1 ? a.partial_width[w] : a.out_width[w]);
+    a.turns = 0;
+    for (int w = 0; w < 2; ++w) a.turns |= a.grid[w].whole > 0 && (a.n % 32 != 0 || odd(a.out_width[w]));
   } else {
-    a.turns |= odd(a.out_width[0]) || (MODE == FORWARD && KEEP == 2 && odd(a.keep_width)) || (MODE == RECOMPUTE && !a.dh_vec);
+    a.turns = a.n % 32 != 0 || odd(a.out_width[0]) || (MODE == FORWARD && KEEP == 2 && odd(a.keep_width)) || (MODE == RECOMPUTE && !a.dh_vec);
   }
   void *args[] = {&a};
   return launch_kernel(fn, dim3((unsigned)(workers * CG)), dim3(kThreads), args, kDynamic, stream, true, CG);

@@ -161,6 +161,14 @@ def test_long_sums(rows, d, f):
     check_backward(fp_module(), Block(rows, d, f, 5), "silu", "act8", dx_dtype=F32, dw_dtype=F32)
 
 
+@pytest.mark.parametrize("rows,d,f,want", [(3000, 1000, 6000, (True, True)), (4999, 1001, 2500, (True, True)),
+                                           (700, 2000, 1500, (True, True)), (3000, 1000, 6000, (True, False)),
+                                           (3000, 1000, 6000, (False, True))])
+def test_uneven_shares(rows, d, f, want):
+    """Tiles of two lengths that come out in no whole rounds: some workers go ahead, the last tiles are in parts."""
+    check_backward(fp_module(), Block(rows, d, f, rows), "silu", "none", want=want)
+
+
 @pytest.mark.parametrize("want", [(True, False), (False, True), (False, False)])
 def test_parts(want):
     check_backward(fp_module(), Block(100, 96, 200, 1), "gelu", "none", want=want)
