@@ -102,14 +102,17 @@ __device__ __forceinline__ uint32_t act8_code(float x, uint32_t s) {
 // Bits of the largest magnitude, a NaN's where there is one.
 template <int PAIRS>
 __device__ __forceinline__ uint32_t act8_top(const float2 (&v)[PAIRS]) {
-  float top = 0.0f;
+  constexpr int kChains = PAIRS < 4 ? 1 : PAIRS < 16 ? 2 : 4;  // side by side, each step waits for the one before
+  float top[kChains] = {};
 #pragma unroll
   for (int i = 0; i < PAIRS; ++i) {
     float r;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(top), "f"(fabsf(v[i].x)), "f"(fabsf(v[i].y)));
-    top = r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(top[i % kChains]), "f"(fabsf(v[i].x)), "f"(fabsf(v[i].y)));
+    top[i % kChains] = r;
   }
-  return __float_as_uint(top);
+#pragma unroll
+  for (int i = 1; i < kChains; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top[0]) : "f"(top[i]));
+  return __float_as_uint(top[0]);
 }
 
 // Codes of a word, made unsigned once for act8_value: code + 128 in each byte.

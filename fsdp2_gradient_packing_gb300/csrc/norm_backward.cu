@@ -19,8 +19,9 @@ namespace {
 using namespace norm;
 
 // Threads of a block at most.  A thread's column sums and its values of a row take 128
-// registers at 4 chunks, 64 at 2.  (Three groups of 128 threads at 168 registers spill:
-// 71 us instead of 66 at 16384 x 4096 in BF16 from the checkpoint.)
+// registers at 4 chunks, 64 at 2.  (A third group of 128 threads leaves 168 registers and
+// spills: 16384 x 4096 takes 91 us from BF16 with it, 70 without; the smallest kernel, from
+// the checkpoint, 64.6 and 66.3, but 32768 x 1024 43 and 39.)
 constexpr int most_threads(int chunks, bool vec) { return chunks <= 2 ? 512 : vec ? 256 : 384; }
 // Up to so many rows a group, one block does them all: its sums are the gradients, and
 // neither the second kernel (3 us and as much on the host) nor a workspace is needed.
