@@ -2,9 +2,8 @@
 //
 // Both directions move bytes and do a handful of operations per element, so the
 // bound is HBM: 2 + 33/32 bytes per BF16 element, 4 + 33/32 per FP32 element.  8192 x
-// 12288 in BF16 is stored in 45 us and loaded in 46 (6.7 TB/s each way, a plain copy's
-// rate); a first form without pairs was bound by what it issued, at 58 us.  4099 x 1411
-// to FP32, element by element, is loaded in about 9 us (3.2 TB/s).
+// 12288 in BF16 is stored in 46 us and loaded in 47 (6.6 and 6.5 TB/s, a plain copy's
+// rate); 4099 x 1411 in FP32, element by element, in 11.8 and 9.1 (2.5 and 3.2 TB/s).
 // A thread holds one 16-byte vector of the matrix (8 BF16 or 4 FP32 elements),
 // so a group of 32 is 4 or 8 neighbouring lanes and its maximum 2 or 3
 // shuffles; each thread has kUnroll vectors in flight.  Rows that no vector

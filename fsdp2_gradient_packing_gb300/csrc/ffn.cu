@@ -117,8 +117,10 @@ struct SlopeArgs {
   int32_t dh_vec, kept_vec;
 };
 
-// Bound: HBM, 2 + 33/16 + 4 bytes an element from 8-bit checkpoints.  Eight columns
-// make a unit; a thread has kUnits of them in flight.
+// Bound: HBM, 2 + 33/16 + 4 bytes an element from 8-bit checkpoints; 8192 x 1408 takes 17
+// us from a cold start (5.5 TB/s).  Eight columns make a unit; a thread has kUnits of them
+// in flight.  (Sixteen columns at once by whole sectors: the whole backward call 1 %
+// faster from the checkpoint, 3 % slower from BF16 and for ragged rows.)
 constexpr int kUnits = 2;
 
 template <int ACT, bool ACT8>
@@ -196,8 +198,8 @@ struct JoinArgs {
   int32_t bf16, vec;
 };
 
-// Bound: L2, where the parts still are.  Four columns of a row to a thread; a tile to
-// the blocks of one y.
+// Bound: L2, where the parts still are: 72 parts of 256 x 256 take 7 us.  Four columns of
+// a row to a thread; a tile to the blocks of one y.
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ JoinArgs a) {
   const int part = a.tile_m * a.tile_n, i = ((int)blockIdx.x * kThreads + (int)threadIdx.x) * 4;
   const int2 tile = tile_at(a.grid, a.grid.whole + (int)blockIdx.y);

@@ -5,6 +5,8 @@
 // 4 d f bytes of weights.  A warp reads whole rows of both weights, 512 bytes of
 // each of 8 rows (4 features, gate and up) in flight at a time, which streams better
 // than the tile path's 128-byte pieces of many rows (few_rows() has both sides).
+// One row through 4096 x 12288 takes 31 us: 201 MB at 6.4 TB/s, 94 % of a plain copy's
+// rate.  (A second set of weights in flight spills: 44 us.)
 #include "ffn.h"
 
 namespace fsdp {
