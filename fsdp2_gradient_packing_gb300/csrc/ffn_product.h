@@ -238,25 +238,53 @@ __device__ __forceinline__ void store_turned(void *p, int64_t ld, bool bf16, con
   }
 }
 
+// 64 bytes of each row, from a row to a thread, as two threads to a row: neighbours
+// exchange halves and store first the even one's row, then the odd one's, so that a row's
+// two sectors leave together (forward 8192 x 1024 x 4096 80 and 78.5 us, with 8-bit copies
+// 98 and 95.5).  `row`: this thread's; `pitch`: bytes.
+__device__ __forceinline__ void store_pairs(void *row, int64_t pitch, const uint32_t (&w)[16], int rows) {
+  const int lane = threadIdx.x & 31;
+  const bool odd = lane & 1;
+  uint32_t a[8], b[8];  // for the even row, the odd row
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[i] : w[8 + i], 1);
+    a[i] = odd ? other : w[i];
+    b[i] = odd ? w[8 + i] : other;
+  }
+  uint8_t *const even = static_cast<uint8_t *>(row) - (odd ? pitch - 32 : 0);
+  if ((lane & ~1) < rows) store32(even, a);
+  if ((lane | 1) < rows) store32(even + pitch, b);
+}
+
 // Binary32 values (as bits), or BF16 pairs, in memory.
 __device__ __forceinline__ void store_part(void *p, int64_t ld, bool bf16, int width, const uint32_t (&v)[32], const Part &q) {
   if (!whole(width, q))
     return store_turned(p, ld, bf16, q, [&](int e) { return __uint_as_float(v[e]); });
-  if ((int)(threadIdx.x & 31) >= q.rows) return;
   const int64_t at = q.row * ld + q.col;
   if (bf16) {
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = bf16_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-    store_words(static_cast<uint16_t *>(p) + at, width, w);
-  } else {
+    if (width == 32)
+      store_pairs(static_cast<uint16_t *>(p) + at, ld * 2, w, q.rows);
+    else if ((int)(threadIdx.x & 31) < q.rows)
+      store_words(static_cast<uint16_t *>(p) + at, width, w);
+  } else if (width == 32) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+      store_pairs(static_cast<float *>(p) + at + 16 * half, ld * 4, reinterpret_cast<const uint32_t(&)[16]>(v[16 * half]), q.rows);
+  } else if ((int)(threadIdx.x & 31) < q.rows) {
     store_words(static_cast<float *>(p) + at, width, v);
   }
 }
 __device__ __forceinline__ void store_part(void *p, int64_t ld, int width, const uint32_t (&w)[16], const Part &q) {
   if (!whole(width, q))
     return store_turned(p, ld, true, q, [&](int e) { return e % 2 ? bf16_high(w[e / 2]) : bf16_low(w[e / 2]); });
-  if ((int)(threadIdx.x & 31) < q.rows) store_words(static_cast<uint16_t *>(p) + q.row * ld + q.col, width, w);
+  if (width == 32)
+    store_pairs(static_cast<uint16_t *>(p) + q.row * ld + q.col, ld * 2, w, q.rows);
+  else if ((int)(threadIdx.x & 31) < q.rows)
+    store_words(static_cast<uint16_t *>(p) + q.row * ld + q.col, width, w);
 }
 
 // The part of a BF16 matrix as pairs, 0 where there is none; `vec`: its rows start on
