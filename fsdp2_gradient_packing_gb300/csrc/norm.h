@@ -49,7 +49,7 @@ struct Args {
   int32_t stages, stage_bytes;
   uint32_t *status;
   uint64_t wait_limit_ns;
-  int32_t fault;             // test hook: block 0 leaves its first stage empty
+  int32_t fault;             // test hook, see skips_first()
   const void *weight, *bias;
   float *mean, *rstd;        // written forward, read backward
   // forward
@@ -73,6 +73,12 @@ struct alignas(16) Shared {
   uint64_t full[kMaxWarps][kMaxStages], empty[kMaxWarps][kMaxStages];  // one ring to a group
   uint32_t stop;
 };
+
+// Test hook: bit 0 makes a row group of block 0 (bits 8 and up say which) leave its
+// first stage empty, so that its wait gives up.
+__device__ __forceinline__ bool skips_first(const Args &a, int group) {
+  return (a.fault & 1) != 0 && blockIdx.x == 0 && group == a.fault >> 8;
+}
 
 template <int G>
 __device__ __forceinline__ void group_sync(int group) {
@@ -204,7 +210,7 @@ __device__ __forceinline__ void load_rows(const Args &a, Shared &sh, uint8_t *me
     bytes[i] = s.elem ? width * s.elem : (width + (int)kActGroup - 1) / (int)kActGroup;
   }
   const uint32_t ring = tc::smem(memory) + (uint32_t)lane * a.stages * a.stage_bytes;
-  bool skip = a.fault != 0 && blockIdx.x == 0 && lane == 0;
+  bool skip = skips_first(a, lane);
   int stage = 0;
   uint32_t parity = 1;
   for (; row < a.rows; row += step) {
@@ -382,8 +388,12 @@ __device__ __forceinline__ void begin_block(Shared &sh, int groups, int stages, 
   if (CLUSTER) tc::cluster_sync();
 }
 // Records a wait that gave up; copies that it did not wait for get a fixed time to
-// land before the block leaves its shared memory.
+// land before the block leaves its shared memory.  By the whole block: its row groups
+// and its loading warp have nothing else in common after their last rows, and any of
+// them may be the one whose wait gives up.
 __device__ __forceinline__ void end_block(Shared &sh, const Args &a) {
+  __syncwarp();  // the loading warp's lanes come from loops of their own
+  __syncthreads();
   if (threadIdx.x == 0 && *(volatile uint32_t *)&sh.stop) {
     atomicOr(a.status, kStatusNorm);
     const uint64_t began = tc::now_ns();

@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(most_threads(K, VEC), 1) backward_kernel(const
   __syncthreads();
   Filler<G, K> filler(a, sh, stages, group, base, row, step);
   for (int i = 0; i < a.stages; ++i)
-    if (row + i * step < a.rows) filler.fill(a, i, a.fault != 0 && blockIdx.x == 0 && group == 0 && i == 0);
+    if (row + i * step < a.rows) filler.fill(a, i, i == 0 && skips_first(a, group));
 
   const int mine = columns_of<VEC, G, K>(ring.width, t);
   const int dx_size = a.dx_bf16 ? 2 : 4;

@@ -34,7 +34,8 @@
  *   - NaN and infinities propagate as the formulas say.
  *   - Every wait inside the kernels is bounded; fsdp_ops_sync_status tells
  *     whether one gave up.  fsdp_debug_set_wait_fault (the limit and the test
- *     hook) holds for these kernels' pipelines too.
+ *     hook) holds for these kernels' pipelines too; fault = 1 + 256 * g starves
+ *     the g-th group of rows of a layer norm's first block.
  */
 #ifndef FSDP_OPS_H
 #define FSDP_OPS_H

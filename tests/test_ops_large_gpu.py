@@ -126,3 +126,43 @@ def test_norm_wait_that_gives_up():
     fp.fsdp_layer_norm_backward(x, x, None, mean, rstd, dxa, dwa)
     fp.fsdp_ops_sync_status()
     assert torch.equal(again, y) and torch.equal(dxa, dx) and torch.equal(dwa, dw)
+
+
+@pytest.mark.parametrize("cols,group", [(1024, 23), (1024, 5), (4096, 5), (2048, 1)])
+def test_norm_wait_that_gives_up_in_a_later_group(cols, group):
+    """A row group of a block gives up long after the first one has left: the status says so all the same.  One row to
+    each group of every SM (24 groups of a block up to 1,024 columns, 6 to 4,096), so that the first block has them all."""
+    fp = fp_module()
+    groups = 24 if cols <= 1024 else 6
+    x = torch.randn(torch.cuda.get_device_properties(0).multi_processor_count * groups, cols, device="cuda")
+    y = torch.empty_like(x)
+    fp.fsdp_layer_norm_forward(x, None, None, y)
+    fp.fsdp_ops_sync_status()
+    fp.fsdp_debug_set_wait_fault(1 + 256 * group, 20_000_000)
+    try:
+        fp.fsdp_layer_norm_forward(x, None, None, torch.empty_like(x))
+        with pytest.raises(fp.FsdpError, match="gave up"):
+            fp.fsdp_ops_sync_status()
+    finally:
+        fp.fsdp_debug_set_wait_fault(0, 0)
+    again = torch.empty_like(x)
+    fp.fsdp_layer_norm_forward(x, None, None, again)
+    fp.fsdp_ops_sync_status()
+    assert torch.equal(again, y)
+
+
+@pytest.mark.parametrize("group", [1, 7])
+def test_norm_backward_wait_that_gives_up_in_a_later_group(group):
+    """The same of the backward pass, eight groups of a block to 1,024 columns."""
+    fp = fp_module()
+    x = torch.randn(torch.cuda.get_device_properties(0).multi_processor_count * 8, 1024, device="cuda")
+    mean, rstd = torch.zeros(x.shape[0], device="cuda"), torch.ones(x.shape[0], device="cuda")
+    fp.fsdp_ops_sync_status()
+    fp.fsdp_debug_set_wait_fault(1 + 256 * group, 20_000_000)
+    try:
+        fp.fsdp_layer_norm_backward(x, x, None, mean, rstd, torch.empty_like(x), torch.empty(1024, device="cuda"))
+        with pytest.raises(fp.FsdpError, match="gave up"):
+            fp.fsdp_ops_sync_status()
+    finally:
+        fp.fsdp_debug_set_wait_fault(0, 0)
+    fp.fsdp_ops_sync_status()
