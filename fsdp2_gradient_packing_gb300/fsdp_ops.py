@@ -166,9 +166,12 @@ def _workspace(where, given, nbytes, handle, device):
         return given.data_ptr(), given.numel(), given
     if nbytes == 0:
         return None, 0, None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=_device(device))
-    if handle != _current_stream():  # the allocator may not reuse it before the call's stream is done with it
-        ws.record_stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream())
+    if handle == _current_stream():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=_device(device))
+    else:  # from the pool of the call's stream: what the current one gave back, its earlier launches may still be using
+        other = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+        with torch.cuda.stream(other):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=_device(device))
     return ws.data_ptr(), nbytes, ws
 
 

@@ -265,6 +265,24 @@ def test_same_bits_on_every_run_and_stream():
         assert all(torch.equal(p, q) for p, q in zip(o, outs[0]))
 
 
+def test_workspace_comes_from_the_stream_of_the_call():
+    """Scratch for a call on one stream is no block that another stream has just given back: what was launched there may
+    still be at work on it.  (Memory only; nothing is launched.)"""
+    fp_module()
+    from fsdp2_gradient_packing_gb300 import fsdp_ops
+    device, n, side = torch.cuda.current_device(), 1 << 22, torch.cuda.Stream()
+    for current, other in ((torch.cuda.default_stream(), side), (side, torch.cuda.default_stream())):
+        with torch.cuda.stream(current):
+            given_back = torch.empty(n, dtype=torch.uint8, device="cuda").data_ptr()
+            again = torch.empty(n, dtype=torch.uint8, device="cuda").data_ptr()
+            assert again == given_back  # the allocator's own rule, within a stream
+            at, size, _owner = fsdp_ops._workspace("here", None, n, other.cuda_stream, device)
+            assert size == n and not given_back <= at < given_back + n
+            at, size, _owner = fsdp_ops._workspace("here", None, n, current.cuda_stream, device)
+            assert at == given_back
+            assert torch.cuda.current_stream() == current
+
+
 def test_in_a_graph():
     fp = fp_module()
     b = Block(140, 64, 96, 6)
