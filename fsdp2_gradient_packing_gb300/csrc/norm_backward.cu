@@ -72,17 +72,20 @@ __global__ void __launch_bounds__(most_threads(K, VEC), 1) backward_kernel(const
     ring.wait();
     read_row<XK, VEC, G, K>(xh, unit, ring.data(0, row, VEC), ring.data(1, row, false), a.x_kind, mine, t, sh.zeros);
     read_row<DK, VEC, G, K>(g, one, ring.data(2, row, VEC), nullptr, dy_kind, mine, t, sh.zeros);
-    const float r = rstd, m = -mean * rstd;
+    const float r = rstd, m = -mean;
     if (row + step < a.rows) mean = a.mean[row + step], rstd = a.rstd[row + step];
     float2 s0 = both(0.0f), s1 = both(0.0f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float2 w[4];
       read_param<VEC, G, K>(w, weight, t, k);
-      const float2 by = both(r * unit[k]), from = both(m);
+      // The difference first: in x r - mean r the rounded mean r, many times xh where a
+      // row is far from 0, would leave its error in xh.
+      const float2 by = both(unit[k]), from = both(m);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        xh[k][e] = __ffma2_rn(xh[k][e], by, from);
+        xh[k][e] = VEC && XK == X_ACT8 ? __ffma2_rn(xh[k][e], by, from) : __fadd2_rn(xh[k][e], from);
+        xh[k][e] = __fmul2_rn(xh[k][e], both(r));
         db[k][e] = __fadd2_rn(db[k][e], g[k][e]);
         dw[k][e] = __ffma2_rn(g[k][e], xh[k][e], dw[k][e]);
         g[k][e] = __fmul2_rn(g[k][e], w[e]);

@@ -165,6 +165,35 @@ def test_backward(cols, dtype, y_dtype, dx_dtype):
     check_backward(fp, x, w, dy, dx_dtype, BF16, from_ckpt=True)
 
 
+@pytest.mark.parametrize("shift,std", [(3000.0, 1.0), (100.0, 0.01)])
+@pytest.mark.parametrize("from_ckpt", [False, True])
+@pytest.mark.parametrize("cols", [96, 99, 1024, 2048, 4104, 5001, 9000])
+def test_backward_far_from_zero(cols, from_ckpt, shift, std):
+    """Rows whose mean is many times their deviation, and a constant row, whose xh is 0.  xh is a difference rounded once
+    and a product rounded once, so its error is 2 u of xh itself, whatever the mean: dx is then within the sums' 64 u of its
+    terms, and dweight within its chains' of the terms' magnitudes."""
+    fp = fp_module()
+    rows = 40
+    x = (normals(cols, rows, cols, std=std) + shift).float()
+    x[7] = shift + 1.3
+    w, dy = (1 + normals(1, cols, std=0.2)).float(), normals(2, rows, cols).float()
+    x64 = x.double()
+    _, m64, r64 = reference(x64, None, None, 1e-5)
+    mean, rstd = m64.float(), r64.float()
+    arg = x.cuda()
+    if from_ckpt:
+        enc = act8_encode(x64.numpy())
+        arg, x64 = fp.Act8(rows, cols, act8_buffer(*enc)), torch.from_numpy(act8_decode(*enc, cols))
+    dx, dw, db = torch.empty(rows, cols, device="cuda"), torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    fp.fsdp_layer_norm_backward(dy.cuda(), arg, w.cuda(), mean.cuda(), rstd.cuda(), dx, dw, db)
+    dx64, dw64, db64, xh, g, _, _ = backward_reference(x64, w.double(), dy.double(), mean.double(), rstd.double())
+    assert from_ckpt or bool((xh[7] == 0).all())
+    parts = g.abs() + g.abs().mean(-1, keepdim=True) + 2 * xh.abs() * (g * xh).abs().mean(-1, keepdim=True)
+    close(dx, dx64, U * rstd.double()[:, None] * parts, "dx")
+    close(dw, dw64, U * (dy.double() * xh).abs().sum(0), "dweight")
+    close(db, db64, U * dy.double().abs().sum(0), "dbias")
+
+
 @pytest.mark.parametrize("rows", [1, 2, 5, 1000, 9001])
 @pytest.mark.parametrize("cols", [96, 99, 1024])
 def test_backward_rows(rows, cols):
