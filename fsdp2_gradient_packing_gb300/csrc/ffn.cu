@@ -534,8 +534,8 @@ struct Call {
 
   // Launches one product; args' operands, tiles and outputs are set.
   fsdp_status_t launch(Mode mode, bool pair, Args &a) {
-    cudaError_t e = status_word(&a.status);
-    if (e != cudaSuccess) return fail(FSDP_ECUDA, std::string("status word: ") + cudaGetErrorString(e));
+    cudaError_t e = gave_up_count(GAVE_UP_PRODUCT, &a.gave_up);
+    if (e != cudaSuccess) return fail(FSDP_ECUDA, std::string("status count: ") + cudaGetErrorString(e));
     a.wait_limit_ns = wait_limit_ns();
     a.fault = wait_fault();
     a.act = d->activation == FSDP_ACT_SILU ? SILU : GELU;

@@ -37,7 +37,6 @@ enum Act { SILU = 0, GELU = 1 };
 
 constexpr int kTileM = 128;  // rows of a block's tile (TMEM lanes)
 constexpr int kTileK = 64;   // K values of a stage: one 128-byte swizzled row
-constexpr uint32_t kStatusGemm = 16u;  // a wait of this kernel gave up
 
 // The tiles of one product, m x n of them.  In the order of tile_at, the first `whole`
 // are units of work; the K loops of the others are in `splits` parts, each of them a unit.
@@ -60,7 +59,7 @@ __device__ __forceinline__ int2 tile_at(const Grid &g, int t) {
 struct Args {
   CUtensorMap a[2];   // FORWARD, RECOMPUTE: x; BACKWARD: dg, du
   CUtensorMap b[3];   // Wg, Wu; BACKWARD: also x
-  uint32_t *status;
+  uint32_t *gave_up;  // count of blocks whose waits gave up
   uint64_t wait_limit_ns;
   int32_t fault;
   int32_t act;        // Act

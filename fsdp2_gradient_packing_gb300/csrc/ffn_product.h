@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   tc::fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && sh.stop) {
-    atomicOr(a.status, kStatusGemm);
+    atomicAdd(a.gave_up, 1u);
     land_copies(sh, a, stage_count, rank, skips_first(a, worker));
   }
   __syncthreads();

@@ -30,7 +30,6 @@ namespace norm {
 
 enum XKind { X_F32 = 0, X_BF16 = 1, X_ACT8 = 2 };
 
-constexpr uint32_t kStatusNorm = 32u;  // a wait of these kernels gave up
 constexpr int kMaxCluster = 8;
 constexpr int kMaxWarps = 32;
 constexpr int kMaxStages = 8;
@@ -47,7 +46,7 @@ struct Stream {
 struct Args {
   Stream in[3];              // x or its codes; its scales; dy
   int32_t stages, stage_bytes;
-  uint32_t *status;
+  uint32_t *gave_up;         // count of blocks whose waits gave up
   uint64_t wait_limit_ns;
   int32_t fault;             // test hook, see skips_first()
   const void *weight, *bias;
@@ -395,7 +394,7 @@ __device__ __forceinline__ void end_block(Shared &sh, const Args &a) {
   __syncwarp();  // the loading warp's lanes come from loops of their own
   __syncthreads();
   if (threadIdx.x == 0 && *(volatile uint32_t *)&sh.stop) {
-    atomicOr(a.status, kStatusNorm);
+    atomicAdd(a.gave_up, 1u);
     const uint64_t began = tc::now_ns();
     while (tc::now_ns() - began < 1000000) {
     }
@@ -500,8 +499,8 @@ inline void set_x(Args &a, const fsdp_norm_desc_t *d, const void *x) {
 
 // `more`: threads of a block beside its row groups (a loading warp's).
 inline fsdp_status_t run(const void *fn, Args &a, const Launch &l, const Shape &s, int more, cudaStream_t stream) {
-  cudaError_t e = status_word(&a.status);
-  if (e != cudaSuccess) return fail(FSDP_ECUDA, std::string("status word: ") + cudaGetErrorString(e));
+  cudaError_t e = gave_up_count(GAVE_UP_NORM, &a.gave_up);
+  if (e != cudaSuccess) return fail(FSDP_ECUDA, std::string("status count: ") + cudaGetErrorString(e));
   a.wait_limit_ns = wait_limit_ns();
   a.fault = wait_fault();
   if (l.smem > 32 * 1024) {

@@ -1,5 +1,5 @@
 // Host side that the training operators (fsdp_ops.h) share: device queries,
-// argument checks, launches, and the word that records waits that gave up.
+// argument checks, launches, and the counts of waits that gave up.
 #include "ops.h"
 
 #include <mutex>
@@ -7,25 +7,33 @@
 namespace fsdp {
 namespace {
 constexpr int kMaxDevices = 64;
-__device__ uint32_t g_status;
-}  // namespace
+__device__ uint32_t g_gave_up[GAVE_UP_KINDS];
 
-cudaError_t status_word(uint32_t **word) {
+// The current device's counts, and its index.
+cudaError_t counts(uint32_t **at, int *device) {
   static std::mutex lock;
-  static uint32_t *at[kMaxDevices];
+  static uint32_t *known[kMaxDevices];
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> hold(lock);
-  if (!at[dev]) {
+  if (!known[dev]) {
     void *p = nullptr;
-    e = cudaGetSymbolAddress(&p, g_status);
+    e = cudaGetSymbolAddress(&p, g_gave_up);
     if (e != cudaSuccess) return e;
-    at[dev] = static_cast<uint32_t *>(p);
+    known[dev] = static_cast<uint32_t *>(p);
   }
-  *word = at[dev];
+  *at = known[dev], *device = dev;
   return cudaSuccess;
+}
+}  // namespace
+
+cudaError_t gave_up_count(GaveUp kind, uint32_t **count) {
+  int dev;
+  cudaError_t e = counts(count, &dev);
+  if (e == cudaSuccess) *count += kind;
+  return e;
 }
 
 int device_sms() {
@@ -80,14 +88,20 @@ cudaError_t launch_kernel(const void *fn, dim3 grid, dim3 block, void **args, si
 using namespace fsdp;
 
 extern "C" fsdp_status_t fsdp_ops_sync_status(fsdp_stream_t stream) {
-  uint32_t *at = nullptr, word = 0;
-  cudaError_t e = status_word(&at);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
-  if (e == cudaSuccess) e = cudaMemcpy(&word, at, sizeof(word), cudaMemcpyDeviceToHost);
-  if (e == cudaSuccess && word) e = cudaMemset(at, 0, sizeof(word));
+  static thread_local uint32_t seen[kMaxDevices][GAVE_UP_KINDS];
+  uint32_t *at = nullptr, now[GAVE_UP_KINDS] = {}, kinds = 0;
+  int dev = -1;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = counts(&at, &dev);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(now, at, sizeof(now), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return fail(FSDP_ECUDA, std::string("status read: ") + cudaGetErrorString(e));
-  if (word)
-    return fail(FSDP_ETIMEOUT, "a bounded device wait gave up (status bits " + std::to_string(word) + ")");
+  for (int k = 0; k < GAVE_UP_KINDS; ++k) {
+    if (now[k] != seen[dev][k]) kinds |= 16u << k;
+    seen[dev][k] = now[k];
+  }
+  if (kinds)
+    return fail(FSDP_ETIMEOUT, "a bounded device wait gave up (status bits " + std::to_string(kinds) + ")");
   clear_error();
   return FSDP_OK;
 }

@@ -13,8 +13,11 @@
 
 namespace fsdp {
 
-// The current device's word in which kernels record waits that gave up.
-cudaError_t status_word(uint32_t **word);
+// The current device's counts of blocks whose waits gave up, by kind of kernel.  Kernels
+// add to them and nothing takes away, so no failure is lost between a read and a reset;
+// who asks (fsdp_ops_sync_status) remembers what it has seen.
+enum GaveUp { GAVE_UP_PRODUCT = 0, GAVE_UP_NORM = 1, GAVE_UP_KINDS = 2 };
+cudaError_t gave_up_count(GaveUp kind, uint32_t **count);
 
 // SMs of the current device (cached per device); 0 if there is none.
 int device_sms();

@@ -379,4 +379,5 @@ def fsdp_gated_ffn_backward(dh, x, w_gate, w_up, dx=None, dw_gate=None, dw_up=No
 
 
 def fsdp_ops_sync_status(stream=None) -> None:
+    """Raises ``FsdpError`` (FSDP_ETIMEOUT) if a wait on this device gave up since this thread last asked."""
     _check(_lib.fsdp_ops_sync_status(_fp._stream(stream)), "fsdp_ops_sync_status")

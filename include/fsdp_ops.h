@@ -204,10 +204,13 @@ fsdp_status_t fsdp_gated_ffn_backward(const fsdp_ffn_desc_t *desc, const void *d
                                       void *dx, void *dw_gate, void *dw_up, void *workspace,
                                       int64_t workspace_bytes, fsdp_stream_t stream);
 
-/* Synchronise `stream`, then read and clear the device word in which the
- * kernels of this header record a wait that gave up.  The word is one per
- * device, shared by all calls of the process.  FSDP_ETIMEOUT if any was
- * recorded since the last call. */
+/* Synchronise `stream`, then say whether a wait of this header's kernels gave
+ * up.  Failures are counted per device, for all streams and threads of the
+ * process together, and the counts are never reset: FSDP_ETIMEOUT if one has
+ * grown since this host thread last asked on this device (for a thread that
+ * never asked: since the process began).  So every thread that asks is told of
+ * every failure once, whoever else was told; a thread may be told of one on
+ * another's stream. */
 fsdp_status_t fsdp_ops_sync_status(fsdp_stream_t stream);
 
 #ifdef __cplusplus

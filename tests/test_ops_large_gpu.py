@@ -1,5 +1,8 @@
 """The training operators on matrices of more than 2^31 elements, whose last rows are compared with the same rows computed
 alone; and waits that give up."""
+import contextlib
+from concurrent.futures import ThreadPoolExecutor
+
 import pytest
 import torch
 
@@ -166,3 +169,38 @@ def test_norm_backward_wait_that_gives_up_in_a_later_group(group):
     finally:
         fp.fsdp_debug_set_wait_fault(0, 0)
     fp.fsdp_ops_sync_status()
+
+
+def test_every_thread_is_told_of_a_wait_that_gave_up():
+    """One thread's asking does not take the failure away from another, whose results it may be."""
+    fp = fp_module()
+    x = torch.randn(300, 1024, device="cuda")
+
+    def told():
+        try:
+            fp.fsdp_ops_sync_status()
+        except fp.FsdpError as e:
+            assert e.status == fp.FSDP_ETIMEOUT and "gave up" in str(e)
+            return True
+        return False
+
+    def forward():
+        y = torch.empty_like(x)
+        fp.fsdp_layer_norm_forward(x, None, None, y)
+        torch.cuda.synchronize()
+
+    with contextlib.ExitStack() as stack:
+        one, two = (stack.enter_context(ThreadPoolExecutor(1)) for _ in range(2))
+        threads = [lambda f: f(), lambda f: one.submit(f).result(), lambda f: two.submit(f).result()]
+        forward()
+        for run in threads:
+            run(told)  # earlier failures, of which a new thread is told too
+        assert not any(run(told) for run in threads)
+        fp.fsdp_debug_set_wait_fault(1, 20_000_000)
+        try:
+            two.submit(forward).result()
+        finally:
+            fp.fsdp_debug_set_wait_fault(0, 0)
+        assert [run(told) for run in threads] == [True, True, True]
+        forward()
+        assert not any(run(told) for run in threads)
