@@ -313,10 +313,11 @@ def _ffn_workspace(backward, device, *fields) -> int:
 
 
 def fsdp_gated_ffn_workspace(rows: int, d: int, f: int, backward: bool, keep: int = FSDP_KEEP_NONE,
-                             x_act8: bool = False) -> int:
-    """Bytes of workspace of a call on contiguous matrices, d and f multiples of 8, that start on 16-byte boundaries;
-    for others, an upper bound with everything that may have to be copied."""
-    odd = 0 if d % 8 == 0 else 7
+                             x_act8: bool = False, aligned: bool = True) -> int:
+    """Bytes of workspace of a call.  ``aligned``: every row of x and of the weights starts on a 16-byte boundary, as those
+    of contiguous tensors with d a multiple of 8 do; if not (views at an offset, other row distances), x and both weights
+    may have to be copied, and the size is enough for every such call."""
+    odd = 0 if aligned and d % 8 == 0 else 7
     return _ffn_workspace(int(backward), torch.cuda.current_device() if torch.cuda.is_available() else None, rows, d, f, d, d, d, f,
                           f, d, d, d, FSDP_ACT_SILU, keep, FSDP_ACT8 if x_act8 else FSDP_DTYPE_BF16, FSDP_DTYPE_BF16,
                           FSDP_DTYPE_BF16, odd)

@@ -265,6 +265,22 @@ def test_same_bits_on_every_run_and_stream():
         assert all(torch.equal(p, q) for p, q in zip(o, outs[0]))
 
 
+@pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (3, 5)])
+def test_workspace_for_views(pad, offset):
+    """A kept workspace of the size that the binding names is enough for views of aligned widths."""
+    fp = fp_module()
+    b = Block(140, 64, 96, 5, pad, offset)
+    h, dx, dwg, dwu = (b.out(*s, BF16).t for s in ((140, 96), (140, 64), (96, 64), (96, 64)))
+    ws = [torch.empty(fp.fsdp_gated_ffn_workspace(140, 64, 96, back, aligned=False), dtype=torch.uint8, device="cuda")
+          for back in (False, True)]
+    fp.fsdp_gated_ffn_forward(b.mx.t, b.mwg.t, b.mwu.t, h, workspace=ws[0])
+    fp.fsdp_gated_ffn_backward(b.mdh.t, b.mx.t, b.mwg.t, b.mwu.t, dx, dwg, dwu, workspace=ws[1])
+    want = [torch.empty(*s, dtype=BF16, device="cuda") for s in ((140, 96), (140, 64), (96, 64), (96, 64))]
+    fp.fsdp_gated_ffn_forward(b.mx.t, b.mwg.t, b.mwu.t, want[0])
+    fp.fsdp_gated_ffn_backward(b.mdh.t, b.mx.t, b.mwg.t, b.mwu.t, *want[1:])
+    assert all(torch.equal(p, q) for p, q in zip((h, dx, dwg, dwu), want))
+
+
 def test_workspace_comes_from_the_stream_of_the_call():
     """Scratch for a call on one stream is no block that another stream has just given back: what was launched there may
     still be at work on it.  (Memory only; nothing is launched.)"""

@@ -152,6 +152,21 @@ def test_ffn_workspace(fp):
     assert fp.fsdp_gated_ffn_workspace(0, 64, 96, True) == 0
 
 
+@pytest.mark.parametrize("backward,x_act8", [(False, False), (True, False), (True, True)])
+@pytest.mark.parametrize("rows,d,f", [(1, 64, 96), (5, 64, 96), (1000, 64, 96), (1000, 65, 96), (129, 512, 1408)])
+def test_ffn_workspace_of_views(fp, rows, d, f, backward, x_act8):
+    """What the binding gives for operands that are not aligned is enough for every row distance and offset of each."""
+    bound = fp.fsdp_gated_ffn_workspace(rows, d, f, backward, x_act8=x_act8, aligned=False)
+    assert bound >= fp.fsdp_gated_ffn_workspace(rows, d, f, backward, x_act8=x_act8)
+    out = ctypes.c_int64()
+    for off in range(8):
+        for lx, lg, lu in ((0, 0, 0), (1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 3, 5), (8, 8, 8)):
+            desc = ffn(fp, rows=rows, d=d, f=f, ld_x=d + lx, ld_w_gate=d + lg, ld_w_up=d + lu, ld_h=f, ld_kept=f, ld_dx=d,
+                       ld_dw_gate=d, ld_dw_up=d, x_dtype=2 if x_act8 else 1, unaligned=off)
+            assert fp._lib.fsdp_gated_ffn_workspace(desc, int(backward), ctypes.byref(out)) == fp.FSDP_OK
+            assert out.value <= bound
+
+
 def test_binding_checks_without_tensors_on_a_gpu(fp):
     import torch
     x = torch.zeros(4, 64)
