@@ -15,9 +15,10 @@
 // Bound: the tensor cores, for long products under the power limit: 16384 x 4096 x 12288
 // forward takes 1.88 ms (1.76 PFLOP/s; the library's products sustain 1.71), 8192 x 4096 x
 // 12288 backward with gate and up computed again 3.13 ms (1.58 PFLOP/s).  Where K is short,
-// each tile's start and drain show: 8192 x 1024 x 4096 forward takes 77 us (1.78 PFLOP/s),
-// as long as two library products of that size without an epilogue, and 92 with 8-bit
-// copies of gate and up, whose stores hold up the operands' loads.
+// each tile's start and drain show: 8192 x 1024 x 4096 forward takes 77 us (1.79 PFLOP/s),
+// as long as two library products of that size without an epilogue, and with copies of gate
+// and up, whose stores hold up the operands' loads, 84 (8 bits) and 87 (BF16); in a graph,
+// operands and results rotating past L2.
 //
 // Work is split by role: one lane loads 64-deep K slices with TMA into a ring of
 // shared-memory stages, one lane issues tcgen05.mma into one of two accumulators

@@ -240,8 +240,8 @@ __device__ __forceinline__ void store_turned(void *p, int64_t ld, bool bf16, con
 
 // 64 bytes of each row, from a row to a thread, as two threads to a row: neighbours
 // exchange halves and store first the even one's row, then the odd one's, so that a row's
-// two sectors leave together (forward 8192 x 1024 x 4096 80 and 78.5 us, with 8-bit copies
-// 98 and 95.5).  `row`: this thread's; `pitch`: bytes.
+// two sectors leave together (forward 8192 x 1024 x 4096 80 us without the exchange, 78.5
+// with it; with 8-bit copies 98 and 95.5: measured in turn as single calls among others).  `row`: this thread's; `pitch`: bytes.
 __device__ __forceinline__ void store_pairs(void *row, int64_t pitch, const uint32_t (&w)[16], int rows) {
   const int lane = threadIdx.x & 31;
   const bool odd = lane & 1;

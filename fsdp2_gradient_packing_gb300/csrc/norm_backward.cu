@@ -7,9 +7,9 @@
 // once, [units][2][cols] in binary32; a second kernel adds the units in order.
 // Bound: HBM; 2 + 2 + 2 bytes an element in BF16 (5.03 from the checkpoint); what is
 // left above it is the latency of a row's sum, which a block hides behind one or two
-// more rows.  16384 x 4096 in BF16 takes 69.9 us with its column sums (5.8 TB/s), from
-// the checkpoint 66.3 (5.1 TB/s); 8192 x 4096 in FP32 70.3 (5.7 TB/s); 16385 x 1409 in
-// FP32, element by element, 53.3 (5.2 TB/s).
+// more rows.  16384 x 4096 in BF16 takes 69.7 us with its column sums (5.8 TB/s), from
+// the checkpoint 67.0 (5.1 TB/s); 8192 x 4096 in FP32 69.3 (5.8 TB/s); 16385 x 1409 in
+// FP32, element by element, 52.3 (5.3 TB/s).
 #include <algorithm>
 
 #include "norm.h"
@@ -189,9 +189,10 @@ __global__ void __launch_bounds__(kSumThreads) column_sum_kernel(const float *pa
 
 // The narrowest shape that holds a row.  What a row costs a warp beside its columns is
 // about 170 instructions, as much as 16 columns a thread cost, so vector kernels have
-// 32 columns a thread (us in BF16, with 16 columns and twice the threads / with 32:
-// 32768 x 1024 48.8 / 41.0, 32768 x 2048 74.9 / 70.9, 16384 x 4096 72.1 / 69.9, 8192 x
-// 8192 88.6 / 73.2, 4096 x 16384 135 / 118).  Kernels that go element by element are
+// 32 columns a thread (us in BF16, with 16 columns and twice the threads / with 32, where
+// xh was one operation less: 32768 x 1024 48.8 / 41.0, 32768 x 2048 74.9 / 70.9, 16384 x
+// 4096 72.1 / 69.9, 8192 x 8192 88.6 / 73.2, 4096 x 16384 135 / 118; now 40.7, 70.7, 69.7,
+// 74.5 and 119).  Kernels that go element by element are
 // bound by their accesses, which want threads, except where a warp has a row to itself
 // (16385 x 1409 from the checkpoint 60 / 65, 2048 x 20001 340 / 356; 32769 x 515 77 / 52).
 Shape shape_of(int64_t cols, bool vec) {

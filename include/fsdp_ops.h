@@ -22,6 +22,10 @@
  *   - Every pointer need only be aligned to its element size, except
  *     checkpoints and workspaces (16 bytes).  Rows whose start is 16-byte
  *     aligned take faster paths.
+ *   - Of inputs, the whole 16-byte units that a row, or a checkpoint's scale
+ *     bytes, lie in may be read: up to 15 bytes beside them, whose values are
+ *     ignored.  They never leave an allocation's 16-byte unit.  Nothing is written
+ *     outside a matrix.
  *   - Indexing is 64-bit throughout.
  *   - No call allocates device memory: calls that need scratch take a
  *     workspace, whose size the matching _workspace call gives.  A workspace
@@ -151,9 +155,10 @@ fsdp_status_t fsdp_layer_norm_workspace(const fsdp_norm_desc_t *desc, int64_t *b
  * with act(g) = g / (1 + e^-g) (FSDP_ACT_SILU) or g * Phi(g), Phi the normal
  * distribution (FSDP_ACT_GELU, the exact form).  Matrices are BF16 unless a
  * dtype field says otherwise; products run on the tensor cores with binary32
- * sums, and activations, their derivatives and products in binary32.  dg and du
- * are rounded to BF16 once, as operands of the backward products; g and u are
- * not rounded unless they are kept.
+ * sums, whose additions may cut where binary32 units round, and activations,
+ * their derivatives and products in binary32.  dg and du are rounded to BF16
+ * once, as operands of the backward products; g and u are not rounded unless
+ * they are kept.
  *
  * Kept for the backward pass (`keep`): nothing (the backward call computes g
  * and u again), the 8-bit checkpoints of g and u (33/32 byte an element), or
@@ -180,7 +185,10 @@ typedef struct {
 
 /* Bytes of workspace of the forward (backward = 0) or backward call.  Operands
  * whose rows do not all start on 16-byte boundaries (by their row distance or
- * by `unaligned`) are copied there once per call, which costs their bytes. */
+ * by `unaligned`) are copied there once per call, which costs their bytes.  The
+ * backward call holds dg and du there in BF16, 4 bytes for each element of h,
+ * and of an x given by its checkpoint a BF16 copy: it saves memory between the
+ * passes, not during this one. */
 fsdp_status_t fsdp_gated_ffn_workspace(const fsdp_ffn_desc_t *desc, int32_t backward, int64_t *bytes);
 
 /*
