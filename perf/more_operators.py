@@ -155,6 +155,7 @@ def prepare(case, seed):
         drift = _normal(gen, rows, std=0.2)
         for border in (math.log(1 - CLIP[0]), math.log(1 + CLIP[1])):
             drift = torch.where((drift - border).abs() < 1e-3, border + 2e-3, drift)
+        s["logp"] = logp
         s["old"], s["ref"] = logp - drift, logp - _normal(gen, rows, std=0.3)
     del scaled
     if op.endswith("bwd"):
@@ -206,7 +207,8 @@ def _run_own(s, c):
     choice = dict(ref_logp=None if op.startswith("distill") else s["ref"], weight=s["weight"], temperature=c["temperature"],
                   clip_low=CLIP[0], clip_high=CLIP[1], kl=KL)
     if op == "policy_bwd":
-        fp.fsdp_policy_loss_backward(logits, s["ids"], s["old"], s["advantage"], s["lse"], dlogits, dloss=s["dloss"], **choice)
+        fp.fsdp_policy_loss_backward(logits, s["ids"], s["old"], s["advantage"], s["logp"], s["lse"], dlogits, dloss=s["dloss"],
+                                     **choice)
         return dlogits
     loss, lse = torch.empty(rows, dtype=F32, device="cuda"), torch.empty(rows, dtype=F32, device="cuda")
     if op.startswith("distill"):
@@ -314,7 +316,7 @@ def _run_plain(s, c):
         g.scatter_add_(1, ids, -q)
         g *= (up * soft)[:, None]
     else:
-        logp = z.gather(1, s["ids"][:, None])[:, 0] - lse
+        logp = s["logp"] if op == "policy_bwd" else z.gather(1, s["ids"][:, None])[:, 0] - lse
         ratio, adv, rest = torch.exp(logp - s["old"]), s["advantage"], s["ref"] - logp
         clipped = ratio.clamp(1 - CLIP[0], 1 + CLIP[1])
         loss = -torch.minimum(ratio * adv, clipped * adv) + KL * (torch.exp(rest) - rest - 1)
