@@ -257,7 +257,7 @@ def _plain_scan(s, c):
     before = torch.empty_like(h)
     before[1:] = h[:-1]
     before[first] = s["initial"][which]
-    grad = s["dh"].float()
+    grad = s["dh"].float().clone()  # the conversion of an FP32 tensor is the tensor itself
     grad[last] += s["dfinal"][which]
     later = torch.zeros_like(cut)
     later[:-1] = cut[1:]
