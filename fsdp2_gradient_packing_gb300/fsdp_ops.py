@@ -25,12 +25,18 @@ FSDP_ACT8_GROUP = 32
 FSDP_NORM_MAX_COLS = 65536
 FSDP_ACT_SILU, FSDP_ACT_GELU = 0, 1
 FSDP_KEEP_NONE, FSDP_KEEP_ACT8, FSDP_KEEP_BF16 = 0, 1, 2
+FSDP_INDEX_I32, FSDP_INDEX_I64 = 0, 1
+FSDP_DISTILL_MAX_TOP = 1024
 
 __all__ = ["FSDP_ACT8", "FSDP_ACT8_GROUP", "FSDP_NORM_MAX_COLS", "fsdp_norm_desc_t", "Act8", "fsdp_act8_bytes",
            "fsdp_act8_store", "fsdp_act8_load", "fsdp_layer_norm_forward", "fsdp_layer_norm_backward",
            "fsdp_layer_norm_workspace", "FSDP_ACT_SILU", "FSDP_ACT_GELU", "FSDP_KEEP_NONE", "FSDP_KEEP_ACT8",
            "FSDP_KEEP_BF16", "fsdp_ffn_desc_t", "fsdp_gated_ffn_forward", "fsdp_gated_ffn_backward",
-           "fsdp_gated_ffn_workspace", "fsdp_ops_sync_status"]
+           "fsdp_gated_ffn_workspace", "fsdp_ops_sync_status", "FSDP_INDEX_I32", "FSDP_INDEX_I64", "FSDP_DISTILL_MAX_TOP",
+           "fsdp_embedding_desc_t", "fsdp_embedding_forward", "fsdp_embedding_backward", "fsdp_embedding_workspace",
+           "fsdp_scan_desc_t", "fsdp_gated_scan_forward", "fsdp_gated_scan_backward", "fsdp_gated_scan_states",
+           "fsdp_gated_scan_workspace", "fsdp_distill_desc_t", "fsdp_distill_loss_forward", "fsdp_distill_loss_backward",
+           "fsdp_policy_desc_t", "fsdp_policy_loss_forward", "fsdp_policy_loss_backward"]
 
 _CODE = {torch.float32: FSDP_DTYPE_F32, torch.bfloat16: FSDP_DTYPE_BF16}
 
@@ -48,6 +54,28 @@ class fsdp_ffn_desc_t(ctypes.Structure):
                [(n, ctypes.c_int32) for n in ("activation", "keep", "x_dtype", "dx_dtype", "dw_dtype", "unaligned")]
 
 
+class fsdp_embedding_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "vocab", "cols", "ld_weight", "ld_out")] + \
+               [(n, ctypes.c_int32) for n in ("token_dtype", "weight_dtype", "out_dtype", "accumulate")] + [("scale", ctypes.c_float)]
+
+
+class fsdp_scan_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "cols", "seqs", "seq_len", "ld_x", "ld_gate", "ld_h", "ld_dx", "ld_dgate")] + \
+               [(n, ctypes.c_int32) for n in ("packed", "offset_dtype", "x_dtype", "h_dtype", "dx_dtype", "param_dtype", "grad_dtype")]
+
+
+class fsdp_distill_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "vocab", "ld_logits", "ld_dlogits", "top", "ld_tokens", "ld_teacher")] + \
+               [(n, ctypes.c_int32) for n in ("logits_dtype", "dlogits_dtype", "teacher_dtype", "token_dtype")] + \
+               [("temperature", ctypes.c_float)]
+
+
+class fsdp_policy_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "vocab", "ld_logits", "ld_dlogits")] + \
+               [(n, ctypes.c_int32) for n in ("logits_dtype", "dlogits_dtype", "token_dtype")] + \
+               [(n, ctypes.c_float) for n in ("temperature", "clip_low", "clip_high", "kl")]
+
+
 _P, _ST, _I64, _I32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int32
 _SIGNATURES = {
     "fsdp_act8_bytes": [_I64, _I64, ctypes.POINTER(_I64)],
@@ -60,6 +88,17 @@ _SIGNATURES = {
     "fsdp_gated_ffn_forward": [ctypes.POINTER(fsdp_ffn_desc_t), _P, _P, _P, _P, _P, _P, _P, _I64, _P],
     "fsdp_gated_ffn_backward": [ctypes.POINTER(fsdp_ffn_desc_t)] + [_P] * 10 + [_I64, _P],
     "fsdp_ops_sync_status": [_P],
+    "fsdp_embedding_forward": [ctypes.POINTER(fsdp_embedding_desc_t)] + [_P] * 4,
+    "fsdp_embedding_backward": [ctypes.POINTER(fsdp_embedding_desc_t)] + [_P] * 4 + [_I64, _P],
+    "fsdp_embedding_workspace": [ctypes.POINTER(fsdp_embedding_desc_t), ctypes.POINTER(_I64)],
+    "fsdp_gated_scan_states": [_I64, _I64, ctypes.POINTER(_I64)],
+    "fsdp_gated_scan_workspace": [ctypes.POINTER(fsdp_scan_desc_t), _I32, ctypes.POINTER(_I64)],
+    "fsdp_gated_scan_forward": [ctypes.POINTER(fsdp_scan_desc_t)] + [_P] * 9 + [_I64, _P],
+    "fsdp_gated_scan_backward": [ctypes.POINTER(fsdp_scan_desc_t)] + [_P] * 13 + [_I64, _P],
+    "fsdp_distill_loss_forward": [ctypes.POINTER(fsdp_distill_desc_t)] + [_P] * 8,
+    "fsdp_distill_loss_backward": [ctypes.POINTER(fsdp_distill_desc_t)] + [_P] * 8,
+    "fsdp_policy_loss_forward": [ctypes.POINTER(fsdp_policy_desc_t)] + [_P] * 11,
+    "fsdp_policy_loss_backward": [ctypes.POINTER(fsdp_policy_desc_t)] + [_P] * 11,
 }
 for _name, _args in _SIGNATURES.items():
     _fn = getattr(_lib, _name)
@@ -72,6 +111,7 @@ for _name, _args in _SIGNATURES.items():
 # on (None before the first).  A small call costs little more on the GPU than
 # these checks do on the host, so they are plain functions with few steps.
 # ---------------------------------------------------------------------------
+_INDEX = {torch.int32: FSDP_INDEX_I32, torch.int64: FSDP_INDEX_I64}
 _BOTH, _BF16, _F32 = dict(_CODE), {torch.bfloat16: FSDP_DTYPE_BF16}, {torch.float32: FSDP_DTYPE_F32}
 _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
@@ -377,6 +417,258 @@ def fsdp_gated_ffn_backward(dh, x, w_gate, w_up, dx=None, dw_gate=None, dw_up=No
     pws, nws, _owner = _workspace(where, workspace, _ffn_workspace(1, dev, *fields), handle, dev)
     _check(_lib.fsdp_gated_ffn_backward(ctypes.byref(fsdp_ffn_desc_t(*fields)), pdh, px, pg, pu, pkg, pku, pdx, pdg, pdu, pws, nws,
                                         handle), where)
+
+
+# ---------------------------------------------------------------------------
+# Embedding
+# ---------------------------------------------------------------------------
+def _tokens(where, what, t, device):
+    """(pointer, count, dtype code, device) of a contiguous tensor of token ids, of any shape."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{where}: {what} is not a tensor")
+    code = _INDEX.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{where}: {what} is {t.dtype}, not one of {', '.join(map(str, _INDEX))}")
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {what} is not contiguous")
+    index = t.get_device()
+    if index != device:
+        _misplaced(where, what, index, device)
+    return t.data_ptr(), t.numel(), code, index
+
+
+def fsdp_embedding_forward(tokens, weight, out, scale=1.0, stream=None) -> None:
+    """out[i] = scale * weight[tokens[i]]; tokens of any shape, those outside the vocabulary give rows of zeros."""
+    where = "fsdp_embedding_forward"
+    pt, rows, dt_t, dev = _tokens(where, "tokens", tokens, None)
+    pw, ld_w, dt_w, dev = _matrix(where, "weight", weight, None, None, _BOTH, dev)
+    vocab, cols = weight.shape
+    po, ld_o, dt_o, dev = _matrix(where, "out", out, rows, cols, _BOTH, dev)
+    d = fsdp_embedding_desc_t(rows, vocab, cols, ld_w, ld_o, dt_t, dt_w, dt_o, 0, scale)
+    _check(_lib.fsdp_embedding_forward(ctypes.byref(d), pt, pw, po, _handle(where, stream, dev)), where)
+
+
+@functools.lru_cache(maxsize=1024)
+def _embedding_workspace(rows, vocab, cols) -> int:
+    d = fsdp_embedding_desc_t(rows, vocab, cols, cols, cols, 0, 0, 0, 0, 1.0)
+    out = _I64()
+    _check(_lib.fsdp_embedding_workspace(ctypes.byref(d), ctypes.byref(out)), "fsdp_embedding_workspace")
+    return out.value
+
+
+def fsdp_embedding_workspace(rows: int, vocab: int, cols: int) -> int:
+    """Bytes of workspace that fsdp_embedding_backward needs for that many tokens and a [vocab, cols] gradient."""
+    return _embedding_workspace(rows, vocab, cols)
+
+
+def fsdp_embedding_backward(tokens, dout, dweight, scale=1.0, accumulate=False, workspace=None, stream=None) -> None:
+    """dweight[v] = scale * sum of dout's rows of token v, written whole, or added where ``accumulate``."""
+    where = "fsdp_embedding_backward"
+    pt, rows, dt_t, dev = _tokens(where, "tokens", tokens, None)
+    pw, ld_w, dt_w, dev = _matrix(where, "dweight", dweight, None, None, _BOTH, dev)
+    vocab, cols = dweight.shape
+    po, ld_o, dt_o, dev = _matrix(where, "dout", dout, rows, cols, _BOTH, dev)
+    d = fsdp_embedding_desc_t(rows, vocab, cols, ld_w, ld_o, dt_t, dt_w, dt_o, bool(accumulate), scale)
+    handle = _handle(where, stream, dev)
+    pws, nws, _owner = _workspace(where, workspace, _embedding_workspace(rows, vocab, cols), handle, dev)
+    _check(_lib.fsdp_embedding_backward(ctypes.byref(d), pt, po, pw, pws, nws, handle), where)
+
+
+# ---------------------------------------------------------------------------
+# Gated linear recurrence
+# ---------------------------------------------------------------------------
+def fsdp_gated_scan_states(rows: int, cols: int) -> int:
+    """Rows of the FP32 matrix [n, cols] that a forward call fills for the backward call."""
+    out = _I64()
+    _check(_lib.fsdp_gated_scan_states(rows, cols, ctypes.byref(out)), "fsdp_gated_scan_states")
+    return out.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _scan_workspace(rows, cols, seqs, packed, backward, device) -> int:
+    d = fsdp_scan_desc_t(rows, cols, seqs, 0 if packed or not seqs else rows // seqs, cols, cols, cols, cols, cols, packed, 0, 0, 0, 0, 0, 0)
+    out = _I64()
+    _check(_lib.fsdp_gated_scan_workspace(ctypes.byref(d), backward, ctypes.byref(out)), "fsdp_gated_scan_workspace")
+    return out.value
+
+
+def fsdp_gated_scan_workspace(rows: int, cols: int, seqs: int, packed: bool, backward: bool) -> int:
+    """Bytes of workspace of a call over ``seqs`` sequences in ``rows`` rows."""
+    return _scan_workspace(rows, cols, seqs, int(packed), int(backward),
+                           torch.cuda.current_device() if torch.cuda.is_available() else None)
+
+
+def _sequences(where, rows, seq_len, offsets, dev):
+    """(sequences, rows of each, offsets pointer, their dtype code, device)."""
+    if (seq_len is None) == (offsets is None):
+        raise ValueError(f"{where}: either seq_len or offsets is needed")
+    if offsets is None:
+        if seq_len < 1 or rows % seq_len:
+            raise ValueError(f"{where}: {rows} rows are not sequences of {seq_len}")
+        return rows // seq_len, seq_len, None, 0, dev
+    po, n, code, dev = _tokens(where, "offsets", offsets, dev)
+    if n < 1:
+        raise ValueError(f"{where}: offsets is empty")
+    return n - 1, 0, po, code, dev
+
+
+def _states(where, what, t, rows, cols, dev):
+    """(pointer, device) of a contiguous FP32 matrix [rows, cols], or of nothing."""
+    if t is None:
+        return None, dev
+    p, ld, _, dev = _matrix(where, what, t, rows, cols, _F32, dev)
+    if ld != cols:
+        raise ValueError(f"{where}: {what} has gaps between its rows")
+    return p, dev
+
+
+def fsdp_gated_scan_forward(x, gate, h, bias=None, initial=None, final=None, seq_len=None, offsets=None, states=None,
+                            workspace=None, stream=None) -> None:
+    """Sequences of ``seq_len`` rows each, or from ``offsets[s]`` up to ``offsets[s + 1]``.  initial, final: FP32
+    [sequences, cols] (may be one tensor); states: FP32 [fsdp_gated_scan_states(rows, cols), cols] for the backward pass."""
+    where = "fsdp_gated_scan_forward"
+    px, ld_x, dt_x, dev = _matrix(where, "x", x, None, None, _BOTH, None)
+    rows, cols = x.shape
+    pg, ld_g, dt_g, dev = _matrix(where, "gate", gate, rows, cols, _BOTH, dev)
+    if dt_g != dt_x:
+        raise ValueError(f"{where}: x and gate have different dtypes")
+    ph, ld_h, dt_h, dev = _matrix(where, "h", h, rows, cols, _BOTH, dev)
+    pb, dt_b, dev = _vector(where, "bias", bias, cols, _BOTH, dev)
+    seqs, length, po, dt_o, dev = _sequences(where, rows, seq_len, offsets, dev)
+    pi, dev = _states(where, "initial", initial, seqs, cols, dev)
+    pf, dev = _states(where, "final", final, seqs, cols, dev)
+    ps = None
+    if states is not None:
+        ps, dev = _states(where, "states", states, fsdp_gated_scan_states(rows, cols), cols, dev)
+    packed = po is not None
+    d = fsdp_scan_desc_t(rows, cols, seqs, length, ld_x, ld_g, ld_h, cols, cols, packed, dt_o, dt_x, dt_h, FSDP_DTYPE_F32,
+                         FSDP_DTYPE_F32 if dt_b is None else dt_b, FSDP_DTYPE_F32)
+    handle = _handle(where, stream, dev)
+    pws, nws, _owner = _workspace(where, workspace, _scan_workspace(rows, cols, seqs, int(packed), 0, dev), handle, dev)
+    _check(_lib.fsdp_gated_scan_forward(ctypes.byref(d), px, pg, pb, pi, po, ph, pf, ps, pws, nws, handle), where)
+
+
+def fsdp_gated_scan_backward(dh, x, gate, states, dx, dgate, bias=None, dbias=None, initial=None, dinitial=None, dfinal=None,
+                             seq_len=None, offsets=None, workspace=None, stream=None) -> None:
+    """states: as the forward call wrote them; dbias and dinitial: written if given."""
+    where = "fsdp_gated_scan_backward"
+    ph, ld_h, dt_h, dev = _matrix(where, "dh", dh, None, None, _BOTH, None)
+    rows, cols = dh.shape
+    px, ld_x, dt_x, dev = _matrix(where, "x", x, rows, cols, _BOTH, dev)
+    pg, ld_g, dt_g, dev = _matrix(where, "gate", gate, rows, cols, _BOTH, dev)
+    if dt_g != dt_x:
+        raise ValueError(f"{where}: x and gate have different dtypes")
+    pdx, ld_dx, dt_dx, dev = _matrix(where, "dx", dx, rows, cols, _BOTH, dev)
+    pdg, ld_dg, dt_dg, dev = _matrix(where, "dgate", dgate, rows, cols, _BOTH, dev)
+    if dt_dg != dt_dx:
+        raise ValueError(f"{where}: dx and dgate have different dtypes")
+    pb, dt_b, dev = _vector(where, "bias", bias, cols, _BOTH, dev)
+    pdb, dt_db, dev = _vector(where, "dbias", dbias, cols, _BOTH, dev)
+    seqs, length, po, dt_o, dev = _sequences(where, rows, seq_len, offsets, dev)
+    if states is None:
+        raise ValueError(f"{where}: states is needed")
+    ps, dev = _states(where, "states", states, fsdp_gated_scan_states(rows, cols), cols, dev)
+    pi, dev = _states(where, "initial", initial, seqs, cols, dev)
+    pdi, dev = _states(where, "dinitial", dinitial, seqs, cols, dev)
+    pdf, dev = _states(where, "dfinal", dfinal, seqs, cols, dev)
+    packed = po is not None
+    d = fsdp_scan_desc_t(rows, cols, seqs, length, ld_x, ld_g, ld_h, ld_dx, ld_dg, packed, dt_o, dt_x, dt_h, dt_dx,
+                         FSDP_DTYPE_F32 if dt_b is None else dt_b, FSDP_DTYPE_F32 if dt_db is None else dt_db)
+    handle = _handle(where, stream, dev)
+    pws, nws, _owner = _workspace(where, workspace, _scan_workspace(rows, cols, seqs, int(packed), 1, dev), handle, dev)
+    _check(_lib.fsdp_gated_scan_backward(ctypes.byref(d), ph, px, pg, pb, pi, po, ps, pdf, pdx, pdg, pdb, pdi, pws, nws, handle), where)
+
+
+# ---------------------------------------------------------------------------
+# Losses over logits
+# ---------------------------------------------------------------------------
+def _distill(where, logits, dlogits, teacher_tokens, teacher_logits, weight, temperature):
+    """(descriptor, pointers of logits, dlogits, tokens, teacher and weight, device)."""
+    pz, ld_z, dt_z, dev = _matrix(where, "logits", logits, None, None, _BOTH, None)
+    rows, vocab = logits.shape
+    pd, ld_d, dt_d = None, vocab, dt_z
+    if dlogits is not None:
+        pd, ld_d, dt_d, dev = _matrix(where, "dlogits", dlogits, rows, vocab, _BOTH, dev)
+    pi, ld_i, dt_i, dev = _matrix(where, "teacher_tokens", teacher_tokens, rows, None, _INDEX, dev)
+    top = teacher_tokens.shape[1]
+    pt, ld_t, dt_t, dev = _matrix(where, "teacher_logits", teacher_logits, rows, top, _BOTH, dev)
+    pw, _, dev = _vector(where, "weight", weight, rows, _F32, dev)
+    return fsdp_distill_desc_t(rows, vocab, ld_z, ld_d, top, ld_i, ld_t, dt_z, dt_d, dt_t, dt_i, temperature), pz, pd, pi, pt, pw, dev
+
+
+def _needed(where, what, t, n, codes, dev):
+    if t is None:
+        raise ValueError(f"{where}: {what} is needed")
+    p, _, dev = _vector(where, what, t, n, codes, dev)
+    return p, dev
+
+
+def fsdp_distill_loss_forward(logits, teacher_tokens, teacher_logits, loss, lse, temperature=1.0, weight=None, dlogits=None,
+                              stream=None) -> None:
+    """Rows' losses against a teacher's top logits [rows, top]; dlogits: receives the gradient of their sum in the same
+    pass (it may be ``logits`` itself)."""
+    where = "fsdp_distill_loss_forward"
+    d, pz, pd, pi, pt, pw, dev = _distill(where, logits, dlogits, teacher_tokens, teacher_logits, weight, temperature)
+    pl, dev = _needed(where, "loss", loss, d.rows, _F32, dev)
+    pe, dev = _needed(where, "lse", lse, d.rows, _F32, dev)
+    _check(_lib.fsdp_distill_loss_forward(ctypes.byref(d), pz, pi, pt, pw, pl, pe, pd, _handle(where, stream, dev)), where)
+
+
+def fsdp_distill_loss_backward(logits, teacher_tokens, teacher_logits, lse, dlogits, temperature=1.0, weight=None, dloss=None,
+                               stream=None) -> None:
+    """dlogits from the lse of a forward call; dloss: the gradient of each row's loss (None: 1)."""
+    where = "fsdp_distill_loss_backward"
+    if dlogits is None:
+        raise ValueError(f"{where}: dlogits is needed")
+    d, pz, pd, pi, pt, pw, dev = _distill(where, logits, dlogits, teacher_tokens, teacher_logits, weight, temperature)
+    pe, dev = _needed(where, "lse", lse, d.rows, _F32, dev)
+    pu, _, dev = _vector(where, "dloss", dloss, d.rows, _F32, dev)
+    _check(_lib.fsdp_distill_loss_backward(ctypes.byref(d), pz, pi, pt, pw, pe, pu, pd, _handle(where, stream, dev)), where)
+
+
+def _policy(where, logits, dlogits, tokens, old_logp, ref_logp, advantage, weight, temperature, clip_low, clip_high, kl):
+    """(descriptor, pointers of logits, dlogits, tokens, old_logp, ref_logp, advantage and weight, device)."""
+    pz, ld_z, dt_z, dev = _matrix(where, "logits", logits, None, None, _BOTH, None)
+    rows, vocab = logits.shape
+    pd, ld_d, dt_d = None, vocab, dt_z
+    if dlogits is not None:
+        pd, ld_d, dt_d, dev = _matrix(where, "dlogits", dlogits, rows, vocab, _BOTH, dev)
+    pi, n, dt_i, dev = _tokens(where, "tokens", tokens, dev)
+    if n != rows:
+        raise ValueError(f"{where}: {n} tokens for {rows} rows")
+    po, _, dev = _vector(where, "old_logp", old_logp, rows, _F32, dev)
+    pr, _, dev = _vector(where, "ref_logp", ref_logp, rows, _F32, dev)
+    pa, dev = _needed(where, "advantage", advantage, rows, _F32, dev)
+    pw, _, dev = _vector(where, "weight", weight, rows, _F32, dev)
+    d = fsdp_policy_desc_t(rows, vocab, ld_z, ld_d, dt_z, dt_d, dt_i, temperature, clip_low, clip_high, kl)
+    return d, pz, pd, pi, po, pr, pa, pw, dev
+
+
+def fsdp_policy_loss_forward(logits, tokens, old_logp, advantage, loss, logp, lse, ref_logp=None, weight=None, temperature=1.0,
+                             clip_low=0.2, clip_high=0.2, kl=0.0, dlogits=None, stream=None) -> None:
+    """Rows' losses and the log-probabilities of their tokens; old_logp None: the policy itself; dlogits: receives the
+    gradient of the losses' sum in the same pass (it may be ``logits`` itself)."""
+    where = "fsdp_policy_loss_forward"
+    d, pz, pd, pi, po, pr, pa, pw, dev = _policy(where, logits, dlogits, tokens, old_logp, ref_logp, advantage, weight, temperature,
+                                                 clip_low, clip_high, kl)
+    pl, dev = _needed(where, "loss", loss, d.rows, _F32, dev)
+    pp, dev = _needed(where, "logp", logp, d.rows, _F32, dev)
+    pe, dev = _needed(where, "lse", lse, d.rows, _F32, dev)
+    _check(_lib.fsdp_policy_loss_forward(ctypes.byref(d), pz, pi, po, pr, pa, pw, pl, pp, pe, pd, _handle(where, stream, dev)), where)
+
+
+def fsdp_policy_loss_backward(logits, tokens, old_logp, advantage, logp, lse, dlogits, ref_logp=None, weight=None, dloss=None,
+                              temperature=1.0, clip_low=0.2, clip_high=0.2, kl=0.0, stream=None) -> None:
+    """dlogits from the logp and lse of a forward call; dloss: the gradient of each row's loss (None: 1)."""
+    where = "fsdp_policy_loss_backward"
+    if dlogits is None:
+        raise ValueError(f"{where}: dlogits is needed")
+    d, pz, pd, pi, po, pr, pa, pw, dev = _policy(where, logits, dlogits, tokens, old_logp, ref_logp, advantage, weight, temperature,
+                                                 clip_low, clip_high, kl)
+    pp, dev = _needed(where, "logp", logp, d.rows, _F32, dev)
+    pe, dev = _needed(where, "lse", lse, d.rows, _F32, dev)
+    pu, _, dev = _vector(where, "dloss", dloss, d.rows, _F32, dev)
+    _check(_lib.fsdp_policy_loss_backward(ctypes.byref(d), pz, pi, po, pr, pa, pw, pp, pe, pu, pd, _handle(where, stream, dev)), where)
 
 
 def fsdp_ops_sync_status(stream=None) -> None:

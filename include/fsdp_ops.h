@@ -9,6 +9,13 @@
  *   fsdp_gated_ffn_forward / _backward    both projections, the activation
  *                                         and the product of a gated
  *                                         feed-forward block
+ *   fsdp_embedding_forward / _backward    embedding lookup, its gradient by
+ *                                         sorted tokens
+ *   fsdp_gated_scan_forward / _backward   gated linear recurrence over
+ *                                         sequences
+ *   fsdp_distill_loss_forward / _backward distillation from a teacher's top
+ *                                         logits
+ *   fsdp_policy_loss_forward / _backward  clipped policy loss with a KL term
  *
  * The backward calls read the 8-bit checkpoints in place of the tensors they
  * were taken from, and write gradients in the dtypes that
@@ -211,6 +218,189 @@ fsdp_status_t fsdp_gated_ffn_backward(const fsdp_ffn_desc_t *desc, const void *d
                                       const void *w_gate, const void *w_up, const void *gate, const void *up,
                                       void *dx, void *dw_gate, void *dw_up, void *workspace,
                                       int64_t workspace_bytes, fsdp_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Embedding lookup and its gradient.
+ *   out[i] = scale * weight[tokens[i]]
+ *   dweight[v] = (dweight[v] +) scale * sum over i with tokens[i] = v of dout[i]
+ * A token outside [0, vocab) (padding) gives a row of zeros and no gradient.
+ * The gradient's rows are summed in binary32 in the order of i, in pieces whose
+ * length depends on the sizes alone, and rounded once.
+ */
+#define FSDP_INDEX_I32 0
+#define FSDP_INDEX_I64 1
+
+typedef struct {
+  int64_t rows;         /* tokens, 0 .. 2^31 - 1 */
+  int64_t vocab;        /* rows of weight, 1 .. 2^31 - 2 */
+  int64_t cols;         /* features, >= 1 */
+  int64_t ld_weight;    /* row distance of weight (forward) or dweight (backward) */
+  int64_t ld_out;       /* row distance of out (forward) or dout (backward) */
+  int32_t token_dtype;  /* FSDP_INDEX_I32 or _I64 */
+  int32_t weight_dtype; /* F32 or BF16, of weight or dweight */
+  int32_t out_dtype;    /* F32 or BF16, of out or dout */
+  int32_t accumulate;   /* backward: 0 writes all of dweight, rows without tokens as 0;
+                           1 adds to it and leaves those rows as they were (a tied output
+                           layer's gradient is there already) */
+  float scale;          /* finite */
+} fsdp_embedding_desc_t;
+
+/* tokens: rows indices; weight [vocab, cols]; out [rows, cols]. */
+fsdp_status_t fsdp_embedding_forward(const fsdp_embedding_desc_t *desc, const void *tokens, const void *weight, void *out,
+                                     fsdp_stream_t stream);
+
+/* dout [rows, cols]; dweight [vocab, cols]; workspace: fsdp_embedding_workspace bytes. */
+fsdp_status_t fsdp_embedding_backward(const fsdp_embedding_desc_t *desc, const void *tokens, const void *dout,
+                                      void *dweight, void *workspace, int64_t workspace_bytes, fsdp_stream_t stream);
+
+/* Bytes of workspace of the backward call: the tokens' order and partial sums of
+ * rows that many tokens share. */
+fsdp_status_t fsdp_embedding_workspace(const fsdp_embedding_desc_t *desc, int64_t *bytes);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Gated linear recurrence along the rows of each sequence, every column on its own:
+ *   a_t = 1 / (1 + e^-(gate_t + bias)),   h_t = a_t h_(t-1) + (1 - a_t) x_t
+ * from the sequence's initial state, and for the backward pass, with
+ * D_t = dh_t + a_(t+1) D_(t+1) (at a sequence's last row dh_t + dfinal):
+ *   dx_t = (1 - a_t) D_t,   dgate_t = D_t (h_(t-1) - x_t) a_t (1 - a_t),
+ *   dbias = sum of dgate over the rows of all sequences,   dinitial = a_1 D_1
+ * States and sums are binary32.  One row a sequence is a step of generation: pass the
+ * states in `initial` and receive them in `final`, which may be the same buffer.
+ *
+ * The rows of a batch are its sequences one after another: `seqs` of `seq_len` rows each,
+ * or with `packed` sequence s from row offsets[s] up to offsets[s + 1], where offsets has
+ * seqs + 1 device values that do not decrease and lie in [0, rows].  Rows outside every
+ * sequence (behind the last, say) are neither read into a result nor written, and a
+ * sequence without rows passes its state on (final = initial, dinitial = dfinal).
+ * Offsets that break this give unspecified results within the arrays, no other access.
+ */
+typedef struct {
+  int64_t rows, cols;          /* of x; rows >= 0, cols >= 1 */
+  int64_t seqs;                /* sequences, >= 0 */
+  int64_t seq_len;             /* rows of each, with packed = 0: rows = seqs * seq_len */
+  int64_t ld_x, ld_gate;       /* row distances */
+  int64_t ld_h;                /* of h (forward) or dh (backward) */
+  int64_t ld_dx, ld_dgate;
+  int32_t packed;              /* 1: offsets say where sequences are; seq_len is ignored */
+  int32_t offset_dtype;        /* FSDP_INDEX_I32 or _I64 */
+  int32_t x_dtype;             /* F32 or BF16, of x and gate */
+  int32_t h_dtype;             /* F32 or BF16, of h or dh */
+  int32_t dx_dtype;            /* F32 or BF16, of dx and dgate */
+  int32_t param_dtype;         /* F32 or BF16, of bias */
+  int32_t grad_dtype;          /* F32 or BF16, of dbias */
+} fsdp_scan_desc_t;
+
+/* Rows of the matrix [n, cols] of binary32 that a forward call fills for the backward call
+ * (states some rows apart, from which the backward call makes h again): n depends on rows
+ * and cols alone. */
+fsdp_status_t fsdp_gated_scan_states(int64_t rows, int64_t cols, int64_t *n);
+
+/* Bytes of workspace of the forward (backward = 0) or backward call. */
+fsdp_status_t fsdp_gated_scan_workspace(const fsdp_scan_desc_t *desc, int32_t backward, int64_t *bytes);
+
+/*
+ *   x, gate, h [rows, cols];  bias: cols elements, or NULL for 0.
+ *   initial: [seqs, cols] binary32 without gaps, or NULL for 0;  final: the same, written,
+ *            or NULL.
+ *   offsets: seqs + 1 device values with packed, else NULL.
+ *   states:  what the backward call needs, or NULL.
+ */
+fsdp_status_t fsdp_gated_scan_forward(const fsdp_scan_desc_t *desc, const void *x, const void *gate, const void *bias,
+                                      const float *initial, const void *offsets, void *h, float *final,
+                                      float *states, void *workspace, int64_t workspace_bytes, fsdp_stream_t stream);
+
+/*
+ *   x, gate, bias, initial, offsets: as in the forward call;  states: what it wrote.
+ *   dh [rows, cols];  dfinal: [seqs, cols] binary32, or NULL for 0.
+ *   dx, dgate [rows, cols], both written;  dbias (cols elements) and dinitial ([seqs, cols]
+ *   binary32): written, or NULL if not wanted.
+ */
+fsdp_status_t fsdp_gated_scan_backward(const fsdp_scan_desc_t *desc, const void *dh, const void *x, const void *gate,
+                                       const void *bias, const float *initial, const void *offsets,
+                                       const float *states, const float *dfinal, void *dx, void *dgate, void *dbias,
+                                       float *dinitial, void *workspace, int64_t workspace_bytes, fsdp_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Losses over rows of logits z [rows, vocab].  With p = softmax(z / T) of a row and
+ * lse = log sum e^(z / T):
+ *
+ * Distillation from a teacher's top logits: entries j of a row name tokens and the
+ * teacher's logits for them; q is the softmax of those logits / T over the row's entries.
+ *   loss = weight T^2 sum_j q_j (log q_j - log p_(token j))
+ *   dlogits_i = dloss weight T (p_i - sum of q_j over entries with token j = i)
+ * Entries with a token outside [0, vocab), or a logit of -infinity, do not count; a row
+ * without entries has loss and gradient 0.  A token may be named more than once.
+ *
+ * Clipped policy loss: token a was taken with log-probability old_logp and advantage A.
+ * With logp = z_a / T - lse, r = e^(logp - old_logp), and k = ref_logp - logp:
+ *   loss = weight (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl (e^k - k - 1))
+ *   dlogits_i = dloss weight c / T ([i = a] - p_i),
+ *   c = (r A <= clip(r) A ? -r A : 0) + kl (1 - e^k)
+ * old_logp NULL: r is 1 (and its derivative r).  ref_logp NULL: no KL term.  A row whose token
+ * is outside [0, vocab) has loss, logp and gradient 0 (and its lse).
+ *
+ * A row of weight 0 is not read: its loss, logp, lse and gradient are written as 0, whatever
+ * its logits hold.  Sums are binary32.  Logits of -infinity have probability 0.
+ *
+ * With dlogits given, the forward call also writes the gradient of the sum of the rows'
+ * losses (dloss = 1), for which a row stays on the chip; the backward call computes it from
+ * the lse (and logp) of a forward call.  dlogits may be logits itself, with the same row
+ * distance and dtype; no other overlap is allowed.
+ */
+#define FSDP_DISTILL_MAX_TOP 1024
+
+typedef struct {
+  int64_t rows, vocab;         /* rows >= 0, vocab 1 .. 2^31 - 1 */
+  int64_t ld_logits, ld_dlogits;
+  int64_t top;                 /* entries of a row, 0 .. FSDP_DISTILL_MAX_TOP */
+  int64_t ld_tokens, ld_teacher;
+  int32_t logits_dtype, dlogits_dtype, teacher_dtype; /* F32 or BF16 */
+  int32_t token_dtype;         /* FSDP_INDEX_I32 or _I64 */
+  float temperature;           /* T, finite and > 0 */
+} fsdp_distill_desc_t;
+
+/*
+ *   logits [rows, vocab];  teacher_tokens, teacher_logits [rows, top];  weight: rows binary32
+ *   values, or NULL for 1.
+ *   loss, lse: rows binary32 values, written;  dlogits [rows, vocab], or NULL.
+ */
+fsdp_status_t fsdp_distill_loss_forward(const fsdp_distill_desc_t *desc, const void *logits, const void *teacher_tokens,
+                                        const void *teacher_logits, const float *weight, float *loss, float *lse,
+                                        void *dlogits, fsdp_stream_t stream);
+
+/* dloss: rows binary32 values, or NULL for 1. */
+fsdp_status_t fsdp_distill_loss_backward(const fsdp_distill_desc_t *desc, const void *logits, const void *teacher_tokens,
+                                         const void *teacher_logits, const float *weight, const float *lse,
+                                         const float *dloss, void *dlogits, fsdp_stream_t stream);
+
+typedef struct {
+  int64_t rows, vocab;         /* rows >= 0, vocab 1 .. 2^31 - 1 */
+  int64_t ld_logits, ld_dlogits;
+  int32_t logits_dtype, dlogits_dtype; /* F32 or BF16 */
+  int32_t token_dtype;         /* FSDP_INDEX_I32 or _I64 */
+  float temperature;           /* T, finite and > 0 */
+  float clip_low, clip_high;   /* >= 0; infinity: no bound */
+  float kl;                    /* weight of the KL term, finite, >= 0 */
+} fsdp_policy_desc_t;
+
+/*
+ *   tokens: rows indices;  old_logp, ref_logp, advantage, weight: rows binary32 values each
+ *   (old_logp, ref_logp and weight may be NULL).
+ *   loss, logp, lse: rows binary32 values, written;  dlogits [rows, vocab], or NULL.
+ */
+fsdp_status_t fsdp_policy_loss_forward(const fsdp_policy_desc_t *desc, const void *logits, const void *tokens,
+                                       const float *old_logp, const float *ref_logp, const float *advantage,
+                                       const float *weight, float *loss, float *logp, float *lse, void *dlogits,
+                                       fsdp_stream_t stream);
+
+/* logp, lse: what the forward call wrote;  dloss: rows binary32 values, or NULL for 1. */
+fsdp_status_t fsdp_policy_loss_backward(const fsdp_policy_desc_t *desc, const void *logits, const void *tokens,
+                                        const float *old_logp, const float *ref_logp, const float *advantage,
+                                        const float *weight, const float *logp, const float *lse, const float *dloss,
+                                        void *dlogits, fsdp_stream_t stream);
 
 /* Synchronise `stream`, then say whether a wait of this header's kernels gave
  * up.  Failures are counted per device, for all streams and threads of the
