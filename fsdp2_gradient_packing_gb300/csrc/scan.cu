@@ -1,8 +1,24 @@
 // Gated linear recurrence (fsdp_gated_scan_*): a = sigmoid(gate + bias),
 // h_t = a_t h_(t-1) + (1 - a_t) x_t, forward and backward.
 //
-// A thread to a sequence and a column, row by row.  Backward, the state before each tile
-// of kTileRows rows comes from the forward pass and the tile's states are made again.
+// Rows are cut into tiles of 8 WARPS rows and 64 columns, whatever sequences they belong to;
+// where one begins, the state before it is its own initial one.  A thread has two columns and
+// kSteps rows.  Its rows take a state h to A h + B; so do a warp's, one behind the other, and a
+// tile's.  A tile makes its A and B known, then looks back over the tiles before it for the
+// nearest one whose state behind its last row is known, and comes from there to its own start by
+// the A and B in between.  So every matrix is read and written once and long sequences keep all
+// SMs busy.  Tiles are handed out in the order of their rows, so what a tile waits for has begun;
+// a wait is bounded.  Whatever a tile finds known when it looks back, the state at its start is the
+// same chain of A h + B from the sequence's start, so results are the same bits on every run.
+//
+// What bounds it is the time from a tile's rows to its carry, so that is kept short: the next
+// tile's rows are on their way into shared memory meanwhile (cp.async, two stages), and the values
+// that tiles leave for one another are their own flags (all ones: not there yet), which costs no
+// fence and one trip to L2 instead of two.
+//
+// Backward the same goes from the last row to the first, with a_t D_t in place of the state.
+// The states are made again from those that the forward pass keeps every kStateRows rows:
+// 4 bytes a column instead of a read of h, and in binary32.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -11,90 +27,552 @@
 
 #include "layout.h"
 #include "ops.h"
+#include "tc.h"
 
 namespace fsdp {
 namespace scan {
 namespace {
 
-constexpr int kTileRows = 128, kThreads = 128;
+constexpr int kSteps = 8, kCols = 64;
+constexpr int kStateRows = 64;
+// Warps of a block, each with kSteps rows: as many as the look-back takes in at once.
+constexpr int warps_of(bool f32) { return f32 ? 8 : 16; }
 
 struct Args {
   const void *x, *gate, *bias, *offsets, *dh;
   const float *initial, *dfinal, *states_in;
   void *h, *dx, *dgate;
   float *final_state, *dinitial, *states, *partial;
+  uint2 *parts;        // [time tiles][padded columns]: A and B
+  uint32_t *carried;   // [time tiles][padded columns]: the state behind the tile
+  uint32_t *ticket;
+  int32_t *begins, *ends;  // packed: the sequence that begins or ends at a row, or -1
+  uint32_t *gave_up;
+  uint64_t wait_limit_ns;
   int64_t rows, cols, seqs, seq_len, ld_x, ld_gate, ld_h, ld_dx, ld_dgate;
-  int32_t packed, wide, x_bf16, h_bf16, dx_bf16, param_bf16;
+  int64_t padded_cols;  // whole column tiles
+  uint32_t column_tiles, time_tiles, tiles;
+  int32_t packed, wide, h_bf16, dx_bf16, param_bf16, fault;
 };
 
 __device__ __forceinline__ int64_t offset_at(const Args &a, int64_t s) {
-  if (!a.packed) return s * a.seq_len;
   const int64_t o = a.wide ? static_cast<const int64_t *>(a.offsets)[s] : static_cast<const int32_t *>(a.offsets)[s];
   return min(max(o, (int64_t)0), a.rows);
 }
-__device__ __forceinline__ void gates(float z, float &a, float &keep) {
-  const float e = expf(-fabsf(z)), big = 1.0f / (1.0f + e), small = e * big;
-  a = z >= 0 ? big : small, keep = z >= 0 ? small : big;
+
+// a = 1 / (1 + e^-z) and 1 - a = e^-z a, each to a few ulp of its own size.  Where e^-z is far above 1, up
+// to infinity, 1 - a is 1: the product with an a of 0 would be a NaN.
+__device__ __forceinline__ void gates(float2 z, float2 &a, float2 &keep) {
+  const float2 t = __fmul2_rn(z, both(-1.4426950408889634f));
+  float2 e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  const float2 d = __fadd2_rn(e, both(1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a.y) : "f"(d.y));
+  const float2 k = __fmul2_rn(e, a);
+  keep = make_float2(t.x > 100.0f ? 1.0f : k.x, t.y > 100.0f ? 1.0f : k.y);
+}
+// Both as one number, the lesser of them, negative where that is a; and back, the other rounded once.
+__device__ __forceinline__ float2 join(float2 a, float2 keep) {
+  return make_float2(a.x < keep.x ? -a.x : keep.x, a.y < keep.y ? -a.y : keep.y);
+}
+__device__ __forceinline__ void split(float2 gate, float2 &a, float2 &keep) {
+  const float2 q = make_float2(fabsf(gate.x), fabsf(gate.y)), p = __ffma2_rn(q, both(-1.0f), both(1.0f));
+  const bool nx = __float_as_int(gate.x) < 0, ny = __float_as_int(gate.y) < 0;
+  a = make_float2(nx ? q.x : p.x, ny ? q.y : p.y), keep = make_float2(nx ? p.x : q.x, ny ? p.y : q.y);
 }
 
-__global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant__ Args a) {
-  const int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (j >= a.cols) return;
-  const float bias = a.bias ? load_any(a.bias, j, a.param_bf16) : 0.0f;
-  for (int64_t s = blockIdx.y; s < a.seqs; s += gridDim.y) {
-    const int64_t begin = offset_at(a, s), end = offset_at(a, s + 1);
-    float h = a.initial ? a.initial[s * a.cols + j] : 0.0f;
-    for (int64_t t = begin; t < end; ++t) {
-      if (a.states && t % kTileRows == 0) a.states[t / kTileRows * a.cols + j] = h;
-      float g, keep;
-      gates(load_any(a.gate, t * a.ld_gate + j, a.x_bf16) + bias, g, keep);
-      h = fmaf(g, h, keep * load_any(a.x, t * a.ld_x + j, a.x_bf16));
-      store_any(a.h, t * a.ld_h + j, a.h_bf16, h);
+// Two columns of a lane, neighbours (VEC) or 32 apart, of a row in global or shared memory.
+template <bool VEC>
+__device__ __forceinline__ float2 get(const void *p, int64_t at, bool bf16, bool there, bool second) {
+  if (!there) return make_float2(0, 0);
+  if constexpr (VEC) {
+    if (bf16) {
+      const uint32_t r = *reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p) + at);
+      return make_float2(bf16_low(r), bf16_high(r));
     }
-    if (a.final_state) a.final_state[s * a.cols + j] = h;
+    return *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + at);
+  } else {
+    return make_float2(load_any(p, at, bf16), second ? load_any(p, at + 32, bf16) : 0.0f);
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void put(void *p, int64_t at, bool bf16, bool second, float2 v) {
+  if constexpr (VEC) {
+    if (bf16)
+      *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p) + at) = bf16_pair(v.x, v.y);
+    else
+      *reinterpret_cast<float2 *>(static_cast<float *>(p) + at) = v;
+  } else {
+    store_any(p, at, bf16, v.x);
+    if (second) store_any(p, at + 32, bf16, v.y);
+  }
+}
+// Two columns of a matrix of binary32 values that is aligned to nothing more.
+template <bool VEC>
+__device__ __forceinline__ float2 get_f32(const float *p, bool second) {
+  return make_float2(p[0], second ? p[VEC ? 1 : 32] : 0.0f);
+}
+template <bool VEC>
+__device__ __forceinline__ void put_f32(float *p, bool second, float2 v) {
+  p[0] = v.x;
+  if (second) p[VEC ? 1 : 32] = v.y;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+// The sequence that begins (shift 0) or ends (shift 1) at row t, or -1.
+__device__ __forceinline__ int32_t mark_at(const Args &a, const int32_t *marks, int64_t t, int32_t shift) {
+  if (t >= a.rows) return -1;
+  if (a.packed) return marks[t];
+  const uint32_t u = (uint32_t)t + shift, n = (uint32_t)a.seq_len, q = u / n;
+  return q * n == u ? (int32_t)q - shift : -1;
+}
+
+template <int WARPS>
+struct Shared {
+  float2 a[WARPS][32], b[WARPS][32];
+  float2 forward[WARPS][32];  // backward pass: B of the states
+  uint4 look[WARPS][32];      // what earlier tiles have left: A and B, or the state
+  float2 carry[32];
+  uint32_t cut[WARPS], found[WARPS], ticket, stop;
+};
+
+// One tensor's rows of a tile on their way into shared memory: rows of kCols elements, 16-byte
+// units, zeros outside the matrix.
+template <int WARPS>
+__device__ __forceinline__ void fetch(uint8_t *to, const void *from, int64_t ld, int size_log2, int64_t first, int64_t column, const Args &a) {
+  const int units_log2 = 2 + size_log2;  // 16-byte units of a row
+  const int64_t unit_cols = 16 >> size_log2;
+#pragma unroll 4
+  for (int c = threadIdx.x; c < (WARPS * kSteps) << units_log2; c += WARPS * 32) {
+    const int r = c >> units_log2;
+    const int64_t j = column + (c & ((1 << units_log2) - 1)) * unit_cols;
+    const bool there = first + r < a.rows && j < a.cols;
+    const uint8_t *src = static_cast<const uint8_t *>(from) + (there ? (((first + r) * ld + j) << size_log2) : 0);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem(to) + c * 16), "l"(src), "r"(there ? 16 : 0) : "memory");
   }
 }
 
-__global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ Args a) {
-  const int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (j >= a.cols) return;
-  const float bias = a.bias ? load_any(a.bias, j, a.param_bf16) : 0.0f;
-  for (int64_t s = blockIdx.y; s < a.seqs; s += gridDim.y) {
-    const int64_t begin = offset_at(a, s), end = offset_at(a, s + 1);
-    float d = a.dfinal ? a.dfinal[s * a.cols + j] : 0.0f, db = 0.0f;
-    for (int64_t hi = end; hi > begin;) {
-      const int64_t lo = max(begin, (hi - 1) / kTileRows * kTileRows);
-      float before[kTileRows];
-      float h = lo == begin ? (a.initial ? a.initial[s * a.cols + j] : 0.0f) : a.states_in[lo / kTileRows * a.cols + j];
-      for (int64_t t = lo; t < hi; ++t) {
-        before[t - lo] = h;
-        float g, keep;
-        gates(load_any(a.gate, t * a.ld_gate + j, a.x_bf16) + bias, g, keep);
-        h = fmaf(g, h, keep * load_any(a.x, t * a.ld_x + j, a.x_bf16));
+// Where a tile, this lane's columns and this warp's rows are.
+template <int WARPS, bool VEC>
+struct Place {
+  int64_t tile, column, first;  // time tile; first column of the lane; first row of the warp
+  int64_t at0;                  // of the lane among the values that tiles leave
+  bool in, second;              // whether the lane's columns exist
+  __device__ Place(const Args &a, uint32_t ticket, bool backward) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t q = ticket / a.column_tiles;
+    tile = backward ? a.time_tiles - 1 - q : q;
+    const int64_t left = (int64_t)(ticket - q * a.column_tiles) * kCols;
+    column = left + (VEC ? 2 * lane : lane);
+    at0 = left + 2 * lane;
+    first = tile * (WARPS * kSteps) + threadIdx.x / 32 * kSteps;
+    in = column < a.cols, second = column + (VEC ? 1 : 32) < a.cols;
+  }
+};
+
+// Boundaries in a warp's rows: bit i for row first + i; lane i has the sequence.
+struct Marks {
+  int32_t begin, end;
+  uint32_t begins, ends, valid;
+  __device__ Marks(const Args &a, int64_t first, int64_t lo, int64_t hi) {
+    const int lane = threadIdx.x & 31;
+    begin = end = -1;
+    const int64_t t = first + lane;
+    if (lane < kSteps) begin = mark_at(a, a.begins, t, 0), end = mark_at(a, a.ends, t, 1);
+    begins = __ballot_sync(0xFFFFFFFFu, begin >= 0), ends = __ballot_sync(0xFFFFFFFFu, end >= 0);
+    valid = __ballot_sync(0xFFFFFFFFu, lane < kSteps && t >= lo && t < hi);
+  }
+  __device__ bool plain() const { return (begins | ends) == 0 && valid == (1u << kSteps) - 1; }
+};
+
+// Values that tiles leave for others.  All ones means not there yet; the NaN of that pattern
+// is left as another one.
+__device__ __forceinline__ uint32_t as_left(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u == 0xFFFFFFFFu ? 0x7FFFFFFFu : u;
+}
+__device__ __forceinline__ void leave_part(const Args &a, int64_t at, float2 A, float2 B) {
+  asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(a.parts + at),
+               "l"((uint64_t)as_left(B.x) << 32 | as_left(A.x)), "l"((uint64_t)as_left(B.y) << 32 | as_left(A.y))
+               : "memory");
+}
+__device__ __forceinline__ void leave_state(const Args &a, int64_t at, float2 s) {
+  asm volatile("st.relaxed.gpu.global.v2.b32 [%0], {%1, %2};" ::"l"(a.carried + at), "r"(as_left(s.x)), "r"(as_left(s.y)) : "memory");
+}
+
+// All warps: the state that comes into a tile from `towards` (-1: the tiles before it, 1: those
+// behind).  Warp w reads what the tile w + 1 away has left.  In s.carry of warp 0's lanes.
+template <int WARPS>
+__device__ __forceinline__ float2 look_back(const Args &a, Shared<WARPS> &s, int64_t tile, int towards, int64_t at0) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int64_t other = tile + (int64_t)towards * (1 + warp);
+  const bool exists = other >= 0 && other < a.time_tiles;
+  const uint64_t began = tc::now_ns();
+  for (;;) {
+    uint32_t found = 0;  // 1: A and B, 2: the state
+    uint64_t p0 = 0, p1 = 0;
+    uint32_t c0 = 0, c1 = 0;
+    for (uint32_t n = 1; exists; ++n) {
+      const int64_t at = other * a.padded_cols + at0;
+      asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(p0), "=l"(p1) : "l"(a.parts + at) : "memory");
+      asm volatile("ld.relaxed.gpu.global.v2.b32 {%0, %1}, [%2];" : "=r"(c0), "=r"(c1) : "l"(a.carried + at) : "memory");
+      const bool state = c0 != 0xFFFFFFFFu && c1 != 0xFFFFFFFFu;
+      const bool part = (uint32_t)p0 != 0xFFFFFFFFu && (uint32_t)p1 != 0xFFFFFFFFu && p0 >> 32 != 0xFFFFFFFFu && p1 >> 32 != 0xFFFFFFFFu;
+      found = __all_sync(0xFFFFFFFFu, state) ? 2 : __all_sync(0xFFFFFFFFu, part) ? 1 : 0;
+      if (found) break;
+      if ((n & 15u) == 0 && __shfl_sync(0xFFFFFFFFu, tc::now_ns() - began > a.wait_limit_ns || *(volatile uint32_t *)&s.stop, 0)) {
+        break;
       }
-      for (int64_t t = hi - 1; t >= lo; --t) {
-        float g, keep;
-        gates(load_any(a.gate, t * a.ld_gate + j, a.x_bf16) + bias, g, keep);
-        d += load_any(a.dh, t * a.ld_h + j, a.h_bf16);
-        const float dz = d * (before[t - lo] - load_any(a.x, t * a.ld_x + j, a.x_bf16)) * (g * keep);
-        store_any(a.dx, t * a.ld_dx + j, a.dx_bf16, keep * d);
-        store_any(a.dgate, t * a.ld_dgate + j, a.dx_bf16, dz);
-        db += dz;
-        d *= g;
-      }
-      hi = lo;
     }
-    if (a.dinitial) a.dinitial[s * a.cols + j] = d;
-    if (a.partial) a.partial[s * a.cols + j] = db;
+    if (tc::now_ns() - began > a.wait_limit_ns && found != 2 && exists) s.stop = 1;  // before the barrier: all threads see the same
+    s.look[warp][lane] = found == 2 ? make_uint4(c0, 0, c1, 0) : make_uint4((uint32_t)p0, (uint32_t)(p0 >> 32), (uint32_t)p1, (uint32_t)(p1 >> 32));
+    if (lane == 0) s.found[warp] = found;
+    __syncthreads();
+    const uint32_t states = __ballot_sync(0xFFFFFFFFu, lane < WARPS && s.found[lane % WARPS] == 2);
+    float2 carry = make_float2(0, 0);
+    if (s.stop) return carry;
+    if (states) {
+      if (warp == 0) {
+        const int back = __ffs(states) - 1;
+        const uint4 r = s.look[back][lane];
+        carry = make_float2(__uint_as_float(r.x), __uint_as_float(r.z));
+        for (int w = back - 1; w >= 0; --w) {
+          const uint4 q = s.look[w][lane];
+          carry = fma2(make_float2(__uint_as_float(q.x), __uint_as_float(q.z)), carry, make_float2(__uint_as_float(q.y), __uint_as_float(q.w)));
+        }
+      }
+      return carry;
+    }
+    __syncthreads();  // none of them knows its state yet
   }
 }
 
-__global__ void __launch_bounds__(kThreads) column_sum_kernel(const float *partial, int64_t n, int64_t cols, void *out, int32_t bf16) {
-  const int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (j >= cols) return;
+// Between a tile's warps: A and B of the whole (from the first warp to the last, or backward the other
+// way), left for other tiles, and the state that comes in.  `cut`: which warps let nothing
+// through; `alone`: nothing comes into the tile.
+template <int WARPS, bool BACKWARD>
+__device__ __forceinline__ void carry_over(const Args &a, Shared<WARPS> &s, int64_t tile, int64_t at0, bool alone) {
+  constexpr uint32_t kBit = BACKWARD ? 2 : 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  float2 A = both(1.0f), B = both(0.0f), carry = both(0.0f);
+  bool cut = false;
+  const bool last = tile == (BACKWARD ? 0 : a.time_tiles - 1);  // nothing goes out
+  const int64_t at = tile * a.padded_cols + at0;
+  if (a.time_tiles > 1) {
+    if (warp == 0 && !last) {
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) {
+        const int w = BACKWARD ? WARPS - 1 - k : k;
+        const bool c = s.cut[w] & kBit;
+        A = __fmul2_rn(A, s.a[w][lane]);
+        B = c ? s.b[w][lane] : fma2(s.a[w][lane], B, s.b[w][lane]);
+        cut |= c;
+      }
+      if (!cut && !alone)
+        leave_part(a, at, A, B);
+      else if (!(a.fault & 1) || tile != (BACKWARD ? a.time_tiles - 1 : 0))  // the test hook leaves out the first
+        leave_state(a, at, B);
+    }
+    if (!alone) {
+      carry = look_back<WARPS>(a, s, tile, BACKWARD ? 1 : -1, at0);
+      if (warp == 0 && !last && !cut) leave_state(a, at, fma2(A, carry, B));
+    }
+  }
+  if (warp == 0) s.carry[lane] = carry;
+}
+
+template <class T, bool VEC, bool STAGED, bool BACKWARD>
+struct Tile {
+  static constexpr int W = warps_of(sizeof(T) == 4), kApart = VEC ? 1 : 32, kRows = W * kSteps;
+  static constexpr bool kBf16 = sizeof(T) == 2;
+  static constexpr int kMatrix = kRows * kCols * (int)sizeof(T);           // bytes of x or gate in a stage
+  static constexpr int kStage = STAGED ? (BACKWARD ? 3 : 2) * kMatrix : 0;  // dh is no wider than x where staged
+  static constexpr int kSmem = 2 * kStage;
+
+  __device__ static void start(const Args &a, uint8_t *stage, uint32_t ticket) {
+    if constexpr (STAGED) {
+      if (ticket < a.tiles) {
+        const uint32_t q = ticket / a.column_tiles;
+        const int64_t first = (int64_t)(BACKWARD ? a.time_tiles - 1 - q : q) * kRows, column = (int64_t)(ticket - q * a.column_tiles) * kCols;
+        fetch<W>(stage, a.x, a.ld_x, kBf16 ? 1 : 2, first, column, a);
+        fetch<W>(stage + kMatrix, a.gate, a.ld_gate, kBf16 ? 1 : 2, first, column, a);
+        if constexpr (BACKWARD) fetch<W>(stage + 2 * kMatrix, a.dh, a.ld_h, a.h_bf16 ? 1 : 2, first, column, a);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  }
+  // Row i of the warp's in x, gate or dh (m 0, 1, 2).
+  __device__ __forceinline__ static float2 row(const Args &a, const uint8_t *stage, const Place<W, VEC> &at, int m, int i) {
+    const bool bf16 = m == 2 ? a.h_bf16 != 0 : kBf16;
+    if constexpr (STAGED) {
+      return get<VEC>(stage + m * kMatrix, (threadIdx.x / 32 * kSteps + i) * kCols + 2 * (threadIdx.x & 31), bf16, true, true);
+    } else {
+      const void *p = m == 0 ? a.x : m == 1 ? a.gate : a.dh;
+      const int64_t ld = m == 0 ? a.ld_x : m == 1 ? a.ld_gate : a.ld_h, t = at.first + i;
+      return get<VEC>(p, t * ld + at.column, bf16, at.in && t < a.rows, at.second);
+    }
+  }
+  __device__ static float2 bias(const Args &a, const Place<W, VEC> &at) {
+    if (!a.bias || !at.in) return make_float2(0, 0);
+    return make_float2(load_any(a.bias, at.column, a.param_bf16), at.second ? load_any(a.bias, at.column + kApart, a.param_bf16) : 0.0f);
+  }
+  // A lane's columns of row s of `initial` or `dfinal`.
+  __device__ __forceinline__ static float2 given(const Args &a, const float *p, int32_t s, const Place<W, VEC> &at) {
+    return p && at.in ? get_f32<VEC>(p + (int64_t)s * a.cols + at.column, at.second) : both(0.0f);
+  }
+  // One tile, from its stage; starts the next one's loads into the other stage, and returns its ticket.
+  __device__ static uint32_t forward(const Args &a, Shared<W> &sh, uint8_t *stage, uint8_t *other, uint32_t ticket, int64_t lo, int64_t hi);
+  __device__ static uint32_t backward(const Args &a, Shared<W> &sh, uint8_t *stage, uint8_t *other, uint32_t ticket, int64_t lo, int64_t hi);
+};
+
+// A warp's A: 1 - K, where K is the recurrence's answer to inputs of 1, or the rows' product where that is
+// the smaller: near 1, as a slow column's is, a product of rounded factors would lose a rounding a row.
+__device__ __forceinline__ float2 factor(float2 product, float2 K) {
+  return make_float2(K.x < 0.5f ? 1.0f - K.x : product.x, K.y < 0.5f ? 1.0f - K.y : product.y);
+}
+
+template <class T, bool VEC, bool STAGED, bool BACKWARD>
+__device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::forward(const Args &a, Shared<W> &sh, uint8_t *stage, uint8_t *other,
+                                                                           uint32_t ticket, int64_t lo, int64_t hi) {
+  const Place<W, VEC> at(a, ticket, false);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const float2 shift = bias(a, at);
+  const Marks m(a, at.first, lo, hi);
+  const bool plain = m.plain();
+  // A row takes h to f h + b.
+  float2 f[kSteps], b[kSteps], A = both(1.0f), B = both(0.0f), K = both(0.0f);
+  if (plain) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      float2 keep;
+      gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f[i], keep);
+      b[i] = __fmul2_rn(keep, row(a, stage, at, 0, i));
+      A = __fmul2_rn(A, f[i]), B = fma2(f[i], B, b[i]), K = fma2(f[i], K, keep);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      float2 keep;
+      gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f[i], keep);
+      b[i] = __fmul2_rn(keep, row(a, stage, at, 0, i));
+      if (!(m.valid >> i & 1)) f[i] = both(1.0f), keep = b[i] = both(0.0f);
+      if (m.begins >> i & 1) {
+        b[i] = fma2(f[i], given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at), b[i]);
+        B = b[i];
+      } else {
+        A = __fmul2_rn(A, f[i]), B = fma2(f[i], B, b[i]), K = fma2(f[i], K, keep);
+      }
+    }
+  }
+  sh.a[warp][lane] = factor(A, K);
+  sh.b[warp][lane] = B;
+  if (lane == 0) sh.cut[warp] = m.begins ? 1 : 0;
+  __syncthreads();
+  const uint32_t next = sh.ticket;
+  start(a, other, next);
+  const bool alone = at.tile == 0 || mark_at(a, a.begins, at.tile * kRows, 0) >= 0;
+  carry_over<W, false>(a, sh, at.tile, at.at0, alone);
+  __syncthreads();
+  float2 h = sh.carry[lane];
+  for (int w = 0; w < warp; ++w) h = sh.cut[w] ? sh.b[w][lane] : fma2(sh.a[w][lane], h, sh.b[w][lane]);
+  if (a.states && at.in && at.first % kStateRows == 0 && at.first < a.rows)
+    put_f32<VEC>(a.states + at.first / kStateRows * a.cols + at.column, at.second, h);
+  if (plain) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      h = fma2(f[i], h, b[i]);
+      if (at.in) put<VEC>(a.h, (at.first + i) * a.ld_h + at.column, a.h_bf16, at.second, h);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      h = m.begins >> i & 1 ? b[i] : fma2(f[i], h, b[i]);
+      if (at.in && (m.valid >> i & 1)) put<VEC>(a.h, (at.first + i) * a.ld_h + at.column, a.h_bf16, at.second, h);
+      if (m.ends >> i & 1) {
+        const int32_t s = __shfl_sync(0xFFFFFFFFu, m.end, i);
+        if (at.in && a.final_state) put_f32<VEC>(a.final_state + (int64_t)s * a.cols + at.column, at.second, h);
+      }
+    }
+  }
+  return next;
+}
+
+template <class T, bool VEC, bool STAGED, bool BACKWARD>
+__device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::backward(const Args &a, Shared<W> &sh, uint8_t *stage, uint8_t *other,
+                                                                            uint32_t ticket, int64_t lo, int64_t hi) {
+  const Place<W, VEC> at(a, ticket, true);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const float2 shift = bias(a, at);
+  const Marks m(a, at.first, lo, hi);
+  const bool plain = m.plain();
+  // The state before the warp's rows comes from the nearest kept one above.
+  constexpr int kPer = kStateRows / kSteps;  // warps to a kept state
+  const int64_t kept = (at.tile * kRows + warp / kPer * kStateRows) / kStateRows;
+  float2 h = at.in && kept * kStateRows < a.rows ? get_f32<VEC>(a.states_in + kept * a.cols + at.column, at.second) : both(0.0f);
+  // States go A h + B over the warp's rows; e = a_(t+1) D_(t+1) comes in from below and leaves as
+  // A e + C.
+  float2 A = both(1.0f), B = both(0.0f), C = both(0.0f), K = both(0.0f);
+  if (plain) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      float2 f, keep;
+      gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f, keep);
+      A = __fmul2_rn(A, f), K = fma2(f, K, keep);
+      B = fma2(f, B, __fmul2_rn(keep, row(a, stage, at, 0, i)));
+      C = fma2(A, row(a, stage, at, 2, i), C);
+    }
+  } else {
+    bool open = true;  // whether what comes from this row on reaches the warp's first row
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      float2 f, keep;
+      gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f, keep);
+      float2 b = __fmul2_rn(keep, row(a, stage, at, 0, i)), d = row(a, stage, at, 2, i);
+      if (!(m.valid >> i & 1)) f = both(1.0f), keep = b = d = both(0.0f);
+      if (m.begins >> i & 1) {
+        B = fma2(f, given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at), b);
+        open = false;
+      } else {
+        B = fma2(f, B, b);
+      }
+      A = __fmul2_rn(A, f), K = fma2(f, K, keep);
+      if (m.ends >> i & 1) d = __fadd2_rn(d, given(a, a.dfinal, __shfl_sync(0xFFFFFFFFu, m.end, i), at));
+      if (open) C = fma2(A, d, C);
+      if (m.ends >> i & 1) open = false;
+    }
+  }
+  sh.a[warp][lane] = factor(A, K);
+  sh.b[warp][lane] = C, sh.forward[warp][lane] = B;
+  if (lane == 0) sh.cut[warp] = (m.begins ? 1u : 0u) | (m.begins | m.ends ? 2u : 0u);
+  __syncthreads();
+  const uint32_t next = sh.ticket;
+  start(a, other, next);
+  const bool alone = at.tile == a.time_tiles - 1 || mark_at(a, a.ends, at.tile * kRows + kRows - 1, 1) >= 0;
+  carry_over<W, true>(a, sh, at.tile, at.at0, alone);
+  // Rows' slopes (h_(t-1) - x_t) a_t (1 - a_t), downwards from the warp's state.
+  for (int w = warp / kPer * kPer; w < warp; ++w) h = sh.cut[w] & 1 ? sh.forward[w][lane] : fma2(sh.a[w][lane], h, sh.forward[w][lane]);
+  float2 gate[kSteps], slope[kSteps];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const float2 z = __fadd2_rn(row(a, stage, at, 1, i), shift), x = row(a, stage, at, 0, i);
+    float2 f, keep;
+    gates(z, f, keep);
+    gate[i] = join(f, keep);
+    if (!plain && (m.begins >> i & 1)) h = given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at);
+    slope[i] = __fmul2_rn(fma2(x, both(-1.0f), h), __fmul2_rn(f, keep));
+    if (plain || (m.valid >> i & 1)) h = fma2(f, h, __fmul2_rn(keep, x));
+  }
+  __syncthreads();
+  float2 e = sh.carry[lane], db = both(0.0f);
+  for (int w = W - 1; w > warp; --w) e = sh.cut[w] & 2 ? sh.b[w][lane] : fma2(sh.a[w][lane], e, sh.b[w][lane]);
+#pragma unroll
+  for (int i = kSteps - 1; i >= 0; --i) {
+    if (!plain) {
+      if (m.ends >> i & 1) e = given(a, a.dfinal, __shfl_sync(0xFFFFFFFFu, m.end, i), at);
+      if (!(m.valid >> i & 1)) continue;  // e passes
+    }
+    float2 f, keep;
+    split(gate[i], f, keep);
+    const float2 d = __fadd2_rn(row(a, stage, at, 2, i), e), dz = __fmul2_rn(d, slope[i]);
+    if (at.in) {
+      put<VEC>(a.dx, (at.first + i) * a.ld_dx + at.column, a.dx_bf16, at.second, __fmul2_rn(keep, d));
+      put<VEC>(a.dgate, (at.first + i) * a.ld_dgate + at.column, a.dx_bf16, at.second, dz);
+    }
+    db = __fadd2_rn(db, dz);
+    e = __fmul2_rn(f, d);
+    if (!plain && (m.begins >> i & 1)) {
+      const int32_t s = __shfl_sync(0xFFFFFFFFu, m.begin, i);
+      if (at.in && a.dinitial) put_f32<VEC>(a.dinitial + (int64_t)s * a.cols + at.column, at.second, e);
+    }
+  }
+  if (a.partial) {
+    __syncthreads();
+    sh.a[warp][lane] = db;
+    __syncthreads();
+    if (warp == 0 && at.in) {
+      for (int w = 1; w < W; ++w) db = __fadd2_rn(db, sh.a[w][lane]);
+      put_f32<VEC>(a.partial + at.tile * a.cols + at.column, at.second, db);
+    }
+  }
+  return next;
+}
+
+template <class T, bool VEC, bool STAGED, bool BACKWARD>
+__global__ void __launch_bounds__(Tile<T, VEC, STAGED, BACKWARD>::W * 32, sizeof(T) == 4 ? 2 : STAGED ? 2 : 1) tile_kernel(const __grid_constant__ Args a) {
+  using Work = Tile<T, VEC, STAGED, BACKWARD>;
+  extern __shared__ __align__(128) uint8_t stages[];
+  __shared__ Shared<Work::W> sh;
+  if (threadIdx.x == 0) sh.stop = 0;
+  wait_for_previous();
+  // Tiles by ticket where they wait for one another, else by block.  A ticket is taken when the tile
+  // before it is under way, so that tiles begin in the order of their tickets.
+  const bool by_ticket = a.time_tiles > 1;
+  uint32_t now = blockIdx.x;
+  if (by_ticket) {
+    if (threadIdx.x == 0) sh.ticket = atomicAdd(a.ticket, 1u) + 1;
+    __syncthreads();
+    now = sh.ticket;
+    __syncthreads();
+  }
+  let_next_start();
+  int64_t lo = 0, hi = a.rows;
+  if (a.packed) lo = offset_at(a, 0), hi = offset_at(a, a.seqs);
+  Work::start(a, stages, now);
+  for (uint32_t n = 0; now < a.tiles; ++n) {
+    uint8_t *stage = stages + (n & 1) * Work::kStage, *other = stages + (~n & 1) * Work::kStage;
+    if (threadIdx.x == 0) sh.ticket = by_ticket ? atomicAdd(a.ticket, 1u) + 1 : now + gridDim.x;
+    if constexpr (STAGED) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();
+    }
+    now = BACKWARD ? Work::backward(a, sh, stage, other, now, lo, hi) : Work::forward(a, sh, stage, other, now, lo, hi);
+    __syncthreads();
+  }
+  if constexpr (STAGED) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (threadIdx.x == 0 && sh.stop) atomicAdd(a.gave_up, 1u);
+}
+
+// Packed sequences: marks where they begin and end, and the states of those without rows.
+// A warp to a sequence.
+__global__ void __launch_bounds__(256) mark_kernel(const __grid_constant__ Args a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t s = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  wait_for_previous();
+  let_next_start();
+  if (s >= a.seqs) return;
+  const int64_t begin = offset_at(a, s), end = offset_at(a, s + 1);
+  if (begin < end) {
+    if (lane == 0) a.begins[begin] = (int32_t)s, a.ends[end - 1] = (int32_t)s;
+    return;
+  }
+  for (int64_t j = lane; j < a.cols; j += 32) {
+    if (a.final_state) a.final_state[s * a.cols + j] = a.initial ? a.initial[s * a.cols + j] : 0.0f;
+    if (a.dinitial) a.dinitial[s * a.cols + j] = a.dfinal ? a.dfinal[s * a.cols + j] : 0.0f;
+  }
+}
+
+// Sums of the tiles' parts of dbias, in a fixed order: 32 columns to a block.
+constexpr int kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads) column_sum_kernel(const float *partial, int64_t n, int64_t cols, void *out, int32_t bf16) {
+  __shared__ float part[kSumThreads / 32][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int64_t j = (int64_t)blockIdx.x * 32 + lane;
+  wait_for_previous();
+  let_next_start();
   float s = 0.0f;
-  for (int64_t i = 0; i < n; ++i) s += partial[i * cols + j];
-  store_any(out, j, bf16, s);
+  if (j < cols) {
+#pragma unroll 8
+    for (int64_t i = warp; i < n; i += kSumThreads / 32) s += partial[i * cols + j];
+  }
+  part[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && j < cols) {
+    for (int w = 1; w < kSumThreads / 32; ++w) s += part[w][lane];
+    store_any(out, j, bf16 != 0, s);
+  }
 }
 
 fsdp_status_t check(const fsdp_scan_desc_t *d) {
@@ -104,7 +582,7 @@ fsdp_status_t check(const fsdp_scan_desc_t *d) {
   if (d->rows > INT32_MAX - 1024 || d->seqs > INT32_MAX - 1024) return fail(FSDP_EUNSUPPORTED, "2^31 rows or sequences");
   if (d->packed != 0 && d->packed != 1) return fail(FSDP_EINVAL, "packed is neither 0 nor 1");
   if (!d->packed) {
-    if (d->seq_len < 0) return fail(FSDP_EINVAL, "seq_len < 0");
+    if (d->seq_len < 1) return fail(FSDP_EINVAL, "seq_len < 1 (sequences without rows come packed)");
     if (d->seqs > 0 && (d->seq_len > d->rows || d->seqs * d->seq_len != d->rows)) return fail(FSDP_EINVAL, "rows is not seqs * seq_len");
     if (d->seqs == 0 && d->rows != 0) return fail(FSDP_EINVAL, "rows is not seqs * seq_len");
   }
@@ -138,7 +616,93 @@ fsdp_status_t check_workspace(const void *workspace, int64_t given, int64_t need
   return check_ptr(workspace, needed, 16, "workspace", -1);
 }
 
-int64_t workspace_of(const fsdp_scan_desc_t &d, bool backward) { return backward ? d.seqs * d.cols * 4 : 0; }
+// The workspace: parts of dbias, then what has to be 0xFF: what tiles leave for one another,
+// the ticket, and the marks of packed sequences.
+struct Plan {
+  int64_t column_tiles, time_tiles, padded_cols;
+  int64_t partial, clear, carried, ticket, parts, begins, ends, bytes;
+};
+Plan plan_of(const fsdp_scan_desc_t &d, bool backward) {
+  Plan p = {};
+  const int64_t tile = warps_of(d.x_dtype == FSDP_DTYPE_F32) * kSteps;
+  p.column_tiles = (d.cols + kCols - 1) / kCols;
+  p.time_tiles = (d.rows + tile - 1) / tile;
+  p.padded_cols = p.column_tiles * kCols;
+  auto take = [&](int64_t bytes) {
+    const int64_t at = p.bytes;
+    p.bytes += (bytes + 15) / 16 * 16;
+    return at;
+  };
+  const bool several = p.time_tiles > 1;
+  p.partial = take(backward ? p.time_tiles * d.cols * 4 : 0);
+  p.clear = p.bytes;
+  p.parts = take(several ? p.time_tiles * p.padded_cols * 8 : 0);
+  p.carried = take(several ? p.time_tiles * p.padded_cols * 4 : 0);
+  p.ticket = take(several ? 4 : 0);
+  p.begins = take(d.packed ? d.rows * 4 : 0);
+  p.ends = take(d.packed ? d.rows * 4 : 0);
+  return p;
+}
+
+template <class K>
+const void *kernel(K *k) {
+  return reinterpret_cast<const void *>(k);
+}
+
+// The largest number of blocks that the device holds at once.
+template <class Work>
+cudaError_t launch_tiles(void (*fn)(Args), Args &a, cudaStream_t s) {
+  static_assert(Work::kSmem <= 112 * 1024, "two blocks of an SM");
+  constexpr int64_t kBlocks = Work::kBf16 || Work::kSmem > 72 * 1024 ? 2 : 3;  // of an SM
+  cudaError_t e = cudaFuncSetAttribute(kernel(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, Work::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = std::min<int64_t>(a.tiles, (int64_t)device_sms() * kBlocks);
+  void *args[] = {&a};
+  return launch_kernel(kernel(fn), dim3((unsigned)grid), dim3(Work::W * 32), args, Work::kSmem, s, true);
+}
+template <bool BACKWARD, class T>
+cudaError_t launch_as(bool vec, bool staged, Args &a, cudaStream_t s) {
+  if (staged) return launch_tiles<Tile<T, true, true, BACKWARD>>(&tile_kernel<T, true, true, BACKWARD>, a, s);
+  if (vec) return launch_tiles<Tile<T, true, false, BACKWARD>>(&tile_kernel<T, true, false, BACKWARD>, a, s);
+  return launch_tiles<Tile<T, false, false, BACKWARD>>(&tile_kernel<T, false, false, BACKWARD>, a, s);
+}
+
+// How the lanes' pairs of columns and the 16-byte units of staged rows fit a matrix.
+struct Fit {
+  bool pairs = true, units = true;
+  void matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t size) {
+    pairs &= cols % 2 == 0 && (uintptr_t)p % (2 * size) == 0 && (rows <= 1 || ld % 2 == 0);
+    units &= cols * size % 16 == 0 && aligned16(p) && (rows <= 1 || ld * size % 16 == 0);
+  }
+};
+
+// Fill the marks and the values to come, mark packed sequences, and launch the tiles.
+template <bool BACKWARD>
+fsdp_status_t run(const fsdp_scan_desc_t &d, Args &a, const Plan &p, void *workspace, const Fit &fit, cudaStream_t s) {
+  uint8_t *w = static_cast<uint8_t *>(workspace);
+  if (p.time_tiles * p.column_tiles > INT32_MAX / 2) return fail(FSDP_EUNSUPPORTED, "more than 2^30 tiles");
+  if (p.bytes > p.clear) {
+    const cudaError_t e = cudaMemsetAsync(w + p.clear, 0xFF, p.bytes - p.clear, s);
+    if (e != cudaSuccess) return fail(FSDP_ECUDA, std::string("memset: ") + cudaGetErrorString(e));
+  }
+  a.parts = reinterpret_cast<uint2 *>(w + p.parts), a.carried = reinterpret_cast<uint32_t *>(w + p.carried);
+  a.ticket = reinterpret_cast<uint32_t *>(w + p.ticket);
+  a.begins = reinterpret_cast<int32_t *>(w + p.begins), a.ends = reinterpret_cast<int32_t *>(w + p.ends);
+  a.column_tiles = (uint32_t)p.column_tiles, a.time_tiles = (uint32_t)p.time_tiles, a.padded_cols = p.padded_cols;
+  a.tiles = a.column_tiles * a.time_tiles;
+  a.fault = wait_fault(), a.wait_limit_ns = wait_limit_ns();
+  cudaError_t e = gave_up_count(GAVE_UP_SCAN, &a.gave_up);
+  if (e != cudaSuccess) return fail(FSDP_ECUDA, std::string("status: ") + cudaGetErrorString(e));
+  if (d.packed) {
+    void *args[] = {&a};
+    e = launch_kernel(kernel(&mark_kernel), dim3((unsigned)((d.seqs + 7) / 8)), dim3(256), args, 0, s);
+  }
+  const bool staged = fit.units && (!BACKWARD || dtype_bytes(d.h_dtype) <= dtype_bytes(d.x_dtype));
+  if (e == cudaSuccess && a.tiles > 0)
+    e = d.x_dtype == FSDP_DTYPE_BF16 ? launch_as<BACKWARD, __nv_bfloat16>(fit.pairs, staged, a, s)
+                                     : launch_as<BACKWARD, float>(fit.pairs, staged, a, s);
+  return launched(e);
+}
 
 Args args_of(const fsdp_scan_desc_t &d, const void *x, const void *gate, const void *bias, const float *initial, const void *offsets) {
   Args a = {};
@@ -146,7 +710,7 @@ Args args_of(const fsdp_scan_desc_t &d, const void *x, const void *gate, const v
   a.rows = d.rows, a.cols = d.cols, a.seqs = d.seqs, a.seq_len = d.seq_len;
   a.ld_x = d.ld_x, a.ld_gate = d.ld_gate, a.ld_h = d.ld_h, a.ld_dx = d.ld_dx, a.ld_dgate = d.ld_dgate;
   a.packed = d.packed, a.wide = d.offset_dtype == FSDP_INDEX_I64;
-  a.x_bf16 = d.x_dtype == FSDP_DTYPE_BF16, a.h_bf16 = d.h_dtype == FSDP_DTYPE_BF16, a.dx_bf16 = d.dx_dtype == FSDP_DTYPE_BF16;
+  a.h_bf16 = d.h_dtype == FSDP_DTYPE_BF16, a.dx_bf16 = d.dx_dtype == FSDP_DTYPE_BF16;
   a.param_bf16 = d.param_dtype == FSDP_DTYPE_BF16;
   return a;
 }
@@ -163,7 +727,7 @@ extern "C" {
 fsdp_status_t fsdp_gated_scan_states(int64_t rows, int64_t cols, int64_t *n) {
   if (!n) return fail(FSDP_EINVAL, "n is NULL");
   if (rows < 0 || cols < 1) return fail(FSDP_EINVAL, "rows < 0 or cols < 1");
-  *n = (rows + kTileRows - 1) / kTileRows;
+  *n = (rows + kStateRows - 1) / kStateRows;
   clear_error();
   return FSDP_OK;
 }
@@ -172,7 +736,7 @@ fsdp_status_t fsdp_gated_scan_workspace(const fsdp_scan_desc_t *desc, int32_t ba
   fsdp_status_t st = check(desc);
   if (st != FSDP_OK) return st;
   if (!bytes) return fail(FSDP_EINVAL, "bytes is NULL");
-  *bytes = workspace_of(*desc, backward != 0);
+  *bytes = plan_of(*desc, backward != 0).bytes;
   clear_error();
   return FSDP_OK;
 }
@@ -187,14 +751,16 @@ fsdp_status_t fsdp_gated_scan_forward(const fsdp_scan_desc_t *desc, const void *
   if ((st = check_matrix(h, d.rows, d.cols, d.ld_h, dtype_bytes(d.h_dtype), "h")) != FSDP_OK) return st;
   if (final && (st = check_ptr(final, d.seqs * d.cols * 4, 4, "final", -1)) != FSDP_OK) return st;
   if (states && (st = check_ptr(states, d.rows * 4, 4, "states", -1)) != FSDP_OK) return st;
-  if ((st = check_workspace(workspace, workspace_bytes, workspace_of(d, false))) != FSDP_OK) return st;
+  const Plan plan = plan_of(d, false);
+  if ((st = check_workspace(workspace, workspace_bytes, plan.bytes)) != FSDP_OK) return st;
   if (d.seqs > 0) {
     Args a = args_of(d, x, gate, bias, initial, offsets);
     a.h = h, a.final_state = final, a.states = states;
-    void *args[] = {&a};
-    st = launched(launch_kernel(reinterpret_cast<const void *>(&forward_kernel),
-                                dim3((unsigned)((d.cols + kThreads - 1) / kThreads), (unsigned)std::min<int64_t>(d.seqs, 65535)),
-                                dim3(kThreads), args, 0, reinterpret_cast<cudaStream_t>(stream)));
+    const int64_t sx = dtype_bytes(d.x_dtype);
+    Fit fit;
+    fit.matrix(x, d.rows, d.cols, d.ld_x, sx), fit.matrix(gate, d.rows, d.cols, d.ld_gate, sx);
+    fit.matrix(h, d.rows, d.cols, d.ld_h, dtype_bytes(d.h_dtype));
+    st = run<false>(d, a, plan, workspace, fit, reinterpret_cast<cudaStream_t>(stream));
     if (st != FSDP_OK) return st;
   }
   clear_error();
@@ -217,24 +783,27 @@ fsdp_status_t fsdp_gated_scan_backward(const fsdp_scan_desc_t *desc, const void 
   const int64_t gsize = dtype_bytes(d.grad_dtype);
   if (dbias && (st = check_ptr(dbias, d.cols * gsize, gsize, "dbias", -1)) != FSDP_OK) return st;
   if (dinitial && (st = check_ptr(dinitial, d.seqs * d.cols * 4, 4, "dinitial", -1)) != FSDP_OK) return st;
-  if ((st = check_workspace(workspace, workspace_bytes, workspace_of(d, true))) != FSDP_OK) return st;
+  const Plan plan = plan_of(d, true);
+  if ((st = check_workspace(workspace, workspace_bytes, plan.bytes)) != FSDP_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned blocks = (unsigned)((d.cols + kThreads - 1) / kThreads);
+  float *partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + plan.partial);
   if (d.seqs > 0) {
     Args a = args_of(d, x, gate, bias, initial, offsets);
     a.dh = dh, a.states_in = states, a.dfinal = dfinal, a.dx = dx, a.dgate = dgate, a.dinitial = dinitial;
-    a.partial = dbias ? static_cast<float *>(workspace) : nullptr;
-    void *args[] = {&a};
-    st = launched(launch_kernel(reinterpret_cast<const void *>(&backward_kernel), dim3(blocks, (unsigned)std::min<int64_t>(d.seqs, 65535)),
-                                dim3(kThreads), args, 0, s));
+    a.partial = dbias ? partial : nullptr;
+    const int64_t sx = dtype_bytes(d.x_dtype), sd = dtype_bytes(d.dx_dtype);
+    Fit fit;
+    fit.matrix(x, d.rows, d.cols, d.ld_x, sx), fit.matrix(gate, d.rows, d.cols, d.ld_gate, sx);
+    fit.matrix(dh, d.rows, d.cols, d.ld_h, dtype_bytes(d.h_dtype));
+    fit.matrix(dx, d.rows, d.cols, d.ld_dx, sd), fit.matrix(dgate, d.rows, d.cols, d.ld_dgate, sd);
+    st = run<true>(d, a, plan, workspace, fit, s);
     if (st != FSDP_OK) return st;
   }
   if (dbias) {
-    const float *partial = static_cast<const float *>(workspace);
-    int64_t n = d.seqs, cols = d.cols;
+    int64_t n = d.seqs > 0 ? plan.time_tiles : 0, cols = d.cols;
     int32_t bf16 = d.grad_dtype == FSDP_DTYPE_BF16;
     void *args[] = {&partial, &n, &cols, &dbias, &bf16};
-    st = launched(launch_kernel(reinterpret_cast<const void *>(&column_sum_kernel), dim3(blocks), dim3(kThreads), args, 0, s));
+    st = launched(launch_kernel(reinterpret_cast<const void *>(&column_sum_kernel), dim3((unsigned)((d.cols + 31) / 32)), dim3(kSumThreads), args, 0, s, true));
     if (st != FSDP_OK) return st;
   }
   clear_error();

@@ -486,7 +486,7 @@ def fsdp_gated_scan_states(rows: int, cols: int) -> int:
 
 @functools.lru_cache(maxsize=1024)
 def _scan_workspace(rows, cols, seqs, packed, backward, device) -> int:
-    d = fsdp_scan_desc_t(rows, cols, seqs, 0 if packed or not seqs else rows // seqs, cols, cols, cols, cols, cols, packed, 0, 0, 0, 0, 0, 0)
+    d = fsdp_scan_desc_t(rows, cols, seqs, 1 if packed or not seqs else rows // seqs, cols, cols, cols, cols, cols, packed, 0, 0, 0, 0, 0, 0)
     out = _I64()
     _check(_lib.fsdp_gated_scan_workspace(ctypes.byref(d), backward, ctypes.byref(out)), "fsdp_gated_scan_workspace")
     return out.value
