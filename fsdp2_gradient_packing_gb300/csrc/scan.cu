@@ -1,9 +1,9 @@
 // Gated linear recurrence (fsdp_gated_scan_*): a = sigmoid(gate + bias),
 // h_t = a_t h_(t-1) + (1 - a_t) x_t, forward and backward.
 //
-// Rows are cut into tiles of 8 WARPS rows and 64 columns, whatever sequences they belong to;
+// Rows are cut into tiles of 128 (BF16) or 64 rows and 64 columns, whatever sequences they belong to;
 // where one begins, the state before it is its own initial one.  A thread has two columns and
-// kSteps rows.  Its rows take a state h to A h + B; so do a warp's, one behind the other, and a
+// 16 or 8 rows.  Its rows take a state h to A h + B; so do a warp's, one behind the other, and a
 // tile's.  A tile makes its A and B known, then looks back over the tiles before it for the
 // nearest one whose state behind its last row is known, and comes from there to its own start by
 // the A and B in between.  So every matrix is read and written once and long sequences keep all
@@ -33,10 +33,12 @@ namespace fsdp {
 namespace scan {
 namespace {
 
-constexpr int kSteps = 8, kCols = 64;
+constexpr int kCols = 64, kWarps = 8, kThreads = kWarps * 32;
 constexpr int kStateRows = 64;
-// Warps of a block, each with kSteps rows: as many as the look-back takes in at once.
-constexpr int warps_of(bool f32) { return f32 ? 8 : 16; }
+constexpr int kWindow = 16;  // tiles that a look back takes in at once
+// Rows of a warp.  What a tile costs a warp beside its rows is about 400 instructions, 30 to 60 a row;
+// of FP32 rows, two stages and two blocks of an SM hold 64.
+constexpr int steps_of(int64_t size) { return size == 4 ? 8 : 16; }
 
 struct Args {
   const void *x, *gate, *bias, *offsets, *dh;
@@ -78,9 +80,9 @@ __device__ __forceinline__ float2 join(float2 a, float2 keep) {
   return make_float2(a.x < keep.x ? -a.x : keep.x, a.y < keep.y ? -a.y : keep.y);
 }
 __device__ __forceinline__ void split(float2 gate, float2 &a, float2 &keep) {
-  const float2 q = make_float2(fabsf(gate.x), fabsf(gate.y)), p = __ffma2_rn(q, both(-1.0f), both(1.0f));
+  const float px = 1.0f - fabsf(gate.x), py = 1.0f - fabsf(gate.y);
   const bool nx = __float_as_int(gate.x) < 0, ny = __float_as_int(gate.y) < 0;
-  a = make_float2(nx ? q.x : p.x, ny ? q.y : p.y), keep = make_float2(nx ? p.x : q.x, ny ? p.y : q.y);
+  a = make_float2(nx ? fabsf(gate.x) : px, ny ? fabsf(gate.y) : py), keep = make_float2(nx ? px : gate.x, ny ? py : gate.y);
 }
 
 // Two columns of a lane, neighbours (VEC) or 32 apart, of a row in global or shared memory.
@@ -98,7 +100,7 @@ __device__ __forceinline__ float2 get(const void *p, int64_t at, bool bf16, bool
   }
 }
 template <bool VEC>
-__device__ __forceinline__ void put(void *p, int64_t at, bool bf16, bool second, float2 v) {
+__device__ __forceinline__ void put(void *p, int64_t at, bool bf16, bool second, float2 v) {  // bf16 is known where tiles are staged
   if constexpr (VEC) {
     if (bf16)
       *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p) + at) = bf16_pair(v.x, v.y);
@@ -122,70 +124,105 @@ __device__ __forceinline__ void put_f32(float *p, bool second, float2 v) {
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
-// The sequence that begins (shift 0) or ends (shift 1) at row t, or -1.
-__device__ __forceinline__ int32_t mark_at(const Args &a, const int32_t *marks, int64_t t, int32_t shift) {
-  if (t >= a.rows) return -1;
-  if (a.packed) return marks[t];
-  const uint32_t u = (uint32_t)t + shift, n = (uint32_t)a.seq_len, q = u / n;
-  return q * n == u ? (int32_t)q - shift : -1;
-}
-
-template <int WARPS>
-struct Shared {
-  float2 a[WARPS][32], b[WARPS][32];
-  float2 forward[WARPS][32];  // backward pass: B of the states
-  uint4 look[WARPS][32];      // what earlier tiles have left: A and B, or the state
-  float2 carry[32];
-  uint32_t cut[WARPS], found[WARPS], ticket, stop;
-};
-
 // One tensor's rows of a tile on their way into shared memory: rows of kCols elements, 16-byte
 // units, zeros outside the matrix.
-template <int WARPS>
-__device__ __forceinline__ void fetch(uint8_t *to, const void *from, int64_t ld, int size_log2, int64_t first, int64_t column, const Args &a) {
-  const int units_log2 = 2 + size_log2;  // 16-byte units of a row
-  const int64_t unit_cols = 16 >> size_log2;
-#pragma unroll 4
-  for (int c = threadIdx.x; c < (WARPS * kSteps) << units_log2; c += WARPS * 32) {
-    const int r = c >> units_log2;
-    const int64_t j = column + (c & ((1 << units_log2) - 1)) * unit_cols;
-    const bool there = first + r < a.rows && j < a.cols;
-    const uint8_t *src = static_cast<const uint8_t *>(from) + (there ? (((first + r) * ld + j) << size_log2) : 0);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem(to) + c * 16), "l"(src), "r"(there ? 16 : 0) : "memory");
+template <int ROWS, int SIZE>
+__device__ __forceinline__ void fetch(uint8_t *to, const void *from, int64_t ld, int64_t first, int64_t column, const Args &a) {
+  constexpr int kUnits = kCols * SIZE / 16, kStep = kThreads / kUnits;  // 16-byte units of a row; rows of a round
+  const int r = threadIdx.x / kUnits, u = threadIdx.x % kUnits;
+  const int64_t j = column + u * (16 / SIZE);
+  const bool in = j < a.cols;
+  const int64_t left = a.rows - first - r;
+  const uint8_t *src = static_cast<const uint8_t *>(from) + (in ? ((first + r) * ld + j) * SIZE : 0);
+  const int64_t pitch = ld * SIZE * kStep;
+  const uint32_t dst = tc::smem(to) + threadIdx.x * 16;
+#pragma unroll
+  for (int k = 0; k < ROWS / kStep; ++k) {
+    const bool there = in && k * kStep < left;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + k * (kThreads * 16)), "l"(there ? src : static_cast<const uint8_t *>(from)),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+    src += pitch;
   }
 }
 
-// Where a tile, this lane's columns and this warp's rows are.
-template <int WARPS, bool VEC>
+// Where a tile is, found by one thread: its time tile and first column; and without packing, the sequence
+// of its first row, that row's place in it, and whether all its rows lie inside that sequence.
+struct Spot {
+  int64_t tile, left;
+  int32_t sequence;
+  uint32_t place;
+  bool inside;
+};
+template <int ROWS>
+__device__ __forceinline__ Spot spot_of(const Args &a, uint32_t ticket, bool backward) {
+  Spot p = {};
+  const uint32_t q = ticket / a.column_tiles;
+  p.tile = backward ? a.time_tiles - 1 - q : q;
+  p.left = (int64_t)(ticket - q * a.column_tiles) * kCols;
+  if (!a.packed) {
+    const uint32_t t = (uint32_t)p.tile * ROWS, n = (uint32_t)a.seq_len;
+    p.sequence = t / n, p.place = t - p.sequence * n;
+    p.inside = p.place > 0 && p.place + ROWS < n;
+  }
+  return p;
+}
+
+struct Shared {
+  float2 a[kWarps][32], b[kWarps][32];
+  float2 forward[kWarps][32];  // backward pass: B of the states
+  uint4 look[kWindow][32];     // what other tiles have left: A and B, or the state
+  float2 carry[32];
+  uint32_t cut[kWarps], found[kWindow], ticket, stop;
+  Spot spot;  // of `ticket`
+};
+// Bits of `cut`: nothing passes a warp's rows downwards, or upwards; a sequence begins at their
+// first row; one ends at their last.
+enum Cut : uint32_t { CUT_DOWN = 1, CUT_UP = 2, CUT_FIRST = 4, CUT_LAST = 8 };
+
+// This lane's columns and this warp's rows.
+template <int STEPS, bool VEC>
 struct Place {
   int64_t tile, column, first;  // time tile; first column of the lane; first row of the warp
   int64_t at0;                  // of the lane among the values that tiles leave
   bool in, second;              // whether the lane's columns exist
-  __device__ Place(const Args &a, uint32_t ticket, bool backward) {
+  __device__ __forceinline__ Place(const Args &a, const Spot &p) {
     const int lane = threadIdx.x & 31;
-    const uint32_t q = ticket / a.column_tiles;
-    tile = backward ? a.time_tiles - 1 - q : q;
-    const int64_t left = (int64_t)(ticket - q * a.column_tiles) * kCols;
-    column = left + (VEC ? 2 * lane : lane);
-    at0 = left + 2 * lane;
-    first = tile * (WARPS * kSteps) + threadIdx.x / 32 * kSteps;
+    tile = p.tile;
+    column = p.left + (VEC ? 2 * lane : lane);
+    at0 = p.left + 2 * lane;
+    first = tile * (kWarps * STEPS) + threadIdx.x / 32 * STEPS;
     in = column < a.cols, second = column + (VEC ? 1 : 32) < a.cols;
   }
 };
 
 // Boundaries in a warp's rows: bit i for row first + i; lane i has the sequence.
+template <int STEPS>
 struct Marks {
   int32_t begin, end;
   uint32_t begins, ends, valid;
-  __device__ Marks(const Args &a, int64_t first, int64_t lo, int64_t hi) {
+  __device__ __forceinline__ Marks(const Args &a, const Spot &p, int64_t first, int64_t lo, int64_t hi) {
+    begin = end = -1, begins = ends = 0, valid = (1u << STEPS) - 1;
+    if (p.inside) return;
     const int lane = threadIdx.x & 31;
-    begin = end = -1;
     const int64_t t = first + lane;
-    if (lane < kSteps) begin = mark_at(a, a.begins, t, 0), end = mark_at(a, a.ends, t, 1);
-    begins = __ballot_sync(0xFFFFFFFFu, begin >= 0), ends = __ballot_sync(0xFFFFFFFFu, end >= 0);
-    valid = __ballot_sync(0xFFFFFFFFu, lane < kSteps && t >= lo && t < hi);
+    if (a.packed) {
+      const bool there = lane < STEPS && t < a.rows;
+      if (there) begin = a.begins[t], end = a.ends[t];
+      begins = __ballot_sync(0xFFFFFFFFu, begin >= 0), ends = __ballot_sync(0xFFFFFFFFu, end >= 0);
+    } else {  // one ends where the next one begins
+      const uint32_t n = (uint32_t)a.seq_len, u = p.place + threadIdx.x / 32 * STEPS + lane, q = u / n;
+      begin = end = p.sequence + (int32_t)q;
+      const uint32_t on = __ballot_sync(0xFFFFFFFFu, lane <= STEPS && t <= a.rows && q * n == u);
+      begins = on & __ballot_sync(0xFFFFFFFFu, lane < STEPS && t < a.rows), ends = on >> 1;
+    }
+    valid = __ballot_sync(0xFFFFFFFFu, lane < STEPS && t >= lo && t < hi);
   }
-  __device__ bool plain() const { return (begins | ends) == 0 && valid == (1u << kSteps) - 1; }
+  // Rows that are not in the middle of a sequence.
+  __device__ __forceinline__ uint32_t odd() const { return (begins | ends | ~valid) & ((1u << STEPS) - 1); }
+  __device__ __forceinline__ uint32_t cut() const {
+    return (begins ? CUT_DOWN : 0u) | (begins | ends ? CUT_UP : 0u) | (begins & 1 ? CUT_FIRST : 0u) | (ends >> (STEPS - 1) & 1 ? CUT_LAST : 0u);
+  }
 };
 
 // Values that tiles leave for others.  All ones means not there yet; the NaN of that pattern
@@ -203,35 +240,45 @@ __device__ __forceinline__ void leave_state(const Args &a, int64_t at, float2 s)
   asm volatile("st.relaxed.gpu.global.v2.b32 [%0], {%1, %2};" ::"l"(a.carried + at), "r"(as_left(s.x)), "r"(as_left(s.y)) : "memory");
 }
 
+// Whether a warp has waited for longer than it may, since it first asked.
+__device__ __forceinline__ bool too_late(const Args &a, uint64_t &began) {
+  const uint64_t now = __shfl_sync(0xFFFFFFFFu, tc::now_ns(), 0);
+  if (began == 0) began = now;
+  return now - began > a.wait_limit_ns;
+}
+
 // All warps: the state that comes into a tile from `towards` (-1: the tiles before it, 1: those
-// behind).  Warp w reads what the tile w + 1 away has left.  In s.carry of warp 0's lanes.
-template <int WARPS>
-__device__ __forceinline__ float2 look_back(const Args &a, Shared<WARPS> &s, int64_t tile, int towards, int64_t at0) {
+// behind).  A warp reads what kWindow / kWarps of the kWindow nearest tiles have left.  For warp 0.
+__device__ __forceinline__ float2 look_back(const Args &a, Shared &s, int64_t tile, int towards, int64_t at0) {
+  constexpr int kEach = kWindow / kWarps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int64_t other = tile + (int64_t)towards * (1 + warp);
-  const bool exists = other >= 0 && other < a.time_tiles;
-  const uint64_t began = tc::now_ns();
+  uint64_t began = 0;
+  bool late = false;
   for (;;) {
-    uint32_t found = 0;  // 1: A and B, 2: the state
-    uint64_t p0 = 0, p1 = 0;
-    uint32_t c0 = 0, c1 = 0;
-    for (uint32_t n = 1; exists; ++n) {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int slot = warp + e * kWarps;
+      const int64_t other = tile + (int64_t)towards * (1 + slot);
+      const bool exists = other >= 0 && other < a.time_tiles;
       const int64_t at = other * a.padded_cols + at0;
-      asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(p0), "=l"(p1) : "l"(a.parts + at) : "memory");
-      asm volatile("ld.relaxed.gpu.global.v2.b32 {%0, %1}, [%2];" : "=r"(c0), "=r"(c1) : "l"(a.carried + at) : "memory");
-      const bool state = c0 != 0xFFFFFFFFu && c1 != 0xFFFFFFFFu;
-      const bool part = (uint32_t)p0 != 0xFFFFFFFFu && (uint32_t)p1 != 0xFFFFFFFFu && p0 >> 32 != 0xFFFFFFFFu && p1 >> 32 != 0xFFFFFFFFu;
-      found = __all_sync(0xFFFFFFFFu, state) ? 2 : __all_sync(0xFFFFFFFFu, part) ? 1 : 0;
-      if (found) break;
-      if ((n & 15u) == 0 && __shfl_sync(0xFFFFFFFFu, tc::now_ns() - began > a.wait_limit_ns || *(volatile uint32_t *)&s.stop, 0)) {
-        break;
+      uint32_t found = 0;  // 1: A and B, 2: the state
+      uint64_t p0 = 0, p1 = 0;
+      uint32_t c0 = 0, c1 = 0;
+      for (uint32_t n = 1; exists; ++n) {
+        asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(p0), "=l"(p1) : "l"(a.parts + at) : "memory");
+        asm volatile("ld.relaxed.gpu.global.v2.b32 {%0, %1}, [%2];" : "=r"(c0), "=r"(c1) : "l"(a.carried + at) : "memory");
+        const bool state = c0 != 0xFFFFFFFFu && c1 != 0xFFFFFFFFu;
+        const bool part = (uint32_t)p0 != 0xFFFFFFFFu && (uint32_t)p1 != 0xFFFFFFFFu && p0 >> 32 != 0xFFFFFFFFu && p1 >> 32 != 0xFFFFFFFFu;
+        found = __all_sync(0xFFFFFFFFu, state) ? 2 : __all_sync(0xFFFFFFFFu, part) ? 1 : 0;
+        if (found) break;
+        if ((n & 15u) == 0 && (late = too_late(a, began))) break;
       }
+      s.look[slot][lane] = found == 2 ? make_uint4(c0, 0, c1, 0) : make_uint4((uint32_t)p0, (uint32_t)(p0 >> 32), (uint32_t)p1, (uint32_t)(p1 >> 32));
+      if (lane == 0) s.found[slot] = found;
     }
-    if (tc::now_ns() - began > a.wait_limit_ns && found != 2 && exists) s.stop = 1;  // before the barrier: all threads see the same
-    s.look[warp][lane] = found == 2 ? make_uint4(c0, 0, c1, 0) : make_uint4((uint32_t)p0, (uint32_t)(p0 >> 32), (uint32_t)p1, (uint32_t)(p1 >> 32));
-    if (lane == 0) s.found[warp] = found;
+    if (late) s.stop = 1;  // before the barrier: all threads see the same
     __syncthreads();
-    const uint32_t states = __ballot_sync(0xFFFFFFFFu, lane < WARPS && s.found[lane % WARPS] == 2);
+    const uint32_t states = __ballot_sync(0xFFFFFFFFu, lane < kWindow && s.found[lane % kWindow] == 2);
     float2 carry = make_float2(0, 0);
     if (s.stop) return carry;
     if (states) {
@@ -239,6 +286,7 @@ __device__ __forceinline__ float2 look_back(const Args &a, Shared<WARPS> &s, int
         const int back = __ffs(states) - 1;
         const uint4 r = s.look[back][lane];
         carry = make_float2(__uint_as_float(r.x), __uint_as_float(r.z));
+#pragma unroll 4
         for (int w = back - 1; w >= 0; --w) {
           const uint4 q = s.look[w][lane];
           carry = fma2(make_float2(__uint_as_float(q.x), __uint_as_float(q.z)), carry, make_float2(__uint_as_float(q.y), __uint_as_float(q.w)));
@@ -247,25 +295,27 @@ __device__ __forceinline__ float2 look_back(const Args &a, Shared<WARPS> &s, int
       return carry;
     }
     __syncthreads();  // none of them knows its state yet
+    late = too_late(a, began);
   }
 }
 
 // Between a tile's warps: A and B of the whole (from the first warp to the last, or backward the other
-// way), left for other tiles, and the state that comes in.  `cut`: which warps let nothing
-// through; `alone`: nothing comes into the tile.
-template <int WARPS, bool BACKWARD>
-__device__ __forceinline__ void carry_over(const Args &a, Shared<WARPS> &s, int64_t tile, int64_t at0, bool alone) {
-  constexpr uint32_t kBit = BACKWARD ? 2 : 1;
+// way), left for other tiles, and the state that comes in.
+template <bool BACKWARD>
+__device__ __forceinline__ void carry_over(const Args &a, Shared &s, int64_t tile, int64_t at0) {
+  constexpr uint32_t kBit = BACKWARD ? CUT_UP : CUT_DOWN;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   float2 A = both(1.0f), B = both(0.0f), carry = both(0.0f);
   bool cut = false;
-  const bool last = tile == (BACKWARD ? 0 : a.time_tiles - 1);  // nothing goes out
-  const int64_t at = tile * a.padded_cols + at0;
   if (a.time_tiles > 1) {
+    // Whether nothing comes in, and nothing goes out.
+    const bool alone = BACKWARD ? tile == a.time_tiles - 1 || (s.cut[kWarps - 1] & CUT_LAST) : tile == 0 || (s.cut[0] & CUT_FIRST);
+    const bool last = tile == (BACKWARD ? 0 : a.time_tiles - 1);
+    const int64_t at = tile * a.padded_cols + at0;
     if (warp == 0 && !last) {
 #pragma unroll
-      for (int k = 0; k < WARPS; ++k) {
-        const int w = BACKWARD ? WARPS - 1 - k : k;
+      for (int k = 0; k < kWarps; ++k) {
+        const int w = BACKWARD ? kWarps - 1 - k : k;
         const bool c = s.cut[w] & kBit;
         A = __fmul2_rn(A, s.a[w][lane]);
         B = c ? s.b[w][lane] : fma2(s.a[w][lane], B, s.b[w][lane]);
@@ -277,7 +327,7 @@ __device__ __forceinline__ void carry_over(const Args &a, Shared<WARPS> &s, int6
         leave_state(a, at, B);
     }
     if (!alone) {
-      carry = look_back<WARPS>(a, s, tile, BACKWARD ? 1 : -1, at0);
+      carry = look_back(a, s, tile, BACKWARD ? 1 : -1, at0);
       if (warp == 0 && !last && !cut) leave_state(a, at, fma2(A, carry, B));
     }
   }
@@ -286,46 +336,69 @@ __device__ __forceinline__ void carry_over(const Args &a, Shared<WARPS> &s, int6
 
 template <class T, bool VEC, bool STAGED, bool BACKWARD>
 struct Tile {
-  static constexpr int W = warps_of(sizeof(T) == 4), kApart = VEC ? 1 : 32, kRows = W * kSteps;
+  static constexpr int kSteps = steps_of(sizeof(T)), kApart = VEC ? 1 : 32, kRows = kWarps * kSteps;
+  using At = Place<kSteps, VEC>;
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int kMatrix = kRows * kCols * (int)sizeof(T);           // bytes of x or gate in a stage
-  static constexpr int kStage = STAGED ? (BACKWARD ? 3 : 2) * kMatrix : 0;  // dh is no wider than x where staged
+  static constexpr int kStage = STAGED ? (BACKWARD ? 3 : 2) * kMatrix : 0;
   static constexpr int kSmem = 2 * kStage;
 
-  __device__ static void start(const Args &a, uint8_t *stage, uint32_t ticket) {
+  // Where tiles are staged, all matrices have x's type.
+  __device__ __forceinline__ static bool out_bf16(int32_t bf16) { return STAGED ? kBf16 : bf16 != 0; }
+
+  __device__ __forceinline__ static int64_t out_size(int32_t bf16) { return out_bf16(bf16) ? 2 : 4; }
+
+  __device__ __forceinline__ static void start(const Args &a, uint8_t *stage, uint32_t ticket, const Spot &p) {
     if constexpr (STAGED) {
       if (ticket < a.tiles) {
-        const uint32_t q = ticket / a.column_tiles;
-        const int64_t first = (int64_t)(BACKWARD ? a.time_tiles - 1 - q : q) * kRows, column = (int64_t)(ticket - q * a.column_tiles) * kCols;
-        fetch<W>(stage, a.x, a.ld_x, kBf16 ? 1 : 2, first, column, a);
-        fetch<W>(stage + kMatrix, a.gate, a.ld_gate, kBf16 ? 1 : 2, first, column, a);
-        if constexpr (BACKWARD) fetch<W>(stage + 2 * kMatrix, a.dh, a.ld_h, a.h_bf16 ? 1 : 2, first, column, a);
+        fetch<kRows, sizeof(T)>(stage, a.x, a.ld_x, p.tile * kRows, p.left, a);
+        fetch<kRows, sizeof(T)>(stage + kMatrix, a.gate, a.ld_gate, p.tile * kRows, p.left, a);
+        if constexpr (BACKWARD) fetch<kRows, sizeof(T)>(stage + 2 * kMatrix, a.dh, a.ld_h, p.tile * kRows, p.left, a);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
   }
   // Row i of the warp's in x, gate or dh (m 0, 1, 2).
-  __device__ __forceinline__ static float2 row(const Args &a, const uint8_t *stage, const Place<W, VEC> &at, int m, int i) {
-    const bool bf16 = m == 2 ? a.h_bf16 != 0 : kBf16;
+  __device__ __forceinline__ static float2 row(const Args &a, const uint8_t *stage, const At &at, int m, int i) {
     if constexpr (STAGED) {
-      return get<VEC>(stage + m * kMatrix, (threadIdx.x / 32 * kSteps + i) * kCols + 2 * (threadIdx.x & 31), bf16, true, true);
+      return get<VEC>(stage + m * kMatrix, (threadIdx.x / 32 * kSteps + i) * kCols + 2 * (threadIdx.x & 31), kBf16, true, true);
     } else {
+      const bool bf16 = m == 2 ? a.h_bf16 != 0 : kBf16;
       const void *p = m == 0 ? a.x : m == 1 ? a.gate : a.dh;
       const int64_t ld = m == 0 ? a.ld_x : m == 1 ? a.ld_gate : a.ld_h, t = at.first + i;
       return get<VEC>(p, t * ld + at.column, bf16, at.in && t < a.rows, at.second);
     }
   }
-  __device__ static float2 bias(const Args &a, const Place<W, VEC> &at) {
+  __device__ static float2 bias(const Args &a, const At &at) {
     if (!a.bias || !at.in) return make_float2(0, 0);
     return make_float2(load_any(a.bias, at.column, a.param_bf16), at.second ? load_any(a.bias, at.column + kApart, a.param_bf16) : 0.0f);
   }
   // A lane's columns of row s of `initial` or `dfinal`.
-  __device__ __forceinline__ static float2 given(const Args &a, const float *p, int32_t s, const Place<W, VEC> &at) {
+  __device__ __forceinline__ static float2 given(const Args &a, const float *p, int32_t s, const At &at) {
     return p && at.in ? get_f32<VEC>(p + (int64_t)s * a.cols + at.column, at.second) : both(0.0f);
   }
-  // One tile, from its stage; starts the next one's loads into the other stage, and returns its ticket.
-  __device__ static uint32_t forward(const Args &a, Shared<W> &sh, uint8_t *stage, uint8_t *other, uint32_t ticket, int64_t lo, int64_t hi);
-  __device__ static uint32_t backward(const Args &a, Shared<W> &sh, uint8_t *stage, uint8_t *other, uint32_t ticket, int64_t lo, int64_t hi);
+  // One row of the second and of the third pass over a backward tile.
+  __device__ __forceinline__ static void slope_step(float2 x, float2 gate, float2 &h, float2 &slope) {
+    float2 f, keep;
+    split(gate, f, keep);
+    slope = __fmul2_rn(fma2(x, both(-1.0f), h), __fmul2_rn(f, keep));
+    h = fma2(f, h, __fmul2_rn(keep, x));
+  }
+  __device__ __forceinline__ static float2 gradient_step(const Args &a, float2 dh, float2 gate, float2 slope, const At &at, void *dx,
+                                                         void *dgate, float2 &e) {
+    float2 f, keep;
+    split(gate, f, keep);
+    const float2 d = __fadd2_rn(dh, e), dz = __fmul2_rn(d, slope);
+    if (at.in) {
+      put<VEC>(dx, 0, out_bf16(a.dx_bf16), at.second, __fmul2_rn(keep, d));
+      put<VEC>(dgate, 0, out_bf16(a.dx_bf16), at.second, dz);
+    }
+    e = __fmul2_rn(f, d);
+    return dz;
+  }
+  // One tile, from its stage; starts the next one's loads into the other stage, and gives its ticket and its place.
+  __device__ static uint32_t forward(const Args &a, Shared &sh, uint8_t *stage, uint8_t *other, Spot &p, int64_t lo, int64_t hi);
+  __device__ static uint32_t backward(const Args &a, Shared &sh, uint8_t *stage, uint8_t *other, Spot &p, int64_t lo, int64_t hi);
 };
 
 // A warp's A: 1 - K, where K is the recurrence's answer to inputs of 1, or the rows' product where that is
@@ -335,16 +408,16 @@ __device__ __forceinline__ float2 factor(float2 product, float2 K) {
 }
 
 template <class T, bool VEC, bool STAGED, bool BACKWARD>
-__device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::forward(const Args &a, Shared<W> &sh, uint8_t *stage, uint8_t *other,
-                                                                           uint32_t ticket, int64_t lo, int64_t hi) {
-  const Place<W, VEC> at(a, ticket, false);
+__device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::forward(const Args &a, Shared &sh, uint8_t *stage, uint8_t *other,
+    Spot &p, int64_t lo, int64_t hi) {
+  const At at(a, p);
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const float2 shift = bias(a, at);
-  const Marks m(a, at.first, lo, hi);
-  const bool plain = m.plain();
+  const Marks<kSteps> m(a, p, at.first, lo, hi);
+  const uint32_t odd = m.odd();
   // A row takes h to f h + b.
   float2 f[kSteps], b[kSteps], A = both(1.0f), B = both(0.0f), K = both(0.0f);
-  if (plain) {
+  if (__builtin_expect(odd == 0, 1)) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       float2 keep;
@@ -358,39 +431,45 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::forward(cons
       float2 keep;
       gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f[i], keep);
       b[i] = __fmul2_rn(keep, row(a, stage, at, 0, i));
-      if (!(m.valid >> i & 1)) f[i] = both(1.0f), keep = b[i] = both(0.0f);
-      if (m.begins >> i & 1) {
-        b[i] = fma2(f[i], given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at), b[i]);
-        B = b[i];
-      } else {
-        A = __fmul2_rn(A, f[i]), B = fma2(f[i], B, b[i]), K = fma2(f[i], K, keep);
+      if (odd >> i & 1) {
+        if (!(m.valid >> i & 1)) f[i] = both(1.0f), keep = b[i] = both(0.0f);
+        if (m.begins >> i & 1) {
+          b[i] = fma2(f[i], given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at), b[i]);
+          f[i] = keep = both(0.0f);
+          if (B.x - B.x != 0.0f || B.y - B.y != 0.0f) B = both(0.0f);  // an infinity or NaN ends with its sequence
+        }
       }
+      A = __fmul2_rn(A, f[i]), B = fma2(f[i], B, b[i]), K = fma2(f[i], K, keep);
     }
   }
   sh.a[warp][lane] = factor(A, K);
   sh.b[warp][lane] = B;
-  if (lane == 0) sh.cut[warp] = m.begins ? 1 : 0;
+  if (lane == 0) sh.cut[warp] = m.cut();
   __syncthreads();
   const uint32_t next = sh.ticket;
-  start(a, other, next);
-  const bool alone = at.tile == 0 || mark_at(a, a.begins, at.tile * kRows, 0) >= 0;
-  carry_over<W, false>(a, sh, at.tile, at.at0, alone);
+  p = sh.spot;
+  start(a, other, next, p);
+  carry_over<false>(a, sh, at.tile, at.at0);
   __syncthreads();
   float2 h = sh.carry[lane];
-  for (int w = 0; w < warp; ++w) h = sh.cut[w] ? sh.b[w][lane] : fma2(sh.a[w][lane], h, sh.b[w][lane]);
+  for (int w = 0; w < warp; ++w) h = sh.cut[w] & CUT_DOWN ? sh.b[w][lane] : fma2(sh.a[w][lane], h, sh.b[w][lane]);
   if (a.states && at.in && at.first % kStateRows == 0 && at.first < a.rows)
     put_f32<VEC>(a.states + at.first / kStateRows * a.cols + at.column, at.second, h);
-  if (plain) {
+  const int64_t pitch = a.ld_h * out_size(a.h_bf16);
+  uint8_t *out = static_cast<uint8_t *>(a.h) + (at.first * a.ld_h + at.column) * out_size(a.h_bf16);
+  if (__builtin_expect(odd == 0, 1)) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       h = fma2(f[i], h, b[i]);
-      if (at.in) put<VEC>(a.h, (at.first + i) * a.ld_h + at.column, a.h_bf16, at.second, h);
+      if (at.in) put<VEC>(out, 0, out_bf16(a.h_bf16), at.second, h);
+      out += pitch;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       h = m.begins >> i & 1 ? b[i] : fma2(f[i], h, b[i]);
-      if (at.in && (m.valid >> i & 1)) put<VEC>(a.h, (at.first + i) * a.ld_h + at.column, a.h_bf16, at.second, h);
+      if (at.in && (m.valid >> i & 1)) put<VEC>(out, 0, out_bf16(a.h_bf16), at.second, h);
+      out += pitch;
       if (m.ends >> i & 1) {
         const int32_t s = __shfl_sync(0xFFFFFFFFu, m.end, i);
         if (at.in && a.final_state) put_f32<VEC>(a.final_state + (int64_t)s * a.cols + at.column, at.second, h);
@@ -401,91 +480,97 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::forward(cons
 }
 
 template <class T, bool VEC, bool STAGED, bool BACKWARD>
-__device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::backward(const Args &a, Shared<W> &sh, uint8_t *stage, uint8_t *other,
-                                                                            uint32_t ticket, int64_t lo, int64_t hi) {
-  const Place<W, VEC> at(a, ticket, true);
+__device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::backward(const Args &a, Shared &sh, uint8_t *stage, uint8_t *other,
+    Spot &p, int64_t lo, int64_t hi) {
+  const At at(a, p);
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const float2 shift = bias(a, at);
-  const Marks m(a, at.first, lo, hi);
-  const bool plain = m.plain();
+  const Marks<kSteps> m(a, p, at.first, lo, hi);
+  const uint32_t odd = m.odd();
   // The state before the warp's rows comes from the nearest kept one above.
   constexpr int kPer = kStateRows / kSteps;  // warps to a kept state
   const int64_t kept = (at.tile * kRows + warp / kPer * kStateRows) / kStateRows;
   float2 h = at.in && kept * kStateRows < a.rows ? get_f32<VEC>(a.states_in + kept * a.cols + at.column, at.second) : both(0.0f);
   // States go A h + B over the warp's rows; e = a_(t+1) D_(t+1) comes in from below and leaves as
   // A e + C.
-  float2 A = both(1.0f), B = both(0.0f), C = both(0.0f), K = both(0.0f);
-  if (plain) {
+  float2 A = both(1.0f), B = both(0.0f), C = both(0.0f), K = both(0.0f), gate[kSteps];
+  if (__builtin_expect(odd == 0, 1)) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       float2 f, keep;
       gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f, keep);
-      A = __fmul2_rn(A, f), K = fma2(f, K, keep);
-      B = fma2(f, B, __fmul2_rn(keep, row(a, stage, at, 0, i)));
+      gate[i] = join(f, keep);
+      A = __fmul2_rn(A, f), B = fma2(f, B, __fmul2_rn(keep, row(a, stage, at, 0, i))), K = fma2(f, K, keep);
       C = fma2(A, row(a, stage, at, 2, i), C);
     }
   } else {
     bool open = true;  // whether what comes from this row on reaches the warp's first row
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      float2 f, keep;
+      float2 f, keep, d = row(a, stage, at, 2, i);
       gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f, keep);
-      float2 b = __fmul2_rn(keep, row(a, stage, at, 0, i)), d = row(a, stage, at, 2, i);
+      float2 b = __fmul2_rn(keep, row(a, stage, at, 0, i));
       if (!(m.valid >> i & 1)) f = both(1.0f), keep = b = d = both(0.0f);
+      gate[i] = join(f, keep);
       if (m.begins >> i & 1) {
         B = fma2(f, given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at), b);
         open = false;
       } else {
         B = fma2(f, B, b);
       }
-      A = __fmul2_rn(A, f), K = fma2(f, K, keep);
       if (m.ends >> i & 1) d = __fadd2_rn(d, given(a, a.dfinal, __shfl_sync(0xFFFFFFFFu, m.end, i), at));
+      A = __fmul2_rn(A, f), K = fma2(f, K, keep);
       if (open) C = fma2(A, d, C);
       if (m.ends >> i & 1) open = false;
     }
   }
   sh.a[warp][lane] = factor(A, K);
   sh.b[warp][lane] = C, sh.forward[warp][lane] = B;
-  if (lane == 0) sh.cut[warp] = (m.begins ? 1u : 0u) | (m.begins | m.ends ? 2u : 0u);
+  if (lane == 0) sh.cut[warp] = m.cut();
   __syncthreads();
   const uint32_t next = sh.ticket;
-  start(a, other, next);
-  const bool alone = at.tile == a.time_tiles - 1 || mark_at(a, a.ends, at.tile * kRows + kRows - 1, 1) >= 0;
-  carry_over<W, true>(a, sh, at.tile, at.at0, alone);
+  p = sh.spot;
+  start(a, other, next, p);
+  carry_over<true>(a, sh, at.tile, at.at0);
   // Rows' slopes (h_(t-1) - x_t) a_t (1 - a_t), downwards from the warp's state.
-  for (int w = warp / kPer * kPer; w < warp; ++w) h = sh.cut[w] & 1 ? sh.forward[w][lane] : fma2(sh.a[w][lane], h, sh.forward[w][lane]);
-  float2 gate[kSteps], slope[kSteps];
+  for (int w = warp / kPer * kPer; w < warp; ++w) h = sh.cut[w] & CUT_DOWN ? sh.forward[w][lane] : fma2(sh.a[w][lane], h, sh.forward[w][lane]);
+  float2 slope[kSteps];
+  if (__builtin_expect(odd == 0, 1)) {
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const float2 z = __fadd2_rn(row(a, stage, at, 1, i), shift), x = row(a, stage, at, 0, i);
-    float2 f, keep;
-    gates(z, f, keep);
-    gate[i] = join(f, keep);
-    if (!plain && (m.begins >> i & 1)) h = given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at);
-    slope[i] = __fmul2_rn(fma2(x, both(-1.0f), h), __fmul2_rn(f, keep));
-    if (plain || (m.valid >> i & 1)) h = fma2(f, h, __fmul2_rn(keep, x));
+    for (int i = 0; i < kSteps; ++i) slope_step(row(a, stage, at, 0, i), gate[i], h, slope[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (m.begins >> i & 1) h = given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at);
+      slope_step(row(a, stage, at, 0, i), gate[i], h, slope[i]);
+    }
   }
   __syncthreads();
   float2 e = sh.carry[lane], db = both(0.0f);
-  for (int w = W - 1; w > warp; --w) e = sh.cut[w] & 2 ? sh.b[w][lane] : fma2(sh.a[w][lane], e, sh.b[w][lane]);
+  for (int w = kWarps - 1; w > warp; --w) e = sh.cut[w] & CUT_UP ? sh.b[w][lane] : fma2(sh.a[w][lane], e, sh.b[w][lane]);
+  const int64_t size = out_size(a.dx_bf16), pitch_x = a.ld_dx * size, pitch_g = a.ld_dgate * size;
+  uint8_t *dx = static_cast<uint8_t *>(a.dx) + ((at.first + kSteps - 1) * a.ld_dx + at.column) * size;
+  uint8_t *dgate = static_cast<uint8_t *>(a.dgate) + ((at.first + kSteps - 1) * a.ld_dgate + at.column) * size;
+  if (__builtin_expect(odd == 0, 1)) {
 #pragma unroll
-  for (int i = kSteps - 1; i >= 0; --i) {
-    if (!plain) {
+    for (int i = kSteps - 1; i >= 0; --i) {
+      const float2 dz = gradient_step(a, row(a, stage, at, 2, i), gate[i], slope[i], at, dx, dgate, e);
+      db = __fadd2_rn(db, dz);
+      dx -= pitch_x, dgate -= pitch_g;
+    }
+  } else {
+#pragma unroll
+    for (int i = kSteps - 1; i >= 0; --i) {
       if (m.ends >> i & 1) e = given(a, a.dfinal, __shfl_sync(0xFFFFFFFFu, m.end, i), at);
-      if (!(m.valid >> i & 1)) continue;  // e passes
-    }
-    float2 f, keep;
-    split(gate[i], f, keep);
-    const float2 d = __fadd2_rn(row(a, stage, at, 2, i), e), dz = __fmul2_rn(d, slope[i]);
-    if (at.in) {
-      put<VEC>(a.dx, (at.first + i) * a.ld_dx + at.column, a.dx_bf16, at.second, __fmul2_rn(keep, d));
-      put<VEC>(a.dgate, (at.first + i) * a.ld_dgate + at.column, a.dx_bf16, at.second, dz);
-    }
-    db = __fadd2_rn(db, dz);
-    e = __fmul2_rn(f, d);
-    if (!plain && (m.begins >> i & 1)) {
-      const int32_t s = __shfl_sync(0xFFFFFFFFu, m.begin, i);
-      if (at.in && a.dinitial) put_f32<VEC>(a.dinitial + (int64_t)s * a.cols + at.column, at.second, e);
+      if (m.valid >> i & 1) {  // else e passes
+        const float2 dz = gradient_step(a, row(a, stage, at, 2, i), gate[i], slope[i], at, dx, dgate, e);
+        db = __fadd2_rn(db, dz);
+      }
+      dx -= pitch_x, dgate -= pitch_g;
+      if (m.begins >> i & 1) {
+        const int32_t s = __shfl_sync(0xFFFFFFFFu, m.begin, i);
+        if (at.in && a.dinitial) put_f32<VEC>(a.dinitial + (int64_t)s * a.cols + at.column, at.second, e);
+      }
     }
   }
   if (a.partial) {
@@ -493,7 +578,7 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::backward(con
     sh.a[warp][lane] = db;
     __syncthreads();
     if (warp == 0 && at.in) {
-      for (int w = 1; w < W; ++w) db = __fadd2_rn(db, sh.a[w][lane]);
+      for (int w = 1; w < kWarps; ++w) db = __fadd2_rn(db, sh.a[w][lane]);
       put_f32<VEC>(a.partial + at.tile * a.cols + at.column, at.second, db);
     }
   }
@@ -501,34 +586,39 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::backward(con
 }
 
 template <class T, bool VEC, bool STAGED, bool BACKWARD>
-__global__ void __launch_bounds__(Tile<T, VEC, STAGED, BACKWARD>::W * 32, sizeof(T) == 4 ? 2 : STAGED ? 2 : 1) tile_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant__ Args a) {
   using Work = Tile<T, VEC, STAGED, BACKWARD>;
   extern __shared__ __align__(128) uint8_t stages[];
-  __shared__ Shared<Work::W> sh;
+  __shared__ Shared sh;
   if (threadIdx.x == 0) sh.stop = 0;
   wait_for_previous();
   // Tiles by ticket where they wait for one another, else by block.  A ticket is taken when the tile
   // before it is under way, so that tiles begin in the order of their tickets.
   const bool by_ticket = a.time_tiles > 1;
   uint32_t now = blockIdx.x;
-  if (by_ticket) {
-    if (threadIdx.x == 0) sh.ticket = atomicAdd(a.ticket, 1u) + 1;
-    __syncthreads();
-    now = sh.ticket;
-    __syncthreads();
+  if (threadIdx.x == 0) {
+    sh.ticket = by_ticket ? atomicAdd(a.ticket, 1u) + 1 : now;
+    sh.spot = spot_of<Work::kRows>(a, sh.ticket, BACKWARD);
   }
+  __syncthreads();
+  now = sh.ticket;
+  Spot p = sh.spot;
+  __syncthreads();
   let_next_start();
   int64_t lo = 0, hi = a.rows;
   if (a.packed) lo = offset_at(a, 0), hi = offset_at(a, a.seqs);
-  Work::start(a, stages, now);
+  Work::start(a, stages, now, p);
   for (uint32_t n = 0; now < a.tiles; ++n) {
     uint8_t *stage = stages + (n & 1) * Work::kStage, *other = stages + (~n & 1) * Work::kStage;
-    if (threadIdx.x == 0) sh.ticket = by_ticket ? atomicAdd(a.ticket, 1u) + 1 : now + gridDim.x;
+    if (threadIdx.x == 0) {
+      const uint32_t t = by_ticket ? atomicAdd(a.ticket, 1u) + 1 : now + gridDim.x;
+      sh.ticket = t, sh.spot = spot_of<Work::kRows>(a, t, BACKWARD);
+    }
     if constexpr (STAGED) {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();
     }
-    now = BACKWARD ? Work::backward(a, sh, stage, other, now, lo, hi) : Work::forward(a, sh, stage, other, now, lo, hi);
+    now = BACKWARD ? Work::backward(a, sh, stage, other, p, lo, hi) : Work::forward(a, sh, stage, other, p, lo, hi);
     __syncthreads();
   }
   if constexpr (STAGED) asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -624,7 +714,7 @@ struct Plan {
 };
 Plan plan_of(const fsdp_scan_desc_t &d, bool backward) {
   Plan p = {};
-  const int64_t tile = warps_of(d.x_dtype == FSDP_DTYPE_F32) * kSteps;
+  const int64_t tile = kWarps * steps_of(dtype_bytes(d.x_dtype));
   p.column_tiles = (d.cols + kCols - 1) / kCols;
   p.time_tiles = (d.rows + tile - 1) / tile;
   p.padded_cols = p.column_tiles * kCols;
@@ -653,12 +743,11 @@ const void *kernel(K *k) {
 template <class Work>
 cudaError_t launch_tiles(void (*fn)(Args), Args &a, cudaStream_t s) {
   static_assert(Work::kSmem <= 112 * 1024, "two blocks of an SM");
-  constexpr int64_t kBlocks = Work::kBf16 || Work::kSmem > 72 * 1024 ? 2 : 3;  // of an SM
   cudaError_t e = cudaFuncSetAttribute(kernel(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, Work::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t grid = std::min<int64_t>(a.tiles, (int64_t)device_sms() * kBlocks);
+  const int64_t grid = std::min<int64_t>(a.tiles, (int64_t)device_sms() * 2);
   void *args[] = {&a};
-  return launch_kernel(kernel(fn), dim3((unsigned)grid), dim3(Work::W * 32), args, Work::kSmem, s, true);
+  return launch_kernel(kernel(fn), dim3((unsigned)grid), dim3(kThreads), args, Work::kSmem, s, true);
 }
 template <bool BACKWARD, class T>
 cudaError_t launch_as(bool vec, bool staged, Args &a, cudaStream_t s) {
@@ -697,7 +786,7 @@ fsdp_status_t run(const fsdp_scan_desc_t &d, Args &a, const Plan &p, void *works
     void *args[] = {&a};
     e = launch_kernel(kernel(&mark_kernel), dim3((unsigned)((d.seqs + 7) / 8)), dim3(256), args, 0, s);
   }
-  const bool staged = fit.units && (!BACKWARD || dtype_bytes(d.h_dtype) <= dtype_bytes(d.x_dtype));
+  const bool staged = fit.units && d.h_dtype == d.x_dtype && (!BACKWARD || d.dx_dtype == d.x_dtype);
   if (e == cudaSuccess && a.tiles > 0)
     e = d.x_dtype == FSDP_DTYPE_BF16 ? launch_as<BACKWARD, __nv_bfloat16>(fit.pairs, staged, a, s)
                                      : launch_as<BACKWARD, float>(fit.pairs, staged, a, s);
