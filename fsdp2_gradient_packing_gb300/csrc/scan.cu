@@ -168,13 +168,17 @@ __device__ __forceinline__ Spot spot_of(const Args &a, uint32_t ticket, bool bac
   return p;
 }
 
-struct Shared {
+struct Warps {
   float2 a[kWarps][32], b[kWarps][32];
-  float2 forward[kWarps][32];  // backward pass: B of the states
-  uint4 look[kWindow][32];     // what other tiles have left: A and B, or the state
-  float2 carry[32];
-  uint32_t cut[kWarps], found[kWindow], ticket, stop;
+  uint32_t cut[kWarps], found[kWindow], ticket;
   Spot spot;  // of `ticket`
+};
+template <bool BACKWARD, bool STAGED>
+struct Shared {
+  Warps now[2];  // by turns: a warp may still read one tile's while another writes the next one's
+  float2 forward[BACKWARD ? 2 : 0][kWarps][32];  // backward pass: B of the states
+  uint4 look[STAGED ? 0 : kWindow][32];          // what other tiles have left: A and B, or the state
+  uint32_t stop;
 };
 // Bits of `cut`: nothing passes a warp's rows downwards, or upwards; a sequence begins at their
 // first row; one ends at their last.
@@ -248,8 +252,8 @@ __device__ __forceinline__ bool too_late(const Args &a, uint64_t &began) {
 }
 
 // All warps: the state that comes into a tile from `towards` (-1: the tiles before it, 1: those
-// behind).  A warp reads what kWindow / kWarps of the kWindow nearest tiles have left.  For warp 0.
-__device__ __forceinline__ float2 look_back(const Args &a, Shared &s, int64_t tile, int towards, int64_t at0) {
+// behind).  A warp reads what kWindow / kWarps of the kWindow nearest tiles have left.
+__device__ __forceinline__ float2 look_back(const Args &a, Warps &s, uint32_t &stop, uint4 *look, int64_t tile, int towards, int64_t at0) {
   constexpr int kEach = kWindow / kWarps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   uint64_t began = 0;
@@ -273,24 +277,22 @@ __device__ __forceinline__ float2 look_back(const Args &a, Shared &s, int64_t ti
         if (found) break;
         if ((n & 15u) == 0 && (late = too_late(a, began))) break;
       }
-      s.look[slot][lane] = found == 2 ? make_uint4(c0, 0, c1, 0) : make_uint4((uint32_t)p0, (uint32_t)(p0 >> 32), (uint32_t)p1, (uint32_t)(p1 >> 32));
+      look[slot * 32 + lane] = found == 2 ? make_uint4(c0, 0, c1, 0) : make_uint4((uint32_t)p0, (uint32_t)(p0 >> 32), (uint32_t)p1, (uint32_t)(p1 >> 32));
       if (lane == 0) s.found[slot] = found;
     }
-    if (late) s.stop = 1;  // before the barrier: all threads see the same
+    if (late) stop = 1;  // before the barrier: all threads see the same
     __syncthreads();
     const uint32_t states = __ballot_sync(0xFFFFFFFFu, lane < kWindow && s.found[lane % kWindow] == 2);
     float2 carry = make_float2(0, 0);
-    if (s.stop) return carry;
+    if (*(volatile uint32_t *)&stop) return carry;
     if (states) {
-      if (warp == 0) {
-        const int back = __ffs(states) - 1;
-        const uint4 r = s.look[back][lane];
-        carry = make_float2(__uint_as_float(r.x), __uint_as_float(r.z));
+      const int back = __ffs(states) - 1;
+      const uint4 r = look[back * 32 + lane];
+      carry = make_float2(__uint_as_float(r.x), __uint_as_float(r.z));
 #pragma unroll 4
-        for (int w = back - 1; w >= 0; --w) {
-          const uint4 q = s.look[w][lane];
-          carry = fma2(make_float2(__uint_as_float(q.x), __uint_as_float(q.z)), carry, make_float2(__uint_as_float(q.y), __uint_as_float(q.w)));
-        }
+      for (int w = back - 1; w >= 0; --w) {
+        const uint4 q = look[w * 32 + lane];
+        carry = fma2(make_float2(__uint_as_float(q.x), __uint_as_float(q.z)), carry, make_float2(__uint_as_float(q.y), __uint_as_float(q.w)));
       }
       return carry;
     }
@@ -299,49 +301,57 @@ __device__ __forceinline__ float2 look_back(const Args &a, Shared &s, int64_t ti
   }
 }
 
-// Between a tile's warps: A and B of the whole (from the first warp to the last, or backward the other
-// way), left for other tiles, and the state that comes in.
+// A tile's A and B (from its first warp to its last, or backward the other way), left for other tiles by
+// warp 0, which keeps them.
+struct Whole {
+  float2 A, B;
+  bool cut, alone, last;  // nothing passes; nothing comes in; nothing goes out
+};
 template <bool BACKWARD>
-__device__ __forceinline__ void carry_over(const Args &a, Shared &s, int64_t tile, int64_t at0) {
+__device__ __forceinline__ Whole leave(const Args &a, const Warps &s, int64_t tile, int64_t at0) {
   constexpr uint32_t kBit = BACKWARD ? CUT_UP : CUT_DOWN;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  float2 A = both(1.0f), B = both(0.0f), carry = both(0.0f);
-  bool cut = false;
+  Whole t = {both(1.0f), both(0.0f), false, true, true};
   if (a.time_tiles > 1) {
-    // Whether nothing comes in, and nothing goes out.
-    const bool alone = BACKWARD ? tile == a.time_tiles - 1 || (s.cut[kWarps - 1] & CUT_LAST) : tile == 0 || (s.cut[0] & CUT_FIRST);
-    const bool last = tile == (BACKWARD ? 0 : a.time_tiles - 1);
-    const int64_t at = tile * a.padded_cols + at0;
-    if (warp == 0 && !last) {
+    t.alone = BACKWARD ? tile == a.time_tiles - 1 || (s.cut[kWarps - 1] & CUT_LAST) : tile == 0 || (s.cut[0] & CUT_FIRST);
+    t.last = tile == (BACKWARD ? 0 : a.time_tiles - 1);
+    if (warp == 0 && !t.last) {
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
         const int w = BACKWARD ? kWarps - 1 - k : k;
         const bool c = s.cut[w] & kBit;
-        A = __fmul2_rn(A, s.a[w][lane]);
-        B = c ? s.b[w][lane] : fma2(s.a[w][lane], B, s.b[w][lane]);
-        cut |= c;
+        t.A = __fmul2_rn(t.A, s.a[w][lane]);
+        t.B = c ? s.b[w][lane] : fma2(s.a[w][lane], t.B, s.b[w][lane]);
+        t.cut |= c;
       }
-      if (!cut && !alone)
-        leave_part(a, at, A, B);
+      const int64_t at = tile * a.padded_cols + at0;
+      if (!t.cut && !t.alone)
+        leave_part(a, at, t.A, t.B);
       else if (!(a.fault & 1) || tile != (BACKWARD ? a.time_tiles - 1 : 0))  // the test hook leaves out the first
-        leave_state(a, at, B);
-    }
-    if (!alone) {
-      carry = look_back(a, s, tile, BACKWARD ? 1 : -1, at0);
-      if (warp == 0 && !last && !cut) leave_state(a, at, fma2(A, carry, B));
+        leave_state(a, at, t.B);
     }
   }
-  if (warp == 0) s.carry[lane] = carry;
+  return t;
+}
+// The state that comes into the tile.
+template <bool BACKWARD>
+__device__ __forceinline__ float2 take(const Args &a, Warps &s, uint32_t &stop, uint4 *look, const Whole &t, int64_t tile, int64_t at0) {
+  if (t.alone) return both(0.0f);
+  const float2 carry = look_back(a, s, stop, look, tile, BACKWARD ? 1 : -1, at0);
+  if (threadIdx.x < 32 && !t.last && !t.cut) leave_state(a, tile * a.padded_cols + at0, fma2(t.A, carry, t.B));
+  return carry;
 }
 
 template <class T, bool VEC, bool STAGED, bool BACKWARD>
 struct Tile {
   static constexpr int kSteps = steps_of(sizeof(T)), kApart = VEC ? 1 : 32, kRows = kWarps * kSteps;
   using At = Place<kSteps, VEC>;
+  using Block = Shared<BACKWARD, STAGED>;
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int kMatrix = kRows * kCols * (int)sizeof(T);           // bytes of x or gate in a stage
   static constexpr int kStage = STAGED ? (BACKWARD ? 3 : 2) * kMatrix : 0;
   static constexpr int kSmem = 2 * kStage;
+  static constexpr int kBlocks = BACKWARD || !STAGED ? 2 : 3;  // of an SM
 
   // Where tiles are staged, all matrices have x's type.
   __device__ __forceinline__ static bool out_bf16(int32_t bf16) { return STAGED ? kBf16 : bf16 != 0; }
@@ -357,6 +367,14 @@ struct Tile {
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
+  }
+  // Once a tile's gates have been computed, their place holds what other tiles have left.
+  static_assert(!STAGED || kMatrix >= kWindow * 32 * 16, "no room to look back");
+  __device__ __forceinline__ static uint4 *look_at(Block &all, uint8_t *stage) {
+    if constexpr (STAGED)
+      return reinterpret_cast<uint4 *>(stage + kMatrix);
+    else
+      return &all.look[0][0];
   }
   // Row i of the warp's in x, gate or dh (m 0, 1, 2).
   __device__ __forceinline__ static float2 row(const Args &a, const uint8_t *stage, const At &at, int m, int i) {
@@ -397,8 +415,8 @@ struct Tile {
     return dz;
   }
   // One tile, from its stage; starts the next one's loads into the other stage, and gives its ticket and its place.
-  __device__ static uint32_t forward(const Args &a, Shared &sh, uint8_t *stage, uint8_t *other, Spot &p, int64_t lo, int64_t hi);
-  __device__ static uint32_t backward(const Args &a, Shared &sh, uint8_t *stage, uint8_t *other, Spot &p, int64_t lo, int64_t hi);
+  __device__ static uint32_t forward(const Args &a, Block &all, int turn, uint8_t *stage, uint8_t *other, Spot &p, int64_t lo, int64_t hi);
+  __device__ static uint32_t backward(const Args &a, Block &all, int turn, uint8_t *stage, uint8_t *other, Spot &p, int64_t lo, int64_t hi);
 };
 
 // A warp's A: 1 - K, where K is the recurrence's answer to inputs of 1, or the rows' product where that is
@@ -408,38 +426,38 @@ __device__ __forceinline__ float2 factor(float2 product, float2 K) {
 }
 
 template <class T, bool VEC, bool STAGED, bool BACKWARD>
-__device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::forward(const Args &a, Shared &sh, uint8_t *stage, uint8_t *other,
+__device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::forward(const Args &a, Block &all, int turn, uint8_t *stage, uint8_t *other,
     Spot &p, int64_t lo, int64_t hi) {
   const At at(a, p);
+  Warps &sh = all.now[turn];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const float2 shift = bias(a, at);
   const Marks<kSteps> m(a, p, at.first, lo, hi);
   const uint32_t odd = m.odd();
-  // A row takes h to f h + b.
-  float2 f[kSteps], b[kSteps], A = both(1.0f), B = both(0.0f), K = both(0.0f);
+  // A row takes h to f h + b.  Only f stays in registers: over a warp's rows, b from 1 - f is good to a
+  // rounding of x, and a third block fits the SM.
+  float2 f[kSteps], A = both(1.0f), B = both(0.0f), K = both(0.0f);
   if (__builtin_expect(odd == 0, 1)) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       float2 keep;
       gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f[i], keep);
-      b[i] = __fmul2_rn(keep, row(a, stage, at, 0, i));
-      A = __fmul2_rn(A, f[i]), B = fma2(f[i], B, b[i]), K = fma2(f[i], K, keep);
+      A = __fmul2_rn(A, f[i]), B = fma2(f[i], B, __fmul2_rn(keep, row(a, stage, at, 0, i))), K = fma2(f[i], K, keep);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       float2 keep;
       gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f[i], keep);
-      b[i] = __fmul2_rn(keep, row(a, stage, at, 0, i));
-      if (odd >> i & 1) {
-        if (!(m.valid >> i & 1)) f[i] = both(1.0f), keep = b[i] = both(0.0f);
-        if (m.begins >> i & 1) {
-          b[i] = fma2(f[i], given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at), b[i]);
-          f[i] = keep = both(0.0f);
-          if (B.x - B.x != 0.0f || B.y - B.y != 0.0f) B = both(0.0f);  // an infinity or NaN ends with its sequence
-        }
+      float2 b = __fmul2_rn(keep, row(a, stage, at, 0, i));
+      if (!(m.valid >> i & 1)) f[i] = both(1.0f), keep = b = both(0.0f);
+      if (m.begins >> i & 1) {
+        // The row's state itself, kept in place of f: `initial` may be `final`, which a later tile may write
+        // as soon as this one has left its own state.
+        f[i] = B = fma2(f[i], given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at), b);
+      } else {
+        A = __fmul2_rn(A, f[i]), B = fma2(f[i], B, b), K = fma2(f[i], K, keep);
       }
-      A = __fmul2_rn(A, f[i]), B = fma2(f[i], B, b[i]), K = fma2(f[i], K, keep);
     }
   }
   sh.a[warp][lane] = factor(A, K);
@@ -449,9 +467,8 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::forward(cons
   const uint32_t next = sh.ticket;
   p = sh.spot;
   start(a, other, next, p);
-  carry_over<false>(a, sh, at.tile, at.at0);
-  __syncthreads();
-  float2 h = sh.carry[lane];
+  const Whole whole = leave<false>(a, sh, at.tile, at.at0);
+  float2 h = take<false>(a, sh, all.stop, look_at(all, stage), whole, at.tile, at.at0);
   for (int w = 0; w < warp; ++w) h = sh.cut[w] & CUT_DOWN ? sh.b[w][lane] : fma2(sh.a[w][lane], h, sh.b[w][lane]);
   if (a.states && at.in && at.first % kStateRows == 0 && at.first < a.rows)
     put_f32<VEC>(a.states + at.first / kStateRows * a.cols + at.column, at.second, h);
@@ -460,15 +477,17 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::forward(cons
   if (__builtin_expect(odd == 0, 1)) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      h = fma2(f[i], h, b[i]);
+      h = fma2(f[i], h, __fmul2_rn(fma2(f[i], both(-1.0f), both(1.0f)), row(a, stage, at, 0, i)));
       if (at.in) put<VEC>(out, 0, out_bf16(a.h_bf16), at.second, h);
       out += pitch;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      h = m.begins >> i & 1 ? b[i] : fma2(f[i], h, b[i]);
-      if (at.in && (m.valid >> i & 1)) put<VEC>(out, 0, out_bf16(a.h_bf16), at.second, h);
+      if (m.valid >> i & 1) {
+        h = m.begins >> i & 1 ? f[i] : fma2(f[i], h, __fmul2_rn(fma2(f[i], both(-1.0f), both(1.0f)), row(a, stage, at, 0, i)));
+        if (at.in) put<VEC>(out, 0, out_bf16(a.h_bf16), at.second, h);
+      }
       out += pitch;
       if (m.ends >> i & 1) {
         const int32_t s = __shfl_sync(0xFFFFFFFFu, m.end, i);
@@ -480,9 +499,10 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::forward(cons
 }
 
 template <class T, bool VEC, bool STAGED, bool BACKWARD>
-__device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::backward(const Args &a, Shared &sh, uint8_t *stage, uint8_t *other,
+__device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::backward(const Args &a, Block &all, int turn, uint8_t *stage, uint8_t *other,
     Spot &p, int64_t lo, int64_t hi) {
   const At at(a, p);
+  Warps &sh = all.now[turn];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const float2 shift = bias(a, at);
   const Marks<kSteps> m(a, p, at.first, lo, hi);
@@ -525,15 +545,15 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::backward(con
     }
   }
   sh.a[warp][lane] = factor(A, K);
-  sh.b[warp][lane] = C, sh.forward[warp][lane] = B;
+  sh.b[warp][lane] = C, all.forward[turn][warp][lane] = B;
   if (lane == 0) sh.cut[warp] = m.cut();
   __syncthreads();
   const uint32_t next = sh.ticket;
   p = sh.spot;
   start(a, other, next, p);
-  carry_over<true>(a, sh, at.tile, at.at0);
+  const Whole whole = leave<true>(a, sh, at.tile, at.at0);
   // Rows' slopes (h_(t-1) - x_t) a_t (1 - a_t), downwards from the warp's state.
-  for (int w = warp / kPer * kPer; w < warp; ++w) h = sh.cut[w] & CUT_DOWN ? sh.forward[w][lane] : fma2(sh.a[w][lane], h, sh.forward[w][lane]);
+  for (int w = warp / kPer * kPer; w < warp; ++w) h = sh.cut[w] & CUT_DOWN ? all.forward[turn][w][lane] : fma2(sh.a[w][lane], h, all.forward[turn][w][lane]);
   float2 slope[kSteps];
   if (__builtin_expect(odd == 0, 1)) {
 #pragma unroll
@@ -545,8 +565,7 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::backward(con
       slope_step(row(a, stage, at, 0, i), gate[i], h, slope[i]);
     }
   }
-  __syncthreads();
-  float2 e = sh.carry[lane], db = both(0.0f);
+  float2 e = take<true>(a, sh, all.stop, look_at(all, stage), whole, at.tile, at.at0), db = both(0.0f);
   for (int w = kWarps - 1; w > warp; --w) e = sh.cut[w] & CUT_UP ? sh.b[w][lane] : fma2(sh.a[w][lane], e, sh.b[w][lane]);
   const int64_t size = out_size(a.dx_bf16), pitch_x = a.ld_dx * size, pitch_g = a.ld_dgate * size;
   uint8_t *dx = static_cast<uint8_t *>(a.dx) + ((at.first + kSteps - 1) * a.ld_dx + at.column) * size;
@@ -586,10 +605,10 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::backward(con
 }
 
 template <class T, bool VEC, bool STAGED, bool BACKWARD>
-__global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, Tile<T, VEC, STAGED, BACKWARD>::kBlocks) tile_kernel(const __grid_constant__ Args a) {
   using Work = Tile<T, VEC, STAGED, BACKWARD>;
   extern __shared__ __align__(128) uint8_t stages[];
-  __shared__ Shared sh;
+  __shared__ typename Work::Block sh;
   if (threadIdx.x == 0) sh.stop = 0;
   wait_for_previous();
   // Tiles by ticket where they wait for one another, else by block.  A ticket is taken when the tile
@@ -597,31 +616,29 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
   const bool by_ticket = a.time_tiles > 1;
   uint32_t now = blockIdx.x;
   if (threadIdx.x == 0) {
-    sh.ticket = by_ticket ? atomicAdd(a.ticket, 1u) + 1 : now;
-    sh.spot = spot_of<Work::kRows>(a, sh.ticket, BACKWARD);
+    sh.now[1].ticket = by_ticket ? atomicAdd(a.ticket, 1u) + 1 : now;
+    sh.now[1].spot = spot_of<Work::kRows>(a, sh.now[1].ticket, BACKWARD);
   }
   __syncthreads();
-  now = sh.ticket;
-  Spot p = sh.spot;
-  __syncthreads();
+  now = sh.now[1].ticket;
+  Spot p = sh.now[1].spot;
   let_next_start();
   int64_t lo = 0, hi = a.rows;
   if (a.packed) lo = offset_at(a, 0), hi = offset_at(a, a.seqs);
   Work::start(a, stages, now, p);
   for (uint32_t n = 0; now < a.tiles; ++n) {
     uint8_t *stage = stages + (n & 1) * Work::kStage, *other = stages + (~n & 1) * Work::kStage;
+    Warps &turn = sh.now[n & 1];
     if (threadIdx.x == 0) {
       const uint32_t t = by_ticket ? atomicAdd(a.ticket, 1u) + 1 : now + gridDim.x;
-      sh.ticket = t, sh.spot = spot_of<Work::kRows>(a, t, BACKWARD);
+      turn.ticket = t, turn.spot = spot_of<Work::kRows>(a, t, BACKWARD);
     }
-    if constexpr (STAGED) {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      __syncthreads();
-    }
-    now = BACKWARD ? Work::backward(a, sh, stage, other, p, lo, hi) : Work::forward(a, sh, stage, other, p, lo, hi);
-    __syncthreads();
+    if constexpr (STAGED) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the stage is whole, and every warp has left the tile before
+    now = BACKWARD ? Work::backward(a, sh, n & 1, stage, other, p, lo, hi) : Work::forward(a, sh, n & 1, stage, other, p, lo, hi);
   }
   if constexpr (STAGED) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
   if (threadIdx.x == 0 && sh.stop) atomicAdd(a.gave_up, 1u);
 }
 
@@ -742,10 +759,13 @@ const void *kernel(K *k) {
 // The largest number of blocks that the device holds at once.
 template <class Work>
 cudaError_t launch_tiles(void (*fn)(Args), Args &a, cudaStream_t s) {
-  static_assert(Work::kSmem <= 112 * 1024, "two blocks of an SM");
+  static_assert((Work::kSmem + (int)sizeof(typename Work::Block) + 1024) * Work::kBlocks <= 228 * 1024, "an SM's blocks");
   cudaError_t e = cudaFuncSetAttribute(kernel(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, Work::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t grid = std::min<int64_t>(a.tiles, (int64_t)device_sms() * 2);
+  // Few columns are bound by the chain of carries, which a third block of an SM delays (us with two / three blocks, BF16
+  // forward: 65536 x 256 46 / 56, 65536 x 1024 119 / 116, 32768 x 4096 214 / 205).
+  const int blocks = a.column_tiles <= 8 ? 2 : Work::kBlocks;
+  const int64_t grid = std::min<int64_t>(a.tiles, (int64_t)device_sms() * blocks);
   void *args[] = {&a};
   return launch_kernel(kernel(fn), dim3((unsigned)grid), dim3(kThreads), args, Work::kSmem, s, true);
 }
