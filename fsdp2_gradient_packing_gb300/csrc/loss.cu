@@ -1,22 +1,39 @@
 // Losses over rows of logits (fsdp_distill_loss_*, fsdp_policy_loss_*).
 //
-// A block to a row, which it reads once for the sum of exponentials and once more for the
-// gradient.
+// Everything is bound by the logits' bytes: read once for a loss, read once and written once for a gradient
+// or both.  A row is cut into slices of whole 16-byte units; a block reads a slice with one TMA bulk copy
+// into a ring of shared-memory stages, the next one on its way while it works.  For a loss with its gradient
+// a cluster of blocks holds the whole row: each thread keeps its elements' exponentials (relative to its own
+// maximum) in registers, the blocks' maxima and sums meet in distributed shared memory, and the gradient is
+// a product per element, without a second read or exponential.  For a loss alone a block or cluster walks
+// over a row's slices; the gradient alone (given lse) treats slices one by one.  Rows that no
+// cluster holds (above 131,072 BF16 or 65,536 FP32 logits) take these two in turn.
+//
+// A ninth warp fills the ring and prepares what a row has beside its logits: the policy's scalars,
+// or the softmax of the teacher's entries, while the others are at the row before.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <string>
 
 #include "layout.h"
 #include "ops.h"
+#include "tc.h"
 
 namespace fsdp {
 namespace loss {
 namespace {
 
-constexpr int kThreads = 256, kMaxTop = FSDP_DISTILL_MAX_TOP;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kMaxTop = FSDP_DISTILL_MAX_TOP;
+constexpr int kMaxCluster = 8, kMaxStages = 4;
+constexpr int kMostUnits = 8;  // 16-byte units of a slice that a thread has
+constexpr int kMostSmem = 104 * 1024;  // stages, and what goes with a row: 2 x (32 + 16.1) or 4 x (8 + 16.1) KB at most
+constexpr float kLog2E = 1.4426950408889634f;
+
+enum Mode { STATS, BOTH, GRADIENT };
 
 struct Args {
   const void *logits;
@@ -24,141 +41,611 @@ struct Args {
   const void *tokens, *teacher;
   const float *old_logp, *ref_logp, *advantage, *weight, *dloss, *lse_in, *logp_in;
   float *loss, *logp, *lse;
+  uint32_t *gave_up;
+  uint64_t wait_limit_ns;
   int64_t rows, ld_z, ld_g, ld_tokens, ld_teacher;
-  int32_t vocab, top, z_bf16, g_bf16, teacher_bf16, wide, backward;
-  float t, inv_t, low, high, kl;
+  int64_t items;       // rows, or rows x slices
+  int32_t vocab, top, z_bf16, g_bf16, teacher_bf16, wide, backward, fault;
+  int32_t cluster, rounds, slices;  // blocks to a row; slices of a block, one after another; slices as items
+  int32_t units;       // of a slice, at most
+  int32_t stages, stage_bytes, side_bytes;
+  float t, inv_t, scale;  // scale: log2 e / T
+  float low, high, kl;
 };
 
-__device__ __forceinline__ float block_sum(float v, bool take_max, float *part) {
-  for (int m = 16; m > 0; m /= 2) {
-    const float o = __shfl_xor_sync(0xFFFFFFFFu, v, m);
-    v = take_max ? fmaxf(v, o) : v + o;
-  }
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
-  __syncthreads();
-  v = part[0];
-  for (int w = 1; w < kThreads / 32; ++w) v = take_max ? fmaxf(v, part[w]) : v + part[w];
-  return v;
+// What the ninth warp prepares of a row.  Teacher's entries follow it: tokens, q, the gradient's q (negative: another entry
+// of the same token has it), and room for their logits.
+struct alignas(16) Side {
+  float up;          // weight x dloss
+  float weight;
+  float lse;         // backward
+  float slope;       // backward
+  float old, ref, advantage;
+  float mass, q_log_q;  // teacher: sum of q (1 or 0), sum of q log q
+  int32_t token;     // policy, -1: none
+};
+
+struct alignas(16) Shared {
+  float4 warp[2][kWarps];        // maximum and sum of a warp, and what it has of the targets
+  float4 block[2][kMaxCluster];  // the same of the cluster's blocks
+  uint64_t arrived[2], full[kMaxStages], empty[kMaxStages];
+  uint32_t named[kThreads * kMostUnits * 8 / 32];  // the slice's elements that the teacher has named
+  uint32_t stop;
+};
+
+__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-__device__ __forceinline__ int64_t token_at(const Args &a, int64_t i) {
+// Maxima are kept as logits and subtracted before a difference is scaled: logits of the type's lowest
+// value have no finite multiple, but differences that count do.
+// 2^((m - top) scale), 1 where they are equal, infinite or not.
+__device__ __forceinline__ float below(float m, float top, float scale) { return ex2(m == top ? 0.0f : (m - top) * scale); }
+// Maximum and sum (of 2^((z - maximum) scale)) of two sets, without a NaN for empty ones.
+__device__ __forceinline__ void merge(float &m, float &s, float m2, float s2, float scale) {
+  const float top = fmaxf(m, m2);
+  s = s * below(m, top, scale) + s2 * below(m2, top, scale);
+  m = top;
+}
+
+__device__ __forceinline__ int32_t token_at(const Args &a, int64_t i) {
   const int64_t t = a.wide ? static_cast<const int64_t *>(a.tokens)[i] : static_cast<const int32_t *>(a.tokens)[i];
-  return t >= 0 && t < a.vocab ? t : -1;
+  return t >= 0 && t < a.vocab ? (int32_t)t : -1;
 }
 
-template <bool DISTILL>
-__global__ void __launch_bounds__(kThreads) row_kernel(const __grid_constant__ Args a) {
-  __shared__ float part[kThreads / 32];
-  __shared__ int32_t ids[DISTILL ? kMaxTop : 1];
-  __shared__ float q[DISTILL ? kMaxTop : 1], zt[DISTILL ? kMaxTop : 1];
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const float w = a.weight ? a.weight[row] : 1.0f;
-    const int64_t z0 = row * a.ld_z, g0 = row * a.ld_g;
-    if (w == 0.0f) {
-      if (threadIdx.x == 0 && !a.backward) {
-        a.loss[row] = 0.0f, a.lse[row] = 0.0f;
-        if (!DISTILL) a.logp[row] = 0.0f;
-      }
-      for (int32_t i = threadIdx.x; a.dlogits && i < a.vocab; i += kThreads) store_any(a.dlogits, g0 + i, a.g_bf16, 0.0f);
-      continue;
+// Where a slice of a row is: its 16-byte units, which begin up to a unit before the row.
+template <class T>
+struct Slice {
+  static constexpr int kPer = 16 / (int)sizeof(T);  // elements of a unit
+  int64_t row;
+  uintptr_t at;   // of the slice's first unit
+  int32_t phase;  // elements between the row's first unit and the row
+  int32_t first, units;  // first unit in the row, and how many the slice has of it
+  int32_t row_units;
+  __device__ __forceinline__ Slice(const Args &a, int64_t r, int32_t index) : row(r) {
+    const uintptr_t p = (uintptr_t)a.logits + r * a.ld_z * sizeof(T);
+    phase = (int32_t)(p & 15u) / (int)sizeof(T);
+    row_units = (phase + a.vocab + kPer - 1) / kPer;
+    first = index * a.units;
+    units = max(0, min(a.units, row_units - first));
+    at = (p & ~(uintptr_t)15) + (int64_t)first * 16;
+  }
+  // Elements of the row that the slice has.
+  __device__ __forceinline__ int32_t begin() const { return max(0, first * kPer - phase); }
+  __device__ __forceinline__ int32_t end(const Args &a) const { return min(a.vocab, (first + units) * kPer - phase); }
+};
+
+// The policy's loss and its derivative with respect to logp.
+__device__ __forceinline__ void policy_of(const Args &a, float logp, const Side &s, float &loss, float &slope) {
+  const float r = a.old_logp ? expf(logp - s.old) : 1.0f, held = fminf(fmaxf(r, a.low), a.high);
+  const float one = r * s.advantage, two = held * s.advantage;
+  loss = -fminf(one, two);
+  if (one != one) loss = one;
+  slope = one <= two ? -one : one != one ? one : 0.0f;
+  if (a.ref_logp) {
+    const float gap = s.ref - logp, e = expm1f(gap);
+    loss += a.kl * (e - gap);
+    slope -= a.kl * e;
+  }
+}
+
+// ---- the ninth warp ------------------------------------------------------------------------
+template <class T>
+__device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side, int64_t row, const Slice<T> &slice, bool gradient) {
+  const int lane = threadIdx.x & 31;
+  int32_t *ids = reinterpret_cast<int32_t *>(&side + 1);
+  float *q = reinterpret_cast<float *>(ids + a.top), *gq = q + a.top, *v = gq + a.top;
+  float top = -INFINITY;
+  bool nan = false;
+#pragma unroll 2
+  for (int j = lane; j < a.top; j += 32) {
+    const int32_t id = token_at(a, row * a.ld_tokens + j);
+    const float x = id < 0 ? -INFINITY : load_any(a.teacher, row * a.ld_teacher + j, a.teacher_bf16) * a.inv_t;
+    ids[j] = x == -INFINITY ? -1 : id;
+    v[j] = x;
+    top = fmaxf(top, x);
+    nan |= x != x;
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+  nan = __any_sync(0xFFFFFFFFu, nan);
+  float sum = 0.0f;
+  for (int j = lane; j < a.top; j += 32) {
+    const float e = ids[j] < 0 ? 0.0f : ex2((v[j] - top) * kLog2E);
+    q[j] = e;
+    sum += e;
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
+  const bool some = sum > 0.0f || sum != sum || nan;
+  const float inv = some ? 1.0f / sum : 0.0f, log_sum = logf(sum);
+  float total = 0.0f;
+  const int32_t lo = slice.begin(), hi = slice.end(a);
+  bool twice = false;
+  for (int j = lane; j < a.top; j += 32) {
+    const float p = q[j] * inv;
+    q[j] = gq[j] = p;
+    if (p > 0.0f || p != p) total += p * (v[j] - top - log_sum);
+    if (gradient && ids[j] >= lo && ids[j] < hi) {
+      const uint32_t bit = 1u << ((ids[j] - lo) & 31);
+      twice |= (atomicOr(&sh.named[(ids[j] - lo) / 32], bit) & bit) != 0;
     }
-    float lse;
-    if (a.backward) {
-      lse = a.lse_in[row];
-    } else {
-      float top = -INFINITY;
-      bool nan = false;
-      for (int32_t i = threadIdx.x; i < a.vocab; i += kThreads) {
-        const float z = load_any(a.logits, z0 + i, a.z_bf16) * a.inv_t;
-        top = fmaxf(top, z);
-        nan |= z != z;
-      }
-      top = block_sum(top, true, part);
-      float sum = nan ? NAN : 0.0f;
-      const float nans = block_sum(sum, false, part);
-      for (int32_t i = threadIdx.x; i < a.vocab; i += kThreads) sum += expf(load_any(a.logits, z0 + i, a.z_bf16) * a.inv_t - top);
-      sum = block_sum(sum, false, part);
-      lse = nans != nans ? nans : top == -INFINITY ? top : top + logf(sum);
-      if (threadIdx.x == 0) a.lse[row] = lse;
-    }
-    float slope = 0.0f, mass = 0.0f;  // dz_i = slope (mass p_i - q_i)
-    int64_t token = -1;
-    float zq = 0.0f;
-    const float up = w * (a.backward && a.dloss ? a.dloss[row] : 1.0f);
-    if constexpr (DISTILL) {
-      float top = -INFINITY;
-      __syncthreads();
-      for (int k = threadIdx.x; k < a.top; k += kThreads) {
-        const int64_t t = token_at(a, row * a.ld_tokens + k);
-        const float v = t < 0 ? -INFINITY : load_any(a.teacher, row * a.ld_teacher + k, a.teacher_bf16) * a.inv_t;
-        ids[k] = v == -INFINITY ? -1 : (int32_t)t;
-        q[k] = v;
-        zt[k] = ids[k] < 0 ? 0.0f : load_any(a.logits, z0 + t, a.z_bf16) * a.inv_t;
-        top = fmaxf(top, v);
-      }
-      top = block_sum(top, true, part);
-      float sum = 0.0f;
-      for (int k = threadIdx.x; k < a.top; k += kThreads)
-        if (ids[k] >= 0) sum += expf(q[k] - top);
-      sum = block_sum(sum, false, part);
-      float l = 0.0f;
-      for (int k = threadIdx.x; k < a.top; k += kThreads)
-        if (ids[k] >= 0) {
-          const float lq = q[k] - top - logf(sum), p = expf(lq);
-          q[k] = p;
-          if (p > 0.0f || p != p) l += p * (lq - zt[k] + lse);
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m /= 2) total += __shfl_xor_sync(0xFFFFFFFFu, total, m);
+  if (gradient) {
+    __syncwarp();
+    for (int j = lane; j < a.top; j += 32)
+      if (ids[j] >= lo && ids[j] < hi) sh.named[(ids[j] - lo) / 32] = 0;
+    if (__any_sync(0xFFFFFFFFu, twice)) {
+      // A token is named more than once: its first entry takes what the others have, in their order.
+      for (int j = 0; j < a.top; ++j) {
+        if (ids[j] < lo || ids[j] >= hi || gq[j] < 0.0f) continue;
+        float s = gq[j];
+        for (int k0 = j + 1; k0 < a.top; k0 += 32) {
+          const int k = k0 + lane;
+          const bool same = k < a.top && ids[k] == ids[j];
+          const float other = same ? q[k] : 0.0f;
+          uint32_t which = __ballot_sync(0xFFFFFFFFu, same);
+          if (same) gq[k] = -1.0f;
+          for (; which; which &= which - 1) s += __shfl_sync(0xFFFFFFFFu, other, __ffs(which) - 1);
         }
-      l = block_sum(l, false, part);
-      if (threadIdx.x == 0 && !a.backward) a.loss[row] = w * a.t * a.t * l;
-      mass = sum > 0.0f || sum != sum ? 1.0f : 0.0f;
-      slope = up * a.t;
-    } else {
-      token = token_at(a, row);
-      if (token >= 0) {
-        zq = load_any(a.logits, z0 + token, a.z_bf16) * a.inv_t;
-        const float logp = a.backward ? a.logp_in[row] : zq - lse;
-        const float r = a.old_logp ? expf(logp - a.old_logp[row]) : 1.0f, adv = a.advantage[row];
-        const float held = fminf(fmaxf(r, a.low), a.high);
-        const float gap = a.ref_logp ? a.ref_logp[row] - logp : 0.0f;
-        if (threadIdx.x == 0 && !a.backward) {
-          a.logp[row] = logp;
-          a.loss[row] = w * (-fminf(r * adv, held * adv) + (a.ref_logp ? a.kl * (expm1f(gap) - gap) : 0.0f));
-        }
-        slope = -((r * adv <= held * adv ? -r * adv : 0.0f) + (a.ref_logp ? -a.kl * expm1f(gap) : 0.0f)) * up * a.inv_t;
-        mass = 1.0f;
-      } else if (threadIdx.x == 0 && !a.backward) {
-        a.logp[row] = 0.0f, a.loss[row] = 0.0f;
-      }
-    }
-    if (!a.dlogits) continue;
-    __syncthreads();  // every thread has read what it needs of a row that may be overwritten
-    for (int32_t i = threadIdx.x; i < a.vocab; i += kThreads) {
-      const float p = mass != 0.0f ? expf(load_any(a.logits, z0 + i, a.z_bf16) * a.inv_t - lse) : 0.0f;
-      store_any(a.dlogits, g0 + i, a.g_bf16, mass != 0.0f ? slope * (p - (i == token ? 1.0f : 0.0f)) : 0.0f);
-    }
-    if constexpr (DISTILL) {
-      __syncthreads();
-      for (int k = threadIdx.x; k < a.top; k += kThreads) {
-        if (ids[k] < 0) continue;
-        float s = 0.0f;
-        bool first = true;
-        for (int m = 0; m < a.top; ++m)
-          if (ids[m] == ids[k]) {
-            first &= m >= k;
-            s += q[m];
-          }
-        if (first) store_any(a.dlogits, g0 + ids[k], a.g_bf16, slope * (expf(zt[k] - lse) - s));
+        __syncwarp();
+        if (lane == 0) gq[j] = s;
+        __syncwarp();
       }
     }
   }
+  if (lane == 0) side.mass = some ? 1.0f : 0.0f, side.q_log_q = total;
+}
+
+template <bool DISTILL, class T, Mode MODE>
+__device__ __forceinline__ void feed(const Args &a, Shared &sh, uint8_t *stages, uint32_t rank, int64_t first, int64_t step) {
+  const int lane = threadIdx.x & 31;
+  int stage = 0, side_at = 0;
+  uint32_t parity = 1;
+  auto weight_of = [&](int64_t item) {
+    const int64_t row = MODE == GRADIENT ? item / a.slices : item;
+    return item < a.items && a.weight ? a.weight[row] : 1.0f;
+  };
+  float ahead = weight_of(first);
+  bool skip = (a.fault & 1) != 0 && blockIdx.x == 0;  // test hook: a first stage that stays empty
+  for (int64_t item = first; item < a.items; item += step) {
+    const int64_t row = MODE == GRADIENT ? item / a.slices : item;
+    const float weight = ahead;
+    ahead = weight_of(item + step);
+    for (int round = 0; round < a.rounds; ++round) {
+      const Slice<T> slice(a, row, MODE == GRADIENT ? (int32_t)(item - row * a.slices) : (int32_t)rank * a.rounds + round);
+      const uint32_t full = tc::smem(&sh.full[stage]);
+      tc::bar_wait(tc::smem(&sh.empty[stage]), parity, a.wait_limit_ns, &sh.stop);
+      if (lane == 0) {
+        if (weight != 0.0f && slice.units > 0 && !skip) {
+          tc::bar_expect(full, slice.units * 16);
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                           tc::smem(stages + stage * a.stage_bytes)),
+                       "l"(slice.at), "r"(slice.units * 16), "r"(full)
+                       : "memory");
+        } else if (!skip) {
+          tc::bar_arrive(full);
+        }
+        skip = false;
+      }
+      if (round == 0) {
+        Side &side = *reinterpret_cast<Side *>(stages + a.stages * a.stage_bytes + side_at * a.side_bytes);
+        float slope = 0.0f;
+        const float dloss = MODE == GRADIENT && a.dloss && weight != 0.0f ? a.dloss[row] : 1.0f, up = weight * dloss;
+        if (lane == 0) {
+          side.weight = weight, side.up = up;
+          if (MODE == GRADIENT) side.lse = weight != 0.0f ? a.lse_in[row] : 0.0f;
+        }
+        if (weight != 0.0f) {
+          if constexpr (DISTILL) {
+            teacher_of<T>(a, sh, side, row, slice, MODE != STATS);
+            slope = up * a.t;
+          } else if (lane == 0) {
+            side.old = a.old_logp ? a.old_logp[row] : 0.0f;
+            side.ref = a.ref_logp ? a.ref_logp[row] : 0.0f;
+            side.advantage = a.advantage[row];
+            side.token = token_at(a, row);
+            side.mass = side.token >= 0 ? 1.0f : 0.0f;
+            if (MODE == GRADIENT) {
+              float l, d;
+              policy_of(a, a.logp_in[row], side, l, d);
+              slope = -d * up * a.inv_t;
+            }
+          }
+        }
+        if (lane == 0) side.slope = slope;
+        if (++side_at == a.stages) side_at = 0;
+      }
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(full);
+      if (++stage == a.stages) stage = 0, parity ^= 1u;
+    }
+  }
+}
+
+// ---- the other eight ----------------------------------------------------------------------
+// Element e of unit u of the slice that is in shared memory, as the row's element.
+template <class T>
+__device__ __forceinline__ float staged(const uint8_t *stage, const Slice<T> &s, int32_t element) {
+  return (float)reinterpret_cast<const T *>(stage)[element + s.phase - s.first * Slice<T>::kPer];
+}
+
+// The elements of unit u of a slice (-infinity outside the row) as pairs.
+template <class T>
+__device__ __forceinline__ void unit_of(const Args &a, const uint8_t *stage, const Slice<T> &s, int u, float2 (&z)[Slice<T>::kPer / 2]) {
+  constexpr int P = Slice<T>::kPer;
+  if (u >= s.units) {
+#pragma unroll
+    for (int e = 0; e < P / 2; ++e) z[e] = both(-INFINITY);
+    return;
+  }
+  const uint4 r = *reinterpret_cast<const uint4 *>(stage + u * 16);
+  if constexpr (sizeof(T) == 2) {
+    unpack8(r, z);
+  } else {
+    z[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y)), z[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+  }
+  const int32_t g = s.first + u;
+  if (g == 0 || g == s.row_units - 1) {
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      const int32_t j = g * P + e - s.phase;
+      if (j < 0 || j >= a.vocab) element(z, e) = -INFINITY;
+    }
+  }
+}
+
+// A unit's gradient.  `even`: units of the gradient's rows begin on their own boundaries.
+template <class T>
+__device__ __forceinline__ void put_unit(const Args &a, const Slice<T> &s, void *g_row, bool even, int u, const float2 (&v)[Slice<T>::kPer / 2]) {
+  constexpr int P = Slice<T>::kPer;
+  if (u >= s.units) return;
+  const int32_t g = s.first + u, j = g * P - s.phase;
+  if (even && j >= 0 && j + P <= a.vocab) {
+    if constexpr (P == 8) {
+      store8(g_row, j, a.g_bf16 != 0, v);
+    } else if (a.g_bf16) {
+      *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(g_row) + j) = make_uint2(bf16_pair(v[0].x, v[0].y), bf16_pair(v[1].x, v[1].y));
+    } else {
+      *reinterpret_cast<float4 *>(static_cast<float *>(g_row) + j) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < P; ++e)
+      if (j + e >= 0 && j + e < a.vocab) store_any(g_row, j + e, a.g_bf16 != 0, element(v, e));
+  }
+}
+
+template <bool DISTILL, class T, int K, Mode MODE>
+__device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages, uint32_t rank, int64_t first, int64_t step) {
+  constexpr int P = Slice<T>::kPer;
+  const int t = threadIdx.x, lane = t & 31, warp = t / 32;
+  int stage_at = 0, side_at = 0, turn = 0;
+  uint32_t parity = 0;
+  for (int64_t item = first; item < a.items; item += step) {
+    const int64_t row = MODE == GRADIENT ? item / a.slices : item;
+    Side &side = *reinterpret_cast<Side *>(stages + a.stages * a.stage_bytes + side_at * a.side_bytes);
+    const int32_t *ids = reinterpret_cast<const int32_t *>(&side + 1);
+    const float *q = reinterpret_cast<const float *>(ids + a.top), *gq = q + a.top;
+    float *zt = const_cast<float *>(gq) + a.top;
+    if (++side_at == a.stages) side_at = 0;
+    uint8_t *g_row = static_cast<uint8_t *>(a.dlogits) + row * a.ld_g * (a.g_bf16 ? 2 : 4);
+    float m = -INFINITY, sum = 0.0f, hit = 0.0f;  // of the thread, over the block's slices; what it has of the targets
+    for (int round = 0; round < a.rounds; ++round) {
+      const Slice<T> slice(a, row, MODE == GRADIENT ? (int32_t)(item - row * a.slices) : (int32_t)rank * a.rounds + round);
+      const uint8_t *stage = stages + stage_at * a.stage_bytes;
+      const bool even = ((uintptr_t)g_row - slice.phase * (a.g_bf16 ? 2 : 4)) % (a.g_bf16 ? P * 2 : 16) == 0;
+      tc::bar_wait(tc::smem(&sh.full[stage_at]), parity, a.wait_limit_ns, &sh.stop);
+      const float weight = side.weight;
+      float2 e[MODE == GRADIENT ? 1 : K][P / 2];
+      if (weight != 0.0f) {
+        // The targets' logits.
+        if constexpr (DISTILL) {
+          const int32_t lo = slice.begin(), hi = slice.end(a);
+          for (int j = t; j < a.top; j += kThreads)
+            if (ids[j] >= lo && ids[j] < hi) {
+              const float z = staged(stage, slice, ids[j]);
+              if (MODE != STATS) zt[j] = z;
+              if (MODE != GRADIENT && (q[j] > 0.0f || q[j] != q[j])) hit += q[j] * z;
+            }
+        } else if (MODE != GRADIENT) {
+          if (t == 0 && side.token >= slice.begin() && side.token < slice.end(a)) hit += staged(stage, slice, side.token);
+        }
+        if constexpr (MODE != GRADIENT) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            unit_of(a, stage, slice, k * kThreads + t, e[k]);
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) top = fmaxf(top, fmaxf(e[k][i].x, e[k][i].y));
+          }
+          const float2 less = both(top == -INFINITY ? 0.0f : -top), by = both(a.scale);
+          float2 s = both(0.0f);
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) {
+              const float2 x = __fmul2_rn(__fadd2_rn(e[k][i], less), by);
+              e[k][i] = make_float2(ex2(x.x), ex2(x.y));
+              s = __fadd2_rn(s, e[k][i]);
+            }
+          if constexpr (MODE == BOTH)
+            m = top, sum = s.x + s.y;
+          else
+            merge(m, sum, top, s.x + s.y, a.scale);
+        }
+      }
+      if (MODE != GRADIENT && round == a.rounds - 1) {
+        const int slot = turn & 1;
+        float M = m, S = sum, X = hit;
+        if (weight != 0.0f) {
+#pragma unroll
+          for (int d = 16; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+          S = sum * below(m, M, a.scale);
+#pragma unroll
+          for (int d = 16; d > 0; d /= 2) S += __shfl_xor_sync(0xFFFFFFFFu, S, d), X += __shfl_xor_sync(0xFFFFFFFFu, X, d);
+          if (lane == 0) sh.warp[slot][warp] = make_float4(M, S, X, 0.0f);
+          workers_sync();
+          auto join = [&](const float4 *p, int n) {
+            float4 v = p[0];
+            M = v.x, S = v.y, X = v.z;
+            for (int w = 1; w < n; ++w) {
+              v = p[w];
+              merge(M, S, v.x, v.y, a.scale);
+              X += v.z;
+            }
+          };
+          if (a.cluster > 1) {
+            const uint32_t bar = tc::smem(&sh.arrived[slot]);
+            if (t < a.cluster) {
+              join(sh.warp[slot], kWarps);
+              asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(tc::at_rank(tc::smem(&sh.block[slot][rank]), t)), "f"(M),
+                           "f"(S), "f"(X), "f"(0.0f)
+                           : "memory");
+              tc::bar_arrive_cluster(tc::at_rank(bar, t));
+            }
+            tc::bar_wait(bar, (uint32_t)(turn >> 1) & 1u, a.wait_limit_ns, &sh.stop);
+            join(sh.block[slot], a.cluster);
+          } else {
+            join(sh.warp[slot], kWarps);
+          }
+          ++turn;
+        }
+        float loss = 0.0f, logp = 0.0f, lse = 0.0f, slope = 0.0f;
+        if (weight != 0.0f) {
+          const float log_sum = logf(S);
+          lse = fmaf(M, a.inv_t, log_sum);
+          if constexpr (DISTILL) {
+            if (side.mass != 0.0f) loss = weight * a.t * a.t * (side.q_log_q + lse - a.inv_t * X);
+            slope = side.slope;
+          } else if (side.token >= 0) {
+            logp = fmaf(X - M, a.inv_t, -log_sum);
+            policy_of(a, logp, side, loss, slope);
+            loss *= weight;
+            slope *= -side.up * a.inv_t;
+          }
+        }
+        if (t == 0 && rank == 0) {
+          a.loss[row] = loss, a.lse[row] = lse;
+          if (!DISTILL) a.logp[row] = logp;
+        }
+        if constexpr (MODE == BOTH) {
+          if (weight != 0.0f && side.mass != 0.0f) {
+            const float part = slope / S;
+            const float2 by = both(part * below(m, M, a.scale));
+            const int32_t own = DISTILL ? -1 : (side.token + slice.phase) / P - slice.first;  // the token's unit
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+              for (int i = 0; i < P / 2; ++i) e[k][i] = __fmul2_rn(e[k][i], by);
+              if (!DISTILL && own == k * kThreads + t) {
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                  element(e[k], i) -= i == (side.token + slice.phase) % P ? slope : 0.0f;
+              }
+              put_unit(a, slice, g_row, even, k * kThreads + t, e[k]);
+            }
+            if constexpr (DISTILL) {
+              workers_sync();  // the units are written: now the teacher's tokens, once more
+              const int32_t lo = slice.begin(), hi = slice.end(a);
+              for (int j = t; j < a.top; j += kThreads)
+                if (ids[j] >= lo && ids[j] < hi && !(gq[j] < 0.0f))
+                  store_any(g_row, ids[j], a.g_bf16 != 0, part * below(zt[j], M, a.scale) - slope * gq[j]);
+            }
+          } else {
+            float2 zero[P / 2];
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) zero[i] = both(0.0f);
+#pragma unroll
+            for (int k = 0; k < K; ++k) put_unit(a, slice, g_row, even, k * kThreads + t, zero);
+          }
+        }
+      }
+      if constexpr (MODE == GRADIENT) {
+        const bool none = weight == 0.0f || side.mass == 0.0f;
+        const float slope = side.slope, lse = none ? 0.0f : side.lse;
+        const float2 less = both(-lse), by = both(a.inv_t);
+        const int32_t own = DISTILL || none ? -1 : (side.token + slice.phase) / P - slice.first;
+#pragma unroll 4
+        for (int k = 0; k < K; ++k) {
+          const int u = k * kThreads + t;
+          float2 v[P / 2];
+          if (none) {
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) v[i] = both(0.0f);
+          } else {
+            unit_of(a, stage, slice, u, v);
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) {
+              const float2 x = __fmul2_rn(__ffma2_rn(v[i], by, less), both(kLog2E));
+              v[i] = __fmul2_rn(make_float2(ex2(x.x), ex2(x.y)), both(slope));
+            }
+            if (!DISTILL && own == u) {
+#pragma unroll
+              for (int i = 0; i < P; ++i)
+                element(v, i) -= i == (side.token + slice.phase) % P ? slope : 0.0f;
+            }
+          }
+          put_unit(a, slice, g_row, even, u, v);
+        }
+        if (DISTILL && !none) {
+          workers_sync();
+          const int32_t lo = slice.begin(), hi = slice.end(a);
+          for (int j = t; j < a.top; j += kThreads)
+            if (ids[j] >= lo && ids[j] < hi && !(gq[j] < 0.0f))
+              store_any(g_row, ids[j], a.g_bf16 != 0, slope * (ex2(fmaf(zt[j], a.inv_t, -lse) * kLog2E) - gq[j]));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(tc::smem(&sh.empty[stage_at]));
+      if (++stage_at == a.stages) stage_at = 0, parity ^= 1u;
+    }
+  }
+}
+
+template <bool DISTILL, class T, int K, Mode MODE>
+__global__ void __launch_bounds__(kThreads + 32, MODE != GRADIENT && K == kMostUnits ? 2 : 3) row_kernel(const __grid_constant__ Args a) {
+  extern __shared__ __align__(128) uint8_t stages[];
+  __shared__ Shared sh;
+  if (threadIdx.x == 0) {
+    sh.stop = 0;
+    for (int i = 0; i < kMaxStages; ++i) tc::bar_init(tc::smem(&sh.full[i]), 2), tc::bar_init(tc::smem(&sh.empty[i]), kWarps);
+    for (int i = 0; i < 2; ++i) tc::bar_init(tc::smem(&sh.arrived[i]), a.cluster);
+    tc::bar_init_fence();
+  }
+  for (int i = threadIdx.x; i < (int)(sizeof(sh.named) / 4); i += kThreads + 32) sh.named[i] = 0;
+  wait_for_previous();
+  let_next_start();
+  if (a.cluster > 1)
+    tc::cluster_sync();
+  else
+    __syncthreads();
+  const uint32_t rank = a.cluster > 1 ? tc::cluster_rank() : 0;
+  const int64_t first = blockIdx.x / a.cluster, step = gridDim.x / a.cluster;
+  if (threadIdx.x >= kThreads)
+    feed<DISTILL, T, MODE>(a, sh, stages, rank, first, step);
+  else
+    work<DISTILL, T, K, MODE>(a, sh, stages, rank, first, step);
+  __syncthreads();
+  if (threadIdx.x == 0 && *(volatile uint32_t *)&sh.stop) {
+    atomicAdd(a.gave_up, 1u);
+    // What is still on its way must arrive before the block's memory is another's: for the limit, at most.
+    const uint64_t began = tc::now_ns();
+    while (tc::now_ns() - began < 1000000u) {
+    }
+  }
+  if (a.cluster > 1) tc::cluster_sync();  // no block leaves while another may write to it
+}
+
+// ---- host --------------------------------------------------------------------------------
+template <class K>
+const void *kernel(K *k) {
+  return reinterpret_cast<const void *>(k);
+}
+
+// Blocks of a launch that the device holds at once, in whole clusters.
+cudaError_t resident(const void *fn, int cluster, int smem, int *clusters) {
+  struct Known {
+    const void *fn;
+    int device, cluster, smem, clusters;
+  };
+  static std::mutex lock;
+  static Known known[64];
+  static int n = 0, oldest = 0;
+  int device = -1;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> hold(lock);
+    for (int i = 0; i < n; ++i)
+      if (known[i].fn == fn && known[i].device == device && known[i].cluster == cluster && known[i].smem == smem) {
+        *clusters = known[i].clusters;
+        return cudaSuccess;
+      }
+  }
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);  // one value: the last one set holds
+  if (e != cudaSuccess) return e;
+  int most = 0;
+  if (cluster > 1) {
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)cluster, at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(cluster * 1024)), cfg.blockDim = dim3(kThreads + 32);
+    cfg.dynamicSmemBytes = (size_t)smem, cfg.attrs = &at, cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&most, fn, &cfg);
+  } else {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&most, fn, kThreads + 32, (size_t)smem);
+    most *= device_sms();
+  }
+  if (e != cudaSuccess) return e;
+  if (most < 1) return cudaErrorInvalidConfiguration;
+  std::lock_guard<std::mutex> hold(lock);
+  Known &k = n < 64 ? known[n++] : known[oldest++ & 63];
+  k = {fn, device, cluster, smem, most};
+  *clusters = most;
+  return cudaSuccess;
+}
+
+template <bool DISTILL, class T, Mode MODE>
+cudaError_t launch_rows(Args &a, cudaStream_t s) {
+  constexpr int P = Slice<T>::kPer, kMost = kThreads * kMostUnits;
+  const int64_t row_units = (a.vocab + P - 1) / P + ((uintptr_t)a.logits % 16 != 0 || (a.rows > 1 && a.ld_z % P != 0) ? 1 : 0);
+  const int64_t busy = 2 * device_sms();
+  a.cluster = a.rounds = a.slices = 1;
+  if (MODE == GRADIENT) {
+    a.slices = (int32_t)((row_units + kMost - 1) / kMost);
+  } else {
+    // As many blocks to a row as it needs, or as keep the SMs busy, with 256 units each at least.
+    const int64_t need = MODE == BOTH ? (row_units + kMost - 1) / kMost : 1;
+    const int64_t want = std::min<int64_t>((busy + a.rows - 1) / a.rows, row_units / kThreads);
+    a.cluster = (int32_t)std::min<int64_t>(kMaxCluster, std::max(need, want));
+    a.rounds = (int32_t)((row_units + (int64_t)kMost * a.cluster - 1) / ((int64_t)kMost * a.cluster));
+  }
+  const int64_t parts = (int64_t)a.cluster * a.rounds * a.slices;
+  a.units = (int32_t)((row_units + parts - 1) / parts);
+  a.items = a.rows * a.slices;
+  const bool small = a.units <= 2 * kThreads;
+  const void *fn = small ? kernel(&row_kernel<DISTILL, T, 2, MODE>) : kernel(&row_kernel<DISTILL, T, kMostUnits, MODE>);
+  a.stage_bytes = (a.units * 16 + 127) / 128 * 128;
+  a.side_bytes = ((int)sizeof(Side) + (DISTILL ? a.top * 16 : 0) + 127) / 128 * 128;
+  a.stages = small ? 4 : 2;
+  const int smem = a.stages * (a.stage_bytes + a.side_bytes);
+  int clusters = 0;
+  cudaError_t e = resident(fn, a.cluster, smem, &clusters);
+  if (e != cudaSuccess) return e;
+  e = gave_up_count(GAVE_UP_LOSS, &a.gave_up);
+  if (e != cudaSuccess) return e;
+  a.wait_limit_ns = wait_limit_ns(), a.fault = wait_fault();
+  const int64_t grid = std::min<int64_t>(a.items, clusters) * a.cluster;
+  void *args[] = {&a};
+  return launch_kernel(fn, dim3((unsigned)grid), dim3(kThreads + 32), args, (size_t)smem, s, true, a.cluster);
+}
+
+template <bool DISTILL, class T>
+cudaError_t launch_as(Args &a, cudaStream_t s) {
+  constexpr int64_t kHeld = (int64_t)kMaxCluster * kThreads * kMostUnits * Slice<T>::kPer;  // elements that a cluster holds, and
+  const int64_t held = kHeld - Slice<T>::kPer;                                             // a row that begins inside a unit
+  if (a.backward) return launch_rows<DISTILL, T, GRADIENT>(a, s);
+  if (!a.dlogits) return launch_rows<DISTILL, T, STATS>(a, s);
+  const bool whole = (uintptr_t)a.logits % 16 == 0 && (a.rows == 1 || a.ld_z % Slice<T>::kPer == 0);
+  if (a.vocab <= (whole ? kHeld : held)) return launch_rows<DISTILL, T, BOTH>(a, s);
+  cudaError_t e = launch_rows<DISTILL, T, STATS>(a, s);
+  if (e != cudaSuccess) return e;
+  a.lse_in = a.lse, a.logp_in = a.logp, a.dloss = nullptr;
+  return launch_rows<DISTILL, T, GRADIENT>(a, s);
 }
 
 template <bool DISTILL>
 fsdp_status_t run(Args &a, cudaStream_t s) {
-  void *args[] = {&a};
-  const int64_t grid = std::min<int64_t>(a.rows, 1 << 20);
-  return launched(launch_kernel(reinterpret_cast<const void *>(&row_kernel<DISTILL>), dim3((unsigned)grid), dim3(kThreads), args, 0, s));
+  a.scale = a.inv_t * kLog2E;
+  return launched(a.z_bf16 ? launch_as<DISTILL, __nv_bfloat16>(a, s) : launch_as<DISTILL, float>(a, s));
 }
 
 fsdp_status_t check_rows(const float *p, int64_t rows, bool needed, const char *what) {
