@@ -2,12 +2,15 @@
 //
 // Everything is bound by the logits' bytes: read once for a loss, read once and written once for a gradient
 // or both.  A row is cut into slices of whole 16-byte units; a block reads a slice with one TMA bulk copy
-// into a ring of shared-memory stages, the next one on its way while it works.  For a loss with its gradient
-// a cluster of blocks holds the whole row: each thread keeps its elements' exponentials (relative to its own
-// maximum) in registers, the blocks' maxima and sums meet in distributed shared memory, and the gradient is
-// a product per element, without a second read or exponential.  For a loss alone a block or cluster walks
-// over a row's slices; the gradient alone (given lse) treats slices one by one.  Rows that no
-// cluster holds (above 131,072 BF16 or 65,536 FP32 logits) take these two in turn.
+// into a ring of shared-memory stages, the next one on its way while it works.
+//
+//   STATS     a loss alone: a block walks over a row's slices, or with few rows a cluster shares them and its
+//             sums meet in distributed shared memory.
+//   HELD      a loss with its gradient, of rows of one slice: each thread keeps its elements'
+//             exponentials (relative to its own maximum) in registers, and the gradient is a product per element.
+//   TWICE     the same of longer rows: a block reads its row twice, the second time from L2, which holds
+//             the rows of all blocks (304 of 256 KB at 131,072 BF16 logits).
+//   GRADIENT  the gradient alone, from lse: slices one by one.
 //
 // A ninth warp fills the ring and prepares what a row has beside its logits: the policy's scalars,
 // or the softmax of the teacher's entries, while the others are at the row before.
@@ -31,9 +34,10 @@ constexpr int kThreads = 256, kWarps = kThreads / 32, kMaxTop = FSDP_DISTILL_MAX
 constexpr int kMaxCluster = 8, kMaxStages = 4;
 constexpr int kMostUnits = 8;  // 16-byte units of a slice that a thread has
 constexpr int kMostSmem = 104 * 1024;  // stages, and what goes with a row: 2 x (32 + 16.1) or 4 x (8 + 16.1) KB at most
+constexpr int kNamed = 32768;
 constexpr float kLog2E = 1.4426950408889634f;
 
-enum Mode { STATS, BOTH, GRADIENT };
+enum Mode { STATS, HELD, TWICE, GRADIENT };
 
 struct Args {
   const void *logits;
@@ -69,7 +73,7 @@ struct alignas(16) Shared {
   float4 warp[2][kWarps];        // maximum and sum of a warp, and what it has of the targets
   float4 block[2][kMaxCluster];  // the same of the cluster's blocks
   uint64_t arrived[2], full[kMaxStages], empty[kMaxStages];
-  uint32_t named[kThreads * kMostUnits * 8 / 32];  // the slice's elements that the teacher has named
+  uint32_t named[kNamed / 32];   // tokens that the teacher has named, by their last bits
   uint32_t stop;
 };
 
@@ -135,7 +139,7 @@ __device__ __forceinline__ void policy_of(const Args &a, float logp, const Side 
 
 // ---- the ninth warp ------------------------------------------------------------------------
 template <class T>
-__device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side, int64_t row, const Slice<T> &slice, bool gradient) {
+__device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side, int64_t row, int32_t lo, int32_t hi, bool gradient) {
   const int lane = threadIdx.x & 31;
   int32_t *ids = reinterpret_cast<int32_t *>(&side + 1);
   float *q = reinterpret_cast<float *>(ids + a.top), *gq = q + a.top, *v = gq + a.top;
@@ -164,15 +168,15 @@ __device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side
   const bool some = sum > 0.0f || sum != sum || nan;
   const float inv = some ? 1.0f / sum : 0.0f, log_sum = logf(sum);
   float total = 0.0f;
-  const int32_t lo = slice.begin(), hi = slice.end(a);
   bool twice = false;
   for (int j = lane; j < a.top; j += 32) {
     const float p = q[j] * inv;
     q[j] = gq[j] = p;
     if (p > 0.0f || p != p) total += p * (v[j] - top - log_sum);
+    v[j] = 0.0f;
     if (gradient && ids[j] >= lo && ids[j] < hi) {
-      const uint32_t bit = 1u << ((ids[j] - lo) & 31);
-      twice |= (atomicOr(&sh.named[(ids[j] - lo) / 32], bit) & bit) != 0;
+      const uint32_t bit = 1u << (ids[j] & 31);
+      if (atomicOr(&sh.named[ids[j] % kNamed / 32], bit) & bit) twice = true, v[j] = 1.0f;
     }
   }
 #pragma unroll
@@ -180,23 +184,31 @@ __device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side
   if (gradient) {
     __syncwarp();
     for (int j = lane; j < a.top; j += 32)
-      if (ids[j] >= lo && ids[j] < hi) sh.named[(ids[j] - lo) / 32] = 0;
+      if (ids[j] >= lo && ids[j] < hi) sh.named[ids[j] % kNamed / 32] = 0;
     if (__any_sync(0xFFFFFFFFu, twice)) {
-      // A token is named more than once: its first entry takes what the others have, in their order.
-      for (int j = 0; j < a.top; ++j) {
-        if (ids[j] < lo || ids[j] >= hi || gq[j] < 0.0f) continue;
-        float s = gq[j];
-        for (int k0 = j + 1; k0 < a.top; k0 += 32) {
-          const int k = k0 + lane;
-          const bool same = k < a.top && ids[k] == ids[j];
-          const float other = same ? q[k] : 0.0f;
-          uint32_t which = __ballot_sync(0xFFFFFFFFu, same);
-          if (same) gq[k] = -1.0f;
-          for (; which; which &= which - 1) s += __shfl_sync(0xFFFFFFFFu, other, __ffs(which) - 1);
+      // Tokens that are named more than once (v is 1 at all but one of a token's entries, and where tokens differ by
+      // multiples of kNamed): the first entry takes what the others have, in their order.
+      for (int j0 = 0; j0 < a.top; j0 += 32) {
+        const int j = j0 + lane;
+        uint32_t which = __ballot_sync(0xFFFFFFFFu, j < a.top && v[j] == 1.0f);
+        for (; which; which &= which - 1) {
+          const int at = j0 + __ffs(which) - 1, id = ids[at];
+          if (v[at] != 1.0f) continue;  // its token has been joined
+          int first = -1;
+          float s = 0.0f;
+          for (int k0 = 0; k0 < a.top; k0 += 32) {
+            const int k = k0 + lane;
+            const bool same = k < a.top && ids[k] == id;
+            const float other = same ? q[k] : 0.0f;
+            uint32_t more = __ballot_sync(0xFFFFFFFFu, same);
+            if (more && first < 0) first = k0 + __ffs(more) - 1;
+            for (; more; more &= more - 1) s += __shfl_sync(0xFFFFFFFFu, other, __ffs(more) - 1);
+            if (same) gq[k] = -1.0f, v[k] = 0.0f;
+          }
+          __syncwarp();
+          if (lane == 0) gq[first] = s;
+          __syncwarp();
         }
-        __syncwarp();
-        if (lane == 0) gq[j] = s;
-        __syncwarp();
       }
     }
   }
@@ -218,7 +230,8 @@ __device__ __forceinline__ void feed(const Args &a, Shared &sh, uint8_t *stages,
     const int64_t row = MODE == GRADIENT ? item / a.slices : item;
     const float weight = ahead;
     ahead = weight_of(item + step);
-    for (int round = 0; round < a.rounds; ++round) {
+    for (int turn = 0; turn < (MODE == TWICE ? 2 * a.rounds : a.rounds); ++turn) {
+      const int round = MODE == TWICE && turn >= a.rounds ? turn - a.rounds : turn;
       const Slice<T> slice(a, row, MODE == GRADIENT ? (int32_t)(item - row * a.slices) : (int32_t)rank * a.rounds + round);
       const uint32_t full = tc::smem(&sh.full[stage]);
       tc::bar_wait(tc::smem(&sh.empty[stage]), parity, a.wait_limit_ns, &sh.stop);
@@ -234,7 +247,7 @@ __device__ __forceinline__ void feed(const Args &a, Shared &sh, uint8_t *stages,
         }
         skip = false;
       }
-      if (round == 0) {
+      if (turn == 0) {
         Side &side = *reinterpret_cast<Side *>(stages + a.stages * a.stage_bytes + side_at * a.side_bytes);
         float slope = 0.0f;
         const float dloss = MODE == GRADIENT && a.dloss && weight != 0.0f ? a.dloss[row] : 1.0f, up = weight * dloss;
@@ -244,7 +257,7 @@ __device__ __forceinline__ void feed(const Args &a, Shared &sh, uint8_t *stages,
         }
         if (weight != 0.0f) {
           if constexpr (DISTILL) {
-            teacher_of<T>(a, sh, side, row, slice, MODE != STATS);
+            teacher_of<T>(a, sh, side, row, MODE == GRADIENT ? slice.begin() : 0, MODE == GRADIENT ? slice.end(a) : a.vocab, MODE != STATS);
             slope = up * a.t;
           } else if (lane == 0) {
             side.old = a.old_logp ? a.old_logp[row] : 0.0f;
@@ -322,12 +335,62 @@ __device__ __forceinline__ void put_unit(const Args &a, const Slice<T> &s, void 
   }
 }
 
+// What a row's gradient is made of: part 2^((z by + less) scale) - slope q.
+struct Gradient {
+  float by, less, scale, part, slope;
+  bool none;
+  __device__ __forceinline__ float of(float z) const { return part * ex2(fmaf(z, by, less) * scale); }
+};
+
+// A slice's gradient from its logits.
+template <bool DISTILL, class T, int K>
+__device__ __forceinline__ void write_slice(const Args &a, const Slice<T> &slice, const uint8_t *stage, void *g_row, bool even, int32_t token,
+                                            const Gradient &g) {
+  constexpr int P = Slice<T>::kPer;
+  const int32_t own = DISTILL || g.none ? -1 : (token + slice.phase) / P - slice.first;
+#pragma unroll 4
+  for (int k = 0; k < K; ++k) {
+    const int u = k * kThreads + threadIdx.x;
+    float2 v[P / 2];
+    if (g.none) {
+#pragma unroll
+      for (int i = 0; i < P / 2; ++i) v[i] = both(0.0f);
+    } else {
+      unit_of(a, stage, slice, u, v);
+#pragma unroll
+      for (int i = 0; i < P / 2; ++i) {
+        const float2 x = __fmul2_rn(__ffma2_rn(v[i], both(g.by), both(g.less)), both(g.scale));
+        v[i] = __fmul2_rn(make_float2(ex2(x.x), ex2(x.y)), both(g.part));
+      }
+      if (!DISTILL && own == u) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) element(v, i) -= i == (token + slice.phase) % P ? g.slope : 0.0f;
+      }
+    }
+    put_unit(a, slice, g_row, even, u, v);
+  }
+}
+// Once a slice's units are written: the teacher's tokens in it, once more.
+template <class T>
+__device__ __forceinline__ void write_named(const Args &a, const Slice<T> &slice, void *g_row, const int32_t *ids, const float *gq,
+                                            const float *zt, const Gradient &g) {
+  workers_sync();
+  const int32_t lo = slice.begin(), hi = slice.end(a);
+  for (int j = threadIdx.x; j < a.top; j += kThreads)
+    if (ids[j] >= lo && ids[j] < hi && !(gq[j] < 0.0f)) store_any(g_row, ids[j], a.g_bf16 != 0, g.of(zt[j]) - g.slope * gq[j]);
+}
+
 template <bool DISTILL, class T, int K, Mode MODE>
 __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages, uint32_t rank, int64_t first, int64_t step) {
   constexpr int P = Slice<T>::kPer;
   const int t = threadIdx.x, lane = t & 31, warp = t / 32;
   int stage_at = 0, side_at = 0, turn = 0;
   uint32_t parity = 0;
+  auto next = [&] {  // the stage has been read
+    __syncwarp();
+    if (lane == 0) tc::bar_arrive(tc::smem(&sh.empty[stage_at]));
+    if (++stage_at == a.stages) stage_at = 0, parity ^= 1u;
+  };
   for (int64_t item = first; item < a.items; item += step) {
     const int64_t row = MODE == GRADIENT ? item / a.slices : item;
     Side &side = *reinterpret_cast<Side *>(stages + a.stages * a.stage_bytes + side_at * a.side_bytes);
@@ -335,15 +398,17 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
     const float *q = reinterpret_cast<const float *>(ids + a.top), *gq = q + a.top;
     float *zt = const_cast<float *>(gq) + a.top;
     if (++side_at == a.stages) side_at = 0;
-    uint8_t *g_row = static_cast<uint8_t *>(a.dlogits) + row * a.ld_g * (a.g_bf16 ? 2 : 4);
+    const int g_size = a.g_bf16 ? 2 : 4;
+    uint8_t *g_row = static_cast<uint8_t *>(a.dlogits) + row * a.ld_g * g_size;
+    auto even = [&](const Slice<T> &s) { return ((uintptr_t)g_row - s.phase * g_size) % (a.g_bf16 ? P * 2 : 16) == 0; };
     float m = -INFINITY, sum = 0.0f, hit = 0.0f;  // of the thread, over the block's slices; what it has of the targets
+    float weight = 0.0f;
+    float2 e[MODE == GRADIENT ? 1 : K][P / 2];
     for (int round = 0; round < a.rounds; ++round) {
       const Slice<T> slice(a, row, MODE == GRADIENT ? (int32_t)(item - row * a.slices) : (int32_t)rank * a.rounds + round);
       const uint8_t *stage = stages + stage_at * a.stage_bytes;
-      const bool even = ((uintptr_t)g_row - slice.phase * (a.g_bf16 ? 2 : 4)) % (a.g_bf16 ? P * 2 : 16) == 0;
       tc::bar_wait(tc::smem(&sh.full[stage_at]), parity, a.wait_limit_ns, &sh.stop);
-      const float weight = side.weight;
-      float2 e[MODE == GRADIENT ? 1 : K][P / 2];
+      weight = side.weight;
       if (weight != 0.0f) {
         // The targets' logits.
         if constexpr (DISTILL) {
@@ -375,136 +440,104 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
               e[k][i] = make_float2(ex2(x.x), ex2(x.y));
               s = __fadd2_rn(s, e[k][i]);
             }
-          if constexpr (MODE == BOTH)
+          if constexpr (MODE == HELD)
             m = top, sum = s.x + s.y;
           else
             merge(m, sum, top, s.x + s.y, a.scale);
         }
       }
-      if (MODE != GRADIENT && round == a.rounds - 1) {
-        const int slot = turn & 1;
-        float M = m, S = sum, X = hit;
-        if (weight != 0.0f) {
-#pragma unroll
-          for (int d = 16; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
-          S = sum * below(m, M, a.scale);
-#pragma unroll
-          for (int d = 16; d > 0; d /= 2) S += __shfl_xor_sync(0xFFFFFFFFu, S, d), X += __shfl_xor_sync(0xFFFFFFFFu, X, d);
-          if (lane == 0) sh.warp[slot][warp] = make_float4(M, S, X, 0.0f);
-          workers_sync();
-          auto join = [&](const float4 *p, int n) {
-            float4 v = p[0];
-            M = v.x, S = v.y, X = v.z;
-            for (int w = 1; w < n; ++w) {
-              v = p[w];
-              merge(M, S, v.x, v.y, a.scale);
-              X += v.z;
-            }
-          };
-          if (a.cluster > 1) {
-            const uint32_t bar = tc::smem(&sh.arrived[slot]);
-            if (t < a.cluster) {
-              join(sh.warp[slot], kWarps);
-              asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(tc::at_rank(tc::smem(&sh.block[slot][rank]), t)), "f"(M),
-                           "f"(S), "f"(X), "f"(0.0f)
-                           : "memory");
-              tc::bar_arrive_cluster(tc::at_rank(bar, t));
-            }
-            tc::bar_wait(bar, (uint32_t)(turn >> 1) & 1u, a.wait_limit_ns, &sh.stop);
-            join(sh.block[slot], a.cluster);
-          } else {
-            join(sh.warp[slot], kWarps);
-          }
-          ++turn;
-        }
-        float loss = 0.0f, logp = 0.0f, lse = 0.0f, slope = 0.0f;
-        if (weight != 0.0f) {
-          const float log_sum = logf(S);
-          lse = fmaf(M, a.inv_t, log_sum);
-          if constexpr (DISTILL) {
-            if (side.mass != 0.0f) loss = weight * a.t * a.t * (side.q_log_q + lse - a.inv_t * X);
-            slope = side.slope;
-          } else if (side.token >= 0) {
-            logp = fmaf(X - M, a.inv_t, -log_sum);
-            policy_of(a, logp, side, loss, slope);
-            loss *= weight;
-            slope *= -side.up * a.inv_t;
-          }
-        }
-        if (t == 0 && rank == 0) {
-          a.loss[row] = loss, a.lse[row] = lse;
-          if (!DISTILL) a.logp[row] = logp;
-        }
-        if constexpr (MODE == BOTH) {
-          if (weight != 0.0f && side.mass != 0.0f) {
-            const float part = slope / S;
-            const float2 by = both(part * below(m, M, a.scale));
-            const int32_t own = DISTILL ? -1 : (side.token + slice.phase) / P - slice.first;  // the token's unit
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-#pragma unroll
-              for (int i = 0; i < P / 2; ++i) e[k][i] = __fmul2_rn(e[k][i], by);
-              if (!DISTILL && own == k * kThreads + t) {
-#pragma unroll
-                for (int i = 0; i < P; ++i)
-                  element(e[k], i) -= i == (side.token + slice.phase) % P ? slope : 0.0f;
-              }
-              put_unit(a, slice, g_row, even, k * kThreads + t, e[k]);
-            }
-            if constexpr (DISTILL) {
-              workers_sync();  // the units are written: now the teacher's tokens, once more
-              const int32_t lo = slice.begin(), hi = slice.end(a);
-              for (int j = t; j < a.top; j += kThreads)
-                if (ids[j] >= lo && ids[j] < hi && !(gq[j] < 0.0f))
-                  store_any(g_row, ids[j], a.g_bf16 != 0, part * below(zt[j], M, a.scale) - slope * gq[j]);
-            }
-          } else {
-            float2 zero[P / 2];
-#pragma unroll
-            for (int i = 0; i < P / 2; ++i) zero[i] = both(0.0f);
-#pragma unroll
-            for (int k = 0; k < K; ++k) put_unit(a, slice, g_row, even, k * kThreads + t, zero);
-          }
-        }
-      }
       if constexpr (MODE == GRADIENT) {
-        const bool none = weight == 0.0f || side.mass == 0.0f;
-        const float slope = side.slope, lse = none ? 0.0f : side.lse;
-        const float2 less = both(-lse), by = both(a.inv_t);
-        const int32_t own = DISTILL || none ? -1 : (side.token + slice.phase) / P - slice.first;
-#pragma unroll 4
-        for (int k = 0; k < K; ++k) {
-          const int u = k * kThreads + t;
-          float2 v[P / 2];
-          if (none) {
-#pragma unroll
-            for (int i = 0; i < P / 2; ++i) v[i] = both(0.0f);
-          } else {
-            unit_of(a, stage, slice, u, v);
-#pragma unroll
-            for (int i = 0; i < P / 2; ++i) {
-              const float2 x = __fmul2_rn(__ffma2_rn(v[i], by, less), both(kLog2E));
-              v[i] = __fmul2_rn(make_float2(ex2(x.x), ex2(x.y)), both(slope));
-            }
-            if (!DISTILL && own == u) {
-#pragma unroll
-              for (int i = 0; i < P; ++i)
-                element(v, i) -= i == (side.token + slice.phase) % P ? slope : 0.0f;
-            }
-          }
-          put_unit(a, slice, g_row, even, u, v);
-        }
-        if (DISTILL && !none) {
-          workers_sync();
-          const int32_t lo = slice.begin(), hi = slice.end(a);
-          for (int j = t; j < a.top; j += kThreads)
-            if (ids[j] >= lo && ids[j] < hi && !(gq[j] < 0.0f))
-              store_any(g_row, ids[j], a.g_bf16 != 0, slope * (ex2(fmaf(zt[j], a.inv_t, -lse) * kLog2E) - gq[j]));
-        }
+        Gradient g = {a.inv_t, -side.lse, kLog2E, side.slope, side.slope, weight == 0.0f || side.mass == 0.0f};
+        write_slice<DISTILL, T, K>(a, slice, stage, g_row, even(slice), side.token, g);
+        if (DISTILL && !g.none) write_named(a, slice, g_row, ids, gq, zt, g);
       }
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(tc::smem(&sh.empty[stage_at]));
-      if (++stage_at == a.stages) stage_at = 0, parity ^= 1u;
+      if (MODE != HELD) next();
+    }
+    if constexpr (MODE == GRADIENT) continue;
+    // The row's maximum and sum.
+    float M = m, S = sum, X = hit;
+    if (weight != 0.0f) {
+      const int slot = turn & 1;
+#pragma unroll
+      for (int d = 16; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+      S = sum * below(m, M, a.scale);
+#pragma unroll
+      for (int d = 16; d > 0; d /= 2) S += __shfl_xor_sync(0xFFFFFFFFu, S, d), X += __shfl_xor_sync(0xFFFFFFFFu, X, d);
+      if (lane == 0) sh.warp[slot][warp] = make_float4(M, S, X, 0.0f);
+      workers_sync();
+      auto join = [&](const float4 *p, int n) {
+        float4 v = p[0];
+        M = v.x, S = v.y, X = v.z;
+        for (int w = 1; w < n; ++w) {
+          v = p[w];
+          merge(M, S, v.x, v.y, a.scale);
+          X += v.z;
+        }
+      };
+      if (MODE == STATS && a.cluster > 1) {
+        const uint32_t bar = tc::smem(&sh.arrived[slot]);
+        if (t < a.cluster) {
+          join(sh.warp[slot], kWarps);
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(tc::at_rank(tc::smem(&sh.block[slot][rank]), t)), "f"(M),
+                       "f"(S), "f"(X), "f"(0.0f)
+                       : "memory");
+          tc::bar_arrive_cluster(tc::at_rank(bar, t));
+        }
+        tc::bar_wait(bar, (uint32_t)(turn >> 1) & 1u, a.wait_limit_ns, &sh.stop);
+        join(sh.block[slot], a.cluster);
+      } else {
+        join(sh.warp[slot], kWarps);
+      }
+      ++turn;
+    }
+    float loss = 0.0f, logp = 0.0f, lse = 0.0f, slope = 0.0f;
+    if (weight != 0.0f) {
+      const float log_sum = logf(S);
+      lse = fmaf(M, a.inv_t, log_sum);
+      if constexpr (DISTILL) {
+        if (side.mass != 0.0f) loss = weight * a.t * a.t * (side.q_log_q + lse - a.inv_t * X);
+        slope = side.slope;
+      } else if (side.token >= 0) {
+        logp = fmaf(X - M, a.inv_t, -log_sum);
+        policy_of(a, logp, side, loss, slope);
+        loss *= weight;
+        slope *= -side.up * a.inv_t;
+      }
+    }
+    if (t == 0 && rank == 0) {
+      a.loss[row] = loss, a.lse[row] = lse;
+      if (!DISTILL) a.logp[row] = logp;
+    }
+    if constexpr (MODE == STATS) continue;
+    const Gradient g = {1.0f, -M, a.scale, slope / S, slope, weight == 0.0f || side.mass == 0.0f};
+    if constexpr (MODE == HELD) {
+      const Slice<T> slice(a, row, 0);
+      if (g.none) {
+        write_slice<DISTILL, T, K>(a, slice, stages, g_row, even(slice), 0, g);
+      } else {
+        const float2 by = both(g.part * below(m, M, a.scale));
+        const int32_t own = DISTILL ? -1 : (side.token + slice.phase) / P;  // the token's unit
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+          for (int i = 0; i < P / 2; ++i) e[k][i] = __fmul2_rn(e[k][i], by);
+          if (!DISTILL && own == k * kThreads + t) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) element(e[k], i) -= i == (side.token + slice.phase) % P ? slope : 0.0f;
+          }
+          put_unit(a, slice, g_row, even(slice), k * kThreads + t, e[k]);
+        }
+        if (DISTILL) write_named(a, slice, g_row, ids, gq, zt, g);
+      }
+      next();
+    } else {
+      for (int round = 0; round < a.rounds; ++round) {
+        const Slice<T> slice(a, row, round);
+        tc::bar_wait(tc::smem(&sh.full[stage_at]), parity, a.wait_limit_ns, &sh.stop);
+        write_slice<DISTILL, T, K>(a, slice, stages + stage_at * a.stage_bytes, g_row, even(slice), side.token, g);
+        if (DISTILL && !g.none) write_named(a, slice, g_row, ids, gq, zt, g);
+        next();
+      }
     }
   }
 }
@@ -593,20 +626,27 @@ cudaError_t resident(const void *fn, int cluster, int smem, int *clusters) {
   return cudaSuccess;
 }
 
+// Units of the longest row, which may begin anywhere in its first.
+template <class T>
+int64_t units_of(const Args &a) {
+  constexpr int P = Slice<T>::kPer;
+  return (a.vocab + P - 1) / P + ((uintptr_t)a.logits % 16 != 0 || (a.rows > 1 && a.ld_z % P != 0) ? 1 : 0);
+}
+
 template <bool DISTILL, class T, Mode MODE>
 cudaError_t launch_rows(Args &a, cudaStream_t s) {
-  constexpr int P = Slice<T>::kPer, kMost = kThreads * kMostUnits;
-  const int64_t row_units = (a.vocab + P - 1) / P + ((uintptr_t)a.logits % 16 != 0 || (a.rows > 1 && a.ld_z % P != 0) ? 1 : 0);
-  const int64_t busy = 2 * device_sms();
+  constexpr int64_t kMost = kThreads * kMostUnits;
+  const int64_t row_units = units_of<T>(a);
   a.cluster = a.rounds = a.slices = 1;
   if (MODE == GRADIENT) {
     a.slices = (int32_t)((row_units + kMost - 1) / kMost);
-  } else {
-    // As many blocks to a row as it needs, or as keep the SMs busy, with 256 units each at least.
-    const int64_t need = MODE == BOTH ? (row_units + kMost - 1) / kMost : 1;
-    const int64_t want = std::min<int64_t>((busy + a.rows - 1) / a.rows, row_units / kThreads);
-    a.cluster = (int32_t)std::min<int64_t>(kMaxCluster, std::max(need, want));
-    a.rounds = (int32_t)((row_units + (int64_t)kMost * a.cluster - 1) / ((int64_t)kMost * a.cluster));
+  } else if (MODE != HELD) {
+    // A loss alone of few rows: as many blocks to a row as keep the SMs busy, with 256 units each at least.
+    if (MODE == STATS) {
+      const int64_t want = std::min<int64_t>((2 * device_sms() + a.rows - 1) / a.rows, row_units / kThreads);
+      a.cluster = (int32_t)std::min<int64_t>(kMaxCluster, std::max<int64_t>(1, want));
+    }
+    a.rounds = (int32_t)((row_units + kMost * a.cluster - 1) / (kMost * a.cluster));
   }
   const int64_t parts = (int64_t)a.cluster * a.rounds * a.slices;
   a.units = (int32_t)((row_units + parts - 1) / parts);
@@ -630,12 +670,11 @@ cudaError_t launch_rows(Args &a, cudaStream_t s) {
 
 template <bool DISTILL, class T>
 cudaError_t launch_as(Args &a, cudaStream_t s) {
-  constexpr int64_t kHeld = (int64_t)kMaxCluster * kThreads * kMostUnits * Slice<T>::kPer;  // elements that a cluster holds, and
-  const int64_t held = kHeld - Slice<T>::kPer;                                             // a row that begins inside a unit
   if (a.backward) return launch_rows<DISTILL, T, GRADIENT>(a, s);
   if (!a.dlogits) return launch_rows<DISTILL, T, STATS>(a, s);
-  const bool whole = (uintptr_t)a.logits % 16 == 0 && (a.rows == 1 || a.ld_z % Slice<T>::kPer == 0);
-  if (a.vocab <= (whole ? kHeld : held)) return launch_rows<DISTILL, T, BOTH>(a, s);
+  if (units_of<T>(a) <= kThreads * kMostUnits) return launch_rows<DISTILL, T, HELD>(a, s);
+  // Fewer rows than SMs: two launches that share rows out.
+  if (a.rows >= device_sms()) return launch_rows<DISTILL, T, TWICE>(a, s);
   cudaError_t e = launch_rows<DISTILL, T, STATS>(a, s);
   if (e != cudaSuccess) return e;
   a.lse_in = a.lse, a.logp_in = a.logp, a.dloss = nullptr;
