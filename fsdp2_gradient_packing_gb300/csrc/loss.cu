@@ -8,8 +8,8 @@
 //             sums meet in distributed shared memory.
 //   HELD      a loss with its gradient, of rows of one slice: each thread keeps its elements'
 //             exponentials (relative to its own maximum) in registers, and the gradient is a product per element.
-//   TWICE     the same of longer rows: a block reads its row twice, the second time from L2, which holds
-//             the rows of all blocks (304 of 256 KB at 131,072 BF16 logits).
+//   TWICE     the same of longer rows: a block, or a cluster that shares a row, reads it twice, the second
+//             time from L2.
 //   GRADIENT  the gradient alone, from lse: slices one by one.
 //
 // A ninth warp fills the ring and prepares what a row has beside its logits: the policy's scalars,
@@ -21,6 +21,7 @@
 #include <cstdint>
 #include <mutex>
 #include <string>
+#include <type_traits>
 
 #include "layout.h"
 #include "ops.h"
@@ -35,6 +36,7 @@ constexpr int kMaxCluster = 8, kMaxStages = 4;
 constexpr int kMostUnits = 8;  // 16-byte units of a slice that a thread has
 constexpr int kMostSmem = 104 * 1024;  // stages, and what goes with a row: 2 x (32 + 16.1) or 4 x (8 + 16.1) KB at most
 constexpr int kNamed = 32768;
+constexpr int64_t kL2Rows = 40 << 20;  // bytes of rows that are read twice while L2 still has them
 constexpr float kLog2E = 1.4426950408889634f;
 
 enum Mode { STATS, HELD, TWICE, GRADIENT };
@@ -110,6 +112,7 @@ struct Slice {
   int32_t phase;  // elements between the row's first unit and the row
   int32_t first, units;  // first unit in the row, and how many the slice has of it
   int32_t row_units;
+  bool clean;     // all its units lie inside the row
   __device__ __forceinline__ Slice(const Args &a, int64_t r, int32_t index) : row(r) {
     const uintptr_t p = (uintptr_t)a.logits + r * a.ld_z * sizeof(T);
     phase = (int32_t)(p & 15u) / (int)sizeof(T);
@@ -117,6 +120,7 @@ struct Slice {
     first = index * a.units;
     units = max(0, min(a.units, row_units - first));
     at = (p & ~(uintptr_t)15) + (int64_t)first * 16;
+    clean = (phase == 0 || first > 0) && (row_units * kPer == phase + a.vocab || first + units < row_units);
   }
   // Elements of the row that the slice has.
   __device__ __forceinline__ int32_t begin() const { return max(0, first * kPer - phase); }
@@ -145,7 +149,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side
   float *q = reinterpret_cast<float *>(ids + a.top), *gq = q + a.top, *v = gq + a.top;
   float top = -INFINITY;
   bool nan = false;
-#pragma unroll 2
+#pragma unroll 8
   for (int j = lane; j < a.top; j += 32) {
     const int32_t id = token_at(a, row * a.ld_tokens + j);
     const float x = id < 0 ? -INFINITY : load_any(a.teacher, row * a.ld_teacher + j, a.teacher_bf16) * a.inv_t;
@@ -158,6 +162,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side
   for (int m = 16; m > 0; m /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
   nan = __any_sync(0xFFFFFFFFu, nan);
   float sum = 0.0f;
+#pragma unroll 4
   for (int j = lane; j < a.top; j += 32) {
     const float e = ids[j] < 0 ? 0.0f : ex2((v[j] - top) * kLog2E);
     q[j] = e;
@@ -169,6 +174,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side
   const float inv = some ? 1.0f / sum : 0.0f, log_sum = logf(sum);
   float total = 0.0f;
   bool twice = false;
+#pragma unroll 4
   for (int j = lane; j < a.top; j += 32) {
     const float p = q[j] * inv;
     q[j] = gq[j] = p;
@@ -289,38 +295,81 @@ __device__ __forceinline__ float staged(const uint8_t *stage, const Slice<T> &s,
   return (float)reinterpret_cast<const T *>(stage)[element + s.phase - s.first * Slice<T>::kPer];
 }
 
-// The elements of unit u of a slice (-infinity outside the row) as pairs.
-template <class T>
-__device__ __forceinline__ void unit_of(const Args &a, const uint8_t *stage, const Slice<T> &s, int u, float2 (&z)[Slice<T>::kPer / 2]) {
+// A thread's units of a slice, as they are stored; -infinity outside the row.
+template <class T, int K>
+__device__ __forceinline__ void load_units(const Args &a, const uint8_t *stage, const Slice<T> &s, uint4 (&r)[K]) {
   constexpr int P = Slice<T>::kPer;
-  if (u >= s.units) {
+  constexpr uint32_t kNone = P == 8 ? 0xFF80FF80u : 0xFF800000u;
 #pragma unroll
-    for (int e = 0; e < P / 2; ++e) z[e] = both(-INFINITY);
-    return;
+  for (int k = 0; k < K; ++k) {
+    const int u = k * kThreads + threadIdx.x;
+    r[k] = u < s.units ? *reinterpret_cast<const uint4 *>(stage + u * 16) : make_uint4(kNone, kNone, kNone, kNone);
   }
-  const uint4 r = *reinterpret_cast<const uint4 *>(stage + u * 16);
+  if (!s.clean) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int32_t g = s.first + k * kThreads + (int)threadIdx.x;
+      if (g != 0 && g != s.row_units - 1) continue;
+      uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const int32_t j = g * P + e - s.phase;
+        const uint32_t bits = P == 8 ? 0xFFFFu << (e % 2 * 16) : 0xFFFFFFFFu;
+        if (j < 0 || j >= a.vocab) w[e * 4 / P] = (w[e * 4 / P] & ~bits) | (kNone & bits);
+      }
+      r[k] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+template <class T>
+__device__ __forceinline__ void unpack(uint4 r, float2 (&z)[Slice<T>::kPer / 2]) {
   if constexpr (sizeof(T) == 2) {
     unpack8(r, z);
   } else {
     z[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y)), z[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
   }
-  const int32_t g = s.first + u;
-  if (g == 0 || g == s.row_units - 1) {
+}
+template <class T, int K>
+__device__ __forceinline__ float top_of(const uint4 (&r)[K]) {
+  if constexpr (sizeof(T) == 2) {
+    __nv_bfloat162 m[2];
 #pragma unroll
-    for (int e = 0; e < P; ++e) {
-      const int32_t j = g * P + e - s.phase;
-      if (j < 0 || j >= a.vocab) element(z, e) = -INFINITY;
+    for (int k = 0; k < K; ++k) {
+      const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&r[k]);
+      m[0] = k ? __hmax2(m[0], __hmax2(p[0], p[1])) : __hmax2(p[0], p[1]);
+      m[1] = k ? __hmax2(m[1], __hmax2(p[2], p[3])) : __hmax2(p[2], p[3]);
     }
+    const float2 v = __bfloat1622float2(__hmax2(m[0], m[1]));
+    return fmaxf(fmaxf(v.x, v.y), -INFINITY);  // of NaN alone: as of nothing
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(r[k].x), __uint_as_float(r[k].y)), fmaxf(__uint_as_float(r[k].z), __uint_as_float(r[k].w))));
+    return m;
   }
 }
+
+// (z - from) scale as z scale + by: one operation, where the product is finite, with the rounding of `by` taken
+// back afterwards (`left`, of the exponent).  Else a difference and a product.
+struct Exponent {
+  float from, scale, by, left;
+  bool quick;
+  __device__ __forceinline__ Exponent(float f, float s) : from(f), scale(s) {
+    by = -f * s, left = fmaf(f, s, by);
+    quick = fabsf(by) < 1e37f;
+  }
+  __device__ __forceinline__ float2 quickly(float2 z) const { return __ffma2_rn(z, both(scale), both(by)); }
+  __device__ __forceinline__ float2 carefully(float2 z) const { return __fmul2_rn(__fadd2_rn(z, both(-from)), both(scale)); }
+};
+__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
 
 // A unit's gradient.  `even`: units of the gradient's rows begin on their own boundaries.
 template <class T>
 __device__ __forceinline__ void put_unit(const Args &a, const Slice<T> &s, void *g_row, bool even, int u, const float2 (&v)[Slice<T>::kPer / 2]) {
   constexpr int P = Slice<T>::kPer;
-  if (u >= s.units) return;
-  const int32_t g = s.first + u, j = g * P - s.phase;
-  if (even && j >= 0 && j + P <= a.vocab) {
+  const int32_t j = (s.first + u) * P - s.phase;
+  if (even && (s.clean || (j >= 0 && j + P <= a.vocab))) {
     if constexpr (P == 8) {
       store8(g_row, j, a.g_bf16 != 0, v);
     } else if (a.g_bf16) {
@@ -335,11 +384,12 @@ __device__ __forceinline__ void put_unit(const Args &a, const Slice<T> &s, void 
   }
 }
 
-// What a row's gradient is made of: part 2^((z by + less) scale) - slope q.
+// What a row's gradient is made of: part 2^exponent - slope q.
 struct Gradient {
-  float by, less, scale, part, slope;
+  Exponent x;
+  float part, slope;
   bool none;
-  __device__ __forceinline__ float of(float z) const { return part * ex2(fmaf(z, by, less) * scale); }
+  __device__ __forceinline__ float of(float z) const { return part * ex2((z - x.from) * x.scale); }
 };
 
 // A slice's gradient from its logits.
@@ -347,28 +397,35 @@ template <bool DISTILL, class T, int K>
 __device__ __forceinline__ void write_slice(const Args &a, const Slice<T> &slice, const uint8_t *stage, void *g_row, bool even, int32_t token,
                                             const Gradient &g) {
   constexpr int P = Slice<T>::kPer;
-  const int32_t own = DISTILL || g.none ? -1 : (token + slice.phase) / P - slice.first;
-#pragma unroll 4
-  for (int k = 0; k < K; ++k) {
-    const int u = k * kThreads + threadIdx.x;
+  if (g.none) {
     float2 v[P / 2];
-    if (g.none) {
 #pragma unroll
-      for (int i = 0; i < P / 2; ++i) v[i] = both(0.0f);
-    } else {
-      unit_of(a, stage, slice, u, v);
+    for (int i = 0; i < P / 2; ++i) v[i] = both(0.0f);
+    for (int u = threadIdx.x; u < slice.units; u += kThreads) put_unit(a, slice, g_row, even, u, v);
+    return;
+  }
+  const int32_t own = DISTILL ? -1 : (token + slice.phase) / P - slice.first;
+  const float2 part = both(g.x.quick ? g.part * ex2(-g.x.left) : g.part);
+  auto each = [&](auto quick) {
+#pragma unroll 4
+    for (int k = 0; k < K; ++k) {
+      const int u = k * kThreads + threadIdx.x;
+      if (u >= slice.units) break;
+      float2 v[P / 2];
+      unpack<T>(*reinterpret_cast<const uint4 *>(stage + u * 16), v);
 #pragma unroll
-      for (int i = 0; i < P / 2; ++i) {
-        const float2 x = __fmul2_rn(__ffma2_rn(v[i], both(g.by), both(g.less)), both(g.scale));
-        v[i] = __fmul2_rn(make_float2(ex2(x.x), ex2(x.y)), both(g.part));
-      }
+      for (int i = 0; i < P / 2; ++i) v[i] = __fmul2_rn(ex2(quick ? g.x.quickly(v[i]) : g.x.carefully(v[i])), part);
       if (!DISTILL && own == u) {
 #pragma unroll
         for (int i = 0; i < P; ++i) element(v, i) -= i == (token + slice.phase) % P ? g.slope : 0.0f;
       }
+      put_unit(a, slice, g_row, even, u, v);
     }
-    put_unit(a, slice, g_row, even, u, v);
-  }
+  };
+  if (g.x.quick)
+    each(std::true_type());
+  else
+    each(std::false_type());
 }
 // Once a slice's units are written: the teacher's tokens in it, once more.
 template <class T>
@@ -403,7 +460,8 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
     auto even = [&](const Slice<T> &s) { return ((uintptr_t)g_row - s.phase * g_size) % (a.g_bf16 ? P * 2 : 16) == 0; };
     float m = -INFINITY, sum = 0.0f, hit = 0.0f;  // of the thread, over the block's slices; what it has of the targets
     float weight = 0.0f;
-    float2 e[MODE == GRADIENT ? 1 : K][P / 2];
+    float held = 1.0f;               // what the exponentials of a row that is held are still to be multiplied by
+    float2 e[MODE == HELD ? K : 1][P / 2];
     for (int round = 0; round < a.rounds; ++round) {
       const Slice<T> slice(a, row, MODE == GRADIENT ? (int32_t)(item - row * a.slices) : (int32_t)rank * a.rounds + round);
       const uint8_t *stage = stages + stage_at * a.stage_bytes;
@@ -423,23 +481,33 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
           if (t == 0 && side.token >= slice.begin() && side.token < slice.end(a)) hit += staged(stage, slice, side.token);
         }
         if constexpr (MODE != GRADIENT) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            unit_of(a, stage, slice, k * kThreads + t, e[k]);
-#pragma unroll
-            for (int i = 0; i < P / 2; ++i) top = fmaxf(top, fmaxf(e[k][i].x, e[k][i].y));
-          }
-          const float2 less = both(top == -INFINITY ? 0.0f : -top), by = both(a.scale);
+          uint4 raw[K];
+          load_units<T, K>(a, stage, slice, raw);
+          const float top = top_of<T, K>(raw);
+          const Exponent x(top == -INFINITY ? 0.0f : top, a.scale);
           float2 s = both(0.0f);
+          auto each = [&](auto quick) {
 #pragma unroll
-          for (int k = 0; k < K; ++k)
+            for (int k = 0; k < K; ++k) {
+              float2 z[P / 2];
+              unpack<T>(raw[k], z);
 #pragma unroll
-            for (int i = 0; i < P / 2; ++i) {
-              const float2 x = __fmul2_rn(__fadd2_rn(e[k][i], less), by);
-              e[k][i] = make_float2(ex2(x.x), ex2(x.y));
-              s = __fadd2_rn(s, e[k][i]);
+              for (int i = 0; i < P / 2; ++i) {
+                const float2 y = ex2(quick ? x.quickly(z[i]) : x.carefully(z[i]));
+                s = __fadd2_rn(s, y);
+                if constexpr (MODE == HELD) e[k][i] = y;
+              }
             }
+          };
+          float whole = 1.0f;
+          if (__all_sync(0xFFFFFFFFu, x.quick)) {
+            each(std::true_type());
+            whole = ex2(-x.left);
+          } else {
+            each(std::false_type());
+          }
+          if constexpr (MODE == HELD) held = whole;
+          s = __fmul2_rn(s, both(whole));
           if constexpr (MODE == HELD)
             m = top, sum = s.x + s.y;
           else
@@ -447,7 +515,8 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
         }
       }
       if constexpr (MODE == GRADIENT) {
-        Gradient g = {a.inv_t, -side.lse, kLog2E, side.slope, side.slope, weight == 0.0f || side.mass == 0.0f};
+        // p = 2^((z - lse T) / T log2 e)
+        const Gradient g = {Exponent(side.lse * a.t, a.scale), side.slope, side.slope, weight == 0.0f || side.mass == 0.0f};
         write_slice<DISTILL, T, K>(a, slice, stage, g_row, even(slice), side.token, g);
         if (DISTILL && !g.none) write_named(a, slice, g_row, ids, gq, zt, g);
       }
@@ -474,7 +543,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
           X += v.z;
         }
       };
-      if (MODE == STATS && a.cluster > 1) {
+      if (MODE != HELD && a.cluster > 1) {
         const uint32_t bar = tc::smem(&sh.arrived[slot]);
         if (t < a.cluster) {
           join(sh.warp[slot], kWarps);
@@ -509,13 +578,13 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
       if (!DISTILL) a.logp[row] = logp;
     }
     if constexpr (MODE == STATS) continue;
-    const Gradient g = {1.0f, -M, a.scale, slope / S, slope, weight == 0.0f || side.mass == 0.0f};
+    const Gradient g = {Exponent(M, a.scale), slope / S, slope, weight == 0.0f || side.mass == 0.0f};
     if constexpr (MODE == HELD) {
       const Slice<T> slice(a, row, 0);
       if (g.none) {
         write_slice<DISTILL, T, K>(a, slice, stages, g_row, even(slice), 0, g);
       } else {
-        const float2 by = both(g.part * below(m, M, a.scale));
+        const float2 by = both(g.part * (held * below(m, M, a.scale)));
         const int32_t own = DISTILL ? -1 : (side.token + slice.phase) / P;  // the token's unit
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -525,14 +594,14 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
 #pragma unroll
             for (int i = 0; i < P; ++i) element(e[k], i) -= i == (side.token + slice.phase) % P ? slope : 0.0f;
           }
-          put_unit(a, slice, g_row, even(slice), k * kThreads + t, e[k]);
+          if (k * kThreads + t < slice.units) put_unit(a, slice, g_row, even(slice), k * kThreads + t, e[k]);
         }
         if (DISTILL) write_named(a, slice, g_row, ids, gq, zt, g);
       }
       next();
     } else {
       for (int round = 0; round < a.rounds; ++round) {
-        const Slice<T> slice(a, row, round);
+        const Slice<T> slice(a, row, (int32_t)rank * a.rounds + round);
         tc::bar_wait(tc::smem(&sh.full[stage_at]), parity, a.wait_limit_ns, &sh.stop);
         write_slice<DISTILL, T, K>(a, slice, stages + stage_at * a.stage_bytes, g_row, even(slice), side.token, g);
         if (DISTILL && !g.none) write_named(a, slice, g_row, ids, gq, zt, g);
@@ -641,11 +710,12 @@ cudaError_t launch_rows(Args &a, cudaStream_t s) {
   if (MODE == GRADIENT) {
     a.slices = (int32_t)((row_units + kMost - 1) / kMost);
   } else if (MODE != HELD) {
-    // A loss alone of few rows: as many blocks to a row as keep the SMs busy, with 256 units each at least.
-    if (MODE == STATS) {
-      const int64_t want = std::min<int64_t>((2 * device_sms() + a.rows - 1) / a.rows, row_units / kThreads);
-      a.cluster = (int32_t)std::min<int64_t>(kMaxCluster, std::max<int64_t>(1, want));
-    }
+    // Few rows: as many blocks to a row as keep the SMs busy, with 256 units each at least.  Rows that are read twice: as
+    // many as it takes for all rows at work to stay in L2.
+    const int64_t blocks = 2 * device_sms();
+    int64_t want = std::min<int64_t>((blocks + a.rows - 1) / a.rows, row_units / kThreads);
+    if (MODE == TWICE) want = std::max<int64_t>(want, (blocks * row_units * 16 + kL2Rows - 1) / kL2Rows);
+    a.cluster = (int32_t)std::min<int64_t>(kMaxCluster, std::max<int64_t>(1, want));
     a.rounds = (int32_t)((row_units + kMost * a.cluster - 1) / (kMost * a.cluster));
   }
   const int64_t parts = (int64_t)a.cluster * a.rounds * a.slices;
@@ -673,12 +743,7 @@ cudaError_t launch_as(Args &a, cudaStream_t s) {
   if (a.backward) return launch_rows<DISTILL, T, GRADIENT>(a, s);
   if (!a.dlogits) return launch_rows<DISTILL, T, STATS>(a, s);
   if (units_of<T>(a) <= kThreads * kMostUnits) return launch_rows<DISTILL, T, HELD>(a, s);
-  // Fewer rows than SMs: two launches that share rows out.
-  if (a.rows >= device_sms()) return launch_rows<DISTILL, T, TWICE>(a, s);
-  cudaError_t e = launch_rows<DISTILL, T, STATS>(a, s);
-  if (e != cudaSuccess) return e;
-  a.lse_in = a.lse, a.logp_in = a.logp, a.dloss = nullptr;
-  return launch_rows<DISTILL, T, GRADIENT>(a, s);
+  return launch_rows<DISTILL, T, TWICE>(a, s);
 }
 
 template <bool DISTILL>
