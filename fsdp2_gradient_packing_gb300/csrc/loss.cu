@@ -12,8 +12,8 @@
 //             time from L2.
 //   GRADIENT  the gradient alone, from lse: slices one by one.
 //
-// A ninth warp fills the ring and prepares what a row has beside its logits: the policy's scalars,
-// or the softmax of the teacher's entries, while the others are at the row before.
+// A ninth warp fills the ring, and a tenth prepares what a row has beside its logits: the policy's scalars,
+// or the softmax of the teacher's entries, while the other eight are at the row before.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -31,7 +31,7 @@ namespace fsdp {
 namespace loss {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kMaxTop = FSDP_DISTILL_MAX_TOP;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kBlock = kThreads + 64, kMaxTop = FSDP_DISTILL_MAX_TOP;
 constexpr int kMaxCluster = 8, kMaxStages = 4;
 constexpr int kMostUnits = 8;  // 16-byte units of a slice that a thread has
 constexpr int kMostSmem = 104 * 1024;  // stages, and what goes with a row: 2 x (32 + 16.1) or 4 x (8 + 16.1) KB at most
@@ -59,8 +59,7 @@ struct Args {
   float low, high, kl;
 };
 
-// What the ninth warp prepares of a row.  Teacher's entries follow it: tokens, q, the gradient's q (negative: another entry
-// of the same token has it), and room for their logits.
+// What the tenth warp prepares of a row.  The teacher's entries follow it.
 struct alignas(16) Side {
   float up;          // weight x dloss
   float weight;
@@ -74,7 +73,8 @@ struct alignas(16) Side {
 struct alignas(16) Shared {
   float4 warp[2][kWarps];        // maximum and sum of a warp, and what it has of the targets
   float4 block[2][kMaxCluster];  // the same of the cluster's blocks
-  uint64_t arrived[2], full[kMaxStages], empty[kMaxStages];
+  uint64_t arrived[2], full[kMaxStages], empty[kMaxStages];  // of the cluster's sums; of stages
+  uint64_t ready[kMaxStages], done[kMaxStages];              // of rows' sides
   uint32_t named[kNamed / 32];   // tokens that the teacher has named, by their last bits
   uint32_t stop;
 };
@@ -141,95 +141,189 @@ __device__ __forceinline__ void policy_of(const Args &a, float logp, const Side 
   }
 }
 
-// ---- the ninth warp ------------------------------------------------------------------------
-template <class T>
-__device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side, int64_t row, int32_t lo, int32_t hi, bool gradient) {
-  const int lane = threadIdx.x & 31;
-  int32_t *ids = reinterpret_cast<int32_t *>(&side + 1);
-  float *q = reinterpret_cast<float *>(ids + a.top), *gq = q + a.top, *v = gq + a.top;
-  float top = -INFINITY;
-  bool nan = false;
-#pragma unroll 8
-  for (int j = lane; j < a.top; j += 32) {
-    const int32_t id = token_at(a, row * a.ld_tokens + j);
-    const float x = id < 0 ? -INFINITY : load_any(a.teacher, row * a.ld_teacher + j, a.teacher_bf16) * a.inv_t;
-    ids[j] = x == -INFINITY ? -1 : id;
-    v[j] = x;
-    top = fmaxf(top, x);
-    nan |= x != x;
-  }
+// ---- the ninth and the tenth warp ------------------------------------------------------------------------
+constexpr int kEach = 4;  // teacher's entries that a lane holds in registers: up to 128 in all
+
+// What a row has beside its logits, on its way while the row before is prepared.
+template <bool DISTILL, Mode MODE>
+struct Ahead {
+  float weight = 1.0f, dloss = 1.0f, lse = 0.0f, logp = 0.0f, old = 0.0f, ref = 0.0f, advantage = 0.0f;
+  int32_t token = -1, id[kEach];
+  float v[kEach];
+  __device__ __forceinline__ void load(const Args &a, int64_t item) {
+    if (item >= a.items) return;
+    const int64_t row = MODE == GRADIENT ? item / a.slices : item;
+    const int lane = threadIdx.x & 31;
+    if (a.weight) weight = a.weight[row];
+    if (MODE == GRADIENT) {
+      lse = a.lse_in[row];
+      if (a.dloss) dloss = a.dloss[row];
+    }
+    if constexpr (DISTILL) {
+      if (a.top <= 32 * kEach) {
 #pragma unroll
-  for (int m = 16; m > 0; m /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-  nan = __any_sync(0xFFFFFFFFu, nan);
-  float sum = 0.0f;
-#pragma unroll 4
-  for (int j = lane; j < a.top; j += 32) {
-    const float e = ids[j] < 0 ? 0.0f : ex2((v[j] - top) * kLog2E);
-    q[j] = e;
-    sum += e;
-  }
-#pragma unroll
-  for (int m = 16; m > 0; m /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
-  const bool some = sum > 0.0f || sum != sum || nan;
-  const float inv = some ? 1.0f / sum : 0.0f, log_sum = logf(sum);
-  float total = 0.0f;
-  bool twice = false;
-#pragma unroll 4
-  for (int j = lane; j < a.top; j += 32) {
-    const float p = q[j] * inv;
-    q[j] = gq[j] = p;
-    if (p > 0.0f || p != p) total += p * (v[j] - top - log_sum);
-    v[j] = 0.0f;
-    if (gradient && ids[j] >= lo && ids[j] < hi) {
-      const uint32_t bit = 1u << (ids[j] & 31);
-      if (atomicOr(&sh.named[ids[j] % kNamed / 32], bit) & bit) twice = true, v[j] = 1.0f;
+        for (int i = 0; i < kEach; ++i) {
+          const int j = i * 32 + lane;
+          id[i] = j < a.top ? token_at(a, row * a.ld_tokens + j) : -1;
+          v[i] = j < a.top ? load_any(a.teacher, row * a.ld_teacher + j, a.teacher_bf16) : 0.0f;
+        }
+      }
+    } else {
+      if (MODE == GRADIENT) logp = a.logp_in[row];
+      if (a.old_logp) old = a.old_logp[row];
+      if (a.ref_logp) ref = a.ref_logp[row];
+      advantage = a.advantage[row];
+      token = token_at(a, row);
     }
   }
+};
+
+__device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
-  for (int m = 16; m > 0; m /= 2) total += __shfl_xor_sync(0xFFFFFFFFu, total, m);
-  if (gradient) {
-    __syncwarp();
-    for (int j = lane; j < a.top; j += 32)
-      if (ids[j] >= lo && ids[j] < hi) sh.named[ids[j] % kNamed / 32] = 0;
-    if (__any_sync(0xFFFFFFFFu, twice)) {
-      // Tokens that are named more than once (v is 1 at all but one of a token's entries, and where tokens differ by
-      // multiples of kNamed): the first entry takes what the others have, in their order.
-      for (int j0 = 0; j0 < a.top; j0 += 32) {
-        const int j = j0 + lane;
-        uint32_t which = __ballot_sync(0xFFFFFFFFu, j < a.top && v[j] == 1.0f);
-        for (; which; which &= which - 1) {
-          const int at = j0 + __ffs(which) - 1, id = ids[at];
-          if (v[at] != 1.0f) continue;  // its token has been joined
-          int first = -1;
-          float s = 0.0f;
-          for (int k0 = 0; k0 < a.top; k0 += 32) {
-            const int k = k0 + lane;
-            const bool same = k < a.top && ids[k] == id;
-            const float other = same ? q[k] : 0.0f;
-            uint32_t more = __ballot_sync(0xFFFFFFFFu, same);
-            if (more && first < 0) first = k0 + __ffs(more) - 1;
-            for (; more; more &= more - 1) s += __shfl_sync(0xFFFFFFFFu, other, __ffs(more) - 1);
-            if (same) gq[k] = -1.0f, v[k] = 0.0f;
-          }
-          __syncwarp();
-          if (lane == 0) gq[first] = s;
-          __syncwarp();
+  for (int m = 16; m > 0; m /= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, m));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int m = 16; m > 0; m /= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, m);
+  return x;
+}
+
+// The teacher's entries of a row in shared memory: tokens (-1: none), q for the loss, q for the gradient (negative: another
+// entry of its token has it), and room for their logits.
+struct Teacher {
+  int32_t *ids;
+  float *q, *gq, *z;
+  __device__ __forceinline__ Teacher(Side &side, int top)
+      : ids(reinterpret_cast<int32_t *>(&side + 1)), q(reinterpret_cast<float *>(ids + top)), gq(q + top), z(gq + top) {}
+};
+
+// Whether an entry's token (or another with the same last bits) has been named before; forget() clears that.
+__device__ __forceinline__ bool name(Shared &sh, int32_t id) {
+  const uint32_t bit = 1u << (id & 31);
+  return (atomicOr(&sh.named[id % kNamed / 32], bit) & bit) != 0;
+}
+__device__ __forceinline__ void forget(Shared &sh, int32_t id) { sh.named[id % kNamed / 32] = 0; }
+
+// Tokens that are named more than once (z is 1 at all but one of a token's entries, and where tokens differ by multiples
+// of kNamed): the first entry takes what the others have, in their order.
+__device__ __noinline__ void join_entries(int top, const Teacher &e) {
+  const int lane = threadIdx.x & 31;
+  for (int j0 = 0; j0 < top; j0 += 32) {
+    uint32_t which = __ballot_sync(0xFFFFFFFFu, j0 + lane < top && e.z[j0 + lane] == 1.0f);
+    for (; which; which &= which - 1) {
+      const int at = j0 + __ffs(which) - 1, id = e.ids[at];
+      if (e.z[at] != 1.0f) continue;  // its token has been joined
+      int first = -1;
+      float s = 0.0f;
+      for (int k0 = 0; k0 < top; k0 += 32) {
+        const int k = k0 + lane;
+        const bool same = k < top && e.ids[k] == id;
+        const float other = same ? e.q[k] : 0.0f;
+        uint32_t more = __ballot_sync(0xFFFFFFFFu, same);
+        if (more && first < 0) first = k0 + __ffs(more) - 1;
+        for (; more; more &= more - 1) s += __shfl_sync(0xFFFFFFFFu, other, __ffs(more) - 1);
+        if (same) e.gq[k] = -1.0f, e.z[k] = 0.0f;
+      }
+      __syncwarp();
+      if (lane == 0) e.gq[first] = s;
+      __syncwarp();
+    }
+  }
+}
+
+// The softmax over a row's entries; tokens lo .. hi - 1 are those of this block's gradient.
+template <bool DISTILL, Mode MODE>
+__device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side, int64_t row, int32_t lo, int32_t hi,
+                                           const Ahead<DISTILL, MODE> &ahead) {
+  const int lane = threadIdx.x & 31;
+  const Teacher e(side, a.top);
+  float top = -INFINITY, sum = 0.0f, total = 0.0f;
+  bool nan = false, twice = false;
+  if (a.top <= 32 * kEach) {
+    float v[kEach];
+    int32_t id[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      v[i] = ahead.id[i] < 0 ? -INFINITY : ahead.v[i] * a.inv_t;
+      id[i] = v[i] == -INFINITY ? -1 : ahead.id[i];
+      top = fmaxf(top, v[i]);
+      nan |= v[i] != v[i];
+    }
+    top = warp_max(top);
+    bool again[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const float d = v[i] - top, p = id[i] < 0 ? 0.0f : ex2(d * kLog2E);
+      sum += p;
+      if (p > 0.0f || p != p) total += p * d;
+      v[i] = p;
+      again[i] = MODE != STATS && id[i] >= lo && id[i] < hi && name(sh, id[i]);
+      twice |= again[i];
+    }
+    sum = warp_sum(sum), total = warp_sum(total);
+    const float inv = 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int j = i * 32 + lane;
+      if (j < a.top) {
+        e.ids[j] = id[i];
+        e.q[j] = e.gq[j] = id[i] < 0 ? 0.0f : v[i] * inv;
+        if (MODE != STATS) {
+          e.z[j] = again[i] ? 1.0f : 0.0f;
+          if (id[i] >= lo && id[i] < hi) forget(sh, id[i]);
         }
       }
     }
+  } else {
+#pragma unroll 8
+    for (int j = lane; j < a.top; j += 32) {
+      const int32_t id = token_at(a, row * a.ld_tokens + j);
+      const float x = id < 0 ? -INFINITY : load_any(a.teacher, row * a.ld_teacher + j, a.teacher_bf16) * a.inv_t;
+      e.ids[j] = x == -INFINITY ? -1 : id;
+      e.z[j] = x;
+      top = fmaxf(top, x);
+      nan |= x != x;
+    }
+    top = warp_max(top);
+#pragma unroll 8
+    for (int j = lane; j < a.top; j += 32) {
+      const float d = e.z[j] - top, p = e.ids[j] < 0 ? 0.0f : ex2(d * kLog2E);
+      sum += p;
+      if (p > 0.0f || p != p) total += p * d;
+      e.q[j] = p;
+    }
+    sum = warp_sum(sum), total = warp_sum(total);
+    const float inv = 1.0f / sum;
+#pragma unroll 8
+    for (int j = lane; j < a.top; j += 32) {
+      const int32_t id = e.ids[j];
+      e.q[j] = e.gq[j] = id < 0 ? 0.0f : e.q[j] * inv;
+      if (MODE != STATS) {
+        const bool again = id >= lo && id < hi && name(sh, id);
+        e.z[j] = again ? 1.0f : 0.0f;
+        twice |= again;
+      }
+    }
+    if (MODE != STATS) {
+      __syncwarp();
+      for (int j = lane; j < a.top; j += 32)
+        if (e.ids[j] >= lo && e.ids[j] < hi) forget(sh, e.ids[j]);
+    }
   }
-  if (lane == 0) side.mass = some ? 1.0f : 0.0f, side.q_log_q = total;
+  __syncwarp();
+  if (MODE != STATS && __any_sync(0xFFFFFFFFu, twice)) join_entries(a.top, e);
+  const bool some = sum > 0.0f || sum != sum || __any_sync(0xFFFFFFFFu, nan);
+  // sum q log q, with log q = (v - top) - log sum
+  if (lane == 0) side.mass = some ? 1.0f : 0.0f, side.q_log_q = some ? total / sum - logf(sum) : 0.0f;
 }
 
-template <bool DISTILL, class T, Mode MODE>
+// The ninth warp (one lane of it): slices into the ring.
+template <class T, Mode MODE>
 __device__ __forceinline__ void feed(const Args &a, Shared &sh, uint8_t *stages, uint32_t rank, int64_t first, int64_t step) {
-  const int lane = threadIdx.x & 31;
-  int stage = 0, side_at = 0;
+  int stage = 0;
   uint32_t parity = 1;
-  auto weight_of = [&](int64_t item) {
-    const int64_t row = MODE == GRADIENT ? item / a.slices : item;
-    return item < a.items && a.weight ? a.weight[row] : 1.0f;
-  };
+  auto weight_of = [&](int64_t item) { return item < a.items && a.weight ? a.weight[MODE == GRADIENT ? item / a.slices : item] : 1.0f; };
   float ahead = weight_of(first);
   bool skip = (a.fault & 1) != 0 && blockIdx.x == 0;  // test hook: a first stage that stays empty
   for (int64_t item = first; item < a.items; item += step) {
@@ -241,50 +335,58 @@ __device__ __forceinline__ void feed(const Args &a, Shared &sh, uint8_t *stages,
       const Slice<T> slice(a, row, MODE == GRADIENT ? (int32_t)(item - row * a.slices) : (int32_t)rank * a.rounds + round);
       const uint32_t full = tc::smem(&sh.full[stage]);
       tc::bar_wait(tc::smem(&sh.empty[stage]), parity, a.wait_limit_ns, &sh.stop);
-      if (lane == 0) {
-        if (weight != 0.0f && slice.units > 0 && !skip) {
-          tc::bar_expect(full, slice.units * 16);
-          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                           tc::smem(stages + stage * a.stage_bytes)),
-                       "l"(slice.at), "r"(slice.units * 16), "r"(full)
-                       : "memory");
-        } else if (!skip) {
-          tc::bar_arrive(full);
-        }
-        skip = false;
+      if (weight != 0.0f && slice.units > 0 && !skip) {
+        tc::bar_expect(full, slice.units * 16);
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         tc::smem(stages + stage * a.stage_bytes)),
+                     "l"(slice.at), "r"(slice.units * 16), "r"(full)
+                     : "memory");
+      } else if (!skip) {
+        tc::bar_arrive(full);
       }
-      if (turn == 0) {
-        Side &side = *reinterpret_cast<Side *>(stages + a.stages * a.stage_bytes + side_at * a.side_bytes);
-        float slope = 0.0f;
-        const float dloss = MODE == GRADIENT && a.dloss && weight != 0.0f ? a.dloss[row] : 1.0f, up = weight * dloss;
-        if (lane == 0) {
-          side.weight = weight, side.up = up;
-          if (MODE == GRADIENT) side.lse = weight != 0.0f ? a.lse_in[row] : 0.0f;
-        }
-        if (weight != 0.0f) {
-          if constexpr (DISTILL) {
-            teacher_of<T>(a, sh, side, row, MODE == GRADIENT ? slice.begin() : 0, MODE == GRADIENT ? slice.end(a) : a.vocab, MODE != STATS);
-            slope = up * a.t;
-          } else if (lane == 0) {
-            side.old = a.old_logp ? a.old_logp[row] : 0.0f;
-            side.ref = a.ref_logp ? a.ref_logp[row] : 0.0f;
-            side.advantage = a.advantage[row];
-            side.token = token_at(a, row);
-            side.mass = side.token >= 0 ? 1.0f : 0.0f;
-            if (MODE == GRADIENT) {
-              float l, d;
-              policy_of(a, a.logp_in[row], side, l, d);
-              slope = -d * up * a.inv_t;
-            }
-          }
-        }
-        if (lane == 0) side.slope = slope;
-        if (++side_at == a.stages) side_at = 0;
-      }
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(full);
+      skip = false;
       if (++stage == a.stages) stage = 0, parity ^= 1u;
     }
+  }
+}
+
+// The tenth warp: what rows have beside their logits.
+template <bool DISTILL, class T, Mode MODE>
+__device__ __forceinline__ void prepare(const Args &a, Shared &sh, uint8_t *stages, int64_t first, int64_t step) {
+  const int lane = threadIdx.x & 31;
+  int side_at = 0;
+  uint32_t parity = 1;
+  Ahead<DISTILL, MODE> ahead;
+  ahead.load(a, first);
+  for (int64_t item = first; item < a.items; item += step) {
+    const int64_t row = MODE == GRADIENT ? item / a.slices : item;
+    tc::bar_wait(tc::smem(&sh.done[side_at]), parity, a.wait_limit_ns, &sh.stop);
+    Side &side = *reinterpret_cast<Side *>(stages + a.stages * a.stage_bytes + side_at * a.side_bytes);
+    const float up = ahead.weight * ahead.dloss;
+    if constexpr (DISTILL) {
+      if (ahead.weight != 0.0f) {
+        const Slice<T> slice(a, row, MODE == GRADIENT ? (int32_t)(item - row * a.slices) : 0);
+        teacher_of<DISTILL, MODE>(a, sh, side, row, MODE == GRADIENT ? slice.begin() : 0, MODE == GRADIENT ? slice.end(a) : a.vocab, ahead);
+      }
+    }
+    if (lane == 0) {
+      side.weight = ahead.weight, side.up = up, side.lse = ahead.lse;
+      if constexpr (DISTILL) {
+        side.slope = up * a.t;
+      } else {
+        side.old = ahead.old, side.ref = ahead.ref, side.advantage = ahead.advantage, side.token = ahead.token;
+        side.mass = ahead.token >= 0 ? 1.0f : 0.0f;
+        if (MODE == GRADIENT) {
+          float l, d;
+          policy_of(a, ahead.logp, side, l, d);
+          side.slope = -d * up * a.inv_t;
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) tc::bar_arrive(tc::smem(&sh.ready[side_at]));
+    if (++side_at == a.stages) side_at = 0, parity ^= 1u;
+    ahead.load(a, item + step);
   }
 }
 
@@ -406,26 +508,27 @@ __device__ __forceinline__ void write_slice(const Args &a, const Slice<T> &slice
   }
   const int32_t own = DISTILL ? -1 : (token + slice.phase) / P - slice.first;
   const float2 part = both(g.x.quick ? g.part * ex2(-g.x.left) : g.part);
-  auto each = [&](auto quick) {
-#pragma unroll 4
+  auto each = [&](auto quick, auto full) {
+#pragma unroll(K < 4 ? K : 4)
     for (int k = 0; k < K; ++k) {
       const int u = k * kThreads + threadIdx.x;
-      if (u >= slice.units) break;
       float2 v[P / 2];
-      unpack<T>(*reinterpret_cast<const uint4 *>(stage + u * 16), v);
+      unpack<T>(full || u < slice.units ? *reinterpret_cast<const uint4 *>(stage + u * 16) : make_uint4(0, 0, 0, 0), v);
 #pragma unroll
       for (int i = 0; i < P / 2; ++i) v[i] = __fmul2_rn(ex2(quick ? g.x.quickly(v[i]) : g.x.carefully(v[i])), part);
       if (!DISTILL && own == u) {
 #pragma unroll
         for (int i = 0; i < P; ++i) element(v, i) -= i == (token + slice.phase) % P ? g.slope : 0.0f;
       }
-      put_unit(a, slice, g_row, even, u, v);
+      if (full || u < slice.units) put_unit(a, slice, g_row, even, u, v);
     }
   };
-  if (g.x.quick)
-    each(std::true_type());
+  if (!g.x.quick)
+    each(std::false_type(), std::false_type());
+  else if (slice.units == K * kThreads)
+    each(std::true_type(), std::true_type());
   else
-    each(std::false_type());
+    each(std::true_type(), std::false_type());
 }
 // Once a slice's units are written: the teacher's tokens in it, once more.
 template <class T>
@@ -442,7 +545,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
   constexpr int P = Slice<T>::kPer;
   const int t = threadIdx.x, lane = t & 31, warp = t / 32;
   int stage_at = 0, side_at = 0, turn = 0;
-  uint32_t parity = 0;
+  uint32_t parity = 0, side_parity = 0;
   auto next = [&] {  // the stage has been read
     __syncwarp();
     if (lane == 0) tc::bar_arrive(tc::smem(&sh.empty[stage_at]));
@@ -451,22 +554,28 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
   for (int64_t item = first; item < a.items; item += step) {
     const int64_t row = MODE == GRADIENT ? item / a.slices : item;
     Side &side = *reinterpret_cast<Side *>(stages + a.stages * a.stage_bytes + side_at * a.side_bytes);
-    const int32_t *ids = reinterpret_cast<const int32_t *>(&side + 1);
-    const float *q = reinterpret_cast<const float *>(ids + a.top), *gq = q + a.top;
-    float *zt = const_cast<float *>(gq) + a.top;
-    if (++side_at == a.stages) side_at = 0;
+    const Teacher teacher(side, a.top);
+    const int32_t *ids = teacher.ids;
+    const float *q = teacher.q, *gq = teacher.gq;
+    float *zt = teacher.z;
+    tc::bar_wait(tc::smem(&sh.ready[side_at]), side_parity, a.wait_limit_ns, &sh.stop);
+    const float weight = side.weight;
+    const uint32_t done = tc::smem(&sh.done[side_at]);
+    if (++side_at == a.stages) side_at = 0, side_parity ^= 1u;
+    auto leave = [&] {  // the row's side has been read
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(done);
+    };
     const int g_size = a.g_bf16 ? 2 : 4;
     uint8_t *g_row = static_cast<uint8_t *>(a.dlogits) + row * a.ld_g * g_size;
     auto even = [&](const Slice<T> &s) { return ((uintptr_t)g_row - s.phase * g_size) % (a.g_bf16 ? P * 2 : 16) == 0; };
     float m = -INFINITY, sum = 0.0f, hit = 0.0f;  // of the thread, over the block's slices; what it has of the targets
-    float weight = 0.0f;
     float held = 1.0f;               // what the exponentials of a row that is held are still to be multiplied by
     float2 e[MODE == HELD ? K : 1][P / 2];
     for (int round = 0; round < a.rounds; ++round) {
       const Slice<T> slice(a, row, MODE == GRADIENT ? (int32_t)(item - row * a.slices) : (int32_t)rank * a.rounds + round);
       const uint8_t *stage = stages + stage_at * a.stage_bytes;
       tc::bar_wait(tc::smem(&sh.full[stage_at]), parity, a.wait_limit_ns, &sh.stop);
-      weight = side.weight;
       if (weight != 0.0f) {
         // The targets' logits.
         if constexpr (DISTILL) {
@@ -522,7 +631,10 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
       }
       if (MODE != HELD) next();
     }
-    if constexpr (MODE == GRADIENT) continue;
+    if constexpr (MODE == GRADIENT) {
+      leave();
+      continue;
+    }
     // The row's maximum and sum.
     float M = m, S = sum, X = hit;
     if (weight != 0.0f) {
@@ -577,7 +689,10 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
       a.loss[row] = loss, a.lse[row] = lse;
       if (!DISTILL) a.logp[row] = logp;
     }
-    if constexpr (MODE == STATS) continue;
+    if constexpr (MODE == STATS) {
+      leave();
+      continue;
+    }
     const Gradient g = {Exponent(M, a.scale), slope / S, slope, weight == 0.0f || side.mass == 0.0f};
     if constexpr (MODE == HELD) {
       const Slice<T> slice(a, row, 0);
@@ -608,20 +723,22 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
         next();
       }
     }
+    leave();
   }
 }
 
 template <bool DISTILL, class T, int K, Mode MODE>
-__global__ void __launch_bounds__(kThreads + 32, MODE != GRADIENT && K == kMostUnits ? 2 : 3) row_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kBlock, MODE != GRADIENT && K == kMostUnits ? 2 : 3) row_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ Shared sh;
   if (threadIdx.x == 0) {
     sh.stop = 0;
-    for (int i = 0; i < kMaxStages; ++i) tc::bar_init(tc::smem(&sh.full[i]), 2), tc::bar_init(tc::smem(&sh.empty[i]), kWarps);
+    for (int i = 0; i < kMaxStages; ++i) tc::bar_init(tc::smem(&sh.full[i]), 1), tc::bar_init(tc::smem(&sh.empty[i]), kWarps), tc::bar_init(tc::smem(&sh.ready[i]), 1),
+          tc::bar_init(tc::smem(&sh.done[i]), kWarps);
     for (int i = 0; i < 2; ++i) tc::bar_init(tc::smem(&sh.arrived[i]), a.cluster);
     tc::bar_init_fence();
   }
-  for (int i = threadIdx.x; i < (int)(sizeof(sh.named) / 4); i += kThreads + 32) sh.named[i] = 0;
+  for (int i = threadIdx.x; i < (int)(sizeof(sh.named) / 4); i += kBlock) sh.named[i] = 0;
   wait_for_previous();
   let_next_start();
   if (a.cluster > 1)
@@ -630,9 +747,11 @@ __global__ void __launch_bounds__(kThreads + 32, MODE != GRADIENT && K == kMostU
     __syncthreads();
   const uint32_t rank = a.cluster > 1 ? tc::cluster_rank() : 0;
   const int64_t first = blockIdx.x / a.cluster, step = gridDim.x / a.cluster;
-  if (threadIdx.x >= kThreads)
-    feed<DISTILL, T, MODE>(a, sh, stages, rank, first, step);
-  else
+  if (threadIdx.x == kThreads)
+    feed<T, MODE>(a, sh, stages, rank, first, step);
+  else if (threadIdx.x >= kThreads + 32)
+    prepare<DISTILL, T, MODE>(a, sh, stages, first, step);
+  else if (threadIdx.x < kThreads)
     work<DISTILL, T, K, MODE>(a, sh, stages, rank, first, step);
   __syncthreads();
   if (threadIdx.x == 0 && *(volatile uint32_t *)&sh.stop) {
@@ -679,11 +798,11 @@ cudaError_t resident(const void *fn, int cluster, int smem, int *clusters) {
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = (unsigned)cluster, at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(cluster * 1024)), cfg.blockDim = dim3(kThreads + 32);
+    cfg.gridDim = dim3((unsigned)(cluster * 1024)), cfg.blockDim = dim3(kBlock);
     cfg.dynamicSmemBytes = (size_t)smem, cfg.attrs = &at, cfg.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(&most, fn, &cfg);
   } else {
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&most, fn, kThreads + 32, (size_t)smem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&most, fn, kBlock, (size_t)smem);
     most *= device_sms();
   }
   if (e != cudaSuccess) return e;
@@ -735,7 +854,7 @@ cudaError_t launch_rows(Args &a, cudaStream_t s) {
   a.wait_limit_ns = wait_limit_ns(), a.fault = wait_fault();
   const int64_t grid = std::min<int64_t>(a.items, clusters) * a.cluster;
   void *args[] = {&a};
-  return launch_kernel(fn, dim3((unsigned)grid), dim3(kThreads + 32), args, (size_t)smem, s, true, a.cluster);
+  return launch_kernel(fn, dim3((unsigned)grid), dim3(kBlock), args, (size_t)smem, s, true, a.cluster);
 }
 
 template <bool DISTILL, class T>
