@@ -34,12 +34,16 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32, kBlock = kThreads + 64, kMaxTop = FSDP_DISTILL_MAX_TOP;
 constexpr int kMaxCluster = 8, kMaxStages = 4;
 constexpr int kMostUnits = 8;  // 16-byte units of a slice that a thread has
-constexpr int kMostSmem = 104 * 1024;  // stages, and what goes with a row: 2 x (32 + 16.1) or 4 x (8 + 16.1) KB at most
+constexpr int kMostSmem = 106 * 1024;  // stages, and what goes with rows: 2 x (32 + 16.1) KB at least
 constexpr int kNamed = 32768;
 constexpr int64_t kL2Rows = 40 << 20;  // bytes of rows that are read twice while L2 still has them
 constexpr float kLog2E = 1.4426950408889634f;
 
 enum Mode { STATS, HELD, TWICE, GRADIENT };
+// Blocks of an SM.  Gradients alone only stream, and want many blocks more than deep rings (4096 x 131072 BF16: three
+// blocks of two stages 319 us, two of three 369); rows that are read twice want two blocks of three stages (8192 x 32768 BF16:
+// 177 us, two stages 194, three blocks of half as long slices 188).
+constexpr int blocks_of_mode(Mode m) { return m == GRADIENT ? 3 : 2; }
 
 struct Args {
   const void *logits;
@@ -728,7 +732,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
 }
 
 template <bool DISTILL, class T, int K, Mode MODE>
-__global__ void __launch_bounds__(kBlock, MODE != GRADIENT && K == kMostUnits ? 2 : 3) row_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kBlock, K > 2 ? blocks_of_mode(MODE) : 3) row_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ Shared sh;
   if (threadIdx.x == 0) {
@@ -823,6 +827,7 @@ int64_t units_of(const Args &a) {
 
 template <bool DISTILL, class T, Mode MODE>
 cudaError_t launch_rows(Args &a, cudaStream_t s) {
+  constexpr int kBlocks = blocks_of_mode(MODE);
   constexpr int64_t kMost = kThreads * kMostUnits;
   const int64_t row_units = units_of<T>(a);
   a.cluster = a.rounds = a.slices = 1;
@@ -831,7 +836,7 @@ cudaError_t launch_rows(Args &a, cudaStream_t s) {
   } else if (MODE != HELD) {
     // Few rows: as many blocks to a row as keep the SMs busy, with 256 units each at least.  Rows that are read twice: as
     // many as it takes for all rows at work to stay in L2.
-    const int64_t blocks = 2 * device_sms();
+    const int64_t blocks = kBlocks * device_sms();
     int64_t want = std::min<int64_t>((blocks + a.rows - 1) / a.rows, row_units / kThreads);
     if (MODE == TWICE) want = std::max<int64_t>(want, (blocks * row_units * 16 + kL2Rows - 1) / kL2Rows);
     a.cluster = (int32_t)std::min<int64_t>(kMaxCluster, std::max<int64_t>(1, want));
@@ -844,7 +849,8 @@ cudaError_t launch_rows(Args &a, cudaStream_t s) {
   const void *fn = small ? kernel(&row_kernel<DISTILL, T, 2, MODE>) : kernel(&row_kernel<DISTILL, T, kMostUnits, MODE>);
   a.stage_bytes = (a.units * 16 + 127) / 128 * 128;
   a.side_bytes = ((int)sizeof(Side) + (DISTILL ? a.top * 16 : 0) + 127) / 128 * 128;
-  a.stages = small ? 4 : 2;
+  a.stages = kMaxStages;  // as many as leave room for the SM's other blocks
+  while (a.stages > 2 && a.stages * (a.stage_bytes + a.side_bytes) > (227 * 1024) / kBlocks - 6 * 1024) --a.stages;
   const int smem = a.stages * (a.stage_bytes + a.side_bytes);
   int clusters = 0;
   cudaError_t e = resident(fn, a.cluster, smem, &clusters);
