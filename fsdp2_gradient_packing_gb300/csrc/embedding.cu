@@ -18,6 +18,7 @@
 
 #include "layout.h"
 #include "ops.h"
+#include "tc.h"
 
 namespace fsdp {
 namespace embedding {
@@ -104,53 +105,62 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
 }
 
 // ---- sorting -----------------------------------------------------------------
-// A pass sorts by one digit of up to kMaxBits bits: each block counts its kTile items by
+// A pass sorts by one digit of up to kMaxBits bits: each block counts its tile's items by
 // digit, then places them behind what the counts of lower digits and earlier blocks say.
 // Within a block the order is that of the items: a warp takes consecutive ones, 32 at a
 // time, and ranks equal digits by lane, so a pass keeps the order of the one before.
-constexpr int kSortThreads = 512, kItems = 8, kTile = kSortThreads * kItems, kMaxBits = 10, kMaxBins = 1 << kMaxBits;
+constexpr int kSortThreads = 512, kItems = 8, kMaxBits = 10, kMaxBins = 1 << kMaxBits;
 constexpr int kSortWarps = kSortThreads / 32;
 
 struct SortArgs {
   const void *tokens;                        // first pass: the caller's; later passes: keys
-  const uint32_t *keys_in, *order_in;
-  uint32_t *keys, *order;
+  const uint2 *pairs_in;                     // tokens and their positions
+  uint2 *pairs;
+  uint32_t *crossing;                        // two counters that the last pass clears, or nullptr
   uint32_t *counts;                          // [blocks][bins] of this pass
   int64_t rows;
   uint32_t vocab, blocks;
   int32_t wide, bits, shift;
+  int32_t items;                             // of a thread: 1 .. kItems
 };
 
-__device__ __forceinline__ uint32_t sort_key(const SortArgs &a, int64_t i) {
-  return a.tokens ? token_at(a.tokens, i, a.wide != 0, a.vocab) : a.keys_in[i];
+// Item i: its token, and its position.
+__device__ __forceinline__ uint2 sort_item(const SortArgs &a, int64_t i) {
+  return a.tokens ? make_uint2(token_at(a.tokens, i, a.wide != 0, a.vocab), (uint32_t)i) : __ldcg(a.pairs_in + i);
 }
 
-__global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_constant__ SortArgs a) {
-  __shared__ uint32_t bin[kMaxBins];
+struct SortShared {
+  uint16_t seen[kSortWarps][kMaxBins];  // items of a digit in a warp, then in the warps before it
+  uint32_t base[kMaxBins];              // counts of a tile; then where the tile's items of a digit go
+  uint32_t total[kSortWarps];
+};
+
+// How many of a tile's items have each digit.
+__device__ __forceinline__ void count_tile(const SortArgs &a, SortShared &s, uint32_t tile) {
   const int bins = 1 << a.bits;
-  for (int d = threadIdx.x; d < bins; d += kSortThreads) bin[d] = 0;
-  wait_for_previous();
-  let_next_start();
+  for (int d = threadIdx.x; d < bins; d += kSortThreads) s.base[d] = 0;
   __syncthreads();
-  const int64_t first = (int64_t)blockIdx.x * kTile;
+  const int64_t first = (int64_t)tile * (a.items * kSortThreads);
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     const int64_t i = first + k * kSortThreads + threadIdx.x;
-    if (i < a.rows) atomicAdd(&bin[(sort_key(a, i) >> a.shift) & (bins - 1)], 1u);
+    if (k < a.items && i < a.rows) atomicAdd(&s.base[(sort_item(a, i).x >> a.shift) & (bins - 1)], 1u);
   }
   __syncthreads();
-  for (int d = threadIdx.x; d < bins; d += kSortThreads) a.counts[(int64_t)blockIdx.x * bins + d] = bin[d];
+  for (int d = threadIdx.x; d < bins; d += kSortThreads) a.counts[(int64_t)tile * bins + d] = s.base[d];
 }
 
-__global__ void __launch_bounds__(kSortThreads) place_kernel(const __grid_constant__ SortArgs a) {
-  __shared__ uint16_t seen[kSortWarps][kMaxBins];  // then: items of earlier warps
-  __shared__ uint32_t base[kMaxBins];              // where the block's items of a digit go
-  __shared__ uint32_t total[kSortWarps];
+// A tile's items to their places.
+__device__ __forceinline__ void place_tile(const SortArgs &a, SortShared &s, uint32_t tile) {
   const int bins = 1 << a.bits, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  for (int i = threadIdx.x; i < kSortWarps * kMaxBins / 2; i += kSortThreads) reinterpret_cast<uint32_t *>(seen)[i] = 0;
-  wait_for_previous();
-  let_next_start();
-  // Where each digit's items start: those of lower digits, then those of earlier blocks.  A
+  for (int i = threadIdx.x; i < kSortWarps * kMaxBins / 2; i += kSortThreads) reinterpret_cast<uint32_t *>(s.seen)[i] = 0;
+  const int64_t first = (int64_t)tile * (a.items * kSortThreads) + warp * (32 * a.items) + lane;
+  const int n = (int)min((int64_t)a.items, (a.rows - first + 31) / 32);  // of this thread
+  uint2 item[kItems];
+  uint32_t rank[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) item[k] = k < n ? sort_item(a, first + k * 32) : make_uint2(0, 0);
+  // Where each digit's items start: behind those of lower digits and those of earlier tiles.  A
   // thread sums two neighbouring digits (bins are at least 2).
   uint32_t before[2] = {0, 0}, all[2] = {0, 0};
   const int d = threadIdx.x * 2;
@@ -158,9 +168,9 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const __grid_consta
     const uint2 *p = reinterpret_cast<const uint2 *>(a.counts + d);
 #pragma unroll 8
     for (uint32_t b = 0; b < a.blocks; ++b) {
-      const uint2 c = p[(int64_t)b * (bins / 2)];
+      const uint2 c = __ldcg(p + (int64_t)b * (bins / 2));
       all[0] += c.x, all[1] += c.y;
-      if (b < blockIdx.x) before[0] += c.x, before[1] += c.y;
+      if (b < tile) before[0] += c.x, before[1] += c.y;
     }
   }
   uint32_t run = all[0] + all[1];
@@ -169,35 +179,28 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const __grid_consta
     const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, run, m);
     if (lane >= m) run += up;
   }
-  if (lane == 31) total[warp] = run;
+  if (lane == 31) s.total[warp] = run;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) run += total[w];
+  for (int w = 0; w < warp; ++w) run += s.total[w];
   if (d < bins) {
-    base[d] = run - all[0] - all[1] + before[0];
-    base[d + 1] = run - all[1] + before[1];
+    s.base[d] = run - all[0] - all[1] + before[0];
+    s.base[d + 1] = run - all[1] + before[1];
   }
   // Ranks within the warp's items of the same digit.
-  const int64_t first = (int64_t)blockIdx.x * kTile + warp * (32 * kItems) + lane;
-  uint32_t key[kItems], from[kItems], rank[kItems];
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    const int64_t i = first + k * 32;
-    key[k] = i < a.rows ? sort_key(a, i) : 0;
-    from[k] = i < a.rows && !a.tokens ? a.order_in[i] : (uint32_t)i;
-  }
-#pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    const bool here = first + k * 32 < a.rows;
-    const uint32_t digit = (key[k] >> a.shift) & (bins - 1);
+    if (k >= a.items) break;
+    const bool here = k < n;
+    const uint32_t digit = (item[k].x >> a.shift) & (bins - 1);
     uint32_t same = __ballot_sync(0xFFFFFFFFu, here);
     for (int b = 0; b < a.bits; ++b) {
       const uint32_t ones = __ballot_sync(0xFFFFFFFFu, digit >> b & 1);
       same &= digit >> b & 1 ? ones : ~ones;
     }
     const uint32_t earlier = same & ((1u << lane) - 1);
-    rank[k] = here ? seen[warp][digit] + __popc(earlier) : 0;
+    rank[k] = here ? s.seen[warp][digit] + __popc(earlier) : 0;
     __syncwarp();
-    if (here && !earlier) seen[warp][digit] = (uint16_t)(rank[k] + __popc(same));
+    if (here && !earlier) s.seen[warp][digit] = (uint16_t)(rank[k] + __popc(same));
     __syncwarp();
   }
   __syncthreads();
@@ -205,24 +208,111 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const __grid_consta
     uint32_t sum = 0;
 #pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
-      const uint32_t n = seen[w][b];
-      seen[w][b] = (uint16_t)sum;
+      const uint32_t n = s.seen[w][b];
+      s.seen[w][b] = (uint16_t)sum;
       sum += n;
     }
   }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    if (first + k * 32 >= a.rows) break;
-    const uint32_t digit = (key[k] >> a.shift) & (bins - 1), at = base[digit] + seen[warp][digit] + rank[k];
-    a.keys[at] = key[k];
-    a.order[at] = from[k];
+    if (k >= n) break;
+    const uint32_t digit = (item[k].x >> a.shift) & (bins - 1);
+    a.pairs[s.base[digit] + s.seen[warp][digit] + rank[k]] = item[k];
+  }
+  if (a.crossing && tile == 0 && threadIdx.x < 2) a.crossing[threadIdx.x] = 0;
+}
+
+__global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_constant__ SortArgs a) {
+  __shared__ SortShared s;
+  wait_for_previous();
+  let_next_start();
+  count_tile(a, s, blockIdx.x);
+}
+__global__ void __launch_bounds__(kSortThreads) place_kernel(const __grid_constant__ SortArgs a) {
+  __shared__ SortShared s;
+  wait_for_previous();
+  let_next_start();
+  place_tile(a, s, blockIdx.x);
+}
+
+// Zeros to a row, by a warp: whole 16-byte units, and what lies before and behind them one by one.
+template <class T>
+__device__ __forceinline__ void clear_row(T *g, int64_t cols) {
+  constexpr int E = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31;
+  const int64_t head = min(cols, (int64_t)((16 - ((uintptr_t)g & 15)) & 15) / (int64_t)sizeof(T)), units = (cols - head) / E;
+  if (lane < head) g[lane] = to<T>(0.0f);
+#pragma unroll 4
+  for (int64_t u = lane; u < units; u += 32) *reinterpret_cast<uint4 *>(g + head + u * E) = make_uint4(0, 0, 0, 0);
+  const int64_t tail = head + units * E + lane;
+  if (tail < cols) g[tail] = to<T>(0.0f);
+}
+
+// Few tokens, up to a cluster's kMaxCluster tiles: all passes of the sort in one launch, by the first cluster.  The
+// others meanwhile clear the rows of the gradient that no token has, each block its share: it looks through all
+// tokens for its own rows, which takes a small part of what the zeros take.
+constexpr int kMaxCluster = 8;
+struct ShortArgs {
+  SortArgs pass[4];
+  const void *tokens;
+  void *grad;          // nullptr: nothing to clear
+  int64_t cols, ld_grad, share;  // rows of a clearing block
+  int32_t passes, grad_bf16;
+};
+template <class T>
+__device__ __forceinline__ void clear_share(const ShortArgs &a, uint32_t *seen, int64_t begin) {
+  const SortArgs &q = a.pass[0];
+  const int64_t last = min(begin + a.share, (int64_t)q.vocab);
+  constexpr int64_t kRows = kMaxBins * 32;  // rows that a block looks for at once
+  for (int64_t lo = begin; lo < last; lo += kRows) {
+    const int64_t hi = min(lo + kRows, last);
+    for (int i = threadIdx.x; i < kMaxBins; i += kSortThreads) seen[i] = 0;
+    __syncthreads();
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < q.rows; i += kSortThreads) {
+      const int64_t t = token_at(a.tokens, i, q.wide != 0, q.vocab) - lo;
+      if (t >= 0 && t < hi - lo) atomicOr(&seen[t / 32], 1u << (t & 31));
+    }
+    __syncthreads();
+    for (int64_t r = lo + threadIdx.x / 32; r < hi; r += kSortWarps)
+      if (!(seen[(r - lo) / 32] >> ((r - lo) & 31) & 1)) clear_row(static_cast<T *>(a.grad) + r * a.ld_grad, a.cols);
+    __syncthreads();
+  }
+}
+__global__ void __launch_bounds__(kSortThreads) short_kernel(const __grid_constant__ ShortArgs a) {
+  __shared__ SortShared s;
+  wait_for_previous();
+  let_next_start();
+  const uint32_t blocks = a.pass[0].blocks;
+  if (blockIdx.x < blocks) {
+    for (int p = 0; p < a.passes; ++p) {
+      count_tile(a.pass[p], s, blockIdx.x);
+      if (blocks > 1)
+        tc::cluster_sync();
+      else
+        __syncthreads();
+      place_tile(a.pass[p], s, blockIdx.x);
+      if (blocks > 1)
+        tc::cluster_sync();
+      else
+        __syncthreads();
+    }
+  } else {
+    const int64_t begin = (int64_t)(blockIdx.x - blocks) * a.share;
+    if (a.grad_bf16)
+      clear_share<__nv_bfloat16>(a, s.base, begin);
+    else
+      clear_share<float>(a, s.base, begin);
   }
 }
 
 // ---- sums --------------------------------------------------------------------
 struct SumArgs {
-  const uint32_t *keys, *order;
+  const uint2 *pairs;     // sorted tokens and their positions
+  // Tokens that go on behind the piece where they begin: how many lie in few and in many pieces; then those
+  // pieces, the few from the front and the many from the back.
+  uint32_t *crossing;
   const void *dout;
   void *grad;
   float *parts;     // [pieces][2][cols]: what a piece has of a token that began before it, and of one that goes on
@@ -235,13 +325,13 @@ struct SumArgs {
   float scale;
 };
 
-constexpr int kBatch = 8;  // rows of loads in flight
+// Rows of loads at a time, two of them in flight: as many as registers hold.
+template <class TD, bool VEC>
+constexpr int kBatch = VEC && sizeof(TD) == 2 ? 8 : 4;
 
-// Eight columns of a lane (VEC: consecutive, 256 columns to a warp), or two 32 apart.
-template <bool VEC>
-struct Strip {
-  static constexpr int kCols = VEC ? 256 : 64;
-};
+// A warp's strip: 256 columns, of which a lane has eight, consecutive (VEC) or 32 apart.
+constexpr int kStrip = 256;
+constexpr int kManyPieces = 8;  // behind the one where a token begins
 
 template <class TD, bool VEC>
 struct Loaded;
@@ -272,12 +362,15 @@ struct Loaded<float, true> {
 };
 template <class TD>
 struct Loaded<TD, false> {
-  float v[2];
+  TD v[8];
   __device__ void load(const TD *p, int64_t j, int64_t cols) {
-    v[0] = j < cols ? (float)p[j] : 0.0f;
-    v[1] = j + 32 < cols ? (float)p[j + 32] : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = j + e * 32 < cols ? p[j + e * 32] : (TD)0.0f;
   }
-  __device__ void add_to(float2 (&s)[4]) const { s[0].x += v[0], s[0].y += v[1]; }
+  __device__ void add_to(float2 (&s)[4]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) element(s, e) += (float)v[e];
+  }
 };
 
 // The sum of a token's rows into its row of the gradient.
@@ -297,12 +390,12 @@ __device__ __forceinline__ void write_row(const SumArgs &a, uint32_t token, int6
     }
     store8(g, j, sizeof(TG) == 2, v);
   } else {
+    TG old[8];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int64_t c = j + e * 32;
-      const float s = e ? sum[0].y : sum[0].x;
-      if (c < a.cols) g[c] = to<TG>(a.add ? fmaf(s, a.scale, (float)g[c]) : s * a.scale);
-    }
+    for (int e = 0; e < 8; ++e) old[e] = a.add && j + e * 32 < a.cols ? g[j + e * 32] : (TG)0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (j + e * 32 < a.cols) g[j + e * 32] = to<TG>(fmaf(element(sum, e), a.scale, (float)old[e]));
   }
 }
 template <bool VEC>
@@ -315,101 +408,115 @@ __device__ __forceinline__ void write_part(const SumArgs &a, int64_t piece, int 
   if constexpr (VEC) {
     if (j < a.cols) store8(p, j, false, sum);
   } else {
-    if (j < a.cols) p[j] = sum[0].x;
-    if (j + 32 < a.cols) p[j + 32] = sum[0].y;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (j + e * 32 < a.cols) p[j + e * 32] = element(sum, e);
   }
 }
 
 template <class TD, class TG, bool VEC>
-__global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ SumArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sum_kernel(const __grid_constant__ SumArgs a) {
+  constexpr int N = kBatch<TD, VEC>;
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
   wait_for_previous();
   let_next_start();
   const int64_t piece = unit / a.strips;
   if (piece >= a.pieces) return;
-  const int64_t j = (unit - piece * a.strips) * Strip<VEC>::kCols + lane * (VEC ? 8 : 1);
+  const int64_t j = (unit - piece * a.strips) * kStrip + lane * (VEC ? 8 : 1);
   const int64_t first = piece * a.length, end = min(first + a.length, a.rows);
-  // The first token of the piece began before it; the last one goes on behind it.
-  const uint32_t ahead = first > 0 ? a.keys[first - 1] : 0xFFFFFFFFu, behind = end < a.rows ? a.keys[end] : 0xFFFFFFFFu;
+  // The first token of the piece may have begun before it; the last one may go on behind it.
+  const uint32_t ahead = first > 0 ? a.pairs[first - 1].x : 0xFFFFFFFFu, behind = end < a.rows ? a.pairs[end].x : 0xFFFFFFFFu;
   float2 sum[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) sum[e] = both(0.0f);
-  bool began = ahead == a.keys[first];
-  uint32_t token = a.keys[first];
-  for (int64_t at = first; at < end; at += kBatch) {
-    // 32 keys and positions could be read at once; lanes 0 .. kBatch - 1 hold a batch's.
-    const int64_t mine = at + (lane & (kBatch - 1));
-    const uint32_t key = mine < end ? a.keys[mine] : a.vocab, from = mine < end ? a.order[mine] : 0;
-    Loaded<TD, VEC> r[kBatch];
+  uint32_t token = a.pairs[first].x;
+  bool began = ahead == token;
+  for (int64_t at = first; at < end; at += 32) {
+    // 32 keys and positions, one a lane; padding (keys of vocab) sorts last.
+    const uint2 pair = at + lane < end ? a.pairs[at + lane] : make_uint2(a.vocab, 0);
+    const uint32_t key = pair.x, from = pair.y;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, key < a.vocab));  // rows to sum
+    Loaded<TD, VEC> r[2][N];
+    auto load = [&](int k0, Loaded<TD, VEC> (&to)[N]) {
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const uint32_t row = __shfl_sync(0xFFFFFFFFu, from, k), t = __shfl_sync(0xFFFFFFFFu, key, k);
-      if (at + k < end && t < a.vocab) r[k].load(static_cast<const TD *>(a.dout) + (int64_t)row * a.ld_dout, j, a.cols);
-    }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const uint32_t t = __shfl_sync(0xFFFFFFFFu, key, k);
-      if (at + k >= end) break;
-      if (t != token) {
-        if (began)
-          write_part<VEC>(a, piece, 0, j, sum);
-        else
-          write_row<TG, VEC>(a, token, j, sum);
-        began = false;
-        token = t;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum[e] = both(0.0f);
+      for (int k = 0; k < N; ++k) {
+        const uint32_t row = __shfl_sync(0xFFFFFFFFu, from, (k0 + k) & 31);
+        if (k0 + k < n) to[k].load(static_cast<const TD *>(a.dout) + (int64_t)row * a.ld_dout, j, a.cols);
       }
-      if (t >= a.vocab) return;  // padding sorts last
-      r[k].add_to(sum);
+    };
+    load(0, r[0]);
+#pragma unroll
+    for (int b = 0; b < 32 / N; ++b) {
+      if (b * N >= n) break;
+      if (b + 1 < 32 / N) load((b + 1) * N, r[(b + 1) & 1]);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const uint32_t t = __shfl_sync(0xFFFFFFFFu, key, b * N + k);
+        if (b * N + k >= n) break;
+        if (t != token) {
+          if (began)
+            write_part<VEC>(a, piece, 0, j, sum);
+          else
+            write_row<TG, VEC>(a, token, j, sum);
+          began = false;
+          token = t;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] = both(0.0f);
+        }
+        r[b & 1][k].add_to(sum);
+      }
     }
   }
-  if (began)
+  if (token >= a.vocab) return;  // nothing but padding
+  if (began) {
     write_part<VEC>(a, piece, 0, j, sum);
-  else if (token == behind)
+  } else if (token == behind) {
     write_part<VEC>(a, piece, 1, j, sum);
-  else
+    if (unit == piece * a.strips && lane == 0) {
+      const int64_t far = end + kManyPieces * (int64_t)a.length;
+      const bool many = far < a.rows && a.pairs[far].x == token;
+      const uint32_t n = atomicAdd(a.crossing + many, 1u);
+      a.crossing[many ? 1 + a.pieces - n : 2 + n] = (uint32_t)piece;
+    }
+  } else {
     write_row<TG, VEC>(a, token, j, sum);
+  }
+}
+
+// By a warp: the first index whose key is not below k.  Each round takes 32 probes, so 16,384 keys take three.
+__device__ __forceinline__ int64_t warp_lower_bound(const uint2 *keys, int64_t n, uint32_t k) {
+  const int lane = threadIdx.x & 31;
+  int64_t lo = 0;  // keys before lo are below k, those from lo + n on are not
+  while (n > 0) {
+    const int64_t step = (n + 32) / 33, at = lo + (lane + 1) * step - 1;
+    const uint32_t below = __ballot_sync(0xFFFFFFFFu, at < lo + n && keys[at].x < k);
+    const int c = __popc(below);  // probes 0 .. c - 1 are below
+    const int64_t from = lo + c * step, to = c < 32 ? min(lo + (c + 1) * step - 1, lo + n) : lo + n;
+    lo = from, n = max((int64_t)0, to - from);
+  }
+  return lo;
 }
 
 // First index whose key is not below k.
-__device__ __forceinline__ int64_t lower_bound(const uint32_t *keys, int64_t n, uint32_t k) {
+__device__ __forceinline__ int64_t lower_bound(const uint2 *keys, int64_t n, uint32_t k) {
   int64_t lo = 0;
   while (n > 0) {
     const int64_t half = n / 2;
-    const bool right = keys[lo + half] < k;
+    const bool right = keys[lo + half].x < k;
     lo = right ? lo + half + 1 : lo;
     n = right ? n - half - 1 : half;
   }
   return lo;
 }
 
-// Tokens whose rows fill more than one piece: a block to the piece where one starts and a
-// strip of columns; its warps share out the pieces and meet in order.
-template <class TG, bool VEC>
-__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ SumArgs a) {
-  __shared__ float2 met[kThreads / 32][32][4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  wait_for_previous();
-  let_next_start();
-  const int64_t piece = blockIdx.x / a.strips, strip = blockIdx.x - piece * a.strips;
-  const int64_t first = piece * a.length, end = first + a.length;
-  if (end >= a.rows) return;
-  const uint32_t token = a.keys[end - 1];
-  if (token >= a.vocab || a.keys[end] != token) return;              // nothing goes on
-  if (a.keys[first] == token && first > 0 && a.keys[first - 1] == token) return;  // it began before this piece
-  const int64_t last = (lower_bound(a.keys + end, a.rows - end, token + 1) + end - 1) / a.length;
-  const int64_t j = strip * Strip<VEC>::kCols + lane * (VEC ? 8 : 1);
-  float2 sum[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) sum[e] = both(0.0f);
-  // Piece `piece` gives its second part, pieces up to `last` their first.
-  const int64_t n = last - piece + 1, share = (n + kThreads / 32 - 1) / (kThreads / 32);
-  const int64_t from = piece + warp * share, to_ = min(from + share, last + 1);
+// Tokens whose rows lie in more than one piece (in any order: each has its own row).  A warp to a token of few pieces
+// and a strip; a block to one of many, whose warps share out the pieces and meet in order.
+template <bool VEC>
+__device__ __forceinline__ void add_parts(const SumArgs &a, int64_t piece, int64_t from, int64_t to_, int64_t j, float2 (&sum)[4]) {
 #pragma unroll 4
   for (int64_t p = from; p < to_; ++p) {
-    const float *q = part_of<VEC>(a, p, p == piece);
+    const float *q = part_of<VEC>(a, p, p == piece);  // the piece where the token begins gives its second part
     if constexpr (VEC) {
       if (j < a.cols) {
         float2 v[4];
@@ -418,49 +525,77 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
         for (int e = 0; e < 4; ++e) sum[e] = __fadd2_rn(sum[e], v[e]);
       }
     } else {
-      if (j < a.cols) sum[0].x += q[j];
-      if (j + 32 < a.cols) sum[0].y += q[j + 32];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j + e * 32 < a.cols) element(sum, e) += q[j + e * 32];
     }
   }
+}
+template <class TG, bool VEC>
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ SumArgs a) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float2 met[kWarps][32][4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  wait_for_previous();
+  let_next_start();
+  const int64_t few = (int64_t)a.crossing[0] * a.strips, many = (int64_t)a.crossing[1] * a.strips;
+  float2 sum[4];
+  for (int64_t unit = (int64_t)blockIdx.x * kWarps + warp; unit < few; unit += (int64_t)gridDim.x * kWarps) {
+    const int64_t at = unit / a.strips, j = (unit - at * a.strips) * kStrip + lane * (VEC ? 8 : 1), piece = a.crossing[2 + at];
+    const uint32_t token = a.pairs[(piece + 1) * a.length].x;
+    // Where it goes on: lane k looks at piece k behind its first.
+    const int64_t next = (piece + 1 + lane) * a.length;
+    const int64_t last = piece + __popc(__ballot_sync(0xFFFFFFFFu, lane <= kManyPieces && next < a.rows && a.pairs[min(next, a.rows - 1)].x == token));
 #pragma unroll
-  for (int e = 0; e < 4; ++e) met[warp][lane][e] = sum[e];
-  __syncthreads();
-  if (warp > 0) return;
-  for (int w = 1; w < kThreads / 32; ++w) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] = __fadd2_rn(sum[e], met[w][lane][e]);
+    for (int e = 0; e < 4; ++e) sum[e] = both(0.0f);
+    add_parts<VEC>(a, piece, piece, last + 1, j, sum);
+    write_row<TG, VEC>(a, token, j, sum);
   }
-  write_row<TG, VEC>(a, token, j, sum);
+  for (int64_t unit = blockIdx.x; unit < many; unit += gridDim.x) {
+    const int64_t at = unit / a.strips, j = (unit - at * a.strips) * kStrip + lane * (VEC ? 8 : 1), piece = a.crossing[1 + a.pieces - at];
+    const int64_t end = (piece + 1) * a.length;
+    const uint32_t token = a.pairs[end].x;
+    const int64_t last = (warp_lower_bound(a.pairs + end, a.rows - end, token + 1) + end - 1) / a.length;  // the piece of its last row
+    const int64_t share = (last - piece + kWarps) / kWarps, from = piece + warp * share;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = both(0.0f);
+    add_parts<VEC>(a, piece, from, min(from + share, last + 1), j, sum);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) met[warp][lane][e] = sum[e];
+    __syncthreads();
+    if (warp == 0) {
+      for (int w = 1; w < kWarps; ++w) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] = __fadd2_rn(sum[e], met[w][lane][e]);
+      }
+      write_row<TG, VEC>(a, token, j, sum);
+    }
+    __syncthreads();
+  }
 }
 
-// Rows of the gradient that no token has: zeros.  A block looks for kThreads rows in the
-// sorted tokens, one a thread, and writes those that are missing.
+// Many tokens: rows of the gradient that no token has, zeros.  A block looks for kThreads rows in the part of the sorted
+// tokens that has them, one a thread, and writes those that are missing.
 template <class TG>
 __global__ void __launch_bounds__(kThreads) clear_kernel(const __grid_constant__ SumArgs a) {
   __shared__ uint32_t missing[kThreads];
+  __shared__ int64_t bound[2];
   __shared__ int32_t n;
   if (threadIdx.x == 0) n = 0;
   wait_for_previous();
   let_next_start();
+  const int64_t first = (int64_t)blockIdx.x * kThreads, v = first + threadIdx.x;
+  if (threadIdx.x < 64) {
+    const int64_t at = warp_lower_bound(a.pairs, a.rows, (uint32_t)min(first + threadIdx.x / 32 * kThreads, (int64_t)a.vocab));
+    if (threadIdx.x % 32 == 0) bound[threadIdx.x / 32] = at;
+  }
   __syncthreads();
-  const int64_t v = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (v < a.vocab) {
-    const int64_t at = lower_bound(a.keys, a.rows, (uint32_t)v);
-    if (at >= a.rows || a.keys[at] != (uint32_t)v) missing[atomicAdd(&n, 1)] = (uint32_t)v;
+    const int64_t at = bound[0] + lower_bound(a.pairs + bound[0], bound[1] - bound[0], (uint32_t)v);
+    if (at >= bound[1] || a.pairs[at].x != (uint32_t)v) missing[atomicAdd(&n, 1)] = (uint32_t)v;
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31;
-  for (int r = threadIdx.x / 32; r < n; r += kThreads / 32) {
-    TG *g = static_cast<TG *>(a.grad) + (int64_t)missing[r] * a.ld_grad;
-    // Whole 16-byte units, and what lies before and behind them one by one.
-    constexpr int E = 16 / sizeof(TG);
-    const int64_t head = min(a.cols, (int64_t)((16 - ((uintptr_t)g & 15)) & 15) / (int64_t)sizeof(TG));
-    const int64_t units = (a.cols - head) / E;
-    if (lane < head) g[lane] = to<TG>(0.0f);
-    for (int64_t u = lane; u < units; u += 32) *reinterpret_cast<uint4 *>(g + head + u * E) = make_uint4(0, 0, 0, 0);
-    const int64_t tail = head + units * E + lane;
-    if (tail < a.cols) g[tail] = to<TG>(0.0f);
-  }
+  for (int r = threadIdx.x / 32; r < n; r += kThreads / 32) clear_row(static_cast<TG *>(a.grad) + (int64_t)missing[r] * a.ld_grad, a.cols);
 }
 
 // ---- host --------------------------------------------------------------------
@@ -490,14 +625,16 @@ bool rows_aligned(const void *p, int64_t rows, int64_t ld, int64_t size) {
 // How the gradient's work is cut, from the sizes alone.
 struct Cut {
   int64_t blocks, pieces, padded_cols;
-  int32_t length, passes, bits;
-  int64_t keys[2], order[2], counts, parts, bytes;  // offsets in the workspace
+  int32_t length, passes, bits, items;
+  int64_t pairs[2], counts, crossing, parts, bytes;  // offsets in the workspace
 };
 
 Cut cut_of(const fsdp_embedding_desc_t &d) {
   Cut c = {};
   c.padded_cols = (d.cols + 7) / 8 * 8;
-  c.blocks = (d.rows + kTile - 1) / kTile;
+  // Tiles as small as a cluster's blocks allow, so that all of them have work.
+  c.items = (int32_t)std::min<int64_t>(kItems, std::max<int64_t>(1, (d.rows + kMaxCluster * kSortThreads - 1) / (kMaxCluster * kSortThreads)));
+  c.blocks = (d.rows + c.items * kSortThreads - 1) / (c.items * kSortThreads);
   int bits = 1;
   while ((d.vocab >> bits) != 0) ++bits;  // keys are 0 .. vocab
   c.passes = (bits + kMaxBits - 1) / kMaxBits;
@@ -512,8 +649,9 @@ Cut cut_of(const fsdp_embedding_desc_t &d) {
     c.bytes += (bytes + 15) / 16 * 16;
     return at;
   };
-  for (int k = 0; k < 2; ++k) c.keys[k] = take(d.rows * 4), c.order[k] = take(d.rows * 4);
+  for (int k = 0; k < 2; ++k) c.pairs[k] = take(d.rows * 8);
   c.counts = take(c.blocks * (4ll << c.bits));
+  c.crossing = take(d.rows > 0 ? c.pieces * 4 + 8 : 0);
   c.parts = take(c.pieces * 2 * c.padded_cols * 4);
   return c;
 }
@@ -525,11 +663,12 @@ const void *kernel(K *k) {
 
 template <class TD, class TG, bool VEC>
 fsdp_status_t sums(SumArgs a, cudaStream_t s) {
-  a.strips = (a.cols + Strip<VEC>::kCols - 1) / Strip<VEC>::kCols;
+  a.strips = (a.cols + kStrip - 1) / kStrip;
   void *args[] = {&a};
   const int64_t warps = kThreads / 32, units = a.pieces * a.strips;
-  const int64_t grid = (units + warps - 1) / warps, joins = (a.pieces - 1) * a.strips;
-  if (grid > INT32_MAX || joins > INT32_MAX) return fail(FSDP_EUNSUPPORTED, "the gradient is too large for one launch");
+  const int64_t grid = (units + warps - 1) / warps;
+  const int64_t joins = std::min<int64_t>((a.pieces - 1) * a.strips, (int64_t)device_sms() * 8);
+  if (grid > INT32_MAX) return fail(FSDP_EUNSUPPORTED, "the gradient is too large for one launch");
   fsdp_status_t st = launched(launch_kernel(kernel(&sum_kernel<TD, TG, VEC>), dim3((unsigned)grid), dim3(kThreads), args, 0, s, true));
   if (st == FSDP_OK && joins > 0)
     st = launched(launch_kernel(kernel(&join_kernel<TG, VEC>), dim3((unsigned)joins), dim3(kThreads), args, 0, s, true));
@@ -609,26 +748,50 @@ fsdp_status_t fsdp_embedding_backward(const fsdp_embedding_desc_t *desc, const v
   SortArgs q = {};
   q.rows = d.rows, q.vocab = (uint32_t)d.vocab, q.blocks = (uint32_t)c.blocks;
   q.wide = d.token_dtype == FSDP_INDEX_I64, q.bits = c.bits, q.counts = d.rows > 0 ? words(c.counts) : nullptr;
-  for (int p = 0; p < c.passes && d.rows > 0; ++p) {
-    q.tokens = p == 0 ? tokens : nullptr;
-    q.keys_in = words(c.keys[(p + 1) & 1]), q.order_in = words(c.order[(p + 1) & 1]);
-    q.keys = words(c.keys[p & 1]), q.order = words(c.order[p & 1]);
-    q.shift = p * c.bits;
-    void *args[] = {&q};
+  const bool gb = d.weight_dtype == FSDP_DTYPE_BF16, db = d.out_dtype == FSDP_DTYPE_BF16;
+  auto pass_of = [&](int p) {
+    SortArgs r = q;
+    r.tokens = p == 0 ? tokens : nullptr;
+    r.pairs_in = reinterpret_cast<const uint2 *>(w + c.pairs[(p + 1) & 1]);
+    r.pairs = reinterpret_cast<uint2 *>(w + c.pairs[p & 1]);
+    r.shift = p * c.bits, r.items = c.items;
+    if (p == c.passes - 1) r.crossing = words(c.crossing);
+    return r;
+  };
+  const bool few = c.blocks <= kMaxCluster;
+  if (few && (d.rows > 0 || !d.accumulate)) {
+    ShortArgs r = {};
+    for (int p = 0; p < c.passes; ++p) r.pass[p] = pass_of(p);
+    r.passes = c.passes, r.tokens = tokens, r.cols = d.cols, r.ld_grad = d.ld_weight, r.grad_bf16 = gb;
+    const int cluster = std::max<int>(1, (int)c.blocks);
+    int64_t clearing = 0;
+    if (!d.accumulate) {
+      // As many clearing blocks as fill the SMs beside the sort (two fit an SM), of 16 rows at least.
+      r.grad = dweight;
+      clearing = std::max<int64_t>(1, std::min<int64_t>((int64_t)device_sms() * 2 - c.blocks, (d.vocab + 15) / 16));
+      clearing = (clearing + cluster - 1) / cluster * cluster;
+      r.share = (d.vocab + clearing - 1) / clearing;
+    }
+    void *args[] = {&r};
+    st = launched(launch_kernel(kernel(&short_kernel), dim3((unsigned)(c.blocks + clearing)), dim3(kSortThreads), args, 0, s, true, cluster));
+    if (st != FSDP_OK) return st;
+  }
+  for (int p = 0; p < c.passes && !few; ++p) {
+    SortArgs r = pass_of(p);
+    void *args[] = {&r};
     for (const void *fn : {kernel(&count_kernel), kernel(&place_kernel)}) {
       st = launched(launch_kernel(fn, dim3((unsigned)c.blocks), dim3(kSortThreads), args, 0, s, true));
       if (st != FSDP_OK) return st;
     }
   }
   SumArgs a = {};
-  if (d.rows > 0) a.keys = words(c.keys[(c.passes - 1) & 1]), a.order = words(c.order[(c.passes - 1) & 1]);
+  a.pairs = reinterpret_cast<const uint2 *>(w + c.pairs[(c.passes - 1) & 1]), a.crossing = words(c.crossing);
   a.dout = dout, a.grad = dweight;
   a.parts = reinterpret_cast<float *>(w + c.parts);
   a.rows = d.rows, a.cols = d.cols, a.ld_dout = d.ld_out, a.ld_grad = d.ld_weight;
   a.pieces = c.pieces, a.length = c.length;
   a.vocab = (uint32_t)d.vocab, a.add = d.accumulate, a.scale = d.scale;
-  const bool gb = d.weight_dtype == FSDP_DTYPE_BF16, db = d.out_dtype == FSDP_DTYPE_BF16;
-  if (!d.accumulate) {
+  if (!d.accumulate && !few) {
     void *args[] = {&a};
     st = launched(launch_kernel(gb ? kernel(&clear_kernel<__nv_bfloat16>) : kernel(&clear_kernel<float>),
                                 dim3((unsigned)((d.vocab + kThreads - 1) / kThreads)), dim3(kThreads), args, 0, s, true));
