@@ -250,33 +250,52 @@ __device__ __forceinline__ void clear_row(T *g, int64_t cols) {
 }
 
 // Few tokens, up to a cluster's kMaxCluster tiles: all passes of the sort in one launch, by the first cluster.  The
-// others meanwhile clear the rows of the gradient that no token has, each block its share: it looks through all
-// tokens for its own rows, which takes a small part of what the zeros take.
-constexpr int kMaxCluster = 8;
+// others meanwhile clear the rows of the gradient that no token has, each its share: a cluster's blocks look
+// through a part of the tokens each for the rows of all of them.
+constexpr int kMaxCluster = 8, kClearBytes = 100 << 20;
 struct ShortArgs {
   SortArgs pass[4];
   const void *tokens;
   void *grad;          // nullptr: nothing to clear
-  int64_t cols, ld_grad, share;  // rows of a clearing block
+  int64_t cols, ld_grad, share, clear_to;  // rows of a clearing cluster; the first row that is not cleared here
   int32_t passes, grad_bf16;
 };
 template <class T>
-__device__ __forceinline__ void clear_share(const ShortArgs &a, uint32_t *seen, int64_t begin) {
+__device__ __forceinline__ void clear_share(const ShortArgs &a, SortShared &s, int64_t begin, uint32_t blocks) {
   const SortArgs &q = a.pass[0];
-  const int64_t last = min(begin + a.share, (int64_t)q.vocab);
-  constexpr int64_t kRows = kMaxBins * 32;  // rows that a block looks for at once
+  const uint32_t rank = blocks > 1 ? tc::cluster_rank() : 0;
+  uint32_t *mine = s.base, *all = reinterpret_cast<uint32_t *>(s.seen);  // rows that this block's part of the tokens has, and all have
+  const int64_t last = min(begin + a.share, a.clear_to);
+  constexpr int64_t kRows = kMaxBins * 32;  // rows that are looked for at once
+  auto sync = [&] {
+    if (blocks > 1)
+      tc::cluster_sync();
+    else
+      __syncthreads();
+  };
   for (int64_t lo = begin; lo < last; lo += kRows) {
     const int64_t hi = min(lo + kRows, last);
-    for (int i = threadIdx.x; i < kMaxBins; i += kSortThreads) seen[i] = 0;
+    const int words = (int)(hi - lo + 31) / 32;
+    for (int i = threadIdx.x; i < words; i += kSortThreads) mine[i] = 0;
     __syncthreads();
-#pragma unroll 8
-    for (int64_t i = threadIdx.x; i < q.rows; i += kSortThreads) {
+#pragma unroll 4
+    for (int64_t i = (int64_t)rank * kSortThreads + threadIdx.x; i < q.rows; i += (int64_t)blocks * kSortThreads) {
       const int64_t t = token_at(a.tokens, i, q.wide != 0, q.vocab) - lo;
-      if (t >= 0 && t < hi - lo) atomicOr(&seen[t / 32], 1u << (t & 31));
+      if (t >= 0 && t < hi - lo) atomicOr(&mine[t / 32], 1u << (t & 31));
     }
-    __syncthreads();
-    for (int64_t r = lo + threadIdx.x / 32; r < hi; r += kSortWarps)
-      if (!(seen[(r - lo) / 32] >> ((r - lo) & 31) & 1)) clear_row(static_cast<T *>(a.grad) + r * a.ld_grad, a.cols);
+    sync();
+    for (int i = threadIdx.x; i < words; i += kSortThreads) {
+      uint32_t any = mine[i];
+      for (uint32_t r = 0; r < blocks && blocks > 1; ++r) {
+        uint32_t w;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(w) : "r"(tc::at_rank(tc::smem(mine + i), r)) : "memory");
+        any |= w;
+      }
+      all[i] = any;
+    }
+    sync();  // no block begins again, or leaves, while another reads its rows
+    for (int64_t r = lo + rank * kSortWarps + threadIdx.x / 32; r < hi; r += blocks * kSortWarps)
+      if (!(all[(r - lo) / 32] >> ((r - lo) & 31) & 1)) clear_row(static_cast<T *>(a.grad) + r * a.ld_grad, a.cols);
     __syncthreads();
   }
 }
@@ -299,11 +318,12 @@ __global__ void __launch_bounds__(kSortThreads) short_kernel(const __grid_consta
         __syncthreads();
     }
   } else {
-    const int64_t begin = (int64_t)(blockIdx.x - blocks) * a.share;
+    const uint32_t cluster = max(blocks, 1u);
+    const int64_t begin = (int64_t)((blockIdx.x - blocks) / cluster) * a.share;
     if (a.grad_bf16)
-      clear_share<__nv_bfloat16>(a, s.base, begin);
+      clear_share<__nv_bfloat16>(a, s, begin, cluster);
     else
-      clear_share<float>(a, s.base, begin);
+      clear_share<float>(a, s, begin, cluster);
   }
 }
 
@@ -323,6 +343,8 @@ struct SumArgs {
   uint32_t vocab;
   int32_t add;
   float scale;
+  // Rows from clear_from on are cleared where no token has them: by this many blocks, one in every `every`.
+  int64_t clear_from, clear_blocks, every;
 };
 
 // Rows of loads at a time, two of them in flight: as many as registers hold.
@@ -414,14 +436,71 @@ __device__ __forceinline__ void write_part(const SumArgs &a, int64_t piece, int 
   }
 }
 
+// First index whose key is not below k.
+__device__ __forceinline__ int64_t lower_bound(const uint2 *keys, int64_t n, uint32_t k) {
+  int64_t lo = 0;
+  while (n > 0) {
+    const int64_t half = n / 2;
+    const bool right = keys[lo + half].x < k;
+    lo = right ? lo + half + 1 : lo;
+    n = right ? n - half - 1 : half;
+  }
+  return lo;
+}
+// By a warp: the first index whose key is not below k.  Each round takes 32 probes, so 16,384 keys take three.
+__device__ __forceinline__ int64_t warp_lower_bound(const uint2 *keys, int64_t n, uint32_t k) {
+  const int lane = threadIdx.x & 31;
+  int64_t lo = 0;  // keys before lo are below k, those from lo + n on are not
+  while (n > 0) {
+    const int64_t step = (n + 32) / 33, at = lo + (lane + 1) * step - 1;
+    const uint32_t below = __ballot_sync(0xFFFFFFFFu, at < lo + n && keys[at].x < k);
+    const int c = __popc(below);  // probes 0 .. c - 1 are below
+    const int64_t from = lo + c * step, to = c < 32 ? min(lo + (c + 1) * step - 1, lo + n) : lo + n;
+    lo = from, n = max((int64_t)0, to - from);
+  }
+  return lo;
+}
+
+
+// Rows first .. first + kClearRows - 1 of the gradient, zeros where no token has them: a block looks for them in the part
+// of the sorted tokens that has them, one a thread, and writes those that are missing.
+constexpr int kClearRows = 64;
+template <class TG>
+__device__ __forceinline__ void clear_rows(const SumArgs &a, int64_t first) {
+  __shared__ uint32_t missing[kClearRows];
+  __shared__ int64_t bound[2];
+  __shared__ int32_t n;
+  const int64_t v = first + threadIdx.x;
+  if (threadIdx.x == 0) n = 0;
+  if (threadIdx.x < 64) {
+    const int64_t at = warp_lower_bound(a.pairs, a.rows, (uint32_t)min(first + threadIdx.x / 32 * kClearRows, (int64_t)a.vocab));
+    if (threadIdx.x % 32 == 0) bound[threadIdx.x / 32] = at;
+  }
+  __syncthreads();
+  if (threadIdx.x < kClearRows && v < a.vocab) {
+    const int64_t at = bound[0] + lower_bound(a.pairs + bound[0], bound[1] - bound[0], (uint32_t)v);
+    if (at >= bound[1] || a.pairs[at].x != (uint32_t)v) missing[atomicAdd(&n, 1)] = (uint32_t)v;
+  }
+  __syncthreads();
+  for (int r = threadIdx.x / 32; r < n; r += kThreads / 32) clear_row(static_cast<TG *>(a.grad) + (int64_t)missing[r] * a.ld_grad, a.cols);
+}
+
 template <class TD, class TG, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const __grid_constant__ SumArgs a) {
   constexpr int N = kBatch<TD, VEC>;
   const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
   wait_for_previous();
   let_next_start();
-  const int64_t piece = unit / a.strips;
+  int64_t block = blockIdx.x;
+  if (a.clear_blocks > 0) {  // every so many blocks, one clears rows
+    const int64_t q = block / a.every;
+    if (q * a.every == block && q < a.clear_blocks) {
+      clear_rows<TG>(a, a.clear_from + q * kClearRows);
+      return;
+    }
+    block -= min(a.clear_blocks, q + 1);
+  }
+  const int64_t unit = block * (kThreads / 32) + threadIdx.x / 32, piece = unit / a.strips;
   if (piece >= a.pieces) return;
   const int64_t j = (unit - piece * a.strips) * kStrip + lane * (VEC ? 8 : 1);
   const int64_t first = piece * a.length, end = min(first + a.length, a.rows);
@@ -482,32 +561,6 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const __grid_constant_
   } else {
     write_row<TG, VEC>(a, token, j, sum);
   }
-}
-
-// By a warp: the first index whose key is not below k.  Each round takes 32 probes, so 16,384 keys take three.
-__device__ __forceinline__ int64_t warp_lower_bound(const uint2 *keys, int64_t n, uint32_t k) {
-  const int lane = threadIdx.x & 31;
-  int64_t lo = 0;  // keys before lo are below k, those from lo + n on are not
-  while (n > 0) {
-    const int64_t step = (n + 32) / 33, at = lo + (lane + 1) * step - 1;
-    const uint32_t below = __ballot_sync(0xFFFFFFFFu, at < lo + n && keys[at].x < k);
-    const int c = __popc(below);  // probes 0 .. c - 1 are below
-    const int64_t from = lo + c * step, to = c < 32 ? min(lo + (c + 1) * step - 1, lo + n) : lo + n;
-    lo = from, n = max((int64_t)0, to - from);
-  }
-  return lo;
-}
-
-// First index whose key is not below k.
-__device__ __forceinline__ int64_t lower_bound(const uint2 *keys, int64_t n, uint32_t k) {
-  int64_t lo = 0;
-  while (n > 0) {
-    const int64_t half = n / 2;
-    const bool right = keys[lo + half].x < k;
-    lo = right ? lo + half + 1 : lo;
-    n = right ? n - half - 1 : half;
-  }
-  return lo;
 }
 
 // Tokens whose rows lie in more than one piece (in any order: each has its own row).  A warp to a token of few pieces
@@ -572,30 +625,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     }
     __syncthreads();
   }
-}
-
-// Many tokens: rows of the gradient that no token has, zeros.  A block looks for kThreads rows in the part of the sorted
-// tokens that has them, one a thread, and writes those that are missing.
-template <class TG>
-__global__ void __launch_bounds__(kThreads) clear_kernel(const __grid_constant__ SumArgs a) {
-  __shared__ uint32_t missing[kThreads];
-  __shared__ int64_t bound[2];
-  __shared__ int32_t n;
-  if (threadIdx.x == 0) n = 0;
-  wait_for_previous();
-  let_next_start();
-  const int64_t first = (int64_t)blockIdx.x * kThreads, v = first + threadIdx.x;
-  if (threadIdx.x < 64) {
-    const int64_t at = warp_lower_bound(a.pairs, a.rows, (uint32_t)min(first + threadIdx.x / 32 * kThreads, (int64_t)a.vocab));
-    if (threadIdx.x % 32 == 0) bound[threadIdx.x / 32] = at;
-  }
-  __syncthreads();
-  if (v < a.vocab) {
-    const int64_t at = bound[0] + lower_bound(a.pairs + bound[0], bound[1] - bound[0], (uint32_t)v);
-    if (at >= bound[1] || a.pairs[at].x != (uint32_t)v) missing[atomicAdd(&n, 1)] = (uint32_t)v;
-  }
-  __syncthreads();
-  for (int r = threadIdx.x / 32; r < n; r += kThreads / 32) clear_row(static_cast<TG *>(a.grad) + (int64_t)missing[r] * a.ld_grad, a.cols);
 }
 
 // ---- host --------------------------------------------------------------------
@@ -666,7 +695,9 @@ fsdp_status_t sums(SumArgs a, cudaStream_t s) {
   a.strips = (a.cols + kStrip - 1) / kStrip;
   void *args[] = {&a};
   const int64_t warps = kThreads / 32, units = a.pieces * a.strips;
-  const int64_t grid = (units + warps - 1) / warps;
+  a.clear_blocks = (a.vocab - a.clear_from + kClearRows - 1) / kClearRows;
+  const int64_t grid = (units + warps - 1) / warps + a.clear_blocks;
+  a.every = a.clear_blocks > 0 ? std::max<int64_t>(1, grid / a.clear_blocks) : 1;
   const int64_t joins = std::min<int64_t>((a.pieces - 1) * a.strips, (int64_t)device_sms() * 8);
   if (grid > INT32_MAX) return fail(FSDP_EUNSUPPORTED, "the gradient is too large for one launch");
   fsdp_status_t st = launched(launch_kernel(kernel(&sum_kernel<TD, TG, VEC>), dim3((unsigned)grid), dim3(kThreads), args, 0, s, true));
@@ -759,6 +790,10 @@ fsdp_status_t fsdp_embedding_backward(const fsdp_embedding_desc_t *desc, const v
     return r;
   };
   const bool few = c.blocks <= kMaxCluster;
+  // Rows that are cleared beside the sort: what it leaves time for, at 5 TB/s and 20 us.  The others are cleared beside
+  // the sums, whose reads go well with writes (zeros alone reach 5.8 TB/s, a copy 6.8).
+  const int64_t row_bytes = d.cols * sg;
+  const int64_t cleared = d.accumulate ? d.vocab : !few ? 0 : d.rows == 0 ? d.vocab : std::min(d.vocab, (int64_t)kClearBytes / row_bytes + 1);
   if (few && (d.rows > 0 || !d.accumulate)) {
     ShortArgs r = {};
     for (int p = 0; p < c.passes; ++p) r.pass[p] = pass_of(p);
@@ -768,9 +803,10 @@ fsdp_status_t fsdp_embedding_backward(const fsdp_embedding_desc_t *desc, const v
     if (!d.accumulate) {
       // As many clearing blocks as fill the SMs beside the sort (two fit an SM), of 16 rows at least.
       r.grad = dweight;
-      clearing = std::max<int64_t>(1, std::min<int64_t>((int64_t)device_sms() * 2 - c.blocks, (d.vocab + 15) / 16));
+      clearing = std::max<int64_t>(1, std::min<int64_t>((int64_t)device_sms() * 2 - c.blocks, (cleared + 15) / 16));
       clearing = (clearing + cluster - 1) / cluster * cluster;
-      r.share = (d.vocab + clearing - 1) / clearing;
+      r.share = (cleared + clearing / cluster - 1) / (clearing / cluster);
+      r.clear_to = cleared;
     }
     void *args[] = {&r};
     st = launched(launch_kernel(kernel(&short_kernel), dim3((unsigned)(c.blocks + clearing)), dim3(kSortThreads), args, 0, s, true, cluster));
@@ -790,13 +826,7 @@ fsdp_status_t fsdp_embedding_backward(const fsdp_embedding_desc_t *desc, const v
   a.parts = reinterpret_cast<float *>(w + c.parts);
   a.rows = d.rows, a.cols = d.cols, a.ld_dout = d.ld_out, a.ld_grad = d.ld_weight;
   a.pieces = c.pieces, a.length = c.length;
-  a.vocab = (uint32_t)d.vocab, a.add = d.accumulate, a.scale = d.scale;
-  if (!d.accumulate && !few) {
-    void *args[] = {&a};
-    st = launched(launch_kernel(gb ? kernel(&clear_kernel<__nv_bfloat16>) : kernel(&clear_kernel<float>),
-                                dim3((unsigned)((d.vocab + kThreads - 1) / kThreads)), dim3(kThreads), args, 0, s, true));
-    if (st != FSDP_OK) return st;
-  }
+  a.vocab = (uint32_t)d.vocab, a.add = d.accumulate, a.scale = d.scale, a.clear_from = cleared;
   if (d.rows > 0) {
     const bool vec = d.cols % 8 == 0 && rows_aligned(dweight, d.vocab, d.ld_weight, sg) && rows_aligned(dout, d.rows, d.ld_out, sd);
     using B = __nv_bfloat16;
