@@ -79,7 +79,7 @@ struct alignas(16) Shared {
   float4 block[2][kMaxCluster];  // the same of the cluster's blocks
   uint64_t arrived[2], full[kMaxStages], empty[kMaxStages];  // of the cluster's sums; of stages
   uint64_t ready[kMaxStages], done[kMaxStages];              // of rows' sides
-  uint32_t named[kNamed / 32];   // tokens that the teacher has named, by their last bits
+  uint32_t named[kNamed / 32];   // tokens that the teacher has named, by their hash
   uint32_t stop;
 };
 
@@ -202,15 +202,17 @@ struct Teacher {
       : ids(reinterpret_cast<int32_t *>(&side + 1)), q(reinterpret_cast<float *>(ids + top)), gq(q + top), z(gq + top) {}
 };
 
-// Whether an entry's token (or another with the same last bits) has been named before; forget() clears that.
+// Whether an entry's token (or another with the same hash) has been named before; forget() clears that.  The hash is the top of
+// a product with 2^32 over the golden ratio, which spreads tokens at equal distances too.
+__device__ __forceinline__ uint32_t hash(int32_t id) { return (uint32_t)id * 2654435769u / (0xFFFFFFFFu / kNamed + 1); }
 __device__ __forceinline__ bool name(Shared &sh, int32_t id) {
-  const uint32_t bit = 1u << (id & 31);
-  return (atomicOr(&sh.named[id % kNamed / 32], bit) & bit) != 0;
+  const uint32_t h = hash(id), bit = 1u << (h & 31);
+  return (atomicOr(&sh.named[h / 32], bit) & bit) != 0;
 }
-__device__ __forceinline__ void forget(Shared &sh, int32_t id) { sh.named[id % kNamed / 32] = 0; }
+__device__ __forceinline__ void forget(Shared &sh, int32_t id) { sh.named[hash(id) / 32] = 0; }
 
-// Tokens that are named more than once (z is 1 at all but one of a token's entries, and where tokens differ by multiples
-// of kNamed): the first entry takes what the others have, in their order.
+// Tokens that are named more than once (z is 1 at all but one of a token's entries, and where hashes
+// meet): the first entry takes what the others have, in their order.
 __device__ __noinline__ void join_entries(int top, const Teacher &e) {
   const int lane = threadIdx.x & 31;
   for (int j0 = 0; j0 < top; j0 += 32) {

@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <string>
 
@@ -85,41 +86,32 @@ __device__ __forceinline__ void split(float2 gate, float2 &a, float2 &keep) {
   a = make_float2(nx ? fabsf(gate.x) : px, ny ? fabsf(gate.y) : py), keep = make_float2(nx ? px : gate.x, ny ? py : gate.y);
 }
 
-// Two columns of a lane, neighbours (VEC) or 32 apart, of a row in global or shared memory.
-template <bool VEC>
-__device__ __forceinline__ float2 get(const void *p, int64_t at, bool bf16, bool there, bool second) {
-  if (!there) return make_float2(0, 0);
-  if constexpr (VEC) {
-    if (bf16) {
-      const uint32_t r = *reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p) + at);
-      return make_float2(bf16_low(r), bf16_high(r));
-    }
-    return *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + at);
-  } else {
-    return make_float2(load_any(p, at, bf16), second ? load_any(p, at + 32, bf16) : 0.0f);
-  }
-}
-template <bool VEC>
-__device__ __forceinline__ void put(void *p, int64_t at, bool bf16, bool second, float2 v) {  // bf16 is known where tiles are staged
-  if constexpr (VEC) {
+// How a tile comes and goes.  DIRECT: each value by its own load and store, of any types, a lane's columns 32 apart.  WORDS:
+// x, gate and dh, of one type, staged by 4-byte words wherever rows begin, results stored one by one.  UNITS: all matrices
+// of one type, staged by 16 bytes, results stored in pairs.
+enum Way { DIRECT, WORDS, UNITS };
+
+template <Way WAY>
+__device__ __forceinline__ void put(void *p, bool bf16, bool second, float2 v) {
+  if constexpr (WAY == UNITS) {
     if (bf16)
-      *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p) + at) = bf16_pair(v.x, v.y);
+      *static_cast<uint32_t *>(p) = bf16_pair(v.x, v.y);
     else
-      *reinterpret_cast<float2 *>(static_cast<float *>(p) + at) = v;
+      *static_cast<float2 *>(p) = v;
   } else {
-    store_any(p, at, bf16, v.x);
-    if (second) store_any(p, at + 32, bf16, v.y);
+    store_any(p, 0, bf16, v.x);
+    if (second) store_any(p, WAY == WORDS ? 1 : 32, bf16, v.y);
   }
 }
 // Two columns of a matrix of binary32 values that is aligned to nothing more.
-template <bool VEC>
+template <Way WAY>
 __device__ __forceinline__ float2 get_f32(const float *p, bool second) {
-  return make_float2(p[0], second ? p[VEC ? 1 : 32] : 0.0f);
+  return make_float2(p[0], second ? p[WAY == DIRECT ? 32 : 1] : 0.0f);
 }
-template <bool VEC>
+template <Way WAY>
 __device__ __forceinline__ void put_f32(float *p, bool second, float2 v) {
   p[0] = v.x;
-  if (second) p[VEC ? 1 : 32] = v.y;
+  if (second) p[WAY == DIRECT ? 32 : 1] = v.y;
 }
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
@@ -143,6 +135,35 @@ __device__ __forceinline__ void fetch(uint8_t *to, const void *from, int64_t ld,
                  "r"(there ? 16 : 0)
                  : "memory");
     src += pitch;
+  }
+}
+
+// The same by words, whatever the rows' alignment: a row's 64 columns lie in 64 words (FP32), or in 32 or, where they begin in the
+// middle of one, 33 (BF16).  A warp takes the rows that it works on.
+constexpr int row_words(int size) { return size == 4 ? 64 : 33; }
+template <int STEPS, int SIZE>
+__device__ __forceinline__ void fetch_words(uint8_t *to, const void *from, int64_t ld, int64_t tile_first, int64_t column, const Args &a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int64_t first = tile_first + warp * STEPS;
+  uintptr_t p = (uintptr_t)from + (first * ld + column) * SIZE;
+  uint32_t dst = tc::smem(to) + warp * STEPS * row_words(SIZE) * 4 + lane * 4;
+  const int64_t cols = a.cols - column;
+  const int rows = (int)min((int64_t)STEPS, a.rows - first);
+#pragma unroll 4
+  for (int i = 0; i < STEPS; ++i) {
+    const int phase = SIZE == 2 ? (int)(p >> 1 & 1) : 0;  // elements of the first word that lie before the columns
+    const uintptr_t at = (p & ~(uintptr_t)3) + lane * 4;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      if (SIZE == 2 && w == 1 && (lane > 0 || phase == 0)) continue;
+      const int64_t word = lane + w * 32, element = SIZE == 2 ? 2 * word - phase : word;
+      const bool there = i < rows && element < cols;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + w * 128), "l"(there ? at + w * 128 : (uintptr_t)from & ~(uintptr_t)3),
+                   "r"(there ? 4 : 0)
+                   : "memory");
+    }
+    if (i + 1 < rows) p += ld * SIZE;  // never to a row that is not there
+    dst += row_words(SIZE) * 4;
   }
 }
 
@@ -173,11 +194,11 @@ struct Warps {
   uint32_t cut[kWarps], found[kWindow], ticket;
   Spot spot;  // of `ticket`
 };
-template <bool BACKWARD, bool STAGED>
+template <bool BACKWARD, Way WAY>
 struct Shared {
   Warps now[2];  // by turns: a warp may still read one tile's while another writes the next one's
   float2 forward[BACKWARD ? 2 : 0][kWarps][32];  // backward pass: B of the states
-  uint4 look[STAGED ? 0 : kWindow][32];          // what other tiles have left: A and B, or the state
+  uint4 look[WAY == DIRECT ? kWindow : 0][32];          // what other tiles have left: A and B, or the state
   uint32_t stop;
 };
 // Bits of `cut`: nothing passes a warp's rows downwards, or upwards; a sequence begins at their
@@ -185,7 +206,7 @@ struct Shared {
 enum Cut : uint32_t { CUT_DOWN = 1, CUT_UP = 2, CUT_FIRST = 4, CUT_LAST = 8 };
 
 // This lane's columns and this warp's rows.
-template <int STEPS, bool VEC>
+template <int STEPS, Way WAY>
 struct Place {
   int64_t tile, column, first;  // time tile; first column of the lane; first row of the warp
   int64_t at0;                  // of the lane among the values that tiles leave
@@ -193,10 +214,10 @@ struct Place {
   __device__ __forceinline__ Place(const Args &a, const Spot &p) {
     const int lane = threadIdx.x & 31;
     tile = p.tile;
-    column = p.left + (VEC ? 2 * lane : lane);
+    column = p.left + (WAY == DIRECT ? lane : 2 * lane);
     at0 = p.left + 2 * lane;
     first = tile * (kWarps * STEPS) + threadIdx.x / 32 * STEPS;
-    in = column < a.cols, second = column + (VEC ? 1 : 32) < a.cols;
+    in = column < a.cols, second = column + (WAY == DIRECT ? 32 : 1) < a.cols;
   }
 };
 
@@ -342,58 +363,78 @@ __device__ __forceinline__ float2 take(const Args &a, Warps &s, uint32_t &stop, 
   return carry;
 }
 
-template <class T, bool VEC, bool STAGED, bool BACKWARD>
+template <class T, Way WAY, bool BACKWARD>
 struct Tile {
-  static constexpr int kSteps = steps_of(sizeof(T)), kApart = VEC ? 1 : 32, kRows = kWarps * kSteps;
-  using At = Place<kSteps, VEC>;
-  using Block = Shared<BACKWARD, STAGED>;
-  static constexpr bool kBf16 = sizeof(T) == 2;
-  static constexpr int kMatrix = kRows * kCols * (int)sizeof(T);           // bytes of x or gate in a stage
-  static constexpr int kStage = STAGED ? (BACKWARD ? 3 : 2) * kMatrix : 0;
+  static constexpr int kSteps = steps_of(sizeof(T)), kRows = kWarps * kSteps, kSize = (int)sizeof(T);
+  using At = Place<kSteps, WAY>;
+  using Block = Shared<BACKWARD, WAY>;
+  static constexpr bool kBf16 = kSize == 2;
+  static constexpr int kPitch = WAY == WORDS ? row_words(kSize) * 4 : kCols * kSize;  // bytes of a row of x or gate in a stage
+  static constexpr int kMatrix = kRows * kPitch;
+  static constexpr int kStage = WAY == DIRECT ? 0 : (BACKWARD ? 3 : 2) * kMatrix;
   static constexpr int kSmem = 2 * kStage;
-  static constexpr int kBlocks = BACKWARD || !STAGED ? 2 : 3;  // of an SM
-
-  // Where tiles are staged, all matrices have x's type.
-  __device__ __forceinline__ static bool out_bf16(int32_t bf16) { return STAGED ? kBf16 : bf16 != 0; }
-
+  static constexpr int kBlocks = BACKWARD || WAY != UNITS ? 2 : 3;  // of an SM
+  // Where all matrices have x's type, that of the results is known.
+  __device__ __forceinline__ static bool out_bf16(int32_t bf16) { return WAY == UNITS ? kBf16 : bf16 != 0; }
   __device__ __forceinline__ static int64_t out_size(int32_t bf16) { return out_bf16(bf16) ? 2 : 4; }
 
+  __device__ __forceinline__ static void fetch_matrix(uint8_t *to, const void *from, int64_t ld, const Spot &p, const Args &a) {
+    if constexpr (WAY == UNITS)
+      fetch<kRows, kSize>(to, from, ld, p.tile * kRows, p.left, a);
+    else
+      fetch_words<kSteps, kSize>(to, from, ld, p.tile * kRows, p.left, a);
+  }
   __device__ __forceinline__ static void start(const Args &a, uint8_t *stage, uint32_t ticket, const Spot &p) {
-    if constexpr (STAGED) {
+    if constexpr (WAY != DIRECT) {
       if (ticket < a.tiles) {
-        fetch<kRows, sizeof(T)>(stage, a.x, a.ld_x, p.tile * kRows, p.left, a);
-        fetch<kRows, sizeof(T)>(stage + kMatrix, a.gate, a.ld_gate, p.tile * kRows, p.left, a);
-        if constexpr (BACKWARD) fetch<kRows, sizeof(T)>(stage + 2 * kMatrix, a.dh, a.ld_h, p.tile * kRows, p.left, a);
+        fetch_matrix(stage, a.x, a.ld_x, p, a);
+        fetch_matrix(stage + kMatrix, a.gate, a.ld_gate, p, a);
+        if constexpr (BACKWARD) fetch_matrix(stage + 2 * kMatrix, a.dh, a.ld_h, p, a);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
   }
   // Once a tile's gates have been computed, their place holds what other tiles have left.
-  static_assert(!STAGED || kMatrix >= kWindow * 32 * 16, "no room to look back");
+  static_assert(WAY == DIRECT || kMatrix >= kWindow * 32 * 16, "no room to look back");
   __device__ __forceinline__ static uint4 *look_at(Block &all, uint8_t *stage) {
-    if constexpr (STAGED)
+    if constexpr (WAY != DIRECT)
       return reinterpret_cast<uint4 *>(stage + kMatrix);
     else
       return &all.look[0][0];
   }
   // Row i of the warp's in x, gate or dh (m 0, 1, 2).
   __device__ __forceinline__ static float2 row(const Args &a, const uint8_t *stage, const At &at, int m, int i) {
-    if constexpr (STAGED) {
-      return get<VEC>(stage + m * kMatrix, (threadIdx.x / 32 * kSteps + i) * kCols + 2 * (threadIdx.x & 31), kBf16, true, true);
-    } else {
+    const int lane = threadIdx.x & 31;
+    const void *p = m == 0 ? a.x : m == 1 ? a.gate : a.dh;
+    const int64_t ld = m == 0 ? a.ld_x : m == 1 ? a.ld_gate : a.ld_h;
+    if constexpr (WAY == DIRECT) {
       const bool bf16 = m == 2 ? a.h_bf16 != 0 : kBf16;
-      const void *p = m == 0 ? a.x : m == 1 ? a.gate : a.dh;
-      const int64_t ld = m == 0 ? a.ld_x : m == 1 ? a.ld_gate : a.ld_h, t = at.first + i;
-      return get<VEC>(p, t * ld + at.column, bf16, at.in && t < a.rows, at.second);
+      const int64_t t = at.first + i, k = t * ld + at.column;
+      if (!at.in || t >= a.rows) return both(0.0f);
+      return make_float2(load_any(p, k, bf16), at.second ? load_any(p, k + 32, bf16) : 0.0f);
+    } else {
+      const uint8_t *r = stage + m * kMatrix + (threadIdx.x / 32 * kSteps + i) * kPitch;
+      if constexpr (!kBf16) {
+        if constexpr (WAY == UNITS) return *reinterpret_cast<const float2 *>(r + lane * 8);
+        return make_float2(*reinterpret_cast<const float *>(r + lane * 8), *reinterpret_cast<const float *>(r + lane * 8 + 4));
+      } else {
+        uint32_t w = *reinterpret_cast<const uint32_t *>(r + lane * 4);
+        if constexpr (WAY == WORDS) {
+          const uint32_t phase = ((uint32_t)((uintptr_t)p >> 1) + (uint32_t)(at.first + i) * (uint32_t)ld) & 1u;
+          w = __funnelshift_r(w, *reinterpret_cast<const uint32_t *>(r + lane * 4 + 4), phase * 16);
+        }
+        return make_float2(bf16_low(w), bf16_high(w));
+      }
     }
   }
   __device__ static float2 bias(const Args &a, const At &at) {
     if (!a.bias || !at.in) return make_float2(0, 0);
-    return make_float2(load_any(a.bias, at.column, a.param_bf16), at.second ? load_any(a.bias, at.column + kApart, a.param_bf16) : 0.0f);
+    return make_float2(load_any(a.bias, at.column, a.param_bf16),
+                       at.second ? load_any(a.bias, at.column + (WAY == DIRECT ? 32 : 1), a.param_bf16) : 0.0f);
   }
   // A lane's columns of row s of `initial` or `dfinal`.
   __device__ __forceinline__ static float2 given(const Args &a, const float *p, int32_t s, const At &at) {
-    return p && at.in ? get_f32<VEC>(p + (int64_t)s * a.cols + at.column, at.second) : both(0.0f);
+    return p && at.in ? get_f32<WAY>(p + (int64_t)s * a.cols + at.column, at.second) : both(0.0f);
   }
   // One row of the second and of the third pass over a backward tile.
   __device__ __forceinline__ static void slope_step(float2 x, float2 gate, float2 &h, float2 &slope) {
@@ -408,8 +449,8 @@ struct Tile {
     split(gate, f, keep);
     const float2 d = __fadd2_rn(dh, e), dz = __fmul2_rn(d, slope);
     if (at.in) {
-      put<VEC>(dx, 0, out_bf16(a.dx_bf16), at.second, __fmul2_rn(keep, d));
-      put<VEC>(dgate, 0, out_bf16(a.dx_bf16), at.second, dz);
+      put<WAY>(dx, out_bf16(a.dx_bf16), at.second, __fmul2_rn(keep, d));
+      put<WAY>(dgate, out_bf16(a.dx_bf16), at.second, dz);
     }
     e = __fmul2_rn(f, d);
     return dz;
@@ -425,8 +466,8 @@ __device__ __forceinline__ float2 factor(float2 product, float2 K) {
   return make_float2(K.x < 0.5f ? 1.0f - K.x : product.x, K.y < 0.5f ? 1.0f - K.y : product.y);
 }
 
-template <class T, bool VEC, bool STAGED, bool BACKWARD>
-__device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::forward(const Args &a, Block &all, int turn, uint8_t *stage, uint8_t *other,
+template <class T, Way WAY, bool BACKWARD>
+__device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::forward(const Args &a, Block &all, int turn, uint8_t *stage, uint8_t *other,
     Spot &p, int64_t lo, int64_t hi) {
   const At at(a, p);
   Warps &sh = all.now[turn];
@@ -471,14 +512,14 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::forward(cons
   float2 h = take<false>(a, sh, all.stop, look_at(all, stage), whole, at.tile, at.at0);
   for (int w = 0; w < warp; ++w) h = sh.cut[w] & CUT_DOWN ? sh.b[w][lane] : fma2(sh.a[w][lane], h, sh.b[w][lane]);
   if (a.states && at.in && at.first % kStateRows == 0 && at.first < a.rows)
-    put_f32<VEC>(a.states + at.first / kStateRows * a.cols + at.column, at.second, h);
+    put_f32<WAY>(a.states + at.first / kStateRows * a.cols + at.column, at.second, h);
   const int64_t pitch = a.ld_h * out_size(a.h_bf16);
   uint8_t *out = static_cast<uint8_t *>(a.h) + (at.first * a.ld_h + at.column) * out_size(a.h_bf16);
   if (__builtin_expect(odd == 0, 1)) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       h = fma2(f[i], h, __fmul2_rn(fma2(f[i], both(-1.0f), both(1.0f)), row(a, stage, at, 0, i)));
-      if (at.in) put<VEC>(out, 0, out_bf16(a.h_bf16), at.second, h);
+      if (at.in) put<WAY>(out, out_bf16(a.h_bf16), at.second, h);
       out += pitch;
     }
   } else {
@@ -486,20 +527,20 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::forward(cons
     for (int i = 0; i < kSteps; ++i) {
       if (m.valid >> i & 1) {
         h = m.begins >> i & 1 ? f[i] : fma2(f[i], h, __fmul2_rn(fma2(f[i], both(-1.0f), both(1.0f)), row(a, stage, at, 0, i)));
-        if (at.in) put<VEC>(out, 0, out_bf16(a.h_bf16), at.second, h);
+        if (at.in) put<WAY>(out, out_bf16(a.h_bf16), at.second, h);
       }
       out += pitch;
       if (m.ends >> i & 1) {
         const int32_t s = __shfl_sync(0xFFFFFFFFu, m.end, i);
-        if (at.in && a.final_state) put_f32<VEC>(a.final_state + (int64_t)s * a.cols + at.column, at.second, h);
+        if (at.in && a.final_state) put_f32<WAY>(a.final_state + (int64_t)s * a.cols + at.column, at.second, h);
       }
     }
   }
   return next;
 }
 
-template <class T, bool VEC, bool STAGED, bool BACKWARD>
-__device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::backward(const Args &a, Block &all, int turn, uint8_t *stage, uint8_t *other,
+template <class T, Way WAY, bool BACKWARD>
+__device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args &a, Block &all, int turn, uint8_t *stage, uint8_t *other,
     Spot &p, int64_t lo, int64_t hi) {
   const At at(a, p);
   Warps &sh = all.now[turn];
@@ -510,7 +551,7 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::backward(con
   // The state before the warp's rows comes from the nearest kept one above.
   constexpr int kPer = kStateRows / kSteps;  // warps to a kept state
   const int64_t kept = (at.tile * kRows + warp / kPer * kStateRows) / kStateRows;
-  float2 h = at.in && kept * kStateRows < a.rows ? get_f32<VEC>(a.states_in + kept * a.cols + at.column, at.second) : both(0.0f);
+  float2 h = at.in && kept * kStateRows < a.rows ? get_f32<WAY>(a.states_in + kept * a.cols + at.column, at.second) : both(0.0f);
   // States go A h + B over the warp's rows; e = a_(t+1) D_(t+1) comes in from below and leaves as
   // A e + C.
   float2 A = both(1.0f), B = both(0.0f), C = both(0.0f), K = both(0.0f), gate[kSteps];
@@ -588,7 +629,7 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::backward(con
       dx -= pitch_x, dgate -= pitch_g;
       if (m.begins >> i & 1) {
         const int32_t s = __shfl_sync(0xFFFFFFFFu, m.begin, i);
-        if (at.in && a.dinitial) put_f32<VEC>(a.dinitial + (int64_t)s * a.cols + at.column, at.second, e);
+        if (at.in && a.dinitial) put_f32<WAY>(a.dinitial + (int64_t)s * a.cols + at.column, at.second, e);
       }
     }
   }
@@ -598,15 +639,15 @@ __device__ __forceinline__ uint32_t Tile<T, VEC, STAGED, BACKWARD>::backward(con
     __syncthreads();
     if (warp == 0 && at.in) {
       for (int w = 1; w < kWarps; ++w) db = __fadd2_rn(db, sh.a[w][lane]);
-      put_f32<VEC>(a.partial + at.tile * a.cols + at.column, at.second, db);
+      put_f32<WAY>(a.partial + at.tile * a.cols + at.column, at.second, db);
     }
   }
   return next;
 }
 
-template <class T, bool VEC, bool STAGED, bool BACKWARD>
-__global__ void __launch_bounds__(kThreads, Tile<T, VEC, STAGED, BACKWARD>::kBlocks) tile_kernel(const __grid_constant__ Args a) {
-  using Work = Tile<T, VEC, STAGED, BACKWARD>;
+template <class T, Way WAY, bool BACKWARD>
+__global__ void __launch_bounds__(kThreads, Tile<T, WAY, BACKWARD>::kBlocks) tile_kernel(const __grid_constant__ Args a) {
+  using Work = Tile<T, WAY, BACKWARD>;
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ typename Work::Block sh;
   if (threadIdx.x == 0) sh.stop = 0;
@@ -633,11 +674,11 @@ __global__ void __launch_bounds__(kThreads, Tile<T, VEC, STAGED, BACKWARD>::kBlo
       const uint32_t t = by_ticket ? atomicAdd(a.ticket, 1u) + 1 : now + gridDim.x;
       turn.ticket = t, turn.spot = spot_of<Work::kRows>(a, t, BACKWARD);
     }
-    if constexpr (STAGED) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if constexpr (WAY != DIRECT) asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();  // the stage is whole, and every warp has left the tile before
     now = BACKWARD ? Work::backward(a, sh, n & 1, stage, other, p, lo, hi) : Work::forward(a, sh, n & 1, stage, other, p, lo, hi);
   }
-  if constexpr (STAGED) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if constexpr (WAY != DIRECT) asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
   if (threadIdx.x == 0 && sh.stop) atomicAdd(a.gave_up, 1u);
 }
@@ -756,12 +797,19 @@ const void *kernel(K *k) {
   return reinterpret_cast<const void *>(k);
 }
 
-// The largest number of blocks that the device holds at once.
 template <class Work>
 cudaError_t launch_tiles(void (*fn)(Args), Args &a, cudaStream_t s) {
   static_assert((Work::kSmem + (int)sizeof(typename Work::Block) + 1024) * Work::kBlocks <= 228 * 1024, "an SM's blocks");
-  cudaError_t e = cudaFuncSetAttribute(kernel(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, Work::kSmem);
+  static std::atomic<uint64_t> ready{0};  // devices on which this kernel may have its shared memory
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (device & 63);
+  if (Work::kSmem > 0 && (device > 63 || !(ready.load(std::memory_order_relaxed) & bit))) {
+    e = cudaFuncSetAttribute(kernel(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, Work::kSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   // Few columns are bound by the chain of carries, which a third block of an SM delays (us with two / three blocks, BF16
   // forward: 65536 x 256 46 / 56, 65536 x 1024 119 / 116, 32768 x 4096 214 / 205).
   const int blocks = a.column_tiles <= 8 ? 2 : Work::kBlocks;
@@ -770,17 +818,16 @@ cudaError_t launch_tiles(void (*fn)(Args), Args &a, cudaStream_t s) {
   return launch_kernel(kernel(fn), dim3((unsigned)grid), dim3(kThreads), args, Work::kSmem, s, true);
 }
 template <bool BACKWARD, class T>
-cudaError_t launch_as(bool vec, bool staged, Args &a, cudaStream_t s) {
-  if (staged) return launch_tiles<Tile<T, true, true, BACKWARD>>(&tile_kernel<T, true, true, BACKWARD>, a, s);
-  if (vec) return launch_tiles<Tile<T, true, false, BACKWARD>>(&tile_kernel<T, true, false, BACKWARD>, a, s);
-  return launch_tiles<Tile<T, false, false, BACKWARD>>(&tile_kernel<T, false, false, BACKWARD>, a, s);
+cudaError_t launch_as(Way way, Args &a, cudaStream_t s) {
+  if (way == UNITS) return launch_tiles<Tile<T, UNITS, BACKWARD>>(&tile_kernel<T, UNITS, BACKWARD>, a, s);
+  if (way == WORDS) return launch_tiles<Tile<T, WORDS, BACKWARD>>(&tile_kernel<T, WORDS, BACKWARD>, a, s);
+  return launch_tiles<Tile<T, DIRECT, BACKWARD>>(&tile_kernel<T, DIRECT, BACKWARD>, a, s);
 }
 
-// How the lanes' pairs of columns and the 16-byte units of staged rows fit a matrix.
+// Whether the 16-byte units of staged rows, and so the lanes' pairs of columns, fit all matrices.
 struct Fit {
-  bool pairs = true, units = true;
+  bool units = true;
   void matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t size) {
-    pairs &= cols % 2 == 0 && (uintptr_t)p % (2 * size) == 0 && (rows <= 1 || ld % 2 == 0);
     units &= cols * size % 16 == 0 && aligned16(p) && (rows <= 1 || ld * size % 16 == 0);
   }
 };
@@ -806,10 +853,11 @@ fsdp_status_t run(const fsdp_scan_desc_t &d, Args &a, const Plan &p, void *works
     void *args[] = {&a};
     e = launch_kernel(kernel(&mark_kernel), dim3((unsigned)((d.seqs + 7) / 8)), dim3(256), args, 0, s);
   }
-  const bool staged = fit.units && d.h_dtype == d.x_dtype && (!BACKWARD || d.dx_dtype == d.x_dtype);
+  Way way = DIRECT;
+  if (!BACKWARD || d.h_dtype == d.x_dtype) way = fit.units && d.h_dtype == d.x_dtype && (!BACKWARD || d.dx_dtype == d.x_dtype) ? UNITS : WORDS;
   if (e == cudaSuccess && a.tiles > 0)
-    e = d.x_dtype == FSDP_DTYPE_BF16 ? launch_as<BACKWARD, __nv_bfloat16>(fit.pairs, staged, a, s)
-                                     : launch_as<BACKWARD, float>(fit.pairs, staged, a, s);
+    e = d.x_dtype == FSDP_DTYPE_BF16 ? launch_as<BACKWARD, __nv_bfloat16>(way, a, s)
+                                     : launch_as<BACKWARD, float>(way, a, s);
   return launched(e);
 }
 
