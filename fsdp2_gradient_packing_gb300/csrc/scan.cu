@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kCols = 64, kWarps = 8, kThreads = kWarps * 32;
 constexpr int kStateRows = 64;
-constexpr int kWindow = 16;  // tiles that a look back takes in at once
+constexpr int kWindow = 2 * kWarps;  // tiles that a look back takes in at once, at most
 // Rows of a warp.  What a tile costs a warp beside its rows is about 400 instructions, 30 to 60 a row;
 // of FP32 rows, two stages and two blocks of an SM hold 64.
 constexpr int steps_of(int64_t size) { return size == 4 ? 8 : 16; }
@@ -56,6 +56,7 @@ struct Args {
   int64_t padded_cols;  // whole column tiles
   uint32_t column_tiles, time_tiles, tiles;
   int32_t packed, wide, h_bf16, dx_bf16, param_bf16, fault;
+  int32_t each;  // tiles of a look back that a warp reads
 };
 
 __device__ __forceinline__ int64_t offset_at(const Args &a, int64_t s) {
@@ -273,15 +274,13 @@ __device__ __forceinline__ bool too_late(const Args &a, uint64_t &began) {
 }
 
 // All warps: the state that comes into a tile from `towards` (-1: the tiles before it, 1: those
-// behind).  A warp reads what kWindow / kWarps of the kWindow nearest tiles have left.
+// behind).  A warp reads what one or two (`each`) of the nearest tiles have left.
 __device__ __forceinline__ float2 look_back(const Args &a, Warps &s, uint32_t &stop, uint4 *look, int64_t tile, int towards, int64_t at0) {
-  constexpr int kEach = kWindow / kWarps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   uint64_t began = 0;
   bool late = false;
   for (;;) {
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
+    for (int e = 0; e < a.each; ++e) {
       const int slot = warp + e * kWarps;
       const int64_t other = tile + (int64_t)towards * (1 + slot);
       const bool exists = other >= 0 && other < a.time_tiles;
@@ -303,7 +302,7 @@ __device__ __forceinline__ float2 look_back(const Args &a, Warps &s, uint32_t &s
     }
     if (late) stop = 1;  // before the barrier: all threads see the same
     __syncthreads();
-    const uint32_t states = __ballot_sync(0xFFFFFFFFu, lane < kWindow && s.found[lane % kWindow] == 2);
+    const uint32_t states = __ballot_sync(0xFFFFFFFFu, lane < a.each * kWarps && s.found[lane % kWindow] == 2);
     float2 carry = make_float2(0, 0);
     if (*(volatile uint32_t *)&stop) return carry;
     if (states) {
@@ -846,6 +845,9 @@ fsdp_status_t run(const fsdp_scan_desc_t &d, Args &a, const Plan &p, void *works
   a.begins = reinterpret_cast<int32_t *>(w + p.begins), a.ends = reinterpret_cast<int32_t *>(w + p.ends);
   a.column_tiles = (uint32_t)p.column_tiles, a.time_tiles = (uint32_t)p.time_tiles, a.padded_cols = p.padded_cols;
   a.tiles = a.column_tiles * a.time_tiles;
+  // Few columns have long chains of tiles at work, which want a wide look back; many columns' are short, and the look back
+  // costs what it reads (us with 8 / 16 tiles, BF16 forward: 131072 x 64 119 / 81, 65536 x 1024 123 / 116, 32768 x 4096 181 / 205).
+  a.each = a.column_tiles <= 16 ? 2 : 1;
   a.fault = wait_fault(), a.wait_limit_ns = wait_limit_ns();
   cudaError_t e = gave_up_count(GAVE_UP_SCAN, &a.gave_up);
   if (e != cudaSuccess) return fail(FSDP_ECUDA, std::string("status: ") + cudaGetErrorString(e));
