@@ -117,7 +117,8 @@ struct SortArgs {
   const uint2 *pairs_in;                     // tokens and their positions
   uint2 *pairs;
   uint32_t *crossing;                        // two counters that the last pass clears, or nullptr
-  uint32_t *counts;                          // [blocks][bins] of this pass
+  uint32_t *counts;                          // [blocks][bins] of this pass; with `totals`, those of earlier tiles
+  uint32_t *totals;                          // [bins], or nullptr: tiles sum the counts themselves
   int64_t rows;
   uint32_t vocab, blocks;
   int32_t wide, bits, shift;
@@ -164,7 +165,10 @@ __device__ __forceinline__ void place_tile(const SortArgs &a, SortShared &s, uin
   // thread sums two neighbouring digits (bins are at least 2).
   uint32_t before[2] = {0, 0}, all[2] = {0, 0};
   const int d = threadIdx.x * 2;
-  if (d < bins) {
+  if (d < bins && a.totals) {
+    const uint2 t = *reinterpret_cast<const uint2 *>(a.totals + d), c = *reinterpret_cast<const uint2 *>(a.counts + (int64_t)tile * bins + d);
+    all[0] = t.x, all[1] = t.y, before[0] = c.x, before[1] = c.y;
+  } else if (d < bins) {
     const uint2 *p = reinterpret_cast<const uint2 *>(a.counts + d);
 #pragma unroll 8
     for (uint32_t b = 0; b < a.blocks; ++b) {
@@ -228,6 +232,33 @@ __global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_consta
   wait_for_previous();
   let_next_start();
   count_tile(a, s, blockIdx.x);
+}
+// Many tiles: their counts become those of earlier tiles, and a digit's total.  32 digits to a block, whose warps share out
+// the tiles.  (Summing all counts in each tile would cost the square of their number.)
+constexpr int kFewTiles = 32;
+__global__ void __launch_bounds__(1024) offsets_kernel(const __grid_constant__ SortArgs a) {
+  __shared__ uint32_t part[32][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, bins = 1 << a.bits, d = blockIdx.x * 32 + lane;
+  wait_for_previous();
+  let_next_start();
+  const int64_t share = ((int64_t)a.blocks + 31) / 32, begin = min(warp * share, (int64_t)a.blocks), end = min(begin + share, (int64_t)a.blocks);
+  uint32_t sum = 0;
+  if (d < bins) {
+#pragma unroll 8
+    for (int64_t b = begin; b < end; ++b) sum += a.counts[b * bins + d];
+  }
+  part[warp][lane] = sum;
+  __syncthreads();
+  uint32_t before = 0;
+  for (int w = 0; w < warp; ++w) before += part[w][lane];
+  if (d >= bins) return;
+  if (warp == 31) a.totals[d] = before + sum;
+#pragma unroll 8
+  for (int64_t b = begin; b < end; ++b) {
+    const uint32_t n = a.counts[b * bins + d];
+    a.counts[b * bins + d] = before;
+    before += n;
+  }
 }
 __global__ void __launch_bounds__(kSortThreads) place_kernel(const __grid_constant__ SortArgs a) {
   __shared__ SortShared s;
@@ -655,7 +686,7 @@ bool rows_aligned(const void *p, int64_t rows, int64_t ld, int64_t size) {
 struct Cut {
   int64_t blocks, pieces, padded_cols;
   int32_t length, passes, bits, items;
-  int64_t pairs[2], counts, crossing, parts, bytes;  // offsets in the workspace
+  int64_t pairs[2], counts, totals, crossing, parts, bytes;  // offsets in the workspace
 };
 
 Cut cut_of(const fsdp_embedding_desc_t &d) {
@@ -680,6 +711,7 @@ Cut cut_of(const fsdp_embedding_desc_t &d) {
   };
   for (int k = 0; k < 2; ++k) c.pairs[k] = take(d.rows * 8);
   c.counts = take(c.blocks * (4ll << c.bits));
+  c.totals = take(c.blocks > kFewTiles ? 4ll << c.bits : 0);
   c.crossing = take(d.rows > 0 ? c.pieces * 4 + 8 : 0);
   c.parts = take(c.pieces * 2 * c.padded_cols * 4);
   return c;
@@ -815,10 +847,13 @@ fsdp_status_t fsdp_embedding_backward(const fsdp_embedding_desc_t *desc, const v
   for (int p = 0; p < c.passes && !few; ++p) {
     SortArgs r = pass_of(p);
     void *args[] = {&r};
-    for (const void *fn : {kernel(&count_kernel), kernel(&place_kernel)}) {
-      st = launched(launch_kernel(fn, dim3((unsigned)c.blocks), dim3(kSortThreads), args, 0, s, true));
-      if (st != FSDP_OK) return st;
+    st = launched(launch_kernel(kernel(&count_kernel), dim3((unsigned)c.blocks), dim3(kSortThreads), args, 0, s, true));
+    if (st == FSDP_OK && c.blocks > kFewTiles) {
+      r.totals = words(c.totals);
+      st = launched(launch_kernel(kernel(&offsets_kernel), dim3((unsigned)((1 << c.bits) + 31) / 32), dim3(1024), args, 0, s, true));
     }
+    if (st == FSDP_OK) st = launched(launch_kernel(kernel(&place_kernel), dim3((unsigned)c.blocks), dim3(kSortThreads), args, 0, s, true));
+    if (st != FSDP_OK) return st;
   }
   SumArgs a = {};
   a.pairs = reinterpret_cast<const uint2 *>(w + c.pairs[(c.passes - 1) & 1]), a.crossing = words(c.crossing);
