@@ -87,10 +87,10 @@ __device__ __forceinline__ void split(float2 gate, float2 &a, float2 &keep) {
   a = make_float2(nx ? fabsf(gate.x) : px, ny ? fabsf(gate.y) : py), keep = make_float2(nx ? px : gate.x, ny ? py : gate.y);
 }
 
-// How a tile comes and goes.  DIRECT: each value by its own load and store, of any types, a lane's columns 32 apart.  WORDS:
-// x, gate and dh, of one type, staged by 4-byte words wherever rows begin, results stored one by one.  UNITS: all matrices
-// of one type, staged by 16 bytes, results stored in pairs.
-enum Way { DIRECT, WORDS, UNITS };
+// How a tile comes and goes.  DIRECT: each value by its own load and store, of any types, a lane's columns 32 apart.  ANY:
+// x, gate and dh, of one type, staged wherever rows begin, otherwise as DIRECT.  UNITS: all matrices of one
+// type, staged by 16 bytes, a lane's columns neighbours, results stored in pairs.
+enum Way { DIRECT, ANY, UNITS };
 
 template <Way WAY>
 __device__ __forceinline__ void put(void *p, bool bf16, bool second, float2 v) {
@@ -101,18 +101,18 @@ __device__ __forceinline__ void put(void *p, bool bf16, bool second, float2 v) {
       *static_cast<float2 *>(p) = v;
   } else {
     store_any(p, 0, bf16, v.x);
-    if (second) store_any(p, WAY == WORDS ? 1 : 32, bf16, v.y);
+    if (second) store_any(p, 32, bf16, v.y);
   }
 }
 // Two columns of a matrix of binary32 values that is aligned to nothing more.
 template <Way WAY>
 __device__ __forceinline__ float2 get_f32(const float *p, bool second) {
-  return make_float2(p[0], second ? p[WAY == DIRECT ? 32 : 1] : 0.0f);
+  return make_float2(p[0], second ? p[WAY == UNITS ? 1 : 32] : 0.0f);
 }
 template <Way WAY>
 __device__ __forceinline__ void put_f32(float *p, bool second, float2 v) {
   p[0] = v.x;
-  if (second) p[WAY == DIRECT ? 32 : 1] = v.y;
+  if (second) p[WAY == UNITS ? 1 : 32] = v.y;
 }
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
@@ -139,32 +139,28 @@ __device__ __forceinline__ void fetch(uint8_t *to, const void *from, int64_t ld,
   }
 }
 
-// The same by words, whatever the rows' alignment: a row's 64 columns lie in 64 words (FP32), or in 32 or, where they begin in the
-// middle of one, 33 (BF16).  A warp takes the rows that it works on.
-constexpr int row_words(int size) { return size == 4 ? 64 : 33; }
-template <int STEPS, int SIZE>
-__device__ __forceinline__ void fetch_words(uint8_t *to, const void *from, int64_t ld, int64_t tile_first, int64_t column, const Args &a) {
+// The same whatever the rows' alignment: the units of GRAIN bytes that a row's 64 columns lie in, which begin up to a unit before
+// them.  A warp takes the rows that it works on.
+constexpr int row_units(int size, int grain) { return (kCols * size + 2 * grain - size - 1) / grain; }
+template <int STEPS, int SIZE, int GRAIN>
+__device__ __forceinline__ void fetch_any(uint8_t *to, const void *from, int64_t ld, int64_t tile_first, int64_t column, const Args &a) {
+  constexpr int kUnits = row_units(SIZE, GRAIN);
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int64_t first = tile_first + warp * STEPS;
-  uintptr_t p = (uintptr_t)from + (first * ld + column) * SIZE;
-  uint32_t dst = tc::smem(to) + warp * STEPS * row_words(SIZE) * 4 + lane * 4;
-  const int64_t cols = a.cols - column;
+  const int64_t first = tile_first + warp * STEPS, cols = a.cols - column;
   const int rows = (int)min((int64_t)STEPS, a.rows - first);
+  const uintptr_t base = (uintptr_t)from + column * SIZE;
+  const uint32_t dst = tc::smem(to) + warp * (STEPS * kUnits * GRAIN);
 #pragma unroll 4
-  for (int i = 0; i < STEPS; ++i) {
-    const int phase = SIZE == 2 ? (int)(p >> 1 & 1) : 0;  // elements of the first word that lie before the columns
-    const uintptr_t at = (p & ~(uintptr_t)3) + lane * 4;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      if (SIZE == 2 && w == 1 && (lane > 0 || phase == 0)) continue;
-      const int64_t word = lane + w * 32, element = SIZE == 2 ? 2 * word - phase : word;
-      const bool there = i < rows && element < cols;
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + w * 128), "l"(there ? at + w * 128 : (uintptr_t)from & ~(uintptr_t)3),
-                   "r"(there ? 4 : 0)
-                   : "memory");
-    }
-    if (i + 1 < rows) p += ld * SIZE;  // never to a row that is not there
-    dst += row_words(SIZE) * 4;
+  for (int u = lane; u < STEPS * kUnits; u += 32) {
+    const int r = u / kUnits, k = u - r * kUnits;
+    const uintptr_t p = base + (r < rows ? (first + r) * ld * SIZE : 0);
+    const int phase = (int)(p & (GRAIN - 1)) / SIZE;  // elements of the first unit that lie before the columns
+    const bool there = r < rows && k * (GRAIN / SIZE) - phase < cols;
+    const uintptr_t at = (p & ~(uintptr_t)(GRAIN - 1)) + (there ? k * GRAIN : 0);
+    if constexpr (GRAIN == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + u * 16), "l"(at), "r"(there ? 16 : 0) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + u * 4), "l"(at), "r"(there ? 4 : 0) : "memory");
   }
 }
 
@@ -192,13 +188,14 @@ __device__ __forceinline__ Spot spot_of(const Args &a, uint32_t ticket, bool bac
 
 struct Warps {
   float2 a[kWarps][32], b[kWarps][32];
-  uint32_t cut[kWarps], found[kWindow], ticket;
-  Spot spot;  // of `ticket`
+  uint32_t cut[kWarps], found[kWindow];
 };
 template <bool BACKWARD, Way WAY>
 struct Shared {
-  Warps now[2];  // by turns: a warp may still read one tile's while another writes the next one's
-  float2 forward[BACKWARD ? 2 : 0][kWarps][32];  // backward pass: B of the states
+  Warps warps;
+  uint32_t ticket[2];  // of the next tile, by turns: one may still be read while the next one is written
+  Spot spot[2];
+  float2 forward[BACKWARD ? kWarps : 0][32];  // backward pass: B of the states
   uint4 look[WAY == DIRECT ? kWindow : 0][32];          // what other tiles have left: A and B, or the state
   uint32_t stop;
 };
@@ -215,10 +212,10 @@ struct Place {
   __device__ __forceinline__ Place(const Args &a, const Spot &p) {
     const int lane = threadIdx.x & 31;
     tile = p.tile;
-    column = p.left + (WAY == DIRECT ? lane : 2 * lane);
+    column = p.left + (WAY == UNITS ? 2 * lane : lane);
     at0 = p.left + 2 * lane;
     first = tile * (kWarps * STEPS) + threadIdx.x / 32 * STEPS;
-    in = column < a.cols, second = column + (WAY == DIRECT ? 32 : 1) < a.cols;
+    in = column < a.cols, second = column + (WAY == UNITS ? 1 : 32) < a.cols;
   }
 };
 
@@ -368,7 +365,10 @@ struct Tile {
   using At = Place<kSteps, WAY>;
   using Block = Shared<BACKWARD, WAY>;
   static constexpr bool kBf16 = kSize == 2;
-  static constexpr int kPitch = WAY == WORDS ? row_words(kSize) * 4 : kCols * kSize;  // bytes of a row of x or gate in a stage
+  // Bytes of a row of x or gate in a stage.  The three BF16 matrices of a backward tile leave no room for rows' first and
+  // last units of 16 bytes, only of 4.
+  static constexpr int kGrain = BACKWARD && kBf16 ? 4 : 16;
+  static constexpr int kPitch = WAY == ANY ? row_units(kSize, kGrain) * kGrain : kCols * kSize;
   static constexpr int kMatrix = kRows * kPitch;
   static constexpr int kStage = WAY == DIRECT ? 0 : (BACKWARD ? 3 : 2) * kMatrix;
   static constexpr int kSmem = 2 * kStage;
@@ -381,7 +381,7 @@ struct Tile {
     if constexpr (WAY == UNITS)
       fetch<kRows, kSize>(to, from, ld, p.tile * kRows, p.left, a);
     else
-      fetch_words<kSteps, kSize>(to, from, ld, p.tile * kRows, p.left, a);
+      fetch_any<kSteps, kSize, kGrain>(to, from, ld, p.tile * kRows, p.left, a);
   }
   __device__ __forceinline__ static void start(const Args &a, uint8_t *stage, uint32_t ticket, const Spot &p) {
     if constexpr (WAY != DIRECT) {
@@ -413,23 +413,22 @@ struct Tile {
       return make_float2(load_any(p, k, bf16), at.second ? load_any(p, k + 32, bf16) : 0.0f);
     } else {
       const uint8_t *r = stage + m * kMatrix + (threadIdx.x / 32 * kSteps + i) * kPitch;
-      if constexpr (!kBf16) {
-        if constexpr (WAY == UNITS) return *reinterpret_cast<const float2 *>(r + lane * 8);
-        return make_float2(*reinterpret_cast<const float *>(r + lane * 8), *reinterpret_cast<const float *>(r + lane * 8 + 4));
-      } else {
-        uint32_t w = *reinterpret_cast<const uint32_t *>(r + lane * 4);
-        if constexpr (WAY == WORDS) {
-          const uint32_t phase = ((uint32_t)((uintptr_t)p >> 1) + (uint32_t)(at.first + i) * (uint32_t)ld) & 1u;
-          w = __funnelshift_r(w, *reinterpret_cast<const uint32_t *>(r + lane * 4 + 4), phase * 16);
-        }
+      if constexpr (WAY == ANY) {
+        const uint32_t first = (uint32_t)(uintptr_t)p / kSize + (uint32_t)(at.first + i) * (uint32_t)ld + (uint32_t)(at.column - lane);
+        const T *q = reinterpret_cast<const T *>(r) + lane + first % (kGrain / kSize);
+        return make_float2((float)q[0], (float)q[32]);
+      } else if constexpr (kBf16) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(r + lane * 4);
         return make_float2(bf16_low(w), bf16_high(w));
+      } else {
+        return *reinterpret_cast<const float2 *>(r + lane * 8);
       }
     }
   }
   __device__ static float2 bias(const Args &a, const At &at) {
     if (!a.bias || !at.in) return make_float2(0, 0);
     return make_float2(load_any(a.bias, at.column, a.param_bf16),
-                       at.second ? load_any(a.bias, at.column + (WAY == DIRECT ? 32 : 1), a.param_bf16) : 0.0f);
+                       at.second ? load_any(a.bias, at.column + (WAY == UNITS ? 1 : 32), a.param_bf16) : 0.0f);
   }
   // A lane's columns of row s of `initial` or `dfinal`.
   __device__ __forceinline__ static float2 given(const Args &a, const float *p, int32_t s, const At &at) {
@@ -469,7 +468,7 @@ template <class T, Way WAY, bool BACKWARD>
 __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::forward(const Args &a, Block &all, int turn, uint8_t *stage, uint8_t *other,
     Spot &p, int64_t lo, int64_t hi) {
   const At at(a, p);
-  Warps &sh = all.now[turn];
+  Warps &sh = all.warps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const float2 shift = bias(a, at);
   const Marks<kSteps> m(a, p, at.first, lo, hi);
@@ -504,8 +503,8 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::forward(const Args &
   sh.b[warp][lane] = B;
   if (lane == 0) sh.cut[warp] = m.cut();
   __syncthreads();
-  const uint32_t next = sh.ticket;
-  p = sh.spot;
+  const uint32_t next = all.ticket[turn];
+  p = all.spot[turn];
   start(a, other, next, p);
   const Whole whole = leave<false>(a, sh, at.tile, at.at0);
   float2 h = take<false>(a, sh, all.stop, look_at(all, stage), whole, at.tile, at.at0);
@@ -542,7 +541,7 @@ template <class T, Way WAY, bool BACKWARD>
 __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args &a, Block &all, int turn, uint8_t *stage, uint8_t *other,
     Spot &p, int64_t lo, int64_t hi) {
   const At at(a, p);
-  Warps &sh = all.now[turn];
+  Warps &sh = all.warps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const float2 shift = bias(a, at);
   const Marks<kSteps> m(a, p, at.first, lo, hi);
@@ -585,15 +584,15 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
     }
   }
   sh.a[warp][lane] = factor(A, K);
-  sh.b[warp][lane] = C, all.forward[turn][warp][lane] = B;
+  sh.b[warp][lane] = C, all.forward[warp][lane] = B;
   if (lane == 0) sh.cut[warp] = m.cut();
   __syncthreads();
-  const uint32_t next = sh.ticket;
-  p = sh.spot;
+  const uint32_t next = all.ticket[turn];
+  p = all.spot[turn];
   start(a, other, next, p);
   const Whole whole = leave<true>(a, sh, at.tile, at.at0);
   // Rows' slopes (h_(t-1) - x_t) a_t (1 - a_t), downwards from the warp's state.
-  for (int w = warp / kPer * kPer; w < warp; ++w) h = sh.cut[w] & CUT_DOWN ? all.forward[turn][w][lane] : fma2(sh.a[w][lane], h, all.forward[turn][w][lane]);
+  for (int w = warp / kPer * kPer; w < warp; ++w) h = sh.cut[w] & CUT_DOWN ? all.forward[w][lane] : fma2(sh.a[w][lane], h, all.forward[w][lane]);
   float2 slope[kSteps];
   if (__builtin_expect(odd == 0, 1)) {
 #pragma unroll
@@ -656,22 +655,21 @@ __global__ void __launch_bounds__(kThreads, Tile<T, WAY, BACKWARD>::kBlocks) til
   const bool by_ticket = a.time_tiles > 1;
   uint32_t now = blockIdx.x;
   if (threadIdx.x == 0) {
-    sh.now[1].ticket = by_ticket ? atomicAdd(a.ticket, 1u) + 1 : now;
-    sh.now[1].spot = spot_of<Work::kRows>(a, sh.now[1].ticket, BACKWARD);
+    sh.ticket[1] = by_ticket ? atomicAdd(a.ticket, 1u) + 1 : now;
+    sh.spot[1] = spot_of<Work::kRows>(a, sh.ticket[1], BACKWARD);
   }
   __syncthreads();
-  now = sh.now[1].ticket;
-  Spot p = sh.now[1].spot;
+  now = sh.ticket[1];
+  Spot p = sh.spot[1];
   let_next_start();
   int64_t lo = 0, hi = a.rows;
   if (a.packed) lo = offset_at(a, 0), hi = offset_at(a, a.seqs);
   Work::start(a, stages, now, p);
   for (uint32_t n = 0; now < a.tiles; ++n) {
     uint8_t *stage = stages + (n & 1) * Work::kStage, *other = stages + (~n & 1) * Work::kStage;
-    Warps &turn = sh.now[n & 1];
     if (threadIdx.x == 0) {
       const uint32_t t = by_ticket ? atomicAdd(a.ticket, 1u) + 1 : now + gridDim.x;
-      turn.ticket = t, turn.spot = spot_of<Work::kRows>(a, t, BACKWARD);
+      sh.ticket[n & 1] = t, sh.spot[n & 1] = spot_of<Work::kRows>(a, t, BACKWARD);
     }
     if constexpr (WAY != DIRECT) asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();  // the stage is whole, and every warp has left the tile before
@@ -819,7 +817,7 @@ cudaError_t launch_tiles(void (*fn)(Args), Args &a, cudaStream_t s) {
 template <bool BACKWARD, class T>
 cudaError_t launch_as(Way way, Args &a, cudaStream_t s) {
   if (way == UNITS) return launch_tiles<Tile<T, UNITS, BACKWARD>>(&tile_kernel<T, UNITS, BACKWARD>, a, s);
-  if (way == WORDS) return launch_tiles<Tile<T, WORDS, BACKWARD>>(&tile_kernel<T, WORDS, BACKWARD>, a, s);
+  if (way == ANY) return launch_tiles<Tile<T, ANY, BACKWARD>>(&tile_kernel<T, ANY, BACKWARD>, a, s);
   return launch_tiles<Tile<T, DIRECT, BACKWARD>>(&tile_kernel<T, DIRECT, BACKWARD>, a, s);
 }
 
@@ -856,7 +854,7 @@ fsdp_status_t run(const fsdp_scan_desc_t &d, Args &a, const Plan &p, void *works
     e = launch_kernel(kernel(&mark_kernel), dim3((unsigned)((d.seqs + 7) / 8)), dim3(256), args, 0, s);
   }
   Way way = DIRECT;
-  if (!BACKWARD || d.h_dtype == d.x_dtype) way = fit.units && d.h_dtype == d.x_dtype && (!BACKWARD || d.dx_dtype == d.x_dtype) ? UNITS : WORDS;
+  if (!BACKWARD || d.h_dtype == d.x_dtype) way = fit.units && d.h_dtype == d.x_dtype && (!BACKWARD || d.dx_dtype == d.x_dtype) ? UNITS : ANY;
   if (e == cudaSuccess && a.tiles > 0)
     e = d.x_dtype == FSDP_DTYPE_BF16 ? launch_as<BACKWARD, __nv_bfloat16>(way, a, s)
                                      : launch_as<BACKWARD, float>(way, a, s);
