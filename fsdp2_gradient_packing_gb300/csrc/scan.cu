@@ -77,16 +77,6 @@ __device__ __forceinline__ void gates(float2 z, float2 &a, float2 &keep) {
   const float2 k = __fmul2_rn(e, a);
   keep = make_float2(t.x > 100.0f ? 1.0f : k.x, t.y > 100.0f ? 1.0f : k.y);
 }
-// Both as one number, the lesser of them, negative where that is a; and back, the other rounded once.
-__device__ __forceinline__ float2 join(float2 a, float2 keep) {
-  return make_float2(a.x < keep.x ? -a.x : keep.x, a.y < keep.y ? -a.y : keep.y);
-}
-__device__ __forceinline__ void split(float2 gate, float2 &a, float2 &keep) {
-  const float px = 1.0f - fabsf(gate.x), py = 1.0f - fabsf(gate.y);
-  const bool nx = __float_as_int(gate.x) < 0, ny = __float_as_int(gate.y) < 0;
-  a = make_float2(nx ? fabsf(gate.x) : px, ny ? fabsf(gate.y) : py), keep = make_float2(nx ? px : gate.x, ny ? py : gate.y);
-}
-
 // How a tile comes and goes.  DIRECT: each value by its own load and store, of any types, a lane's columns 32 apart.  ANY:
 // x, gate and dh, of one type, staged wherever rows begin, otherwise as DIRECT.  UNITS: all matrices of one
 // type, staged by 16 bytes, a lane's columns neighbours, results stored in pairs.
@@ -372,7 +362,7 @@ struct Tile {
   static constexpr int kMatrix = kRows * kPitch;
   static constexpr int kStage = WAY == DIRECT ? 0 : (BACKWARD ? 3 : 2) * kMatrix;
   static constexpr int kSmem = 2 * kStage;
-  static constexpr int kBlocks = BACKWARD || WAY != UNITS ? 2 : 3;  // of an SM
+  static constexpr int kBlocks = BACKWARD || WAY == DIRECT || (WAY == ANY && kBf16) ? 2 : 3;  // of an SM
   // Where all matrices have x's type, that of the results is known.
   __device__ __forceinline__ static bool out_bf16(int32_t bf16) { return WAY == UNITS ? kBf16 : bf16 != 0; }
   __device__ __forceinline__ static int64_t out_size(int32_t bf16) { return out_bf16(bf16) ? 2 : 4; }
@@ -434,24 +424,32 @@ struct Tile {
   __device__ __forceinline__ static float2 given(const Args &a, const float *p, int32_t s, const At &at) {
     return p && at.in ? get_f32<WAY>(p + (int64_t)s * a.cols + at.column, at.second) : both(0.0f);
   }
-  // One row of the second and of the third pass over a backward tile.
-  __device__ __forceinline__ static void slope_step(float2 x, float2 gate, float2 &h, float2 &slope) {
-    float2 f, keep;
-    split(gate, f, keep);
-    slope = __fmul2_rn(fma2(x, both(-1.0f), h), __fmul2_rn(f, keep));
-    h = fma2(f, h, __fmul2_rn(keep, x));
+  // One row of the second and of the third pass over a backward tile, from 1 - a and a (1 - a), each good to a few ulp
+  // of its own size; a itself is then 1 - (1 - a), a rounding of 1 off, as the state and D bear.
+  __device__ __forceinline__ static float2 less_than_1(float2 keep) { return fma2(keep, both(-1.0f), both(1.0f)); }
+  __device__ __forceinline__ static void slope_step(float2 x, float2 keep, float2 &h, float2 &slope) {
+    slope = __fmul2_rn(fma2(x, both(-1.0f), h), slope);
+    h = fma2(less_than_1(keep), h, __fmul2_rn(keep, x));
   }
-  __device__ __forceinline__ static float2 gradient_step(const Args &a, float2 dh, float2 gate, float2 slope, const At &at, void *dx,
+  __device__ __forceinline__ static float2 gradient_step(const Args &a, float2 dh, float2 keep, float2 slope, const At &at, void *dx,
                                                          void *dgate, float2 &e) {
-    float2 f, keep;
-    split(gate, f, keep);
     const float2 d = __fadd2_rn(dh, e), dz = __fmul2_rn(d, slope);
     if (at.in) {
       put<WAY>(dx, out_bf16(a.dx_bf16), at.second, __fmul2_rn(keep, d));
       put<WAY>(dgate, out_bf16(a.dx_bf16), at.second, dz);
     }
-    e = __fmul2_rn(f, d);
+    e = __fmul2_rn(less_than_1(keep), d);
     return dz;
+  }
+  // a of row t to a few ulp, once more: of a sequence's first row, for the gradient of its initial state.
+  __device__ static float2 first_gate(const Args &a, const At &at, float2 shift, int64_t t) {
+    float2 z = both(0.0f), f, keep;
+    if (at.in) {
+      const int64_t k = t * a.ld_gate + at.column;
+      z = make_float2(load_any(a.gate, k, kBf16), at.second ? load_any(a.gate, k + (WAY == UNITS ? 1 : 32), kBf16) : 0.0f);
+    }
+    gates(__fadd2_rn(z, shift), f, keep);
+    return f;
   }
   // One tile, from its stage; starts the next one's loads into the other stage, and gives its ticket and its place.
   __device__ static uint32_t forward(const Args &a, Block &all, int turn, uint8_t *stage, uint8_t *other, Spot &p, int64_t lo, int64_t hi);
@@ -552,13 +550,13 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
   float2 h = at.in && kept * kStateRows < a.rows ? get_f32<WAY>(a.states_in + kept * a.cols + at.column, at.second) : both(0.0f);
   // States go A h + B over the warp's rows; e = a_(t+1) D_(t+1) comes in from below and leaves as
   // A e + C.
-  float2 A = both(1.0f), B = both(0.0f), C = both(0.0f), K = both(0.0f), gate[kSteps];
+  float2 A = both(1.0f), B = both(0.0f), C = both(0.0f), K = both(0.0f), keeps[kSteps], slope[kSteps];
   if (__builtin_expect(odd == 0, 1)) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       float2 f, keep;
       gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f, keep);
-      gate[i] = join(f, keep);
+      keeps[i] = keep, slope[i] = __fmul2_rn(f, keep);
       A = __fmul2_rn(A, f), B = fma2(f, B, __fmul2_rn(keep, row(a, stage, at, 0, i))), K = fma2(f, K, keep);
       C = fma2(A, row(a, stage, at, 2, i), C);
     }
@@ -570,7 +568,7 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
       gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f, keep);
       float2 b = __fmul2_rn(keep, row(a, stage, at, 0, i));
       if (!(m.valid >> i & 1)) f = both(1.0f), keep = b = d = both(0.0f);
-      gate[i] = join(f, keep);
+      keeps[i] = keep, slope[i] = __fmul2_rn(f, keep);
       if (m.begins >> i & 1) {
         B = fma2(f, given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at), b);
         open = false;
@@ -593,15 +591,14 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
   const Whole whole = leave<true>(a, sh, at.tile, at.at0);
   // Rows' slopes (h_(t-1) - x_t) a_t (1 - a_t), downwards from the warp's state.
   for (int w = warp / kPer * kPer; w < warp; ++w) h = sh.cut[w] & CUT_DOWN ? all.forward[w][lane] : fma2(sh.a[w][lane], h, all.forward[w][lane]);
-  float2 slope[kSteps];
   if (__builtin_expect(odd == 0, 1)) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) slope_step(row(a, stage, at, 0, i), gate[i], h, slope[i]);
+    for (int i = 0; i < kSteps; ++i) slope_step(row(a, stage, at, 0, i), keeps[i], h, slope[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       if (m.begins >> i & 1) h = given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at);
-      slope_step(row(a, stage, at, 0, i), gate[i], h, slope[i]);
+      slope_step(row(a, stage, at, 0, i), keeps[i], h, slope[i]);
     }
   }
   float2 e = take<true>(a, sh, all.stop, look_at(all, stage), whole, at.tile, at.at0), db = both(0.0f);
@@ -612,7 +609,7 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
   if (__builtin_expect(odd == 0, 1)) {
 #pragma unroll
     for (int i = kSteps - 1; i >= 0; --i) {
-      const float2 dz = gradient_step(a, row(a, stage, at, 2, i), gate[i], slope[i], at, dx, dgate, e);
+      const float2 dz = gradient_step(a, row(a, stage, at, 2, i), keeps[i], slope[i], at, dx, dgate, e);
       db = __fadd2_rn(db, dz);
       dx -= pitch_x, dgate -= pitch_g;
     }
@@ -620,14 +617,16 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
 #pragma unroll
     for (int i = kSteps - 1; i >= 0; --i) {
       if (m.ends >> i & 1) e = given(a, a.dfinal, __shfl_sync(0xFFFFFFFFu, m.end, i), at);
+      const float2 below = e;
       if (m.valid >> i & 1) {  // else e passes
-        const float2 dz = gradient_step(a, row(a, stage, at, 2, i), gate[i], slope[i], at, dx, dgate, e);
+        const float2 dz = gradient_step(a, row(a, stage, at, 2, i), keeps[i], slope[i], at, dx, dgate, e);
         db = __fadd2_rn(db, dz);
       }
       dx -= pitch_x, dgate -= pitch_g;
       if (m.begins >> i & 1) {
         const int32_t s = __shfl_sync(0xFFFFFFFFu, m.begin, i);
-        if (at.in && a.dinitial) put_f32<WAY>(a.dinitial + (int64_t)s * a.cols + at.column, at.second, e);
+        const float2 d0 = __fmul2_rn(first_gate(a, at, shift, at.first + i), __fadd2_rn(row(a, stage, at, 2, i), below));
+        if (at.in && a.dinitial) put_f32<WAY>(a.dinitial + (int64_t)s * a.cols + at.column, at.second, d0);
       }
     }
   }
