@@ -679,6 +679,66 @@ __global__ void __launch_bounds__(kThreads, Tile<T, WAY, BACKWARD>::kBlocks) til
   if (threadIdx.x == 0 && sh.stop) atomicAdd(a.gave_up, 1u);
 }
 
+// Sequences of one row each, a step of generation: nothing to scan.  A lane to 4 columns of a row (PAIRS: in pairs, whose
+// addresses all matrices align; else 32 apart), a warp to 128.
+template <class T, bool PAIRS>
+__global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Args a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t strips = (a.cols + 127) / 128, unit = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
+  const int64_t t = unit / strips, left = (unit - t * strips) * 128;
+  wait_for_previous();
+  let_next_start();
+  if (t >= a.rows) return;
+  const T *x = static_cast<const T *>(a.x) + t * a.ld_x, *gate = static_cast<const T *>(a.gate) + t * a.ld_gate;
+  const int64_t s = t * a.cols;
+  if constexpr (PAIRS) {
+    float2 u[2], z[2], b[2], h0[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t j = left + i * 64 + lane * 2;
+      u[i] = z[i] = b[i] = h0[i] = both(0.0f);
+      if (j >= a.cols) continue;
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t p = *reinterpret_cast<const uint32_t *>(x + j), q = *reinterpret_cast<const uint32_t *>(gate + j);
+        u[i] = make_float2(bf16_low(p), bf16_high(p)), z[i] = make_float2(bf16_low(q), bf16_high(q));
+      } else {
+        u[i] = *reinterpret_cast<const float2 *>(x + j), z[i] = *reinterpret_cast<const float2 *>(gate + j);
+      }
+      if (a.bias) b[i] = make_float2(load_any(a.bias, j, a.param_bf16), load_any(a.bias, j + 1, a.param_bf16));
+      if (a.initial) h0[i] = make_float2(a.initial[s + j], a.initial[s + j + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t j = left + i * 64 + lane * 2;
+      if (j >= a.cols) continue;
+      float2 f, keep;
+      gates(__fadd2_rn(z[i], b[i]), f, keep);
+      const float2 h = fma2(f, h0[i], __fmul2_rn(keep, u[i]));
+      put<UNITS>(static_cast<uint8_t *>(a.h) + (t * a.ld_h + j) * (a.h_bf16 ? 2 : 4), a.h_bf16 != 0, true, h);
+      if (a.final_state) a.final_state[s + j] = h.x, a.final_state[s + j + 1] = h.y;
+    }
+  } else {
+    float u[4], z[4], b[4], h0[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t j = left + i * 32 + lane;
+      const bool in = j < a.cols;
+      u[i] = in ? (float)x[j] : 0.0f, z[i] = in ? (float)gate[j] : 0.0f;
+      b[i] = in && a.bias ? load_any(a.bias, j, a.param_bf16) : 0.0f, h0[i] = in && a.initial ? a.initial[s + j] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t j = left + i * 32 + lane;
+      if (j >= a.cols) continue;
+      float2 f, keep;
+      gates(both(z[i] + b[i]), f, keep);
+      const float h = fmaf(f.x, h0[i], keep.x * u[i]);
+      store_any(a.h, t * a.ld_h + j, a.h_bf16 != 0, h);
+      if (a.final_state) a.final_state[s + j] = h;
+    }
+  }
+}
+
 // Packed sequences: marks where they begin and end, and the states of those without rows.
 // A warp to a sequence.
 __global__ void __launch_bounds__(256) mark_kernel(const __grid_constant__ Args a) {
@@ -777,7 +837,7 @@ Plan plan_of(const fsdp_scan_desc_t &d, bool backward) {
     p.bytes += (bytes + 15) / 16 * 16;
     return at;
   };
-  const bool several = p.time_tiles > 1;
+  const bool several = p.time_tiles > 1 && (backward || d.packed || d.seq_len != 1);
   p.partial = take(backward ? p.time_tiles * d.cols * 4 : 0);
   p.clear = p.bytes;
   p.parts = take(several ? p.time_tiles * p.padded_cols * 8 : 0);
@@ -820,10 +880,11 @@ cudaError_t launch_as(Way way, Args &a, cudaStream_t s) {
   return launch_tiles<Tile<T, DIRECT, BACKWARD>>(&tile_kernel<T, DIRECT, BACKWARD>, a, s);
 }
 
-// Whether the 16-byte units of staged rows, and so the lanes' pairs of columns, fit all matrices.
+// Whether pairs of columns, and the 16-byte units of staged rows, fit all matrices.
 struct Fit {
-  bool units = true;
+  bool pairs = true, units = true;
   void matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t size) {
+    pairs &= cols % 2 == 0 && (uintptr_t)p % (2 * size) == 0 && (rows <= 1 || ld % 2 == 0);
     units &= cols * size % 16 == 0 && aligned16(p) && (rows <= 1 || ld * size % 16 == 0);
   }
 };
@@ -832,6 +893,17 @@ struct Fit {
 template <bool BACKWARD>
 fsdp_status_t run(const fsdp_scan_desc_t &d, Args &a, const Plan &p, void *workspace, const Fit &fit, cudaStream_t s) {
   uint8_t *w = static_cast<uint8_t *>(workspace);
+  if (!BACKWARD && !d.packed && d.seq_len == 1) {
+    // A tile's rows would each begin and end a sequence (64 x 4096 in BF16 5.4 us, here 1.9).
+    const int64_t blocks = (d.rows * ((d.cols + 127) / 128) + kWarps - 1) / kWarps;
+    if (blocks > INT32_MAX) return fail(FSDP_EUNSUPPORTED, "the step is too large for one launch");
+    using B = __nv_bfloat16;
+    const bool bf16 = d.x_dtype == FSDP_DTYPE_BF16;
+    const void *fn = fit.pairs ? (bf16 ? kernel(&step_kernel<B, true>) : kernel(&step_kernel<float, true>))
+                               : (bf16 ? kernel(&step_kernel<B, false>) : kernel(&step_kernel<float, false>));
+    void *args[] = {&a};
+    return launched(launch_kernel(fn, dim3((unsigned)blocks), dim3(kThreads), args, 0, s, true));
+  }
   if (p.time_tiles * p.column_tiles > INT32_MAX / 2) return fail(FSDP_EUNSUPPORTED, "more than 2^30 tiles");
   if (p.bytes > p.clear) {
     const cudaError_t e = cudaMemsetAsync(w + p.clear, 0xFF, p.bytes - p.clear, s);

@@ -327,3 +327,11 @@ def test_binding_refusals():
             fp.fsdp_gated_scan_forward(*args, **kw)
     with pytest.raises(ValueError, match="states is needed"):
         fp.fsdp_gated_scan_backward(x, x, x, None, x, x, seq_len=4)
+
+
+@pytest.mark.parametrize("kind", range(len(KINDS)))
+@pytest.mark.parametrize("rows,cols,ld,offset", [(1, 1, None, 0), (1, 4096, None, 0), (70, 130, None, 0), (5, 515, None, 0), (200, 64, 65, 1), (3, 128, 130, 2)])
+def test_one_row_sequences(rows, cols, ld, offset, kind):
+    """Steps of generation, aligned and not, through the backward pass too."""
+    check(fp_module(), rows, cols, 1, ld=ld, offset=offset, seed=rows + cols, **KINDS[kind])
+    check(fp_module(), rows, cols, 1, ld=ld, offset=offset, seed=rows + cols, with_states=False, **KINDS[kind])
