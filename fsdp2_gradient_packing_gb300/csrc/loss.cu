@@ -889,7 +889,7 @@ template <class D>
 fsdp_status_t check(const D *d, const void *logits, void *dlogits, bool backward) {
   if (!d) return fail(FSDP_EINVAL, "desc is NULL");
   if (d->rows < 0 || d->vocab < 1) return fail(FSDP_EINVAL, "rows < 0 or vocab < 1");
-  if (d->vocab > INT32_MAX) return fail(FSDP_EUNSUPPORTED, "a vocabulary of 2^31 or more");
+  if (d->vocab > INT32_MAX - 63) return fail(FSDP_EUNSUPPORTED, "a vocabulary of 2^31 - 63 or more");  // places in whole units
   if (d->rows > INT64_MAX / 64 / d->vocab) return fail(FSDP_EUNSUPPORTED, "the matrices are too large");
   if (!float_dtype(d->logits_dtype)) return fail(FSDP_EINVAL, "unknown logits_dtype");
   if (d->token_dtype != FSDP_INDEX_I32 && d->token_dtype != FSDP_INDEX_I64) return fail(FSDP_EINVAL, "unknown token_dtype");

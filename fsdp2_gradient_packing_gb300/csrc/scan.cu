@@ -1011,6 +1011,7 @@ fsdp_status_t fsdp_gated_scan_backward(const fsdp_scan_desc_t *desc, const void 
   const int64_t gsize = dtype_bytes(d.grad_dtype);
   if (dbias && (st = check_ptr(dbias, d.cols * gsize, gsize, "dbias", -1)) != FSDP_OK) return st;
   if (dinitial && (st = check_ptr(dinitial, d.seqs * d.cols * 4, 4, "dinitial", -1)) != FSDP_OK) return st;
+  if (dinitial && dinitial == dfinal) return fail(FSDP_EINVAL, "dinitial is dfinal");
   const Plan plan = plan_of(d, true);
   if ((st = check_workspace(workspace, workspace_bytes, plan.bytes)) != FSDP_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -267,7 +267,8 @@ fsdp_status_t fsdp_embedding_workspace(const fsdp_embedding_desc_t *desc, int64_
  *   dx_t = (1 - a_t) D_t,   dgate_t = D_t (h_(t-1) - x_t) a_t (1 - a_t),
  *   dbias = sum of dgate over the rows of all sequences,   dinitial = a_1 D_1
  * States and sums are binary32.  One row a sequence is a step of generation: pass the
- * states in `initial` and receive them in `final`, which may be the same buffer.
+ * states in `initial` and receive them in `final`, which may be the same buffer; no
+ * other output may overlap an input.
  *
  * The rows of a batch are its sequences one after another: `seqs` of `seq_len` rows each,
  * or with `packed` sequence s from row offsets[s] up to offsets[s + 1], where offsets has
@@ -315,7 +316,8 @@ fsdp_status_t fsdp_gated_scan_forward(const fsdp_scan_desc_t *desc, const void *
  *   x, gate, bias, initial, offsets: as in the forward call;  states: what it wrote.
  *   dh [rows, cols];  dfinal: [seqs, cols] binary32, or NULL for 0.
  *   dx, dgate [rows, cols], both written;  dbias (cols elements) and dinitial ([seqs, cols]
- *   binary32): written, or NULL if not wanted.
+ *   binary32): written, or NULL if not wanted.  dinitial may not be dfinal: a sequence's first
+ *   rows may be done before its last ones.
  */
 fsdp_status_t fsdp_gated_scan_backward(const fsdp_scan_desc_t *desc, const void *dh, const void *x, const void *gate,
                                        const void *bias, const float *initial, const void *offsets,
@@ -353,7 +355,7 @@ fsdp_status_t fsdp_gated_scan_backward(const fsdp_scan_desc_t *desc, const void 
 #define FSDP_DISTILL_MAX_TOP 1024
 
 typedef struct {
-  int64_t rows, vocab;         /* rows >= 0, vocab 1 .. 2^31 - 1 */
+  int64_t rows, vocab;         /* rows >= 0, vocab 1 .. 2^31 - 64 */
   int64_t ld_logits, ld_dlogits;
   int64_t top;                 /* entries of a row, 0 .. FSDP_DISTILL_MAX_TOP */
   int64_t ld_tokens, ld_teacher;
@@ -377,7 +379,7 @@ fsdp_status_t fsdp_distill_loss_backward(const fsdp_distill_desc_t *desc, const 
                                          const float *dloss, void *dlogits, fsdp_stream_t stream);
 
 typedef struct {
-  int64_t rows, vocab;         /* rows >= 0, vocab 1 .. 2^31 - 1 */
+  int64_t rows, vocab;         /* rows >= 0, vocab 1 .. 2^31 - 64 */
   int64_t ld_logits, ld_dlogits;
   int32_t logits_dtype, dlogits_dtype; /* F32 or BF16 */
   int32_t token_dtype;         /* FSDP_INDEX_I32 or _I64 */

@@ -91,7 +91,7 @@ def test_scan_refusals(fp):
     def forward(d, x=P, g=P, b=P, i=P, o=None, h=P, f=P, s=P, ws=P, n=BIG):
         return lib.fsdp_gated_scan_forward(d, x, g, b, i, o, h, f, s, ws, n, None)
 
-    def backward(d, h=P, x=P, g=P, b=P, i=P, o=None, s=P, df=P, dx=P, dg=P, db=P, di=P, ws=P, n=BIG):
+    def backward(d, h=P, x=P, g=P, b=P, i=P, o=None, s=P, df=P, dx=P, dg=P, db=P, di=ctypes.c_void_p(1 << 20), ws=P, n=BIG):
         return lib.fsdp_gated_scan_backward(d, h, x, g, b, i, o, s, df, dx, dg, db, di, ws, n, None)
 
     for call in (forward, backward):
@@ -129,6 +129,7 @@ def test_scan_refusals(fp):
     refused(fp, backward(scan(fp), db=ODD), E, "dbias")
     refused(fp, backward(scan(fp), df=ODD), E, "dfinal")
     refused(fp, backward(scan(fp), di=ODD), E, "dinitial")
+    refused(fp, backward(scan(fp), di=P), E, "dinitial is dfinal")
     refused(fp, backward(scan(fp), n=0), E, "workspace_bytes")
     refused(fp, backward(scan(fp), ws=None), E, "workspace is NULL")
     assert forward(scan(fp, rows=0, seqs=0), x=None, g=None, h=None) == fp.FSDP_OK
@@ -174,6 +175,7 @@ def test_loss_refusals(fp):
         refused(fp, call(desc(fp, rows=-1)), E, "rows")
         refused(fp, call(desc(fp, vocab=0)), E, "vocab")
         refused(fp, call(desc(fp, vocab=1 << 31)), N, "2^31")
+        refused(fp, call(desc(fp, vocab=(1 << 31) - 63)), N, "2^31")
         refused(fp, call(desc(fp, rows=1 << 55)), N, "too large")
         refused(fp, call(desc(fp, logits_dtype=2)), E, "logits_dtype")
         refused(fp, call(desc(fp, dlogits_dtype=2)), E, "dlogits_dtype")
