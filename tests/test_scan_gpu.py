@@ -335,3 +335,10 @@ def test_one_row_sequences(rows, cols, ld, offset, kind):
     """Steps of generation, aligned and not, through the backward pass too."""
     check(fp_module(), rows, cols, 1, ld=ld, offset=offset, seed=rows + cols, **KINDS[kind])
     check(fp_module(), rows, cols, 1, ld=ld, offset=offset, seed=rows + cols, with_states=False, **KINDS[kind])
+
+
+@pytest.mark.parametrize("seqs,length,cols,dtype", [(3, 1536, 70, BF16), (3, 1536, 64, F32), (2, 2560, 200, BF16), (5, 128, 66, BF16),
+                                                    (9, 640, 1100, BF16)])
+def test_sequences_of_whole_tiles(seqs, length, cols, dtype):
+    """Sequences that begin where tiles do, many tiles long: they are gone through side by side."""
+    check(fp_module(), seqs * length, cols, length, dtype=dtype, seed=length, slow=7.0)
