@@ -56,7 +56,7 @@ struct Args {
   int64_t padded_cols;  // whole column tiles
   uint32_t column_tiles, time_tiles, tiles;
   int32_t packed, wide, h_bf16, dx_bf16, param_bf16, fault;
-  int32_t each;    // tiles of a look back that a warp reads
+  int32_t window;  // tiles that a look back takes in at once
   uint32_t aside;  // sequences that go side by side
 };
 
@@ -271,14 +271,13 @@ __device__ __forceinline__ bool too_late(const Args &a, uint64_t &began) {
 }
 
 // All warps: the state that comes into a tile from `towards` (-1: the tiles before it, 1: those
-// behind).  A warp reads what one or two (`each`) of the nearest tiles have left.
+// behind).  A warp reads what one or two of the nearest tiles have left.
 __device__ __forceinline__ float2 look_back(const Args &a, Warps &s, uint32_t &stop, uint4 *look, int64_t tile, uint32_t reach, int towards, int64_t at0) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   uint64_t began = 0;
   bool late = false;
   for (;;) {
-    for (int e = 0; e < a.each; ++e) {
-      const int slot = warp + e * kWarps;
+    for (int slot = warp; slot < a.window; slot += kWarps) {
       const int64_t other = tile + (int64_t)towards * (1 + slot);
       const bool exists = (uint32_t)slot < reach;
       const int64_t at = other * a.padded_cols + at0;
@@ -299,7 +298,7 @@ __device__ __forceinline__ float2 look_back(const Args &a, Warps &s, uint32_t &s
     }
     if (late) stop = 1;  // before the barrier: all threads see the same
     __syncthreads();
-    const uint32_t states = __ballot_sync(0xFFFFFFFFu, lane < a.each * kWarps && s.found[lane % kWindow] == 2);
+    const uint32_t states = __ballot_sync(0xFFFFFFFFu, lane < a.window && s.found[lane % kWindow] == 2);
     float2 carry = make_float2(0, 0);
     if (*(volatile uint32_t *)&stop) return carry;
     if (states) {
@@ -925,11 +924,14 @@ fsdp_status_t run(const fsdp_scan_desc_t &d, Args &a, const Plan &p, void *works
   a.column_tiles = (uint32_t)p.column_tiles, a.time_tiles = (uint32_t)p.time_tiles, a.padded_cols = p.padded_cols;
   a.tiles = a.column_tiles * a.time_tiles;
   // Where tiles do not cross sequences, these go side by side: the tile before one is then further back in the order and has
-  // mostly been done when it is looked for (4 x 8192 x 4096 BF16: forward 182 us one behind the other, ASIDE us so).
+  // mostly been done when it is looked for (us one behind the other / side by side, forward: 4 x 8192 x 4096 BF16 182 / 174,
+  // 16 x 2048 x 2048 FP32 159 / 141).
   a.aside = !d.packed && d.seqs > 1 && a.time_tiles > 1 && d.seq_len % (kWarps * steps_of(dtype_bytes(d.x_dtype))) == 0 ? (uint32_t)d.seqs : 1;
-  // Few columns have long chains of tiles at work, which want a wide look back; many columns' are short, and the look back
-  // costs what it reads (us with 8 / 16 tiles, BF16 forward: 131072 x 64 119 / 81, 65536 x 1024 123 / 116, 32768 x 4096 181 / 205).
-  a.each = a.column_tiles * a.aside <= 16 ? 2 : 1;
+  // Few chains of tiles are long ones at work, which want a wide look back; many are short, and the look back costs what it
+  // reads (us with 2 / 8 / 16 tiles, BF16 forward: 131072 x 64 - / 119 / 75, 65536 x 1024 - / 123 / 110, 32768 x 4096 in one
+  // sequence after another - / 182 / 205, four side by side 168 / 174 / -).
+  const uint32_t chains = a.column_tiles * a.aside;
+  a.window = chains <= 16 ? kWindow : chains < 256 ? kWindow / 2 : 2;
   a.fault = wait_fault(), a.wait_limit_ns = wait_limit_ns();
   cudaError_t e = gave_up_count(GAVE_UP_SCAN, &a.gave_up);
   if (e != cudaSuccess) return fail(FSDP_ECUDA, std::string("status: ") + cudaGetErrorString(e));
