@@ -79,7 +79,7 @@ struct alignas(16) Shared {
   float4 block[2][kMaxCluster];  // the same of the cluster's blocks
   uint64_t arrived[2], full[kMaxStages], empty[kMaxStages];  // of the cluster's sums; of stages
   uint64_t ready[kMaxStages], done[kMaxStages];              // of rows' sides
-  uint32_t named[kNamed / 32];   // tokens that the teacher has named, by their hash
+  uint32_t named[kNamed / 32];   // tokens that the teacher has named
   uint32_t stop;
 };
 
@@ -202,14 +202,23 @@ struct Teacher {
       : ids(reinterpret_cast<int32_t *>(&side + 1)), q(reinterpret_cast<float *>(ids + top)), gq(q + top), z(gq + top) {}
 };
 
-// Whether an entry's token (or another with the same hash) has been named before; forget() clears that.  The hash is the top of
-// a product with 2^32 over the golden ratio, which spreads tokens at equal distances too.
-__device__ __forceinline__ uint32_t hash(int32_t id) { return (uint32_t)id * 2654435769u / (0xFFFFFFFFu / kNamed + 1); }
-__device__ __forceinline__ bool name(Shared &sh, int32_t id) {
-  const uint32_t h = hash(id), bit = 1u << (h & 31);
-  return (atomicOr(&sh.named[h / 32], bit) & bit) != 0;
-}
-__device__ __forceinline__ void forget(Shared &sh, int32_t id) { sh.named[hash(id) / 32] = 0; }
+// Whether an entry's token has been named before; forget() clears that.  Tokens from lo on have a bit each where kNamed bits are
+// enough for those up to hi, else by a hash, the top of a product with 2^32 over the golden ratio (which spreads tokens
+// at equal distances too): then another token may have been named.
+struct Names {
+  uint32_t *bits;
+  int32_t lo;
+  bool exact;
+  __device__ __forceinline__ Names(Shared &sh, int32_t l, int32_t hi) : bits(sh.named), lo(l), exact(hi - l <= kNamed) {}
+  __device__ __forceinline__ uint32_t at(int32_t id) const {
+    return exact ? (uint32_t)(id - lo) : (uint32_t)id * 2654435769u / (0xFFFFFFFFu / kNamed + 1);
+  }
+  __device__ __forceinline__ bool name(int32_t id) const {
+    const uint32_t h = at(id), bit = 1u << (h & 31);
+    return (atomicOr(&bits[h / 32], bit) & bit) != 0;
+  }
+  __device__ __forceinline__ void forget(int32_t id) const { bits[at(id) / 32] = 0; }
+};
 
 // Tokens that are named more than once (z is 1 at all but one of a token's entries, and where hashes
 // meet): the first entry takes what the others have, in their order.
@@ -244,6 +253,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side
                                            const Ahead<DISTILL, MODE> &ahead) {
   const int lane = threadIdx.x & 31;
   const Teacher e(side, a.top);
+  const Names names(sh, lo, hi);
   float top = -INFINITY, sum = 0.0f, total = 0.0f;
   bool nan = false, twice = false;
   if (a.top <= 32 * kEach) {
@@ -264,7 +274,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side
       sum += p;
       if (p > 0.0f || p != p) total += p * d;
       v[i] = p;
-      again[i] = MODE != STATS && id[i] >= lo && id[i] < hi && name(sh, id[i]);
+      again[i] = MODE != STATS && id[i] >= lo && id[i] < hi && names.name(id[i]);
       twice |= again[i];
     }
     sum = warp_sum(sum), total = warp_sum(total);
@@ -277,7 +287,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side
         e.q[j] = e.gq[j] = id[i] < 0 ? 0.0f : v[i] * inv;
         if (MODE != STATS) {
           e.z[j] = again[i] ? 1.0f : 0.0f;
-          if (id[i] >= lo && id[i] < hi) forget(sh, id[i]);
+          if (id[i] >= lo && id[i] < hi) names.forget(id[i]);
         }
       }
     }
@@ -306,7 +316,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side
       const int32_t id = e.ids[j];
       e.q[j] = e.gq[j] = id < 0 ? 0.0f : e.q[j] * inv;
       if (MODE != STATS) {
-        const bool again = id >= lo && id < hi && name(sh, id);
+        const bool again = id >= lo && id < hi && names.name(id);
         e.z[j] = again ? 1.0f : 0.0f;
         twice |= again;
       }
@@ -314,7 +324,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side
     if (MODE != STATS) {
       __syncwarp();
       for (int j = lane; j < a.top; j += 32)
-        if (e.ids[j] >= lo && e.ids[j] < hi) forget(sh, e.ids[j]);
+        if (e.ids[j] >= lo && e.ids[j] < hi) names.forget(e.ids[j]);
     }
   }
   __syncwarp();
