@@ -136,31 +136,36 @@ struct SortShared {
   uint32_t total[kSortWarps];
 };
 
+// A thread's items of a tile: a warp has consecutive ones, 32 at a time.
+struct Items {
+  uint2 item[kItems];
+  int n;
+  __device__ __forceinline__ Items(const SortArgs &a, uint32_t tile) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int64_t first = (int64_t)tile * (a.items * kSortThreads) + warp * (32 * a.items) + lane;
+    n = (int)min((int64_t)a.items, (a.rows - first + 31) / 32);
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) item[k] = k < n ? sort_item(a, first + k * 32) : make_uint2(0, 0);
+  }
+};
+
 // How many of a tile's items have each digit.
-__device__ __forceinline__ void count_tile(const SortArgs &a, SortShared &s, uint32_t tile) {
+__device__ __forceinline__ void count_tile(const SortArgs &a, SortShared &s, uint32_t tile, const Items &own) {
   const int bins = 1 << a.bits;
   for (int d = threadIdx.x; d < bins; d += kSortThreads) s.base[d] = 0;
   __syncthreads();
-  const int64_t first = (int64_t)tile * (a.items * kSortThreads);
 #pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    const int64_t i = first + k * kSortThreads + threadIdx.x;
-    if (k < a.items && i < a.rows) atomicAdd(&s.base[(sort_item(a, i).x >> a.shift) & (bins - 1)], 1u);
-  }
+  for (int k = 0; k < kItems; ++k)
+    if (k < own.n) atomicAdd(&s.base[(own.item[k].x >> a.shift) & (bins - 1)], 1u);
   __syncthreads();
   for (int d = threadIdx.x; d < bins; d += kSortThreads) a.counts[(int64_t)tile * bins + d] = s.base[d];
 }
 
 // A tile's items to their places.
-__device__ __forceinline__ void place_tile(const SortArgs &a, SortShared &s, uint32_t tile) {
+__device__ __forceinline__ void place_tile(const SortArgs &a, SortShared &s, uint32_t tile, const Items &own) {
   const int bins = 1 << a.bits, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  for (int i = threadIdx.x; i < kSortWarps * kMaxBins / 2; i += kSortThreads) reinterpret_cast<uint32_t *>(s.seen)[i] = 0;
-  const int64_t first = (int64_t)tile * (a.items * kSortThreads) + warp * (32 * a.items) + lane;
-  const int n = (int)min((int64_t)a.items, (a.rows - first + 31) / 32);  // of this thread
-  uint2 item[kItems];
+  for (int i = lane; i < bins / 2; i += 32) reinterpret_cast<uint32_t *>(s.seen[warp])[i] = 0;
   uint32_t rank[kItems];
-#pragma unroll
-  for (int k = 0; k < kItems; ++k) item[k] = k < n ? sort_item(a, first + k * 32) : make_uint2(0, 0);
   // Where each digit's items start: behind those of lower digits and those of earlier tiles.  A
   // thread sums two neighbouring digits (bins are at least 2).
   uint32_t before[2] = {0, 0}, all[2] = {0, 0};
@@ -191,11 +196,12 @@ __device__ __forceinline__ void place_tile(const SortArgs &a, SortShared &s, uin
     s.base[d + 1] = run - all[1] + before[1];
   }
   // Ranks within the warp's items of the same digit.
+  __syncwarp();
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     if (k >= a.items) break;
-    const bool here = k < n;
-    const uint32_t digit = (item[k].x >> a.shift) & (bins - 1);
+    const bool here = k < own.n;
+    const uint32_t digit = (own.item[k].x >> a.shift) & (bins - 1);
     uint32_t same = __ballot_sync(0xFFFFFFFFu, here);
     for (int b = 0; b < a.bits; ++b) {
       const uint32_t ones = __ballot_sync(0xFFFFFFFFu, digit >> b & 1);
@@ -220,9 +226,9 @@ __device__ __forceinline__ void place_tile(const SortArgs &a, SortShared &s, uin
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    if (k >= n) break;
-    const uint32_t digit = (item[k].x >> a.shift) & (bins - 1);
-    a.pairs[s.base[digit] + s.seen[warp][digit] + rank[k]] = item[k];
+    if (k >= own.n) break;
+    const uint32_t digit = (own.item[k].x >> a.shift) & (bins - 1);
+    a.pairs[s.base[digit] + s.seen[warp][digit] + rank[k]] = own.item[k];
   }
   if (a.crossing && tile == 0 && threadIdx.x < 2) a.crossing[threadIdx.x] = 0;
 }
@@ -231,7 +237,7 @@ __global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_consta
   __shared__ SortShared s;
   wait_for_previous();
   let_next_start();
-  count_tile(a, s, blockIdx.x);
+  count_tile(a, s, blockIdx.x, Items(a, blockIdx.x));
 }
 // Many tiles: their counts become those of earlier tiles, and a digit's total.  32 digits to a block, whose warps share out
 // the tiles.  (Summing all counts in each tile would cost the square of their number.)
@@ -264,7 +270,7 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const __grid_consta
   __shared__ SortShared s;
   wait_for_previous();
   let_next_start();
-  place_tile(a, s, blockIdx.x);
+  place_tile(a, s, blockIdx.x, Items(a, blockIdx.x));
 }
 
 // Zeros to a row, by a warp: whole 16-byte units, and what lies before and behind them one by one.
@@ -337,12 +343,13 @@ __global__ void __launch_bounds__(kSortThreads) short_kernel(const __grid_consta
   const uint32_t blocks = a.pass[0].blocks;
   if (blockIdx.x < blocks) {
     for (int p = 0; p < a.passes; ++p) {
-      count_tile(a.pass[p], s, blockIdx.x);
+      const Items own(a.pass[p], blockIdx.x);
+      count_tile(a.pass[p], s, blockIdx.x, own);
       if (blocks > 1)
         tc::cluster_sync();
       else
         __syncthreads();
-      place_tile(a.pass[p], s, blockIdx.x);
+      place_tile(a.pass[p], s, blockIdx.x, own);
       if (blocks > 1)
         tc::cluster_sync();
       else
@@ -730,7 +737,7 @@ fsdp_status_t sums(SumArgs a, cudaStream_t s) {
   a.clear_blocks = (a.vocab - a.clear_from + kClearRows - 1) / kClearRows;
   const int64_t grid = (units + warps - 1) / warps + a.clear_blocks;
   a.every = a.clear_blocks > 0 ? std::max<int64_t>(1, grid / a.clear_blocks) : 1;
-  const int64_t joins = std::min<int64_t>((a.pieces - 1) * a.strips, (int64_t)device_sms() * 8);
+  const int64_t joins = std::min<int64_t>((a.pieces - 1) * a.strips, (int64_t)device_sms() * 4);
   if (grid > INT32_MAX) return fail(FSDP_EUNSUPPORTED, "the gradient is too large for one launch");
   fsdp_status_t st = launched(launch_kernel(kernel(&sum_kernel<TD, TG, VEC>), dim3((unsigned)grid), dim3(kThreads), args, 0, s, true));
   if (st == FSDP_OK && joins > 0)
