@@ -209,7 +209,7 @@ struct Names {
   uint32_t *bits;
   int32_t lo;
   bool exact;
-  __device__ __forceinline__ Names(Shared &sh, int32_t l, int32_t hi) : bits(sh.named), lo(l), exact(hi - l <= kNamed) {}
+  __device__ __forceinline__ Names(uint32_t *named, int32_t l, int32_t hi) : bits(named), lo(l), exact(hi - l <= kNamed) {}
   __device__ __forceinline__ uint32_t at(int32_t id) const {
     return exact ? (uint32_t)(id - lo) : (uint32_t)id * 2654435769u / (0xFFFFFFFFu / kNamed + 1);
   }
@@ -249,11 +249,11 @@ __device__ __noinline__ void join_entries(int top, const Teacher &e) {
 
 // The softmax over a row's entries; tokens lo .. hi - 1 are those of this block's gradient.
 template <bool DISTILL, Mode MODE>
-__device__ __forceinline__ void teacher_of(const Args &a, Shared &sh, Side &side, int64_t row, int32_t lo, int32_t hi,
+__device__ __forceinline__ void teacher_of(const Args &a, uint32_t *named, Side &side, int64_t row, int32_t lo, int32_t hi,
                                            const Ahead<DISTILL, MODE> &ahead) {
   const int lane = threadIdx.x & 31;
   const Teacher e(side, a.top);
-  const Names names(sh, lo, hi);
+  const Names names(named, lo, hi);
   float top = -INFINITY, sum = 0.0f, total = 0.0f;
   bool nan = false, twice = false;
   if (a.top <= 32 * kEach) {
@@ -366,6 +366,32 @@ __device__ __forceinline__ void feed(const Args &a, Shared &sh, uint8_t *stages,
   }
 }
 
+// What a row, or one of its slices, has beside its logits.
+template <bool DISTILL, class T, Mode MODE>
+__device__ __forceinline__ void side_of(const Args &a, uint32_t *named, Side &side, int64_t row, int32_t index, const Ahead<DISTILL, MODE> &ahead) {
+  const float up = ahead.weight * ahead.dloss;
+  if constexpr (DISTILL) {
+    if (ahead.weight != 0.0f) {
+      const Slice<T> slice(a, row, index);
+      teacher_of<DISTILL, MODE>(a, named, side, row, MODE == GRADIENT ? slice.begin() : 0, MODE == GRADIENT ? slice.end(a) : a.vocab, ahead);
+    }
+  }
+  if ((threadIdx.x & 31) == 0) {
+    side.weight = ahead.weight, side.up = up, side.lse = ahead.lse;
+    if constexpr (DISTILL) {
+      side.slope = up * a.t;
+    } else {
+      side.old = ahead.old, side.ref = ahead.ref, side.advantage = ahead.advantage, side.token = ahead.token;
+      side.mass = ahead.token >= 0 ? 1.0f : 0.0f;
+      if (MODE == GRADIENT) {
+        float l, d;
+        policy_of(a, ahead.logp, side, l, d);
+        side.slope = -d * up * a.inv_t;
+      }
+    }
+  }
+}
+
 // The tenth warp: what rows have beside their logits.
 template <bool DISTILL, class T, Mode MODE>
 __device__ __forceinline__ void prepare(const Args &a, Shared &sh, uint8_t *stages, int64_t first, int64_t step) {
@@ -378,27 +404,7 @@ __device__ __forceinline__ void prepare(const Args &a, Shared &sh, uint8_t *stag
     const int64_t row = MODE == GRADIENT ? item / a.slices : item;
     tc::bar_wait(tc::smem(&sh.done[side_at]), parity, a.wait_limit_ns, &sh.stop);
     Side &side = *reinterpret_cast<Side *>(stages + a.stages * a.stage_bytes + side_at * a.side_bytes);
-    const float up = ahead.weight * ahead.dloss;
-    if constexpr (DISTILL) {
-      if (ahead.weight != 0.0f) {
-        const Slice<T> slice(a, row, MODE == GRADIENT ? (int32_t)(item - row * a.slices) : 0);
-        teacher_of<DISTILL, MODE>(a, sh, side, row, MODE == GRADIENT ? slice.begin() : 0, MODE == GRADIENT ? slice.end(a) : a.vocab, ahead);
-      }
-    }
-    if (lane == 0) {
-      side.weight = ahead.weight, side.up = up, side.lse = ahead.lse;
-      if constexpr (DISTILL) {
-        side.slope = up * a.t;
-      } else {
-        side.old = ahead.old, side.ref = ahead.ref, side.advantage = ahead.advantage, side.token = ahead.token;
-        side.mass = ahead.token >= 0 ? 1.0f : 0.0f;
-        if (MODE == GRADIENT) {
-          float l, d;
-          policy_of(a, ahead.logp, side, l, d);
-          side.slope = -d * up * a.inv_t;
-        }
-      }
-    }
+    side_of<DISTILL, T, MODE>(a, sh.named, side, row, MODE == GRADIENT ? (int32_t)(item - row * a.slices) : 0, ahead);
     __syncwarp();
     if (lane == 0) tc::bar_arrive(tc::smem(&sh.ready[side_at]));
     if (++side_at == a.stages) side_at = 0, parity ^= 1u;
@@ -413,30 +419,34 @@ __device__ __forceinline__ float staged(const uint8_t *stage, const Slice<T> &s,
   return (float)reinterpret_cast<const T *>(stage)[element + s.phase - s.first * Slice<T>::kPer];
 }
 
-// A thread's units of a slice, as they are stored; -infinity outside the row.
-template <class T, int K>
-__device__ __forceinline__ void load_units(const Args &a, const uint8_t *stage, const Slice<T> &s, uint4 (&r)[K]) {
-  constexpr int P = Slice<T>::kPer;
-  constexpr uint32_t kNone = P == 8 ? 0xFF80FF80u : 0xFF800000u;
+// A thread's units of a slice, one in N, as they are stored; -infinity behind them.
+template <class T, int K, int N>
+__device__ __forceinline__ void load_units(const uint8_t *units, const Slice<T> &s, int t, uint4 (&r)[K]) {
+  constexpr uint32_t kNone = Slice<T>::kPer == 8 ? 0xFF80FF80u : 0xFF800000u;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int u = k * kThreads + threadIdx.x;
-    r[k] = u < s.units ? *reinterpret_cast<const uint4 *>(stage + u * 16) : make_uint4(kNone, kNone, kNone, kNone);
+    const int u = k * N + t;
+    r[k] = u < s.units ? *reinterpret_cast<const uint4 *>(units + u * 16) : make_uint4(kNone, kNone, kNone, kNone);
   }
-  if (!s.clean) {
+}
+// -infinity in the first and last unit's elements that lie outside the row.
+template <class T, int K, int N>
+__device__ __forceinline__ void mask_units(const Args &a, const Slice<T> &s, int t, uint4 (&r)[K]) {
+  constexpr int P = Slice<T>::kPer;
+  constexpr uint32_t kNone = P == 8 ? 0xFF80FF80u : 0xFF800000u;
+  if (s.clean) return;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int32_t g = s.first + k * kThreads + (int)threadIdx.x;
-      if (g != 0 && g != s.row_units - 1) continue;
-      uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+  for (int k = 0; k < K; ++k) {
+    const int32_t g = s.first + k * N + t;
+    if (g != 0 && g != s.row_units - 1) continue;
+    uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
 #pragma unroll
-      for (int e = 0; e < P; ++e) {
-        const int32_t j = g * P + e - s.phase;
-        const uint32_t bits = P == 8 ? 0xFFFFu << (e % 2 * 16) : 0xFFFFFFFFu;
-        if (j < 0 || j >= a.vocab) w[e * 4 / P] = (w[e * 4 / P] & ~bits) | (kNone & bits);
-      }
-      r[k] = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int e = 0; e < P; ++e) {
+      const int32_t j = g * P + e - s.phase;
+      const uint32_t bits = P == 8 ? 0xFFFFu << (e % 2 * 16) : 0xFFFFFFFFu;
+      if (j < 0 || j >= a.vocab) w[e * 4 / P] = (w[e * 4 / P] & ~bits) | (kNone & bits);
     }
+    r[k] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 template <class T>
@@ -482,6 +492,11 @@ struct Exponent {
 };
 __device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
 
+// Whether units of the gradient's row begin on their own boundaries.
+template <class T>
+__device__ __forceinline__ bool even_rows(const Args &a, const Slice<T> &s, const void *g_row) {
+  return ((uintptr_t)g_row - s.phase * (a.g_bf16 ? 2 : 4)) % (a.g_bf16 ? Slice<T>::kPer * 2 : 16) == 0;
+}
 // A unit's gradient.  `even`: units of the gradient's rows begin on their own boundaries.
 template <class T>
 __device__ __forceinline__ void put_unit(const Args &a, const Slice<T> &s, void *g_row, bool even, int u, const float2 (&v)[Slice<T>::kPer / 2]) {
@@ -510,26 +525,27 @@ struct Gradient {
   __device__ __forceinline__ float of(float z) const { return part * ex2((z - x.from) * x.scale); }
 };
 
-// A slice's gradient from its logits.
-template <bool DISTILL, class T, int K>
-__device__ __forceinline__ void write_slice(const Args &a, const Slice<T> &slice, const uint8_t *stage, void *g_row, bool even, int32_t token,
+// A slice's gradient from its logits: `unit(k, u)` gives unit u, the thread's k-th, of which N threads have one each.
+template <bool DISTILL, class T, int K, int N, class Unit>
+__device__ __forceinline__ void write_slice(const Args &a, const Slice<T> &slice, int t, Unit unit, void *g_row, bool even, int32_t token,
                                             const Gradient &g) {
   constexpr int P = Slice<T>::kPer;
   if (g.none) {
     float2 v[P / 2];
 #pragma unroll
     for (int i = 0; i < P / 2; ++i) v[i] = both(0.0f);
-    for (int u = threadIdx.x; u < slice.units; u += kThreads) put_unit(a, slice, g_row, even, u, v);
+    for (int u = t; u < slice.units; u += N) put_unit(a, slice, g_row, even, u, v);
     return;
   }
   const int32_t own = DISTILL ? -1 : (token + slice.phase) / P - slice.first;
   const float2 part = both(g.x.quick ? g.part * ex2(-g.x.left) : g.part);
   auto each = [&](auto quick, auto full) {
-#pragma unroll(K < 4 ? K : 4)
+#pragma unroll(K < 4 || N == 32 ? K : 4)
     for (int k = 0; k < K; ++k) {
-      const int u = k * kThreads + threadIdx.x;
+      const int u = k * N + t;
+      if (N == 32 && k * N >= slice.units) break;
       float2 v[P / 2];
-      unpack<T>(full || u < slice.units ? *reinterpret_cast<const uint4 *>(stage + u * 16) : make_uint4(0, 0, 0, 0), v);
+      unpack<T>(full || u < slice.units ? unit(k, u) : make_uint4(0, 0, 0, 0), v);
 #pragma unroll
       for (int i = 0; i < P / 2; ++i) v[i] = __fmul2_rn(ex2(quick ? g.x.quickly(v[i]) : g.x.carefully(v[i])), part);
       if (!DISTILL && own == u) {
@@ -541,7 +557,7 @@ __device__ __forceinline__ void write_slice(const Args &a, const Slice<T> &slice
   };
   if (!g.x.quick)
     each(std::false_type(), std::false_type());
-  else if (slice.units == K * kThreads)
+  else if (N > 32 && slice.units == K * N)
     each(std::true_type(), std::true_type());
   else
     each(std::true_type(), std::false_type());
@@ -556,12 +572,37 @@ __device__ __forceinline__ void write_named(const Args &a, const Slice<T> &slice
     if (ids[j] >= lo && ids[j] < hi && !(gq[j] < 0.0f)) store_any(g_row, ids[j], a.g_bf16 != 0, g.of(zt[j]) - g.slope * gq[j]);
 }
 
+// A row's results from its maximum and sum and what X its targets make of its logits; returns the slope of its gradient.
+template <bool DISTILL>
+__device__ __forceinline__ float results(const Args &a, const Side &side, int64_t row, float weight, float M, float S, float X, bool write) {
+  float loss = 0.0f, logp = 0.0f, lse = 0.0f, slope = 0.0f;
+  if (weight != 0.0f) {
+    const float log_sum = logf(S);
+    lse = fmaf(M, a.inv_t, log_sum);
+    if constexpr (DISTILL) {
+      if (side.mass != 0.0f) loss = weight * a.t * a.t * (side.q_log_q + lse - a.inv_t * X);
+      slope = side.slope;
+    } else if (side.token >= 0) {
+      logp = fmaf(X - M, a.inv_t, -log_sum);
+      policy_of(a, logp, side, loss, slope);
+      loss *= weight;
+      slope *= -side.up * a.inv_t;
+    }
+  }
+  if (write) {
+    a.loss[row] = loss, a.lse[row] = lse;
+    if (!DISTILL) a.logp[row] = logp;
+  }
+  return slope;
+}
+
 template <bool DISTILL, class T, int K, Mode MODE>
 __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages, uint32_t rank, int64_t first, int64_t step) {
   constexpr int P = Slice<T>::kPer;
   const int t = threadIdx.x, lane = t & 31, warp = t / 32;
   int stage_at = 0, side_at = 0, turn = 0;
   uint32_t parity = 0, side_parity = 0;
+  auto staged_unit = [](const uint8_t *stage) { return [stage](int, int u) { return *reinterpret_cast<const uint4 *>(stage + u * 16); }; };
   auto next = [&] {  // the stage has been read
     __syncwarp();
     if (lane == 0) tc::bar_arrive(tc::smem(&sh.empty[stage_at]));
@@ -582,9 +623,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
       __syncwarp();
       if (lane == 0) tc::bar_arrive(done);
     };
-    const int g_size = a.g_bf16 ? 2 : 4;
-    uint8_t *g_row = static_cast<uint8_t *>(a.dlogits) + row * a.ld_g * g_size;
-    auto even = [&](const Slice<T> &s) { return ((uintptr_t)g_row - s.phase * g_size) % (a.g_bf16 ? P * 2 : 16) == 0; };
+    uint8_t *g_row = static_cast<uint8_t *>(a.dlogits) + row * a.ld_g * (a.g_bf16 ? 2 : 4);
     float m = -INFINITY, sum = 0.0f, hit = 0.0f;  // of the thread, over the block's slices; what it has of the targets
     float held = 1.0f;               // what the exponentials of a row that is held are still to be multiplied by
     float2 e[MODE == HELD ? K : 1][P / 2];
@@ -607,7 +646,8 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
         }
         if constexpr (MODE != GRADIENT) {
           uint4 raw[K];
-          load_units<T, K>(a, stage, slice, raw);
+          load_units<T, K, kThreads>(stage, slice, t, raw);
+          mask_units<T, K, kThreads>(a, slice, t, raw);
           const float top = top_of<T, K>(raw);
           const Exponent x(top == -INFINITY ? 0.0f : top, a.scale);
           float2 s = both(0.0f);
@@ -642,7 +682,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
       if constexpr (MODE == GRADIENT) {
         // p = 2^((z - lse T) / T log2 e)
         const Gradient g = {Exponent(side.lse * a.t, a.scale), side.slope, side.slope, weight == 0.0f || side.mass == 0.0f};
-        write_slice<DISTILL, T, K>(a, slice, stage, g_row, even(slice), side.token, g);
+        write_slice<DISTILL, T, K, kThreads>(a, slice, t, staged_unit(stage), g_row, even_rows<T>(a, slice, g_row), side.token, g);
         if (DISTILL && !g.none) write_named(a, slice, g_row, ids, gq, zt, g);
       }
       if (MODE != HELD) next();
@@ -687,24 +727,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
       }
       ++turn;
     }
-    float loss = 0.0f, logp = 0.0f, lse = 0.0f, slope = 0.0f;
-    if (weight != 0.0f) {
-      const float log_sum = logf(S);
-      lse = fmaf(M, a.inv_t, log_sum);
-      if constexpr (DISTILL) {
-        if (side.mass != 0.0f) loss = weight * a.t * a.t * (side.q_log_q + lse - a.inv_t * X);
-        slope = side.slope;
-      } else if (side.token >= 0) {
-        logp = fmaf(X - M, a.inv_t, -log_sum);
-        policy_of(a, logp, side, loss, slope);
-        loss *= weight;
-        slope *= -side.up * a.inv_t;
-      }
-    }
-    if (t == 0 && rank == 0) {
-      a.loss[row] = loss, a.lse[row] = lse;
-      if (!DISTILL) a.logp[row] = logp;
-    }
+    const float slope = results<DISTILL>(a, side, row, weight, M, S, X, t == 0 && rank == 0);
     if constexpr (MODE == STATS) {
       leave();
       continue;
@@ -713,7 +736,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
     if constexpr (MODE == HELD) {
       const Slice<T> slice(a, row, 0);
       if (g.none) {
-        write_slice<DISTILL, T, K>(a, slice, stages, g_row, even(slice), 0, g);
+        write_slice<DISTILL, T, K, kThreads>(a, slice, t, staged_unit(stages), g_row, even_rows<T>(a, slice, g_row), 0, g);
       } else {
         const float2 by = both(g.part * (held * below(m, M, a.scale)));
         const int32_t own = DISTILL ? -1 : (side.token + slice.phase) / P;  // the token's unit
@@ -725,7 +748,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
 #pragma unroll
             for (int i = 0; i < P; ++i) element(e[k], i) -= i == (side.token + slice.phase) % P ? slope : 0.0f;
           }
-          if (k * kThreads + t < slice.units) put_unit(a, slice, g_row, even(slice), k * kThreads + t, e[k]);
+          if (k * kThreads + t < slice.units) put_unit(a, slice, g_row, even_rows<T>(a, slice, g_row), k * kThreads + t, e[k]);
         }
         if (DISTILL) write_named(a, slice, g_row, ids, gq, zt, g);
       }
@@ -734,7 +757,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
       for (int round = 0; round < a.rounds; ++round) {
         const Slice<T> slice(a, row, (int32_t)rank * a.rounds + round);
         tc::bar_wait(tc::smem(&sh.full[stage_at]), parity, a.wait_limit_ns, &sh.stop);
-        write_slice<DISTILL, T, K>(a, slice, stages + stage_at * a.stage_bytes, g_row, even(slice), side.token, g);
+        write_slice<DISTILL, T, K, kThreads>(a, slice, t, staged_unit(stages + stage_at * a.stage_bytes), g_row, even_rows<T>(a, slice, g_row), side.token, g);
         if (DISTILL && !g.none) write_named(a, slice, g_row, ids, gq, zt, g);
         next();
       }
@@ -778,6 +801,101 @@ __global__ void __launch_bounds__(kBlock, K > 2 ? blocks_of_mode(MODE) : 3) row_
     }
   }
   if (a.cluster > 1) tc::cluster_sync();  // no block leaves while another may write to it
+}
+
+// Rows of up to kShortUnits units: a warp to each, its units in registers from the only read on, its sums by shuffles. No
+// row waits for another: latencies of loads and sums are hidden by the other warps of an SM, 16 to 32 by what a row's units
+// take in registers (128 registers for 512 units and a teacher, where 96 would spill: loss and gradient of 16384 x 4096 69 us, 76).
+constexpr int kShortUnits = 512;
+constexpr int kShortTop = 32 * kEach;
+constexpr int kShortThreads = 128;
+template <bool DISTILL, class T, int K, Mode MODE>
+__global__ void __launch_bounds__(kShortThreads, K > 4 ? (DISTILL ? 4 : 5) : 8) short_kernel(const __grid_constant__ Args a) {
+  constexpr int P = Slice<T>::kPer, kWords = K * P;
+  extern __shared__ __align__(16) uint8_t sides[];  // of each warp: its row's side, and a bit for each token
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  constexpr int kNames = DISTILL && MODE != STATS ? kWords : 0;
+  Side &side = *reinterpret_cast<Side *>(sides + warp * (a.side_bytes + kNames * 4));
+  uint32_t *named = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(&side) + a.side_bytes);
+  for (int i = lane; i < kNames; i += 32) named[i] = 0;
+  __syncwarp();
+  wait_for_previous();
+  let_next_start();
+  const int64_t row = (int64_t)blockIdx.x * (kShortThreads / 32) + warp;
+  if (row >= a.rows) return;
+  Ahead<DISTILL, MODE> ahead;
+  ahead.load(a, row);
+  const Slice<T> slice(a, row, 0);
+  const T *z_row = static_cast<const T *>(a.logits) + row * a.ld_z;
+  uint8_t *g_row = static_cast<uint8_t *>(a.dlogits) + row * a.ld_g * (a.g_bf16 ? 2 : 4);
+  const float weight = ahead.weight;
+  uint4 raw[K];
+  float zt[kEach];  // the targets' logits
+  if (weight != 0.0f) {
+    load_units<T, K, 32>(reinterpret_cast<const uint8_t *>(slice.at), slice, lane, raw);
+    if constexpr (DISTILL) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) zt[i] = ahead.id[i] >= 0 ? (float)z_row[ahead.id[i]] : 0.0f;
+    } else if (MODE != GRADIENT) {
+      zt[0] = ahead.token >= 0 ? (float)z_row[ahead.token] : 0.0f;
+    }
+  }
+  side_of<DISTILL, T, MODE>(a, named, side, row, 0, ahead);
+  __syncwarp();
+  const Teacher teacher(side, a.top);
+  Gradient g = {Exponent(side.lse * a.t, a.scale), side.slope, side.slope, weight == 0.0f || side.mass == 0.0f};
+  if constexpr (MODE != GRADIENT) {
+    float M = 0.0f, S = 1.0f, X = 0.0f;
+    if (weight != 0.0f) {
+      mask_units<T, K, 32>(a, slice, lane, raw);
+      const float m = top_of<T, K>(raw);
+      const Exponent x(m == -INFINITY ? 0.0f : m, a.scale);
+      float2 s = both(0.0f);
+      auto each = [&](auto quick) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (k * 32 >= slice.units) break;
+          float2 z[P / 2];
+          unpack<T>(raw[k], z);
+#pragma unroll
+          for (int i = 0; i < P / 2; ++i) s = __fadd2_rn(s, ex2(quick ? x.quickly(z[i]) : x.carefully(z[i])));
+        }
+      };
+      float whole = 1.0f;
+      if (__all_sync(0xFFFFFFFFu, x.quick)) {
+        each(std::true_type());
+        whole = ex2(-x.left);
+      } else {
+        each(std::false_type());
+      }
+      if constexpr (DISTILL) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const int j = i * 32 + lane;
+          if (j < a.top && teacher.ids[j] >= 0 && (teacher.q[j] > 0.0f || teacher.q[j] != teacher.q[j])) X += teacher.q[j] * zt[i];
+        }
+        X = warp_sum(X);
+      } else {
+        X = zt[0];
+      }
+      M = warp_max(m);
+      S = warp_sum((s.x + s.y) * whole * below(m, M, a.scale));
+    }
+    const float slope = results<DISTILL>(a, side, row, weight, M, S, X, lane == 0);
+    g = {Exponent(M, a.scale), slope / S, slope, g.none};
+  }
+  if constexpr (MODE != STATS) {
+    write_slice<DISTILL, T, K, 32>(a, slice, lane, [&](int k, int) { return raw[k]; }, g_row, even_rows<T>(a, slice, g_row), side.token, g);
+    if constexpr (DISTILL) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int j = i * 32 + lane;
+        if (!g.none && j < a.top && teacher.ids[j] >= 0 && !(teacher.gq[j] < 0.0f))
+          store_any(g_row, teacher.ids[j], a.g_bf16 != 0, g.of(zt[i]) - g.slope * teacher.gq[j]);
+      }
+    }
+  }
 }
 
 // ---- host --------------------------------------------------------------------------------
@@ -875,8 +993,30 @@ cudaError_t launch_rows(Args &a, cudaStream_t s) {
   return launch_kernel(fn, dim3((unsigned)grid), dim3(kBlock), args, (size_t)smem, s, true, a.cluster);
 }
 
+template <bool DISTILL, class T, Mode MODE>
+cudaError_t launch_short(Args &a, cudaStream_t s) {
+  constexpr int kRows = kShortThreads / 32, kFew = kShortUnits / 4;  // rows of a block; units of the shortest rows
+  const bool few = units_of<T>(a) <= kFew;
+  a.cluster = a.rounds = a.slices = 1;
+  a.units = kShortUnits, a.items = a.rows;
+  a.side_bytes = ((int)sizeof(Side) + (DISTILL ? a.top * 16 : 0) + 15) / 16 * 16;
+  const int smem = kRows * (a.side_bytes + (DISTILL && MODE != STATS ? (few ? kFew : kShortUnits) * Slice<T>::kPer / 8 : 0));
+  static_assert(kRows * ((int)sizeof(Side) + kShortTop * 16 + kShortUnits) <= 48 * 1024, "more than any kernel may have");
+  const void *fn = few ? kernel(&short_kernel<DISTILL, T, kFew / 32, MODE>) : kernel(&short_kernel<DISTILL, T, kShortUnits / 32, MODE>);
+  void *args[] = {&a};
+  return launch_kernel(fn, dim3((unsigned)((a.rows + kRows - 1) / kRows)), dim3(kShortThreads), args, (size_t)smem, s, true);
+}
+
 template <bool DISTILL, class T>
 cudaError_t launch_as(Args &a, cudaStream_t s) {
+  // Rows of whole blocks are bound by the latency of their sums, one after the other; a warp to each is slower only where a
+  // gradient's rows are too few for all SMs (us by block / by warp, distillation in BF16: loss alone 16384 x 4096 93 / 37, 16 x 4096
+  // 4.6 / 3.7; with gradient 16384 x 4096 117 / 69, 16384 x 512 93 / 19, 1024 x 4096 9.4 / 8.0, 512 x 4096 6.6 / 6.8).
+  const bool gradient = a.backward || a.dlogits;
+  if (units_of<T>(a) <= kShortUnits && a.top <= kShortTop && (!gradient || a.rows > 4 * device_sms())) {
+    if (a.backward) return launch_short<DISTILL, T, GRADIENT>(a, s);
+    return a.dlogits ? launch_short<DISTILL, T, HELD>(a, s) : launch_short<DISTILL, T, STATS>(a, s);
+  }
   if (a.backward) return launch_rows<DISTILL, T, GRADIENT>(a, s);
   if (!a.dlogits) return launch_rows<DISTILL, T, STATS>(a, s);
   if (units_of<T>(a) <= kThreads * kMostUnits) return launch_rows<DISTILL, T, HELD>(a, s);

@@ -417,3 +417,72 @@ def test_binding_refusals():
             fp.fsdp_policy_loss_forward(z, tok, v, v, v, v, v, **kw)
     with pytest.raises(fp.FsdpError, match="dlogits is logits"):
         fp.fsdp_policy_loss_forward(z, tok, v, v, v, v, v, dlogits=z.view(BF16)[:, :50])
+
+
+MANY = 1000  # rows, of which short ones go to a warp each
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("vocab", [1, 7, 33, 512, 513, 1021, 2048, 2049, 4089, 4096])
+def test_many_short_rows(vocab, dtype):
+    check_distill(fp_module(), *distill_data(MANY, vocab, 13, vocab, dtype), t=0.8)
+    check_policy(fp_module(), *policy_data(MANY, vocab, vocab, dtype, t=0.8), t=0.8)
+
+
+@pytest.mark.parametrize("ld,offset", [(1000, 1), (1003, 0), (1008, 8), (1001, 3)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_short_rows_apart(ld, offset, dtype):
+    other = F32 if dtype == BF16 else BF16
+    check_distill(fp_module(), *distill_data(MANY, 1000, 9, ld, dtype), ld=ld, offset=offset, ld_t=11, g_dtype=other)
+    check_distill(fp_module(), *distill_data(MANY, 1000, 9, ld, dtype), ld=ld, offset=offset, in_place=True)
+    check_policy(fp_module(), *policy_data(MANY, 1000, ld, dtype), ld=ld, offset=offset, g_dtype=other)
+    check_policy(fp_module(), *policy_data(MANY, 1000, ld, dtype), ld=ld, offset=offset, in_place=True)
+
+
+@pytest.mark.parametrize("top", [1, 32, 33, 128, 129])
+def test_tops_of_many_short_rows(top):
+    check_distill(fp_module(), *distill_data(MANY, 300, top, top, BF16, torch.int32))
+
+
+def test_tokens_named_more_than_once_in_many_short_rows():
+    logits, ids, teacher, w = distill_data(MANY, 700, 40, 8, F32)
+    ids[::4] = 3
+    ids[1::4] = ids[1::4, :20].repeat(1, 2)
+    ids[2::4, 5], ids[2::4, 30] = 699, 699
+    ids[3::4, ::3] = 0
+    check_distill(fp_module(), logits, ids, teacher, None)
+
+
+def test_specials_in_many_short_rows():
+    """The rows of ``test_specials`` and of ``test_rows_without_entries_and_without_weight``, over and over."""
+    fp = fp_module()
+    n = MANY // 8
+    logits, ids, old, ref, adv, _ = policy_data(8, 600, 12)
+    ids = ids.clamp(0, 599)
+    logits[0, 5], logits[1, 599], logits[2], logits[3, 7] = float("nan"), INF, -INF, 3e38
+    logits[4], logits[4, 9] = -INF, float("nan")
+    logits[5, 300:], ids[5] = -3e38, 5
+    g = torch.empty(8 * n, 600, device="cuda")
+    out = [torch.empty(8 * n, device="cuda") for _ in range(3)]
+    many = [v.repeat(n, *[1] * (v.dim() - 1)).cuda() for v in (logits, ids, old, ref, adv)]
+    fp.fsdp_policy_loss_forward(many[0], many[1], many[2], many[4], *out, ref_logp=many[3], kl=0.1, dlogits=g)
+    first = torch.arange(0, 8 * n, 8)
+    assert all(bool(torch.isnan(g[first + r]).all()) for r in (0, 1, 2, 4)) and all(bool(torch.isfinite(g[first + r]).all()) for r in (5, 6, 7))
+    assert all(bool(torch.isnan(out[2][first + r]).all()) for r in (0, 1, 4))
+    assert bool((out[2][first + 2] == -INF).all()) and bool((out[2][first + 3] == logits[3, 7].item()).all())
+
+    logits, ids, teacher, w = distill_data(8, 600, 6, 2, F32, masked=False)
+    w = torch.ones(8)
+    ids[0], teacher[1], ids[2, :5], teacher[3, 2:] = -1, -INF, -7, -INF
+    w[4], logits[4], logits[5, ids[5, 0]] = 0, float("nan"), -INF
+    teacher[6, 0], logits[6, ids[6, 0]] = -INF, -INF
+    want = distill_reference(torch.where(w[:, None] == 0, 0.0, logits), ids, teacher, 1.0, w.double(), torch.ones(8, dtype=F64))
+    want = {k: v.repeat(n, *[1] * (v.dim() - 1)) for k, v in want.items()}
+    many = [v.repeat(n, *[1] * (v.dim() - 1)).cuda() for v in (logits, ids, teacher, w)]
+    loss, lse = (torch.empty(8 * n, device="cuda") for _ in range(2))
+    fp.fsdp_distill_loss_forward(*many[:3], loss, lse, weight=many[3], dlogits=g)
+    expect(g, want["grad"], want["grad_tol"], F32, "dlogits")
+    expect(loss, want["loss"], want["loss_tol"], F32, "loss")
+    assert bool((lse[first + 4] == 0).all())
+    fp.fsdp_distill_loss_backward(*many[:3], lse, g, weight=many[3])
+    expect(g, want["grad"], want["grad_tol"], F32, "dlogits of the backward call")
