@@ -980,7 +980,7 @@ cudaError_t launch_rows(Args &a, cudaStream_t s) {
   a.stage_bytes = (a.units * 16 + 127) / 128 * 128;
   a.side_bytes = ((int)sizeof(Side) + (DISTILL ? a.top * 16 : 0) + 127) / 128 * 128;
   a.stages = kMaxStages;  // as many as leave room for the SM's other blocks
-  while (a.stages > 2 && a.stages * (a.stage_bytes + a.side_bytes) > (227 * 1024) / kBlocks - 6 * 1024) --a.stages;
+  while (a.stages > 2 && a.stages * (a.stage_bytes + a.side_bytes) > std::min(kMostSmem, (227 * 1024) / kBlocks - 6 * 1024)) --a.stages;
   const int smem = a.stages * (a.stage_bytes + a.side_bytes);
   int clusters = 0;
   cudaError_t e = resident(fn, a.cluster, smem, &clusters);

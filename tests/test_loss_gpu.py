@@ -486,3 +486,9 @@ def test_specials_in_many_short_rows():
     assert bool((lse[first + 4] == 0).all())
     fp.fsdp_distill_loss_backward(*many[:3], lse, g, weight=many[3])
     expect(g, want["grad"], want["grad_tol"], F32, "dlogits of the backward call")
+
+
+@pytest.mark.parametrize("vocab,top", [(13000, 64), (13100, 64), (13184, 9), (26200, 64), (40000, 216), (40000, 230), (131072, 240)])
+def test_rings_that_nearly_fill_an_sm(vocab, top):
+    """Slices and teacher's entries of which three or four take 106 to 108 KB: one stage fewer."""
+    check_distill(fp_module(), *distill_data(5, vocab, top, 1, BF16, torch.int32))
