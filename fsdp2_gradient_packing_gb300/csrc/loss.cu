@@ -40,10 +40,12 @@ constexpr int64_t kL2Rows = 40 << 20;  // bytes of rows that are read twice whil
 constexpr float kLog2E = 1.4426950408889634f;
 
 enum Mode { STATS, HELD, TWICE, GRADIENT };
-// Blocks of an SM.  Gradients alone only stream, and want many blocks more than deep rings (4096 x 131072 BF16: three
-// blocks of two stages 319 us, two of three 369); rows that are read twice want two blocks of three stages (8192 x 32768 BF16:
-// 177 us, two stages 194, three blocks of half as long slices 188).
-constexpr int blocks_of_mode(Mode m) { return m == GRADIENT ? 3 : 2; }
+// Blocks of an SM (three of the kernels for slices of up to 512 units), and stages of a ring. Rows that are read twice want deep
+// rings (8192 x 32768 BF16: three stages 177 us, two 194, three blocks of half as long slices 188). Gradients alone want few and long
+// slices under way, which DRAM's pages like (4096 x 131072 BF16: two blocks of two stages 328 us, three of two 346, two of three
+// 369, three of two half as long 372).
+constexpr int kBlocks = 2;
+constexpr int stages_of_mode(Mode m) { return m == GRADIENT ? 2 : kMaxStages; }
 
 struct Args {
   const void *logits;
@@ -148,6 +150,30 @@ __device__ __forceinline__ void policy_of(const Args &a, float logp, const Side 
 // ---- the ninth and the tenth warp ------------------------------------------------------------------------
 constexpr int kEach = 4;  // teacher's entries that a lane holds in registers: up to 128 in all
 
+// Entries j, j + 32 and so on of a row of the teacher's. Types are asked for once, so that all loads are under way together.
+template <int N>
+__device__ __forceinline__ void load_entries(const Args &a, int64_t row, int j, int32_t (&id)[N], float (&v)[N]) {
+  auto ids = [&](const auto *p) {
+    std::remove_cv_t<std::remove_pointer_t<decltype(p)>> t[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) t[i] = j + i * 32 < a.top ? p[i * 32] : -1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) id[i] = t[i] >= 0 && t[i] < a.vocab ? (int32_t)t[i] : -1;
+  };
+  auto logits = [&](const auto *p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = j + i * 32 < a.top ? (float)p[i * 32] : 0.0f;
+  };
+  if (a.teacher_bf16)
+    logits(static_cast<const __nv_bfloat16 *>(a.teacher) + row * a.ld_teacher + j);
+  else
+    logits(static_cast<const float *>(a.teacher) + row * a.ld_teacher + j);
+  if (a.wide)
+    ids(static_cast<const int64_t *>(a.tokens) + row * a.ld_tokens + j);
+  else
+    ids(static_cast<const int32_t *>(a.tokens) + row * a.ld_tokens + j);
+}
+
 // What a row has beside its logits, on its way while the row before is prepared.
 template <bool DISTILL, Mode MODE>
 struct Ahead {
@@ -165,12 +191,7 @@ struct Ahead {
     }
     if constexpr (DISTILL) {
       if (a.top <= 32 * kEach) {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-          const int j = i * 32 + lane;
-          id[i] = j < a.top ? token_at(a, row * a.ld_tokens + j) : -1;
-          v[i] = j < a.top ? load_any(a.teacher, row * a.ld_teacher + j, a.teacher_bf16) : 0.0f;
-        }
+        load_entries<kEach>(a, row, lane, id, v);
       }
     } else {
       if (MODE == GRADIENT) logp = a.logp_in[row];
@@ -292,39 +313,61 @@ __device__ __forceinline__ void teacher_of(const Args &a, uint32_t *named, Side 
       }
     }
   } else {
-#pragma unroll 8
-    for (int j = lane; j < a.top; j += 32) {
-      const int32_t id = token_at(a, row * a.ld_tokens + j);
-      const float x = id < 0 ? -INFINITY : load_any(a.teacher, row * a.ld_teacher + j, a.teacher_bf16) * a.inv_t;
-      e.ids[j] = x == -INFINITY ? -1 : id;
-      e.z[j] = x;
-      top = fmaxf(top, x);
-      nan |= x != x;
+// Several entries of a lane at a time, all loads before the first store: a store to shared memory may, for all
+    // that the compiler knows, be to what the next load reads.
+    constexpr int N = 8;
+    int32_t id[N];
+    float x[N];
+    for (int j0 = lane; j0 < a.top; j0 += 32 * N) {
+      load_entries<N>(a, row, j0, id, x);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        x[i] = id[i] < 0 ? -INFINITY : x[i] * a.inv_t;
+        if (x[i] == -INFINITY) id[i] = -1;
+        top = fmaxf(top, x[i]);
+        nan |= x[i] != x[i];
+        if (j0 + i * 32 < a.top) e.ids[j0 + i * 32] = id[i], e.z[j0 + i * 32] = x[i];
+      }
     }
     top = warp_max(top);
-#pragma unroll 8
-    for (int j = lane; j < a.top; j += 32) {
-      const float d = e.z[j] - top, p = e.ids[j] < 0 ? 0.0f : ex2(d * kLog2E);
-      sum += p;
-      if (p > 0.0f || p != p) total += p * d;
-      e.q[j] = p;
+    for (int j0 = lane; j0 < a.top; j0 += 32 * N) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = j0 + i * 32 < a.top ? e.z[j0 + i * 32] : -INFINITY;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float d = x[i] - top, p = x[i] == -INFINITY ? 0.0f : ex2(d * kLog2E);
+        sum += p;
+        if (p > 0.0f || p != p) total += p * d;
+        if (j0 + i * 32 < a.top) e.q[j0 + i * 32] = p;
+      }
     }
     sum = warp_sum(sum), total = warp_sum(total);
     const float inv = 1.0f / sum;
-#pragma unroll 8
-    for (int j = lane; j < a.top; j += 32) {
-      const int32_t id = e.ids[j];
-      e.q[j] = e.gq[j] = id < 0 ? 0.0f : e.q[j] * inv;
-      if (MODE != STATS) {
-        const bool again = id >= lo && id < hi && names.name(id);
-        e.z[j] = again ? 1.0f : 0.0f;
-        twice |= again;
+    for (int j0 = lane; j0 < a.top; j0 += 32 * N) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const bool here = j0 + i * 32 < a.top;
+        id[i] = here ? e.ids[j0 + i * 32] : -1, x[i] = here ? e.q[j0 + i * 32] : 0.0f;
+      }
+      bool again[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) again[i] = MODE != STATS && id[i] >= lo && id[i] < hi && names.name(id[i]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int j = j0 + i * 32;
+        twice |= again[i];
+        if (j >= a.top) continue;
+        e.q[j] = e.gq[j] = id[i] < 0 ? 0.0f : x[i] * inv;
+        if (MODE != STATS) e.z[j] = again[i] ? 1.0f : 0.0f;
       }
     }
     if (MODE != STATS) {
       __syncwarp();
-      for (int j = lane; j < a.top; j += 32)
-        if (e.ids[j] >= lo && e.ids[j] < hi) names.forget(e.ids[j]);
+#pragma unroll 8
+      for (int j = lane; j < a.top; j += 32) {
+        const int32_t k = e.ids[j];
+        if (k >= lo && k < hi) names.forget(k);
+      }
     }
   }
   __syncwarp();
@@ -337,6 +380,12 @@ __device__ __forceinline__ void teacher_of(const Args &a, uint32_t *named, Side 
 // The ninth warp (one lane of it): slices into the ring.
 template <class T, Mode MODE>
 __device__ __forceinline__ void feed(const Args &a, Shared &sh, uint8_t *stages, uint32_t rank, int64_t first, int64_t step) {
+  // What L2 is to make of a row that is read again soon, and of one that is not (4096 x 131072 BF16 with and without, BF16 gradients
+  // of rows that are read twice stored as what nothing reads again: loss and gradient 389 / 397 us, gradient alone 328 / 329;
+  // 8192 x 32768 174 / 176, 166 / 169).
+  uint64_t again, once;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(again));
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
   int stage = 0;
   uint32_t parity = 1;
   auto weight_of = [&](int64_t item) { return item < a.items && a.weight ? a.weight[MODE == GRADIENT ? item / a.slices : item] : 1.0f; };
@@ -353,10 +402,15 @@ __device__ __forceinline__ void feed(const Args &a, Shared &sh, uint8_t *stages,
       tc::bar_wait(tc::smem(&sh.empty[stage]), parity, a.wait_limit_ns, &sh.stop);
       if (weight != 0.0f && slice.units > 0 && !skip) {
         tc::bar_expect(full, slice.units * 16);
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                         tc::smem(stages + stage * a.stage_bytes)),
-                     "l"(slice.at), "r"(slice.units * 16), "r"(full)
-                     : "memory");
+        const uint32_t to = tc::smem(stages + stage * a.stage_bytes), bytes = slice.units * 16;
+        if constexpr (MODE == GRADIENT || MODE == TWICE)
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(to),
+                       "l"(slice.at), "r"(bytes), "r"(full), "l"(MODE == TWICE && turn < a.rounds ? again : once)
+                       : "memory");
+        else
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(slice.at),
+                       "r"(bytes), "r"(full)
+                       : "memory");
       } else if (!skip) {
         tc::bar_arrive(full);
       }
@@ -498,13 +552,17 @@ __device__ __forceinline__ bool even_rows(const Args &a, const Slice<T> &s, cons
   return ((uintptr_t)g_row - s.phase * (a.g_bf16 ? 2 : 4)) % (a.g_bf16 ? Slice<T>::kPer * 2 : 16) == 0;
 }
 // A unit's gradient.  `even`: units of the gradient's rows begin on their own boundaries.
-template <class T>
+template <class T, Mode MODE>
 __device__ __forceinline__ void put_unit(const Args &a, const Slice<T> &s, void *g_row, bool even, int u, const float2 (&v)[Slice<T>::kPer / 2]) {
   constexpr int P = Slice<T>::kPer;
   const int32_t j = (s.first + u) * P - s.phase;
   if (even && (s.clean || (j >= 0 && j + P <= a.vocab))) {
     if constexpr (P == 8) {
-      store8(g_row, j, a.g_bf16 != 0, v);
+      if (MODE == TWICE && a.g_bf16)
+        __stcs(reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(g_row) + j),
+               make_uint4(bf16_pair(v[0].x, v[0].y), bf16_pair(v[1].x, v[1].y), bf16_pair(v[2].x, v[2].y), bf16_pair(v[3].x, v[3].y)));
+      else
+        store8(g_row, j, a.g_bf16 != 0, v);
     } else if (a.g_bf16) {
       *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(g_row) + j) = make_uint2(bf16_pair(v[0].x, v[0].y), bf16_pair(v[1].x, v[1].y));
     } else {
@@ -526,7 +584,7 @@ struct Gradient {
 };
 
 // A slice's gradient from its logits: `unit(k, u)` gives unit u, the thread's k-th, of which N threads have one each.
-template <bool DISTILL, class T, int K, int N, class Unit>
+template <bool DISTILL, class T, int K, int N, Mode MODE, class Unit>
 __device__ __forceinline__ void write_slice(const Args &a, const Slice<T> &slice, int t, Unit unit, void *g_row, bool even, int32_t token,
                                             const Gradient &g) {
   constexpr int P = Slice<T>::kPer;
@@ -534,7 +592,7 @@ __device__ __forceinline__ void write_slice(const Args &a, const Slice<T> &slice
     float2 v[P / 2];
 #pragma unroll
     for (int i = 0; i < P / 2; ++i) v[i] = both(0.0f);
-    for (int u = t; u < slice.units; u += N) put_unit(a, slice, g_row, even, u, v);
+    for (int u = t; u < slice.units; u += N) put_unit<T, MODE>(a, slice, g_row, even, u, v);
     return;
   }
   const int32_t own = DISTILL ? -1 : (token + slice.phase) / P - slice.first;
@@ -552,7 +610,7 @@ __device__ __forceinline__ void write_slice(const Args &a, const Slice<T> &slice
 #pragma unroll
         for (int i = 0; i < P; ++i) element(v, i) -= i == (token + slice.phase) % P ? g.slope : 0.0f;
       }
-      if (full || u < slice.units) put_unit(a, slice, g_row, even, u, v);
+      if (full || u < slice.units) put_unit<T, MODE>(a, slice, g_row, even, u, v);
     }
   };
   if (!g.x.quick)
@@ -682,7 +740,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
       if constexpr (MODE == GRADIENT) {
         // p = 2^((z - lse T) / T log2 e)
         const Gradient g = {Exponent(side.lse * a.t, a.scale), side.slope, side.slope, weight == 0.0f || side.mass == 0.0f};
-        write_slice<DISTILL, T, K, kThreads>(a, slice, t, staged_unit(stage), g_row, even_rows<T>(a, slice, g_row), side.token, g);
+        write_slice<DISTILL, T, K, kThreads, MODE>(a, slice, t, staged_unit(stage), g_row, even_rows<T>(a, slice, g_row), side.token, g);
         if (DISTILL && !g.none) write_named(a, slice, g_row, ids, gq, zt, g);
       }
       if (MODE != HELD) next();
@@ -736,7 +794,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
     if constexpr (MODE == HELD) {
       const Slice<T> slice(a, row, 0);
       if (g.none) {
-        write_slice<DISTILL, T, K, kThreads>(a, slice, t, staged_unit(stages), g_row, even_rows<T>(a, slice, g_row), 0, g);
+        write_slice<DISTILL, T, K, kThreads, MODE>(a, slice, t, staged_unit(stages), g_row, even_rows<T>(a, slice, g_row), 0, g);
       } else {
         const float2 by = both(g.part * (held * below(m, M, a.scale)));
         const int32_t own = DISTILL ? -1 : (side.token + slice.phase) / P;  // the token's unit
@@ -748,7 +806,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
 #pragma unroll
             for (int i = 0; i < P; ++i) element(e[k], i) -= i == (side.token + slice.phase) % P ? slope : 0.0f;
           }
-          if (k * kThreads + t < slice.units) put_unit(a, slice, g_row, even_rows<T>(a, slice, g_row), k * kThreads + t, e[k]);
+          if (k * kThreads + t < slice.units) put_unit<T, MODE>(a, slice, g_row, even_rows<T>(a, slice, g_row), k * kThreads + t, e[k]);
         }
         if (DISTILL) write_named(a, slice, g_row, ids, gq, zt, g);
       }
@@ -757,7 +815,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
       for (int round = 0; round < a.rounds; ++round) {
         const Slice<T> slice(a, row, (int32_t)rank * a.rounds + round);
         tc::bar_wait(tc::smem(&sh.full[stage_at]), parity, a.wait_limit_ns, &sh.stop);
-        write_slice<DISTILL, T, K, kThreads>(a, slice, t, staged_unit(stages + stage_at * a.stage_bytes), g_row, even_rows<T>(a, slice, g_row), side.token, g);
+        write_slice<DISTILL, T, K, kThreads, MODE>(a, slice, t, staged_unit(stages + stage_at * a.stage_bytes), g_row, even_rows<T>(a, slice, g_row), side.token, g);
         if (DISTILL && !g.none) write_named(a, slice, g_row, ids, gq, zt, g);
         next();
       }
@@ -767,7 +825,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
 }
 
 template <bool DISTILL, class T, int K, Mode MODE>
-__global__ void __launch_bounds__(kBlock, K > 2 ? blocks_of_mode(MODE) : 3) row_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kBlock, K > 2 ? kBlocks : 3) row_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ Shared sh;
   if (threadIdx.x == 0) {
@@ -885,7 +943,7 @@ __global__ void __launch_bounds__(kShortThreads, K > 4 ? (DISTILL ? 4 : 5) : 8) 
     g = {Exponent(M, a.scale), slope / S, slope, g.none};
   }
   if constexpr (MODE != STATS) {
-    write_slice<DISTILL, T, K, 32>(a, slice, lane, [&](int k, int) { return raw[k]; }, g_row, even_rows<T>(a, slice, g_row), side.token, g);
+    write_slice<DISTILL, T, K, 32, MODE>(a, slice, lane, [&](int k, int) { return raw[k]; }, g_row, even_rows<T>(a, slice, g_row), side.token, g);
     if constexpr (DISTILL) {
       __syncwarp();
 #pragma unroll
@@ -957,7 +1015,6 @@ int64_t units_of(const Args &a) {
 
 template <bool DISTILL, class T, Mode MODE>
 cudaError_t launch_rows(Args &a, cudaStream_t s) {
-  constexpr int kBlocks = blocks_of_mode(MODE);
   constexpr int64_t kMost = kThreads * kMostUnits;
   const int64_t row_units = units_of<T>(a);
   a.cluster = a.rounds = a.slices = 1;
@@ -979,8 +1036,8 @@ cudaError_t launch_rows(Args &a, cudaStream_t s) {
   const void *fn = small ? kernel(&row_kernel<DISTILL, T, 2, MODE>) : kernel(&row_kernel<DISTILL, T, kMostUnits, MODE>);
   a.stage_bytes = (a.units * 16 + 127) / 128 * 128;
   a.side_bytes = ((int)sizeof(Side) + (DISTILL ? a.top * 16 : 0) + 127) / 128 * 128;
-  a.stages = kMaxStages;  // as many as leave room for the SM's other blocks
-  while (a.stages > 2 && a.stages * (a.stage_bytes + a.side_bytes) > std::min(kMostSmem, (227 * 1024) / kBlocks - 6 * 1024)) --a.stages;
+  a.stages = stages_of_mode(MODE);  // as many as leave room for the SM's other blocks
+  while (a.stages > 2 && a.stages * (a.stage_bytes + a.side_bytes) > kMostSmem) --a.stages;
   const int smem = a.stages * (a.stage_bytes + a.side_bytes);
   int clusters = 0;
   cudaError_t e = resident(fn, a.cluster, smem, &clusters);
