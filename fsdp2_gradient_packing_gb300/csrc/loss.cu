@@ -598,10 +598,10 @@ __device__ __forceinline__ void write_slice(const Args &a, const Slice<T> &slice
   const int32_t own = DISTILL ? -1 : (token + slice.phase) / P - slice.first;
   const float2 part = both(g.x.quick ? g.part * ex2(-g.x.left) : g.part);
   auto each = [&](auto quick, auto full) {
-#pragma unroll(K < 4 || N == 32 ? K : 4)
+#pragma unroll(K < 4 || N < kThreads ? K : 4)
     for (int k = 0; k < K; ++k) {
       const int u = k * N + t;
-      if (N == 32 && k * N >= slice.units) break;
+      if (N < kThreads && k * N >= slice.units) break;
       float2 v[P / 2];
       unpack<T>(full || u < slice.units ? unit(k, u) : make_uint4(0, 0, 0, 0), v);
 #pragma unroll
@@ -615,7 +615,7 @@ __device__ __forceinline__ void write_slice(const Args &a, const Slice<T> &slice
   };
   if (!g.x.quick)
     each(std::false_type(), std::false_type());
-  else if (N > 32 && slice.units == K * N)
+  else if (N == kThreads && slice.units == K * N)
     each(std::true_type(), std::true_type());
   else
     each(std::true_type(), std::false_type());
@@ -861,28 +861,39 @@ __global__ void __launch_bounds__(kBlock, K > 2 ? kBlocks : 3) row_kernel(const 
   if (a.cluster > 1) tc::cluster_sync();  // no block leaves while another may write to it
 }
 
-// Rows of up to kShortUnits units: a warp to each, its units in registers from the only read on, its sums by shuffles. No
-// row waits for another: latencies of loads and sums are hidden by the other warps of an SM, 16 to 32 by what a row's units
-// take in registers (128 registers for 512 units and a teacher, where 96 would spill: loss and gradient of 16384 x 4096 69 us, 76).
-constexpr int kShortUnits = 512;
-constexpr int kShortTop = 32 * kEach;
+// Short rows, many of them: G warps to each, its units in registers from the only read on. No row waits for another:
+// latencies of loads and sums are hidden by the other warps of an SM, 16 to 32 by what a row's units take in registers
+// (128 registers for 16 units of a lane and a teacher, where 96 would spill: loss and gradient of 16384 x 4096 69 us, 76).
 constexpr int kShortThreads = 128;
-template <bool DISTILL, class T, int K, Mode MODE>
+constexpr int kShortTop = 32 * kEach;
+template <bool DISTILL, class T, int K, int G, Mode MODE>
 __global__ void __launch_bounds__(kShortThreads, K > 4 ? (DISTILL ? 4 : 5) : 8) short_kernel(const __grid_constant__ Args a) {
-  constexpr int P = Slice<T>::kPer, kWords = K * P;
-  extern __shared__ __align__(16) uint8_t sides[];  // of each warp: its row's side, and a bit for each token
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  constexpr int kNames = DISTILL && MODE != STATS ? kWords : 0;
-  Side &side = *reinterpret_cast<Side *>(sides + warp * (a.side_bytes + kNames * 4));
+  constexpr int P = Slice<T>::kPer, N = 32 * G, kNames = DISTILL && MODE != STATS ? K * P * G : 0;
+  extern __shared__ __align__(16) uint8_t sides[];  // of each row: its side, and a bit for each token
+  __shared__ float4 meet[kShortThreads / 32];
+  const int t = threadIdx.x % N, lane = t % 32, group = threadIdx.x / N;
+  const bool leads = t < 32;  // the warp that deals with what the row has beside its logits
+  Side &side = *reinterpret_cast<Side *>(sides + group * (a.side_bytes + kNames * 4));
   uint32_t *named = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(&side) + a.side_bytes);
-  for (int i = lane; i < kNames; i += 32) named[i] = 0;
-  __syncwarp();
+  auto sync = [&] {
+    if constexpr (G == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(N) : "memory");
+  };
+  if (leads) {
+    for (int i = lane; i < kNames; i += 32) named[i] = 0;
+    __syncwarp();
+  }
   wait_for_previous();
   let_next_start();
-  const int64_t row = (int64_t)blockIdx.x * (kShortThreads / 32) + warp;
+  const int64_t row = (int64_t)blockIdx.x * (kShortThreads / N) + group;
   if (row >= a.rows) return;
   Ahead<DISTILL, MODE> ahead;
-  ahead.load(a, row);
+  if (leads)
+    ahead.load(a, row);
+  else if (a.weight)
+    ahead.weight = a.weight[row];
   const Slice<T> slice(a, row, 0);
   const T *z_row = static_cast<const T *>(a.logits) + row * a.ld_z;
   uint8_t *g_row = static_cast<uint8_t *>(a.dlogits) + row * a.ld_g * (a.g_bf16 ? 2 : 4);
@@ -890,29 +901,34 @@ __global__ void __launch_bounds__(kShortThreads, K > 4 ? (DISTILL ? 4 : 5) : 8) 
   uint4 raw[K];
   float zt[kEach];  // the targets' logits
   if (weight != 0.0f) {
-    load_units<T, K, 32>(reinterpret_cast<const uint8_t *>(slice.at), slice, lane, raw);
+    load_units<T, K, N>(reinterpret_cast<const uint8_t *>(slice.at), slice, t, raw);
     if constexpr (DISTILL) {
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) zt[i] = ahead.id[i] >= 0 ? (float)z_row[ahead.id[i]] : 0.0f;
+      for (int i = 0; i < kEach; ++i) zt[i] = leads && ahead.id[i] >= 0 ? (float)z_row[ahead.id[i]] : 0.0f;
     } else if (MODE != GRADIENT) {
-      zt[0] = ahead.token >= 0 ? (float)z_row[ahead.token] : 0.0f;
+      zt[0] = leads && ahead.token >= 0 ? (float)z_row[ahead.token] : 0.0f;
     }
   }
-  side_of<DISTILL, T, MODE>(a, named, side, row, 0, ahead);
-  __syncwarp();
+  if (leads) {
+    side_of<DISTILL, T, MODE>(a, named, side, row, 0, ahead);
+    __syncwarp();
+  }
   const Teacher teacher(side, a.top);
-  Gradient g = {Exponent(side.lse * a.t, a.scale), side.slope, side.slope, weight == 0.0f || side.mass == 0.0f};
-  if constexpr (MODE != GRADIENT) {
+  Gradient g = {Exponent(0.0f, a.scale), 0.0f, 0.0f, true};
+  if constexpr (MODE == GRADIENT) {
+    sync();
+    g = {Exponent(side.lse * a.t, a.scale), side.slope, side.slope, weight == 0.0f || side.mass == 0.0f};
+  } else {
     float M = 0.0f, S = 1.0f, X = 0.0f;
     if (weight != 0.0f) {
-      mask_units<T, K, 32>(a, slice, lane, raw);
+      mask_units<T, K, N>(a, slice, t, raw);
       const float m = top_of<T, K>(raw);
       const Exponent x(m == -INFINITY ? 0.0f : m, a.scale);
       float2 s = both(0.0f);
       auto each = [&](auto quick) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          if (k * 32 >= slice.units) break;
+          if (k * N >= slice.units) break;
           float2 z[P / 2];
           unpack<T>(raw[k], z);
 #pragma unroll
@@ -926,26 +942,35 @@ __global__ void __launch_bounds__(kShortThreads, K > 4 ? (DISTILL ? 4 : 5) : 8) 
       } else {
         each(std::false_type());
       }
-      if constexpr (DISTILL) {
+      if constexpr (!DISTILL) {
+        X = zt[0];
+      } else if (leads) {
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
           const int j = i * 32 + lane;
           if (j < a.top && teacher.ids[j] >= 0 && (teacher.q[j] > 0.0f || teacher.q[j] != teacher.q[j])) X += teacher.q[j] * zt[i];
         }
         X = warp_sum(X);
-      } else {
-        X = zt[0];
       }
       M = warp_max(m);
       S = warp_sum((s.x + s.y) * whole * below(m, M, a.scale));
     }
-    const float slope = results<DISTILL>(a, side, row, weight, M, S, X, lane == 0);
-    g = {Exponent(M, a.scale), slope / S, slope, g.none};
+    if constexpr (G > 1) {
+      if (lane == 0) meet[threadIdx.x / 32] = make_float4(M, S, X, 0.0f);
+      sync();
+      const float4 *v = meet + group * G;
+      M = v[0].x, S = v[0].y, X = v[0].z;
+#pragma unroll
+      for (int w = 1; w < G; ++w) merge(M, S, v[w].x, v[w].y, a.scale);
+    }
+    const float slope = results<DISTILL>(a, side, row, weight, M, S, X, t == 0);
+    g = {Exponent(M, a.scale), slope / S, slope, weight == 0.0f || side.mass == 0.0f};
   }
   if constexpr (MODE != STATS) {
-    write_slice<DISTILL, T, K, 32, MODE>(a, slice, lane, [&](int k, int) { return raw[k]; }, g_row, even_rows<T>(a, slice, g_row), side.token, g);
+    write_slice<DISTILL, T, K, N, MODE>(a, slice, t, [&](int k, int) { return raw[k]; }, g_row, even_rows<T>(a, slice, g_row), side.token, g);
     if constexpr (DISTILL) {
-      __syncwarp();
+      sync();
+      if (!leads) return;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         const int j = i * 32 + lane;
@@ -1050,34 +1075,40 @@ cudaError_t launch_rows(Args &a, cudaStream_t s) {
   return launch_kernel(fn, dim3((unsigned)grid), dim3(kBlock), args, (size_t)smem, s, true, a.cluster);
 }
 
-template <bool DISTILL, class T, Mode MODE>
+template <bool DISTILL, class T, int K, int G, Mode MODE>
 cudaError_t launch_short(Args &a, cudaStream_t s) {
-  constexpr int kRows = kShortThreads / 32, kFew = kShortUnits / 4;  // rows of a block; units of the shortest rows
-  const bool few = units_of<T>(a) <= kFew;
+  constexpr int kRows = kShortThreads / (32 * G), kNames = DISTILL && MODE != STATS ? K * G * Slice<T>::kPer * 4 : 0;
+  static_assert(kRows * ((int)sizeof(Side) + kShortTop * 16 + kNames) <= 47 * 1024, "more than any kernel may have");
   a.cluster = a.rounds = a.slices = 1;
-  a.units = kShortUnits, a.items = a.rows;
+  a.units = K * G * 32, a.items = a.rows;
   a.side_bytes = ((int)sizeof(Side) + (DISTILL ? a.top * 16 : 0) + 15) / 16 * 16;
-  const int smem = kRows * (a.side_bytes + (DISTILL && MODE != STATS ? (few ? kFew : kShortUnits) * Slice<T>::kPer / 8 : 0));
-  static_assert(kRows * ((int)sizeof(Side) + kShortTop * 16 + kShortUnits) <= 48 * 1024, "more than any kernel may have");
-  const void *fn = few ? kernel(&short_kernel<DISTILL, T, kFew / 32, MODE>) : kernel(&short_kernel<DISTILL, T, kShortUnits / 32, MODE>);
   void *args[] = {&a};
-  return launch_kernel(fn, dim3((unsigned)((a.rows + kRows - 1) / kRows)), dim3(kShortThreads), args, (size_t)smem, s, true);
+  return launch_kernel(kernel(&short_kernel<DISTILL, T, K, G, MODE>), dim3((unsigned)((a.rows + kRows - 1) / kRows)), dim3(kShortThreads), args,
+                       (size_t)(kRows * (a.side_bytes + kNames)), s, true);
 }
 
+template <bool DISTILL, class T, Mode MODE>
+cudaError_t launch_mode(Args &a, cudaStream_t s) {
+  // Rows of a block, one after another, are bound by the latency of their sums, and rows of a warp or two by bytes (us by
+  // block / so, BF16: distillation loss 16384 x 512 74 / 12, 16384 x 4096 93 / 30, 8192 x 8192 55 / 39, 16 x 4096 4.6 / 3.7; with
+  // gradient 93 / 18, 117 / 62, 86 / 66). A gradient's rows have to be enough for all SMs (512 x 4096 6.6 / 6.8, 1024 x 4096
+  // 9.4 / 8.0). Four warps to a row wait too long for one's teacher, but not for the policy's scalars (8192 x 16384 distillation
+  // 57 / 71, with gradient 109 / 130; policy 55 / 47, 104 / 95).
+  const int64_t units = units_of<T>(a);
+  if (a.top <= kShortTop && (MODE == STATS || a.rows > 4 * device_sms())) {
+    if (units <= 128) return launch_short<DISTILL, T, 4, 1, MODE>(a, s);
+    if (units <= 512) return launch_short<DISTILL, T, 16, 1, MODE>(a, s);
+    if (units <= 1024) return launch_short<DISTILL, T, 16, 2, MODE>(a, s);
+    if constexpr (!DISTILL)
+      if (units <= 2048) return launch_short<DISTILL, T, 16, 4, MODE>(a, s);
+  }
+  if (MODE == HELD && units > kThreads * kMostUnits) return launch_rows<DISTILL, T, TWICE>(a, s);
+  return launch_rows<DISTILL, T, MODE>(a, s);
+}
 template <bool DISTILL, class T>
 cudaError_t launch_as(Args &a, cudaStream_t s) {
-  // Rows of whole blocks are bound by the latency of their sums, one after the other; a warp to each is slower only where a
-  // gradient's rows are too few for all SMs (us by block / by warp, distillation in BF16: loss alone 16384 x 4096 93 / 37, 16 x 4096
-  // 4.6 / 3.7; with gradient 16384 x 4096 117 / 69, 16384 x 512 93 / 19, 1024 x 4096 9.4 / 8.0, 512 x 4096 6.6 / 6.8).
-  const bool gradient = a.backward || a.dlogits;
-  if (units_of<T>(a) <= kShortUnits && a.top <= kShortTop && (!gradient || a.rows > 4 * device_sms())) {
-    if (a.backward) return launch_short<DISTILL, T, GRADIENT>(a, s);
-    return a.dlogits ? launch_short<DISTILL, T, HELD>(a, s) : launch_short<DISTILL, T, STATS>(a, s);
-  }
-  if (a.backward) return launch_rows<DISTILL, T, GRADIENT>(a, s);
-  if (!a.dlogits) return launch_rows<DISTILL, T, STATS>(a, s);
-  if (units_of<T>(a) <= kThreads * kMostUnits) return launch_rows<DISTILL, T, HELD>(a, s);
-  return launch_rows<DISTILL, T, TWICE>(a, s);
+  if (a.backward) return launch_mode<DISTILL, T, GRADIENT>(a, s);
+  return a.dlogits ? launch_mode<DISTILL, T, HELD>(a, s) : launch_mode<DISTILL, T, STATS>(a, s);
 }
 
 template <bool DISTILL>

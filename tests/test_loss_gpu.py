@@ -492,3 +492,22 @@ def test_specials_in_many_short_rows():
 def test_rings_that_nearly_fill_an_sm(vocab, top):
     """Slices and teacher's entries of which three or four take 106 to 108 KB: one stage fewer."""
     check_distill(fp_module(), *distill_data(5, vocab, top, 1, BF16, torch.int32))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("vocab", [4097, 8191, 8192, 8193, 16384])
+def test_many_rows_of_several_warps(vocab, dtype):
+    vocab = vocab if dtype == BF16 else vocab // 2
+    check_distill(fp_module(), *distill_data(700, vocab, 40, vocab, dtype), t=0.8)
+    check_policy(fp_module(), *policy_data(700, vocab, vocab, dtype, t=0.8), t=0.8)
+
+
+@pytest.mark.parametrize("vocab", [5001, 15001])
+def test_many_rows_of_several_warps_apart(vocab):
+    """Rows that begin anywhere, in place and in another type, entries that name a token again."""
+    logits, ids, teacher, w = distill_data(700, vocab, 100, vocab, BF16)
+    ids[::3, 50:] = ids[::3, :50]
+    ids[1::3] = vocab - 1
+    check_distill(fp_module(), logits, ids, teacher, w, ld=vocab + 4, offset=3, ld_t=101, in_place=True)
+    check_distill(fp_module(), logits, ids, teacher, None, ld=vocab + 2, offset=1, g_dtype=F32)
+    check_policy(fp_module(), *policy_data(700, vocab, 5, BF16), ld=vocab + 4, offset=3, in_place=True)
