@@ -139,7 +139,7 @@ def test_loss_wait_that_gives_up(rows, vocab):
 
     def distill():
         loss, lse, g = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda"), torch.empty_like(z)
-        fp.fsdp_distill_loss_forward(z, ids, t, loss, lse)
+        fp.fsdp_distill_loss_forward(z, ids, t, loss, lse, dlogits=g if vocab == 3000 else None)  # of short rows a loss alone waits for nothing
         return loss, lse
 
     def policy():
