@@ -36,7 +36,9 @@ constexpr int kMaxCluster = 8, kMaxStages = 4;
 constexpr int kMostUnits = 8;  // 16-byte units of a slice that a thread has
 constexpr int kMostSmem = 106 * 1024;  // stages, and what goes with rows: 2 x (32 + 16.1) KB at least
 constexpr int kNamed = 32768;
-constexpr int64_t kL2Rows = 40 << 20;  // bytes of rows that are read twice while L2 still has them
+// Bytes of rows at work of which L2 still has what is read a second time; beyond, a row takes more blocks and their sums longer
+// (4096 x 50021 FP32 289 us with 80 MB and one block to a row, 319 with 40 MB and two).
+constexpr int64_t kL2Rows = 80 << 20;
 constexpr float kLog2E = 1.4426950408889634f;
 
 enum Mode { STATS, HELD, TWICE, GRADIENT };
@@ -1042,31 +1044,36 @@ template <bool DISTILL, class T, Mode MODE>
 cudaError_t launch_rows(Args &a, cudaStream_t s) {
   constexpr int64_t kMost = kThreads * kMostUnits;
   const int64_t row_units = units_of<T>(a);
-  a.cluster = a.rounds = a.slices = 1;
+  a.cluster = a.slices = 1;
+  int64_t least = 1;
   if (MODE == GRADIENT) {
     a.slices = (int32_t)((row_units + kMost - 1) / kMost);
   } else if (MODE != HELD) {
-    // Few rows: as many blocks to a row as keep the SMs busy, with 256 units each at least.  Rows that are read twice: as
-    // many as it takes for all rows at work to stay in L2.
-    const int64_t blocks = kBlocks * device_sms();
-    int64_t want = std::min<int64_t>((blocks + a.rows - 1) / a.rows, row_units / kThreads);
-    if (MODE == TWICE) want = std::max<int64_t>(want, (blocks * row_units * 16 + kL2Rows - 1) / kL2Rows);
-    a.cluster = (int32_t)std::min<int64_t>(kMaxCluster, std::max<int64_t>(1, want));
-    a.rounds = (int32_t)((row_units + kMost * a.cluster - 1) / (kMost * a.cluster));
+    // Few rows: as many blocks to a row as the SMs have room for, with 256 units each at least. Rows that are read twice: as
+    // many as it takes for all rows at work to stay in L2. Clusters of three or five leave SMs idle (us, BF16, with a power of
+    // two / without: 61 x 131072 loss alone 6.5 / 9.8, 102 x 32768 5.1 / 7.7, 2048 x 200000 with gradient 307 / 480).
+    const int64_t blocks = kBlocks * device_sms(), room = std::min<int64_t>(blocks / a.rows, row_units / kThreads);
+    if (MODE == TWICE) least = (blocks * row_units * 16 + kL2Rows - 1) / kL2Rows;
+    while (a.cluster < kMaxCluster && (a.cluster * 2 <= room || a.cluster < least)) a.cluster *= 2;
   }
-  const int64_t parts = (int64_t)a.cluster * a.rounds * a.slices;
-  a.units = (int32_t)((row_units + parts - 1) / parts);
   a.items = a.rows * a.slices;
-  const bool small = a.units <= 2 * kThreads;
-  const void *fn = small ? kernel(&row_kernel<DISTILL, T, 2, MODE>) : kernel(&row_kernel<DISTILL, T, kMostUnits, MODE>);
-  a.stage_bytes = (a.units * 16 + 127) / 128 * 128;
   a.side_bytes = ((int)sizeof(Side) + (DISTILL ? a.top * 16 : 0) + 127) / 128 * 128;
-  a.stages = stages_of_mode(MODE);  // as many as leave room for the SM's other blocks
-  while (a.stages > 2 && a.stages * (a.stage_bytes + a.side_bytes) > kMostSmem) --a.stages;
-  const int smem = a.stages * (a.stage_bytes + a.side_bytes);
-  int clusters = 0;
-  cudaError_t e = resident(fn, a.cluster, smem, &clusters);
-  if (e != cudaSuccess) return e;
+  const void *fn = nullptr;
+  int smem = 0, clusters = 0;
+  cudaError_t e;
+  for (;; a.cluster /= 2) {
+    a.rounds = MODE == STATS || MODE == TWICE ? (int32_t)((row_units + kMost * a.cluster - 1) / (kMost * a.cluster)) : 1;
+    const int64_t parts = (int64_t)a.cluster * a.rounds * a.slices;
+    a.units = (int32_t)((row_units + parts - 1) / parts);
+    fn = a.units <= 2 * kThreads ? kernel(&row_kernel<DISTILL, T, 2, MODE>) : kernel(&row_kernel<DISTILL, T, kMostUnits, MODE>);
+    a.stage_bytes = (a.units * 16 + 127) / 128 * 128;
+    a.stages = stages_of_mode(MODE);  // as many as leave room for the SM's other blocks
+    while (a.stages > 2 && a.stages * (a.stage_bytes + a.side_bytes) > kMostSmem) --a.stages;
+    smem = a.stages * (a.stage_bytes + a.side_bytes);
+    if ((e = resident(fn, a.cluster, smem, &clusters)) != cudaSuccess) return e;
+    // Large clusters do not fill all SMs: rather smaller ones than a second turn (us: 76 x 131072 in BF16, loss alone, 7.7 / 9.9).
+    if (a.cluster / 2 < least || a.cluster == 1 || a.rows <= clusters) break;
+  }
   e = gave_up_count(GAVE_UP_LOSS, &a.gave_up);
   if (e != cudaSuccess) return e;
   a.wait_limit_ns = wait_limit_ns(), a.fault = wait_fault();

@@ -511,3 +511,9 @@ def test_many_rows_of_several_warps_apart(vocab):
     check_distill(fp_module(), logits, ids, teacher, w, ld=vocab + 4, offset=3, ld_t=101, in_place=True)
     check_distill(fp_module(), logits, ids, teacher, None, ld=vocab + 2, offset=1, g_dtype=F32)
     check_policy(fp_module(), *policy_data(700, vocab, 5, BF16), ld=vocab + 4, offset=3, in_place=True)
+
+
+@pytest.mark.parametrize("rows", [20, 38, 61, 76, 152, 305])
+def test_rows_for_clusters_of_every_size(rows):
+    check_distill(fp_module(), *distill_data(rows, 33001, 20, rows, BF16))
+    check_policy(fp_module(), *policy_data(rows, 33001, rows, BF16))
