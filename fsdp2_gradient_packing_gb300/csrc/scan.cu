@@ -11,6 +11,9 @@
 // a wait is bounded.  Whatever a tile finds known when it looks back, the state at its start is the
 // same chain of A h + B from the sequence's start, so results are the same bits on every run.
 //
+// Measured in BF16: 65536 x 1024 in one sequence 110 us forward (403 MB at 3.7 TB/s) and 187 backward (671 MB at 3.6); 32768 x
+// 4096 in four 168 us (806 MB at 4.8 TB/s) and 322 (1342 MB at 4.2). A copy without the look back took 74 us for 107 at 32768 x 2048.
+//
 // What bounds it is the time from a tile's rows to its carry, so that is kept short: the next
 // tile's rows are on their way into shared memory meanwhile (cp.async, two stages), and the values
 // that tiles leave for one another are their own flags (all ones: not there yet), which costs no
@@ -37,8 +40,8 @@ namespace {
 constexpr int kCols = 64, kWarps = 8, kThreads = kWarps * 32;
 constexpr int kStateRows = 64;
 constexpr int kWindow = 2 * kWarps;  // tiles that a look back takes in at once, at most
-// Rows of a warp.  What a tile costs a warp beside its rows is about 400 instructions, 30 to 60 a row;
-// of FP32 rows, two stages and two blocks of an SM hold 64.
+// Rows of a warp.  What a tile costs a warp beside its rows is about 400 instructions, 30 to 60 a row: 1 x 65536 x 1024 in
+// BF16 with 16 rows 121 us, with 8 197.  Of FP32 rows, two stages and two blocks of an SM hold 64.
 constexpr int steps_of(int64_t size) { return size == 4 ? 8 : 16; }
 
 struct Args {
