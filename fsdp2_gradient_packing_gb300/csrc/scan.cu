@@ -878,9 +878,9 @@ cudaError_t launch_tiles(void (*fn)(Args), Args &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  // Few columns are bound by the chain of carries, which a third block of an SM delays (us with two / three blocks, BF16
-  // forward: 65536 x 256 46 / 56, 65536 x 1024 119 / 116, 32768 x 4096 214 / 205).
-  const int blocks = a.column_tiles <= 8 ? 2 : Work::kBlocks;
+  // Few chains are bound by their carries, which a third block of an SM delays (us with two / three blocks, BF16 forward: 65536 rows
+  // of one sequence, 64 columns 41 / 46, 256 50 / 51, 384 62 / 59, 1024 127 / 109; of sequences of 2048, 64 14.6 / 14.8, 256 34 / 29).
+  const int blocks = a.column_tiles * a.aside <= 4 ? std::min(2, Work::kBlocks) : Work::kBlocks;
   const int64_t grid = std::min<int64_t>(a.tiles, (int64_t)device_sms() * blocks);
   void *args[] = {&a};
   return launch_kernel(kernel(fn), dim3((unsigned)grid), dim3(kThreads), args, Work::kSmem, s, true);
