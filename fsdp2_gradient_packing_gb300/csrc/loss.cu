@@ -538,14 +538,15 @@ __device__ __forceinline__ float top_of(const uint4 (&r)[K]) {
   }
 }
 
-// (z - from) scale as z scale + by: one operation, where the product is finite, with the rounding of `by` taken
-// back afterwards (`left`, of the exponent).  Else a difference and a product.
+// (z - from) scale as z scale + by: one operation, with the rounding of `by` taken back afterwards (`left`, of the
+// exponent).  That is at most half an ulp of `by`, and so at most 1 up to 2^25; a mask value of -1e10 would leave hundreds, whose power
+// of two is infinite.  Beyond, and where `by` is not finite: a difference and a product.
 struct Exponent {
   float from, scale, by, left;
   bool quick;
   __device__ __forceinline__ Exponent(float f, float s) : from(f), scale(s) {
     by = -f * s, left = fmaf(f, s, by);
-    quick = fabsf(by) < 1e37f;
+    quick = fabsf(left) <= 1.0f;  // not of a NaN
   }
   __device__ __forceinline__ float2 quickly(float2 z) const { return __ffma2_rn(z, both(scale), both(by)); }
   __device__ __forceinline__ float2 carefully(float2 z) const { return __fmul2_rn(__fadd2_rn(z, both(-from)), both(scale)); }
