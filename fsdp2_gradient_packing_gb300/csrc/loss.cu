@@ -83,7 +83,7 @@ struct alignas(16) Side {
 };
 
 struct alignas(16) Shared {
-  float4 warp[2][kWarps];        // maximum and sum of a warp, and what it has of the targets
+  float4 warp[2][kWarps];        // maximum and sum of a warp, what it has of the targets, and their mass
   float4 block[2][kMaxCluster];  // the same of the cluster's blocks
   uint64_t arrived[2], full[kMaxStages], empty[kMaxStages];  // of the cluster's sums; of stages
   uint64_t ready[kMaxStages], done[kMaxStages];              // of rows' sides
@@ -108,6 +108,12 @@ __device__ __forceinline__ void merge(float &m, float &s, float m2, float s2, fl
   const float top = fmaxf(m, m2);
   s = s * below(m, top, scale) + s2 * below(m2, top, scale);
   m = top;
+}
+
+// A teacher's targets: sum of q (z - top), with `mass` the sum of q and `top` no less than any of their logits. So all its terms have
+// one sign: sum q z against lse would leave nothing of their difference where the logits are large beside it. As of a larger top:
+__device__ __forceinline__ float raised(float x, float mass, float top, float to) {
+  return top == to || mass == 0.0f ? x : fmaf(mass, top - to, x);
 }
 
 __device__ __forceinline__ int32_t token_at(const Args &a, int64_t i) {
@@ -637,7 +643,8 @@ __device__ __forceinline__ void write_named(const Args &a, const Slice<T> &slice
     if (ids[j] >= lo && ids[j] < hi && !(gq[j] < 0.0f)) store_any(g_row, ids[j], a.g_bf16 != 0, g.of(zt[j]) - g.slope * gq[j]);
 }
 
-// A row's results from its maximum and sum and what X its targets make of its logits; returns the slope of its gradient.
+// A row's results from its maximum M and sum S and what X its targets make of its logits (a teacher's the sum of q (z - M), the
+// policy's token its logit); returns the slope of its gradient.
 template <bool DISTILL>
 __device__ __forceinline__ float results(const Args &a, const Side &side, int64_t row, float weight, float M, float S, float X, bool write) {
   float loss = 0.0f, logp = 0.0f, lse = 0.0f, slope = 0.0f;
@@ -645,7 +652,7 @@ __device__ __forceinline__ float results(const Args &a, const Side &side, int64_
     const float log_sum = logf(S);
     lse = fmaf(M, a.inv_t, log_sum);
     if constexpr (DISTILL) {
-      if (side.mass != 0.0f) loss = weight * a.t * a.t * (side.q_log_q + lse - a.inv_t * X);
+      if (side.mass != 0.0f) loss = weight * a.t * a.t * (side.q_log_q + (log_sum - a.inv_t * X) + (M - M));  // M infinite: NaN
       slope = side.slope;
     } else if (side.token >= 0) {
       logp = fmaf(X - M, a.inv_t, -log_sum);
@@ -689,7 +696,8 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
       if (lane == 0) tc::bar_arrive(done);
     };
     uint8_t *g_row = static_cast<uint8_t *>(a.dlogits) + row * a.ld_g * (a.g_bf16 ? 2 : 4);
-    float m = -INFINITY, sum = 0.0f, hit = 0.0f;  // of the thread, over the block's slices; what it has of the targets
+    float m = -INFINITY, sum = 0.0f;                // of the thread, over the block's slices
+    float hit = 0.0f, mass = 0.0f, high = -INFINITY;  // what it has of the targets; of a teacher's, relative to the highest
     float held = 1.0f;               // what the exponentials of a row that is held are still to be multiplied by
     float2 e[MODE == HELD ? K : 1][P / 2];
     for (int round = 0; round < a.rounds; ++round) {
@@ -697,18 +705,27 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
       const uint8_t *stage = stages + stage_at * a.stage_bytes;
       tc::bar_wait(tc::smem(&sh.full[stage_at]), parity, a.wait_limit_ns, &sh.stop);
       if (weight != 0.0f) {
-        // The targets' logits.
-        if constexpr (DISTILL) {
-          const int32_t lo = slice.begin(), hi = slice.end(a);
-          for (int j = t; j < a.top; j += kThreads)
-            if (ids[j] >= lo && ids[j] < hi) {
-              const float z = staged(stage, slice, ids[j]);
-              if (MODE != STATS) zt[j] = z;
-              if (MODE != GRADIENT && (q[j] > 0.0f || q[j] != q[j])) hit += q[j] * z;
-            }
-        } else if (MODE != GRADIENT) {
-          if (t == 0 && side.token >= slice.begin() && side.token < slice.end(a)) hit += staged(stage, slice, side.token);
-        }
+        auto targets = [&] {  // their logits
+          if constexpr (DISTILL) {
+            const int32_t lo = slice.begin(), hi = slice.end(a);
+            for (int j = t; j < a.top; j += kThreads)
+              if (ids[j] >= lo && ids[j] < hi) {
+                const float z = staged(stage, slice, ids[j]);
+                if (MODE != STATS) zt[j] = z;
+                if (MODE != GRADIENT && (q[j] > 0.0f || q[j] != q[j])) {
+                  const float top = fmaxf(high, z);
+                  hit = raised(raised(hit, mass, high, top), q[j], z, top);
+                  mass += q[j], high = top;
+                }
+              }
+          } else if (MODE != GRADIENT) {
+            if (t == 0 && side.token >= slice.begin() && side.token < slice.end(a)) hit += staged(stage, slice, side.token);
+          }
+        };
+        // Rows that are held have few registers while their exponentials are made (8192 x 16384 BF16 distillation with gradient 116 us with the
+        // targets first, 112 so); others wait less for targets that come first (8192 x 32768 174 and 177).
+        constexpr bool kFirst = MODE != HELD || !DISTILL;
+        if constexpr (kFirst) targets();
         if constexpr (MODE != GRADIENT) {
           uint4 raw[K];
           load_units<T, K, kThreads>(stage, slice, t, raw);
@@ -743,6 +760,7 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
           else
             merge(m, sum, top, s.x + s.y, a.scale);
         }
+        if constexpr (!kFirst) targets();
       }
       if constexpr (MODE == GRADIENT) {
         // p = 2^((z - lse T) / T log2 e)
@@ -757,35 +775,49 @@ __device__ __forceinline__ void work(const Args &a, Shared &sh, uint8_t *stages,
       continue;
     }
     // The row's maximum and sum.
-    float M = m, S = sum, X = hit;
+    float M = DISTILL ? fmaxf(m, high) : m, S = sum, X = hit, W = mass;
     if (weight != 0.0f) {
       const int slot = turn & 1;
 #pragma unroll
       for (int d = 16; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
       S = sum * below(m, M, a.scale);
 #pragma unroll
-      for (int d = 16; d > 0; d /= 2) S += __shfl_xor_sync(0xFFFFFFFFu, S, d), X += __shfl_xor_sync(0xFFFFFFFFu, X, d);
-      if (lane == 0) sh.warp[slot][warp] = make_float4(M, S, X, 0.0f);
+      for (int d = 16; d > 0; d /= 2) S += __shfl_xor_sync(0xFFFFFFFFu, S, d);
+      if (!DISTILL || __any_sync(0xFFFFFFFFu, mass != 0.0f)) {  // few warps have targets
+        if (DISTILL) X = raised(hit, mass, high, M);
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) {
+          X += __shfl_xor_sync(0xFFFFFFFFu, X, d);
+          if (DISTILL) W += __shfl_xor_sync(0xFFFFFFFFu, W, d);
+        }
+      }
+      if (lane == 0) sh.warp[slot][warp] = make_float4(M, S, X, W);
       workers_sync();
+      // Of n warps or blocks, a power of two: each lane takes one, and all lanes have what they join to.
       auto join = [&](const float4 *p, int n) {
-        float4 v = p[0];
-        M = v.x, S = v.y, X = v.z;
-        for (int w = 1; w < n; ++w) {
-          v = p[w];
-          merge(M, S, v.x, v.y, a.scale);
-          X += v.z;
+        const float4 v = p[lane & (n - 1)];
+        M = v.x;
+        for (int d = n / 2; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+        S = v.y * below(v.x, M, a.scale), X = DISTILL ? raised(v.z, v.w, v.x, M) : v.z, W = v.w;
+        for (int d = n / 2; d > 0; d /= 2) {
+          S += __shfl_xor_sync(0xFFFFFFFFu, S, d), X += __shfl_xor_sync(0xFFFFFFFFu, X, d);
+          if (DISTILL) W += __shfl_xor_sync(0xFFFFFFFFu, W, d);
         }
       };
       if (MODE != HELD && a.cluster > 1) {
         const uint32_t bar = tc::smem(&sh.arrived[slot]);
-        if (t < a.cluster) {
+        if (warp == 0) {
           join(sh.warp[slot], kWarps);
-          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(tc::at_rank(tc::smem(&sh.block[slot][rank]), t)), "f"(M),
-                       "f"(S), "f"(X), "f"(0.0f)
-                       : "memory");
-          tc::bar_arrive_cluster(tc::at_rank(bar, t));
+          if (t < a.cluster) {
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(tc::at_rank(tc::smem(&sh.block[slot][rank]), t)), "f"(M),
+                         "f"(S), "f"(X), "f"(W)
+                         : "memory");
+            tc::bar_arrive_cluster(tc::at_rank(bar, t));
+          }
+          __syncwarp();
         }
         tc::bar_wait(bar, (uint32_t)(turn >> 1) & 1u, a.wait_limit_ns, &sh.stop);
+        __syncwarp();
         join(sh.block[slot], a.cluster);
       } else {
         join(sh.warp[slot], kWarps);
@@ -950,16 +982,7 @@ __global__ void __launch_bounds__(kShortThreads, K > 4 ? (DISTILL ? 4 : 5) : 8) 
       } else {
         each(std::false_type());
       }
-      if constexpr (!DISTILL) {
-        X = zt[0];
-      } else if (leads) {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-          const int j = i * 32 + lane;
-          if (j < a.top && teacher.ids[j] >= 0 && (teacher.q[j] > 0.0f || teacher.q[j] != teacher.q[j])) X += teacher.q[j] * zt[i];
-        }
-        X = warp_sum(X);
-      }
+      if constexpr (!DISTILL) X = zt[0];
       M = warp_max(m);
       S = warp_sum((s.x + s.y) * whole * below(m, M, a.scale));
     }
@@ -970,6 +993,14 @@ __global__ void __launch_bounds__(kShortThreads, K > 4 ? (DISTILL ? 4 : 5) : 8) 
       M = v[0].x, S = v[0].y, X = v[0].z;
 #pragma unroll
       for (int w = 1; w < G; ++w) merge(M, S, v[w].x, v[w].y, a.scale);
+    }
+    if (DISTILL && leads && weight != 0.0f) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int j = i * 32 + lane;
+        if (j < a.top && teacher.ids[j] >= 0 && (teacher.q[j] > 0.0f || teacher.q[j] != teacher.q[j])) X = raised(X, teacher.q[j], zt[i], M);
+      }
+      X = warp_sum(X);
     }
     const float slope = results<DISTILL>(a, side, row, weight, M, S, X, t == 0);
     g = {Exponent(M, a.scale), slope / S, slope, weight == 0.0f || side.mass == 0.0f};

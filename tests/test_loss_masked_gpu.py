@@ -79,3 +79,86 @@ def test_policy(mask, dtype, shape):
         expect(mg.t[1:], (want * by)[1:], ((tol + 8 * U * want.abs()) * by.abs())[1:], "dlogits")
         assert ml.intact() and mg.intact()
     fp.fsdp_ops_sync_status()
+
+
+def check_distill(rows, vocab, logits, ids, teacher, t, lse_counts, named_tol=0.0):
+    """Loss, lse and gradients against the definition; the gradient from lse of rows where that counts."""
+    fp = fp_module()
+    z, log_sum, p, d, lse, lse_tol = parts(logits, t)
+    here = (ids >= 0) & (teacher.double() > -INF)
+    v = torch.where(here, teacher.double(), -INF)
+    v = (v - v.amax(-1, keepdim=True)) / t
+    log_q = torch.where(here, v - torch.logsumexp(v, -1, keepdim=True), 0.0)
+    q = torch.where(here, torch.exp(log_q), 0.0)
+    rel_q = (8 * (torch.where(v > -104, -v, 0.0).amax(-1, keepdim=True) + 1) + 270) * U
+    safe = torch.where(here, ids, 0).long()
+    gap = torch.where(q > 0, log_q - z.gather(1, safe) + log_sum, 0.0)
+    loss = t * t * (q * gap).sum(-1)
+    # Terms log q, (z - maximum) / T and log sum, each rounded to a few u of its size and weighed by a q that is off by rel_q.
+    size = torch.where(q > 0, log_q.abs() + z.gather(1, safe).abs() + log_sum.abs(), 0.0)
+    loss_tol = t * t * ((q * size).sum(-1) * (2 * rel_q[:, 0] + 16 * U) + 2 * d[:, 0] + 2 * rel_q[:, 0])
+    want = p.clone()
+    want.scatter_add_(1, safe, -q)
+    tol = p * (2 * d + 16 * U)
+    tol.scatter_add_(1, safe, q * (2 * rel_q + 64 * U))
+    want, tol = want * t, (tol + 4 * U * want.abs()) * t
+    some = here.any(-1)
+    want, tol = torch.where(some[:, None], want, 0.0), torch.where(some[:, None], tol, 0.0)
+    loss = torch.where(some, loss, 0.0)
+    ml, mg = Matrix(rows, vocab, logits.dtype, None, 0, logits), Matrix(rows, vocab, logits.dtype)
+    mt = teacher.cuda()
+    got, got_l = (torch.empty(rows, device="cuda") for _ in range(2))
+    for g in (None, mg.t):
+        fp.fsdp_distill_loss_forward(ml.t, ids.cuda(), mt, got, got_l, temperature=t, dlogits=g)
+        expect(got, loss, loss_tol, "loss")
+        if float(logits.double().abs().max()) / t < 3e38:
+            expect(got_l, lse, lse_tol, "lse")
+    expect(mg.t, want, tol, "dlogits of the forward call")
+    fp.fsdp_distill_loss_backward(ml.t, ids.cuda(), mt, got_l, mg.t, temperature=t)
+    tol = tol + p * (6 * U * t) * lse.abs()[:, None]
+    expect(mg.t[lse_counts], want[lse_counts], tol[lse_counts], "dlogits")
+    fp.fsdp_ops_sync_status()
+    assert ml.intact() and mg.intact()
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("mask", [-1e4, -1e9, -1e10, -1e20, -1e30, "lowest"])
+def test_distill(mask, dtype, shape):
+    vocab, rows = shape
+    value = LOW[dtype] if mask == "lowest" else mask
+    logits, first, n, gen = masked(rows, vocab, value, dtype, vocab + 1)
+    top = 9
+    ids = first + (torch.rand(rows, top, generator=gen) * n).long()  # within the run; of rows 0 and 1 one token, named again and again
+    ids[0] = torch.arange(top) * (vocab // top)
+    teacher = (torch.randn(rows, top, generator=gen, dtype=F64) * 2).to(dtype)
+    if mask != "lowest":  # a token that the student rules out: a large loss
+        ids[2, 4] = (first[2, 0] + vocab // 2) % vocab
+    for t in (0.7, 1.0):
+        check_distill(rows, vocab, logits, ids, teacher, t, slice(1, None))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("vocab", [600, 40001])
+@pytest.mark.parametrize("offset", [-3e4, 1e3, 2e5])
+def test_far_offsets(offset, vocab, dtype):
+    """All of a row's logits around a number that is large beside their differences."""
+    gen = torch.Generator().manual_seed(vocab)
+    logits = (torch.randn(5, vocab, generator=gen, dtype=F64) * abs(offset) / 1e3 + offset).to(dtype)
+    ids = torch.randint(0, vocab, (5, 20), generator=gen)
+    check_distill(5, vocab, logits, ids, torch.randn(5, 20, generator=gen, dtype=F64).to(dtype), 1.0, slice(0, 5))
+
+
+@pytest.mark.parametrize("vocab", [600, 40001])
+def test_rows_of_infinities(vocab):
+    """A row of -infinity alone has no distribution: its loss and gradient are NaN, and no other row's."""
+    fp = fp_module()
+    logits = torch.randn(4, vocab, generator=torch.Generator().manual_seed(1))
+    logits[1], logits[2, 3] = -INF, INF
+    ids = torch.arange(12).reshape(4, 3)
+    loss, lse = (torch.empty(4, device="cuda") for _ in range(2))
+    g = torch.empty(4, vocab, device="cuda")
+    for d in (None, g):
+        fp.fsdp_distill_loss_forward(logits.cuda(), ids.cuda(), torch.zeros(4, 3, device="cuda"), loss, lse, dlogits=d)
+        assert torch.isnan(loss).tolist() == [False, True, True, False] and lse[1] == -INF
+    assert bool(torch.isnan(g[1:3]).all()) and bool(torch.isfinite(g[[0, 3]]).all())
