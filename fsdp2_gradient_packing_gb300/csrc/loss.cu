@@ -280,7 +280,8 @@ __device__ __noinline__ void join_entries(int top, const Teacher &e) {
   }
 }
 
-// The softmax over a row's entries; tokens lo .. hi - 1 are those of this block's gradient.
+// The softmax over a row's entries; tokens lo .. hi - 1 are those of this block's gradient.  Their logits, too, are scaled after the
+// maximum is subtracted: of the type's lowest value, which counts, a multiple may be -infinity, which does not.
 template <bool DISTILL, Mode MODE>
 __device__ __forceinline__ void teacher_of(const Args &a, uint32_t *named, Side &side, int64_t row, int32_t lo, int32_t hi,
                                            const Ahead<DISTILL, MODE> &ahead) {
@@ -294,7 +295,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, uint32_t *named, Side 
     int32_t id[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      v[i] = ahead.id[i] < 0 ? -INFINITY : ahead.v[i] * a.inv_t;
+      v[i] = ahead.id[i] < 0 ? -INFINITY : ahead.v[i];
       id[i] = v[i] == -INFINITY ? -1 : ahead.id[i];
       top = fmaxf(top, v[i]);
       nan |= v[i] != v[i];
@@ -303,7 +304,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, uint32_t *named, Side 
     bool again[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const float d = v[i] - top, p = id[i] < 0 ? 0.0f : ex2(d * kLog2E);
+      const float d = (v[i] - top) * a.inv_t, p = id[i] < 0 ? 0.0f : ex2(d * kLog2E);
       sum += p;
       if (p > 0.0f || p != p) total += p * d;
       v[i] = p;
@@ -334,7 +335,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, uint32_t *named, Side 
       load_entries<N>(a, row, j0, id, x);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        x[i] = id[i] < 0 ? -INFINITY : x[i] * a.inv_t;
+        x[i] = id[i] < 0 ? -INFINITY : x[i];
         if (x[i] == -INFINITY) id[i] = -1;
         top = fmaxf(top, x[i]);
         nan |= x[i] != x[i];
@@ -347,7 +348,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, uint32_t *named, Side 
       for (int i = 0; i < N; ++i) x[i] = j0 + i * 32 < a.top ? e.z[j0 + i * 32] : -INFINITY;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float d = x[i] - top, p = x[i] == -INFINITY ? 0.0f : ex2(d * kLog2E);
+        const float d = (x[i] - top) * a.inv_t, p = x[i] == -INFINITY ? 0.0f : ex2(d * kLog2E);
         sum += p;
         if (p > 0.0f || p != p) total += p * d;
         if (j0 + i * 32 < a.top) e.q[j0 + i * 32] = p;
@@ -385,7 +386,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, uint32_t *named, Side 
   __syncwarp();
   if (MODE != STATS && __any_sync(0xFFFFFFFFu, twice)) join_entries(a.top, e);
   const bool some = sum > 0.0f || sum != sum || __any_sync(0xFFFFFFFFu, nan);
-  // sum q log q, with log q = (v - top) - log sum
+  // sum q log q, with log q = (v - top) / T - log sum
   if (lane == 0) side.mass = some ? 1.0f : 0.0f, side.q_log_q = some ? total / sum - logf(sum) : 0.0f;
 }
 

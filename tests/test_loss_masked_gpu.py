@@ -162,3 +162,17 @@ def test_rows_of_infinities(vocab):
         fp.fsdp_distill_loss_forward(logits.cuda(), ids.cuda(), torch.zeros(4, 3, device="cuda"), loss, lse, dlogits=d)
         assert torch.isnan(loss).tolist() == [False, True, True, False] and lse[1] == -INF
     assert bool(torch.isnan(g[1:3]).all()) and bool(torch.isfinite(g[[0, 3]]).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("top", [5, 128, 129, 700])
+@pytest.mark.parametrize("t", [0.5, 0.7, 1.0])
+def test_masked_teachers(t, top, dtype):
+    """A teacher's logits of the type's lowest value, throughout or in part, and of its highest: values like others, which count."""
+    gen = torch.Generator().manual_seed(top)
+    logits = torch.randn(6, 3000, generator=gen, dtype=F64).to(dtype)
+    ids = torch.stack([torch.randperm(3000, generator=gen)[:top] for _ in range(6)])
+    teacher = torch.randn(6, top, generator=gen, dtype=F64).to(dtype)
+    teacher[0], teacher[1, 1:], teacher[2, ::2], teacher[3, top - 1] = LOW[dtype], LOW[dtype], LOW[dtype], -LOW[dtype]
+    teacher[4, :] = -1e30
+    check_distill(6, 3000, logits, ids, teacher, t, slice(0, 6))
