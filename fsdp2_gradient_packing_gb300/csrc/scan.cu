@@ -68,19 +68,38 @@ __device__ __forceinline__ int64_t offset_at(const Args &a, int64_t s) {
   return min(max(o, (int64_t)0), a.rows);
 }
 
-// a = 1 / (1 + e^-z) and 1 - a = e^-z a, each to a few ulp of its own size.  Where e^-z is far above 1, up
-// to infinity, 1 - a is 1: the product with an a of 0 would be a NaN.
-__device__ __forceinline__ void gates(float2 z, float2 &a, float2 &keep) {
-  const float2 t = __fmul2_rn(z, both(-1.4426950408889634f));
+// A gate is held as its odds o = (1 - a) / a = e^-z, from which a = 1 / (1 + o) and 1 - a = o a both come to a few ulp of their own
+// sizes; one made from the other would lose the bits of the lesser.
+__device__ __forceinline__ float2 ex2(float2 t) {
   float2 e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-  const float2 d = __fadd2_rn(e, both(1.0f));
+  return e;
+}
+__device__ __forceinline__ float2 odds(float2 z) { return ex2(__fmul2_rn(z, both(-1.4426950408889634f))); }
+__device__ __forceinline__ float2 gate_of(float2 o) {
+  const float2 d = __fadd2_rn(o, both(1.0f));
+  float2 a;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a.x) : "f"(d.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a.y) : "f"(d.y));
-  const float2 k = __fmul2_rn(e, a);
-  keep = make_float2(t.x > 100.0f ? 1.0f : k.x, t.y > 100.0f ? 1.0f : k.y);
+  return a;
 }
+// Of any odds, up to infinity, whose product with an a of 0 would be a NaN: held to 2^125, which stand for a gate that is shut.
+// 1 - a is then 1, and a, less 2^-125, 0.  A NaN stays one.
+__device__ __forceinline__ float2 held_odds(float2 z) {
+  float2 t = __fmul2_rn(z, both(-1.4426950408889634f));
+  asm("min.NaN.f32 %0, %0, 0f42FA0000;" : "+f"(t.x));
+  asm("min.NaN.f32 %0, %0, 0f42FA0000;" : "+f"(t.y));
+  return ex2(t);
+}
+__device__ __forceinline__ void gates(float2 o, float2 &a, float2 &keep) {
+  a = gate_of(o), keep = __fmul2_rn(o, a);
+  a = __fadd2_rn(a, both(-0x1p-125f));
+}
+// Odds of up to 2^100 go a shorter way, which takes h to a (h + o x).  A row beyond makes K, of which kMuch times as much is held,
+// infinite or a NaN, and so do o x beyond all bounds the state: then a warp takes its rows once more, the other way.
+constexpr float kMuch = 0x1p28f;
+
 // How a tile comes and goes.  DIRECT: each value by its own load and store, of any types, a lane's columns 32 apart.  ANY:
 // x, gate and dh, of one type, staged wherever rows begin, otherwise as DIRECT.  UNITS: all matrices of one
 // type, staged by 16 bytes, a lane's columns neighbours, results stored in pairs.
@@ -436,6 +455,14 @@ struct Tile {
   __device__ __forceinline__ static float2 given(const Args &a, const float *p, int32_t s, const At &at) {
     return p && at.in ? get_f32<WAY>(p + (int64_t)s * a.cols + at.column, at.second) : both(0.0f);
   }
+  // A row's state.  PLAIN: odds of up to 2^100.
+  template <bool PLAIN>
+  __device__ __forceinline__ static float2 state_step(float2 x, float2 o, float2 h) {
+    if constexpr (PLAIN) return __fmul2_rn(gate_of(o), fma2(o, x, h));
+    float2 f, keep;
+    gates(o, f, keep);
+    return fma2(f, h, __fmul2_rn(keep, x));
+  }
   // One row of the second and of the third pass over a backward tile, from 1 - a and a (1 - a), each good to a few ulp
   // of its own size; a itself is then 1 - (1 - a), a rounding of 1 off, as the state and D bear.
   __device__ __forceinline__ static float2 less_than_1(float2 keep) { return fma2(keep, both(-1.0f), both(1.0f)); }
@@ -460,7 +487,7 @@ struct Tile {
       const int64_t k = t * a.ld_gate + at.column;
       z = make_float2(load_any(a.gate, k, kBf16), at.second ? load_any(a.gate, k + (WAY == UNITS ? 1 : 32), kBf16) : 0.0f);
     }
-    gates(__fadd2_rn(z, shift), f, keep);
+    gates(held_odds(__fadd2_rn(z, shift)), f, keep);
     return f;
   }
   // One tile, from its stage; starts the next one's loads into the other stage, and gives its ticket and its place.
@@ -468,6 +495,10 @@ struct Tile {
   __device__ static uint32_t backward(const Args &a, Block &all, int turn, uint8_t *stage, uint8_t *other, Spot &p, int64_t lo, int64_t hi);
 };
 
+// Whether a warp's rows went well by the short way, from what they amount to.
+__device__ __forceinline__ bool went_well(float2 B, float2 K) {
+  return __all_sync(0xFFFFFFFFu, fabsf(B.x) + fabsf(B.y) + (K.x + K.y) < INFINITY);
+}
 // A warp's A: 1 - K, where K is the recurrence's answer to inputs of 1, or the rows' product where that is
 // the smaller: near 1, as a slow column's is, a product of rounded factors would lose a rounding a row.
 __device__ __forceinline__ float2 factor(float2 product, float2 K) {
@@ -482,30 +513,34 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::forward(const Args &
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const float2 shift = bias(a, at);
   const Marks<kSteps> m(a, p, at.first, lo, hi);
-  const uint32_t odd = m.odd();
-  // A row takes h to f h + b.  Only f stays in registers: over a warp's rows, b from 1 - f is good to a
-  // rounding of x, and a third block fits the SM.
-  float2 f[kSteps], A = both(1.0f), B = both(0.0f), K = both(0.0f);
-  if (__builtin_expect(odd == 0, 1)) {
+  // A row takes h to f h + b.  Only its odds stay in registers, from which both come again: a third block fits the SM.
+  float2 o[kSteps], A = both(1.0f), B = both(0.0f), K = both(0.0f);
+  bool plain = m.odd() == 0;
+  if (__builtin_expect(plain, 1)) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      float2 keep;
-      gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f[i], keep);
-      A = __fmul2_rn(A, f[i]), B = fma2(f[i], B, __fmul2_rn(keep, row(a, stage, at, 0, i))), K = fma2(f[i], K, keep);
+      o[i] = odds(__fadd2_rn(row(a, stage, at, 1, i), shift));
+      const float2 f = gate_of(o[i]);
+      A = __fmul2_rn(A, f), B = __fmul2_rn(f, fma2(o[i], row(a, stage, at, 0, i), B)), K = __fmul2_rn(f, fma2(o[i], both(kMuch), K));
     }
-  } else {
+    plain = went_well(B, K);
+    K = __fmul2_rn(K, both(1.0f / kMuch));
+  }
+  if (__builtin_expect(!plain, 0)) {
+    A = both(1.0f), B = K = both(0.0f);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      float2 keep;
-      gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f[i], keep);
+      float2 f, keep;
+      o[i] = held_odds(__fadd2_rn(row(a, stage, at, 1, i), shift));
+      gates(o[i], f, keep);
       float2 b = __fmul2_rn(keep, row(a, stage, at, 0, i));
-      if (!(m.valid >> i & 1)) f[i] = both(1.0f), keep = b = both(0.0f);
+      if (!(m.valid >> i & 1)) f = both(1.0f), keep = b = both(0.0f);
       if (m.begins >> i & 1) {
-        // The row's state itself, kept in place of f: `initial` may be `final`, which a later tile may write
+        // The row's state itself, kept in place of the odds: `initial` may be `final`, which a later tile may write
         // as soon as this one has left its own state.
-        f[i] = B = fma2(f[i], given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at), b);
+        o[i] = B = fma2(f, given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at), b);
       } else {
-        A = __fmul2_rn(A, f[i]), B = fma2(f[i], B, b), K = fma2(f[i], K, keep);
+        A = __fmul2_rn(A, f), B = fma2(f, B, b), K = fma2(f, K, keep);
       }
     }
   }
@@ -523,10 +558,10 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::forward(const Args &
     put_f32<WAY>(a.states + at.first / kStateRows * a.cols + at.column, at.second, h);
   const int64_t pitch = a.ld_h * out_size(a.h_bf16);
   uint8_t *out = static_cast<uint8_t *>(a.h) + (at.first * a.ld_h + at.column) * out_size(a.h_bf16);
-  if (__builtin_expect(odd == 0, 1)) {
+  if (__builtin_expect(plain, 1)) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      h = fma2(f[i], h, __fmul2_rn(fma2(f[i], both(-1.0f), both(1.0f)), row(a, stage, at, 0, i)));
+      h = state_step<true>(row(a, stage, at, 0, i), o[i], h);
       if (at.in) put<WAY>(out, out_bf16(a.h_bf16), at.second, h);
       out += pitch;
     }
@@ -534,7 +569,7 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::forward(const Args &
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       if (m.valid >> i & 1) {
-        h = m.begins >> i & 1 ? f[i] : fma2(f[i], h, __fmul2_rn(fma2(f[i], both(-1.0f), both(1.0f)), row(a, stage, at, 0, i)));
+        h = m.begins >> i & 1 ? o[i] : state_step<false>(row(a, stage, at, 0, i), o[i], h);
         if (at.in) put<WAY>(out, out_bf16(a.h_bf16), at.second, h);
       }
       out += pitch;
@@ -567,7 +602,7 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       float2 f, keep;
-      gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f, keep);
+      gates(held_odds(__fadd2_rn(row(a, stage, at, 1, i), shift)), f, keep);
       keeps[i] = keep, slope[i] = __fmul2_rn(f, keep);
       A = __fmul2_rn(A, f), B = fma2(f, B, __fmul2_rn(keep, row(a, stage, at, 0, i))), K = fma2(f, K, keep);
       C = fma2(A, row(a, stage, at, 2, i), C);
@@ -577,7 +612,7 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       float2 f, keep, d = row(a, stage, at, 2, i);
-      gates(__fadd2_rn(row(a, stage, at, 1, i), shift), f, keep);
+      gates(held_odds(__fadd2_rn(row(a, stage, at, 1, i), shift)), f, keep);
       float2 b = __fmul2_rn(keep, row(a, stage, at, 0, i));
       if (!(m.valid >> i & 1)) f = both(1.0f), keep = b = d = both(0.0f);
       keeps[i] = keep, slope[i] = __fmul2_rn(f, keep);
@@ -724,7 +759,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
       const int64_t j = left + i * 64 + lane * 2;
       if (j >= a.cols) continue;
       float2 f, keep;
-      gates(__fadd2_rn(z[i], b[i]), f, keep);
+      gates(held_odds(__fadd2_rn(z[i], b[i])), f, keep);
       const float2 h = fma2(f, h0[i], __fmul2_rn(keep, u[i]));
       put<UNITS>(static_cast<uint8_t *>(a.h) + (t * a.ld_h + j) * (a.h_bf16 ? 2 : 4), a.h_bf16 != 0, true, h);
       if (a.final_state) a.final_state[s + j] = h.x, a.final_state[s + j + 1] = h.y;
@@ -743,7 +778,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
       const int64_t j = left + i * 32 + lane;
       if (j >= a.cols) continue;
       float2 f, keep;
-      gates(both(z[i] + b[i]), f, keep);
+      gates(held_odds(both(z[i] + b[i])), f, keep);
       const float h = fmaf(f.x, h0[i], keep.x * u[i]);
       store_any(a.h, t * a.ld_h + j, a.h_bf16 != 0, h);
       if (a.final_state) a.final_state[s + j] = h;
