@@ -463,32 +463,32 @@ struct Tile {
     gates(o, f, keep);
     return fma2(f, h, __fmul2_rn(keep, x));
   }
-  // One row of the second and of the third pass over a backward tile, from 1 - a and a (1 - a), each good to a few ulp
-  // of its own size; a itself is then 1 - (1 - a), a rounding of 1 off, as the state and D bear.
-  __device__ __forceinline__ static float2 less_than_1(float2 keep) { return fma2(keep, both(-1.0f), both(1.0f)); }
-  __device__ __forceinline__ static void slope_step(float2 x, float2 keep, float2 &h, float2 &slope) {
-    slope = __fmul2_rn(fma2(x, both(-1.0f), h), slope);
-    h = fma2(less_than_1(keep), h, __fmul2_rn(keep, x));
+  // One row of the second and of the third pass over a backward tile.
+  template <bool PLAIN>
+  __device__ __forceinline__ static void slope_step(float2 x, float2 o, float2 &h, float2 &slope) {
+    float2 f, keep;
+    if constexpr (PLAIN)
+      f = gate_of(o), keep = __fmul2_rn(o, f);
+    else
+      gates(o, f, keep);
+    slope = __fmul2_rn(fma2(x, both(-1.0f), h), __fmul2_rn(f, keep));
+    h = PLAIN ? __fmul2_rn(f, fma2(o, x, h)) : fma2(f, h, __fmul2_rn(keep, x));
   }
-  __device__ __forceinline__ static float2 gradient_step(const Args &a, float2 dh, float2 keep, float2 slope, const At &at, void *dx,
+  template <bool PLAIN>
+  __device__ __forceinline__ static float2 gradient_step(const Args &a, float2 dh, float2 o, float2 slope, const At &at, void *dx,
                                                          void *dgate, float2 &e) {
+    float2 f, keep;
+    if constexpr (PLAIN)
+      f = gate_of(o), keep = __fmul2_rn(o, f);
+    else
+      gates(o, f, keep);
     const float2 d = __fadd2_rn(dh, e), dz = __fmul2_rn(d, slope);
     if (at.in) {
       put<WAY>(dx, out_bf16(a.dx_bf16), at.second, __fmul2_rn(keep, d));
       put<WAY>(dgate, out_bf16(a.dx_bf16), at.second, dz);
     }
-    e = __fmul2_rn(less_than_1(keep), d);
+    e = __fmul2_rn(f, d);
     return dz;
-  }
-  // a of row t to a few ulp, once more: of a sequence's first row, for the gradient of its initial state.
-  __device__ static float2 first_gate(const Args &a, const At &at, float2 shift, int64_t t) {
-    float2 z = both(0.0f), f, keep;
-    if (at.in) {
-      const int64_t k = t * a.ld_gate + at.column;
-      z = make_float2(load_any(a.gate, k, kBf16), at.second ? load_any(a.gate, k + (WAY == UNITS ? 1 : 32), kBf16) : 0.0f);
-    }
-    gates(held_odds(__fadd2_rn(z, shift)), f, keep);
-    return f;
   }
   // One tile, from its stage; starts the next one's loads into the other stage, and gives its ticket and its place.
   __device__ static uint32_t forward(const Args &a, Block &all, int turn, uint8_t *stage, uint8_t *other, Spot &p, int64_t lo, int64_t hi);
@@ -590,32 +590,35 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const float2 shift = bias(a, at);
   const Marks<kSteps> m(a, p, at.first, lo, hi);
-  const uint32_t odd = m.odd();
   // The state before the warp's rows comes from the nearest kept one above.
   constexpr int kPer = kStateRows / kSteps;  // warps to a kept state
   const int64_t kept = (at.tile * kRows + warp / kPer * kStateRows) / kStateRows;
   float2 h = at.in && kept * kStateRows < a.rows ? get_f32<WAY>(a.states_in + kept * a.cols + at.column, at.second) : both(0.0f);
   // States go A h + B over the warp's rows; e = a_(t+1) D_(t+1) comes in from below and leaves as
   // A e + C.
-  float2 A = both(1.0f), B = both(0.0f), C = both(0.0f), K = both(0.0f), keeps[kSteps], slope[kSteps];
-  if (__builtin_expect(odd == 0, 1)) {
+  float2 A = both(1.0f), B = both(0.0f), C = both(0.0f), K = both(0.0f), o[kSteps], slope[kSteps];
+  bool plain = m.odd() == 0;
+  if (__builtin_expect(plain, 1)) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      float2 f, keep;
-      gates(held_odds(__fadd2_rn(row(a, stage, at, 1, i), shift)), f, keep);
-      keeps[i] = keep, slope[i] = __fmul2_rn(f, keep);
-      A = __fmul2_rn(A, f), B = fma2(f, B, __fmul2_rn(keep, row(a, stage, at, 0, i))), K = fma2(f, K, keep);
+      o[i] = odds(__fadd2_rn(row(a, stage, at, 1, i), shift));
+      const float2 f = gate_of(o[i]);
+      A = __fmul2_rn(A, f), B = __fmul2_rn(f, fma2(o[i], row(a, stage, at, 0, i), B)), K = __fmul2_rn(f, fma2(o[i], both(kMuch), K));
       C = fma2(A, row(a, stage, at, 2, i), C);
     }
-  } else {
+    plain = went_well(B, K);
+    K = __fmul2_rn(K, both(1.0f / kMuch));
+  }
+  if (__builtin_expect(!plain, 0)) {
+    A = both(1.0f), B = C = K = both(0.0f);
     bool open = true;  // whether what comes from this row on reaches the warp's first row
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       float2 f, keep, d = row(a, stage, at, 2, i);
-      gates(held_odds(__fadd2_rn(row(a, stage, at, 1, i), shift)), f, keep);
+      o[i] = held_odds(__fadd2_rn(row(a, stage, at, 1, i), shift));
+      gates(o[i], f, keep);
       float2 b = __fmul2_rn(keep, row(a, stage, at, 0, i));
       if (!(m.valid >> i & 1)) f = both(1.0f), keep = b = d = both(0.0f);
-      keeps[i] = keep, slope[i] = __fmul2_rn(f, keep);
       if (m.begins >> i & 1) {
         B = fma2(f, given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at), b);
         open = false;
@@ -638,14 +641,14 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
   const Whole whole = leave<true>(a, sh, at.tile, at.at0);
   // Rows' slopes (h_(t-1) - x_t) a_t (1 - a_t), downwards from the warp's state.
   for (int w = warp / kPer * kPer; w < warp; ++w) h = sh.cut[w] & CUT_DOWN ? all.forward[w][lane] : fma2(sh.a[w][lane], h, all.forward[w][lane]);
-  if (__builtin_expect(odd == 0, 1)) {
+  if (__builtin_expect(plain, 1)) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) slope_step(row(a, stage, at, 0, i), keeps[i], h, slope[i]);
+    for (int i = 0; i < kSteps; ++i) slope_step<true>(row(a, stage, at, 0, i), o[i], h, slope[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       if (m.begins >> i & 1) h = given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at);
-      slope_step(row(a, stage, at, 0, i), keeps[i], h, slope[i]);
+      slope_step<false>(row(a, stage, at, 0, i), o[i], h, slope[i]);
     }
   }
   float2 e = take<true>(a, sh, all.stop, look_at(all, stage), whole, at.tile, at.reach, at.at0), db = both(0.0f);
@@ -653,10 +656,10 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
   const int64_t size = out_size(a.dx_bf16), pitch_x = a.ld_dx * size, pitch_g = a.ld_dgate * size;
   uint8_t *dx = static_cast<uint8_t *>(a.dx) + ((at.first + kSteps - 1) * a.ld_dx + at.column) * size;
   uint8_t *dgate = static_cast<uint8_t *>(a.dgate) + ((at.first + kSteps - 1) * a.ld_dgate + at.column) * size;
-  if (__builtin_expect(odd == 0, 1)) {
+  if (__builtin_expect(plain, 1)) {
 #pragma unroll
     for (int i = kSteps - 1; i >= 0; --i) {
-      const float2 dz = gradient_step(a, row(a, stage, at, 2, i), keeps[i], slope[i], at, dx, dgate, e);
+      const float2 dz = gradient_step<true>(a, row(a, stage, at, 2, i), o[i], slope[i], at, dx, dgate, e);
       db = __fadd2_rn(db, dz);
       dx -= pitch_x, dgate -= pitch_g;
     }
@@ -664,16 +667,14 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
 #pragma unroll
     for (int i = kSteps - 1; i >= 0; --i) {
       if (m.ends >> i & 1) e = given(a, a.dfinal, __shfl_sync(0xFFFFFFFFu, m.end, i), at);
-      const float2 below = e;
       if (m.valid >> i & 1) {  // else e passes
-        const float2 dz = gradient_step(a, row(a, stage, at, 2, i), keeps[i], slope[i], at, dx, dgate, e);
+        const float2 dz = gradient_step<false>(a, row(a, stage, at, 2, i), o[i], slope[i], at, dx, dgate, e);
         db = __fadd2_rn(db, dz);
       }
       dx -= pitch_x, dgate -= pitch_g;
       if (m.begins >> i & 1) {
         const int32_t s = __shfl_sync(0xFFFFFFFFu, m.begin, i);
-        const float2 d0 = __fmul2_rn(first_gate(a, at, shift, at.first + i), __fadd2_rn(row(a, stage, at, 2, i), below));
-        if (at.in && a.dinitial) put_f32<WAY>(a.dinitial + (int64_t)s * a.cols + at.column, at.second, d0);
+        if (at.in && a.dinitial) put_f32<WAY>(a.dinitial + (int64_t)s * a.cols + at.column, at.second, e);
       }
     }
   }

@@ -126,6 +126,26 @@ def test_a_sequence_cut_into_calls(call):
     near(state[0], want[-1], tol[-1], "final")
 
 
+@pytest.mark.parametrize("cols", [64, 70])
+@pytest.mark.parametrize("length", [3, 16, 150])
+def test_states_that_decay_at_once(length, cols):
+    """Rows without input behind a large state: h has the precision of a, not that of 1 - a."""
+    seqs = 3
+    initial = normals(7, seqs, cols, std=1e6).float()
+    check(length * seqs, cols, length, -14.0, -2.0, seed=length, initial=initial, x=torch.zeros_like)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols", [64, 70])
+@pytest.mark.parametrize("length", [3, 16, 150])
+def test_gradients_through_rows_without_one(length, cols, dtype):
+    """dh is 0 at all rows but every seventh: D between them is a D and nothing else."""
+    rows = length * 3
+    kept = (torch.arange(rows) % 7 == 2)[:, None]
+    check(rows, cols, length, -14.0, 2.0, dtype=dtype, h_dtype=dtype, seed=length, dh=lambda g: torch.where(kept, g, torch.zeros_like(g)),
+          initial=normals(8, 3, cols).float(), dfinal=normals(9, 3, cols).float())
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_gates_that_are_shut_or_open(dtype):
     """Gates of +-infinity and +-1e4: a is 0 or 1, and every result is what the formulas say."""
@@ -145,3 +165,38 @@ def test_gates_that_are_shut_or_open(dtype):
         assert torch.equal(h[t].cpu(), x[t].float())
     for t in (11, 23):
         assert torch.equal(h[t], h[t - 1])
+
+
+@pytest.mark.parametrize("cols", [64, 70])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gates_that_are_nearly_shut(dtype, cols):
+    """From where odds are large to where they leave the range of binary32, in some columns and rows of a tile and not in others."""
+    initial = normals(10, 3, cols).float()
+    check(450, cols, 150, -130.0, -30.0, dtype=dtype, h_dtype=dtype, seed=5, initial=initial)
+    check(450, cols, 150, -75.0, -65.0, dtype=dtype, h_dtype=dtype, seed=6, initial=initial)
+    check(450, cols, 150, -100.0, 40.0, dtype=dtype, h_dtype=dtype, seed=7, initial=initial)
+
+
+@pytest.mark.parametrize("cols", [64, 70])
+def test_large_inputs_at_shut_gates(cols):
+    """Odds times inputs beyond the range of binary32, where every result lies within it."""
+    check(300, cols, 150, -60.0, 10.0, seed=8, x=lambda v: v * 1e30, initial=normals(11, 2, cols, std=1e30).float())
+
+
+def test_resets():
+    """Rows of x = 0 at a gate of -infinity, here and there: the state is 0 from there on, exactly, over rows, warps and tiles."""
+    fp = fp_module()
+    rows, cols = 400, 70
+    x, gate = torch.zeros(rows, cols), normals(12, rows, cols).float()
+    reset = 37
+    gate[reset] = float("-inf")
+    h, final = torch.empty(rows, cols, device="cuda"), torch.empty(1, cols, device="cuda")
+    initial = torch.ones(1, cols, device="cuda") * 1e30
+    states = torch.empty(fp.fsdp_gated_scan_states(rows, cols), cols, device="cuda")
+    fp.fsdp_gated_scan_forward(x.cuda(), gate.cuda(), h, initial=initial, final=final, states=states, seq_len=rows)
+    assert bool((h[:5] > 0).all()) and bool((h[reset:] == 0).all()) and bool((final == 0).all())
+    dx, dgate, dinitial = torch.empty_like(h), torch.empty_like(h), torch.empty_like(final)
+    dh = torch.zeros(rows, cols)
+    dh[300] = 1e30
+    fp.fsdp_gated_scan_backward(dh.cuda(), x.cuda(), gate.cuda(), states, dx, dgate, initial=initial, dinitial=dinitial, seq_len=rows)
+    assert bool((dx[:reset] == 0).all()) and bool((dgate[:reset + 1] == 0).all()) and bool((dinitial == 0).all())
