@@ -96,8 +96,11 @@ __device__ __forceinline__ void gates(float2 o, float2 &a, float2 &keep) {
   a = gate_of(o), keep = __fmul2_rn(o, a);
   a = __fadd2_rn(a, both(-0x1p-125f));
 }
-// Odds of up to 2^100 go a shorter way, which takes h to a (h + o x).  A row beyond makes K, of which kMuch times as much is held,
-// infinite or a NaN, and so do o x beyond all bounds the state: then a warp takes its rows once more, the other way.
+// How a warp goes over its rows.  SHORT: inside one sequence, taking h to a (h + o x), which is right for odds of up to 2^100.  A row beyond
+// makes K, of which kMuch times as much is held, infinite or a NaN, and so do o x beyond all bounds the state; the warp then takes
+// its rows once more as HELD, with odds that are held (us in BF16, forward and backward, 32768 x 4096: 169 and 318, HELD alone 176 and
+// 317; with a gate that is shut every 512 rows 173 and 318, every 16 rows 215 and 362).  MARKED: with borders of sequences.
+enum Path { SHORT, HELD, MARKED };
 constexpr float kMuch = 0x1p28f;
 
 // How a tile comes and goes.  DIRECT: each value by its own load and store, of any types, a lane's columns 32 apart.  ANY:
@@ -455,30 +458,39 @@ struct Tile {
   __device__ __forceinline__ static float2 given(const Args &a, const float *p, int32_t s, const At &at) {
     return p && at.in ? get_f32<WAY>(p + (int64_t)s * a.cols + at.column, at.second) : both(0.0f);
   }
-  // A row's state.  PLAIN: odds of up to 2^100.
-  template <bool PLAIN>
+  // Whether a warp's rows went well as SHORT, from what they amount to (staged by units, columns that do not exist are 0).  If not,
+  // the gates are read once more, from where a barrier lets no register keep them (without it 193 us for 169).
+  __device__ __forceinline__ static bool went_well(float2 B, float2 K, const At &at) {
+    bool well = fabsf(B.x) + fabsf(B.y) + (K.x + K.y) < INFINITY;
+    if constexpr (WAY != UNITS) well = !at.in || (at.second ? well : fabsf(B.x) + K.x < INFINITY);
+    well = __all_sync(0xFFFFFFFFu, well);
+    if (!well) __syncwarp();
+    return well;
+  }
+  // A row's state.
+  template <Path PATH>
   __device__ __forceinline__ static float2 state_step(float2 x, float2 o, float2 h) {
-    if constexpr (PLAIN) return __fmul2_rn(gate_of(o), fma2(o, x, h));
+    if constexpr (PATH == SHORT) return __fmul2_rn(gate_of(o), fma2(o, x, h));
     float2 f, keep;
     gates(o, f, keep);
     return fma2(f, h, __fmul2_rn(keep, x));
   }
   // One row of the second and of the third pass over a backward tile.
-  template <bool PLAIN>
+  template <Path PATH>
   __device__ __forceinline__ static void slope_step(float2 x, float2 o, float2 &h, float2 &slope) {
     float2 f, keep;
-    if constexpr (PLAIN)
+    if constexpr (PATH == SHORT)
       f = gate_of(o), keep = __fmul2_rn(o, f);
     else
       gates(o, f, keep);
     slope = __fmul2_rn(fma2(x, both(-1.0f), h), __fmul2_rn(f, keep));
-    h = PLAIN ? __fmul2_rn(f, fma2(o, x, h)) : fma2(f, h, __fmul2_rn(keep, x));
+    h = PATH == SHORT ? __fmul2_rn(f, fma2(o, x, h)) : fma2(f, h, __fmul2_rn(keep, x));
   }
-  template <bool PLAIN>
+  template <Path PATH>
   __device__ __forceinline__ static float2 gradient_step(const Args &a, float2 dh, float2 o, float2 slope, const At &at, void *dx,
                                                          void *dgate, float2 &e) {
     float2 f, keep;
-    if constexpr (PLAIN)
+    if constexpr (PATH == SHORT)
       f = gate_of(o), keep = __fmul2_rn(o, f);
     else
       gates(o, f, keep);
@@ -495,10 +507,6 @@ struct Tile {
   __device__ static uint32_t backward(const Args &a, Block &all, int turn, uint8_t *stage, uint8_t *other, Spot &p, int64_t lo, int64_t hi);
 };
 
-// Whether a warp's rows went well by the short way, from what they amount to.
-__device__ __forceinline__ bool went_well(float2 B, float2 K) {
-  return __all_sync(0xFFFFFFFFu, fabsf(B.x) + fabsf(B.y) + (K.x + K.y) < INFINITY);
-}
 // A warp's A: 1 - K, where K is the recurrence's answer to inputs of 1, or the rows' product where that is
 // the smaller: near 1, as a slow column's is, a product of rounded factors would lose a rounding a row.
 __device__ __forceinline__ float2 factor(float2 product, float2 K) {
@@ -515,19 +523,28 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::forward(const Args &
   const Marks<kSteps> m(a, p, at.first, lo, hi);
   // A row takes h to f h + b.  Only its odds stay in registers, from which both come again: a third block fits the SM.
   float2 o[kSteps], A = both(1.0f), B = both(0.0f), K = both(0.0f);
-  bool plain = m.odd() == 0;
-  if (__builtin_expect(plain, 1)) {
+  Path path = m.odd() == 0 ? SHORT : MARKED;
+  if (__builtin_expect(path == SHORT, 1)) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       o[i] = odds(__fadd2_rn(row(a, stage, at, 1, i), shift));
       const float2 f = gate_of(o[i]);
       A = __fmul2_rn(A, f), B = __fmul2_rn(f, fma2(o[i], row(a, stage, at, 0, i), B)), K = __fmul2_rn(f, fma2(o[i], both(kMuch), K));
     }
-    plain = went_well(B, K);
-    K = __fmul2_rn(K, both(1.0f / kMuch));
-  }
-  if (__builtin_expect(!plain, 0)) {
-    A = both(1.0f), B = K = both(0.0f);
+    if (__builtin_expect(!went_well(B, K, at), 0)) {
+      path = HELD;
+      A = both(1.0f), B = K = both(0.0f);
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        float2 f, keep;
+        o[i] = held_odds(__fadd2_rn(row(a, stage, at, 1, i), shift));
+        gates(o[i], f, keep);
+        A = __fmul2_rn(A, f), B = fma2(f, B, __fmul2_rn(keep, row(a, stage, at, 0, i))), K = fma2(f, K, keep);
+      }
+    } else {
+      K = __fmul2_rn(K, both(1.0f / kMuch));
+    }
+  } else {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       float2 f, keep;
@@ -558,18 +575,23 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::forward(const Args &
     put_f32<WAY>(a.states + at.first / kStateRows * a.cols + at.column, at.second, h);
   const int64_t pitch = a.ld_h * out_size(a.h_bf16);
   uint8_t *out = static_cast<uint8_t *>(a.h) + (at.first * a.ld_h + at.column) * out_size(a.h_bf16);
-  if (__builtin_expect(plain, 1)) {
+  auto rows = [&](auto step) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      h = state_step<true>(row(a, stage, at, 0, i), o[i], h);
+      h = step(row(a, stage, at, 0, i), o[i], h);
       if (at.in) put<WAY>(out, out_bf16(a.h_bf16), at.second, h);
       out += pitch;
     }
+  };
+  if (__builtin_expect(path == SHORT, 1)) {
+    rows([](float2 x, float2 o, float2 h) { return state_step<SHORT>(x, o, h); });
+  } else if (path == HELD) {
+    rows([](float2 x, float2 o, float2 h) { return state_step<HELD>(x, o, h); });
   } else {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       if (m.valid >> i & 1) {
-        h = m.begins >> i & 1 ? o[i] : state_step<false>(row(a, stage, at, 0, i), o[i], h);
+        h = m.begins >> i & 1 ? o[i] : state_step<MARKED>(row(a, stage, at, 0, i), o[i], h);
         if (at.in) put<WAY>(out, out_bf16(a.h_bf16), at.second, h);
       }
       out += pitch;
@@ -597,8 +619,8 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
   // States go A h + B over the warp's rows; e = a_(t+1) D_(t+1) comes in from below and leaves as
   // A e + C.
   float2 A = both(1.0f), B = both(0.0f), C = both(0.0f), K = both(0.0f), o[kSteps], slope[kSteps];
-  bool plain = m.odd() == 0;
-  if (__builtin_expect(plain, 1)) {
+  Path path = m.odd() == 0 ? SHORT : MARKED;
+  if (__builtin_expect(path == SHORT, 1)) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       o[i] = odds(__fadd2_rn(row(a, stage, at, 1, i), shift));
@@ -606,11 +628,21 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
       A = __fmul2_rn(A, f), B = __fmul2_rn(f, fma2(o[i], row(a, stage, at, 0, i), B)), K = __fmul2_rn(f, fma2(o[i], both(kMuch), K));
       C = fma2(A, row(a, stage, at, 2, i), C);
     }
-    plain = went_well(B, K);
-    K = __fmul2_rn(K, both(1.0f / kMuch));
-  }
-  if (__builtin_expect(!plain, 0)) {
-    A = both(1.0f), B = C = K = both(0.0f);
+    if (__builtin_expect(!went_well(B, K, at), 0)) {
+      path = HELD;
+      A = both(1.0f), B = C = K = both(0.0f);
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        float2 f, keep;
+        o[i] = held_odds(__fadd2_rn(row(a, stage, at, 1, i), shift));
+        gates(o[i], f, keep);
+        A = __fmul2_rn(A, f), B = fma2(f, B, __fmul2_rn(keep, row(a, stage, at, 0, i))), K = fma2(f, K, keep);
+        C = fma2(A, row(a, stage, at, 2, i), C);
+      }
+    } else {
+      K = __fmul2_rn(K, both(1.0f / kMuch));
+    }
+  } else {
     bool open = true;  // whether what comes from this row on reaches the warp's first row
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
@@ -641,14 +673,17 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
   const Whole whole = leave<true>(a, sh, at.tile, at.at0);
   // Rows' slopes (h_(t-1) - x_t) a_t (1 - a_t), downwards from the warp's state.
   for (int w = warp / kPer * kPer; w < warp; ++w) h = sh.cut[w] & CUT_DOWN ? all.forward[w][lane] : fma2(sh.a[w][lane], h, all.forward[w][lane]);
-  if (__builtin_expect(plain, 1)) {
+  if (__builtin_expect(path == SHORT, 1)) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) slope_step<true>(row(a, stage, at, 0, i), o[i], h, slope[i]);
+    for (int i = 0; i < kSteps; ++i) slope_step<SHORT>(row(a, stage, at, 0, i), o[i], h, slope[i]);
+  } else if (path == HELD) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) slope_step<HELD>(row(a, stage, at, 0, i), o[i], h, slope[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       if (m.begins >> i & 1) h = given(a, a.initial, __shfl_sync(0xFFFFFFFFu, m.begin, i), at);
-      slope_step<false>(row(a, stage, at, 0, i), o[i], h, slope[i]);
+      slope_step<MARKED>(row(a, stage, at, 0, i), o[i], h, slope[i]);
     }
   }
   float2 e = take<true>(a, sh, all.stop, look_at(all, stage), whole, at.tile, at.reach, at.at0), db = both(0.0f);
@@ -656,19 +691,23 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
   const int64_t size = out_size(a.dx_bf16), pitch_x = a.ld_dx * size, pitch_g = a.ld_dgate * size;
   uint8_t *dx = static_cast<uint8_t *>(a.dx) + ((at.first + kSteps - 1) * a.ld_dx + at.column) * size;
   uint8_t *dgate = static_cast<uint8_t *>(a.dgate) + ((at.first + kSteps - 1) * a.ld_dgate + at.column) * size;
-  if (__builtin_expect(plain, 1)) {
+  auto rows = [&](auto step) {
 #pragma unroll
     for (int i = kSteps - 1; i >= 0; --i) {
-      const float2 dz = gradient_step<true>(a, row(a, stage, at, 2, i), o[i], slope[i], at, dx, dgate, e);
-      db = __fadd2_rn(db, dz);
+      db = __fadd2_rn(db, step(row(a, stage, at, 2, i), o[i], slope[i]));
       dx -= pitch_x, dgate -= pitch_g;
     }
+  };
+  if (__builtin_expect(path == SHORT, 1)) {
+    rows([&](float2 dh, float2 o, float2 slope) { return gradient_step<SHORT>(a, dh, o, slope, at, dx, dgate, e); });
+  } else if (path == HELD) {
+    rows([&](float2 dh, float2 o, float2 slope) { return gradient_step<HELD>(a, dh, o, slope, at, dx, dgate, e); });
   } else {
 #pragma unroll
     for (int i = kSteps - 1; i >= 0; --i) {
       if (m.ends >> i & 1) e = given(a, a.dfinal, __shfl_sync(0xFFFFFFFFu, m.end, i), at);
       if (m.valid >> i & 1) {  // else e passes
-        const float2 dz = gradient_step<false>(a, row(a, stage, at, 2, i), o[i], slope[i], at, dx, dgate, e);
+        const float2 dz = gradient_step<MARKED>(a, row(a, stage, at, 2, i), o[i], slope[i], at, dx, dgate, e);
         db = __fadd2_rn(db, dz);
       }
       dx -= pitch_x, dgate -= pitch_g;
