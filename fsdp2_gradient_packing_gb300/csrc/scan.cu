@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, Tile<T, WAY, BACKWARD>::kBlocks) til
 }
 
 // Sequences of one row each, a step of generation: nothing to scan.  A lane to 4 columns of a row (PAIRS: in pairs, whose
-// addresses all matrices align; else 32 apart), a warp to 128.
+// addresses all matrices align; else 32 apart), a warp to 128.  The states kept for the backward pass are initial ones.
 template <class T, bool PAIRS>
 __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Args a) {
   const int lane = threadIdx.x & 31;
@@ -778,6 +778,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
   if (t >= a.rows) return;
   const T *x = static_cast<const T *>(a.x) + t * a.ld_x, *gate = static_cast<const T *>(a.gate) + t * a.ld_gate;
   const int64_t s = t * a.cols;
+  float *kept = a.states && t % kStateRows == 0 ? a.states + t / kStateRows * a.cols : nullptr;
   if constexpr (PAIRS) {
     float2 u[2], z[2], b[2], h0[2];
 #pragma unroll
@@ -802,6 +803,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
       gates(held_odds(__fadd2_rn(z[i], b[i])), f, keep);
       const float2 h = fma2(f, h0[i], __fmul2_rn(keep, u[i]));
       put<UNITS>(static_cast<uint8_t *>(a.h) + (t * a.ld_h + j) * (a.h_bf16 ? 2 : 4), a.h_bf16 != 0, true, h);
+      if (kept) kept[j] = h0[i].x, kept[j + 1] = h0[i].y;
       if (a.final_state) a.final_state[s + j] = h.x, a.final_state[s + j + 1] = h.y;
     }
   } else {
@@ -821,6 +823,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
       gates(held_odds(both(z[i] + b[i])), f, keep);
       const float h = fmaf(f.x, h0[i], keep.x * u[i]);
       store_any(a.h, t * a.ld_h + j, a.h_bf16 != 0, h);
+      if (kept) kept[j] = h0[i];
       if (a.final_state) a.final_state[s + j] = h;
     }
   }

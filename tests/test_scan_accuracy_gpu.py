@@ -200,3 +200,20 @@ def test_resets():
     dh[300] = 1e30
     fp.fsdp_gated_scan_backward(dh.cuda(), x.cuda(), gate.cuda(), states, dx, dgate, initial=initial, dinitial=dinitial, seq_len=rows)
     assert bool((dx[:reset] == 0).all()) and bool((dgate[:reset + 1] == 0).all()) and bool((dinitial == 0).all())
+
+
+@pytest.mark.parametrize("dtype,cols", [(F32, 64), (F32, 67), (BF16, 64), (BF16, 67)])
+@pytest.mark.parametrize("with_initial", [False, True])
+def test_states_of_sequences_of_one_row(dtype, cols, with_initial):
+    """A forward call fills the states for the backward call, whatever the sequences' length."""
+    fp = fp_module()
+    rows = 300
+    x, gate = normals(13, rows, cols).to(dtype).cuda(), normals(14, rows, cols).to(dtype).cuda()
+    initial = normals(15, rows, cols).float().cuda() if with_initial else None
+    states = torch.full((fp.fsdp_gated_scan_states(rows, cols), cols), float("nan"), device="cuda")
+    h = torch.empty_like(x)
+    fp.fsdp_gated_scan_forward(x, gate, h, initial=initial, seq_len=1, states=states)
+    assert torch.equal(states, torch.zeros_like(states) if initial is None else initial[::64])
+    dh, dx, dgate, dinitial = torch.ones_like(x), torch.empty_like(x), torch.empty_like(x), torch.empty(rows, cols, device="cuda")
+    fp.fsdp_gated_scan_backward(dh, x, gate, states, dx, dgate, initial=initial, dinitial=dinitial, seq_len=1)
+    assert all(bool(torch.isfinite(t).all()) for t in (dx, dgate, dinitial))
