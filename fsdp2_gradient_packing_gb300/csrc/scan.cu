@@ -103,8 +103,8 @@ __device__ __forceinline__ void gates(float2 o, float2 &a, float2 &keep) {
 enum Path { SHORT, HELD, MARKED };
 constexpr float kMuch = 0x1p28f;
 
-// How a tile comes and goes.  DIRECT: each value by its own load and store, of any types, a lane's columns 32 apart.  ANY:
-// x, gate and dh, of one type, staged wherever rows begin, otherwise as DIRECT.  UNITS: all matrices of one
+// How a tile comes and goes.  DIRECT: each value by its own load and store, of any types, a lane's columns 32 apart (backward, where dh
+// is of another type than x).  ANY: x, gate and dh, of one type, staged wherever rows begin, otherwise as DIRECT.  UNITS: all matrices of one
 // type, staged by 16 bytes, a lane's columns neighbours, results stored in pairs.
 enum Way { DIRECT, ANY, UNITS };
 
@@ -396,7 +396,7 @@ struct Tile {
   static constexpr int kMatrix = kRows * kPitch;
   static constexpr int kStage = WAY == DIRECT ? 0 : (BACKWARD ? 3 : 2) * kMatrix;
   static constexpr int kSmem = 2 * kStage;
-  static constexpr int kBlocks = BACKWARD || WAY == DIRECT || (WAY == ANY && kBf16) ? 2 : 3;  // of an SM
+  static constexpr int kBlocks = BACKWARD || (WAY == ANY && kBf16) ? 2 : 3;  // of an SM
   // Where all matrices have x's type, that of the results is known.
   __device__ __forceinline__ static bool out_bf16(int32_t bf16) { return WAY == UNITS ? kBf16 : bf16 != 0; }
   __device__ __forceinline__ static int64_t out_size(int32_t bf16) { return out_bf16(bf16) ? 2 : 4; }
@@ -967,7 +967,8 @@ template <bool BACKWARD, class T>
 cudaError_t launch_as(Way way, Args &a, cudaStream_t s) {
   if (way == UNITS) return launch_tiles<Tile<T, UNITS, BACKWARD>>(&tile_kernel<T, UNITS, BACKWARD>, a, s);
   if (way == ANY) return launch_tiles<Tile<T, ANY, BACKWARD>>(&tile_kernel<T, ANY, BACKWARD>, a, s);
-  return launch_tiles<Tile<T, DIRECT, BACKWARD>>(&tile_kernel<T, DIRECT, BACKWARD>, a, s);
+  if constexpr (BACKWARD) return launch_tiles<Tile<T, DIRECT, true>>(&tile_kernel<T, DIRECT, true>, a, s);
+  return cudaErrorInvalidValue;  // forward, x and gate are always of one type
 }
 
 // Whether pairs of columns, and the 16-byte units of staged rows, fit all matrices.
@@ -1020,8 +1021,8 @@ fsdp_status_t run(const fsdp_scan_desc_t &d, Args &a, const Plan &p, void *works
     void *args[] = {&a};
     e = launch_kernel(kernel(&mark_kernel), dim3((unsigned)((d.seqs + 7) / 8)), dim3(256), args, 0, s);
   }
-  Way way = DIRECT;
-  if (!BACKWARD || d.h_dtype == d.x_dtype) way = fit.units && d.h_dtype == d.x_dtype && (!BACKWARD || d.dx_dtype == d.x_dtype) ? UNITS : ANY;
+  const bool alike = d.h_dtype == d.x_dtype;
+  const Way way = BACKWARD && !alike ? DIRECT : fit.units && alike && (!BACKWARD || d.dx_dtype == d.x_dtype) ? UNITS : ANY;
   if (e == cudaSuccess && a.tiles > 0)
     e = d.x_dtype == FSDP_DTYPE_BF16 ? launch_as<BACKWARD, __nv_bfloat16>(way, a, s)
                                      : launch_as<BACKWARD, float>(way, a, s);
