@@ -462,13 +462,12 @@ __device__ __forceinline__ void write_row(const SumArgs &a, uint32_t token, int6
       if (j + e * 32 < a.cols) g[j + e * 32] = to<TG>(fmaf(element(sum, e), a.scale, (float)old[e]));
   }
 }
-template <bool VEC>
 __device__ __forceinline__ float *part_of(const SumArgs &a, int64_t piece, int which) {
   return a.parts + (piece * 2 + which) * ((a.cols + 7) / 8 * 8);
 }
 template <bool VEC>
 __device__ __forceinline__ void write_part(const SumArgs &a, int64_t piece, int which, int64_t j, const float2 (&sum)[4]) {
-  float *p = part_of<VEC>(a, piece, which);
+  float *p = part_of(a, piece, which);
   if constexpr (VEC) {
     if (j < a.cols) store8(p, j, false, sum);
   } else {
@@ -502,7 +501,6 @@ __device__ __forceinline__ int64_t warp_lower_bound(const uint2 *keys, int64_t n
   }
   return lo;
 }
-
 
 // Rows first .. first + kClearRows - 1 of the gradient, zeros where no token has them: a block looks for them in the part
 // of the sorted tokens that has them, one a thread, and writes those that are missing.
@@ -611,7 +609,7 @@ template <bool VEC>
 __device__ __forceinline__ void add_parts(const SumArgs &a, int64_t piece, int64_t from, int64_t to_, int64_t j, float2 (&sum)[4]) {
 #pragma unroll 4
   for (int64_t p = from; p < to_; ++p) {
-    const float *q = part_of<VEC>(a, p, p == piece);  // the piece where the token begins gives its second part
+    const float *q = part_of(a, p, p == piece);  // the piece where the token begins gives its second part
     if constexpr (VEC) {
       if (j < a.cols) {
         float2 v[4];

@@ -235,9 +235,9 @@ struct Teacher {
       : ids(reinterpret_cast<int32_t *>(&side + 1)), q(reinterpret_cast<float *>(ids + top)), gq(q + top), z(gq + top) {}
 };
 
-// Whether an entry's token has been named before; forget() clears that.  Tokens from lo on have a bit each where kNamed bits are
-// enough for those up to hi, else by a hash, the top of a product with 2^32 over the golden ratio (which spreads tokens
-// at equal distances too): then another token may have been named.
+// Whether an entry's token has been named before; forget() clears that, for a next row.  Tokens from lo on have a bit each where
+// kNamed bits are enough for those up to hi, else by a hash, the top of a product with 2^32 over the golden ratio (which spreads
+// tokens at equal distances too): then another token may have been named.
 struct Names {
   uint32_t *bits;
   int32_t lo;
@@ -281,8 +281,9 @@ __device__ __noinline__ void join_entries(int top, const Teacher &e) {
 }
 
 // The softmax over a row's entries; tokens lo .. hi - 1 are those of this block's gradient.  Their logits, too, are scaled after the
-// maximum is subtracted: of the type's lowest value, which counts, a multiple may be -infinity, which does not.
-template <bool DISTILL, Mode MODE>
+// maximum is subtracted: of the type's lowest value, which counts, a multiple may be -infinity, which does not.  ONCE: the caller has
+// this row alone, of up to 32 kEach entries.
+template <bool DISTILL, Mode MODE, bool ONCE>
 __device__ __forceinline__ void teacher_of(const Args &a, uint32_t *named, Side &side, int64_t row, int32_t lo, int32_t hi,
                                            const Ahead<DISTILL, MODE> &ahead) {
   const int lane = threadIdx.x & 31;
@@ -290,7 +291,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, uint32_t *named, Side 
   const Names names(named, lo, hi);
   float top = -INFINITY, sum = 0.0f, total = 0.0f;
   bool nan = false, twice = false;
-  if (a.top <= 32 * kEach) {
+  if (ONCE || a.top <= 32 * kEach) {
     float v[kEach];
     int32_t id[kEach];
 #pragma unroll
@@ -321,7 +322,7 @@ __device__ __forceinline__ void teacher_of(const Args &a, uint32_t *named, Side 
         e.q[j] = e.gq[j] = id[i] < 0 ? 0.0f : v[i] * inv;
         if (MODE != STATS) {
           e.z[j] = again[i] ? 1.0f : 0.0f;
-          if (id[i] >= lo && id[i] < hi) names.forget(id[i]);
+          if (!ONCE && id[i] >= lo && id[i] < hi) names.forget(id[i]);
         }
       }
     }
@@ -434,13 +435,13 @@ __device__ __forceinline__ void feed(const Args &a, Shared &sh, uint8_t *stages,
 }
 
 // What a row, or one of its slices, has beside its logits.
-template <bool DISTILL, class T, Mode MODE>
+template <bool DISTILL, class T, Mode MODE, bool ONCE>
 __device__ __forceinline__ void side_of(const Args &a, uint32_t *named, Side &side, int64_t row, int32_t index, const Ahead<DISTILL, MODE> &ahead) {
   const float up = ahead.weight * ahead.dloss;
   if constexpr (DISTILL) {
     if (ahead.weight != 0.0f) {
       const Slice<T> slice(a, row, index);
-      teacher_of<DISTILL, MODE>(a, named, side, row, MODE == GRADIENT ? slice.begin() : 0, MODE == GRADIENT ? slice.end(a) : a.vocab, ahead);
+      teacher_of<DISTILL, MODE, ONCE>(a, named, side, row, MODE == GRADIENT ? slice.begin() : 0, MODE == GRADIENT ? slice.end(a) : a.vocab, ahead);
     }
   }
   if ((threadIdx.x & 31) == 0) {
@@ -471,7 +472,7 @@ __device__ __forceinline__ void prepare(const Args &a, Shared &sh, uint8_t *stag
     const int64_t row = MODE == GRADIENT ? item / a.slices : item;
     tc::bar_wait(tc::smem(&sh.done[side_at]), parity, a.wait_limit_ns, &sh.stop);
     Side &side = *reinterpret_cast<Side *>(stages + a.stages * a.stage_bytes + side_at * a.side_bytes);
-    side_of<DISTILL, T, MODE>(a, sh.named, side, row, MODE == GRADIENT ? (int32_t)(item - row * a.slices) : 0, ahead);
+    side_of<DISTILL, T, MODE, false>(a, sh.named, side, row, MODE == GRADIENT ? (int32_t)(item - row * a.slices) : 0, ahead);
     __syncwarp();
     if (lane == 0) tc::bar_arrive(tc::smem(&sh.ready[side_at]));
     if (++side_at == a.stages) side_at = 0, parity ^= 1u;
@@ -951,7 +952,7 @@ __global__ void __launch_bounds__(kShortThreads, K > 4 ? (DISTILL ? 4 : 5) : 8) 
     }
   }
   if (leads) {
-    side_of<DISTILL, T, MODE>(a, named, side, row, 0, ahead);
+    side_of<DISTILL, T, MODE, true>(a, named, side, row, 0, ahead);
     __syncwarp();
   }
   const Teacher teacher(side, a.top);
