@@ -582,6 +582,20 @@ def fsdp_gated_scan_backward(dh, x, gate, states, dx, dgate, bias=None, dbias=No
 # ---------------------------------------------------------------------------
 # Losses over logits
 # ---------------------------------------------------------------------------
+def _entries(where, what, t, rows, top, codes, device):
+    """As _matrix, of a teacher's entries: a row may have none."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[1] > 0 or top:
+        return _matrix(where, what, t, rows, top, codes, device)
+    if t.shape[0] != rows:
+        raise ValueError(f"{where}: {what} is {t.shape[0]} x 0, not {rows} x 0")
+    code = codes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{where}: {what} is {t.dtype}, not one of {', '.join(map(str, codes))}")
+    if t.get_device() != device:
+        _misplaced(where, what, t.get_device(), device)
+    return None, 0, code, device
+
+
 def _distill(where, logits, dlogits, teacher_tokens, teacher_logits, weight, temperature):
     """(descriptor, pointers of logits, dlogits, tokens, teacher and weight, device)."""
     pz, ld_z, dt_z, dev = _matrix(where, "logits", logits, None, None, _BOTH, None)
@@ -589,9 +603,9 @@ def _distill(where, logits, dlogits, teacher_tokens, teacher_logits, weight, tem
     pd, ld_d, dt_d = None, vocab, dt_z
     if dlogits is not None:
         pd, ld_d, dt_d, dev = _matrix(where, "dlogits", dlogits, rows, vocab, _BOTH, dev)
-    pi, ld_i, dt_i, dev = _matrix(where, "teacher_tokens", teacher_tokens, rows, None, _INDEX, dev)
+    pi, ld_i, dt_i, dev = _entries(where, "teacher_tokens", teacher_tokens, rows, None, _INDEX, dev)
     top = teacher_tokens.shape[1]
-    pt, ld_t, dt_t, dev = _matrix(where, "teacher_logits", teacher_logits, rows, top, _BOTH, dev)
+    pt, ld_t, dt_t, dev = _entries(where, "teacher_logits", teacher_logits, rows, top, _BOTH, dev)
     pw, _, dev = _vector(where, "weight", weight, rows, _F32, dev)
     return fsdp_distill_desc_t(rows, vocab, ld_z, ld_d, top, ld_i, ld_t, dt_z, dt_d, dt_t, dt_i, temperature), pz, pd, pi, pt, pw, dev
 

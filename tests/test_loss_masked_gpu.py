@@ -176,3 +176,36 @@ def test_masked_teachers(t, top, dtype):
     teacher[0], teacher[1, 1:], teacher[2, ::2], teacher[3, top - 1] = LOW[dtype], LOW[dtype], LOW[dtype], -LOW[dtype]
     teacher[4, :] = -1e30
     check_distill(6, 3000, logits, ids, teacher, t, slice(0, 6))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("vocab,rows", [(600, 5), (600, 1300), (16000, 5), (40001, 5), (131072, 4), (600, 0)])
+def test_no_entries(vocab, rows, dtype):
+    """A batch whose rows have no teacher's entries at all: losses and gradients of 0, and their lse."""
+    fp = fp_module()
+    logits = torch.randn(rows, vocab, generator=torch.Generator().manual_seed(2), dtype=F64).to(dtype)
+    ids, teacher = torch.empty(rows, 0, dtype=torch.int64, device="cuda"), torch.empty(rows, 0, device="cuda")
+    loss, lse = (torch.full((rows,), 9.0, device="cuda") for _ in range(2))
+    for g in (None, torch.full((rows, vocab), 9.0, dtype=dtype, device="cuda")):
+        fp.fsdp_distill_loss_forward(logits.cuda(), ids, teacher, loss, lse, dlogits=g)
+        assert bool((loss == 0).all())
+        if rows:
+            *_, want, tol = parts(logits, 1.0)
+            expect(lse, want, tol, "lse")
+    assert bool((g == 0).all())
+    g.fill_(9.0)
+    fp.fsdp_distill_loss_backward(logits.cuda(), ids, teacher, lse, g)
+    assert bool((g == 0).all())
+    fp.fsdp_ops_sync_status()
+
+
+def test_no_entries_refusals():
+    fp = fp_module()
+    z, loss, lse = torch.randn(5, 100, device="cuda"), torch.empty(5, device="cuda"), torch.empty(5, device="cuda")
+    ids, teacher = torch.empty(5, 0, dtype=torch.int64, device="cuda"), torch.empty(5, 0, device="cuda")
+    for bad, t, word in ((ids[:4], teacher, "4 x 0"), (ids.float(), teacher, "float32"), (ids, teacher[:3], "3 x 0"), (ids, teacher.double(), "float64"),
+                         (ids, torch.empty(5, 2, device="cuda"), "5 x 2"), (torch.zeros(5, 2, dtype=torch.int64, device="cuda"), teacher, "5 x 0"),
+                         (ids.cpu(), teacher, "not a CUDA tensor"), (ids, teacher.cpu(), "not a CUDA tensor"), (ids[0], teacher, "dimensions"),
+                         (None, teacher, "not a tensor")):
+        with pytest.raises(ValueError, match=word):
+            fp.fsdp_distill_loss_forward(z, bad, t, loss, lse)
