@@ -485,7 +485,7 @@ def fsdp_gated_scan_states(rows: int, cols: int) -> int:
 
 
 @functools.lru_cache(maxsize=1024)
-def _scan_workspace(rows, cols, seqs, packed, backward, device) -> int:
+def _scan_workspace(rows, cols, seqs, packed, backward) -> int:
     d = fsdp_scan_desc_t(rows, cols, seqs, 1 if packed or not seqs else rows // seqs, cols, cols, cols, cols, cols, packed, 0, 0, 0, 0, 0, 0)
     out = _I64()
     _check(_lib.fsdp_gated_scan_workspace(ctypes.byref(d), backward, ctypes.byref(out)), "fsdp_gated_scan_workspace")
@@ -494,8 +494,7 @@ def _scan_workspace(rows, cols, seqs, packed, backward, device) -> int:
 
 def fsdp_gated_scan_workspace(rows: int, cols: int, seqs: int, packed: bool, backward: bool) -> int:
     """Bytes of workspace of a call over ``seqs`` sequences in ``rows`` rows."""
-    return _scan_workspace(rows, cols, seqs, int(packed), int(backward),
-                           torch.cuda.current_device() if torch.cuda.is_available() else None)
+    return _scan_workspace(rows, cols, seqs, int(packed), int(backward))
 
 
 def _sequences(where, rows, seq_len, offsets, dev):
@@ -544,7 +543,7 @@ def fsdp_gated_scan_forward(x, gate, h, bias=None, initial=None, final=None, seq
     d = fsdp_scan_desc_t(rows, cols, seqs, length, ld_x, ld_g, ld_h, cols, cols, packed, dt_o, dt_x, dt_h, FSDP_DTYPE_F32,
                          FSDP_DTYPE_F32 if dt_b is None else dt_b, FSDP_DTYPE_F32)
     handle = _handle(where, stream, dev)
-    pws, nws, _owner = _workspace(where, workspace, _scan_workspace(rows, cols, seqs, int(packed), 0, dev), handle, dev)
+    pws, nws, _owner = _workspace(where, workspace, _scan_workspace(rows, cols, seqs, int(packed), 0), handle, dev)
     _check(_lib.fsdp_gated_scan_forward(ctypes.byref(d), px, pg, pb, pi, po, ph, pf, ps, pws, nws, handle), where)
 
 
@@ -575,7 +574,7 @@ def fsdp_gated_scan_backward(dh, x, gate, states, dx, dgate, bias=None, dbias=No
     d = fsdp_scan_desc_t(rows, cols, seqs, length, ld_x, ld_g, ld_h, ld_dx, ld_dg, packed, dt_o, dt_x, dt_h, dt_dx,
                          FSDP_DTYPE_F32 if dt_b is None else dt_b, FSDP_DTYPE_F32 if dt_db is None else dt_db)
     handle = _handle(where, stream, dev)
-    pws, nws, _owner = _workspace(where, workspace, _scan_workspace(rows, cols, seqs, int(packed), 1, dev), handle, dev)
+    pws, nws, _owner = _workspace(where, workspace, _scan_workspace(rows, cols, seqs, int(packed), 1), handle, dev)
     _check(_lib.fsdp_gated_scan_backward(ctypes.byref(d), ph, px, pg, pb, pi, po, ps, pdf, pdx, pdg, pdb, pdi, pws, nws, handle), where)
 
 
