@@ -98,7 +98,8 @@ __device__ __forceinline__ void gates(float2 o, float2 &a, float2 &keep) {
 }
 // How a warp goes over its rows.  SHORT: inside one sequence, taking h to a (h + o x), which is right for odds of up to 2^100.  A row beyond
 // makes K, of which kMuch times as much is held, infinite or a NaN, and so do o x beyond all bounds the state; the warp then takes
-// its rows once more as HELD, with odds that are held (us in BF16, forward and backward, 32768 x 4096: 169 and 318, HELD alone 176 and
+// its rows once more as HELD, with odds that are held and an h that is multiplied by a before anything is added to it, as it takes
+// the second time over them where a state beyond 2^100 comes in (us in BF16, forward and backward, 32768 x 4096: 169 and 318, HELD alone 176 and
 // 317; with a gate that is shut every 512 rows 173 and 318, every 16 rows 215 and 362).  MARKED: with borders of sequences.
 enum Path { SHORT, HELD, MARKED };
 constexpr float kMuch = 0x1p28f;
@@ -467,6 +468,9 @@ struct Tile {
     if (!well) __syncwarp();
     return well;
   }
+  __device__ __forceinline__ static Path second_path(Path path, float2 h) {
+    return path == SHORT && __any_sync(0xFFFFFFFFu, fmaxf(fabsf(h.x), fabsf(h.y)) > 0x1p100f) ? HELD : path;
+  }
   // A row's state.
   template <Path PATH>
   __device__ __forceinline__ static float2 state_step(float2 x, float2 o, float2 h) {
@@ -479,12 +483,15 @@ struct Tile {
   template <Path PATH>
   __device__ __forceinline__ static void slope_step(float2 x, float2 o, float2 &h, float2 &slope) {
     float2 f, keep;
-    if constexpr (PATH == SHORT)
+    if constexpr (PATH == SHORT) {
       f = gate_of(o), keep = __fmul2_rn(o, f);
-    else
+      slope = __fmul2_rn(fma2(x, both(-1.0f), h), __fmul2_rn(f, keep));
+      h = __fmul2_rn(f, fma2(o, x, h));
+    } else {  // the difference may be beyond all bounds where a quarter of it, which a (1 - a) is at most, is not
       gates(o, f, keep);
-    slope = __fmul2_rn(fma2(x, both(-1.0f), h), __fmul2_rn(f, keep));
-    h = PATH == SHORT ? __fmul2_rn(f, fma2(o, x, h)) : fma2(f, h, __fmul2_rn(keep, x));
+      slope = __fmul2_rn(fma2(x, both(-0.25f), __fmul2_rn(h, both(0.25f))), __fmul2_rn(__fmul2_rn(f, both(4.0f)), keep));
+      h = fma2(f, h, __fmul2_rn(keep, x));
+    }
   }
   template <Path PATH>
   __device__ __forceinline__ static float2 gradient_step(const Args &a, float2 dh, float2 o, float2 slope, const At &at, void *dx,
@@ -573,6 +580,7 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::forward(const Args &
   for (int w = 0; w < warp; ++w) h = sh.cut[w] & CUT_DOWN ? sh.b[w][lane] : fma2(sh.a[w][lane], h, sh.b[w][lane]);
   if (a.states && at.in && at.first % kStateRows == 0 && at.first < a.rows)
     put_f32<WAY>(a.states + at.first / kStateRows * a.cols + at.column, at.second, h);
+  path = second_path(path, h);
   const int64_t pitch = a.ld_h * out_size(a.h_bf16);
   uint8_t *out = static_cast<uint8_t *>(a.h) + (at.first * a.ld_h + at.column) * out_size(a.h_bf16);
   auto rows = [&](auto step) {
@@ -673,6 +681,7 @@ __device__ __forceinline__ uint32_t Tile<T, WAY, BACKWARD>::backward(const Args 
   const Whole whole = leave<true>(a, sh, at.tile, at.at0);
   // Rows' slopes (h_(t-1) - x_t) a_t (1 - a_t), downwards from the warp's state.
   for (int w = warp / kPer * kPer; w < warp; ++w) h = sh.cut[w] & CUT_DOWN ? all.forward[w][lane] : fma2(sh.a[w][lane], h, all.forward[w][lane]);
+  path = second_path(path, h);
   if (__builtin_expect(path == SHORT, 1)) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) slope_step<SHORT>(row(a, stage, at, 0, i), o[i], h, slope[i]);

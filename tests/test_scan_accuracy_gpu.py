@@ -217,3 +217,12 @@ def test_states_of_sequences_of_one_row(dtype, cols, with_initial):
     dh, dx, dgate, dinitial = torch.ones_like(x), torch.empty_like(x), torch.empty_like(x), torch.empty(rows, cols, device="cuda")
     fp.fsdp_gated_scan_backward(dh, x, gate, states, dx, dgate, initial=initial, dinitial=dinitial, seq_len=1)
     assert all(bool(torch.isfinite(t).all()) for t in (dx, dgate, dinitial))
+
+
+@pytest.mark.parametrize("cols", [64, 70])
+def test_states_near_the_end_of_the_range(cols):
+    """A state and inputs whose sum leaves the range of binary32, and whose mean does not."""
+    initial = torch.full((2, cols), 3.3e38)
+    check(300, cols, 150, -1.0, 1.0, seed=16, x=lambda v: (0.5 + 0.5 * torch.sigmoid(v)) * 1e38, initial=initial)
+    check(300, cols, 150, 3.0, 9.0, seed=17, x=lambda v: (0.5 + 0.5 * torch.sigmoid(v)) * 1e38, initial=-initial)
+    check(300, cols, 150, 2.0, 4.0, seed=18, x=lambda v: (0.99 + 0.01 * torch.sigmoid(v)) * 3.3e38, initial=initial)
