@@ -12,8 +12,8 @@
 //             time from L2.
 //   GRADIENT  the gradient alone, from lse: slices one by one.
 //
-// Measured in BF16 against 6.79 TB/s of a copy: a loss alone of 4096 x 131072 153 us (7.0 TB/s), of 8192 x 32768 83 us (6.5);
-// gradients from lse 325 us (6.6) and 166 (6.5); TWICE 390 us (5.5, bound by L2, which gives each row twice and takes the
+// Measured in BF16 against 6.79 TB/s of a copy: distillation's loss alone of 4096 x 131072 153 us (7.0 TB/s), of 8192 x 32768 81
+// us (6.6); gradients from lse 327 us (6.6) and 166 (6.5); TWICE 395 us (5.4, bound by L2, which gives each row twice and takes the
 // gradient) and 174 us (6.2). Rows of up to 8192 or 16384 logits are another kernel's, further down.
 //
 // A ninth warp fills the ring, and a tenth prepares what a row has beside its logits: the policy's scalars,
@@ -40,7 +40,7 @@ constexpr int kMaxCluster = 8, kMaxStages = 4;
 constexpr int kMostUnits = 8;  // 16-byte units of a slice that a thread has
 constexpr int kMostSmem = 106 * 1024;  // stages, and what goes with rows: 2 x (32 + 16.1) KB at least
 constexpr int kNamed = 32768;
-// Bytes of rows at work of which L2 still has what is read a second time; beyond, a row takes more blocks and their sums longer
+// Bytes of rows at work of which L2 (129 MB) still has what is read a second time; beyond, a row takes more blocks and their sums longer
 // (4096 x 50021 FP32 289 us with 80 MB and one block to a row, 319 with 40 MB and two).
 constexpr int64_t kL2Rows = 80 << 20;
 constexpr float kLog2E = 1.4426950408889634f;
@@ -905,7 +905,7 @@ __global__ void __launch_bounds__(kBlock, K > 2 ? kBlocks : 3) row_kernel(const 
 // Short rows, many of them (16384 x 4096 BF16: policy loss 24 us, 5.6 TB/s, with gradient 49 us, 5.4 TB/s): G warps to each,
 // its units in registers from the only read on. No row waits for another: latencies of loads and sums are hidden by the
 // other warps of an SM, 16 to 32 by what a row's units take in registers (128 registers for 16 units of a lane and a
-// teacher, where 96 would spill: loss and gradient of 16384 x 4096 69 us, 76).
+// teacher, where 96 would spill: loss and gradient of 16384 x 4096 62 us; it was 76 for 69 when tried).
 constexpr int kShortThreads = 128;
 constexpr int kShortTop = 32 * kEach;
 template <bool DISTILL, class T, int K, int G, Mode MODE>
@@ -1136,10 +1136,10 @@ cudaError_t launch_short(Args &a, cudaStream_t s) {
 template <bool DISTILL, class T, Mode MODE>
 cudaError_t launch_mode(Args &a, cudaStream_t s) {
   // Rows of a block, one after another, are bound by the latency of their sums, and rows of a warp or two by bytes (us by
-  // block / so, BF16: distillation loss 16384 x 512 74 / 12, 16384 x 4096 93 / 30, 8192 x 8192 55 / 39, 16 x 4096 4.6 / 3.7; with
-  // gradient 93 / 18, 117 / 62, 86 / 66). A gradient's rows have to be enough for all SMs (512 x 4096 6.6 / 6.8, 1024 x 4096
+  // block / so, BF16: distillation loss 16384 x 512 74 / 12, 16384 x 4096 93 / 30, 8192 x 8192 55 / 37, 16 x 4096 4.6 / 3.1; with
+  // gradient 93 / 18, 117 / 62, 86 / 67). A gradient's rows have to be enough for all SMs (512 x 4096 6.6 / 6.8, 1024 x 4096
   // 9.4 / 8.0). Four warps to a row wait too long for one's teacher, but not for the policy's scalars (8192 x 16384 distillation
-  // 57 / 71, with gradient 109 / 130; policy 55 / 47, 104 / 95).
+  // 55 / 71, with gradient 112 / 130; policy 55 / 46, 104 / 95).
   const int64_t units = units_of<T>(a);
   if (a.top <= kShortTop && (MODE == STATS || a.rows > 4 * device_sms())) {
     if (units <= 128) return launch_short<DISTILL, T, 4, 1, MODE>(a, s);

@@ -11,8 +11,8 @@
 // a wait is bounded.  Whatever a tile finds known when it looks back, the state at its start is the
 // same chain of A h + B from the sequence's start, so results are the same bits on every run.
 //
-// Measured in BF16: 65536 x 1024 in one sequence 110 us forward (403 MB at 3.7 TB/s) and 187 backward (671 MB at 3.6); 32768 x
-// 4096 in four 168 us (806 MB at 4.8 TB/s) and 322 (1342 MB at 4.2). A copy without the look back took 74 us for 107 at 32768 x 2048.
+// Measured in BF16: 65536 x 1024 in one sequence 110 us forward (403 MB at 3.7 TB/s) and 185 backward (671 MB at 3.6); 32768 x
+// 4096 in four 169 us (806 MB at 4.8 TB/s) and 321 (1342 MB at 4.2). A copy without the look back took 74 us for 107 at 32768 x 2048.
 //
 // What bounds it is the time from a tile's rows to its carry, so that is kept short: the next
 // tile's rows are on their way into shared memory meanwhile (cp.async, two stages), and the values
@@ -96,11 +96,12 @@ __device__ __forceinline__ void gates(float2 o, float2 &a, float2 &keep) {
   a = gate_of(o), keep = __fmul2_rn(o, a);
   a = __fadd2_rn(a, both(-0x1p-125f));
 }
-// How a warp goes over its rows.  SHORT: inside one sequence, taking h to a (h + o x), which is right for odds of up to 2^100.  A row beyond
-// makes K, of which kMuch times as much is held, infinite or a NaN, and so do o x beyond all bounds the state; the warp then takes
-// its rows once more as HELD, with odds that are held and an h that is multiplied by a before anything is added to it, as it takes
-// the second time over them where a state beyond 2^100 comes in (us in BF16, forward and backward, 32768 x 4096: 169 and 318, HELD alone 176 and
-// 317; with a gate that is shut every 512 rows 173 and 318, every 16 rows 215 and 362).  MARKED: with borders of sequences.
+// How a warp goes over its rows.  SHORT: inside one sequence, taking h to a (h + o x), which is right for odds of up to 2^100.  A row
+// beyond makes K, of which kMuch times as much is held, infinite or a NaN, and so do o x beyond all bounds the state; the warp then
+// takes its rows once more as HELD, with odds that are held and an h that is multiplied by a before anything is added to it.  The
+// later passes go so, too, where a state beyond 2^100 comes in.  MARKED: as HELD, with borders of sequences.  (us in BF16, 32768 x 4096,
+// forward and backward: 169 and 321, HELD alone 176 and 317; with a gate that is shut every 512 rows 174 and 321, every 16 rows, so
+// that every warp meets one, 216 and 370.)
 enum Path { SHORT, HELD, MARKED };
 constexpr float kMuch = 0x1p28f;
 

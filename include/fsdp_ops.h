@@ -266,7 +266,10 @@ fsdp_status_t fsdp_embedding_workspace(const fsdp_embedding_desc_t *desc, int64_
  * D_t = dh_t + a_(t+1) D_(t+1) (at a sequence's last row dh_t + dfinal):
  *   dx_t = (1 - a_t) D_t,   dgate_t = D_t (h_(t-1) - x_t) a_t (1 - a_t),
  *   dbias = sum of dgate over the rows of all sequences,   dinitial = a_1 D_1
- * States and sums are binary32.  One row a sequence is a step of generation: pass the
+ * States and sums are binary32, and a and 1 - a each good to a few ulp of their own sizes (an a
+ * below 2^-125 counts as 0): slow columns and gates that are nearly shut keep their precision, and
+ * a sequence has the same states however it is cut into calls, but for roundings.  Gates below
+ * -69 cost a little: the rows around them are taken twice.  One row a sequence is a step of generation: pass the
  * states in `initial` and receive them in `final`, which may be the same buffer; no
  * other output may overlap an input.
  *
@@ -306,7 +309,7 @@ fsdp_status_t fsdp_gated_scan_workspace(const fsdp_scan_desc_t *desc, int32_t ba
  *   initial: [seqs, cols] binary32 without gaps, or NULL for 0;  final: the same, written,
  *            or NULL.
  *   offsets: seqs + 1 device values with packed, else NULL.
- *   states:  what the backward call needs, or NULL.
+ *   states:  what the backward call needs, or NULL (of rows outside every sequence unspecified).
  */
 fsdp_status_t fsdp_gated_scan_forward(const fsdp_scan_desc_t *desc, const void *x, const void *gate, const void *bias,
                                       const float *initial, const void *offsets, void *h, float *final,
@@ -345,11 +348,15 @@ fsdp_status_t fsdp_gated_scan_backward(const fsdp_scan_desc_t *desc, const void 
  * is outside [0, vocab) has loss, logp and gradient 0 (and its lse).
  *
  * A row of weight 0 is not read: its loss, logp, lse and gradient are written as 0, whatever
- * its logits hold.  Sums are binary32.  Logits of -infinity have probability 0.
+ * its logits hold.  Sums are binary32.  Logits of -infinity have probability 0 (a row of nothing
+ * else has no distribution: NaN); those of any finite value are values like others, masks of -1e10
+ * or of the type's lowest value too.
  *
  * With dlogits given, the forward call also writes the gradient of the sum of the rows'
  * losses (dloss = 1), for which a row stays on the chip; the backward call computes it from
- * the lse (and logp) of a forward call.  dlogits may be logits itself, with the same row
+ * the lse (and logp) of a forward call, whose rounding it carries: 2^-24 |lse| in each
+ * probability, relative, so that of a row masked with -1e10 throughout nothing is left (the
+ * forward call's gradient is right there, too).  dlogits may be logits itself, with the same row
  * distance and dtype; no other overlap is allowed.
  */
 #define FSDP_DISTILL_MAX_TOP 1024
