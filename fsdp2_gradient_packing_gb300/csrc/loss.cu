@@ -111,9 +111,10 @@ __device__ __forceinline__ void merge(float &m, float &s, float m2, float s2, fl
 }
 
 // A teacher's targets: sum of q (z - top), with `mass` the sum of q and `top` no less than any of their logits. So all its terms have
-// one sign: sum q z against lse would leave nothing of their difference where the logits are large beside it. As of a larger top:
+// one sign: sum q z against lse would leave nothing of their difference where the logits are large beside it. As of a larger top (in
+// halves: the difference of two logits may leave the range that a part of it lies in):
 __device__ __forceinline__ float raised(float x, float mass, float top, float to) {
-  return top == to || mass == 0.0f ? x : fmaf(mass, top - to, x);
+  return top == to || mass == 0.0f ? x : fmaf(2.0f * mass, 0.5f * top - 0.5f * to, x);
 }
 
 __device__ __forceinline__ int32_t token_at(const Args &a, int64_t i) {
@@ -1139,7 +1140,7 @@ cudaError_t launch_mode(Args &a, cudaStream_t s) {
   // block / so, BF16: distillation loss 16384 x 512 74 / 12, 16384 x 4096 93 / 30, 8192 x 8192 55 / 37, 16 x 4096 4.6 / 3.1; with
   // gradient 93 / 18, 117 / 62, 86 / 67). A gradient's rows have to be enough for all SMs (512 x 4096 6.6 / 6.8, 1024 x 4096
   // 9.4 / 8.0). Four warps to a row wait too long for one's teacher, but not for the policy's scalars (8192 x 16384 distillation
-  // 55 / 71, with gradient 112 / 130; policy 55 / 46, 104 / 95).
+  // 55 / 71, with gradient 113 / 130; policy 55 / 46, 104 / 95).
   const int64_t units = units_of<T>(a);
   if (a.top <= kShortTop && (MODE == STATS || a.rows > 4 * device_sms())) {
     if (units <= 128) return launch_short<DISTILL, T, 4, 1, MODE>(a, s);

@@ -209,3 +209,22 @@ def test_no_entries_refusals():
                          (None, teacher, "not a tensor")):
         with pytest.raises(ValueError, match=word):
             fp.fsdp_distill_loss_forward(z, bad, t, loss, lse)
+
+
+@pytest.mark.parametrize("vocab,rows", [(600, 3), (5001, 700), (12000, 650), (40001, 3), (131072, 4)])
+def test_both_ends_of_the_range(vocab, rows):
+    """A student's maximum and a named token's logit further apart than binary32 reaches, at a small q: the loss lies within it."""
+    fp = fp_module()
+    logits = torch.randn(rows, vocab, generator=torch.Generator().manual_seed(3))
+    logits[:, 7], logits[:, vocab - 5] = 3e38, -3e38
+    ids = torch.tensor([[7, vocab - 5, 11]]).expand(rows, 3).contiguous()
+    teacher = torch.tensor([[8.0, 0.0, float("-inf")]]).expand(rows, 3).contiguous()
+    q = torch.softmax(teacher[0].double(), -1)
+    want = (q[1] * (logits[:, vocab - 5].double() - logits[:, 7].double()).abs())
+    loss, lse = (torch.empty(rows, device="cuda") for _ in range(2))
+    g = torch.empty(rows, vocab, device="cuda")
+    for d in (None, g):
+        fp.fsdp_distill_loss_forward(logits.cuda(), ids.cuda(), teacher.cuda(), loss, lse, dlogits=d)
+        expect(loss, want, want * 400 * U, "loss")  # an exponential of 8 (64 + 4 u), a quotient, a product and roundings of sums
+    for j, value in ((7, 1 - q[0]), (vocab - 5, -q[1]), (11, 0.0)):
+        expect(g[:, j], torch.full((rows,), float(value), dtype=F64), 400 * U, f"dlogits of token {j}")
