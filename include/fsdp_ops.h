@@ -266,8 +266,8 @@ fsdp_status_t fsdp_embedding_workspace(const fsdp_embedding_desc_t *desc, int64_
  * D_t = dh_t + a_(t+1) D_(t+1) (at a sequence's last row dh_t + dfinal):
  *   dx_t = (1 - a_t) D_t,   dgate_t = D_t (h_(t-1) - x_t) a_t (1 - a_t),
  *   dbias = sum of dgate over the rows of all sequences,   dinitial = a_1 D_1
- * States and sums are binary32, and a and 1 - a each good to a few ulp of their own sizes (an a
- * below 2^-125 counts as 0): slow columns and gates that are nearly shut keep their precision, and
+ * States and sums are binary32, and a and 1 - a each good to a few ulp of their own sizes (below
+ * 2^-125 they count as 0): slow columns and gates that are nearly shut keep their precision, and
  * a sequence has the same states however it is cut into calls, but for roundings.  Gates below
  * -69 cost a little: the rows around them are taken twice.  One row a sequence is a step of generation: pass the
  * states in `initial` and receive them in `final`, which may be the same buffer; no
