@@ -269,9 +269,9 @@ fsdp_status_t fsdp_embedding_workspace(const fsdp_embedding_desc_t *desc, int64_
  * States and sums are binary32, and a and 1 - a each good to a few ulp of their own sizes (below
  * 2^-125 they count as 0): slow columns and gates that are nearly shut keep their precision, and
  * a sequence has the same states however it is cut into calls, but for roundings.  Gates below
- * -69 cost a little: the rows around them are taken twice.  One row a sequence is a step of generation: pass the
- * states in `initial` and receive them in `final`, which may be the same buffer; no
- * other output may overlap an input.
+ * -69 cost a little: the rows around them are taken twice.  One row a sequence is a step of
+ * generation: pass the states in `initial` and receive them in `final`, which may be the same
+ * buffer; no other output may overlap an input.
  *
  * The rows of a batch are its sequences one after another: `seqs` of `seq_len` rows each,
  * or with `packed` sequence s from row offsets[s] up to offsets[s + 1], where offsets has
